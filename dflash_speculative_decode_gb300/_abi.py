@@ -50,6 +50,13 @@ class dfl_buffers(ctypes.Structure):
     _fields_ = [("weights", ctypes.c_void_p), ("state", ctypes.c_void_p), ("workspace", ctypes.c_void_p)]
 
 
+class dfl_kv8(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("n_blocks", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_tail", ctypes.c_void_p), ("v_tail", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("sealed", ctypes.c_void_p), ("score", ctypes.c_void_p), ("err", ctypes.c_void_p)]
+
+
 class dfl_sampling(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_float), ("seed", ctypes.c_uint64)]
 
@@ -97,6 +104,15 @@ SIGNATURES = {
     "dfl_bf16_head_scratch_bytes": (ctypes.c_int64, [ctypes.c_int, ctypes.c_int, ctypes.c_int]),
     "dfl_bf16_head_argmax": (ctypes.c_int, [vp, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp,
                                             ctypes.c_size_t, vp]),
+    "dfl_kv8_init": (ctypes.c_int, [P(dfl_kv8), vp]),
+    "dfl_kv8_status": (ctypes.c_int, [P(dfl_kv8), vp]),
+    "dfl_kv8_append": (ctypes.c_int, [P(dfl_kv8), vp, vp, ctypes.c_int, vp, vp, ctypes.c_int64, vp]),
+    "dfl_kv8_stage": (ctypes.c_int, [P(dfl_kv8), vp, vp, ctypes.c_int, vp, vp, ctypes.c_int64, vp]),
+    "dfl_kv8_attn_scratch_bytes": (ctypes.c_int64, [P(dfl_kv8), ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    "dfl_kv8_attn": (ctypes.c_int, [P(dfl_kv8), vp, ctypes.c_int64, ctypes.c_int, ctypes.c_int, vp, vp, ctypes.c_int, ctypes.c_int,
+                                    ctypes.c_float, ctypes.c_int, vp, ctypes.c_int64, vp, ctypes.c_size_t, vp]),
+    "dfl_kv8_evict": (ctypes.c_int, [P(dfl_kv8), vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp]),
+    "dfl_kv8_read": (ctypes.c_int, [P(dfl_kv8), vp, vp, ctypes.c_int, vp, vp, vp]),
     "dfl_q41_gemm_noalloc": (ctypes.c_int, [vp, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int, vp, vp]),
     "dfl_q41_gemm_noalloc_max_scratch": (ctypes.c_int64, []),
     "dfl_q41_gemm_noalloc_status": (ctypes.c_int, [vp]),

@@ -364,6 +364,99 @@ int dfl_q41_gemm_noalloc_status(void *cuda_stream);
  * after a context teardown, or to start from a known state. Must not overlap a product on the GPU. */
 int dfl_q41_gemm_noalloc_reset(void *cuda_stream);
 
+/* ---- a key/value cache in 8 bits: rows in, attention over it, eviction, rows out ------------------- */
+
+/* The fp32 planes of the step take 4 bytes a value. This cache takes one: it holds blocks of
+ * DFL_KV8_BLOCK tokens per key/value head as unsigned codes with one fp32 scale for the block's keys and
+ * one for its values:  value = (code - 128) * scale,  scale = amax / 127 rounded to fp32 (amax = the
+ * largest magnitude of the block's tokens x head_dim values),  code = 128 + the integer nearest to
+ * value / scale (ties to even, limited to -127..127; 128 where the scale is 0). A block that holds an
+ * infinity or a NaN gets the scale NaN and codes 128: rows that see it get NaN, others are not touched.
+ * The newest tokens, which are not a complete block yet or may still be rolled back, stay fp32 in a tail
+ * of DFL_KV8_TAIL rows, so a verify's rows are never quantised before they are committed and a block is
+ * quantised once, from its original rows.
+ *
+ * Everything is DEVICE memory of the caller's, in these layouts (all 16-byte aligned); the calls below
+ * read the struct on the host and enqueue on the stream given. Lengths are device arrays, int32 [n_seq],
+ * so that a captured graph replays at any position; `len` counts a sequence's committed tokens and is
+ * never written here (layers of one model share it): the caller adds the rows that it commits. `cnt`
+ * (nullable: `rows` for every sequence) holds each sequence's rows of this call; values outside 0..rows
+ * are limited to it, and rows behind it are neither read nor written. */
+#define DFL_KV8_BLOCK 32
+#define DFL_KV8_TAIL 48
+typedef struct dfl_kv8 {
+    int32_t n_seq, n_kv, head_dim, n_blocks;  /* head_dim 64, 128 or 256; capacity 32 * n_blocks tokens
+                                                 a sequence; n_seq, n_kv <= 65535; n_blocks <= 2^20 */
+    uint8_t *k;         /* [n_seq][n_kv][n_blocks][head_dim/64][32 tokens][64] */
+    uint8_t *v;         /* [n_seq][n_kv][n_blocks][head_dim][32 tokens] */
+    float *k_scale;     /* [n_seq][n_kv][n_blocks], of the block stored there */
+    float *v_scale;
+    float *k_tail;      /* [n_seq][n_kv][48 tokens][head_dim]: the tokens from 32 * sealed on */
+    float *v_tail;      /* [n_seq][n_kv][head_dim][48 tokens] */
+    int32_t *table;     /* [n_seq][n_kv][n_blocks]: where logical block b is stored; a permutation of
+                           0..n_blocks-1 */
+    int32_t *sealed;    /* [n_seq][n_kv]: logical blocks held as codes */
+    float *score;       /* [n_seq][n_kv][n_blocks]: attention weight that logical block b has received
+                           (nullable: a cache without scores) */
+    int32_t *err;       /* [1] sticky error bits, read and cleared by dfl_kv8_status */
+} dfl_kv8;
+
+/* An empty cache: table = identity, sealed, score and err = 0. Codes, scales and tails need no values. */
+int dfl_kv8_init(const dfl_kv8 *c, void *cuda_stream);
+/* Status of the calls enqueued on a cache so far: synchronises the stream, then DFL_OK, or (clearing the
+ * word) DFL_E_CAPACITY: a sequence's len + rows passed the capacity or was negative; DFL_E_STATE: a len
+ * lay further behind the sealed blocks than the tail reaches (tokens that no call has written);
+ * DFL_E_INVALID_ARG: a table entry or a sealed count outside 0..n_blocks. A sequence (or head) with such
+ * a fault was left as it was by the call that met it, its output rows among them. */
+int dfl_kv8_status(const dfl_kv8 *c, void *cuda_stream);
+/* Append committed rows (a prompt's, or a draft's context): rows k, v (DEVICE fp32, row m of sequence s
+ * at k + (s * rows + m) * ld, [n_kv][head_dim] each; ld in floats, a multiple of 4, >= n_kv * head_dim)
+ * become tokens len..len+cnt-1. Blocks that are complete are sealed, the rest stays in the tail. Where
+ * more is sealed than len holds, the cache is first cut back to len (the tokens of the block that the
+ * cut goes through return to the tail as the values of their codes). Scores of blocks that begin among
+ * the new rows start at 0. The caller then adds cnt to len. */
+int dfl_kv8_append(const dfl_kv8 *c, const int32_t *len, const int32_t *cnt, int rows, const float *k,
+                   const float *v, int64_t ld, void *cuda_stream);
+/* Stage at most DFL_MAX_ROWS rows that may still be rolled back (a verify's, or a draft block's): first
+ * seals the block that the commits since the last call completed, then writes the rows into the tail as
+ * tokens len..len+cnt-1. To commit the first r of them the caller adds r to len; to roll the others back
+ * it does nothing. Cuts back like dfl_kv8_append. */
+int dfl_kv8_stage(const dfl_kv8 *c, const int32_t *len, const int32_t *cnt, int rows, const float *k,
+                  const float *v, int64_t ld, void *cuda_stream);
+/* Scratch bytes that dfl_kv8_attn needs for n_q query heads, rows and score, or -1 for a shape it does not
+ * take. */
+int64_t dfl_kv8_attn_scratch_bytes(const dfl_kv8 *c, int n_q, int rows, int score);
+/* Grouped-query attention of the staged rows (1..DFL_MAX_ROWS) over the cache:
+ *   out[s][m][h] = sum_j softmax_j(scale * q[s][m][h] . k_j) v_j,  key/value head h / (n_q / n_kv).
+ * Row m of sequence s sits at position p = len + m. causal != 0: it sees the tokens j <= p, with
+ * window > 0 only j > p - window. causal == 0 (a draft's block): every row sees the tokens len - window
+ * <= j < len (all of them with window = 0) and all cnt staged ones. n_q / n_kv is at most 16. q and out
+ * are DEVICE fp32, row m of sequence s at (s * rows + m) * ld, [n_q][head_dim] each. score != 0 adds each
+ * logical block's share of row 0's weights, summed over the head's group of query heads in a fixed order,
+ * to c->score (row 0 is the one row of a verify that is always committed). Sums and softmax statistics
+ * are fp32; queries and weights enter the tensor cores as two fp16 halves each, which hold 22 bits.
+ * Results do not depend on what else the batch holds. Calls on one scratch (DEVICE, 256-byte aligned)
+ * must not overlap on the GPU; nothing is kept in it from one call to the next. */
+int dfl_kv8_attn(const dfl_kv8 *c, const float *q, int64_t ldq, int n_q, int rows, const int32_t *len,
+                 const int32_t *cnt, int window, int causal, float scale, int score, float *out, int64_t ldo,
+                 void *scratch, size_t scratch_bytes, void *cuda_stream);
+/* Evict whole blocks (the unit that shares a scale, so no code changes and none moves): of each head's
+ * sealed blocks keep at most `keep`: the first `sink`, the last `recent`, and of the others those with the
+ * largest scores (equal scores: the lower index; a NaN counts as the smallest), in their order. Needs
+ * sink + recent <= keep. Writes, for every head, the table (kept blocks, then those evicted, which are
+ * free again, then the rest as it was), the scores (kept ones, the two blocks that the tail holds, zeros)
+ * and the sealed count to table_out, score_out and sealed_out, and len - 32 * (blocks evicted) to len_out
+ * (all DEVICE, shaped like c's and len, none of them an input of the call). The caller goes on with
+ * these. Tokens then have new positions in the cache, which len, windows and causality count by; a
+ * model's rotary positions are the caller's own. */
+int dfl_kv8_evict(const dfl_kv8 *c, const int32_t *len, int keep, int sink, int recent, int32_t *table_out,
+                  float *score_out, int32_t *sealed_out, int32_t *len_out, void *cuda_stream);
+/* Read rows out in fp32: tokens first..first+rows-1 of each sequence (first: int32 [n_seq], nullable: 0),
+ * as far as they lie below len, to k_out and v_out (DEVICE fp32 [n_seq][rows][n_kv][head_dim]); entries of
+ * other tokens are left as they were. A len that counts staged rows reads these too. */
+int dfl_kv8_read(const dfl_kv8 *c, const int32_t *len, const int32_t *first, int rows, float *k_out,
+                 float *v_out, void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif
