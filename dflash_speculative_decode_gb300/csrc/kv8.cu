@@ -260,19 +260,29 @@ struct AttnKvArgs {
     int n_q, rows, window, causal, score;
     const int32_t *len, *cnt;
     float scale;
+    int groups, splits;   // row groups of a head, splits of a row group's keys (at most)
+    float *part_o;        // [unit][split][rows of a group][head_dim], unit = (sequence, head, row group)
+    float *part_ml;       // [unit][split][rows of a group][2]: running maximum (base 2) and sum
+    int *part_bad;        // [unit][split]: a table entry was out of range
+    float *blk_lse;       // [sequence][head][n_blocks][16]: log2 of the block's share of row 0's sums
 };
 
 struct Span {
     int z, L, n, bad;   // sealed blocks, committed tokens, staged rows
+    int b0, nb;         // blocks that some row sees: b0 .. b0 + nb - 1 (those from z on lie in the tail)
 };
 __device__ __forceinline__ Span span_of(const AttnKvArgs &a, int s, const KvView &w) {
-    Span p{*w.sealed, a.len[s], rows_of(a.cnt, s, a.rows), 0};
+    Span p{*w.sealed, a.len[s], rows_of(a.cnt, s, a.rows), 0, 0, 0};
     if (p.z < 0 || p.z > w.nb)
         p.bad = kErrTable;
     else if (p.L < 0 || p.L > kBlk * w.nb - p.n)
         p.bad = kErrCapacity;
     else if (p.L < kBlk * p.z || p.L + p.n > kBlk * p.z + kTail)
         p.bad = kErrState;
+    if (p.bad || p.n == 0) return p;
+    const int at = a.causal ? p.L : p.L - 1;
+    p.b0 = (a.window > 0 ? max(0, at - a.window + 1) : 0) / kBlk;
+    p.nb = (p.L + p.n - 1) / kBlk + 1 - p.b0;
     return p;
 }
 // the tokens lo..hi-1 that row m sees
@@ -282,86 +292,633 @@ __device__ __forceinline__ void seen(const AttnKvArgs &a, const Span &p, int m, 
     hi = a.causal ? p.L + m + 1 : p.L + p.n;
 }
 
-// One CTA per head of a sequence: its warps share out the keys of one query row after another, a lane takes
-// every 32nd channel.
-constexpr int kSimpleThreads = 256;
-__global__ void __launch_bounds__(kSimpleThreads) k_kv8_attn_simple(AttnKvArgs a) {
-    __shared__ float sm_o[8][256], sm_m[8], sm_l[8];
-    __shared__ int tab_bad;
-    const int h = blockIdx.x, s = blockIdx.y, hd = a.c.head_dim, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Both products run on the tensor cores (m16n8k16, fp16 in, fp32 sums), keys and value channels as the
+// 16-row operand, query rows as the 8 columns: S^T = K Q^T and O^T = V^T P^T, so rows that a call does not
+// have cost at most 7 columns. Codes are whole numbers of at most 7 bits and exact in fp16; the block's
+// scales multiply the fp32 results. A query row (scaled by a power of two to 2^14..2^15) and the weights
+// (2^14 for the row's largest) enter as two fp16 halves, hi + lo, which hold 22 bits.
+//
+// Fragment order. A thread (g = lane / 4, t = lane % 4) loads 16 consecutive channels of a key at once, so
+// channel 64 c + 16 t + 4 j + e is input 2t + e (e < 2) or 2t + 6 + e of the product's step 4 c + j, and
+// the query halves are laid out to match. Row r of 8-key matrix j holds key 8 (r / 2) + 2 j + r % 2: the
+// transposed weights of matrices 2 s and 2 s + 1 are then the inputs of step s of the second product, whose
+// thread t takes the keys 8 t + 4 s .. + 3, 8 consecutive codes of a value channel for both steps.
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kAttnWarpsKv = 8;
+constexpr float kTop = 14.f;   // log2 of the largest weight
+
+template <int HD, int NT>
+struct AttnShape {
+    static constexpr int kUnit = kBlk * HD;                          // bytes of a block's keys (or values)
+    // ring slots per warp: three of 8 KB (head_dim 256: one CTA an SM), three of 4 KB or six of 2 KB (two CTAs
+    // an SM), so that an SM has 128 KB and more requested
+    static constexpr int kRing = HD == 64 ? 6 : 3;
+    static constexpr int kCtas = HD == 256 ? 1 : 2;
+    static constexpr int kQBytes = NT * 8 * HD * 4;                  // query halves
+    static constexpr int kSmem = kQBytes + kAttnWarpsKv * kRing * kUnit;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+// codes of bytes 0, 1 (or 2, 3) of w as two fp16: 0x6400 | c is 1024 + c, less 1152
+__device__ __forceinline__ uint32_t sub1152(uint32_t x) {
+    const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0xE480)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return sub1152(__byte_perm(w, 0x64646464u, 0x4140)); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return sub1152(__byte_perm(w, 0x64646464u, 0x4342)); }
+
+// two fp32 as fp16 halves hi + lo, the first in the low half of a word
+__device__ __forceinline__ void halves2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x0, x1);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+// two fp32 as three bf16 each: 24 bits over fp32's whole range
+__device__ __forceinline__ void thirds2(float x0, float x1, uint32_t (&w)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+        const float2 f = __bfloat1622float2(b);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        x0 -= f.x;
+        x1 -= f.y;
+    }
+}
+// 2^(14 - floor(log2 x)) for x > 0, within the normal range; 1 for 0
+__device__ __forceinline__ float lift(float x) {
+    const int e = int(__float_as_uint(x) >> 23);           // biased exponent; 0 for subnormals
+    if (x == 0.f) return 1.f;
+    return __uint_as_float(uint32_t(min(127 + 14 + 127 - max(e, 1), 253)) << 23);
+}
+__device__ __forceinline__ float group_max(float x) {      // over the eight g of a t
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float group_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_groups() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// the splits that a head's blocks are worth: at least one block a warp
+__device__ __forceinline__ int splits_of(int splits, int nb) { return min(splits, (nb + kAttnWarpsKv - 1) / kAttnWarpsKv); }
+
+// One CTA per split of a row group: 8 NT query rows (row r = m * group + i of the head's rows). Each warp takes
+// every eighth block of the split with a running softmax of its own; no barrier until they are merged at the
+// end. A warp's codes pass through a ring of its own in shared memory (16-byte asynchronous copies).
+template <int HD, int NT>
+__global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k_kv8_attn(AttnKvArgs a) {
+    using S = AttnShape<HD, NT>;
+    constexpr int RG = 8 * NT, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4;
+    static_assert(kAttnWarpsKv * RG * kPitch * 4 <= S::kSmem, "the merge reuses the shared memory");
+    extern __shared__ __align__(16) uint8_t kv_smem[];
+    __shared__ float q_scale[RG], sm_m[kAttnWarpsKv][RG], sm_l[kAttnWarpsKv][RG];
+    __shared__ int sm_bad;
+    const int split = blockIdx.x, h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const KvView w = view(a.c, s, h);
-    Span p = span_of(a, s, w);
-    const int group = a.n_q / a.c.n_kv;
-    if (threadIdx.x == 0) tab_bad = 0;
-    __syncthreads();
-    if (!p.bad)
-        for (int b = threadIdx.x; b < p.z; b += blockDim.x)
-            if (unsigned(w.table[b]) >= unsigned(w.nb)) tab_bad = 1;
-    __syncthreads();
-    if (tab_bad) p.bad = kErrTable;
+    const Span p = span_of(a, s, w);
+    pdl_trigger();
     if (p.bad) {
-        if (threadIdx.x == 0) atomicOr(a.c.err, p.bad);
+        if (tid == 0 && split == 0) atomicOr(a.c.err, p.bad);
         return;
     }
-    const size_t blk = (size_t)kBlk * hd;
-    auto key = [&](int j, int d) {
-        const int b = j / kBlk, t = j % kBlk;
-        if (b >= p.z) return w.kt[(size_t)(j - kBlk * p.z) * hd + d];
-        const int phys = w.table[b];
-        return expand(w.k[phys * blk + k_at(t, d)], w.ks[phys]);
-    };
-    auto value = [&](int j, int d) {
-        const int b = j / kBlk, t = j % kBlk;
-        if (b >= p.z) return w.vt[(size_t)d * kTail + (j - kBlk * p.z)];
-        const int phys = w.table[b];
-        return expand(w.v[phys * blk + v_at(t, d)], w.vs[phys]);
-    };
-    for (int r = 0; r < p.n * group; ++r) {
-        const int m = r / group, qh = h * group + r % group;
-        int lo, hi;
-        seen(a, p, m, lo, hi);
-        const float *q = a.q + ((size_t)s * a.rows + m) * a.ldq + (size_t)qh * hd;
-        float qr[8], o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) qr[i] = 32 * i + lane < hd ? q[32 * i + lane] : 0.f, o[i] = 0.f;
-        auto logit = [&](int j) {
-            float x = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (32 * i < hd) x = fmaf(qr[i], key(j, 32 * i + lane), x);
-            return warp_sum(x) * a.scale;
-        };
-        float mx = -INFINITY, l = 0.f;
-        for (int j = lo + warp; j < hi; j += 8) {
-            const float x = logit(j), mn = fmaxf(mx, x);
-            const float f = mx == mn ? 1.f : expf(mx - mn), e = expf(x - mn);
-            l = fmaf(l, f, e);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (32 * i < hd) o[i] = fmaf(o[i], f, e * value(j, 32 * i + lane));
-            mx = mn;
+    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG;   // rows of this group that exist
+    const int nsplit = splits_of(a.splits, p.nb);
+    if (live <= 0 || split >= nsplit) return;
+    const int x0 = int((long)p.nb * split / nsplit), x1 = int((long)p.nb * (split + 1) / nsplit);
+    const int bfirst = p.b0 + x0 + warp, bend = p.b0 + x1;          // this warp: bfirst, + 8, .. < bend
+    const int ncoded = max(0, (min(bend, p.z) - bfirst + kAttnWarpsKv - 1) / kAttnWarpsKv);
+    if (tid == 0) sm_bad = 0;
+
+    // ---- codes on their way: unit 2 i is block i's keys, unit 2 i + 1 its values ----
+    uint8_t *ring = kv_smem + S::kQBytes + warp * kRing * kUnit;
+    int phys = 0, bad = 0;
+    auto load_phys = [&](int i0) {                                   // lane l: where block i0 + l is stored
+        const int i = i0 + lane;
+        phys = 0;
+        if (i < ncoded) {
+            phys = w.table[bfirst + kAttnWarpsKv * i];
+            if (unsigned(phys) >= unsigned(w.nb)) phys = 0, bad = 1;
         }
-        if (lane == 0) sm_m[warp] = mx, sm_l[warp] = l;
+    };
+    auto issue = [&](int u) {
+        const int i = u >> 1;
+        if (i < ncoded) {
+            if ((u & 63) == 0) load_phys(i);
+            const size_t at = (size_t)__shfl_sync(0xffffffffu, phys, i & 31) * kUnit;
+            const uint8_t *src = ((u & 1) ? w.v : w.k) + at + 16 * lane;
+            uint8_t *dst = ring + (u % kRing) * kUnit + 16 * lane;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (32 * i < hd) sm_o[warp][32 * i + lane] = o[i];
-        __syncthreads();
-        float top = -INFINITY, total = 0.f;
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, sm_m[i]);
-        for (int i = 0; i < 8; ++i) total += sm_m[i] == -INFINITY ? 0.f : sm_l[i] * expf(sm_m[i] - top);
-        for (int d = threadIdx.x; d < hd; d += blockDim.x) {
-            float x = 0.f;
-            for (int i = 0; i < 8; ++i) x += sm_m[i] == -INFINITY ? 0.f : sm_o[i][d] * expf(sm_m[i] - top);
-            a.out[((size_t)s * a.rows + m) * a.ldo + (size_t)qh * hd + d] = x / total;
+            for (int k = 0; k < kUnit / 512; ++k) cp_async16(dst + 512 * k, src + 512 * k);
         }
-        if (a.score && m == 0)
-            for (int b = lo / kBlk + warp; b * kBlk < hi; b += 8) {
-                float x = 0.f;
-                for (int j = max(lo, b * kBlk); j < min(hi, (b + 1) * kBlk); ++j) x += expf(logit(j) - top) / total;
-                if (lane == 0) w.score[b] += x;
-            }
-        __syncthreads();
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int u = 0; u < kRing; ++u) issue(u);
+
+    // ---- query rows into their fragments ----
+    for (int r = warp; r < RG; r += kAttnWarpsKv) {
+        const int rid = rg * RG + r, m = rid / per;
+        float2 x[HD / 64];
+        float amax = 0.f;
+        bool fin = true;
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i) {
+            x[i] = make_float2(0.f, 0.f);
+            if (r < live)
+                x[i] = *reinterpret_cast<const float2 *>(a.q + ((size_t)s * a.rows + m) * a.ldq + (size_t)(h * per + rid % per) * HD + 64 * i + 2 * lane);
+            fin = fin && isfinite(x[i].x) && isfinite(x[i].y);
+            amax = fmaxf(amax, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+        }
+        fin = __all_sync(0xffffffffu, fin);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float f = fin ? lift(amax) : 0.f;
+        if (lane == 0) q_scale[r] = fin ? a.scale * kLog2e / f : NAN;
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i) {
+            uint32_t hi = 0, lo = 0;
+            if (fin) halves2(x[i].x * f, x[i].y * f, hi, lo);
+            const int d = 2 * lane;                                  // of chunk i
+            uint32_t *dst = reinterpret_cast<uint32_t *>(kv_smem) + (((i * NT + r / 8) * 4 + ((d & 15) >> 3)) * 32 + (r & 7) * 4 + (d >> 4)) * 4 + ((d & 7) >> 1);
+            dst[0] = hi;
+            dst[2 * 32 * 4] = lo;
+        }
     }
+    __syncthreads();
+
+    // this thread's rows: 8 nt + 2 t + e
+    int lo[NT][2], hi[NT][2];
+    float qs[NT][2], mx[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * nt + 2 * t + e;
+            lo[nt][e] = hi[nt][e] = 0;
+            if (r < live) seen(a, p, (rg * RG + r) / per, lo[nt][e], hi[nt][e]);
+            qs[nt][e] = q_scale[r];
+            mx[nt][e] = -INFINITY;
+            l[nt][e] = 0.f;
+        }
+    // tokens all..all_end-1 are seen by every row of the group that exists
+    int all_lo, all_hi, dummy;
+    seen(a, p, min(p.n - 1, (rg * RG + RG - 1) / per), all_lo, dummy);
+    seen(a, p, rg * RG / per, dummy, all_hi);
+    float o[HD / 16][NT][4];
+#pragma unroll
+    for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+    const uint4 *qf = reinterpret_cast<const uint4 *>(kv_smem) + lane;
+    const bool keep_lse = a.score && rg == 0;
+    float *lse = keep_lse ? a.blk_lse + ((size_t)s * a.c.n_kv + h) * w.nb * 16 : nullptr;
+    const int key0 = 8 * (g >> 1) + (g & 1);                         // key of row g of matrix 0; matrix j: + 2 j
+
+    // logits (base 2) of block b -> weights x, factors f of what was summed before; x[i][nt]: matrices 2 i
+    // (entries 0, 1) and 2 i + 1 (entries 2, 3)
+    auto softmax = [&](int b, float (&x)[2][NT][4], float (&f)[NT][2]) {
+        const int pos0 = kBlk * b;
+        if (pos0 < all_lo || pos0 + kBlk > all_hi || live < RG) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int pos = pos0 + key0 + 4 * i + 2 * (k >> 1);
+                        if (pos < lo[nt][k & 1] || pos >= hi[nt][k & 1]) x[i][nt][k] = -INFINITY;
+                    }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float top = group_max(fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e])));
+                const float now = fmaxf(mx[nt][e], top), ref = now == -INFINITY ? 0.f : now - kTop;
+                f[nt][e] = mx[nt][e] == now ? 1.f : exp2f(mx[nt][e] - now);
+                mx[nt][e] = now;
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int k = e; k < 4; k += 2) sum += x[i][nt][k] = exp2f(x[i][nt][k] - ref);
+                l[nt][e] = fmaf(l[nt][e], f[nt][e], sum);
+                if (keep_lse) {
+                    const float total = group_sum(sum);
+                    const int r = 8 * nt + 2 * t + e;
+                    if (g == 0 && r < per) lse[(size_t)b * 16 + r] = total == 0.f ? -INFINITY : ref + log2f(total);
+                }
+            }
+    };
+
+    float ks = 0.f, vs = 0.f;
+    for (int i = 0; i < ncoded; ++i) {
+        if ((i & 31) == 0 && i + lane < ncoded) ks = w.ks[phys], vs = w.vs[phys];
+        const int b = bfirst + kAttnWarpsKv * i;
+        const float bks = __shfl_sync(0xffffffffu, ks, i & 31), bvs = __shfl_sync(0xffffffffu, vs, i & 31);
+        cp_async_wait_groups<kRing - 1>();
+        __syncwarp();
+        float x[2][NT][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) x[j][nt][0] = x[j][nt][1] = x[j][nt][2] = x[j][nt][3] = 0.f;
+        const uint8_t *K = ring + ((2 * i) % kRing) * kUnit + key0 * 64 + 16 * t;
+#pragma unroll
+        for (int c = 0; c < HD / 64; ++c) {
+            uint32_t kw[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(kw[j]) = *reinterpret_cast<const uint4 *>(K + (c * kBlk + 2 * j) * 64);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t qh[NT][4], ql[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    *reinterpret_cast<uint4 *>(qh[nt]) = qf[((c * NT + nt) * 4 + half) * 32];
+                    *reinterpret_cast<uint4 *>(ql[nt]) = qf[((c * NT + nt) * 4 + 2 + half) * 32];
+                }
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                    const int j = 2 * half + jj;
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        const uint32_t af[4] = {codes_lo(kw[2 * mt][j]), codes_lo(kw[2 * mt + 1][j]), codes_hi(kw[2 * mt][j]), codes_hi(kw[2 * mt + 1][j])};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(x[mt][nt], af, qh[nt][2 * jj], qh[nt][2 * jj + 1]);
+                            mma_f16(x[mt][nt], af, ql[nt][2 * jj], ql[nt][2 * jj + 1]);
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        issue(2 * i + kRing);
+        float f[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float z = bks * qs[nt][e];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) x[j][nt][e] *= z, x[j][nt][2 + e] *= z;
+            }
+        softmax(b, x, f);
+        uint32_t ph[NT][2][2], pl[NT][2][2];                         // [step][input pair]
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t hw, lw;
+                halves2(x[j >> 1][nt][2 * (j & 1)], x[j >> 1][nt][2 * (j & 1) + 1], hw, lw);
+                ph[nt][j >> 1][j & 1] = transpose8x8(hw);
+                pl[nt][j >> 1][j & 1] = transpose8x8(lw);
+            }
+        float sv[NT][2];   // a row that sees nothing of the block takes nothing of its scale either
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) sv[nt][e] = lo[nt][e] < kBlk * (b + 1) && hi[nt][e] > kBlk * b ? bvs : 0.f;
+        cp_async_wait_groups<kRing - 1>();
+        __syncwarp();
+        const uint8_t *V = ring + ((2 * i + 1) % kRing) * kUnit + g * kBlk + 8 * t;
+#pragma unroll
+        for (int mt = 0; mt < HD / 16; ++mt) {
+            const uint2 v0 = *reinterpret_cast<const uint2 *>(V + (16 * mt) * kBlk), v1 = *reinterpret_cast<const uint2 *>(V + (16 * mt + 8) * kBlk);
+            const uint32_t a0[4] = {codes_lo(v0.x), codes_lo(v1.x), codes_hi(v0.x), codes_hi(v1.x)};
+            const uint32_t a1[4] = {codes_lo(v0.y), codes_lo(v1.y), codes_hi(v0.y), codes_hi(v1.y)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(d, a0, ph[nt][0][0], ph[nt][0][1]);
+                mma_f16(d, a0, pl[nt][0][0], pl[nt][0][1]);
+                mma_f16(d, a1, ph[nt][1][0], ph[nt][1][1]);
+                mma_f16(d, a1, pl[nt][1][0], pl[nt][1][1]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[mt][nt][k] = fmaf(o[mt][nt][k], f[nt][k & 1], sv[nt][k & 1] * d[k]);
+            }
+        }
+        __syncwarp();
+        issue(2 * i + 1 + kRing);
+    }
+
+    // ---- the tail's blocks: fp32 rows. Keys enter as two fp16 halves, each key scaled by a power of two of its own;
+    // values and weights as three bf16 parts (fp32's range, so that no token's size touches another's precision).
+    // A token that holds an infinity or a NaN makes the rows that see it NaN; its own numbers enter as 0. ----
+    for (int b = max(p.z, bfirst + kAttnWarpsKv * ncoded); b < bend; b += kAttnWarpsKv) {
+        const int row0 = kBlk * (b - p.z), rows = min(kBlk, p.L + p.n - kBlk * b);   // rows of the tail
+        float back[4];   // 1 / the power of two of this thread's keys of matrix j, NaN for a token that is not finite
+        float up[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int key = key0 + 2 * j;
+            float amax = 0.f;
+            bool fin = true;
+            if (key < rows) {
+                for (int c = 0; c < HD / 64; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 y = *reinterpret_cast<const float4 *>(w.kt + (size_t)(row0 + key) * HD + 64 * c + 16 * t + 4 * k);
+                        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
+                        fin = fin && isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w);
+                    }
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            int ok = fin;
+            ok &= __shfl_xor_sync(0xffffffffu, ok, 1);
+            ok &= __shfl_xor_sync(0xffffffffu, ok, 2);
+            up[j] = ok && key < rows ? lift(amax) : 0.f;
+            back[j] = ok ? (key < rows ? 1.f / up[j] : 0.f) : NAN;
+        }
+        float x[2][NT][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) x[j][nt][0] = x[j][nt][1] = x[j][nt][2] = x[j][nt][3] = 0.f;
+        for (int c = 0; c < HD / 64; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {                            // step 4 c + j
+                uint32_t ah[2][4], al[2][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {                        // matrix k
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (up[k] != 0.f) y = *reinterpret_cast<const float4 *>(w.kt + (size_t)(row0 + key0 + 2 * k) * HD + 64 * c + 16 * t + 4 * j);
+                    halves2(y.x * up[k], y.y * up[k], ah[k >> 1][k & 1], al[k >> 1][k & 1]);
+                    halves2(y.z * up[k], y.w * up[k], ah[k >> 1][2 + (k & 1)], al[k >> 1][2 + (k & 1)]);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    uint32_t qh[4], ql[4];
+                    *reinterpret_cast<uint4 *>(qh) = qf[((c * NT + nt) * 4 + (j >> 1)) * 32];
+                    *reinterpret_cast<uint4 *>(ql) = qf[((c * NT + nt) * 4 + 2 + (j >> 1)) * 32];
+                    const uint32_t h0 = j & 1 ? qh[2] : qh[0], h1 = j & 1 ? qh[3] : qh[1];
+                    const uint32_t l0 = j & 1 ? ql[2] : ql[0], l1 = j & 1 ? ql[3] : ql[1];
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        mma_f16(x[mt][nt], ah[mt], h0, h1);
+                        mma_f16(x[mt][nt], ah[mt], l0, l1);
+                        mma_f16(x[mt][nt], al[mt], h0, h1);
+                    }
+                }
+            }
+        float f[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[j][nt][k] *= back[2 * j + (k >> 1)] * qs[nt][k & 1];
+        softmax(b, x, f);
+        uint32_t poison = 0;                                         // tokens whose values are not finite
+        uint32_t pf[NT][2][2][3];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t y[3];
+                thirds2(x[j >> 1][nt][2 * (j & 1)], x[j >> 1][nt][2 * (j & 1) + 1], y);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) pf[nt][j >> 1][j & 1][k] = transpose8x8(y[k]);
+            }
+#pragma unroll
+        for (int mt = 0; mt < HD / 16; ++mt) {
+            float d[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                uint32_t af[3][4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {                        // channels 16 mt + g and + 8
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int key = 8 * t + 4 * st;
+                    if (key < rows) y = *reinterpret_cast<const float4 *>(w.vt + (size_t)(16 * mt + g + 8 * k) * kTail + row0 + key);
+                    float v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (key + i >= rows) {
+                            v[i] = 0.f;
+                        } else if (!isfinite(v[i])) {
+                            v[i] = 0.f;
+                            poison |= 1u << (key + i);
+                        }
+                    uint32_t y0[3], y1[3];
+                    thirds2(v[0], v[1], y0);
+                    thirds2(v[2], v[3], y1);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) af[i][k] = y0[i], af[i][2 + k] = y1[i];
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 2; i >= 0; --i)                     // the small products first
+#pragma unroll
+                        for (int k = 2 - i; k >= 0; --k)
+                            mma_bf16(d[nt], af[i][0], af[i][1], af[i][2], af[i][3], pf[nt][st][0][k], pf[nt][st][1][k]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[mt][nt][k] = fmaf(o[mt][nt][k], f[nt][k & 1], d[nt][k]);
+        }
+        poison = __reduce_or_sync(0xffffffffu, poison);
+        if (poison) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    for (int k = 0; k < kBlk; ++k)
+                        if ((poison >> k & 1) && kBlk * b + k >= lo[nt][e] && kBlk * b + k < hi[nt][e]) l[nt][e] = NAN;
+        }
+    }
+
+    // ---- the warps' sums, merged in their order ----
+    cp_async_wait_groups<0>();
+    if (bad) sm_bad = 1;
+    __syncthreads();
+    float *om = reinterpret_cast<float *>(kv_smem) + warp * RG * kPitch;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * nt + 2 * t + e;
+            const float sum = group_sum(l[nt][e]);
+            if (g == 0) sm_m[warp][r] = mx[nt][e], sm_l[warp][r] = sum;
+#pragma unroll
+            for (int mt = 0; mt < HD / 16; ++mt) {
+                om[r * kPitch + 16 * mt + g] = o[mt][nt][e];
+                om[r * kPitch + 16 * mt + g + 8] = o[mt][nt][2 + e];
+            }
+        }
+    __syncthreads();
+    const size_t unit = ((size_t)s * a.c.n_kv + h) * a.groups + rg, at = unit * a.splits + split;
+    if (tid == 0) {
+        if (sm_bad) atomicOr(a.c.err, kErrTable);
+        a.part_bad[at] = sm_bad;
+    }
+    if (sm_bad) return;
+    for (int e = tid; e < min(live, RG) * HD; e += kAttnWarpsKv * 32) {
+        const int r = e / HD, d = e % HD;
+        float top = -INFINITY, sum = 0.f, total = 0.f;
+#pragma unroll
+        for (int i = 0; i < kAttnWarpsKv; ++i) top = fmaxf(top, sm_m[i][r]);
+#pragma unroll
+        for (int i = 0; i < kAttnWarpsKv; ++i) {
+            const float f = sm_m[i][r] == top ? 1.f : exp2f(sm_m[i][r] - top);
+            total = fmaf(sm_l[i][r], f, total);
+            sum = fmaf(reinterpret_cast<const float *>(kv_smem)[(i * RG + r) * kPitch + d], f, sum);
+        }
+        if (nsplit == 1) {
+            const int rid = rg * RG + r;
+            a.out[((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + d] = sum / total;
+        } else {
+            a.part_o[(at * RG + r) * HD + d] = sum;
+        }
+        if (d == 0) a.part_ml[(at * RG + r) * 2] = top, a.part_ml[(at * RG + r) * 2 + 1] = total;
+    }
+}
+
+// Merges the splits of a row, in their order (grid x < rows of a group: one row each), and adds row 0's share
+// of 256 blocks to the scores (grid x behind them, row group 0).
+constexpr int kMergeThreads = 256;
+template <int HD, int NT>
+__global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
+    constexpr int RG = 8 * NT, kLanes = kMergeThreads / (HD / 4);   // splits taken at once
+    __shared__ float4 acc[kLanes][HD / 4];
+    __shared__ float top_s[16], total_s[16];
+    const int h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z, tid = threadIdx.x;
+    pdl_wait();
+    const KvView w = view(a.c, s, h);
+    const Span p = span_of(a, s, w);
+    if (p.bad) return;
+    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, nsplit = splits_of(a.splits, p.nb);
+    const size_t at = (((size_t)s * a.c.n_kv + h) * a.groups + rg) * a.splits;
+    if (live <= 0) return;
+    for (int i = 0; i < nsplit; ++i)
+        if (a.part_bad[at + i]) return;
+    const float *ml = a.part_ml + at * RG * 2;
+    auto top_of = [&](int r) {
+        float top = -INFINITY;
+        for (int i = 0; i < nsplit; ++i) top = fmaxf(top, ml[(i * RG + r) * 2]);
+        return top;
+    };
+    auto weight = [&](int i, int r, float top) {
+        const float m = ml[(i * RG + r) * 2];
+        return m == top ? 1.f : exp2f(m - top);
+    };
+    if (blockIdx.x < RG) {
+        const int r = blockIdx.x;
+        if (nsplit == 1 || r >= live) return;
+        const float top = top_of(r);
+        const int d4 = tid % (HD / 4), i0 = tid / (HD / 4);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float total = 0.f;
+        for (int i = 0; i < nsplit; ++i) total = fmaf(ml[(i * RG + r) * 2 + 1], weight(i, r, top), total);
+        for (int i = i0; i < nsplit; i += kLanes) {
+            const float f = weight(i, r, top);
+            const float4 y = *reinterpret_cast<const float4 *>(a.part_o + ((at + i) * RG + r) * HD + 4 * d4);
+            sum.x = fmaf(y.x, f, sum.x);
+            sum.y = fmaf(y.y, f, sum.y);
+            sum.z = fmaf(y.z, f, sum.z);
+            sum.w = fmaf(y.w, f, sum.w);
+        }
+        acc[i0][d4] = sum;
+        __syncthreads();
+        if (i0 == 0) {
+            for (int i = 1; i < kLanes; ++i) {
+                const float4 y = acc[i][d4];
+                sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+            }
+            const int rid = rg * RG + r;
+            *reinterpret_cast<float4 *>(a.out + ((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + 4 * d4) =
+                make_float4(sum.x / total, sum.y / total, sum.z / total, sum.w / total);
+        }
+        return;
+    }
+    const int b = p.b0 + (int(blockIdx.x) - RG) * kMergeThreads + tid;
+    if (rg != 0 || p.b0 + (int(blockIdx.x) - RG) * kMergeThreads >= p.b0 + p.nb) return;
+    if (tid < per) {
+        const float top = top_of(tid);
+        float total = 0.f;
+        for (int i = 0; i < nsplit; ++i) total = fmaf(ml[(i * RG + tid) * 2 + 1], weight(i, tid, top), total);
+        top_s[tid] = top - kTop;
+        total_s[tid] = total;
+    }
+    __syncthreads();
+    if (b < p.b0 + p.nb) {
+        const float *x = a.blk_lse + (((size_t)s * a.c.n_kv + h) * w.nb + b) * 16;
+        float sum = 0.f;
+        for (int r = 0; r < per; ++r) sum += exp2f(x[r] - top_s[r]) / total_s[r];
+        w.score[b] += sum;
+    }
+}
+
+// ---- host side ----
+// How a call's work is cut: row groups of 8 rows, or of 16 (whose codes are expanded once for two products) where
+// a head has more than 8; splits of a group's keys so that the CTAs fill the SMs evenly. Costs in blocks per
+// warp: a CTA's start and end are worth about 6.
+struct AttnCut {
+    int nt, groups, splits;
+    size_t units, o_bytes, ml_bytes, bad_bytes, lse_bytes, total;
+};
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+constexpr int kMaxSplits = 64;
+AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int score) {
+    AttnCut t{};
+    const int r = rows * (n_q / c->n_kv);
+    t.nt = r > 8 ? 2 : 1;
+    t.groups = (r + 8 * t.nt - 1) / (8 * t.nt);
+    t.units = (size_t)c->n_seq * c->n_kv * t.groups;
+    const int slots = 152 * (c->head_dim == 256 ? 1 : 2), most = (c->n_blocks + kAttnWarpsKv - 1) / kAttnWarpsKv;
+    double best = 0;
+    for (int n = 1; n <= std::min(kMaxSplits, most); ++n) {
+        const double waves = double((t.units * n + slots - 1) / slots);
+        const double cost = waves * (double(c->n_blocks) / kAttnWarpsKv / n + 6);
+        if (n == 1 || cost < best) best = cost, t.splits = n;
+    }
+    const size_t parts = t.units * t.splits * 8 * t.nt;
+    t.o_bytes = up256(t.splits > 1 ? parts * c->head_dim * 4 : 0);
+    t.ml_bytes = up256(parts * 8);
+    t.bad_bytes = up256(t.units * t.splits * 4);
+    t.lse_bytes = score ? up256((size_t)c->n_seq * c->n_kv * c->n_blocks * 64) : 0;
+    t.total = t.o_bytes + t.ml_bytes + t.bad_bytes + t.lse_bytes;
+    return t;
+}
+
+template <int HD, int NT>
+cudaError_t launch_kv8_attn(const AttnKvArgs &a, cudaStream_t s) {
+    static bool attr[kMaxDevices] = {};
+    const int dev = current_device();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    const int smem = AttnShape<HD, NT>::kSmem;
+    if (!attr[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(k_kv8_attn<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        attr[dev] = true;
+    }
+    const unsigned heads = unsigned(a.c.n_kv * a.groups);
+    k_kv8_attn<HD, NT><<<dim3(a.splits, heads, a.c.n_seq), kAttnWarpsKv * 32, smem, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || (a.splits == 1 && !a.score)) return e;
+    const unsigned x = 8 * NT + (a.score ? (a.c.n_blocks + kMergeThreads - 1) / kMergeThreads : 0);
+    return launch_pdl(k_kv8_merge<HD, NT>, dim3(x, heads, a.c.n_seq), dim3(kMergeThreads), 0, s, a);
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -490,7 +1047,7 @@ __global__ void k_kv8_init(dfl_kv8 c) {
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 int check_cache(const dfl_kv8 *c) {
-    if (!c || c->n_seq < 1 || c->n_seq > 65535 || c->n_kv < 1 || c->n_kv > 65535 || c->n_blocks < 1 || c->n_blocks > (1 << 20))
+    if (!c || c->n_seq < 1 || c->n_seq > 65535 || c->n_kv < 1 || c->n_kv > 1024 || c->n_blocks < 1 || c->n_blocks > (1 << 20))
         return DFL_E_INVALID_ARG;
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return DFL_E_UNSUPPORTED;
     const void *p[] = {c->k, c->v, c->k_scale, c->v_scale, c->k_tail, c->v_tail, c->table, c->sealed, c->err};
@@ -559,8 +1116,7 @@ int64_t dfl_kv8_attn_scratch_bytes(const dfl_kv8 *c, int n_q, int rows, int scor
     if (!c || c->n_seq < 1 || c->n_kv < 1 || c->n_blocks < 1 || n_q < 1 || n_q % c->n_kv || n_q / c->n_kv > kMaxGroup || rows < 1 ||
         rows > DFL_MAX_ROWS || (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256))
         return -1;
-    (void)score;
-    return 256;
+    return (int64_t)attn_cut(c, n_q, rows, score).total;
 }
 
 int dfl_kv8_attn(const dfl_kv8 *c, const float *q, int64_t ldq, int n_q, int rows, const int32_t *len, const int32_t *cnt, int window,
@@ -573,9 +1129,22 @@ int dfl_kv8_attn(const dfl_kv8 *c, const float *q, int64_t ldq, int n_q, int row
     if (score && !c->score) return DFL_E_INVALID_ARG;
     if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255) || (int64_t)scratch_bytes < dfl_kv8_attn_scratch_bytes(c, n_q, rows, score))
         return DFL_E_INVALID_ARG;
-    AttnKvArgs a{*c, q, out, ldq, ldo, n_q, rows, window, causal != 0, score != 0, len, cnt, scale};
-    k_kv8_attn_simple<<<dim3(c->n_kv, c->n_seq), kSimpleThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launched();
+    const AttnCut t = attn_cut(c, n_q, rows, score);
+    AttnKvArgs a{*c, q, out, ldq, ldo, n_q, rows, window, causal != 0, score != 0, len, cnt, scale, t.groups, t.splits};
+    uint8_t *at = static_cast<uint8_t *>(scratch);
+    a.part_o = reinterpret_cast<float *>(at);
+    a.part_ml = reinterpret_cast<float *>(at += t.o_bytes);
+    a.part_bad = reinterpret_cast<int *>(at += t.ml_bytes);
+    a.blk_lse = reinterpret_cast<float *>(at += t.bad_bytes);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (c->head_dim == 64)
+        e = t.nt == 1 ? launch_kv8_attn<64, 1>(a, st) : launch_kv8_attn<64, 2>(a, st);
+    else if (c->head_dim == 128)
+        e = t.nt == 1 ? launch_kv8_attn<128, 1>(a, st) : launch_kv8_attn<128, 2>(a, st);
+    else
+        e = t.nt == 1 ? launch_kv8_attn<256, 1>(a, st) : launch_kv8_attn<256, 2>(a, st);
+    return e == cudaSuccess ? DFL_OK : DFL_E_CUDA;
 }
 
 int dfl_kv8_evict(const dfl_kv8 *c, const int32_t *len, int keep, int sink, int recent, int32_t *table_out, float *score_out,

@@ -371,7 +371,8 @@ int dfl_q41_gemm_noalloc_reset(void *cuda_stream);
  * one for its values:  value = (code - 128) * scale,  scale = amax / 127 rounded to fp32 (amax = the
  * largest magnitude of the block's tokens x head_dim values),  code = 128 + the integer nearest to
  * value / scale (ties to even, limited to -127..127; 128 where the scale is 0). A block that holds an
- * infinity or a NaN gets the scale NaN and codes 128: rows that see it get NaN, others are not touched.
+ * infinity or a NaN gets the scale NaN and codes 128. Attention rows that see one of its tokens (or, in the
+ * tail, a token that holds an infinity or a NaN) get NaN; the others are not touched by it.
  * The newest tokens, which are not a complete block yet or may still be rolled back, stay fp32 in a tail
  * of DFL_KV8_TAIL rows, so a verify's rows are never quantised before they are committed and a block is
  * quantised once, from its original rows.
@@ -386,7 +387,8 @@ int dfl_q41_gemm_noalloc_reset(void *cuda_stream);
 #define DFL_KV8_TAIL 48
 typedef struct dfl_kv8 {
     int32_t n_seq, n_kv, head_dim, n_blocks;  /* head_dim 64, 128 or 256; capacity 32 * n_blocks tokens
-                                                 a sequence; n_seq, n_kv <= 65535; n_blocks <= 2^20 */
+                                                 a sequence; n_seq <= 65535, n_kv <= 1024,
+                                                 n_blocks <= 2^20 */
     uint8_t *k;         /* [n_seq][n_kv][n_blocks][head_dim/64][32 tokens][64] */
     uint8_t *v;         /* [n_seq][n_kv][n_blocks][head_dim][32 tokens] */
     float *k_scale;     /* [n_seq][n_kv][n_blocks], of the block stored there */

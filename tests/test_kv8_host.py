@@ -33,7 +33,7 @@ def calls(c, L):
 
 
 @pytest.mark.parametrize("change,code", [
-    (dict(n_seq=0), -1), (dict(n_seq=65536), -1), (dict(n_kv=0), -1), (dict(n_kv=65536), -1), (dict(n_blocks=0), -1), (dict(n_blocks=(1 << 20) + 1), -1),
+    (dict(n_seq=0), -1), (dict(n_seq=65536), -1), (dict(n_kv=0), -1), (dict(n_kv=1025), -1), (dict(n_blocks=0), -1), (dict(n_blocks=(1 << 20) + 1), -1),
     (dict(head_dim=96), -4), (dict(head_dim=512), -4), (dict(head_dim=0), -4), (dict(k=None), -1), (dict(v=A + 8), -1), (dict(k_scale=None), -1),
     (dict(v_scale=A + 4), -1), (dict(k_tail=None), -1), (dict(v_tail=A + 4), -1), (dict(table=None), -1), (dict(sealed=None), -1), (dict(err=None), -1),
     (dict(score=A + 4), -1)])
