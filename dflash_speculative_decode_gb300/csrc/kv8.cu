@@ -262,6 +262,7 @@ struct AttnKvArgs {
     float scale;
     int groups, splits;   // row groups of a head, splits of a row group's keys (at most)
     float *part_o;        // [unit][split][rows of a group][head_dim], unit = (sequence, head, row group)
+    float *part_tail;     // [unit][rows of a group][head_dim]: the tail's share, read by the CTA that wrote it
     float *part_ml;       // [unit][split][rows of a group][2]: running maximum (base 2) and sum
     int *part_bad;        // [unit][split]: a table entry was out of range
     float *blk_lse;       // [sequence][head][n_blocks][16]: log2 of the block's share of row 0's sums
@@ -314,6 +315,9 @@ struct AttnShape {
     // an SM), so that an SM has 128 KB and more requested
     static constexpr int kRing = HD == 64 ? 6 : 3;
     static constexpr int kCtas = HD == 256 ? 1 : 2;
+    static constexpr int kTailCh = HD == 256 ? 32 : 16;              // channels of the tail that a warp takes
+    static constexpr int kHold = HD == 64 ? 2 : 1;                   // slots that lend the tail [48][8 NT] floats a warp
+    static_assert(kTail * 8 * NT * 4 <= kHold * kUnit, "the tail's logits fit");
     static constexpr int kQBytes = NT * 8 * HD * 4;                  // query halves
     static constexpr int kSmem = kQBytes + kAttnWarpsKv * kRing * kUnit;
 };
@@ -375,7 +379,7 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait_groups() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // the splits that a head's blocks are worth: at least one block a warp
-__device__ __forceinline__ int splits_of(int splits, int nb) { return min(splits, (nb + kAttnWarpsKv - 1) / kAttnWarpsKv); }
+__device__ __forceinline__ int splits_of(int splits, int nb) { return max(1, min(splits, (nb + kAttnWarpsKv - 1) / kAttnWarpsKv)); }
 
 // One CTA per split of a row group: 8 NT query rows (row r = m * group + i of the head's rows). Each warp takes
 // every eighth block of the split with a running softmax of its own; no barrier until they are merged at the
@@ -386,8 +390,10 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
     constexpr int RG = 8 * NT, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4;
     static_assert(kAttnWarpsKv * RG * kPitch * 4 <= S::kSmem, "the merge reuses the shared memory");
     extern __shared__ __align__(16) uint8_t kv_smem[];
-    __shared__ float q_scale[RG], sm_m[kAttnWarpsKv][RG], sm_l[kAttnWarpsKv][RG];
+    // running maxima and sums of the warps, and behind them the tail's
+    __shared__ float q_scale[RG], sm_m[kAttnWarpsKv + 1][RG], sm_l[kAttnWarpsKv + 1][RG];
     __shared__ int sm_bad;
+    __shared__ uint32_t sm_poison[2];
     const int split = blockIdx.x, h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const KvView w = view(a.c, s, h);
@@ -398,11 +404,16 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
         return;
     }
     const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG;   // rows of this group that exist
-    const int nsplit = splits_of(a.splits, p.nb);
+    const int coded = min(p.nb, max(0, p.z - p.b0));                // blocks held as codes that some row sees
+    const int nsplit = splits_of(a.splits, coded);
     if (live <= 0 || split >= nsplit) return;
-    const int x0 = int((long)p.nb * split / nsplit), x1 = int((long)p.nb * (split + 1) / nsplit);
-    const int bfirst = p.b0 + x0 + warp, bend = p.b0 + x1;          // this warp: bfirst, + 8, .. < bend
-    const int ncoded = max(0, (min(bend, p.z) - bfirst + kAttnWarpsKv - 1) / kAttnWarpsKv);
+    const bool has_tail = split == nsplit - 1 && p.nb > coded;
+    const int x0 = int((long)coded * split / nsplit), x1 = int((long)coded * (split + 1) / nsplit);
+    const int bfirst = p.b0 + x0 + warp;                             // this warp's blocks: bfirst, + 8, ..
+    const int ncoded = max(0, (x1 - x0 - warp + kAttnWarpsKv - 1) / kAttnWarpsKv);
+    const size_t unit = ((size_t)s * a.c.n_kv + h) * a.groups + rg, at = unit * a.splits + split;
+    if (tid < RG) sm_m[kAttnWarpsKv][tid] = -INFINITY, sm_l[kAttnWarpsKv][tid] = 0.f;
+    if (tid < 2) sm_poison[tid] = 0;
     if (tid == 0) sm_bad = 0;
 
     // ---- codes on their way: unit 2 i is block i's keys, unit 2 i + 1 its values ----
@@ -420,8 +431,8 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
         const int i = u >> 1;
         if (i < ncoded) {
             if ((u & 63) == 0) load_phys(i);
-            const size_t at = (size_t)__shfl_sync(0xffffffffu, phys, i & 31) * kUnit;
-            const uint8_t *src = ((u & 1) ? w.v : w.k) + at + 16 * lane;
+            const size_t off = (size_t)__shfl_sync(0xffffffffu, phys, i & 31) * kUnit;
+            const uint8_t *src = ((u & 1) ? w.v : w.k) + off + 16 * lane;
             uint8_t *dst = ring + (u % kRing) * kUnit + 16 * lane;
 #pragma unroll
             for (int k = 0; k < kUnit / 512; ++k) cp_async16(dst + 512 * k, src + 512 * k);
@@ -429,7 +440,8 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
         cp_async_commit();
     };
 #pragma unroll
-    for (int u = 0; u < kRing; ++u) issue(u);
+    for (int u = 0; u < kRing; ++u)
+        if (u < kRing - S::kHold || !has_tail) issue(u);
 
     // ---- query rows into their fragments ----
     for (int r = warp; r < RG; r += kAttnWarpsKv) {
@@ -480,11 +492,6 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
     int all_lo, all_hi, dummy;
     seen(a, p, min(p.n - 1, (rg * RG + RG - 1) / per), all_lo, dummy);
     seen(a, p, rg * RG / per, dummy, all_hi);
-    float o[HD / 16][NT][4];
-#pragma unroll
-    for (int i = 0; i < HD / 16; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
     const uint4 *qf = reinterpret_cast<const uint4 *>(kv_smem) + lane;
     const bool keep_lse = a.score && rg == 0;
     float *lse = keep_lse ? a.blk_lse + ((size_t)s * a.c.n_kv + h) * w.nb * 16 : nullptr;
@@ -527,6 +534,213 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
             }
     };
 
+    // ---- the tail (at most 48 fp32 rows, by the last split's CTA, while its first codes are on their way): a warp
+    // takes kTailCh channels of every row. Keys enter as two fp16 halves, each scaled by a power of two of its own;
+    // values and weights as three bf16 parts (fp32's range, so that no token's size touches another's precision). A
+    // token that holds an infinity or a NaN makes the rows that see it NaN; its own numbers enter as 0. ----
+    if (has_tail) {
+        constexpr int kSteps = S::kTailCh / 16;                      // steps of the first product, channel tiles of the second
+        const bool active = warp * S::kTailCh < HD;
+        const int rows = p.L + p.n - kBlk * p.z;
+        const int c = warp * kSteps / 4, j0 = warp * kSteps % 4;     // steps 4 c + j0 ..
+        float *mine = reinterpret_cast<float *>(ring + (kRing - S::kHold) * kUnit);   // [48][RG]: slots held back
+        // key of row g of matrix m (of 6): thread t's inputs of step s are then the keys 16 s + 4 t .. + 3
+        auto tail_key = [&](int m) { return 16 * (m >> 1) + 4 * (g >> 1) + 2 * (m & 1) + (g & 1); };
+        float4 kr[6][kSteps], vr[kSteps][2][3];
+#pragma unroll
+        for (int m = 0; m < 6; ++m)
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                kr[m][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (active && tail_key(m) < rows)
+                    kr[m][i] = *reinterpret_cast<const float4 *>(w.kt + (size_t)tail_key(m) * HD + 64 * c + 16 * t + 4 * (j0 + i));
+            }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int st = 0; st < 3; ++st) {
+                    vr[i][k][st] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (active && 16 * st + 4 * t < rows)
+                        vr[i][k][st] = *reinterpret_cast<const float4 *>(w.vt + (size_t)(16 * (warp * kSteps + i) + g + 8 * k) * kTail + 16 * st + 4 * t);
+                }
+        if (active) {
+            uint32_t poison[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int st = 0; st < 3; ++st) {
+                        float *v = &vr[i][k][st].x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = 16 * st + 4 * t + e;
+                            if (key >= rows || !isfinite(v[e])) {
+                                if (key < rows) poison[key >> 5] |= 1u << (key & 31);
+                                v[e] = 0.f;
+                            }
+                        }
+                    }
+            if (poison[0]) atomicOr(&sm_poison[0], poison[0]);
+            if (poison[1]) atomicOr(&sm_poison[1], poison[1]);
+            float up[6], back[6];
+#pragma unroll
+            for (int m = 0; m < 6; ++m) {
+                float amax = 0.f;
+                int fin = 1;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const float4 y = kr[m][i];
+                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
+                    fin &= isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w);
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                fin &= __shfl_xor_sync(0xffffffffu, fin, 1);
+                fin &= __shfl_xor_sync(0xffffffffu, fin, 2);
+                up[m] = fin ? lift(amax) : 0.f;
+                back[m] = fin ? 1.f / up[m] : NAN;
+            }
+            float x[3][NT][4];
+#pragma unroll
+            for (int mt = 0; mt < 3; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) x[mt][nt][0] = x[mt][nt][1] = x[mt][nt][2] = x[mt][nt][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int j = j0 + i;
+                uint2 qh[NT], ql[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint2 *f = reinterpret_cast<const uint2 *>(qf + ((c * NT + nt) * 4 + (j >> 1)) * 32) + (j & 1);
+                    qh[nt] = f[0];
+                    ql[nt] = f[2 * 32 * 2];
+                }
+#pragma unroll
+                for (int mt = 0; mt < 3; ++mt) {
+                    uint32_t ah[4], al[4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int m = 2 * mt + k;
+                        const float4 y = up[m] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : kr[m][i];
+                        halves2(y.x * up[m], y.y * up[m], ah[k], al[k]);
+                        halves2(y.z * up[m], y.w * up[m], ah[2 + k], al[2 + k]);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(x[mt][nt], al, qh[nt].x, qh[nt].y);
+                        mma_f16(x[mt][nt], ah, ql[nt].x, ql[nt].y);
+                        mma_f16(x[mt][nt], ah, qh[nt].x, qh[nt].y);
+                    }
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < 3; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<float2 *>(mine + tail_key(2 * mt + k) * RG + 8 * nt + 2 * t) =
+                            make_float2(x[mt][nt][2 * k] * back[2 * mt + k], x[mt][nt][2 * k + 1] * back[2 * mt + k]);
+        }
+        __syncthreads();
+        constexpr int kParts = HD / S::kTailCh;
+        float *first = mine - warp * (kRing * kUnit / 4);
+        for (int e = tid; e < kTail * RG; e += kAttnWarpsKv * 32) {
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) x += first[i * (kRing * kUnit / 4) + e];
+            first[e] = x;
+        }
+        __syncthreads();
+        if (active) {
+            uint32_t pf[NT][3][2][3];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float x[6][2];
+#pragma unroll
+                for (int m = 0; m < 6; ++m) {
+                    const int key = tail_key(m), pos = kBlk * p.z + key;
+                    const float2 y = *reinterpret_cast<const float2 *>(first + key * RG + 8 * nt + 2 * t);
+                    const bool bad_key = sm_poison[key >> 5] >> (key & 31) & 1;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        x[m][e] = pos < lo[nt][e] || pos >= hi[nt][e] ? -INFINITY : bad_key ? NAN : (e ? y.y : y.x) * qs[nt][e];
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = x[0][e];
+#pragma unroll
+                    for (int m = 1; m < 6; ++m) top = fmaxf(top, x[m][e]);
+                    top = group_max(top);
+                    top = isnan(top) ? -INFINITY : top;
+                    const float ref = top == -INFINITY ? 0.f : top - kTop;
+                    float sum[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int m = 0; m < 6; ++m) sum[m >> 2] += x[m][e] = exp2f(x[m][e] - ref);
+                    sum[0] = group_sum(sum[0]);
+                    sum[1] = group_sum(sum[1]);
+                    const int r = 8 * nt + 2 * t + e;
+                    if (warp == 0 && g == 0) {
+                        sm_m[kAttnWarpsKv][r] = top;
+                        sm_l[kAttnWarpsKv][r] = sum[0] + sum[1];
+                        if (keep_lse && r < per)
+                            for (int i = 0; i < 2; ++i)
+                                if (p.z + i < p.b0 + p.nb) lse[(size_t)(p.z + i) * 16 + r] = sum[i] == 0.f ? -INFINITY : ref + log2f(sum[i]);
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < 6; ++m) {
+                    uint32_t y[3];
+                    thirds2(x[m][0], x[m][1], y);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) pf[nt][m >> 1][m & 1][k] = transpose8x8(y[k]);
+                }
+            }
+            float *to = a.part_tail + unit * RG * HD;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                float d[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
+#pragma unroll
+                for (int st = 0; st < 3; ++st) {
+                    uint32_t af[3][4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {                    // channels g and g + 8 of the tile
+                        const float4 y = vr[i][k][st];
+                        uint32_t y0[3], y1[3];
+                        thirds2(y.x, y.y, y0);
+                        thirds2(y.z, y.w, y1);
+#pragma unroll
+                        for (int q = 0; q < 3; ++q) af[q][k] = y0[q], af[q][2 + k] = y1[q];
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int q = 2; q >= 0; --q)                 // the small products first
+#pragma unroll
+                            for (int k = 2 - q; k >= 0; --k)
+                                mma_bf16(d[nt], af[q][0], af[q][1], af[q][2], af[q][3], pf[nt][st][0][k], pf[nt][st][1][k]);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) to[(8 * nt + 2 * t + (k & 1)) * HD + 16 * (warp * kSteps + i) + g + 8 * (k >> 1)] = d[nt][k];
+            }
+        }
+        __syncthreads();   // the slots held back are free, and the CTA sees its part of the tail
+#pragma unroll
+        for (int u = kRing - S::kHold; u < kRing; ++u) issue(u);
+    }
+
+    float o[HD / 16][NT][4];
+#pragma unroll
+    for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
     float ks = 0.f, vs = 0.f;
     for (int i = 0; i < ncoded; ++i) {
         if ((i & 31) == 0 && i + lane < ncoded) ks = w.ks[phys], vs = w.vs[phys];
@@ -618,137 +832,6 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
         issue(2 * i + 1 + kRing);
     }
 
-    // ---- the tail's blocks: fp32 rows. Keys enter as two fp16 halves, each key scaled by a power of two of its own;
-    // values and weights as three bf16 parts (fp32's range, so that no token's size touches another's precision).
-    // A token that holds an infinity or a NaN makes the rows that see it NaN; its own numbers enter as 0. ----
-    for (int b = max(p.z, bfirst + kAttnWarpsKv * ncoded); b < bend; b += kAttnWarpsKv) {
-        const int row0 = kBlk * (b - p.z), rows = min(kBlk, p.L + p.n - kBlk * b);   // rows of the tail
-        float back[4];   // 1 / the power of two of this thread's keys of matrix j, NaN for a token that is not finite
-        float up[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int key = key0 + 2 * j;
-            float amax = 0.f;
-            bool fin = true;
-            if (key < rows) {
-                for (int c = 0; c < HD / 64; ++c)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 y = *reinterpret_cast<const float4 *>(w.kt + (size_t)(row0 + key) * HD + 64 * c + 16 * t + 4 * k);
-                        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
-                        fin = fin && isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w);
-                    }
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            int ok = fin;
-            ok &= __shfl_xor_sync(0xffffffffu, ok, 1);
-            ok &= __shfl_xor_sync(0xffffffffu, ok, 2);
-            up[j] = ok && key < rows ? lift(amax) : 0.f;
-            back[j] = ok ? (key < rows ? 1.f / up[j] : 0.f) : NAN;
-        }
-        float x[2][NT][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) x[j][nt][0] = x[j][nt][1] = x[j][nt][2] = x[j][nt][3] = 0.f;
-        for (int c = 0; c < HD / 64; ++c)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {                            // step 4 c + j
-                uint32_t ah[2][4], al[2][4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {                        // matrix k
-                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (up[k] != 0.f) y = *reinterpret_cast<const float4 *>(w.kt + (size_t)(row0 + key0 + 2 * k) * HD + 64 * c + 16 * t + 4 * j);
-                    halves2(y.x * up[k], y.y * up[k], ah[k >> 1][k & 1], al[k >> 1][k & 1]);
-                    halves2(y.z * up[k], y.w * up[k], ah[k >> 1][2 + (k & 1)], al[k >> 1][2 + (k & 1)]);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    uint32_t qh[4], ql[4];
-                    *reinterpret_cast<uint4 *>(qh) = qf[((c * NT + nt) * 4 + (j >> 1)) * 32];
-                    *reinterpret_cast<uint4 *>(ql) = qf[((c * NT + nt) * 4 + 2 + (j >> 1)) * 32];
-                    const uint32_t h0 = j & 1 ? qh[2] : qh[0], h1 = j & 1 ? qh[3] : qh[1];
-                    const uint32_t l0 = j & 1 ? ql[2] : ql[0], l1 = j & 1 ? ql[3] : ql[1];
-#pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        mma_f16(x[mt][nt], ah[mt], h0, h1);
-                        mma_f16(x[mt][nt], ah[mt], l0, l1);
-                        mma_f16(x[mt][nt], al[mt], h0, h1);
-                    }
-                }
-            }
-        float f[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[j][nt][k] *= back[2 * j + (k >> 1)] * qs[nt][k & 1];
-        softmax(b, x, f);
-        uint32_t poison = 0;                                         // tokens whose values are not finite
-        uint32_t pf[NT][2][2][3];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t y[3];
-                thirds2(x[j >> 1][nt][2 * (j & 1)], x[j >> 1][nt][2 * (j & 1) + 1], y);
-#pragma unroll
-                for (int k = 0; k < 3; ++k) pf[nt][j >> 1][j & 1][k] = transpose8x8(y[k]);
-            }
-#pragma unroll
-        for (int mt = 0; mt < HD / 16; ++mt) {
-            float d[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                uint32_t af[3][4];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {                        // channels 16 mt + g and + 8
-                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const int key = 8 * t + 4 * st;
-                    if (key < rows) y = *reinterpret_cast<const float4 *>(w.vt + (size_t)(16 * mt + g + 8 * k) * kTail + row0 + key);
-                    float v[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (key + i >= rows) {
-                            v[i] = 0.f;
-                        } else if (!isfinite(v[i])) {
-                            v[i] = 0.f;
-                            poison |= 1u << (key + i);
-                        }
-                    uint32_t y0[3], y1[3];
-                    thirds2(v[0], v[1], y0);
-                    thirds2(v[2], v[3], y1);
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) af[i][k] = y0[i], af[i][2 + k] = y1[i];
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 2; i >= 0; --i)                     // the small products first
-#pragma unroll
-                        for (int k = 2 - i; k >= 0; --k)
-                            mma_bf16(d[nt], af[i][0], af[i][1], af[i][2], af[i][3], pf[nt][st][0][k], pf[nt][st][1][k]);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[mt][nt][k] = fmaf(o[mt][nt][k], f[nt][k & 1], d[nt][k]);
-        }
-        poison = __reduce_or_sync(0xffffffffu, poison);
-        if (poison) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    for (int k = 0; k < kBlk; ++k)
-                        if ((poison >> k & 1) && kBlk * b + k >= lo[nt][e] && kBlk * b + k < hi[nt][e]) l[nt][e] = NAN;
-        }
-    }
-
     // ---- the warps' sums, merged in their order ----
     cp_async_wait_groups<0>();
     if (bad) sm_bad = 1;
@@ -768,7 +851,6 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
             }
         }
     __syncthreads();
-    const size_t unit = ((size_t)s * a.c.n_kv + h) * a.groups + rg, at = unit * a.splits + split;
     if (tid == 0) {
         if (sm_bad) atomicOr(a.c.err, kErrTable);
         a.part_bad[at] = sm_bad;
@@ -778,12 +860,17 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
         const int r = e / HD, d = e % HD;
         float top = -INFINITY, sum = 0.f, total = 0.f;
 #pragma unroll
-        for (int i = 0; i < kAttnWarpsKv; ++i) top = fmaxf(top, sm_m[i][r]);
+        for (int i = 0; i <= kAttnWarpsKv; ++i) top = fmaxf(top, sm_m[i][r]);
 #pragma unroll
         for (int i = 0; i < kAttnWarpsKv; ++i) {
             const float f = sm_m[i][r] == top ? 1.f : exp2f(sm_m[i][r] - top);
             total = fmaf(sm_l[i][r], f, total);
             sum = fmaf(reinterpret_cast<const float *>(kv_smem)[(i * RG + r) * kPitch + d], f, sum);
+        }
+        if (has_tail) {
+            const float f = sm_m[kAttnWarpsKv][r] == top ? 1.f : exp2f(sm_m[kAttnWarpsKv][r] - top);
+            total = fmaf(sm_l[kAttnWarpsKv][r], f, total);
+            sum = fmaf(a.part_tail[(unit * RG + r) * HD + d], f, sum);
         }
         if (nsplit == 1) {
             const int rid = rg * RG + r;
@@ -795,53 +882,62 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
     }
 }
 
-// Merges the splits of a row, in their order (grid x < rows of a group: one row each), and adds row 0's share
-// of 256 blocks to the scores (grid x behind them, row group 0).
+// Merges the splits of a row in a fixed order (grid x < rows of a group: one row each), and adds row 0's share of
+// 256 blocks to the scores (grid x behind them, row group 0).
 constexpr int kMergeThreads = 256;
+constexpr int kMaxSplits = 64;
 template <int HD, int NT>
 __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
     constexpr int RG = 8 * NT, kLanes = kMergeThreads / (HD / 4);   // splits taken at once
     __shared__ float4 acc[kLanes][HD / 4];
-    __shared__ float top_s[16], total_s[16];
-    const int h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z, tid = threadIdx.x;
-    pdl_wait();
+    __shared__ float fac[kMaxSplits], top_s[16], total_s[16];
+    const int h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
+    const bool row_part = blockIdx.x < RG;
+    if (!row_part && rg) return;
     const KvView w = view(a.c, s, h);
     const Span p = span_of(a, s, w);
     if (p.bad) return;
-    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, nsplit = splits_of(a.splits, p.nb);
+    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, nsplit = splits_of(a.splits, min(p.nb, max(0, p.z - p.b0)));
+    const int b0 = p.b0 + (int(blockIdx.x) - RG) * kMergeThreads;
+    if (live <= 0 || (row_part ? int(blockIdx.x) >= live || nsplit == 1 : b0 >= p.b0 + p.nb)) return;
     const size_t at = (((size_t)s * a.c.n_kv + h) * a.groups + rg) * a.splits;
-    if (live <= 0) return;
-    for (int i = 0; i < nsplit; ++i)
-        if (a.part_bad[at + i]) return;
-    const float *ml = a.part_ml + at * RG * 2;
-    auto top_of = [&](int r) {
-        float top = -INFINITY;
-        for (int i = 0; i < nsplit; ++i) top = fmaxf(top, ml[(i * RG + r) * 2]);
-        return top;
+    pdl_wait();
+    if (__syncthreads_or(tid < nsplit && a.part_bad[at + tid])) return;
+    // a warp's view of row r: the largest maximum, the sum, and each split's factor
+    auto state = [&](int r, float &top, float &total, float (&f)[2]) {
+        float m[2], l[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = lane + 32 * k;
+            const float2 y = i < nsplit ? *reinterpret_cast<const float2 *>(a.part_ml + ((at + i) * RG + r) * 2) : make_float2(-INFINITY, 0.f);
+            m[k] = y.x, l[k] = y.y;
+        }
+        top = fmaxf(m[0], m[1]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) f[k] = m[k] == top ? 1.f : exp2f(m[k] - top);
+        total = warp_sum(l[0] * f[0] + l[1] * f[1]);
     };
-    auto weight = [&](int i, int r, float top) {
-        const float m = ml[(i * RG + r) * 2];
-        return m == top ? 1.f : exp2f(m - top);
-    };
-    if (blockIdx.x < RG) {
-        const int r = blockIdx.x;
-        if (nsplit == 1 || r >= live) return;
-        const float top = top_of(r);
-        const int d4 = tid % (HD / 4), i0 = tid / (HD / 4);
+    float top, total, f[2];
+    if (row_part) {
+        const int r = blockIdx.x, d4 = tid % (HD / 4), i0 = tid / (HD / 4);
+        state(r, top, total, f);
+        if (tid < 32) fac[lane] = f[0], fac[lane + 32] = f[1];
+        __syncthreads();
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        float total = 0.f;
-        for (int i = 0; i < nsplit; ++i) total = fmaf(ml[(i * RG + r) * 2 + 1], weight(i, r, top), total);
+#pragma unroll 4
         for (int i = i0; i < nsplit; i += kLanes) {
-            const float f = weight(i, r, top);
             const float4 y = *reinterpret_cast<const float4 *>(a.part_o + ((at + i) * RG + r) * HD + 4 * d4);
-            sum.x = fmaf(y.x, f, sum.x);
-            sum.y = fmaf(y.y, f, sum.y);
-            sum.z = fmaf(y.z, f, sum.z);
-            sum.w = fmaf(y.w, f, sum.w);
+            sum.x = fmaf(y.x, fac[i], sum.x);
+            sum.y = fmaf(y.y, fac[i], sum.y);
+            sum.z = fmaf(y.z, fac[i], sum.z);
+            sum.w = fmaf(y.w, fac[i], sum.w);
         }
         acc[i0][d4] = sum;
         __syncthreads();
         if (i0 == 0) {
+#pragma unroll
             for (int i = 1; i < kLanes; ++i) {
                 const float4 y = acc[i][d4];
                 sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
@@ -852,16 +948,12 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
         }
         return;
     }
-    const int b = p.b0 + (int(blockIdx.x) - RG) * kMergeThreads + tid;
-    if (rg != 0 || p.b0 + (int(blockIdx.x) - RG) * kMergeThreads >= p.b0 + p.nb) return;
-    if (tid < per) {
-        const float top = top_of(tid);
-        float total = 0.f;
-        for (int i = 0; i < nsplit; ++i) total = fmaf(ml[(i * RG + tid) * 2 + 1], weight(i, tid, top), total);
-        top_s[tid] = top - kTop;
-        total_s[tid] = total;
+    for (int r = tid >> 5; r < per; r += kMergeThreads / 32) {
+        state(r, top, total, f);
+        if (lane == 0) top_s[r] = top - kTop, total_s[r] = total;
     }
     __syncthreads();
+    const int b = b0 + tid;
     if (b < p.b0 + p.nb) {
         const float *x = a.blk_lse + (((size_t)s * a.c.n_kv + h) * w.nb + b) * 16;
         float sum = 0.f;
@@ -876,10 +968,9 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
 // warp: a CTA's start and end are worth about 6.
 struct AttnCut {
     int nt, groups, splits;
-    size_t units, o_bytes, ml_bytes, bad_bytes, lse_bytes, total;
+    size_t units, o_bytes, tail_bytes, ml_bytes, bad_bytes, lse_bytes, total;
 };
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-constexpr int kMaxSplits = 64;
 AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int score) {
     AttnCut t{};
     const int r = rows * (n_q / c->n_kv);
@@ -895,10 +986,11 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int score) {
     }
     const size_t parts = t.units * t.splits * 8 * t.nt;
     t.o_bytes = up256(t.splits > 1 ? parts * c->head_dim * 4 : 0);
+    t.tail_bytes = up256(t.units * 8 * t.nt * c->head_dim * 4);
     t.ml_bytes = up256(parts * 8);
     t.bad_bytes = up256(t.units * t.splits * 4);
     t.lse_bytes = score ? up256((size_t)c->n_seq * c->n_kv * c->n_blocks * 64) : 0;
-    t.total = t.o_bytes + t.ml_bytes + t.bad_bytes + t.lse_bytes;
+    t.total = t.o_bytes + t.tail_bytes + t.ml_bytes + t.bad_bytes + t.lse_bytes;
     return t;
 }
 
@@ -1133,7 +1225,8 @@ int dfl_kv8_attn(const dfl_kv8 *c, const float *q, int64_t ldq, int n_q, int row
     AttnKvArgs a{*c, q, out, ldq, ldo, n_q, rows, window, causal != 0, score != 0, len, cnt, scale, t.groups, t.splits};
     uint8_t *at = static_cast<uint8_t *>(scratch);
     a.part_o = reinterpret_cast<float *>(at);
-    a.part_ml = reinterpret_cast<float *>(at += t.o_bytes);
+    a.part_tail = reinterpret_cast<float *>(at += t.o_bytes);
+    a.part_ml = reinterpret_cast<float *>(at += t.tail_bytes);
     a.part_bad = reinterpret_cast<int *>(at += t.ml_bytes);
     a.blk_lse = reinterpret_cast<float *>(at += t.bad_bytes);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
