@@ -296,8 +296,9 @@ __device__ __forceinline__ void seen(const AttnKvArgs &a, const Span &p, int m, 
 // Both products run on the tensor cores (m16n8k16, fp16 in, fp32 sums), keys and value channels as the
 // 16-row operand, query rows as the 8 columns: S^T = K Q^T and O^T = V^T P^T, so rows that a call does not
 // have cost at most 7 columns. Codes are whole numbers of at most 7 bits and exact in fp16; the block's
-// scales multiply the fp32 results. A query row (scaled by a power of two to 2^14..2^15) and the weights
-// (2^14 for the row's largest) enter as two fp16 halves, hi + lo, which hold 22 bits.
+// key scale multiplies the fp32 logits. A query row (scaled by a power of two to 2^14..2^15) and the weights
+// (2^14 for the row's largest, times the block's value scale over the largest one) enter as two fp16 halves,
+// hi + lo, which hold 22 bits, and nothing below 2^-25.
 //
 // Fragment order. A thread (g = lane / 4, t = lane % 4) loads 16 consecutive channels of a key at once, so
 // channel 64 c + 16 t + 4 j + e is input 2t + e (e < 2) or 2t + 6 + e of the product's step 4 c + j, and
@@ -326,6 +327,18 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d = a b
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// 2^x by the hardware's instruction: off by 2 units in the last place, results below 2^-126 are 0
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
@@ -427,18 +440,21 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
             if (unsigned(phys) >= unsigned(w.nb)) phys = 0, bad = 1;
         }
     };
+    uint8_t *put = ring + 16 * lane;                                 // the slot that the next unit goes to
+    const uint8_t *take = ring;                                      // the slot that is read next
     auto issue = [&](int u) {
         const int i = u >> 1;
         if (i < ncoded) {
             if ((u & 63) == 0) load_phys(i);
             const size_t off = (size_t)__shfl_sync(0xffffffffu, phys, i & 31) * kUnit;
             const uint8_t *src = ((u & 1) ? w.v : w.k) + off + 16 * lane;
-            uint8_t *dst = ring + (u % kRing) * kUnit + 16 * lane;
 #pragma unroll
-            for (int k = 0; k < kUnit / 512; ++k) cp_async16(dst + 512 * k, src + 512 * k);
+            for (int k = 0; k < kUnit / 512; ++k) cp_async16(put + 512 * k, src + 512 * k);
+            put = put == ring + (kRing - 1) * kUnit + 16 * lane ? ring + 16 * lane : put + kUnit;
         }
         cp_async_commit();
     };
+    auto taken = [&]() { take = take == ring + (kRing - 1) * kUnit ? ring : take + kUnit; };
 #pragma unroll
     for (int u = 0; u < kRing; ++u)
         if (u < kRing - S::kHold || !has_tail) issue(u);
@@ -518,13 +534,13 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
             for (int e = 0; e < 2; ++e) {
                 const float top = group_max(fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e])));
                 const float now = fmaxf(mx[nt][e], top), ref = now == -INFINITY ? 0.f : now - kTop;
-                f[nt][e] = mx[nt][e] == now ? 1.f : exp2f(mx[nt][e] - now);
+                f[nt][e] = mx[nt][e] == now ? 1.f : ex2(mx[nt][e] - now);
                 mx[nt][e] = now;
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int k = e; k < 4; k += 2) sum += x[i][nt][k] = exp2f(x[i][nt][k] - ref);
+                    for (int k = e; k < 4; k += 2) sum += x[i][nt][k] = ex2(x[i][nt][k] - ref);
                 l[nt][e] = fmaf(l[nt][e], f[nt][e], sum);
                 if (keep_lse) {
                     const float total = group_sum(sum);
@@ -679,7 +695,7 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
                     const float ref = top == -INFINITY ? 0.f : top - kTop;
                     float sum[2] = {0.f, 0.f};
 #pragma unroll
-                    for (int m = 0; m < 6; ++m) sum[m >> 2] += x[m][e] = exp2f(x[m][e] - ref);
+                    for (int m = 0; m < 6; ++m) sum[m >> 2] += x[m][e] = ex2(x[m][e] - ref);
                     sum[0] = group_sum(sum[0]);
                     sum[1] = group_sum(sum[1]);
                     const int r = 8 * nt + 2 * t + e;
@@ -741,19 +757,35 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
     for (int i = 0; i < HD / 16; ++i)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
-    float ks = 0.f, vs = 0.f;
+    // Values are summed in units of v_ref, the largest value scale so far: a block's weights are multiplied by its scale /
+    // v_ref before they are split into halves, so the products add straight to the sums.
+    float ks = 0.f, vs = 0.f, v_ref = 0.f;
     for (int i = 0; i < ncoded; ++i) {
-        if ((i & 31) == 0 && i + lane < ncoded) ks = w.ks[phys], vs = w.vs[phys];
+        if ((i & 31) == 0) {                                         // the next 32 blocks' scales
+            ks = vs = 0.f;
+            if (i + lane < ncoded) ks = w.ks[phys], vs = w.vs[phys];
+            float top = isnan(vs) ? 0.f : vs;
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+            if (top > v_ref) {
+                const float f = v_ref / top;
+#pragma unroll
+                for (int mt = 0; mt < HD / 16; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[mt][nt][k] *= f;
+                v_ref = top;
+            }
+            vs = v_ref > 0.f ? vs / v_ref : vs;
+        }
         const int b = bfirst + kAttnWarpsKv * i;
-        const float bks = __shfl_sync(0xffffffffu, ks, i & 31), bvs = __shfl_sync(0xffffffffu, vs, i & 31);
+        const float bks = __shfl_sync(0xffffffffu, ks, i & 31);
+        float bvs = __shfl_sync(0xffffffffu, vs, i & 31);
         cp_async_wait_groups<kRing - 1>();
         __syncwarp();
-        float x[2][NT][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) x[j][nt][0] = x[j][nt][1] = x[j][nt][2] = x[j][nt][3] = 0.f;
-        const uint8_t *K = ring + ((2 * i) % kRing) * kUnit + key0 * 64 + 16 * t;
+        float x[2][NT][4], xl[2][NT][4];                             // by the query's hi and lo halves
+        const uint8_t *K = take + key0 * 64 + 16 * t;
 #pragma unroll
         for (int c = 0; c < HD / 64; ++c) {
             uint32_t kw[4][4];
@@ -775,14 +807,23 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
                         const uint32_t af[4] = {codes_lo(kw[2 * mt][j]), codes_lo(kw[2 * mt + 1][j]), codes_hi(kw[2 * mt][j]), codes_hi(kw[2 * mt + 1][j])};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16(x[mt][nt], af, qh[nt][2 * jj], qh[nt][2 * jj + 1]);
-                            mma_f16(x[mt][nt], af, ql[nt][2 * jj], ql[nt][2 * jj + 1]);
+                            if (c == 0 && j == 0) {
+                                mma_f16_zero(x[mt][nt], af, qh[nt][0], qh[nt][1]);
+                                if (NT == 1)
+                                    mma_f16_zero(xl[mt][nt], af, ql[nt][0], ql[nt][1]);
+                                else
+                                    mma_f16(x[mt][nt], af, ql[nt][0], ql[nt][1]);
+                            } else {
+                                mma_f16(x[mt][nt], af, qh[nt][2 * jj], qh[nt][2 * jj + 1]);
+                                mma_f16(NT == 1 ? xl[mt][nt] : x[mt][nt], af, ql[nt][2 * jj], ql[nt][2 * jj + 1]);
+                            }
                         }
                     }
                 }
             }
         }
         __syncwarp();
+        taken();
         issue(2 * i + kRing);
         float f[NT][2];
 #pragma unroll
@@ -791,27 +832,43 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
             for (int e = 0; e < 2; ++e) {
                 const float z = bks * qs[nt][e];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) x[j][nt][e] *= z, x[j][nt][2 + e] *= z;
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = e; k < 4; k += 2) x[j][nt][k] = (NT == 1 ? x[j][nt][k] + xl[j][nt][k] : x[j][nt][k]) * z;
             }
         softmax(b, x, f);
-        uint32_t ph[NT][2][2], pl[NT][2][2];                         // [step][input pair]
+        if (isnan(bvs)) {                                            // rows that see the block are NaN, the others take nothing of it
+            bvs = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (lo[nt][e] < kBlk * (b + 1) && hi[nt][e] > kBlk * b) l[nt][e] = NAN;
+        }
+        uint32_t ph[NT][2][2], pl[NT][2][2];                         // [step][input pair]
+        bool moved = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            moved = moved || f[nt][0] != 1.f || f[nt][1] != 1.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t hw, lw;
-                halves2(x[j >> 1][nt][2 * (j & 1)], x[j >> 1][nt][2 * (j & 1) + 1], hw, lw);
+                halves2(x[j >> 1][nt][2 * (j & 1)] * bvs, x[j >> 1][nt][2 * (j & 1) + 1] * bvs, hw, lw);
                 ph[nt][j >> 1][j & 1] = transpose8x8(hw);
                 pl[nt][j >> 1][j & 1] = transpose8x8(lw);
             }
-        float sv[NT][2];   // a row that sees nothing of the block takes nothing of its scale either
+        }
+        if (__any_sync(0xffffffffu, moved)) {                        // seldom, once the maxima have been met
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int mt = 0; mt < HD / 16; ++mt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) sv[nt][e] = lo[nt][e] < kBlk * (b + 1) && hi[nt][e] > kBlk * b ? bvs : 0.f;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[mt][nt][k] *= f[nt][k & 1];
+        }
         cp_async_wait_groups<kRing - 1>();
         __syncwarp();
-        const uint8_t *V = ring + ((2 * i + 1) % kRing) * kUnit + g * kBlk + 8 * t;
+        const uint8_t *V = take + g * kBlk + 8 * t;
 #pragma unroll
         for (int mt = 0; mt < HD / 16; ++mt) {
             const uint2 v0 = *reinterpret_cast<const uint2 *>(V + (16 * mt) * kBlk), v1 = *reinterpret_cast<const uint2 *>(V + (16 * mt + 8) * kBlk);
@@ -819,16 +876,14 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
             const uint32_t a1[4] = {codes_lo(v0.y), codes_lo(v1.y), codes_hi(v0.y), codes_hi(v1.y)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(d, a0, ph[nt][0][0], ph[nt][0][1]);
-                mma_f16(d, a0, pl[nt][0][0], pl[nt][0][1]);
-                mma_f16(d, a1, ph[nt][1][0], ph[nt][1][1]);
-                mma_f16(d, a1, pl[nt][1][0], pl[nt][1][1]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[mt][nt][k] = fmaf(o[mt][nt][k], f[nt][k & 1], sv[nt][k & 1] * d[k]);
+                mma_f16(o[mt][nt], a0, ph[nt][0][0], ph[nt][0][1]);
+                mma_f16(o[mt][nt], a0, pl[nt][0][0], pl[nt][0][1]);
+                mma_f16(o[mt][nt], a1, ph[nt][1][0], ph[nt][1][1]);
+                mma_f16(o[mt][nt], a1, pl[nt][1][0], pl[nt][1][1]);
             }
         }
         __syncwarp();
+        taken();
         issue(2 * i + 1 + kRing);
     }
 
@@ -846,8 +901,8 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
             if (g == 0) sm_m[warp][r] = mx[nt][e], sm_l[warp][r] = sum;
 #pragma unroll
             for (int mt = 0; mt < HD / 16; ++mt) {
-                om[r * kPitch + 16 * mt + g] = o[mt][nt][e];
-                om[r * kPitch + 16 * mt + g + 8] = o[mt][nt][2 + e];
+                om[r * kPitch + 16 * mt + g] = o[mt][nt][e] * v_ref;
+                om[r * kPitch + 16 * mt + g + 8] = o[mt][nt][2 + e] * v_ref;
             }
         }
     __syncthreads();
@@ -863,12 +918,12 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
         for (int i = 0; i <= kAttnWarpsKv; ++i) top = fmaxf(top, sm_m[i][r]);
 #pragma unroll
         for (int i = 0; i < kAttnWarpsKv; ++i) {
-            const float f = sm_m[i][r] == top ? 1.f : exp2f(sm_m[i][r] - top);
+            const float f = sm_m[i][r] == top ? 1.f : ex2(sm_m[i][r] - top);
             total = fmaf(sm_l[i][r], f, total);
             sum = fmaf(reinterpret_cast<const float *>(kv_smem)[(i * RG + r) * kPitch + d], f, sum);
         }
         if (has_tail) {
-            const float f = sm_m[kAttnWarpsKv][r] == top ? 1.f : exp2f(sm_m[kAttnWarpsKv][r] - top);
+            const float f = sm_m[kAttnWarpsKv][r] == top ? 1.f : ex2(sm_m[kAttnWarpsKv][r] - top);
             total = fmaf(sm_l[kAttnWarpsKv][r], f, total);
             sum = fmaf(a.part_tail[(unit * RG + r) * HD + d], f, sum);
         }
@@ -916,7 +971,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll
-        for (int k = 0; k < 2; ++k) f[k] = m[k] == top ? 1.f : exp2f(m[k] - top);
+        for (int k = 0; k < 2; ++k) f[k] = m[k] == top ? 1.f : ex2(m[k] - top);
         total = warp_sum(l[0] * f[0] + l[1] * f[1]);
     };
     float top, total, f[2];
@@ -957,7 +1012,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
     if (b < p.b0 + p.nb) {
         const float *x = a.blk_lse + (((size_t)s * a.c.n_kv + h) * w.nb + b) * 16;
         float sum = 0.f;
-        for (int r = 0; r < per; ++r) sum += exp2f(x[r] - top_s[r]) / total_s[r];
+        for (int r = 0; r < per; ++r) sum += ex2(x[r] - top_s[r]) / total_s[r];
         w.score[b] += sum;
     }
 }
