@@ -306,21 +306,22 @@ __device__ __forceinline__ void seen(const AttnKvArgs &a, const Span &p, int m, 
 // transposed weights of matrices 2 s and 2 s + 1 are then the inputs of step s of the second product, whose
 // thread t takes the keys 8 t + 4 s .. + 3, 8 consecutive codes of a value channel for both steps.
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kAttnWarpsKv = 8;
 constexpr float kTop = 14.f;   // log2 of the largest weight
 
 template <int HD, int NT>
 struct AttnShape {
     static constexpr int kUnit = kBlk * HD;                          // bytes of a block's keys (or values)
-    // ring slots per warp: three of 8 KB (head_dim 256: one CTA an SM), three of 4 KB or six of 2 KB (two CTAs
-    // an SM), so that an SM has 128 KB and more requested
-    static constexpr int kRing = HD == 64 ? 6 : 3;
+    // Warps of a CTA and CTAs of an SM, by the registers that the sums take (HD * NT / 4 a thread): 255 a thread at
+    // head_dim 256, 168 at 128 with 16 rows, 128 otherwise. Ring slots per warp: as many as fit, so that an SM has about
+    // 128 KB requested.
+    static constexpr int kWarps = HD == 128 && NT == 2 ? 6 : 8;
     static constexpr int kCtas = HD == 256 ? 1 : 2;
-    static constexpr int kTailCh = HD == 256 ? 32 : 16;              // channels of the tail that a warp takes
+    static constexpr int kRing = HD == 64 ? 6 : HD == 128 && NT == 2 ? 4 : 3;
+    static constexpr int kTailCh = HD == 64 || (HD == 128 && NT == 1) ? 16 : 32;   // channels of the tail that a warp takes
     static constexpr int kHold = HD == 64 ? 2 : 1;                   // slots that lend the tail [48][8 NT] floats a warp
-    static_assert(kTail * 8 * NT * 4 <= kHold * kUnit, "the tail's logits fit");
+    static_assert(kTail * 8 * NT * 4 <= kHold * kUnit && HD / kTailCh <= kWarps, "the tail's logits and channels fit");
     static constexpr int kQBytes = NT * 8 * HD * 4;                  // query halves
-    static constexpr int kSmem = kQBytes + kAttnWarpsKv * kRing * kUnit;
+    static constexpr int kSmem = kQBytes + kWarps * kRing * kUnit;
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -346,12 +347,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return r;
 }
 // codes of bytes 0, 1 (or 2, 3) of w as two fp16: 0x6400 | c is 1024 + c, less 1152
-__device__ __forceinline__ uint32_t sub1152(uint32_t x) {
-    const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0xE480)));
-    return *reinterpret_cast<const uint32_t *>(&r);
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 x;\n\tprmt.b32 x, %1, 0x64646464, 0x4140;\n\tadd.rn.f16x2 %0, x, %2;\n\t}" : "=r"(r) : "r"(w), "r"(0xE480E480u));
+    return r;
 }
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return sub1152(__byte_perm(w, 0x64646464u, 0x4140)); }
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return sub1152(__byte_perm(w, 0x64646464u, 0x4342)); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 x;\n\tprmt.b32 x, %1, 0x64646464, 0x4342;\n\tadd.rn.f16x2 %0, x, %2;\n\t}" : "=r"(r) : "r"(w), "r"(0xE480E480u));
+    return r;
+}
 
 // two fp32 as fp16 halves hi + lo, the first in the low half of a word
 __device__ __forceinline__ void halves2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
@@ -392,60 +397,103 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait_groups() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // the splits that a head's blocks are worth: at least one block a warp
-__device__ __forceinline__ int splits_of(int splits, int nb) { return max(1, min(splits, (nb + kAttnWarpsKv - 1) / kAttnWarpsKv)); }
+template <int W>
+__device__ __forceinline__ int splits_of(int splits, int nb) { return max(1, min(splits, (nb + W - 1) / W)); }
 
 // One CTA per split of a row group: 8 NT query rows (row r = m * group + i of the head's rows). Each warp takes
-// every eighth block of the split with a running softmax of its own; no barrier until they are merged at the
+// its share of the split's blocks with a running softmax of its own; no barrier until they are merged at the
 // end. A warp's codes pass through a ring of its own in shared memory (16-byte asynchronous copies).
 template <int HD, int NT>
-__global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k_kv8_attn(AttnKvArgs a) {
+__global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, NT>::kCtas) k_kv8_attn(AttnKvArgs a) {
     using S = AttnShape<HD, NT>;
-    constexpr int RG = 8 * NT, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4;
-    static_assert(kAttnWarpsKv * RG * kPitch * 4 <= S::kSmem, "the merge reuses the shared memory");
+    constexpr int RG = 8 * NT, kW = S::kWarps, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4;
+    static_assert(kW * RG * kPitch * 4 <= S::kSmem, "the merge reuses the shared memory");
     extern __shared__ __align__(16) uint8_t kv_smem[];
     // running maxima and sums of the warps, and behind them the tail's
-    __shared__ float q_scale[RG], sm_m[kAttnWarpsKv + 1][RG], sm_l[kAttnWarpsKv + 1][RG];
+    __shared__ float q_scale[RG], sm_m[kW + 1][RG], sm_l[kW + 1][RG];
     __shared__ int sm_bad;
     __shared__ uint32_t sm_poison[2];
     const int split = blockIdx.x, h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const KvView w = view(a.c, s, h);
+    const int per = a.n_q / a.c.n_kv;
+    // What is small is asked for first, so that it does not wait behind the codes: the query rows (a warp takes
+    // every kW-th), lengths, the table, scales, the tail.
+    constexpr int kQRows = (RG + kW - 1) / kW;
+    float2 qx[kQRows][HD / 64];
+#pragma unroll
+    for (int i = 0; i < kQRows; ++i) {
+        const int r = warp + i * kW, rid = rg * RG + r;
+        const bool on = r < RG && rid < a.rows * per;
+        const float *q = a.q + ((size_t)s * a.rows + rid / per) * a.ldq + (size_t)(h * per + rid % per) * HD + 2 * lane;
+#pragma unroll
+        for (int k = 0; k < HD / 64; ++k) qx[i][k] = on ? *reinterpret_cast<const float2 *>(q + 64 * k) : make_float2(0.f, 0.f);
+    }
     const Span p = span_of(a, s, w);
     pdl_trigger();
     if (p.bad) {
         if (tid == 0 && split == 0) atomicOr(a.c.err, p.bad);
         return;
     }
-    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG;   // rows of this group that exist
+    const int live = p.n * per - rg * RG;                            // rows of this group that exist
     const int coded = min(p.nb, max(0, p.z - p.b0));                // blocks held as codes that some row sees
-    const int nsplit = splits_of(a.splits, coded);
+    const int nsplit = splits_of<kW>(a.splits, coded);
     if (live <= 0 || split >= nsplit) return;
     const bool has_tail = split == nsplit - 1 && p.nb > coded;
     const int x0 = int((long)coded * split / nsplit), x1 = int((long)coded * (split + 1) / nsplit);
-    const int bfirst = p.b0 + x0 + warp;                             // this warp's blocks: bfirst, + 8, ..
-    const int ncoded = max(0, (x1 - x0 - warp + kAttnWarpsKv - 1) / kAttnWarpsKv);
+    const int bfirst = p.b0 + x0 + warp;                             // this warp's blocks: bfirst, + kW, ..
+    const int ncoded = max(0, (x1 - x0 - warp + kW - 1) / kW);
     const size_t unit = ((size_t)s * a.c.n_kv + h) * a.groups + rg, at = unit * a.splits + split;
-    if (tid < RG) sm_m[kAttnWarpsKv][tid] = -INFINITY, sm_l[kAttnWarpsKv][tid] = 0.f;
-    if (tid < 2) sm_poison[tid] = 0;
-    if (tid == 0) sm_bad = 0;
 
-    // ---- codes on their way: unit 2 i is block i's keys, unit 2 i + 1 its values ----
-    uint8_t *ring = kv_smem + S::kQBytes + warp * kRing * kUnit;
     int phys = 0, bad = 0;
     auto load_phys = [&](int i0) {                                   // lane l: where block i0 + l is stored
         const int i = i0 + lane;
         phys = 0;
         if (i < ncoded) {
-            phys = w.table[bfirst + kAttnWarpsKv * i];
+            phys = w.table[bfirst + kW * i];
             if (unsigned(phys) >= unsigned(w.nb)) phys = 0, bad = 1;
         }
     };
+    load_phys(0);
+    // the tail's rows: a warp takes kTailCh channels, steps 4 tc + tj0 .. of the first product, and of it the key of
+    // row g of matrix m (of 6), which makes thread t's inputs of step s the keys 16 s + 4 t .. + 3
+    constexpr int kSteps = S::kTailCh / 16;
+    const int tc = warp * kSteps / 4, tj0 = warp * kSteps % 4, trows = p.L + p.n - kBlk * p.z;
+    const bool tactive = has_tail && warp * S::kTailCh < HD;
+    auto tail_key = [&](int m) { return 16 * (m >> 1) + 4 * (g >> 1) + 2 * (m & 1) + (g & 1); };
+    float4 kr[6][kSteps], vr[kSteps][2][3];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+#pragma unroll
+        for (int m = 0; m < 6; ++m) {
+            kr[m][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (tactive && tail_key(m) < trows)
+                kr[m][i] = *reinterpret_cast<const float4 *>(w.kt + (size_t)tail_key(m) * HD + 64 * tc + 16 * t + 4 * (tj0 + i));
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int st = 0; st < 3; ++st) {
+                vr[i][k][st] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (tactive && 16 * st + 4 * t < trows)
+                    vr[i][k][st] = *reinterpret_cast<const float4 *>(w.vt + (size_t)(16 * (warp * kSteps + i) + g + 8 * k) * kTail + 16 * st + 4 * t);
+            }
+    }
+    float ks = 0.f, vs = 0.f;                                        // lane l: scales of block i + l of the window
+    auto load_scales = [&](int i0) {
+        ks = vs = 0.f;
+        if (i0 + lane < ncoded) ks = w.ks[phys], vs = w.vs[phys];
+    };
+    load_scales(0);
+
+    // ---- codes on their way: unit 2 i is block i's keys, unit 2 i + 1 its values ----
+    uint8_t *ring = kv_smem + S::kQBytes + warp * kRing * kUnit;
     uint8_t *put = ring + 16 * lane;                                 // the slot that the next unit goes to
     const uint8_t *take = ring;                                      // the slot that is read next
     auto issue = [&](int u) {
         const int i = u >> 1;
         if (i < ncoded) {
-            if ((u & 63) == 0) load_phys(i);
+            if ((u & 63) == 0 && u > 0) load_phys(i);
             const size_t off = (size_t)__shfl_sync(0xffffffffu, phys, i & 31) * kUnit;
             const uint8_t *src = ((u & 1) ? w.v : w.k) + off + 16 * lane;
 #pragma unroll
@@ -460,18 +508,20 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
         if (u < kRing - S::kHold || !has_tail) issue(u);
 
     // ---- query rows into their fragments ----
-    for (int r = warp; r < RG; r += kAttnWarpsKv) {
-        const int rid = rg * RG + r, m = rid / per;
-        float2 x[HD / 64];
+    if (tid < RG) sm_m[kW][tid] = -INFINITY, sm_l[kW][tid] = 0.f;
+    if (tid < 2) sm_poison[tid] = 0;
+    if (tid == 0) sm_bad = 0;
+#pragma unroll
+    for (int j = 0; j < kQRows; ++j) {
+        const int r = warp + j * kW;
+        if (r >= RG) break;
         float amax = 0.f;
         bool fin = true;
 #pragma unroll
         for (int i = 0; i < HD / 64; ++i) {
-            x[i] = make_float2(0.f, 0.f);
-            if (r < live)
-                x[i] = *reinterpret_cast<const float2 *>(a.q + ((size_t)s * a.rows + m) * a.ldq + (size_t)(h * per + rid % per) * HD + 64 * i + 2 * lane);
-            fin = fin && isfinite(x[i].x) && isfinite(x[i].y);
-            amax = fmaxf(amax, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+            if (r >= live) qx[j][i] = make_float2(0.f, 0.f);
+            fin = fin && isfinite(qx[j][i].x) && isfinite(qx[j][i].y);
+            amax = fmaxf(amax, fmaxf(fabsf(qx[j][i].x), fabsf(qx[j][i].y)));
         }
         fin = __all_sync(0xffffffffu, fin);
 #pragma unroll
@@ -481,7 +531,7 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
 #pragma unroll
         for (int i = 0; i < HD / 64; ++i) {
             uint32_t hi = 0, lo = 0;
-            if (fin) halves2(x[i].x * f, x[i].y * f, hi, lo);
+            if (fin) halves2(qx[j][i].x * f, qx[j][i].y * f, hi, lo);
             const int d = 2 * lane;                                  // of chunk i
             uint32_t *dst = reinterpret_cast<uint32_t *>(kv_smem) + (((i * NT + r / 8) * 4 + ((d & 15) >> 3)) * 32 + (r & 7) * 4 + (d >> 4)) * 4 + ((d & 7) >> 1);
             dst[0] = hi;
@@ -498,7 +548,7 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 8 * nt + 2 * t + e;
-            lo[nt][e] = hi[nt][e] = 0;
+            lo[nt][e] = 0, hi[nt][e] = 1 << 30;                      // a row that does not exist: nothing reads its sums
             if (r < live) seen(a, p, (rg * RG + r) / per, lo[nt][e], hi[nt][e]);
             qs[nt][e] = q_scale[r];
             mx[nt][e] = -INFINITY;
@@ -517,7 +567,7 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
     // (entries 0, 1) and 2 i + 1 (entries 2, 3)
     auto softmax = [&](int b, float (&x)[2][NT][4], float (&f)[NT][2]) {
         const int pos0 = kBlk * b;
-        if (pos0 < all_lo || pos0 + kBlk > all_hi || live < RG) {
+        if (pos0 < all_lo || pos0 + kBlk > all_hi) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -555,33 +605,8 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
     // values and weights as three bf16 parts (fp32's range, so that no token's size touches another's precision). A
     // token that holds an infinity or a NaN makes the rows that see it NaN; its own numbers enter as 0. ----
     if (has_tail) {
-        constexpr int kSteps = S::kTailCh / 16;                      // steps of the first product, channel tiles of the second
-        const bool active = warp * S::kTailCh < HD;
-        const int rows = p.L + p.n - kBlk * p.z;
-        const int c = warp * kSteps / 4, j0 = warp * kSteps % 4;     // steps 4 c + j0 ..
         float *mine = reinterpret_cast<float *>(ring + (kRing - S::kHold) * kUnit);   // [48][RG]: slots held back
-        // key of row g of matrix m (of 6): thread t's inputs of step s are then the keys 16 s + 4 t .. + 3
-        auto tail_key = [&](int m) { return 16 * (m >> 1) + 4 * (g >> 1) + 2 * (m & 1) + (g & 1); };
-        float4 kr[6][kSteps], vr[kSteps][2][3];
-#pragma unroll
-        for (int m = 0; m < 6; ++m)
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                kr[m][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (active && tail_key(m) < rows)
-                    kr[m][i] = *reinterpret_cast<const float4 *>(w.kt + (size_t)tail_key(m) * HD + 64 * c + 16 * t + 4 * (j0 + i));
-            }
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int st = 0; st < 3; ++st) {
-                    vr[i][k][st] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (active && 16 * st + 4 * t < rows)
-                        vr[i][k][st] = *reinterpret_cast<const float4 *>(w.vt + (size_t)(16 * (warp * kSteps + i) + g + 8 * k) * kTail + 16 * st + 4 * t);
-                }
-        if (active) {
+        if (tactive) {
             uint32_t poison[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
@@ -593,8 +618,8 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int key = 16 * st + 4 * t + e;
-                            if (key >= rows || !isfinite(v[e])) {
-                                if (key < rows) poison[key >> 5] |= 1u << (key & 31);
+                            if (key >= trows || !isfinite(v[e])) {
+                                if (key < trows) poison[key >> 5] |= 1u << (key & 31);
                                 v[e] = 0.f;
                             }
                         }
@@ -626,11 +651,11 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
                 for (int nt = 0; nt < NT; ++nt) x[mt][nt][0] = x[mt][nt][1] = x[mt][nt][2] = x[mt][nt][3] = 0.f;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const int j = j0 + i;
+                const int j = tj0 + i;
                 uint2 qh[NT], ql[NT];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const uint2 *f = reinterpret_cast<const uint2 *>(qf + ((c * NT + nt) * 4 + (j >> 1)) * 32) + (j & 1);
+                    const uint2 *f = reinterpret_cast<const uint2 *>(qf + ((tc * NT + nt) * 4 + (j >> 1)) * 32) + (j & 1);
                     qh[nt] = f[0];
                     ql[nt] = f[2 * 32 * 2];
                 }
@@ -664,14 +689,14 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
         __syncthreads();
         constexpr int kParts = HD / S::kTailCh;
         float *first = mine - warp * (kRing * kUnit / 4);
-        for (int e = tid; e < kTail * RG; e += kAttnWarpsKv * 32) {
+        for (int e = tid; e < kTail * RG; e += kW * 32) {
             float x = 0.f;
 #pragma unroll
             for (int i = 0; i < kParts; ++i) x += first[i * (kRing * kUnit / 4) + e];
             first[e] = x;
         }
         __syncthreads();
-        if (active) {
+        if (tactive) {
             uint32_t pf[NT][3][2][3];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -700,8 +725,8 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
                     sum[1] = group_sum(sum[1]);
                     const int r = 8 * nt + 2 * t + e;
                     if (warp == 0 && g == 0) {
-                        sm_m[kAttnWarpsKv][r] = top;
-                        sm_l[kAttnWarpsKv][r] = sum[0] + sum[1];
+                        sm_m[kW][r] = top;
+                        sm_l[kW][r] = sum[0] + sum[1];
                         if (keep_lse && r < per)
                             for (int i = 0; i < 2; ++i)
                                 if (p.z + i < p.b0 + p.nb) lse[(size_t)(p.z + i) * 16 + r] = sum[i] == 0.f ? -INFINITY : ref + log2f(sum[i]);
@@ -759,11 +784,10 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
         for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
     // Values are summed in units of v_ref, the largest value scale so far: a block's weights are multiplied by its scale /
     // v_ref before they are split into halves, so the products add straight to the sums.
-    float ks = 0.f, vs = 0.f, v_ref = 0.f;
+    float v_ref = 0.f;
     for (int i = 0; i < ncoded; ++i) {
         if ((i & 31) == 0) {                                         // the next 32 blocks' scales
-            ks = vs = 0.f;
-            if (i + lane < ncoded) ks = w.ks[phys], vs = w.vs[phys];
+            if (i > 0) load_scales(i);
             float top = isnan(vs) ? 0.f : vs;
 #pragma unroll
             for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
@@ -779,7 +803,7 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
             }
             vs = v_ref > 0.f ? vs / v_ref : vs;
         }
-        const int b = bfirst + kAttnWarpsKv * i;
+        const int b = bfirst + kW * i;
         const float bks = __shfl_sync(0xffffffffu, ks, i & 31);
         float bvs = __shfl_sync(0xffffffffu, vs, i & 31);
         cp_async_wait_groups<kRing - 1>();
@@ -800,25 +824,29 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
                     *reinterpret_cast<uint4 *>(ql[nt]) = qf[((c * NT + nt) * 4 + 2 + half) * 32];
                 }
 #pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
+                for (int jj = 0; jj < 2; ++jj) {                     // four products of different sums, then their low halves
                     const int j = 2 * half + jj;
+                    uint32_t af[2][4];
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt) {
-                        const uint32_t af[4] = {codes_lo(kw[2 * mt][j]), codes_lo(kw[2 * mt + 1][j]), codes_hi(kw[2 * mt][j]), codes_hi(kw[2 * mt + 1][j])};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if (c == 0 && j == 0) {
-                                mma_f16_zero(x[mt][nt], af, qh[nt][0], qh[nt][1]);
-                                if (NT == 1)
-                                    mma_f16_zero(xl[mt][nt], af, ql[nt][0], ql[nt][1]);
-                                else
-                                    mma_f16(x[mt][nt], af, ql[nt][0], ql[nt][1]);
-                            } else {
-                                mma_f16(x[mt][nt], af, qh[nt][2 * jj], qh[nt][2 * jj + 1]);
-                                mma_f16(NT == 1 ? xl[mt][nt] : x[mt][nt], af, ql[nt][2 * jj], ql[nt][2 * jj + 1]);
-                            }
-                        }
+                        af[mt][0] = codes_lo(kw[2 * mt][j]);
+                        af[mt][1] = codes_lo(kw[2 * mt + 1][j]);
+                        af[mt][2] = codes_hi(kw[2 * mt][j]);
+                        af[mt][3] = codes_hi(kw[2 * mt + 1][j]);
                     }
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float(&d)[4] = part && NT == 1 ? xl[mt][nt] : x[mt][nt];
+                                const uint32_t b0 = part ? ql[nt][2 * jj] : qh[nt][2 * jj], b1 = part ? ql[nt][2 * jj + 1] : qh[nt][2 * jj + 1];
+                                if (c == 0 && j == 0 && (part == 0 || NT == 1))
+                                    mma_f16_zero(d, af[mt], b0, b1);
+                                else
+                                    mma_f16(d, af[mt], b0, b1);
+                            }
                 }
             }
         }
@@ -869,18 +897,25 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
         cp_async_wait_groups<kRing - 1>();
         __syncwarp();
         const uint8_t *V = take + g * kBlk + 8 * t;
+        constexpr int kG = NT == 1 ? 4 : 2;                          // channel tiles at once: four different sums
 #pragma unroll
-        for (int mt = 0; mt < HD / 16; ++mt) {
-            const uint2 v0 = *reinterpret_cast<const uint2 *>(V + (16 * mt) * kBlk), v1 = *reinterpret_cast<const uint2 *>(V + (16 * mt + 8) * kBlk);
-            const uint32_t a0[4] = {codes_lo(v0.x), codes_lo(v1.x), codes_hi(v0.x), codes_hi(v1.x)};
-            const uint32_t a1[4] = {codes_lo(v0.y), codes_lo(v1.y), codes_hi(v0.y), codes_hi(v1.y)};
+        for (int m0 = 0; m0 < HD / 16; m0 += kG) {
+            uint32_t af[kG][2][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma_f16(o[mt][nt], a0, ph[nt][0][0], ph[nt][0][1]);
-                mma_f16(o[mt][nt], a0, pl[nt][0][0], pl[nt][0][1]);
-                mma_f16(o[mt][nt], a1, ph[nt][1][0], ph[nt][1][1]);
-                mma_f16(o[mt][nt], a1, pl[nt][1][0], pl[nt][1][1]);
+            for (int i = 0; i < kG; ++i) {
+                const uint2 v0 = *reinterpret_cast<const uint2 *>(V + (16 * (m0 + i)) * kBlk), v1 = *reinterpret_cast<const uint2 *>(V + (16 * (m0 + i) + 8) * kBlk);
+                af[i][0][0] = codes_lo(v0.x), af[i][0][1] = codes_lo(v1.x), af[i][0][2] = codes_hi(v0.x), af[i][0][3] = codes_hi(v1.x);
+                af[i][1][0] = codes_lo(v0.y), af[i][1][1] = codes_lo(v1.y), af[i][1][2] = codes_hi(v0.y), af[i][1][3] = codes_hi(v1.y);
             }
+#pragma unroll
+            for (int st = 0; st < 2; ++st)
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int i = 0; i < kG; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16(o[m0 + i][nt], af[i][st], part ? pl[nt][st][0] : ph[nt][st][0], part ? pl[nt][st][1] : ph[nt][st][1]);
         }
         __syncwarp();
         taken();
@@ -911,29 +946,37 @@ __global__ void __launch_bounds__(kAttnWarpsKv * 32, AttnShape<HD, NT>::kCtas) k
         a.part_bad[at] = sm_bad;
     }
     if (sm_bad) return;
-    for (int e = tid; e < min(live, RG) * HD; e += kAttnWarpsKv * 32) {
-        const int r = e / HD, d = e % HD;
-        float top = -INFINITY, sum = 0.f, total = 0.f;
+    if (tid < RG) {   // each state's factor, in place of its maximum; the sum, in place of the first one
+        float top = -INFINITY, total = 0.f;
 #pragma unroll
-        for (int i = 0; i <= kAttnWarpsKv; ++i) top = fmaxf(top, sm_m[i][r]);
+        for (int i = 0; i <= kW; ++i) top = fmaxf(top, sm_m[i][tid]);
 #pragma unroll
-        for (int i = 0; i < kAttnWarpsKv; ++i) {
-            const float f = sm_m[i][r] == top ? 1.f : ex2(sm_m[i][r] - top);
-            total = fmaf(sm_l[i][r], f, total);
-            sum = fmaf(reinterpret_cast<const float *>(kv_smem)[(i * RG + r) * kPitch + d], f, sum);
+        for (int i = 0; i <= kW; ++i) {
+            const float f = sm_m[i][tid] == top ? 1.f : ex2(sm_m[i][tid] - top);
+            sm_m[i][tid] = f;
+            total = fmaf(sm_l[i][tid], f, total);
         }
-        if (has_tail) {
-            const float f = sm_m[kAttnWarpsKv][r] == top ? 1.f : ex2(sm_m[kAttnWarpsKv][r] - top);
-            total = fmaf(sm_l[kAttnWarpsKv][r], f, total);
-            sum = fmaf(a.part_tail[(unit * RG + r) * HD + d], f, sum);
-        }
+        sm_l[0][tid] = total;
+        *reinterpret_cast<float2 *>(a.part_ml + (at * RG + tid) * 2) = make_float2(top, total);
+    }
+    __syncthreads();
+    for (int e = tid; e < min(live, RG) * (HD / 4); e += kW * 32) {
+        const int r = e / (HD / 4), d = 4 * (e % (HD / 4));
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](const float4 &y, float f) {
+            sum.x = fmaf(y.x, f, sum.x), sum.y = fmaf(y.y, f, sum.y), sum.z = fmaf(y.z, f, sum.z), sum.w = fmaf(y.w, f, sum.w);
+        };
+        if (has_tail) add(*reinterpret_cast<const float4 *>(a.part_tail + (unit * RG + r) * HD + d), sm_m[kW][r]);
+#pragma unroll
+        for (int i = 0; i < kW; ++i) add(*reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(kv_smem) + (i * RG + r) * kPitch + d), sm_m[i][r]);
         if (nsplit == 1) {
             const int rid = rg * RG + r;
-            a.out[((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + d] = sum / total;
+            const float total = sm_l[0][r];
+            *reinterpret_cast<float4 *>(a.out + ((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + d) =
+                make_float4(sum.x / total, sum.y / total, sum.z / total, sum.w / total);
         } else {
-            a.part_o[(at * RG + r) * HD + d] = sum;
+            *reinterpret_cast<float4 *>(a.part_o + (at * RG + r) * HD + d) = sum;
         }
-        if (d == 0) a.part_ml[(at * RG + r) * 2] = top, a.part_ml[(at * RG + r) * 2 + 1] = total;
     }
 }
 
@@ -952,7 +995,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
     const KvView w = view(a.c, s, h);
     const Span p = span_of(a, s, w);
     if (p.bad) return;
-    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, nsplit = splits_of(a.splits, min(p.nb, max(0, p.z - p.b0)));
+    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, nsplit = splits_of<AttnShape<HD, NT>::kWarps>(a.splits, min(p.nb, max(0, p.z - p.b0)));
     const int b0 = p.b0 + (int(blockIdx.x) - RG) * kMergeThreads;
     if (live <= 0 || (row_part ? int(blockIdx.x) >= live || nsplit == 1 : b0 >= p.b0 + p.nb)) return;
     const size_t at = (((size_t)s * a.c.n_kv + h) * a.groups + rg) * a.splits;
@@ -1032,11 +1075,12 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int score) {
     t.nt = r > 8 ? 2 : 1;
     t.groups = (r + 8 * t.nt - 1) / (8 * t.nt);
     t.units = (size_t)c->n_seq * c->n_kv * t.groups;
-    const int slots = 152 * (c->head_dim == 256 ? 1 : 2), most = (c->n_blocks + kAttnWarpsKv - 1) / kAttnWarpsKv;
+    const int warps = c->head_dim == 128 && t.nt == 2 ? AttnShape<128, 2>::kWarps : AttnShape<128, 1>::kWarps;
+    const int slots = 152 * (c->head_dim == 256 ? 1 : 2), most = (c->n_blocks + warps - 1) / warps;
     double best = 0;
     for (int n = 1; n <= std::min(kMaxSplits, most); ++n) {
         const double waves = double((t.units * n + slots - 1) / slots);
-        const double cost = waves * (double(c->n_blocks) / kAttnWarpsKv / n + 6);
+        const double cost = waves * (double(c->n_blocks) / warps / n + 6);
         if (n == 1 || cost < best) best = cost, t.splits = n;
     }
     const size_t parts = t.units * t.splits * 8 * t.nt;
@@ -1061,7 +1105,7 @@ cudaError_t launch_kv8_attn(const AttnKvArgs &a, cudaStream_t s) {
         attr[dev] = true;
     }
     const unsigned heads = unsigned(a.c.n_kv * a.groups);
-    k_kv8_attn<HD, NT><<<dim3(a.splits, heads, a.c.n_seq), kAttnWarpsKv * 32, smem, s>>>(a);
+    k_kv8_attn<HD, NT><<<dim3(a.splits, heads, a.c.n_seq), AttnShape<HD, NT>::kWarps * 32, smem, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (a.splits == 1 && !a.score)) return e;
     const unsigned x = 8 * NT + (a.score ? (a.c.n_blocks + kMergeThreads - 1) / kMergeThreads : 0);
