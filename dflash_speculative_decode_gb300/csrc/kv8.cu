@@ -297,8 +297,8 @@ __device__ __forceinline__ void seen(const AttnKvArgs &a, const Span &p, int m, 
 // 16-row operand, query rows as the 8 columns: S^T = K Q^T and O^T = V^T P^T, so rows that a call does not
 // have cost at most 7 columns. Codes are whole numbers of at most 7 bits and exact in fp16; the block's
 // key scale multiplies the fp32 logits. A query row (scaled by a power of two to 2^14..2^15) and the weights
-// (2^14 for the row's largest, times the block's value scale over the largest one) enter as two fp16 halves,
-// hi + lo, which hold 22 bits, and nothing below 2^-25.
+// (2^7 and more for the row's largest, times the block's value scale over the largest one) enter as two fp16
+// halves, hi + lo, which hold 22 bits, and nothing below 2^-25.
 //
 // Fragment order. A thread (g = lane / 4, t = lane % 4) loads 16 consecutive channels of a key at once, so
 // channel 64 c + 16 t + 4 j + e is input 2t + e (e < 2) or 2t + 6 + e of the product's step 4 c + j, and
@@ -306,7 +306,7 @@ __device__ __forceinline__ void seen(const AttnKvArgs &a, const Span &p, int m, 
 // transposed weights of matrices 2 s and 2 s + 1 are then the inputs of step s of the second product, whose
 // thread t takes the keys 8 t + 4 s .. + 3, 8 consecutive codes of a value channel for both steps.
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kTop = 14.f;   // log2 of the largest weight
+constexpr float kTop = 7.f;    // log2 of the weight at a row's maximum
 
 template <int HD, int NT>
 struct AttnShape {
@@ -563,43 +563,6 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     float *lse = keep_lse ? a.blk_lse + ((size_t)s * a.c.n_kv + h) * w.nb * 16 : nullptr;
     const int key0 = 8 * (g >> 1) + (g & 1);                         // key of row g of matrix 0; matrix j: + 2 j
 
-    // logits (base 2) of block b -> weights x, factors f of what was summed before; x[i][nt]: matrices 2 i
-    // (entries 0, 1) and 2 i + 1 (entries 2, 3)
-    auto softmax = [&](int b, float (&x)[2][NT][4], float (&f)[NT][2]) {
-        const int pos0 = kBlk * b;
-        if (pos0 < all_lo || pos0 + kBlk > all_hi) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int pos = pos0 + key0 + 4 * i + 2 * (k >> 1);
-                        if (pos < lo[nt][k & 1] || pos >= hi[nt][k & 1]) x[i][nt][k] = -INFINITY;
-                    }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float top = group_max(fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e])));
-                const float now = fmaxf(mx[nt][e], top), ref = now == -INFINITY ? 0.f : now - kTop;
-                f[nt][e] = mx[nt][e] == now ? 1.f : ex2(mx[nt][e] - now);
-                mx[nt][e] = now;
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int k = e; k < 4; k += 2) sum += x[i][nt][k] = ex2(x[i][nt][k] - ref);
-                l[nt][e] = fmaf(l[nt][e], f[nt][e], sum);
-                if (keep_lse) {
-                    const float total = group_sum(sum);
-                    const int r = 8 * nt + 2 * t + e;
-                    if (g == 0 && r < per) lse[(size_t)b * 16 + r] = total == 0.f ? -INFINITY : ref + log2f(total);
-                }
-            }
-    };
-
     // ---- the tail (at most 48 fp32 rows, by the last split's CTA, while its first codes are on their way): a warp
     // takes kTailCh channels of every row. Keys enter as two fp16 halves, each scaled by a power of two of its own;
     // values and weights as three bf16 parts (fp32's range, so that no token's size touches another's precision). A
@@ -782,9 +745,11 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     for (int i = 0; i < HD / 16; ++i)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
-    // Values are summed in units of v_ref, the largest value scale so far: a block's weights are multiplied by its scale /
-    // v_ref before they are split into halves, so the products add straight to the sums.
-    float v_ref = 0.f;
+    // A row's weights are 2^(logit - mx + kTop). mx is a maximum that is only renewed when a weight would pass 2^15, so most
+    // blocks need no maximum across the lanes and rescale nothing: the row's largest weight lies in 2^7..2^15. Values are
+    // summed in units of v_ref, the largest value scale so far: the logarithm of a block's scale over v_ref is added to
+    // the exponent, so that the products add straight to the sums, and the sum of the weights takes it back.
+    float v_ref = 0.f, v_lb = 0.f, v_inv = 1.f;
     for (int i = 0; i < ncoded; ++i) {
         if ((i & 31) == 0) {                                         // the next 32 blocks' scales
             if (i > 0) load_scales(i);
@@ -801,11 +766,15 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
                         for (int k = 0; k < 4; ++k) o[mt][nt][k] *= f;
                 v_ref = top;
             }
-            vs = v_ref > 0.f ? vs / v_ref : vs;
+            // a block of zeros counts as any scale; one of 2^-60 and less adds nothing that fp32 could hold
+            const float r = vs > 0.f ? fmaxf(vs / v_ref, 8.673617e-19f) : 1.f;
+            v_lb = log2f(r);
+            v_inv = isnan(vs) ? vs : 1.f / r;
         }
         const int b = bfirst + kW * i;
         const float bks = __shfl_sync(0xffffffffu, ks, i & 31);
-        float bvs = __shfl_sync(0xffffffffu, vs, i & 31);
+        const float blb = __shfl_sync(0xffffffffu, v_lb, i & 31);
+        float binv = __shfl_sync(0xffffffffu, v_inv, i & 31);
         cp_async_wait_groups<kRing - 1>();
         __syncwarp();
         float x[2][NT][4], xl[2][NT][4];                             // by the query's hi and lo halves
@@ -853,47 +822,98 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         __syncwarp();
         taken();
         issue(2 * i + kRing);
-        float f[NT][2];
+        float y[2][NT][4], peak = -INFINITY;                         // exponents of the weights
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float z = bks * qs[nt][e];
+                const float z = bks * qs[nt][e], less = blb + kTop - mx[nt][e];   // +inf before a row's first key
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int k = e; k < 4; k += 2) x[j][nt][k] = (NT == 1 ? x[j][nt][k] + xl[j][nt][k] : x[j][nt][k]) * z;
+                    for (int k = e; k < 4; k += 2) {
+                        if (NT == 1) x[j][nt][k] += xl[j][nt][k];
+                        y[j][nt][k] = fmaf(x[j][nt][k], z, less);
+                    }
             }
-        softmax(b, x, f);
-        if (isnan(bvs)) {                                            // rows that see the block are NaN, the others take nothing of it
-            bvs = 0.f;
+        const int pos0 = kBlk * b;
+        if (pos0 < all_lo || pos0 + kBlk > all_hi) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int pos = pos0 + key0 + 4 * j + 2 * (k >> 1);
+                        if (pos < lo[nt][k & 1] || pos >= hi[nt][k & 1]) y[j][nt][k] = -INFINITY;
+                    }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) peak = fmaxf(peak, y[j][nt][k]);
+        if (__any_sync(0xffffffffu, peak > 15.f)) {                  // seldom, once the maxima have been met
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float z = bks * qs[nt][e];
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int k = e; k < 4; k += 2) {
+                            y[j][nt][k] = y[j][nt][k] == -INFINITY ? -INFINITY : x[j][nt][k] * z;
+                            top = fmaxf(top, y[j][nt][k]);
+                        }
+                    const float now = fmaxf(mx[nt][e], group_max(top)), f = mx[nt][e] == now ? 1.f : ex2(mx[nt][e] - now);
+                    const float less = now == -INFINITY ? 0.f : blb + kTop - now;
+                    mx[nt][e] = now;
+                    l[nt][e] *= f;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int k = e; k < 4; k += 2) y[j][nt][k] += less;
+#pragma unroll
+                    for (int mt = 0; mt < HD / 16; ++mt) o[mt][nt][e] *= f, o[mt][nt][2 + e] *= f;
+                }
+        }
+        if (isnan(binv)) {                                           // rows that see the block are NaN, the others take nothing of it
+            binv = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    if (lo[nt][e] < kBlk * (b + 1) && hi[nt][e] > kBlk * b) l[nt][e] = NAN;
+                    if (lo[nt][e] < pos0 + kBlk && hi[nt][e] > pos0) l[nt][e] = NAN;
         }
-        uint32_t ph[NT][2][2], pl[NT][2][2];                         // [step][input pair]
-        bool moved = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            moved = moved || f[nt][0] != 1.f || f[nt][1] != 1.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = e; k < 4; k += 2) sum += y[j][nt][k] = ex2(y[j][nt][k]);
+                l[nt][e] = fmaf(sum, binv, l[nt][e]);
+                if (keep_lse) {
+                    const float total = group_sum(sum) * binv;
+                    const int r = 8 * nt + 2 * t + e;
+                    if (g == 0 && r < per) lse[(size_t)b * 16 + r] = total == 0.f ? -INFINITY : mx[nt][e] - kTop + log2f(total);
+                }
+            }
+        uint32_t ph[NT][2][2], pl[NT][2][2];                         // [step][input pair]
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t hw, lw;
-                halves2(x[j >> 1][nt][2 * (j & 1)] * bvs, x[j >> 1][nt][2 * (j & 1) + 1] * bvs, hw, lw);
+                halves2(y[j >> 1][nt][2 * (j & 1)], y[j >> 1][nt][2 * (j & 1) + 1], hw, lw);
                 ph[nt][j >> 1][j & 1] = transpose8x8(hw);
                 pl[nt][j >> 1][j & 1] = transpose8x8(lw);
             }
-        }
-        if (__any_sync(0xffffffffu, moved)) {                        // seldom, once the maxima have been met
-#pragma unroll
-            for (int mt = 0; mt < HD / 16; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) o[mt][nt][k] *= f[nt][k & 1];
-        }
         cp_async_wait_groups<kRing - 1>();
         __syncwarp();
         const uint8_t *V = take + g * kBlk + 8 * t;

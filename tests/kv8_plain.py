@@ -82,8 +82,8 @@ class Head:
             d = (np.abs(q[m]).astype(np.float64) @ np.abs(k[lo:hi]).T * abs(scale)).max(-1, keepdims=True) * ((hd + 16) * 2.0 ** -24 + 2.0 ** -21)
             rel = 4 * d + (hi - lo + 64) * 2.0 ** -23
             # A weight has no relative precision below the smallest numbers: fp32 holds multiples of 2^-149 (or nothing below
-            # 2^-126), and the halves hold weights, at 2^14 for the row's largest, to 2^-25: 2^-39 of the largest weight.
-            low = p.max(-1, keepdims=True) * 2.0 ** -39 + 2.0 ** -126
+            # 2^-126), and the halves hold weights, at 2^7 or more for the row's largest, to 2^-25: 2^-32 of it.
+            low = p.max(-1, keepdims=True) * 2.0 ** -32 + 2.0 ** -126
             bound[m] = rel * (p @ np.abs(v[lo:hi])) + low * np.abs(v[lo:hi]).sum(0) + 1e-30
             if m == 0:
                 at = np.arange(lo, hi) // BLOCK
