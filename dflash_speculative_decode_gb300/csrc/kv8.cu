@@ -83,7 +83,7 @@ struct WriteArgs {
 struct Plan {
     int z, have, n, full, cut, bad;
 };
-__device__ __forceinline__ Plan plan_of(const WriteArgs &a, int s, const KvView &w, int *err) {
+__device__ __forceinline__ Plan plan_of(const WriteArgs &a, int s, const KvView &w) {
     Plan p{};
     const int L = a.len[s], zs = *w.sealed;
     p.n = rows_of(a.cnt, s, a.rows);
@@ -102,103 +102,152 @@ __device__ __forceinline__ Plan plan_of(const WriteArgs &a, int s, const KvView 
     return p;
 }
 
-constexpr int kWriteThreads = 512;       // 256 for the keys, 256 for the values
-
-// One CTA per head: it seals the head's blocks one after another, then moves the rest to the tail.
-__global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a) {
-    __shared__ float red[2][8];
-    __shared__ int bad[2];
-    __shared__ int tab_bad;
-    const int h = blockIdx.x, s = blockIdx.y, hd = a.c.head_dim;
-    const bool is_v = threadIdx.x >= 256;
-    const int tid = threadIdx.x & 255, lane = tid & 31, warp = tid >> 5;
-    KvView w = view(a.c, s, h);
-    Plan p = plan_of(a, s, w, a.c.err);
-    if (threadIdx.x == 0) tab_bad = 0;
-    __syncthreads();
-    if (!p.bad)   // every table entry that the call follows
-        for (int b = threadIdx.x; b < max(p.full, p.cut); b += blockDim.x)
-            if (unsigned(w.table[p.z + b]) >= unsigned(w.nb)) tab_bad = 1;
-    __syncthreads();
-    if (tab_bad) p.bad = kErrTable;
-    if (p.bad) {
-        if (threadIdx.x == 0) atomicOr(a.c.err, p.bad);
-        return;
-    }
-    const float *src = (is_v ? a.v : a.k) + (size_t)s * a.rows * a.ld + (size_t)h * hd;
-    float *tail = is_v ? w.vt : w.kt;
-    uint8_t *codes = is_v ? w.v : w.k;
-    float *scales = is_v ? w.vs : w.ks;
-    const size_t blk = (size_t)kBlk * hd;
-    const int cut_phys = p.cut ? w.table[p.z] : 0;
-    const uint8_t *old = codes + cut_phys * blk;
-    const float old_scale = p.cut ? scales[cut_phys] : 0.f;
-    auto row = [&](int r, int d) -> float {   // token 32 z + r, channel d
-        if (r >= p.have) return src[(size_t)(r - p.have) * a.ld + d];
-        if (p.cut) return expand(old[is_v ? v_at(r, d) : k_at(r, d)], old_scale);
-        return is_v ? tail[(size_t)d * kTail + r] : tail[(size_t)r * hd + d];
-    };
-    const int dgroups = hd / 4;              // a thread takes 4 channels (keys) or 4 tokens (values) at a time
-    for (int b = 0; b < p.full; ++b) {
-        float x[8][4];
-        float amax = 0.f;
-        int nonfinite = 0;
-        for (int i = 0; i < hd / 32; ++i) {
-            const int e = i * 256 + tid;
+// Channels d..d+3 of token 32 z + r of a head, keys (V = false) or values.
+template <bool V>
+struct Rows {
+    const float *src;        // the call's rows of this head
+    int64_t ld;
+    const float *tail;
+    const uint8_t *old;      // after a cut: block z's codes and scale
+    float old_scale;
+    int have, cut, hd;
+    __device__ __forceinline__ float4 get(int r, int d) const {
+        if (r >= have) return *reinterpret_cast<const float4 *>(src + (size_t)(r - have) * ld + d);
+        float y[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = is_v ? 4 * (e / hd) + j : e / dgroups;
-                const int d = is_v ? e % hd : 4 * (e % dgroups) + j;
-                const float f = row(kBlk * b + t, d);
-                x[i][j] = f;
-                if (isfinite(f))
-                    amax = fmaxf(amax, fabsf(f));
-                else
-                    nonfinite = 1;
+        for (int k = 0; k < 4; ++k) y[k] = cut ? expand(old[V ? v_at(r, d + k) : k_at(r, d + k)], old_scale) : V ? tail[(size_t)(d + k) * kTail + r] : tail[(size_t)r * hd + d + k];
+        return make_float4(y[0], y[1], y[2], y[3]);
+    }
+};
+template <bool V>
+__device__ __forceinline__ Rows<V> rows_from(const WriteArgs &a, int s, int h, const KvView &w, const Plan &p) {
+    const int hd = a.c.head_dim, phys = p.cut ? w.table[p.z] : 0;
+    return {(V ? a.v : a.k) + (size_t)s * a.rows * a.ld + (size_t)h * hd, a.ld, V ? w.vt : w.kt, (V ? w.v : w.k) + (size_t)phys * kBlk * hd,
+            p.cut ? (V ? w.vs : w.ks)[phys] : 0.f, p.have, p.cut, hd};
+}
+
+constexpr int kWriteThreads = 256;
+
+// Seals block b of the plan: 256 threads, a thread holds 4 tokens x 4 channels at a time. The codes go through shared
+// memory, so that they leave in 16-byte stores whatever their layout.
+template <bool V>
+__device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView &w, int phys, float *red, uint8_t *code) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hd = x.hd, dq = hd / 4;
+    float4 y[2][4];
+    float amax = 0.f;
+    bool fin = true;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = i * kWriteThreads + tid;                       // of 8 * hd / 4 pieces
+        if (e < 8 * dq) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[i][k] = x.get(kBlk * b + 4 * (e / dq) + k, 4 * (e % dq));
+                const float4 v = y[i][k];
+                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+                fin = fin && isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w);
             }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        __syncthreads();
-        if (tid == 0) bad[is_v] = 0;
-        if (lane == 0) red[is_v][warp] = amax;
-        __syncthreads();
-        if (nonfinite) bad[is_v] = 1;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, red[is_v][i]);
-        const float scale = bad[is_v] ? NAN : __fdiv_rn(amax, 127.f);
-        const float inv = scale > 0.f ? 1.f / scale : 0.f;
-        const int phys = w.table[p.z + b];
-        uint8_t *dst = codes + phys * blk;
-        for (int i = 0; i < hd / 32; ++i) {
-            const int e = i * 256 + tid;
-            uint32_t word = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) word |= (scale > 0.f ? code_of(x[i][j], scale, inv) : 128u) << (8 * j);
-            const int at = is_v ? v_at(4 * (e / hd), e % hd) : k_at(e / dgroups, 4 * (e % dgroups));
-            *reinterpret_cast<uint32_t *>(dst + at) = word;
-        }
-        if (tid == 0) scales[phys] = scale;
     }
-    __syncthreads();   // block 0 has read the tail's first rows
-    // The rest moves to the tail's front. A row that comes from the tail lies 32 * full >= 32 rows further
-    // back, behind all rows written here, or is where it belongs.
-    const int left = p.have + p.n - kBlk * p.full;
-    for (int e = tid; e < left * hd; e += 256) {
-        const int t = e / hd, d = e % hd, r = kBlk * p.full + t;
-        if (!p.cut && p.full == 0 && r < p.have) continue;
-        const float f = row(r, d);
-        if (is_v)
-            tail[(size_t)d * kTail + t] = f;
-        else
-            tail[(size_t)t * hd + d] = f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (lane == 0) red[warp] = amax;
+    const bool ok = __syncthreads_and(fin);
+#pragma unroll
+    for (int i = 0; i < kWriteThreads / 32; ++i) amax = fmaxf(amax, red[i]);
+    const float scale = ok ? __fdiv_rn(amax, 127.f) : NAN, inv = scale > 0.f ? 1.f / scale : 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = i * kWriteThreads + tid, t = 4 * (e / dq), d = 4 * (e % dq);
+        if (e < 8 * dq) {
+            uint32_t q[4][4];                                        // [token][channel]
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float v[4] = {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) q[k][c] = scale > 0.f ? code_of(v[c], scale, inv) : 128u;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t word = V ? q[0][k] | q[1][k] << 8 | q[2][k] << 16 | q[3][k] << 24 : q[k][0] | q[k][1] << 8 | q[k][2] << 16 | q[k][3] << 24;
+                *reinterpret_cast<uint32_t *>(code + (V ? v_at(t, d + k) : k_at(t + k, d))) = word;
+            }
+        }
+    }
+    __syncthreads();
+    uint4 *dst = reinterpret_cast<uint4 *>((V ? w.v : w.k) + (size_t)phys * kBlk * hd);
+    for (int e = tid; e < 2 * hd; e += kWriteThreads) dst[e] = reinterpret_cast<const uint4 *>(code)[e];
+    if (tid == 0) (V ? w.vs : w.ks)[phys] = scale;
+}
+
+// A head whose plan follows a table entry out of range is left alone.
+__device__ __forceinline__ bool bad_table(const KvView &w, const Plan &p) {
+    int bad = 0;
+    for (int b = threadIdx.x; b < max(p.full, p.cut); b += blockDim.x) bad |= unsigned(w.table[p.z + b]) >= unsigned(w.nb);
+    return __syncthreads_or(bad);
+}
+
+// Seals an append's blocks, one CTA for the keys or the values of each: grid (2 x blocks, heads, sequences).
+__global__ void __launch_bounds__(kWriteThreads) k_kv8_seal(WriteArgs a) {
+    __shared__ float red[kWriteThreads / 32];
+    __shared__ __align__(16) uint8_t code[kBlk * 256];
+    const int b = blockIdx.x >> 1, h = blockIdx.y, s = blockIdx.z;
+    const KvView w = view(a.c, s, h);
+    const Plan p = plan_of(a, s, w);
+    pdl_trigger();
+    if (p.bad || b >= p.full || bad_table(w, p)) return;            // the launch behind reports what is bad
+    const int phys = w.table[p.z + b];
+    if (blockIdx.x & 1)
+        seal_block<true>(rows_from<true>(a, s, h, w, p), b, w, phys, red, code);
+    else
+        seal_block<false>(rows_from<false>(a, s, h, w, p), b, w, phys, red, code);
+}
+
+// What is left of a call, one CTA per head: seals its blocks unless k_kv8_seal has (sealed_before), moves the rest to the
+// tail's front, starts the scores of new blocks and counts. A row that comes from the tail lies 32 * full >= 32 rows
+// further back than its place, behind all rows written here, or is where it belongs.
+__global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a, int sealed_before) {
+    __shared__ float red[kWriteThreads / 32];
+    __shared__ __align__(16) uint8_t code[kBlk * 256];
+    const int h = blockIdx.x, s = blockIdx.y, hd = a.c.head_dim, tid = threadIdx.x;
+    const KvView w = view(a.c, s, h);
+    Plan p = plan_of(a, s, w);
+    if (!p.bad && bad_table(w, p)) p.bad = kErrTable;
+    if (sealed_before) pdl_wait();   // k_kv8_seal has read the tail
+    if (p.bad) {
+        if (tid == 0) atomicOr(a.c.err, p.bad);
+        return;
+    }
+    const Rows<false> xk = rows_from<false>(a, s, h, w, p);
+    const Rows<true> xv = rows_from<true>(a, s, h, w, p);
+    if (!sealed_before)
+        for (int b = 0; b < p.full; ++b) {
+            const int phys = w.table[p.z + b];
+            seal_block<false>(xk, b, w, phys, red, code);
+            __syncthreads();
+            seal_block<true>(xv, b, w, phys, red, code);
+            __syncthreads();
+        }
+    const int left = p.have + p.n - kBlk * p.full, first = !p.cut && p.full == 0 ? p.have : 0;
+    const int dq = hd / 4;
+    for (int e = tid; e < (left - first) * dq; e += kWriteThreads) {
+        const int t = first + e / dq, d = 4 * (e % dq);
+        *reinterpret_cast<float4 *>(w.kt + (size_t)t * hd + d) = xk.get(kBlk * p.full + t, d);
+    }
+    for (int e = tid; e < (left - first) * dq; e += kWriteThreads) {
+        const int t = first + e / dq, d = 4 * (e % dq);
+        const float4 y = xv.get(kBlk * p.full + t, d);
+        w.vt[(size_t)(d + 0) * kTail + t] = y.x;
+        w.vt[(size_t)(d + 1) * kTail + t] = y.y;
+        w.vt[(size_t)(d + 2) * kTail + t] = y.z;
+        w.vt[(size_t)(d + 3) * kTail + t] = y.w;
     }
     if (w.score) {
         const int L = a.len[s];
-        for (int b = (L + kBlk - 1) / kBlk + threadIdx.x; b * kBlk < L + p.n; b += blockDim.x) w.score[b] = 0.f;
+        for (int b = (L + kBlk - 1) / kBlk + tid; b * kBlk < L + p.n; b += kWriteThreads) w.score[b] = 0.f;
     }
-    if (threadIdx.x == 0) *w.sealed = p.z + p.full;
+    __syncthreads();   // every thread has read the count
+    if (tid == 0) *w.sealed = p.z + p.full;
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -213,6 +262,7 @@ struct ReadArgs {
 
 // One CTA per 32-token block of the range and head: grid (blocks, heads, sequences).
 __global__ void __launch_bounds__(256) k_kv8_read(ReadArgs a) {
+    __shared__ uint32_t vcode[256 * 9];
     const int h = blockIdx.y, s = blockIdx.z, hd = a.c.head_dim;
     const KvView w = view(a.c, s, h);
     const int L = a.len[s], first = a.first ? a.first[s] : 0, z = *w.sealed;
@@ -231,20 +281,44 @@ __global__ void __launch_bounds__(256) k_kv8_read(ReadArgs a) {
         return;
     }
     const int hi = int(min((long long)L, (long long)first + a.rows));
-    const size_t blk = (size_t)kBlk * hd;
-    const int phys = b < z ? w.table[b] : 0;
-    const float ks = b < z ? w.ks[phys] : 0.f, vs = b < z ? w.vs[phys] : 0.f;
-    for (int e = threadIdx.x; e < kBlk * hd; e += blockDim.x) {
-        const int t = e / hd, d = e % hd, pos = kBlk * b + t;
-        if (pos < first || pos >= hi) continue;
-        const size_t o = (((size_t)s * a.rows + (pos - first)) * a.c.n_kv + h) * hd + d;
-        if (b < z) {
-            a.k[o] = expand(w.k[phys * blk + k_at(t, d)], ks);
-            a.v[o] = expand(w.v[phys * blk + v_at(t, d)], vs);
-        } else {
-            const int r = pos - kBlk * z;
-            a.k[o] = w.kt[(size_t)r * hd + d];
-            a.v[o] = w.vt[(size_t)d * kTail + r];
+    const int dq = hd / 4, pos0 = kBlk * b;
+    const size_t blk = (size_t)kBlk * hd, row = (size_t)a.c.n_kv * hd, out0 = ((size_t)s * a.rows * a.c.n_kv + h) * hd;
+    auto put = [&](float *out, int t, int d, const float4 &y) {      // token t of the block, channels d..
+        const int pos = pos0 + t;
+        if (pos >= first && pos < hi) *reinterpret_cast<float4 *>(out + out0 + (size_t)(pos - first) * row + d) = y;
+    };
+    if (b < z) {
+        const int phys = w.table[b];
+        const float ks = w.ks[phys], vs = w.vs[phys];
+        const uint4 *kc = reinterpret_cast<const uint4 *>(w.k + phys * blk), *vc = reinterpret_cast<const uint4 *>(w.v + phys * blk);
+        for (int e = threadIdx.x; e < 2 * hd; e += blockDim.x) {     // a channel's 32 tokens, 36 bytes apart
+            const uint4 y = vc[e];
+            uint32_t *dst = vcode + (e >> 1) * 9 + 4 * (e & 1);
+            dst[0] = y.x, dst[1] = y.y, dst[2] = y.z, dst[3] = y.w;
+        }
+        auto four = [](uint32_t x, float f) {
+            return make_float4(expand(x & 255, f), expand(x >> 8 & 255, f), expand(x >> 16 & 255, f), expand(x >> 24, f));
+        };
+        for (int e = threadIdx.x; e < kBlk * dq; e += blockDim.x) {  // four channels of a token
+            const int t = e / dq, d = 4 * (e % dq);
+            put(a.k, t, d, four(reinterpret_cast<const uint32_t *>(kc)[k_at(t, d) >> 2], ks));
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < 8 * dq; e += blockDim.x) {     // four tokens of four channels
+            const int t = 4 * (e / dq), d = 4 * (e % dq);
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = vcode[(d + k) * 9 + (t >> 2)];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                put(a.v, t + k, d, make_float4(expand(x[0] >> 8 * k & 255, vs), expand(x[1] >> 8 * k & 255, vs), expand(x[2] >> 8 * k & 255, vs), expand(x[3] >> 8 * k & 255, vs)));
+        }
+    } else {
+        for (int e = threadIdx.x; e < kBlk * dq; e += blockDim.x) {
+            const int t = e / dq, d = 4 * (e % dq), r = pos0 + t - kBlk * z;
+            if (pos0 + t >= hi) break;
+            put(a.k, t, d, *reinterpret_cast<const float4 *>(w.kt + (size_t)r * hd + d));
+            put(a.v, t, d, make_float4(w.vt[(size_t)d * kTail + r], w.vt[(size_t)(d + 1) * kTail + r], w.vt[(size_t)(d + 2) * kTail + r], w.vt[(size_t)(d + 3) * kTail + r]));
         }
     }
 }
@@ -445,16 +519,18 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     const int ncoded = max(0, (x1 - x0 - warp + kW - 1) / kW);
     const size_t unit = ((size_t)s * a.c.n_kv + h) * a.groups + rg, at = unit * a.splits + split;
 
-    int phys = 0, bad = 0;
+    int bad = 0;
     auto load_phys = [&](int i0) {                                   // lane l: where block i0 + l is stored
         const int i = i0 + lane;
-        phys = 0;
+        int at = 0;
         if (i < ncoded) {
-            phys = w.table[bfirst + kW * i];
-            if (unsigned(phys) >= unsigned(w.nb)) phys = 0, bad = 1;
+            at = w.table[bfirst + kW * i];
+            if (unsigned(at) >= unsigned(w.nb)) at = 0, bad = 1;
         }
+        return at;
     };
-    load_phys(0);
+    int phys = load_phys(0);                                         // of the window of 32 blocks that is being asked for
+    int phys_next = load_phys(32);                                   // and of the one behind it
     // the tail's rows: a warp takes kTailCh channels, steps 4 tc + tj0 .. of the first product, and of it the key of
     // row g of matrix m (of 6), which makes thread t's inputs of step s the keys 16 s + 4 t .. + 3
     constexpr int kSteps = S::kTailCh / 16;
@@ -479,12 +555,9 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
                     vr[i][k][st] = *reinterpret_cast<const float4 *>(w.vt + (size_t)(16 * (warp * kSteps + i) + g + 8 * k) * kTail + 16 * st + 4 * t);
             }
     }
-    float ks = 0.f, vs = 0.f;                                        // lane l: scales of block i + l of the window
-    auto load_scales = [&](int i0) {
-        ks = vs = 0.f;
-        if (i0 + lane < ncoded) ks = w.ks[phys], vs = w.vs[phys];
-    };
-    load_scales(0);
+    float ks = 0.f, vs = 0.f;                                        // lane l: scales of block l of the window that is read
+    if (lane < ncoded) ks = w.ks[phys], vs = w.vs[phys];
+    float ks_next = 0.f, vs_next = 0.f;
 
     // ---- codes on their way: unit 2 i is block i's keys, unit 2 i + 1 its values ----
     uint8_t *ring = kv_smem + S::kQBytes + warp * kRing * kUnit;
@@ -493,7 +566,10 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     auto issue = [&](int u) {
         const int i = u >> 1;
         if (i < ncoded) {
-            if ((u & 63) == 0 && u > 0) load_phys(i);
+            if ((u & 63) == 0 && u > 0) {
+                phys = phys_next;
+                phys_next = load_phys(i + 32);
+            }
             const size_t off = (size_t)__shfl_sync(0xffffffffu, phys, i & 31) * kUnit;
             const uint8_t *src = ((u & 1) ? w.v : w.k) + off + 16 * lane;
 #pragma unroll
@@ -752,7 +828,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     float v_ref = 0.f, v_lb = 0.f, v_inv = 1.f;
     for (int i = 0; i < ncoded; ++i) {
         if ((i & 31) == 0) {                                         // the next 32 blocks' scales
-            if (i > 0) load_scales(i);
+            if (i > 0) ks = ks_next, vs = vs_next;
             float top = isnan(vs) ? 0.f : vs;
 #pragma unroll
             for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
@@ -770,6 +846,10 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
             const float r = vs > 0.f ? fmaxf(vs / v_ref, 8.673617e-19f) : 1.f;
             v_lb = log2f(r);
             v_inv = isnan(vs) ? vs : 1.f / r;
+        }
+        if ((i & 31) == 16) {                                        // the next window's, half a window ahead
+            ks_next = vs_next = 0.f;
+            if (i + 16 + lane < ncoded) ks_next = w.ks[phys_next], vs_next = w.vs[phys_next];
         }
         const int b = bfirst + kW * i;
         const float bks = __shfl_sync(0xffffffffu, ks, i & 31);
@@ -1011,15 +1091,14 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
     __shared__ float fac[kMaxSplits], top_s[16], total_s[16];
     const int h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
     const bool row_part = blockIdx.x < RG;
-    if (!row_part && rg) return;
     const KvView w = view(a.c, s, h);
     const Span p = span_of(a, s, w);
-    if (p.bad) return;
+    pdl_wait();   // by every CTA, so that this grid does not end before the one it follows
+    if (p.bad || (!row_part && rg)) return;
     const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, nsplit = splits_of<AttnShape<HD, NT>::kWarps>(a.splits, min(p.nb, max(0, p.z - p.b0)));
     const int b0 = p.b0 + (int(blockIdx.x) - RG) * kMergeThreads;
     if (live <= 0 || (row_part ? int(blockIdx.x) >= live || nsplit == 1 : b0 >= p.b0 + p.nb)) return;
     const size_t at = (((size_t)s * a.c.n_kv + h) * a.groups + rg) * a.splits;
-    pdl_wait();
     if (__syncthreads_or(tid < nsplit && a.part_bad[at + tid])) return;
     // a warp's view of row r: the largest maximum, the sum, and each split's factor
     auto state = [&](int r, float &top, float &total, float (&f)[2]) {
@@ -1151,8 +1230,8 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// exclusive prefix sum over the CTA's threads (blockDim.x = 1024); *total = the sum
-__device__ __forceinline__ int block_scan(int v, int *sums, int *total) {
+// exclusive prefix sum over the CTA's 1024 threads
+__device__ __forceinline__ int block_scan(int v, int *sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
 #pragma unroll
@@ -1163,18 +1242,17 @@ __device__ __forceinline__ int block_scan(int v, int *sums, int *total) {
     __syncthreads();
     if (lane == 31) sums[warp] = x;
     __syncthreads();
-    int before = 0, all = 0;
-    for (int i = 0; i < 32; ++i) {
-        if (i < warp) before += sums[i];
-        all += sums[i];
-    }
-    *total = all;
+    int before = lane < warp ? sums[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     return before + x - v;
 }
 
-// One CTA per head. The score of the last block kept by choice is found digit by digit (8 bits at a time, by a
-// histogram of the candidates that agree so far); blocks above it are kept, and as many of those equal to
-// it as there is room for, the lowest indexes first. Then the table is partitioned in order.
+// One CTA per head; a call reads and writes a few bytes a block, so its time is the latency of the steps. The score of
+// the last block kept by choice is found digit by digit (8 bits at a time, by a histogram of the candidates that agree
+// so far); blocks above it are kept, and as many of those equal to it as there is room for, the lowest indexes first.
+// Then the table is partitioned in order: a thread takes a run of consecutive blocks, so two prefix sums over the
+// threads place them all.
 constexpr int kEvictThreads = 1024;
 __global__ void __launch_bounds__(kEvictThreads) k_kv8_evict(EvictArgs a) {
     __shared__ int hist[256], sums[32], pick[2];
@@ -1189,9 +1267,9 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_evict(EvictArgs a) {
     const int keep = min(n, a.keep);
     const int c0 = min(a.sink, n), c1 = max(c0, n - a.recent);   // candidates c0..c1-1
     int room = keep - (c0 + n - c1);                             // how many of them stay
-    const bool all = room >= c1 - c0, none = room <= 0;
+    const bool all = room >= c1 - c0, some = !all && room > 0;
     uint32_t prefix = 0;
-    if (!all && !none) {
+    if (some) {
         for (int shift = 24; shift >= 0; shift -= 8) {
             if (tid < 256) hist[tid] = 0;
             __syncthreads();
@@ -1200,11 +1278,23 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_evict(EvictArgs a) {
                 if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255], 1);
             }
             __syncthreads();
-            if (tid == 0) {
-                int above = 0, d = 255;
-                while (above + hist[d] < room) above += hist[d--];
-                pick[0] = d;
-                pick[1] = above;
+            if (tid < 32) {                                      // lane l: digits 255 - 8 l .. 248 - 8 l, from the top
+                int c[8], mine = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mine += c[k] = hist[255 - 8 * tid - k];
+                int upto = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (tid >= o) upto += y;
+                }
+                int above = upto - mine;
+                if (above < room && upto >= room) {
+                    int k = 0;
+                    while (above + c[k] < room) above += c[k++];
+                    pick[0] = 255 - 8 * tid - k;
+                    pick[1] = above;
+                }
             }
             __syncthreads();
             prefix |= uint32_t(pick[0]) << shift;
@@ -1212,28 +1302,30 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_evict(EvictArgs a) {
         }
     }
     // kept: outside the candidates, or above the last one kept, or equal to it and among the first `room`
-    int kept_before = 0, equal_before = 0;
-    for (int b0 = 0; b0 < w.nb; b0 += kEvictThreads) {
-        const int b = b0 + tid;
-        const bool held = b < n, cand = b >= c0 && b < c1;
-        const uint32_t key = cand && !all && !none ? order_key(w.score[b]) : 0;
-        const int eq = cand && !all && !none && key == prefix;
-        int total_eq = 0;
-        const int rank_eq = equal_before + block_scan(eq, sums, &total_eq);
-        const bool kept = held && (!cand || all || (!none && (key > prefix || (eq && rank_eq < room))));
-        int total_kept = 0;
-        const int rank = kept_before + block_scan(kept, sums, &total_kept);
-        if (b < w.nb) {
-            const int to = kept ? rank : held ? keep + (b - rank) : b;
-            a.table[base + to] = w.table[b];
-            if (kept) a.score[base + to] = w.score[b];
-            if (b >= keep) {   // the tail's two blocks follow the kept ones; nothing is held behind them
-                const int from = b + n - keep;
-                a.score[base + b] = b < keep + 2 && from < w.nb ? w.score[from] : 0.f;
-            }
+    const int run = (w.nb + kEvictThreads - 1) / kEvictThreads, b0 = min(w.nb, tid * run), b1 = min(w.nb, b0 + run);
+    int equal = 0, over = 0;
+    for (int b = b0; b < b1; ++b) {
+        const bool cand = b >= c0 && b < c1;
+        const uint32_t key = some && cand ? order_key(w.score[b]) : 0;
+        equal += some && cand && key == prefix;
+        over += b < n && (!cand || all || (some && key > prefix));
+    }
+    int left = room - block_scan(equal, sums);                   // equal ones that this run may still keep
+    const int kept_here = over + min(max(left, 0), equal);
+    int rank = block_scan(kept_here, sums);
+    for (int b = b0; b < b1; ++b) {
+        const bool cand = b >= c0 && b < c1;
+        const float score = w.score[b];
+        const uint32_t key = some && cand ? order_key(score) : 0;
+        bool kept = b < n && (!cand || all || (some && key > prefix));
+        if (some && cand && key == prefix) kept = left-- > 0;
+        a.table[base + (kept ? rank : b < n ? keep + (b - rank) : b)] = w.table[b];
+        if (kept) a.score[base + rank] = score;
+        if (b >= keep) {   // the tail's two blocks follow the kept ones; nothing is held behind them
+            const int from = b + n - keep;
+            a.score[base + b] = b < keep + 2 && from < w.nb ? w.score[from] : 0.f;
         }
-        kept_before += total_kept;
-        equal_before += total_eq;
+        rank += kept;
     }
     if (tid == 0) {
         a.sealed[(size_t)s * a.c.n_kv + h] = keep;
@@ -1282,8 +1374,17 @@ int write_rows(const dfl_kv8 *c, const int32_t *len, const int32_t *cnt, int row
     if (!commit && rows > DFL_MAX_ROWS) return DFL_E_UNSUPPORTED;
     if (rows > kBlk * c->n_blocks) return DFL_E_CAPACITY;
     WriteArgs a{*c, len, cnt, k, v, ld, rows, commit};
-    k_kv8_write<<<dim3(c->n_kv, c->n_seq), kWriteThreads, 0, s>>>(a);
-    return launched();
+    // Up to 64 rows complete three blocks at most: one launch. More rows are sealed by a launch of their own, a CTA for each
+    // block, and the second one settles the tail. At 1024 rows of 8 heads of 128
+    // the two take 9 us, one CTA a head alone 260 us.
+    if (!commit || rows <= 64) {
+        k_kv8_write<<<dim3(c->n_kv, c->n_seq), kWriteThreads, 0, s>>>(a, 0);
+        return launched();
+    }
+    k_kv8_seal<<<dim3(2 * ((kTail + rows) / kBlk), c->n_kv, c->n_seq), kWriteThreads, 0, s>>>(a);
+    const int l = launched();
+    if (l) return l;
+    return launch_pdl(k_kv8_write, dim3(c->n_kv, c->n_seq), dim3(kWriteThreads), 0, s, a, 1) == cudaSuccess ? DFL_OK : DFL_E_CUDA;
 }
 
 }  // namespace
