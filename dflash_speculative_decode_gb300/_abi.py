@@ -108,7 +108,7 @@ SIGNATURES = {
     "dfl_kv8_status": (ctypes.c_int, [P(dfl_kv8), vp]),
     "dfl_kv8_append": (ctypes.c_int, [P(dfl_kv8), vp, vp, ctypes.c_int, vp, vp, ctypes.c_int64, vp]),
     "dfl_kv8_stage": (ctypes.c_int, [P(dfl_kv8), vp, vp, ctypes.c_int, vp, vp, ctypes.c_int64, vp]),
-    "dfl_kv8_attn_scratch_bytes": (ctypes.c_int64, [P(dfl_kv8), ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    "dfl_kv8_attn_scratch_bytes": (ctypes.c_int64, [P(dfl_kv8), ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
     "dfl_kv8_attn": (ctypes.c_int, [P(dfl_kv8), vp, ctypes.c_int64, ctypes.c_int, ctypes.c_int, vp, vp, ctypes.c_int, ctypes.c_int,
                                     ctypes.c_float, ctypes.c_int, vp, ctypes.c_int64, vp, ctypes.c_size_t, vp]),
     "dfl_kv8_evict": (ctypes.c_int, [P(dfl_kv8), vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp]),

@@ -334,11 +334,12 @@ struct AttnKvArgs {
     int n_q, rows, window, causal, score;
     const int32_t *len, *cnt;
     float scale;
-    int groups, splits;   // row groups of a head, splits of a row group's keys (at most)
-    float *part_o;        // [unit][split][rows of a group][head_dim], unit = (sequence, head, row group)
-    float *part_tail;     // [unit][rows of a group][head_dim]: the tail's share, read by the CTA that wrote it
-    float *part_ml;       // [unit][split][rows of a group][2]: running maximum (base 2) and sum
-    int *part_bad;        // [unit][split]: a table entry was out of range
+    int groups, splits;   // row groups of a head, splits of a row group's coded blocks (at most)
+    int apart;            // 1: the tail has a CTA of its own (grid x 0, the splits follow); 0: the last split's takes it
+    float *part_o;        // [unit][part][rows of a group][head_dim], unit = (sequence, head, row group); part 0 is the
+                          // tail's, the splits follow
+    float *part_ml;       // [unit][part][rows of a group][2]: running maximum (base 2) and sum
+    int *part_bad;        // [unit][part]: a table entry was out of range
     float *blk_lse;       // [sequence][head][n_blocks][16]: log2 of the block's share of row 0's sums
 };
 
@@ -402,12 +403,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// d = a b
-__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // 2^x by the hardware's instruction: off by 2 units in the last place, results below 2^-126 are 0
 __device__ __forceinline__ float ex2(float x) {
@@ -483,11 +478,10 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     constexpr int RG = 8 * NT, kW = S::kWarps, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4;
     static_assert(kW * RG * kPitch * 4 <= S::kSmem, "the merge reuses the shared memory");
     extern __shared__ __align__(16) uint8_t kv_smem[];
-    // running maxima and sums of the warps, and behind them the tail's
-    __shared__ float q_scale[RG], sm_m[kW + 1][RG], sm_l[kW + 1][RG];
+    __shared__ float q_scale[RG], sm_m[kW][RG], sm_l[kW][RG];
     __shared__ int sm_bad;
     __shared__ uint32_t sm_poison[2];
-    const int split = blockIdx.x, h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z;
+    const int split = int(blockIdx.x) - a.apart, h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const KvView w = view(a.c, s, h);
     const int per = a.n_q / a.c.n_kv;
@@ -506,18 +500,19 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     const Span p = span_of(a, s, w);
     pdl_trigger();
     if (p.bad) {
-        if (tid == 0 && split == 0) atomicOr(a.c.err, p.bad);
+        if (tid == 0 && blockIdx.x == 0) atomicOr(a.c.err, p.bad);
         return;
     }
     const int live = p.n * per - rg * RG;                            // rows of this group that exist
     const int coded = min(p.nb, max(0, p.z - p.b0));                // blocks held as codes that some row sees
-    const int nsplit = splits_of<kW>(a.splits, coded);
-    if (live <= 0 || split >= nsplit) return;
-    const bool has_tail = split == nsplit - 1 && p.nb > coded;
-    const int x0 = int((long)coded * split / nsplit), x1 = int((long)coded * (split + 1) / nsplit);
+    const int nsplit = coded ? splits_of<kW>(a.splits, coded) : 0;
+    const bool alone = nsplit == 0, tail = a.apart ? split < 0 : split == max(nsplit - 1, 0);   // every row sees its own token, so the tail is never empty
+    if (live <= 0 || (split >= nsplit && !tail)) return;
+    const bool codes = split >= 0 && split < nsplit;
+    const int x0 = codes ? int((long)coded * split / nsplit) : 0, x1 = codes ? int((long)coded * (split + 1) / nsplit) : 0;
     const int bfirst = p.b0 + x0 + warp;                             // this warp's blocks: bfirst, + kW, ..
     const int ncoded = max(0, (x1 - x0 - warp + kW - 1) / kW);
-    const size_t unit = ((size_t)s * a.c.n_kv + h) * a.groups + rg, at = unit * a.splits + split;
+    const size_t unit = ((size_t)s * a.c.n_kv + h) * a.groups + rg, at = unit * (a.splits + 1);   // the unit's parts: the tail's, then the splits'
 
     int bad = 0;
     auto load_phys = [&](int i0) {                                   // lane l: where block i0 + l is stored
@@ -529,13 +524,72 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         }
         return at;
     };
-    int phys = load_phys(0);                                         // of the window of 32 blocks that is being asked for
-    int phys_next = load_phys(32);                                   // and of the one behind it
+    // this thread's rows: 8 nt + 2 t + e
+    int lo[NT][2], hi[NT][2];
+    float qs[NT][2], mx[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * nt + 2 * t + e;
+            lo[nt][e] = 0, hi[nt][e] = 1 << 30;                      // a row that does not exist: nothing reads its sums
+            if (r < live) seen(a, p, (rg * RG + r) / per, lo[nt][e], hi[nt][e]);
+            mx[nt][e] = -INFINITY;
+            l[nt][e] = 0.f;
+        }
+    // tokens all..all_end-1 are seen by every row of the group that exists
+    int all_lo, all_hi, dummy;
+    seen(a, p, min(p.n - 1, (rg * RG + RG - 1) / per), all_lo, dummy);
+    seen(a, p, rg * RG / per, dummy, all_hi);
+    const uint4 *qf = reinterpret_cast<const uint4 *>(kv_smem) + lane;
+    const bool keep_lse = a.score && rg == 0;
+    float *lse = keep_lse ? a.blk_lse + ((size_t)s * a.c.n_kv + h) * w.nb * 16 : nullptr;
+    const int key0 = 8 * (g >> 1) + (g & 1);                         // key of row g of matrix 0; matrix j: + 2 j
+    auto load_qs = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) qs[nt][e] = q_scale[8 * nt + 2 * t + e];
+    };
+    // query rows into their fragments
+    auto stage_q = [&]() {
+        if (tid < 2) sm_poison[tid] = 0;
+        if (tid == 0) sm_bad = 0;
+#pragma unroll
+        for (int j = 0; j < kQRows; ++j) {
+            const int r = warp + j * kW;
+            if (r >= RG) break;
+            float amax = 0.f;
+            bool fin = true;
+#pragma unroll
+            for (int i = 0; i < HD / 64; ++i) {
+                if (r >= live) qx[j][i] = make_float2(0.f, 0.f);
+                fin = fin && isfinite(qx[j][i].x) && isfinite(qx[j][i].y);
+                amax = fmaxf(amax, fmaxf(fabsf(qx[j][i].x), fabsf(qx[j][i].y)));
+            }
+            fin = __all_sync(0xffffffffu, fin);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const float f = fin ? lift(amax) : 0.f;
+            if (lane == 0) q_scale[r] = fin ? a.scale * kLog2e / f : NAN;
+#pragma unroll
+            for (int i = 0; i < HD / 64; ++i) {
+                uint32_t hi = 0, lo = 0;
+                if (fin) halves2(qx[j][i].x * f, qx[j][i].y * f, hi, lo);
+                const int d = 2 * lane;                                  // of chunk i
+                uint32_t *dst = reinterpret_cast<uint32_t *>(kv_smem) + (((i * NT + r / 8) * 4 + ((d & 15) >> 3)) * 32 + (r & 7) * 4 + (d >> 4)) * 4 + ((d & 7) >> 1);
+                dst[0] = hi;
+                dst[2 * 32 * 4] = lo;
+            }
+        }
+        __syncthreads();
+    };
+
     // the tail's rows: a warp takes kTailCh channels, steps 4 tc + tj0 .. of the first product, and of it the key of
     // row g of matrix m (of 6), which makes thread t's inputs of step s the keys 16 s + 4 t .. + 3
     constexpr int kSteps = S::kTailCh / 16;
     const int tc = warp * kSteps / 4, tj0 = warp * kSteps % 4, trows = p.L + p.n - kBlk * p.z;
-    const bool tactive = has_tail && warp * S::kTailCh < HD;
+    const bool tactive = tail && warp * S::kTailCh < HD;
     auto tail_key = [&](int m) { return 16 * (m >> 1) + 4 * (g >> 1) + 2 * (m & 1) + (g & 1); };
     float4 kr[6][kSteps], vr[kSteps][2][3];
 #pragma unroll
@@ -555,6 +609,8 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
                     vr[i][k][st] = *reinterpret_cast<const float4 *>(w.vt + (size_t)(16 * (warp * kSteps + i) + g + 8 * k) * kTail + 16 * st + 4 * t);
             }
     }
+    int phys = load_phys(0);                                         // of the window of 32 blocks that is being asked for
+    int phys_next = load_phys(32);                                   // and of the one behind it
     float ks = 0.f, vs = 0.f;                                        // lane l: scales of block l of the window that is read
     if (lane < ncoded) ks = w.ks[phys], vs = w.vs[phys];
     float ks_next = 0.f, vs_next = 0.f;
@@ -581,70 +637,17 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     auto taken = [&]() { take = take == ring + (kRing - 1) * kUnit ? ring : take + kUnit; };
 #pragma unroll
     for (int u = 0; u < kRing; ++u)
-        if (u < kRing - S::kHold || !has_tail) issue(u);
+        if (u < kRing - S::kHold || !tail) issue(u);
 
-    // ---- query rows into their fragments ----
-    if (tid < RG) sm_m[kW][tid] = -INFINITY, sm_l[kW][tid] = 0.f;
-    if (tid < 2) sm_poison[tid] = 0;
-    if (tid == 0) sm_bad = 0;
-#pragma unroll
-    for (int j = 0; j < kQRows; ++j) {
-        const int r = warp + j * kW;
-        if (r >= RG) break;
-        float amax = 0.f;
-        bool fin = true;
-#pragma unroll
-        for (int i = 0; i < HD / 64; ++i) {
-            if (r >= live) qx[j][i] = make_float2(0.f, 0.f);
-            fin = fin && isfinite(qx[j][i].x) && isfinite(qx[j][i].y);
-            amax = fmaxf(amax, fmaxf(fabsf(qx[j][i].x), fabsf(qx[j][i].y)));
-        }
-        fin = __all_sync(0xffffffffu, fin);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float f = fin ? lift(amax) : 0.f;
-        if (lane == 0) q_scale[r] = fin ? a.scale * kLog2e / f : NAN;
-#pragma unroll
-        for (int i = 0; i < HD / 64; ++i) {
-            uint32_t hi = 0, lo = 0;
-            if (fin) halves2(qx[j][i].x * f, qx[j][i].y * f, hi, lo);
-            const int d = 2 * lane;                                  // of chunk i
-            uint32_t *dst = reinterpret_cast<uint32_t *>(kv_smem) + (((i * NT + r / 8) * 4 + ((d & 15) >> 3)) * 32 + (r & 7) * 4 + (d >> 4)) * 4 + ((d & 7) >> 1);
-            dst[0] = hi;
-            dst[2 * 32 * 4] = lo;
-        }
-    }
-    __syncthreads();
-
-    // this thread's rows: 8 nt + 2 t + e
-    int lo[NT][2], hi[NT][2];
-    float qs[NT][2], mx[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = 8 * nt + 2 * t + e;
-            lo[nt][e] = 0, hi[nt][e] = 1 << 30;                      // a row that does not exist: nothing reads its sums
-            if (r < live) seen(a, p, (rg * RG + r) / per, lo[nt][e], hi[nt][e]);
-            qs[nt][e] = q_scale[r];
-            mx[nt][e] = -INFINITY;
-            l[nt][e] = 0.f;
-        }
-    // tokens all..all_end-1 are seen by every row of the group that exists
-    int all_lo, all_hi, dummy;
-    seen(a, p, min(p.n - 1, (rg * RG + RG - 1) / per), all_lo, dummy);
-    seen(a, p, rg * RG / per, dummy, all_hi);
-    const uint4 *qf = reinterpret_cast<const uint4 *>(kv_smem) + lane;
-    const bool keep_lse = a.score && rg == 0;
-    float *lse = keep_lse ? a.blk_lse + ((size_t)s * a.c.n_kv + h) * w.nb * 16 : nullptr;
-    const int key0 = 8 * (g >> 1) + (g & 1);                         // key of row g of matrix 0; matrix j: + 2 j
-
-    // ---- the tail (at most 48 fp32 rows, by the last split's CTA, while its first codes are on their way): a warp
-    // takes kTailCh channels of every row. Keys enter as two fp16 halves, each scaled by a power of two of its own;
-    // values and weights as three bf16 parts (fp32's range, so that no token's size touches another's precision). A
-    // token that holds an infinity or a NaN makes the rows that see it NaN; its own numbers enter as 0. ----
-    if (has_tail) {
-        float *mine = reinterpret_cast<float *>(ring + (kRing - S::kHold) * kUnit);   // [48][RG]: slots held back
+    // ---- the tail (at most 48 fp32 rows), while the first codes are on their way: a warp takes kTailCh channels
+    // of every row. Keys enter as two fp16 halves, each scaled by a power of two of its own; values and weights as
+    // three bf16 parts (fp32's range, so that no token's size touches another's precision). A token that holds an
+    // infinity or a NaN makes the rows that see it NaN; its own numbers enter as 0. ----
+    if (tail) {
+        constexpr int kPart = kRing * kUnit / 4;                     // from one warp's partial logits [48][RG] to the next's
+        float *first = reinterpret_cast<float *>(kv_smem + S::kQBytes + (kRing - S::kHold) * kUnit), *mine = first + warp * kPart;
+        stage_q();
+        load_qs();
         if (tactive) {
             uint32_t poison[2] = {0, 0};
 #pragma unroll
@@ -727,16 +730,16 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         }
         __syncthreads();
         constexpr int kParts = HD / S::kTailCh;
-        float *first = mine - warp * (kRing * kUnit / 4);
         for (int e = tid; e < kTail * RG; e += kW * 32) {
             float x = 0.f;
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) x += first[i * (kRing * kUnit / 4) + e];
+            for (int i = 0; i < kParts; ++i) x += first[i * kPart + e];
             first[e] = x;
         }
         __syncthreads();
         if (tactive) {
             uint32_t pf[NT][3][2][3];
+            float total[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float x[6][2];
@@ -763,9 +766,9 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
                     sum[0] = group_sum(sum[0]);
                     sum[1] = group_sum(sum[1]);
                     const int r = 8 * nt + 2 * t + e;
+                    total[nt][e] = sum[0] + sum[1];
                     if (warp == 0 && g == 0) {
-                        sm_m[kW][r] = top;
-                        sm_l[kW][r] = sum[0] + sum[1];
+                        *reinterpret_cast<float2 *>(a.part_ml + (at * RG + r) * 2) = make_float2(top, sum[0] + sum[1]);
                         if (keep_lse && r < per)
                             for (int i = 0; i < 2; ++i)
                                 if (p.z + i < p.b0 + p.nb) lse[(size_t)(p.z + i) * 16 + r] = sum[i] == 0.f ? -INFINITY : ref + log2f(sum[i]);
@@ -779,7 +782,6 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
                     for (int k = 0; k < 3; ++k) pf[nt][m >> 1][m & 1][k] = transpose8x8(y[k]);
                 }
             }
-            float *to = a.part_tail + unit * RG * HD;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
                 float d[NT][4];
@@ -808,12 +810,25 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) to[(8 * nt + 2 * t + (k & 1)) * HD + 16 * (warp * kSteps + i) + g + 8 * (k >> 1)] = d[nt][k];
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = 8 * nt + 2 * t + (k & 1), d0 = 16 * (warp * kSteps + i) + g + 8 * (k >> 1), rid = rg * RG + r;
+                        if (!alone)
+                            a.part_o[(at * RG + r) * HD + d0] = d[nt][k];
+                        else if (r < live)
+                            a.out[((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + d0] = d[nt][k] / total[nt][k & 1];
+                    }
             }
         }
-        __syncthreads();   // the slots held back are free, and the CTA sees its part of the tail
+        if (tid == 0) a.part_bad[at] = 0;
+        if (!codes) return;
+        __syncthreads();                                             // the slots held back are free
 #pragma unroll
         for (int u = kRing - S::kHold; u < kRing; ++u) issue(u);
+    }
+
+    if (!tail) {
+        stage_q();
+        load_qs();
     }
 
     float o[HD / 16][NT][4];
@@ -858,6 +873,12 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         cp_async_wait_groups<kRing - 1>();
         __syncwarp();
         float x[2][NT][4], xl[2][NT][4];                             // by the query's hi and lo halves
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[mt][nt][k] = xl[mt][nt][k] = 0.f;
         const uint8_t *K = take + key0 * 64 + 16 * t;
 #pragma unroll
         for (int c = 0; c < HD / 64; ++c) {
@@ -891,10 +912,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
                             for (int nt = 0; nt < NT; ++nt) {
                                 float(&d)[4] = part && NT == 1 ? xl[mt][nt] : x[mt][nt];
                                 const uint32_t b0 = part ? ql[nt][2 * jj] : qh[nt][2 * jj], b1 = part ? ql[nt][2 * jj + 1] : qh[nt][2 * jj + 1];
-                                if (c == 0 && j == 0 && (part == 0 || NT == 1))
-                                    mma_f16_zero(d, af[mt], b0, b1);
-                                else
-                                    mma_f16(d, af[mt], b0, b1);
+                                mma_f16(d, af[mt], b0, b1);
                             }
                 }
             }
@@ -1041,23 +1059,23 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
             }
         }
     __syncthreads();
+    const size_t mine = at + 1 + split;
     if (tid == 0) {
         if (sm_bad) atomicOr(a.c.err, kErrTable);
-        a.part_bad[at] = sm_bad;
+        a.part_bad[mine] = sm_bad;
     }
     if (sm_bad) return;
-    if (tid < RG) {   // each state's factor, in place of its maximum; the sum, in place of the first one
+    if (tid < RG) {   // each warp's factor, in place of its maximum
         float top = -INFINITY, total = 0.f;
 #pragma unroll
-        for (int i = 0; i <= kW; ++i) top = fmaxf(top, sm_m[i][tid]);
+        for (int i = 0; i < kW; ++i) top = fmaxf(top, sm_m[i][tid]);
 #pragma unroll
-        for (int i = 0; i <= kW; ++i) {
+        for (int i = 0; i < kW; ++i) {
             const float f = sm_m[i][tid] == top ? 1.f : ex2(sm_m[i][tid] - top);
             sm_m[i][tid] = f;
             total = fmaf(sm_l[i][tid], f, total);
         }
-        sm_l[0][tid] = total;
-        *reinterpret_cast<float2 *>(a.part_ml + (at * RG + tid) * 2) = make_float2(top, total);
+        *reinterpret_cast<float2 *>(a.part_ml + (mine * RG + tid) * 2) = make_float2(top, total);
     }
     __syncthreads();
     for (int e = tid; e < min(live, RG) * (HD / 4); e += kW * 32) {
@@ -1066,39 +1084,32 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         auto add = [&](const float4 &y, float f) {
             sum.x = fmaf(y.x, f, sum.x), sum.y = fmaf(y.y, f, sum.y), sum.z = fmaf(y.z, f, sum.z), sum.w = fmaf(y.w, f, sum.w);
         };
-        if (has_tail) add(*reinterpret_cast<const float4 *>(a.part_tail + (unit * RG + r) * HD + d), sm_m[kW][r]);
 #pragma unroll
         for (int i = 0; i < kW; ++i) add(*reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(kv_smem) + (i * RG + r) * kPitch + d), sm_m[i][r]);
-        if (nsplit == 1) {
-            const int rid = rg * RG + r;
-            const float total = sm_l[0][r];
-            *reinterpret_cast<float4 *>(a.out + ((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + d) =
-                make_float4(sum.x / total, sum.y / total, sum.z / total, sum.w / total);
-        } else {
-            *reinterpret_cast<float4 *>(a.part_o + (at * RG + r) * HD + d) = sum;
-        }
+        *reinterpret_cast<float4 *>(a.part_o + (mine * RG + r) * HD + d) = sum;
     }
 }
 
 // Merges the splits of a row in a fixed order (grid x < rows of a group: one row each), and adds row 0's share of
 // 256 blocks to the scores (grid x behind them, row group 0).
 constexpr int kMergeThreads = 256;
-constexpr int kMaxSplits = 64;
+constexpr int kMaxSplits = 63;   // with the tail's, two parts a lane of the merge
 template <int HD, int NT>
 __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
     constexpr int RG = 8 * NT, kLanes = kMergeThreads / (HD / 4);   // splits taken at once
     __shared__ float4 acc[kLanes][HD / 4];
-    __shared__ float fac[kMaxSplits], top_s[16], total_s[16];
+    __shared__ float fac[64], top_s[16], total_s[16];
     const int h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
     const bool row_part = blockIdx.x < RG;
     const KvView w = view(a.c, s, h);
     const Span p = span_of(a, s, w);
     pdl_wait();   // by every CTA, so that this grid does not end before the one it follows
     if (p.bad || (!row_part && rg)) return;
-    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, nsplit = splits_of<AttnShape<HD, NT>::kWarps>(a.splits, min(p.nb, max(0, p.z - p.b0)));
+    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, coded = min(p.nb, max(0, p.z - p.b0));
+    const int nsplit = 1 + (coded ? splits_of<AttnShape<HD, NT>::kWarps>(a.splits, coded) : 0);   // the tail's and the splits' parts
     const int b0 = p.b0 + (int(blockIdx.x) - RG) * kMergeThreads;
     if (live <= 0 || (row_part ? int(blockIdx.x) >= live || nsplit == 1 : b0 >= p.b0 + p.nb)) return;
-    const size_t at = (((size_t)s * a.c.n_kv + h) * a.groups + rg) * a.splits;
+    const size_t at = (((size_t)s * a.c.n_kv + h) * a.groups + rg) * (a.splits + 1);
     if (__syncthreads_or(tid < nsplit && a.part_bad[at + tid])) return;
     // a warp's view of row r: the largest maximum, the sum, and each split's factor
     auto state = [&](int r, float &top, float &total, float (&f)[2]) {
@@ -1160,35 +1171,38 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
 }
 
 // ---- host side ----
-// How a call's work is cut: row groups of 8 rows, or of 16 (whose codes are expanded once for two products) where
-// a head has more than 8; splits of a group's keys so that the CTAs fill the SMs evenly. Costs in blocks per
-// warp: a CTA's start and end are worth about 6.
+// How a call's work is cut: row groups of 8 rows, or of 16 (whose codes are expanded once for two products) where a head
+// has more than 8; splits of a group's keys, and a CTA of its own for the tail or not. Everything should fit in one wave of
+// the part's 152 SMs: CTAs of a second one were measured to wait for tens of microseconds although slots were free. Costs are
+// in blocks a warp; a CTA's start and end are worth about 6, a tail inside a CTA 3.
 struct AttnCut {
-    int nt, groups, splits;
-    size_t units, o_bytes, tail_bytes, ml_bytes, bad_bytes, lse_bytes, total;
+    int nt, groups, splits, apart;
+    size_t units, o_bytes, ml_bytes, bad_bytes, lse_bytes, total;
 };
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int score) {
+AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
     AttnCut t{};
     const int r = rows * (n_q / c->n_kv);
     t.nt = r > 8 ? 2 : 1;
     t.groups = (r + 8 * t.nt - 1) / (8 * t.nt);
     t.units = (size_t)c->n_seq * c->n_kv * t.groups;
     const int warps = c->head_dim == 128 && t.nt == 2 ? AttnShape<128, 2>::kWarps : AttnShape<128, 1>::kWarps;
-    const int slots = 152 * (c->head_dim == 256 ? 1 : 2), most = (c->n_blocks + warps - 1) / warps;
+    const int slots = 152 * (c->head_dim == 256 ? 1 : 2), blocks = window ? std::min(c->n_blocks, window / kBlk + 2) : c->n_blocks;
+    const int most = std::min(kMaxSplits, (blocks + warps - 1) / warps);
     double best = 0;
-    for (int n = 1; n <= std::min(kMaxSplits, most); ++n) {
-        const double waves = double((t.units * n + slots - 1) / slots);
-        const double cost = waves * (double(c->n_blocks) / warps / n + 6);
-        if (n == 1 || cost < best) best = cost, t.splits = n;
-    }
-    const size_t parts = t.units * t.splits * 8 * t.nt;
-    t.o_bytes = up256(t.splits > 1 ? parts * c->head_dim * 4 : 0);
-    t.tail_bytes = up256(t.units * 8 * t.nt * c->head_dim * 4);
+    for (int apart = 0; apart < 2; ++apart)
+        for (int n = 1; n <= most; ++n) {
+            const double waves = double((t.units * (n + apart) + slots - 1) / slots);
+            if (waves > 1 && apart) continue;
+            const double cost = waves * (double((blocks + warps * n - 1) / (warps * n)) + 6 + (apart ? 0 : 3));
+            if ((n == 1 && !apart) || cost < best) best = cost, t.splits = n, t.apart = apart;
+        }
+    const size_t parts = t.units * (t.splits + 1) * 8 * t.nt;
+    t.o_bytes = up256(parts * c->head_dim * 4);
     t.ml_bytes = up256(parts * 8);
-    t.bad_bytes = up256(t.units * t.splits * 4);
+    t.bad_bytes = up256(t.units * (t.splits + 1) * 4);
     t.lse_bytes = score ? up256((size_t)c->n_seq * c->n_kv * c->n_blocks * 64) : 0;
-    t.total = t.o_bytes + t.tail_bytes + t.ml_bytes + t.bad_bytes + t.lse_bytes;
+    t.total = t.o_bytes + t.ml_bytes + t.bad_bytes + t.lse_bytes;
     return t;
 }
 
@@ -1204,9 +1218,9 @@ cudaError_t launch_kv8_attn(const AttnKvArgs &a, cudaStream_t s) {
         attr[dev] = true;
     }
     const unsigned heads = unsigned(a.c.n_kv * a.groups);
-    k_kv8_attn<HD, NT><<<dim3(a.splits, heads, a.c.n_seq), AttnShape<HD, NT>::kWarps * 32, smem, s>>>(a);
+    k_kv8_attn<HD, NT><<<dim3(a.splits + a.apart, heads, a.c.n_seq), AttnShape<HD, NT>::kWarps * 32, smem, s>>>(a);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || (a.splits == 1 && !a.score)) return e;
+    if (e != cudaSuccess) return e;
     const unsigned x = 8 * NT + (a.score ? (a.c.n_blocks + kMergeThreads - 1) / kMergeThreads : 0);
     return launch_pdl(k_kv8_merge<HD, NT>, dim3(x, heads, a.c.n_seq), dim3(kMergeThreads), 0, s, a);
 }
@@ -1424,11 +1438,11 @@ int dfl_kv8_stage(const dfl_kv8 *c, const int32_t *len, const int32_t *cnt, int 
     return write_rows(c, len, cnt, rows, k, v, ld, 0, static_cast<cudaStream_t>(stream));
 }
 
-int64_t dfl_kv8_attn_scratch_bytes(const dfl_kv8 *c, int n_q, int rows, int score) {
+int64_t dfl_kv8_attn_scratch_bytes(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
     if (!c || c->n_seq < 1 || c->n_kv < 1 || c->n_blocks < 1 || n_q < 1 || n_q % c->n_kv || n_q / c->n_kv > kMaxGroup || rows < 1 ||
-        rows > DFL_MAX_ROWS || (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256))
+        rows > DFL_MAX_ROWS || window < 0 || (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256))
         return -1;
-    return (int64_t)attn_cut(c, n_q, rows, score).total;
+    return (int64_t)attn_cut(c, n_q, rows, window, score).total;
 }
 
 int dfl_kv8_attn(const dfl_kv8 *c, const float *q, int64_t ldq, int n_q, int rows, const int32_t *len, const int32_t *cnt, int window,
@@ -1439,14 +1453,13 @@ int dfl_kv8_attn(const dfl_kv8 *c, const float *q, int64_t ldq, int n_q, int row
     if (n_q / c->n_kv > kMaxGroup || rows > DFL_MAX_ROWS) return DFL_E_UNSUPPORTED;
     if ((rc = check_rows(c, q, ldq, n_q)) || (rc = check_rows(c, out, ldo, n_q))) return rc;
     if (score && !c->score) return DFL_E_INVALID_ARG;
-    if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255) || (int64_t)scratch_bytes < dfl_kv8_attn_scratch_bytes(c, n_q, rows, score))
+    if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255) || (int64_t)scratch_bytes < dfl_kv8_attn_scratch_bytes(c, n_q, rows, window, score))
         return DFL_E_INVALID_ARG;
-    const AttnCut t = attn_cut(c, n_q, rows, score);
-    AttnKvArgs a{*c, q, out, ldq, ldo, n_q, rows, window, causal != 0, score != 0, len, cnt, scale, t.groups, t.splits};
+    const AttnCut t = attn_cut(c, n_q, rows, window, score);
+    AttnKvArgs a{*c, q, out, ldq, ldo, n_q, rows, window, causal != 0, score != 0, len, cnt, scale, t.groups, t.splits, t.apart};
     uint8_t *at = static_cast<uint8_t *>(scratch);
     a.part_o = reinterpret_cast<float *>(at);
-    a.part_tail = reinterpret_cast<float *>(at += t.o_bytes);
-    a.part_ml = reinterpret_cast<float *>(at += t.tail_bytes);
+    a.part_ml = reinterpret_cast<float *>(at += t.o_bytes);
     a.part_bad = reinterpret_cast<int *>(at += t.ml_bytes);
     a.blk_lse = reinterpret_cast<float *>(at += t.bad_bytes);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);

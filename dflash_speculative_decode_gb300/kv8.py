@@ -137,12 +137,12 @@ class Kv8Cache:
         pq, M, ldq = self._rows(q, "q", 0)
         n_q = q.shape[2]
         pl, pn = self._ints(length, "length"), self._ints(n, "n", True)
-        key = (n_q, M, score)
+        key = (n_q, M, window, score)
         need = self._need.get(key)
         if need is None:
-            need = self._need[key] = int(self.L.dfl_kv8_attn_scratch_bytes(self._c, n_q, M, score))
+            need = self._need[key] = int(self.L.dfl_kv8_attn_scratch_bytes(self._c, n_q, M, window, score))
             if need < 0:
-                _refuse(f"{n_q} query heads and {M} rows: n_q must be a multiple of n_kv = {self.n_kv}, up to 16 a head, with 1..16 rows")
+                _refuse(f"{n_q} query heads and {M} rows: n_q must be a multiple of n_kv = {self.n_kv}, up to 16 a head, with 1..16 rows and a window >= 0")
             if self._scratch is None or self._scratch.numel() < need:
                 if self._scratch is not None:
                     self._kept.append(self._scratch)   # a captured graph may hold its address

@@ -425,9 +425,9 @@ int dfl_kv8_append(const dfl_kv8 *c, const int32_t *len, const int32_t *cnt, int
  * it does nothing. Cuts back like dfl_kv8_append. */
 int dfl_kv8_stage(const dfl_kv8 *c, const int32_t *len, const int32_t *cnt, int rows, const float *k,
                   const float *v, int64_t ld, void *cuda_stream);
-/* Scratch bytes that dfl_kv8_attn needs for n_q query heads, rows and score, or -1 for a shape it does not
- * take. */
-int64_t dfl_kv8_attn_scratch_bytes(const dfl_kv8 *c, int n_q, int rows, int score);
+/* Scratch bytes that dfl_kv8_attn needs for n_q query heads, rows, window and score, or -1 for a shape it does
+ * not take. */
+int64_t dfl_kv8_attn_scratch_bytes(const dfl_kv8 *c, int n_q, int rows, int window, int score);
 /* Grouped-query attention of the staged rows (1..DFL_MAX_ROWS) over the cache:
  *   out[s][m][h] = sum_j softmax_j(scale * q[s][m][h] . k_j) v_j,  key/value head h / (n_q / n_kv).
  * Row m of sequence s sits at position p = len + m. causal != 0: it sees the tokens j <= p, with

@@ -69,12 +69,12 @@ def test_scores_need_a_cache_that_keeps_them():
     c = cache(score=None)
     assert calls(c, L)["attn"](score=1) == -1
     assert calls(c, L)["evict"]() == -1
-    assert L.dfl_kv8_attn_scratch_bytes(ctypes.byref(cache()), 4, 8, 1) > 0
+    assert L.dfl_kv8_attn_scratch_bytes(ctypes.byref(cache()), 4, 8, 0, 1) > 0
 
 
-@pytest.mark.parametrize("n_q,rows", [(3, 1), (0, 1), (4, 0), (4, 17), (34, 1)])
-def test_scratch_of_shapes_it_does_not_take(n_q, rows):
-    assert _abi.lib().dfl_kv8_attn_scratch_bytes(ctypes.byref(cache()), n_q, rows, 0) == -1
+@pytest.mark.parametrize("n_q,rows,window", [(3, 1, 0), (0, 1, 0), (4, 0, 0), (4, 17, 0), (34, 1, 0), (4, 1, -1)])
+def test_scratch_of_shapes_it_does_not_take(n_q, rows, window):
+    assert _abi.lib().dfl_kv8_attn_scratch_bytes(ctypes.byref(cache()), n_q, rows, window, 0) == -1
 
 
 def test_constants():
