@@ -334,32 +334,49 @@ struct AttnKvArgs {
     int n_q, rows, window, causal, score;
     const int32_t *len, *cnt;
     float scale;
-    int groups, splits;   // row groups of a head, splits of a row group's coded blocks (at most)
-    int apart;            // 1: the tail has a CTA of its own (grid x 0, the splits follow); 0: the last split's takes it
-    float *part_o;        // [unit][part][rows of a group][head_dim], unit = (sequence, head, row group); part 0 is the
-                          // tail's, the splits follow
-    float *part_ml;       // [unit][part][rows of a group][2]: running maximum (base 2) and sum
-    int *part_bad;        // [unit][part]: a table entry was out of range
+    int groups;           // row groups of a head
+    // How the work is cut (see attn_cut). share == 0: `splits` CTAs at most for a unit's coded blocks, and with `apart` one
+    // more for its tail (grid x 0; else the last split's CTA takes it). share != 0: `ctas` CTAs share all units evenly.
+    int splits, apart, share, ctas;
+    float *part_o;        // [part][rows of a group][head_dim]
+    float *part_ml;       // [part][rows of a group][2]: running maximum (base 2) and sum
+    int *part_bad;        // [part]: a table entry was out of range
     float *blk_lse;       // [sequence][head][n_blocks][16]: log2 of the block's share of row 0's sums
 };
 
+// A unit is one row group of a head: unit (s * n_kv + h) * groups + rg. The sums of its tail and of each CTA that has some
+// of its coded blocks are parts, merged by k_kv8_merge. Part ids: with splits, the tail's of every unit, then the
+// splits'; with shares, CTA + unit, which no two (CTA, unit) have in common, as both only grow along the work.
+__device__ __forceinline__ size_t units_of(const AttnKvArgs &a) { return (size_t)a.c.n_seq * a.c.n_kv * a.groups; }
+__device__ __forceinline__ size_t part_of(const AttnKvArgs &a, size_t unit, int i) {   // i: split or CTA
+    return units_of(a) + (a.share ? unit + i : unit * a.splits + i);
+}
+
 struct Span {
     int z, L, n, bad;   // sealed blocks, committed tokens, staged rows
-    int b0, nb;         // blocks that some row sees: b0 .. b0 + nb - 1 (those from z on lie in the tail)
+    int b0, nb;         // blocks that some row sees: b0 .. b0 + nb - 1
+    int coded;          // the first so many of them are held as codes, the others lie in the tail
+    int groups;         // row groups that have rows
 };
-__device__ __forceinline__ Span span_of(const AttnKvArgs &a, int s, const KvView &w) {
-    Span p{*w.sealed, a.len[s], rows_of(a.cnt, s, a.rows), 0, 0, 0};
-    if (p.z < 0 || p.z > w.nb)
+__device__ __forceinline__ Span span_of(const AttnKvArgs &a, int s, int sealed, int rows_per_group) {
+    Span p{sealed, a.len[s], rows_of(a.cnt, s, a.rows), 0, 0, 0, 0, 0};
+    if (p.z < 0 || p.z > a.c.n_blocks)
         p.bad = kErrTable;
-    else if (p.L < 0 || p.L > kBlk * w.nb - p.n)
+    else if (p.L < 0 || p.L > kBlk * a.c.n_blocks - p.n)
         p.bad = kErrCapacity;
     else if (p.L < kBlk * p.z || p.L + p.n > kBlk * p.z + kTail)
         p.bad = kErrState;
     if (p.bad || p.n == 0) return p;
     const int at = a.causal ? p.L : p.L - 1;
     p.b0 = (a.window > 0 ? max(0, at - a.window + 1) : 0) / kBlk;
-    p.nb = (p.L + p.n - 1) / kBlk + 1 - p.b0;
+    p.nb = (p.L + p.n - 1) / kBlk + 1 - p.b0;   // every row sees its own token, so the tail is never empty
+    p.coded = min(p.nb, max(0, p.z - p.b0));
+    p.groups = (p.n * (a.n_q / a.c.n_kv) + rows_per_group - 1) / rows_per_group;
     return p;
+}
+// the span of a sequence by its first head: every call leaves the heads of a sequence with equal sealed counts
+__device__ __forceinline__ Span span_of_seq(const AttnKvArgs &a, int s, int rows_per_group) {
+    return span_of(a, s, a.c.sealed[(size_t)s * a.c.n_kv], rows_per_group);
 }
 // the tokens lo..hi-1 that row m sees
 __device__ __forceinline__ void seen(const AttnKvArgs &a, const Span &p, int m, int &lo, int &hi) {
@@ -465,54 +482,79 @@ __device__ __forceinline__ float group_sum(float x) {
 template <int N>
 __device__ __forceinline__ void cp_async_wait_groups() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// the splits that a head's blocks are worth: at least one block a warp
+// the splits that coded blocks are worth: at least one block a warp
 template <int W>
-__device__ __forceinline__ int splits_of(int splits, int nb) { return max(1, min(splits, (nb + W - 1) / W)); }
+__device__ __forceinline__ int splits_of(int splits, int coded) { return min(splits, (coded + W - 1) / W); }
 
-// One CTA per split of a row group: 8 NT query rows (row r = m * group + i of the head's rows). Each warp takes
-// its share of the split's blocks with a running softmax of its own; no barrier until they are merged at the
-// end. A warp's codes pass through a ring of its own in shared memory (16-byte asynchronous copies).
+// Shares: the work in the order of its units, each weighing its coded blocks and, behind them, its tail as
+// kTailWeight. CTA b of G takes the weights [W b / G, W (b + 1) / G).
+constexpr int kTailWeight = 8;
+__device__ __forceinline__ long weight_of(const AttnKvArgs &a, const Span &p) { return (long)a.c.n_kv * p.groups * (p.coded + kTailWeight); }
+template <int W>
+__device__ __forceinline__ int shares_of(const AttnKvArgs &a, long work) { return int(min((long)a.ctas, (work + W - 1) / W)); }
+
+// block-wide sums of two numbers (all threads call it and get them)
+__device__ __forceinline__ void block_sums(long &x, long &y, long (*sm)[2]) {
+    x = warp_sum(x);
+    y = warp_sum(y);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5][0] = x, sm[threadIdx.x >> 5][1] = y;
+    __syncthreads();
+    x = y = 0;
+    for (int i = 0; i < int(blockDim.x >> 5); ++i) x += sm[i][0], y += sm[i][1];
+}
+
+// What a CTA does of a unit: its coded blocks x0..x1-1 (of the span's), and its tail or not.
+struct Piece {
+    int s, h, rg, x0, x1;
+    bool tail, whole;   // whole: all of the unit, which then needs no merge
+    size_t tail_part, code_part;
+};
 template <int HD, int NT>
-__global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, NT>::kCtas) k_kv8_attn(AttnKvArgs a) {
+struct AttnShared {     // maxima and sums of the warps, and behind them the tail's
+    float q_scale[8 * NT], m[AttnShape<HD, NT>::kWarps + 1][8 * NT], l[AttnShape<HD, NT>::kWarps + 1][8 * NT];
+    int bad;
+    uint32_t poison[2];
+};
+template <int HD, int NT>
+struct QueryRows {      // a warp takes every kWarps-th row of the group
+    static constexpr int kW = AttnShape<HD, NT>::kWarps, kRows = (8 * NT + kW - 1) / kW;
+    float2 x[kRows][HD / 64];
+    __device__ __forceinline__ void load(const AttnKvArgs &a, int s, int h, int rg) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = a.n_q / a.c.n_kv;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = warp + i * kW, rid = rg * 8 * NT + r;
+            const bool on = r < 8 * NT && rid < a.rows * per;
+            const float *q = a.q + ((size_t)s * a.rows + rid / per) * a.ldq + (size_t)(h * per + rid % per) * HD + 2 * lane;
+#pragma unroll
+            for (int k = 0; k < HD / 64; ++k) x[i][k] = on ? *reinterpret_cast<const float2 *>(q + 64 * k) : make_float2(0.f, 0.f);
+        }
+    }
+};
+
+// One CTA's piece of a unit: 8 NT query rows (row r = m * group + i of the head's rows). Each warp takes every kW-th of the
+// blocks with a running softmax of its own; no barrier until they are merged at the end. A warp's codes pass through a
+// ring of its own in shared memory (16-byte asynchronous copies). The caller has the query rows under way: what is small
+// is asked for first, so that it does not wait behind the codes.
+template <int HD, int NT>
+__device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, const Piece &u, QueryRows<HD, NT> &qr, uint8_t *kv_smem, AttnShared<HD, NT> &sh) {
     using S = AttnShape<HD, NT>;
-    constexpr int RG = 8 * NT, kW = S::kWarps, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4;
+    constexpr int RG = 8 * NT, kW = S::kWarps, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4, kQRows = QueryRows<HD, NT>::kRows;
     static_assert(kW * RG * kPitch * 4 <= S::kSmem, "the merge reuses the shared memory");
-    extern __shared__ __align__(16) uint8_t kv_smem[];
-    __shared__ float q_scale[RG], sm_m[kW][RG], sm_l[kW][RG];
-    __shared__ int sm_bad;
-    __shared__ uint32_t sm_poison[2];
-    const int split = int(blockIdx.x) - a.apart, h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z;
+    auto &q_scale = sh.q_scale;
+    auto &sm_m = sh.m;
+    auto &sm_l = sh.l;
+    auto &qx = qr.x;
+    int &sm_bad = sh.bad;
+    uint32_t(&sm_poison)[2] = sh.poison;
+    const int s = u.s, h = u.h, rg = u.rg;
+    const bool tail = u.tail, codes = u.x1 > u.x0, alone = p.coded == 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const KvView w = view(a.c, s, h);
-    const int per = a.n_q / a.c.n_kv;
-    // What is small is asked for first, so that it does not wait behind the codes: the query rows (a warp takes
-    // every kW-th), lengths, the table, scales, the tail.
-    constexpr int kQRows = (RG + kW - 1) / kW;
-    float2 qx[kQRows][HD / 64];
-#pragma unroll
-    for (int i = 0; i < kQRows; ++i) {
-        const int r = warp + i * kW, rid = rg * RG + r;
-        const bool on = r < RG && rid < a.rows * per;
-        const float *q = a.q + ((size_t)s * a.rows + rid / per) * a.ldq + (size_t)(h * per + rid % per) * HD + 2 * lane;
-#pragma unroll
-        for (int k = 0; k < HD / 64; ++k) qx[i][k] = on ? *reinterpret_cast<const float2 *>(q + 64 * k) : make_float2(0.f, 0.f);
-    }
-    const Span p = span_of(a, s, w);
-    pdl_trigger();
-    if (p.bad) {
-        if (tid == 0 && blockIdx.x == 0) atomicOr(a.c.err, p.bad);
-        return;
-    }
-    const int live = p.n * per - rg * RG;                            // rows of this group that exist
-    const int coded = min(p.nb, max(0, p.z - p.b0));                // blocks held as codes that some row sees
-    const int nsplit = coded ? splits_of<kW>(a.splits, coded) : 0;
-    const bool alone = nsplit == 0, tail = a.apart ? split < 0 : split == max(nsplit - 1, 0);   // every row sees its own token, so the tail is never empty
-    if (live <= 0 || (split >= nsplit && !tail)) return;
-    const bool codes = split >= 0 && split < nsplit;
-    const int x0 = codes ? int((long)coded * split / nsplit) : 0, x1 = codes ? int((long)coded * (split + 1) / nsplit) : 0;
-    const int bfirst = p.b0 + x0 + warp;                             // this warp's blocks: bfirst, + kW, ..
-    const int ncoded = max(0, (x1 - x0 - warp + kW - 1) / kW);
-    const size_t unit = ((size_t)s * a.c.n_kv + h) * a.groups + rg, at = unit * (a.splits + 1);   // the unit's parts: the tail's, then the splits'
+    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG;    // rows of this group that exist
+    const int bfirst = p.b0 + u.x0 + warp;                           // this warp's blocks: bfirst, + kW, ..
+    const int ncoded = max(0, (u.x1 - u.x0 - warp + kW - 1) / kW);
 
     int bad = 0;
     auto load_phys = [&](int i0) {                                   // lane l: where block i0 + l is stored
@@ -555,6 +597,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     auto stage_q = [&]() {
         if (tid < 2) sm_poison[tid] = 0;
         if (tid == 0) sm_bad = 0;
+        if (tid < RG) sm_m[kW][tid] = -INFINITY, sm_l[kW][tid] = 0.f;
 #pragma unroll
         for (int j = 0; j < kQRows; ++j) {
             const int r = warp + j * kW;
@@ -768,7 +811,9 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
                     const int r = 8 * nt + 2 * t + e;
                     total[nt][e] = sum[0] + sum[1];
                     if (warp == 0 && g == 0) {
-                        *reinterpret_cast<float2 *>(a.part_ml + (at * RG + r) * 2) = make_float2(top, sum[0] + sum[1]);
+                        *reinterpret_cast<float2 *>(a.part_ml + (u.tail_part * RG + r) * 2) = make_float2(top, sum[0] + sum[1]);
+                        sm_m[kW][r] = top;
+                        sm_l[kW][r] = sum[0] + sum[1];
                         if (keep_lse && r < per)
                             for (int i = 0; i < 2; ++i)
                                 if (p.z + i < p.b0 + p.nb) lse[(size_t)(p.z + i) * 16 + r] = sum[i] == 0.f ? -INFINITY : ref + log2f(sum[i]);
@@ -813,13 +858,12 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
                     for (int k = 0; k < 4; ++k) {
                         const int r = 8 * nt + 2 * t + (k & 1), d0 = 16 * (warp * kSteps + i) + g + 8 * (k >> 1), rid = rg * RG + r;
                         if (!alone)
-                            a.part_o[(at * RG + r) * HD + d0] = d[nt][k];
+                            a.part_o[(u.tail_part * RG + r) * HD + d0] = d[nt][k];
                         else if (r < live)
                             a.out[((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + d0] = d[nt][k] / total[nt][k & 1];
                     }
             }
         }
-        if (tid == 0) a.part_bad[at] = 0;
         if (!codes) return;
         __syncthreads();                                             // the slots held back are free
 #pragma unroll
@@ -1059,23 +1103,22 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
             }
         }
     __syncthreads();
-    const size_t mine = at + 1 + split;
     if (tid == 0) {
         if (sm_bad) atomicOr(a.c.err, kErrTable);
-        a.part_bad[mine] = sm_bad;
+        a.part_bad[u.code_part] = sm_bad;
     }
     if (sm_bad) return;
-    if (tid < RG) {   // each warp's factor, in place of its maximum
+    if (tid < RG) {   // each state's factor, in place of its maximum
         float top = -INFINITY, total = 0.f;
-#pragma unroll
-        for (int i = 0; i < kW; ++i) top = fmaxf(top, sm_m[i][tid]);
-#pragma unroll
-        for (int i = 0; i < kW; ++i) {
+        const int n = u.whole ? kW + 1 : kW;
+        for (int i = 0; i < n; ++i) top = fmaxf(top, sm_m[i][tid]);
+        for (int i = 0; i < n; ++i) {
             const float f = sm_m[i][tid] == top ? 1.f : ex2(sm_m[i][tid] - top);
             sm_m[i][tid] = f;
             total = fmaf(sm_l[i][tid], f, total);
         }
-        *reinterpret_cast<float2 *>(a.part_ml + (mine * RG + tid) * 2) = make_float2(top, total);
+        sm_l[0][tid] = total;
+        *reinterpret_cast<float2 *>(a.part_ml + (u.code_part * RG + tid) * 2) = make_float2(top, total);
     }
     __syncthreads();
     for (int e = tid; e < min(live, RG) * (HD / 4); e += kW * 32) {
@@ -1084,80 +1127,255 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         auto add = [&](const float4 &y, float f) {
             sum.x = fmaf(y.x, f, sum.x), sum.y = fmaf(y.y, f, sum.y), sum.z = fmaf(y.z, f, sum.z), sum.w = fmaf(y.w, f, sum.w);
         };
+        if (u.whole) add(*reinterpret_cast<const float4 *>(a.part_o + (u.tail_part * RG + r) * HD + d), sm_m[kW][r]);
 #pragma unroll
         for (int i = 0; i < kW; ++i) add(*reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(kv_smem) + (i * RG + r) * kPitch + d), sm_m[i][r]);
-        *reinterpret_cast<float4 *>(a.part_o + (mine * RG + r) * HD + d) = sum;
+        if (u.whole) {
+            const int rid = rg * RG + r;
+            const float total = sm_l[0][r];
+            *reinterpret_cast<float4 *>(a.out + ((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + d) =
+                make_float4(sum.x / total, sum.y / total, sum.z / total, sum.w / total);
+        } else {
+            *reinterpret_cast<float4 *>(a.part_o + (u.code_part * RG + r) * HD + d) = sum;
+        }
     }
 }
 
-// Merges the splits of a row in a fixed order (grid x < rows of a group: one row each), and adds row 0's share of
-// 256 blocks to the scores (grid x behind them, row group 0).
-constexpr int kMergeThreads = 256;
-constexpr int kMaxSplits = 63;   // with the tail's, two parts a lane of the merge
+// Splits: grid (splits, heads x row groups, sequences).
 template <int HD, int NT>
-__global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
-    constexpr int RG = 8 * NT, kLanes = kMergeThreads / (HD / 4);   // splits taken at once
-    __shared__ float4 acc[kLanes][HD / 4];
-    __shared__ float fac[64], top_s[16], total_s[16];
-    const int h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
-    const bool row_part = blockIdx.x < RG;
-    const KvView w = view(a.c, s, h);
-    const Span p = span_of(a, s, w);
-    pdl_wait();   // by every CTA, so that this grid does not end before the one it follows
-    if (p.bad || (!row_part && rg)) return;
-    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, coded = min(p.nb, max(0, p.z - p.b0));
-    const int nsplit = 1 + (coded ? splits_of<AttnShape<HD, NT>::kWarps>(a.splits, coded) : 0);   // the tail's and the splits' parts
-    const int b0 = p.b0 + (int(blockIdx.x) - RG) * kMergeThreads;
-    if (live <= 0 || (row_part ? int(blockIdx.x) >= live || nsplit == 1 : b0 >= p.b0 + p.nb)) return;
-    const size_t at = (((size_t)s * a.c.n_kv + h) * a.groups + rg) * (a.splits + 1);
-    if (__syncthreads_or(tid < nsplit && a.part_bad[at + tid])) return;
-    // a warp's view of row r: the largest maximum, the sum, and each split's factor
-    auto state = [&](int r, float &top, float &total, float (&f)[2]) {
-        float m[2], l[2];
+__global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, NT>::kCtas) k_kv8_attn(AttnKvArgs a) {
+    constexpr int RG = 8 * NT, kW = AttnShape<HD, NT>::kWarps;
+    extern __shared__ __align__(16) uint8_t kv_smem[];
+    __shared__ AttnShared<HD, NT> sh;
+    const int split = int(blockIdx.x) - a.apart;
+    Piece u{int(blockIdx.z), int(blockIdx.y) / a.groups, int(blockIdx.y) % a.groups};
+    QueryRows<HD, NT> q;
+    q.load(a, u.s, u.h, u.rg);
+    const Span p = span_of(a, u.s, a.c.sealed[(size_t)u.s * a.c.n_kv + u.h], RG);
+    pdl_trigger();
+    if (p.bad) {
+        if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(a.c.err, p.bad);
+        return;
+    }
+    const int nsplit = splits_of<kW>(a.splits, p.coded);
+    u.tail = a.apart ? split < 0 : split == max(nsplit - 1, 0);
+    if (u.rg >= p.groups || (split >= nsplit && !u.tail)) return;
+    const bool codes = split >= 0 && split < nsplit;
+    u.x0 = codes ? int((long)p.coded * split / nsplit) : 0;
+    u.x1 = codes ? int((long)p.coded * (split + 1) / nsplit) : 0;
+    u.whole = nsplit == 1 && !a.apart;
+    u.tail_part = ((size_t)u.s * a.c.n_kv + u.h) * a.groups + u.rg;
+    u.code_part = part_of(a, u.tail_part, split);
+    attn_piece<HD, NT>(a, p, u, q, kv_smem, sh);
+}
+
+// Shares: a.ctas CTAs.
+template <int HD, int NT>
+__global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, NT>::kCtas) k_kv8_attn_share(AttnKvArgs a) {
+    constexpr int RG = 8 * NT, kW = AttnShape<HD, NT>::kWarps;
+    extern __shared__ __align__(16) uint8_t kv_smem[];
+    __shared__ AttnShared<HD, NT> sh;
+    __shared__ long sm_sums[kW][2], sm_off;
+    __shared__ int sm_seq;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+    pdl_trigger();
+    // the work in all, this CTA's share of it, and the sequence that the share begins in
+    long work = 0, none = 0;
+    for (int i = tid; i < a.c.n_seq; i += kW * 32) {
+        const Span p = span_of_seq(a, i, RG);
+        if (p.bad && cta == 0) atomicOr(a.c.err, p.bad);
+        work += weight_of(a, p);
+    }
+    block_sums(work, none, sm_sums);
+    const int G = shares_of<kW>(a, work);
+    if (cta >= G) return;
+    long pos = work * cta / G, off = 0;
+    const long pos_end = work * (cta + 1) / G;
+    for (int base = 0; base < a.c.n_seq; base += kW * 32) {
+        const long x = base + tid < a.c.n_seq ? weight_of(a, span_of_seq(a, base + tid, RG)) : 0;
+        long upto = x;                                               // of the warp, then of the chunk
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int i = lane + 32 * k;
-            const float2 y = i < nsplit ? *reinterpret_cast<const float2 *>(a.part_ml + ((at + i) * RG + r) * 2) : make_float2(-INFINITY, 0.f);
-            m[k] = y.x, l[k] = y.y;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
         }
-        top = fmaxf(m[0], m[1]);
+        __syncthreads();
+        if (lane == 31) sm_sums[warp][0] = upto;
+        if (tid == 0) sm_seq = -1;
+        __syncthreads();
+        long chunk = 0;
+        for (int i = 0; i < kW; ++i) {
+            if (i < warp) upto += sm_sums[i][0];
+            chunk += sm_sums[i][0];
+        }
+        if (pos < off + upto && pos >= off + upto - x) sm_seq = base + tid, sm_off = off + upto - x;
+        __syncthreads();
+        if (sm_seq >= 0) break;
+        off += chunk;
+    }
+    off = sm_off;
+    for (int s = sm_seq; pos < pos_end;) {
+        const Span p = span_of_seq(a, s, RG);
+        const long mine = weight_of(a, p);
+        if (pos >= off + mine) {                                     // the next sequence
+            off += mine;
+            ++s;
+            continue;
+        }
+        const int weight = p.coded + kTailWeight, ui = int((pos - off) / weight), from = int(pos - off - (long)ui * weight);
+        const int to = int(min((long)weight, from + pos_end - pos));
+        pos += to - from;
+        Piece u{s, ui / p.groups, ui % p.groups, min(from, p.coded), min(to, p.coded)};
+        u.tail = from <= p.coded && to > p.coded;
+        u.whole = from == 0 && u.tail && u.x1 > 0;
+        u.tail_part = ((size_t)s * a.c.n_kv + u.h) * a.groups + u.rg;
+        u.code_part = part_of(a, u.tail_part, cta);
+        if (a.c.sealed[(size_t)s * a.c.n_kv + u.h] != p.z) {         // heads of a sequence that differ: left alone
+            if (tid == 0) atomicOr(a.c.err, kErrState);
+            continue;
+        }
+        if (!u.tail && u.x0 == u.x1) continue;
+        QueryRows<HD, NT> q;
+        q.load(a, s, u.h, u.rg);
+        __syncthreads();                                             // the piece before is done with the shared memory
+        attn_piece<HD, NT>(a, p, u, q, kv_smem, sh);
+    }
+}
+
+// Merges the parts of a unit's rows in a fixed order (grid x < row_ctas), and adds row 0's share of 256 blocks to the
+// scores (grid x behind them, row group 0). HD / 4 threads take four channels each of a row; with `apart_rows` all threads of
+// a CTA take one row and share out its parts (few units of many parts), else each such group takes a row of its own.
+constexpr int kMergeThreads = 256;
+constexpr int kMaxCtas = 304;   // two for each SM
+template <int HD, int NT>
+__global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int row_ctas, int apart_rows) {
+    constexpr int RG = 8 * NT, kLanes = kMergeThreads / (HD / 4), kSome = 4;
+    __shared__ float4 acc[kLanes][HD / 4];
+    __shared__ float fac[kMaxCtas + 1], top_s[16], total_s[16];
+    __shared__ long sums[kMergeThreads / 32][2];
+    const int h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
+    const bool row_part = int(blockIdx.x) < row_ctas;
+    const KvView w = view(a.c, s, h);
+    const int sealed = *w.sealed;
+    const Span p = span_of(a, s, sealed, RG);
+    const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, row0 = blockIdx.x * (apart_rows ? 1 : kLanes);
+    const int b0 = p.b0 + (int(blockIdx.x) - row_ctas) * kMergeThreads;
+    bool off_duty = p.bad || live <= 0 || (row_part ? row0 >= live || p.coded == 0 : rg || b0 >= p.b0 + p.nb);
+    long W = 0, before = 0;                                          // the work in all, and that of the sequences before s
+    if (a.share && !off_duty) {
+        off_duty = a.c.sealed[(size_t)s * a.c.n_kv] != sealed;
+        for (int i = tid; i < a.c.n_seq; i += kMergeThreads) {
+            const long x = weight_of(a, span_of_seq(a, i, RG));
+            W += x;
+            before += i < s ? x : 0;
+        }
+        block_sums(W, before, sums);
+    }
+    // the parts: the tail's, then those of the splits or of the CTAs that took some of the unit's blocks
+    const size_t unit = ((size_t)s * a.c.n_kv + h) * a.groups + rg;
+    int first = 0, parts = 1 + splits_of<AttnShape<HD, NT>::kWarps>(a.splits, p.coded);
+    bool whole = parts == 2 && !a.apart;
+    if (a.share && !off_duty) {
+        const int G = shares_of<AttnShape<HD, NT>::kWarps>(a, W);
+        const long start = before + (long)(h * p.groups + rg) * (p.coded + kTailWeight);
+        first = int(cta_of(start, W, G));
+        parts = p.coded ? 2 + int(cta_of(start + p.coded - 1, W, G)) - first : 1;
+        whole = p.coded && cta_of(start + p.coded, W, G) == first;
+    }
+    pdl_wait();   // by every CTA, so that this grid does not end before the one it follows
+    if (off_duty || (whole && row_part)) return;                     // a whole unit's CTA has written it
+    const size_t part1 = part_of(a, unit, first);
+    auto id = [&](int i) { return i == 0 ? unit : part1 + i - 1; };
+    int bad = 0;
+    for (int i = 1 + tid; i < parts; i += kMergeThreads) bad |= a.part_bad[id(i)];
+    auto put = [&](int r, int d4, const float4 &sum, float total) {
+        const int rid = rg * RG + r;
+        *reinterpret_cast<float4 *>(a.out + ((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + 4 * d4) =
+            make_float4(sum.x / total, sum.y / total, sum.z / total, sum.w / total);
+    };
+    auto add = [](float4 &sum, const float4 &y, float f) {
+        sum.x = fmaf(y.x, f, sum.x), sum.y = fmaf(y.y, f, sum.y), sum.z = fmaf(y.z, f, sum.z), sum.w = fmaf(y.w, f, sum.w);
+    };
+    const int d4 = tid % (HD / 4), i0 = tid / (HD / 4);
+    if (row_part && !apart_rows) {
+        const int r = row0 + i0;
+        const bool on = r < min(live, RG);
+        float2 ml[kSome];
+        float4 y[kSome];
+#pragma unroll
+        for (int i = 0; i < kSome; ++i)                              // the first parts' loads all at once
+            if (on && i < parts) {
+                ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + (id(i) * RG + r) * 2);
+                y[i] = *reinterpret_cast<const float4 *>(a.part_o + (id(i) * RG + r) * HD + 4 * d4);
+            }
+        if (__syncthreads_or(bad) || !on) return;
+        float top = -INFINITY, total = 0.f;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kSome; ++i)
+            if (i < parts) top = fmaxf(top, ml[i].x);
+        for (int i = kSome; i < parts; ++i) top = fmaxf(top, a.part_ml[(id(i) * RG + r) * 2]);
+        auto take = [&](const float2 &x, const float4 &v) {
+            const float f = x.x == top ? 1.f : ex2(x.x - top);
+            total = fmaf(x.y, f, total);
+            add(sum, v, f);
+        };
+#pragma unroll
+        for (int i = 0; i < kSome; ++i)
+            if (i < parts) take(ml[i], y[i]);
+        for (int i = kSome; i < parts; ++i)
+            take(*reinterpret_cast<const float2 *>(a.part_ml + (id(i) * RG + r) * 2), *reinterpret_cast<const float4 *>(a.part_o + (id(i) * RG + r) * HD + 4 * d4));
+        put(r, d4, sum, total);
+        return;
+    }
+    if (__syncthreads_or(bad)) return;
+    // a warp's view of row r: the largest maximum and the sum, and each part's factor to f; a whole unit's coded part holds
+    // the sums of its tail too
+    auto state = [&](int r, float &top, float &total, float *f) {
+        const int i1 = whole ? 1 : 0;
+        top = -INFINITY;
+        for (int i = i1 + lane; i < parts; i += 32) top = fmaxf(top, a.part_ml[(id(i) * RG + r) * 2]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll
-        for (int k = 0; k < 2; ++k) f[k] = m[k] == top ? 1.f : ex2(m[k] - top);
-        total = warp_sum(l[0] * f[0] + l[1] * f[1]);
-    };
-    float top, total, f[2];
-    if (row_part) {
-        const int r = blockIdx.x, d4 = tid % (HD / 4), i0 = tid / (HD / 4);
-        state(r, top, total, f);
-        if (tid < 32) fac[lane] = f[0], fac[lane + 32] = f[1];
-        __syncthreads();
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = i0; i < nsplit; i += kLanes) {
-            const float4 y = *reinterpret_cast<const float4 *>(a.part_o + ((at + i) * RG + r) * HD + 4 * d4);
-            sum.x = fmaf(y.x, fac[i], sum.x);
-            sum.y = fmaf(y.y, fac[i], sum.y);
-            sum.z = fmaf(y.z, fac[i], sum.z);
-            sum.w = fmaf(y.w, fac[i], sum.w);
+        total = 0.f;
+        for (int i = i1 + lane; i < parts; i += 32) {
+            const float2 y = *reinterpret_cast<const float2 *>(a.part_ml + (id(i) * RG + r) * 2);
+            const float x = y.x == top ? 1.f : ex2(y.x - top);
+            total = fmaf(y.y, x, total);
+            if (f) f[i] = x;
         }
+        total = warp_sum(total);
+    };
+    float top, total;
+    if (row_part) {
+        float4 y[kSome], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kSome; ++k)                              // on their way while the factors are found
+            if (i0 + k * kLanes < parts) y[k] = *reinterpret_cast<const float4 *>(a.part_o + (id(i0 + k * kLanes) * RG + row0) * HD + 4 * d4);
+        if (tid < 32) {
+            state(row0, top, total, fac);
+            if (lane == 0) total_s[0] = total;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kSome; ++k)
+            if (i0 + k * kLanes < parts) add(sum, y[k], fac[i0 + k * kLanes]);
+#pragma unroll 4
+        for (int i = i0 + kSome * kLanes; i < parts; i += kLanes) add(sum, *reinterpret_cast<const float4 *>(a.part_o + (id(i) * RG + row0) * HD + 4 * d4), fac[i]);
         acc[i0][d4] = sum;
         __syncthreads();
         if (i0 == 0) {
 #pragma unroll
             for (int i = 1; i < kLanes; ++i) {
-                const float4 y = acc[i][d4];
-                sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+                const float4 v = acc[i][d4];
+                sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
             }
-            const int rid = rg * RG + r;
-            *reinterpret_cast<float4 *>(a.out + ((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + 4 * d4) =
-                make_float4(sum.x / total, sum.y / total, sum.z / total, sum.w / total);
+            put(row0, d4, sum, total_s[0]);
         }
         return;
     }
     for (int r = tid >> 5; r < per; r += kMergeThreads / 32) {
-        state(r, top, total, f);
+        state(r, top, total, nullptr);
         if (lane == 0) top_s[r] = top - kTop, total_s[r] = total;
     }
     __syncthreads();
@@ -1172,14 +1390,15 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a) {
 
 // ---- host side ----
 // How a call's work is cut: row groups of 8 rows, or of 16 (whose codes are expanded once for two products) where a head
-// has more than 8; splits of a group's keys, and a CTA of its own for the tail or not. Everything should fit in one wave of
-// the part's 152 SMs: CTAs of a second one were measured to wait for tens of microseconds although slots were free. Costs are
-// in blocks a warp; a CTA's start and end are worth about 6, a tail inside a CTA 3.
+// has more than 8. Up to as many units as half the CTAs that fit the part's 152 SMs at once: splits of a unit's blocks, and
+// a CTA of its own for the tail or not; all in one wave (CTAs of a second one were measured to wait for tens of microseconds
+// although slots were free). Costs are in blocks a warp; a tail inside a CTA is worth about 3. More units: shares.
 struct AttnCut {
-    int nt, groups, splits, apart;
+    int nt, groups, splits, apart, share, ctas;
     size_t units, o_bytes, ml_bytes, bad_bytes, lse_bytes, total;
 };
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+constexpr int kMaxSplits = 127;
 AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
     AttnCut t{};
     const int r = rows * (n_q / c->n_kv);
@@ -1187,20 +1406,24 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
     t.groups = (r + 8 * t.nt - 1) / (8 * t.nt);
     t.units = (size_t)c->n_seq * c->n_kv * t.groups;
     const int warps = c->head_dim == 128 && t.nt == 2 ? AttnShape<128, 2>::kWarps : AttnShape<128, 1>::kWarps;
-    const int slots = 152 * (c->head_dim == 256 ? 1 : 2), blocks = window ? std::min(c->n_blocks, window / kBlk + 2) : c->n_blocks;
-    const int most = std::min(kMaxSplits, (blocks + warps - 1) / warps);
-    double best = 0;
-    for (int apart = 0; apart < 2; ++apart)
-        for (int n = 1; n <= most; ++n) {
-            const double waves = double((t.units * (n + apart) + slots - 1) / slots);
-            if (waves > 1 && apart) continue;
-            const double cost = waves * (double((blocks + warps * n - 1) / (warps * n)) + 6 + (apart ? 0 : 3));
-            if ((n == 1 && !apart) || cost < best) best = cost, t.splits = n, t.apart = apart;
-        }
-    const size_t parts = t.units * (t.splits + 1) * 8 * t.nt;
-    t.o_bytes = up256(parts * c->head_dim * 4);
-    t.ml_bytes = up256(parts * 8);
-    t.bad_bytes = up256(t.units * (t.splits + 1) * 4);
+    const int slots = c->head_dim == 256 ? kMaxCtas / 2 : kMaxCtas, blocks = window ? std::min(c->n_blocks, window / kBlk + 2) : c->n_blocks;
+    t.splits = 1;
+    if (t.units > (size_t)slots / 2) {
+        t.share = 1;
+        t.ctas = slots;
+    } else {
+        const int most = std::min(kMaxSplits, (blocks + warps - 1) / warps);
+        int best = 0;
+        for (int apart = 0; apart < 2; ++apart)
+            for (int n = 1; n <= most && t.units * (n + apart) <= (size_t)slots; ++n) {
+                const int cost = (blocks + warps * n - 1) / (warps * n) + (apart ? 0 : 3);
+                if (!best || cost < best) best = cost, t.splits = n, t.apart = apart;
+            }
+    }
+    const size_t parts = t.share ? 2 * t.units + t.ctas : t.units * (t.splits + 1);
+    t.o_bytes = up256(parts * 8 * t.nt * c->head_dim * 4);
+    t.ml_bytes = up256(parts * 8 * t.nt * 8);
+    t.bad_bytes = up256(parts * 4);
     t.lse_bytes = score ? up256((size_t)c->n_seq * c->n_kv * c->n_blocks * 64) : 0;
     t.total = t.o_bytes + t.ml_bytes + t.bad_bytes + t.lse_bytes;
     return t;
@@ -1211,18 +1434,24 @@ cudaError_t launch_kv8_attn(const AttnKvArgs &a, cudaStream_t s) {
     static bool attr[kMaxDevices] = {};
     const int dev = current_device();
     if (dev < 0) return cudaErrorInvalidDevice;
-    const int smem = AttnShape<HD, NT>::kSmem;
+    const int smem = AttnShape<HD, NT>::kSmem, threads = AttnShape<HD, NT>::kWarps * 32;
+    cudaError_t e;
     if (!attr[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(k_kv8_attn<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(k_kv8_attn<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(k_kv8_attn_share<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
         attr[dev] = true;
     }
     const unsigned heads = unsigned(a.c.n_kv * a.groups);
-    k_kv8_attn<HD, NT><<<dim3(a.splits + a.apart, heads, a.c.n_seq), AttnShape<HD, NT>::kWarps * 32, smem, s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    const unsigned x = 8 * NT + (a.score ? (a.c.n_blocks + kMergeThreads - 1) / kMergeThreads : 0);
-    return launch_pdl(k_kv8_merge<HD, NT>, dim3(x, heads, a.c.n_seq), dim3(kMergeThreads), 0, s, a);
+    if (a.share)
+        k_kv8_attn_share<HD, NT><<<a.ctas, threads, smem, s>>>(a);
+    else
+        k_kv8_attn<HD, NT><<<dim3(a.splits + a.apart, heads, a.c.n_seq), threads, smem, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (!a.share && a.splits == 1 && !a.apart && !a.score) return cudaSuccess;   // every unit is one CTA's
+    const int apart_rows = !a.share && a.splits > 8, lanes = kMergeThreads / (HD / 4);
+    const int row_ctas = apart_rows ? 8 * NT : (8 * NT + lanes - 1) / lanes;
+    const unsigned x = row_ctas + (a.score ? (a.c.n_blocks + kMergeThreads - 1) / kMergeThreads : 0);
+    return launch_pdl(k_kv8_merge<HD, NT>, dim3(x, heads, a.c.n_seq), dim3(kMergeThreads), 0, s, a, row_ctas, apart_rows);
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -1456,7 +1685,7 @@ int dfl_kv8_attn(const dfl_kv8 *c, const float *q, int64_t ldq, int n_q, int row
     if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255) || (int64_t)scratch_bytes < dfl_kv8_attn_scratch_bytes(c, n_q, rows, window, score))
         return DFL_E_INVALID_ARG;
     const AttnCut t = attn_cut(c, n_q, rows, window, score);
-    AttnKvArgs a{*c, q, out, ldq, ldo, n_q, rows, window, causal != 0, score != 0, len, cnt, scale, t.groups, t.splits, t.apart};
+    AttnKvArgs a{*c, q, out, ldq, ldo, n_q, rows, window, causal != 0, score != 0, len, cnt, scale, t.groups, t.splits, t.apart, t.share, t.ctas};
     uint8_t *at = static_cast<uint8_t *>(scratch);
     a.part_o = reinterpret_cast<float *>(at);
     a.part_ml = reinterpret_cast<float *>(at += t.o_bytes);
