@@ -508,7 +508,7 @@ __device__ __forceinline__ void block_sums(long &x, long &y, long (*sm)[2]) {
 struct Piece {
     int s, h, rg, x0, x1;
     bool tail, whole;   // whole: all of the unit, which then needs no merge
-    size_t tail_part, code_part;
+    int index;          // of its coded part: the split, or the CTA
 };
 template <int HD, int NT>
 struct AttnShared {     // maxima and sums of the warps, and behind them the tail's
@@ -551,8 +551,10 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
     const int s = u.s, h = u.h, rg = u.rg;
     const bool tail = u.tail, codes = u.x1 > u.x0, alone = p.coded == 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const KvView w = view(a.c, s, h);
+    // registers are what limits the CTAs of an SM: what the loop needs seldom is found anew
+    const size_t head = (size_t)s * a.c.n_kv + h, head_blocks = head * a.c.n_blocks;
     const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG;    // rows of this group that exist
+    const int unit = int(head) * a.groups + rg;
     const int bfirst = p.b0 + u.x0 + warp;                           // this warp's blocks: bfirst, + kW, ..
     const int ncoded = max(0, (u.x1 - u.x0 - warp + kW - 1) / kW);
 
@@ -561,38 +563,34 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         const int i = i0 + lane;
         int at = 0;
         if (i < ncoded) {
-            at = w.table[bfirst + kW * i];
-            if (unsigned(at) >= unsigned(w.nb)) at = 0, bad = 1;
+            at = a.c.table[head_blocks + bfirst + kW * i];
+            if (unsigned(at) >= unsigned(a.c.n_blocks)) at = 0, bad = 1;
         }
         return at;
     };
     // this thread's rows: 8 nt + 2 t + e
-    int lo[NT][2], hi[NT][2];
-    float qs[NT][2], mx[NT][2], l[NT][2];
+    float mx[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int r = 8 * nt + 2 * t + e;
-            lo[nt][e] = 0, hi[nt][e] = 1 << 30;                      // a row that does not exist: nothing reads its sums
-            if (r < live) seen(a, p, (rg * RG + r) / per, lo[nt][e], hi[nt][e]);
             mx[nt][e] = -INFINITY;
             l[nt][e] = 0.f;
         }
-    // tokens all..all_end-1 are seen by every row of the group that exists
+    // the tokens lo..hi-1 that row 8 nt + 2 t + e sees; all, if it does not exist: nothing reads its sums
+    auto row_sees = [&](int nt, int e, int &lo, int &hi) {
+        const int r = 8 * nt + 2 * t + e;
+        lo = 0, hi = 1 << 30;
+        if (r < live) seen(a, p, (rg * RG + r) / per, lo, hi);
+    };
+    // tokens all_lo..all_hi-1 are seen by every row of the group that exists
     int all_lo, all_hi, dummy;
     seen(a, p, min(p.n - 1, (rg * RG + RG - 1) / per), all_lo, dummy);
     seen(a, p, rg * RG / per, dummy, all_hi);
     const uint4 *qf = reinterpret_cast<const uint4 *>(kv_smem) + lane;
     const bool keep_lse = a.score && rg == 0;
-    float *lse = keep_lse ? a.blk_lse + ((size_t)s * a.c.n_kv + h) * w.nb * 16 : nullptr;
     const int key0 = 8 * (g >> 1) + (g & 1);                         // key of row g of matrix 0; matrix j: + 2 j
-    auto load_qs = [&]() {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) qs[nt][e] = q_scale[8 * nt + 2 * t + e];
-    };
+    auto scale_of = [&](int nt) { return *reinterpret_cast<const float2 *>(&q_scale[8 * nt + 2 * t]); };
     // query rows into their fragments
     auto stage_q = [&]() {
         if (tid < 2) sm_poison[tid] = 0;
@@ -641,7 +639,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         for (int m = 0; m < 6; ++m) {
             kr[m][i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (tactive && tail_key(m) < trows)
-                kr[m][i] = *reinterpret_cast<const float4 *>(w.kt + (size_t)tail_key(m) * HD + 64 * tc + 16 * t + 4 * (tj0 + i));
+                kr[m][i] = *reinterpret_cast<const float4 *>(a.c.k_tail + (head * kTail + tail_key(m)) * HD + 64 * tc + 16 * t + 4 * (tj0 + i));
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -649,13 +647,13 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             for (int st = 0; st < 3; ++st) {
                 vr[i][k][st] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (tactive && 16 * st + 4 * t < trows)
-                    vr[i][k][st] = *reinterpret_cast<const float4 *>(w.vt + (size_t)(16 * (warp * kSteps + i) + g + 8 * k) * kTail + 16 * st + 4 * t);
+                    vr[i][k][st] = *reinterpret_cast<const float4 *>(a.c.v_tail + (head * HD + 16 * (warp * kSteps + i) + g + 8 * k) * kTail + 16 * st + 4 * t);
             }
     }
     int phys = load_phys(0);                                         // of the window of 32 blocks that is being asked for
     int phys_next = load_phys(32);                                   // and of the one behind it
     float ks = 0.f, vs = 0.f;                                        // lane l: scales of block l of the window that is read
-    if (lane < ncoded) ks = w.ks[phys], vs = w.vs[phys];
+    if (lane < ncoded) ks = a.c.k_scale[head_blocks + phys], vs = a.c.v_scale[head_blocks + phys];
     float ks_next = 0.f, vs_next = 0.f;
 
     // ---- codes on their way: unit 2 i is block i's keys, unit 2 i + 1 its values ----
@@ -669,8 +667,8 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                 phys = phys_next;
                 phys_next = load_phys(i + 32);
             }
-            const size_t off = (size_t)__shfl_sync(0xffffffffu, phys, i & 31) * kUnit;
-            const uint8_t *src = ((u & 1) ? w.v : w.k) + off + 16 * lane;
+            const size_t off = (head_blocks + __shfl_sync(0xffffffffu, phys, i & 31)) * kUnit;
+            const uint8_t *src = ((u & 1) ? a.c.v : a.c.k) + off + 16 * lane;
 #pragma unroll
             for (int k = 0; k < kUnit / 512; ++k) cp_async16(put + 512 * k, src + 512 * k);
             put = put == ring + (kRing - 1) * kUnit + 16 * lane ? ring + 16 * lane : put + kUnit;
@@ -690,7 +688,6 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         constexpr int kPart = kRing * kUnit / 4;                     // from one warp's partial logits [48][RG] to the next's
         float *first = reinterpret_cast<float *>(kv_smem + S::kQBytes + (kRing - S::kHold) * kUnit), *mine = first + warp * kPart;
         stage_q();
-        load_qs();
         if (tactive) {
             uint32_t poison[2] = {0, 0};
 #pragma unroll
@@ -786,6 +783,10 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float x[6][2];
+                int lo[2], hi[2];
+                row_sees(nt, 0, lo[0], hi[0]);
+                row_sees(nt, 1, lo[1], hi[1]);
+                const float2 qs = scale_of(nt);
 #pragma unroll
                 for (int m = 0; m < 6; ++m) {
                     const int key = tail_key(m), pos = kBlk * p.z + key;
@@ -793,7 +794,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                     const bool bad_key = sm_poison[key >> 5] >> (key & 31) & 1;
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        x[m][e] = pos < lo[nt][e] || pos >= hi[nt][e] ? -INFINITY : bad_key ? NAN : (e ? y.y : y.x) * qs[nt][e];
+                        x[m][e] = pos < lo[e] || pos >= hi[e] ? -INFINITY : bad_key ? NAN : (e ? y.y * qs.y : y.x * qs.x);
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -811,12 +812,12 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                     const int r = 8 * nt + 2 * t + e;
                     total[nt][e] = sum[0] + sum[1];
                     if (warp == 0 && g == 0) {
-                        *reinterpret_cast<float2 *>(a.part_ml + (u.tail_part * RG + r) * 2) = make_float2(top, sum[0] + sum[1]);
+                        *reinterpret_cast<float2 *>(a.part_ml + ((size_t)unit * RG + r) * 2) = make_float2(top, sum[0] + sum[1]);
                         sm_m[kW][r] = top;
                         sm_l[kW][r] = sum[0] + sum[1];
                         if (keep_lse && r < per)
                             for (int i = 0; i < 2; ++i)
-                                if (p.z + i < p.b0 + p.nb) lse[(size_t)(p.z + i) * 16 + r] = sum[i] == 0.f ? -INFINITY : ref + log2f(sum[i]);
+                                if (p.z + i < p.b0 + p.nb) a.blk_lse[(head_blocks + p.z + i) * 16 + r] = sum[i] == 0.f ? -INFINITY : ref + log2f(sum[i]);
                     }
                 }
 #pragma unroll
@@ -858,7 +859,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                     for (int k = 0; k < 4; ++k) {
                         const int r = 8 * nt + 2 * t + (k & 1), d0 = 16 * (warp * kSteps + i) + g + 8 * (k >> 1), rid = rg * RG + r;
                         if (!alone)
-                            a.part_o[(u.tail_part * RG + r) * HD + d0] = d[nt][k];
+                            a.part_o[((size_t)unit * RG + r) * HD + d0] = d[nt][k];
                         else if (r < live)
                             a.out[((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + d0] = d[nt][k] / total[nt][k & 1];
                     }
@@ -872,7 +873,6 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 
     if (!tail) {
         stage_q();
-        load_qs();
     }
 
     float o[HD / 16][NT][4];
@@ -908,7 +908,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         }
         if ((i & 31) == 16) {                                        // the next window's, half a window ahead
             ks_next = vs_next = 0.f;
-            if (i + 16 + lane < ncoded) ks_next = w.ks[phys_next], vs_next = w.vs[phys_next];
+            if (i + 16 + lane < ncoded) ks_next = a.c.k_scale[head_blocks + phys_next], vs_next = a.c.v_scale[head_blocks + phys_next];
         }
         const int b = bfirst + kW * i;
         const float bks = __shfl_sync(0xffffffffu, ks, i & 31);
@@ -969,7 +969,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float z = bks * qs[nt][e], less = blb + kTop - mx[nt][e];   // +inf before a row's first key
+                const float z = bks * (e ? scale_of(nt).y : scale_of(nt).x), less = blb + kTop - mx[nt][e];   // +inf before a row's first key
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -981,14 +981,19 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         const int pos0 = kBlk * b;
         if (pos0 < all_lo || pos0 + kBlk > all_hi) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int e = 0; e < 2; ++e) {
+                    int lo, hi;
+                    row_sees(nt, e, lo, hi);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int pos = pos0 + key0 + 4 * j + 2 * (k >> 1);
-                        if (pos < lo[nt][k & 1] || pos >= hi[nt][k & 1]) y[j][nt][k] = -INFINITY;
-                    }
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int k = e; k < 4; k += 2) {
+                            const int pos = pos0 + key0 + 4 * j + 2 * (k >> 1);
+                            if (pos < lo || pos >= hi) y[j][nt][k] = -INFINITY;
+                        }
+                }
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -1001,7 +1006,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float z = bks * qs[nt][e];
+                    const float z = bks * (e ? scale_of(nt).y : scale_of(nt).x);
                     float top = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
@@ -1027,8 +1032,11 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (lo[nt][e] < pos0 + kBlk && hi[nt][e] > pos0) l[nt][e] = NAN;
+                for (int e = 0; e < 2; ++e) {
+                    int lo, hi;
+                    row_sees(nt, e, lo, hi);
+                    if (lo < pos0 + kBlk && hi > pos0) l[nt][e] = NAN;
+                }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -1043,7 +1051,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                 if (keep_lse) {
                     const float total = group_sum(sum) * binv;
                     const int r = 8 * nt + 2 * t + e;
-                    if (g == 0 && r < per) lse[(size_t)b * 16 + r] = total == 0.f ? -INFINITY : mx[nt][e] - kTop + log2f(total);
+                    if (g == 0 && r < per) a.blk_lse[(head_blocks + b) * 16 + r] = total == 0.f ? -INFINITY : mx[nt][e] - kTop + log2f(total);
                 }
             }
         uint32_t ph[NT][2][2], pl[NT][2][2];                         // [step][input pair]
@@ -1103,9 +1111,10 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             }
         }
     __syncthreads();
+    const size_t part = part_of(a, unit, u.index);
     if (tid == 0) {
         if (sm_bad) atomicOr(a.c.err, kErrTable);
-        a.part_bad[u.code_part] = sm_bad;
+        a.part_bad[part] = sm_bad;
     }
     if (sm_bad) return;
     if (tid < RG) {   // each state's factor, in place of its maximum
@@ -1118,7 +1127,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             total = fmaf(sm_l[i][tid], f, total);
         }
         sm_l[0][tid] = total;
-        *reinterpret_cast<float2 *>(a.part_ml + (u.code_part * RG + tid) * 2) = make_float2(top, total);
+        *reinterpret_cast<float2 *>(a.part_ml + (part * RG + tid) * 2) = make_float2(top, total);
     }
     __syncthreads();
     for (int e = tid; e < min(live, RG) * (HD / 4); e += kW * 32) {
@@ -1127,7 +1136,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         auto add = [&](const float4 &y, float f) {
             sum.x = fmaf(y.x, f, sum.x), sum.y = fmaf(y.y, f, sum.y), sum.z = fmaf(y.z, f, sum.z), sum.w = fmaf(y.w, f, sum.w);
         };
-        if (u.whole) add(*reinterpret_cast<const float4 *>(a.part_o + (u.tail_part * RG + r) * HD + d), sm_m[kW][r]);
+        if (u.whole) add(*reinterpret_cast<const float4 *>(a.part_o + ((size_t)unit * RG + r) * HD + d), sm_m[kW][r]);
 #pragma unroll
         for (int i = 0; i < kW; ++i) add(*reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(kv_smem) + (i * RG + r) * kPitch + d), sm_m[i][r]);
         if (u.whole) {
@@ -1136,7 +1145,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             *reinterpret_cast<float4 *>(a.out + ((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + d) =
                 make_float4(sum.x / total, sum.y / total, sum.z / total, sum.w / total);
         } else {
-            *reinterpret_cast<float4 *>(a.part_o + (u.code_part * RG + r) * HD + d) = sum;
+            *reinterpret_cast<float4 *>(a.part_o + (part * RG + r) * HD + d) = sum;
         }
     }
 }
@@ -1164,8 +1173,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     u.x0 = codes ? int((long)p.coded * split / nsplit) : 0;
     u.x1 = codes ? int((long)p.coded * (split + 1) / nsplit) : 0;
     u.whole = nsplit == 1 && !a.apart;
-    u.tail_part = ((size_t)u.s * a.c.n_kv + u.h) * a.groups + u.rg;
-    u.code_part = part_of(a, u.tail_part, split);
+    u.index = split;
     attn_piece<HD, NT>(a, p, u, q, kv_smem, sh);
 }
 
@@ -1228,8 +1236,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         Piece u{s, ui / p.groups, ui % p.groups, min(from, p.coded), min(to, p.coded)};
         u.tail = from <= p.coded && to > p.coded;
         u.whole = from == 0 && u.tail && u.x1 > 0;
-        u.tail_part = ((size_t)s * a.c.n_kv + u.h) * a.groups + u.rg;
-        u.code_part = part_of(a, u.tail_part, cta);
+        u.index = cta;
         if (a.c.sealed[(size_t)s * a.c.n_kv + u.h] != p.z) {         // heads of a sequence that differ: left alone
             if (tid == 0) atomicOr(a.c.err, kErrState);
             continue;
