@@ -56,14 +56,19 @@ __device__ __forceinline__ int rows_of(const int32_t *cnt, int s, int rows) {
     return cnt ? min(max(cnt[s], 0), rows) : rows;
 }
 
-// The code of x at `scale` > 0, 128 + the integer nearest to x / scale, exactly: away from a border between
-// two codes the fp32 quotient (off by less than 2^-15 at |quotient| <= 128) decides; within 2^-10 of one,
-// and for scales whose reciprocal leaves the normal range, the quotient is taken in fp64, which tells the
-// quotient of two fp32 numbers from a border.
+// The code of x at `scale` > 0, 128 + the integer nearest to x / scale, exactly. The fp32 quotient is off by less than
+// 2^-15 (it is at most 128), so it decides except within 2^-10 of a border h between two codes; there the sign of x - h scale
+// does, which a fused multiply-add gives exactly: h scale is a multiple of scale 2^-24, and so is a difference that is not
+// zero, which for scales from 1e-30 is a normal number. Smaller scales take the quotient in fp64.
 __device__ __forceinline__ uint32_t code_of(float x, float scale, float inv) {
     const float y = x * inv;
     float c = rintf(y);
-    if (scale < 1e-30f || fabsf(fabsf(y - c) - 0.5f) < 0.0009765625f) c = float(rint((double)x / (double)scale));
+    if (scale < 1e-30f) {
+        c = float(rint((double)x / (double)scale));
+    } else if (fabsf(fabsf(y - c) - 0.5f) < 0.0009765625f) {
+        const float h = floorf(y) + 0.5f, d = fmaf(-h, scale, x);
+        c = d > 0.f ? h + 0.5f : d < 0.f ? h - 0.5f : rintf(h);
+    }
     return uint32_t(int(fminf(fmaxf(c, -127.f), 127.f)) + 128);
 }
 
@@ -120,19 +125,24 @@ struct Rows {
     }
 };
 template <bool V>
-__device__ __forceinline__ Rows<V> rows_from(const WriteArgs &a, int s, int h, const KvView &w, const Plan &p) {
-    const int hd = a.c.head_dim, phys = p.cut ? w.table[p.z] : 0;
+__device__ __forceinline__ Rows<V> rows_from(const WriteArgs &a, int s, int h, const KvView &w, const Plan &p, bool old) {
+    const int hd = a.c.head_dim, phys = old ? w.table[p.z] : 0;      // old: rows before the call's own are wanted after a cut
     return {(V ? a.v : a.k) + (size_t)s * a.rows * a.ld + (size_t)h * hd, a.ld, V ? w.vt : w.kt, (V ? w.v : w.k) + (size_t)phys * kBlk * hd,
-            p.cut ? (V ? w.vs : w.ks)[phys] : 0.f, p.have, p.cut, hd};
+            old ? (V ? w.vs : w.ks)[phys] : 0.f, p.have, p.cut, hd};
 }
 
 constexpr int kWriteThreads = 256;
+constexpr int kVPitch = 40;
 
 // Seals block b of the plan: 256 threads, a thread holds 4 tokens x 4 channels at a time. The codes go through shared
-// memory, so that they leave in 16-byte stores whatever their layout.
+// memory, so that they leave in 16-byte stores whatever their layout. Nothing is written if `bad` anywhere in the CTA.
 template <bool V>
-__device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView &w, int phys, float *red, uint8_t *code) {
+__device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView &w, int phys, int bad, float *red, uint8_t *code) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hd = x.hd, dq = hd / 4;
+    // piece e: tokens t.. and channels d.. of it, so that a warp's words of shared memory lie in different banks: values with
+    // the tokens innermost, a channel's 32 tokens 40 bytes apart
+    auto piece_t = [&](int e) { return V ? 4 * (e & 7) : 4 * (e / dq); };
+    auto piece_d = [&](int e) { return V ? 4 * (e >> 3) : 4 * (e % dq); };
     float4 y[2][4];
     float amax = 0.f;
     bool fin = true;
@@ -142,7 +152,7 @@ __device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView
         if (e < 8 * dq) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                y[i][k] = x.get(kBlk * b + 4 * (e / dq) + k, 4 * (e % dq));
+                y[i][k] = x.get(kBlk * b + piece_t(e) + k, piece_d(e));
                 const float4 v = y[i][k];
                 amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
                 fin = fin && isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w);
@@ -152,13 +162,14 @@ __device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (lane == 0) red[warp] = amax;
+    if (__syncthreads_or(bad)) return;
     const bool ok = __syncthreads_and(fin);
 #pragma unroll
     for (int i = 0; i < kWriteThreads / 32; ++i) amax = fmaxf(amax, red[i]);
     const float scale = ok ? __fdiv_rn(amax, 127.f) : NAN, inv = scale > 0.f ? 1.f / scale : 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int e = i * kWriteThreads + tid, t = 4 * (e / dq), d = 4 * (e % dq);
+        const int e = i * kWriteThreads + tid, t = piece_t(e), d = piece_d(e);
         if (e < 8 * dq) {
             uint32_t q[4][4];                                        // [token][channel]
 #pragma unroll
@@ -170,13 +181,17 @@ __device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t word = V ? q[0][k] | q[1][k] << 8 | q[2][k] << 16 | q[3][k] << 24 : q[k][0] | q[k][1] << 8 | q[k][2] << 16 | q[k][3] << 24;
-                *reinterpret_cast<uint32_t *>(code + (V ? v_at(t, d + k) : k_at(t + k, d))) = word;
+                *reinterpret_cast<uint32_t *>(code + (V ? (d + k) * kVPitch + t : k_at(t + k, d))) = word;
             }
         }
     }
     __syncthreads();
     uint4 *dst = reinterpret_cast<uint4 *>((V ? w.v : w.k) + (size_t)phys * kBlk * hd);
-    for (int e = tid; e < 2 * hd; e += kWriteThreads) dst[e] = reinterpret_cast<const uint4 *>(code)[e];
+    for (int e = tid; e < 2 * hd; e += kWriteThreads) {
+        const uint2 *from = reinterpret_cast<const uint2 *>(code + (V ? (e >> 1) * kVPitch + 16 * (e & 1) : 16 * e));
+        const uint2 lo = from[0], hi = from[1];
+        dst[e] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
     if (tid == 0) (V ? w.vs : w.ks)[phys] = scale;
 }
 
@@ -190,17 +205,20 @@ __device__ __forceinline__ bool bad_table(const KvView &w, const Plan &p) {
 // Seals an append's blocks, one CTA for the keys or the values of each: grid (2 x blocks, heads, sequences).
 __global__ void __launch_bounds__(kWriteThreads) k_kv8_seal(WriteArgs a) {
     __shared__ float red[kWriteThreads / 32];
-    __shared__ __align__(16) uint8_t code[kBlk * 256];
+    __shared__ __align__(16) uint8_t code[kVPitch * 256];
     const int b = blockIdx.x >> 1, h = blockIdx.y, s = blockIdx.z;
     const KvView w = view(a.c, s, h);
     const Plan p = plan_of(a, s, w);
     pdl_trigger();
-    if (p.bad || b >= p.full || bad_table(w, p)) return;            // the launch behind reports what is bad
+    if (p.bad || b >= p.full) return;                               // the launch behind reports what is bad
+    if (p.cut && b == 0 && bad_table(w, p)) return;                  // the entry is read through below
+    int bad = 0;
+    for (int i = threadIdx.x; i < p.full; i += kWriteThreads) bad |= unsigned(w.table[p.z + i]) >= unsigned(w.nb);
     const int phys = w.table[p.z + b];
     if (blockIdx.x & 1)
-        seal_block<true>(rows_from<true>(a, s, h, w, p), b, w, phys, red, code);
+        seal_block<true>(rows_from<true>(a, s, h, w, p, p.cut && b == 0), b, w, phys, bad, red, code);
     else
-        seal_block<false>(rows_from<false>(a, s, h, w, p), b, w, phys, red, code);
+        seal_block<false>(rows_from<false>(a, s, h, w, p, p.cut && b == 0), b, w, phys, bad, red, code);
 }
 
 // What is left of a call, one CTA per head: seals its blocks unless k_kv8_seal has (sealed_before), moves the rest to the
@@ -208,7 +226,7 @@ __global__ void __launch_bounds__(kWriteThreads) k_kv8_seal(WriteArgs a) {
 // further back than its place, behind all rows written here, or is where it belongs.
 __global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a, int sealed_before) {
     __shared__ float red[kWriteThreads / 32];
-    __shared__ __align__(16) uint8_t code[kBlk * 256];
+    __shared__ __align__(16) uint8_t code[kVPitch * 256];
     const int h = blockIdx.x, s = blockIdx.y, hd = a.c.head_dim, tid = threadIdx.x;
     const KvView w = view(a.c, s, h);
     Plan p = plan_of(a, s, w);
@@ -218,29 +236,50 @@ __global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a, int se
         if (tid == 0) atomicOr(a.c.err, p.bad);
         return;
     }
-    const Rows<false> xk = rows_from<false>(a, s, h, w, p);
-    const Rows<true> xv = rows_from<true>(a, s, h, w, p);
+    const Rows<false> xk = rows_from<false>(a, s, h, w, p, p.cut);
+    const Rows<true> xv = rows_from<true>(a, s, h, w, p, p.cut);
     if (!sealed_before)
         for (int b = 0; b < p.full; ++b) {
             const int phys = w.table[p.z + b];
-            seal_block<false>(xk, b, w, phys, red, code);
+            seal_block<false>(xk, b, w, phys, 0, red, code);
             __syncthreads();
-            seal_block<true>(xv, b, w, phys, red, code);
+            seal_block<true>(xv, b, w, phys, 0, red, code);
             __syncthreads();
         }
     const int left = p.have + p.n - kBlk * p.full, first = !p.cut && p.full == 0 ? p.have : 0;
     const int dq = hd / 4;
-    for (int e = tid; e < (left - first) * dq; e += kWriteThreads) {
-        const int t = first + e / dq, d = 4 * (e % dq);
-        *reinterpret_cast<float4 *>(w.kt + (size_t)t * hd + d) = xk.get(kBlk * p.full + t, d);
+    // values turn through shared memory, 64 channels at a time, so that a channel's tokens are stored together
+    constexpr int kSome = 3, kTurn = 64;                             // kSome: pieces of a thread at once, whose loads overlap
+    __shared__ float turn[kTurn][kTail + 1];
+    for (int e0 = tid; e0 < (left - first) * dq; e0 += 2 * kSome * kWriteThreads) {
+        float4 y[2 * kSome];
+#pragma unroll
+        for (int i = 0; i < 2 * kSome; ++i) {
+            const int e = e0 + i * kWriteThreads;
+            if (e < (left - first) * dq) y[i] = xk.get(kBlk * p.full + first + e / dq, 4 * (e % dq));
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * kSome; ++i) {
+            const int e = e0 + i * kWriteThreads;
+            if (e < (left - first) * dq) *reinterpret_cast<float4 *>(w.kt + (size_t)(first + e / dq) * hd + 4 * (e % dq)) = y[i];
+        }
     }
-    for (int e = tid; e < (left - first) * dq; e += kWriteThreads) {
-        const int t = first + e / dq, d = 4 * (e % dq);
-        const float4 y = xv.get(kBlk * p.full + t, d);
-        w.vt[(size_t)(d + 0) * kTail + t] = y.x;
-        w.vt[(size_t)(d + 1) * kTail + t] = y.y;
-        w.vt[(size_t)(d + 2) * kTail + t] = y.z;
-        w.vt[(size_t)(d + 3) * kTail + t] = y.w;
+    for (int c = 0; c < hd; c += kTurn) {
+        float4 y[kSome];                                             // at most 47 rows of 16 pieces
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) {
+            const int e = tid + i * kWriteThreads;
+            if (e < (left - first) * (kTurn / 4)) y[i] = xv.get(kBlk * p.full + first + e / (kTurn / 4), c + 4 * (e % (kTurn / 4)));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) {
+            const int e = tid + i * kWriteThreads, t = e / (kTurn / 4), d = 4 * (e % (kTurn / 4));
+            if (e < (left - first) * (kTurn / 4)) turn[d][t] = y[i].x, turn[d + 1][t] = y[i].y, turn[d + 2][t] = y[i].z, turn[d + 3][t] = y[i].w;
+        }
+        __syncthreads();
+        for (int d = tid >> 5; d < kTurn; d += kWriteThreads / 32)
+            for (int t = tid & 31; t < left - first; t += 32) w.vt[(size_t)(c + d) * kTail + first + t] = turn[d][t];
     }
     if (w.score) {
         const int L = a.len[s];

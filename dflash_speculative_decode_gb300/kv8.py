@@ -58,8 +58,11 @@ class Kv8Cache:
         self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail = k, v, k_scale, v_scale, k_tail, v_tail
         self.err = torch.zeros(64, dtype=i32, device=self.device)
         self.L = _abi.lib()
+        self._idx, self._f32, self._i32 = self.device.index, f32, i32
+        self._current_device, self._stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         self._take(table, sealed, score)
-        self._scratch, self._kept = None, []
+        self._scale = self.head_dim ** -0.5
+        self._scratch, self._kept, self._scratch_ptr, self._scratch_bytes = None, [], 0, 0
         self._need = {}
 
     def _take(self, table, sealed, score):
@@ -84,35 +87,37 @@ class Kv8Cache:
         self._call(self.L.dfl_kv8_init, "dfl_kv8_init")
         return self
 
-    # ---- marshalling ----
+    # ---- marshalling (a short call's time is mostly the host's: attributes that are cheap to read come first) ----
     def _call(self, f, what, *args):
-        cuda = self.torch.cuda
-        if cuda.current_device() != self.device.index:
-            with cuda.device(self.device):
-                rc = f(self._c, *args, cuda.current_stream(self.device).cuda_stream)
+        idx = self._idx
+        if self._current_device() != idx:
+            with self.torch.cuda.device(idx):
+                rc = f(self._c, *args, self._stream(idx))
         else:
-            rc = f(self._c, *args, cuda.current_stream(self.device).cuda_stream)
+            rc = f(self._c, *args, self._stream(idx))
         if rc != DFL_OK:
             raise DflError(rc, what)
 
     def _ints(self, t, name, optional=False):
         if t is None and optional:
             return None
-        if t is None or t.dtype != self.torch.int32 or t.shape != (self.n_seq,) or not t.is_contiguous() or t.device != self.device:
+        if t is None or t.dtype is not self._i32 or t.get_device() != self._idx or t.dim() != 1 or t.numel() != self.n_seq or not t.is_contiguous():
             _refuse(f"{name} must be int32 [{self.n_seq}] on {self.device}")
         return t.data_ptr()
 
     def _rows(self, t, name, heads):
         """A row tensor fp32 [n_seq][rows][heads][head_dim] whose rows lie a fixed distance apart: (pointer, rows, distance in floats)."""
-        shape, stride = t.shape, t.stride()
-        if (t.dtype != self.torch.float32 or t.device != self.device or len(shape) != 4 or shape[0] != self.n_seq or shape[3] != self.head_dim
-                or (heads and shape[2] != heads) or stride[3] != 1 or (shape[2] > 1 and stride[2] != self.head_dim)):
-            _refuse(f"{name} must be fp32 [{self.n_seq}][rows][{heads or 'heads'}][{self.head_dim}] on {self.device}, heads and channels contiguous")
-        M = shape[1]
-        ld = stride[1] if M > 1 else stride[0] if self.n_seq > 1 else shape[2] * self.head_dim
-        if self.n_seq > 1 and stride[0] != M * ld:
-            _refuse(f"{name}: the rows of all sequences must lie one fixed distance apart")
-        return t.data_ptr(), M, ld
+        if t.dtype is self._f32 and t.get_device() == self._idx and t.dim() == 4:
+            S, M, H, hd = t.shape
+            if S == self.n_seq and hd == self.head_dim and (H == heads or not heads):
+                if t.is_contiguous():
+                    return t.data_ptr(), M, H * hd
+                s0, s1, s2, s3 = t.stride()
+                ld = s1 if M > 1 else s0 if S > 1 else H * hd
+                if s3 == 1 and (H == 1 or s2 == hd) and (S == 1 or s0 == M * ld):
+                    return t.data_ptr(), M, ld
+        _refuse(f"{name} must be fp32 [{self.n_seq}][rows][{heads or 'heads'}][{self.head_dim}] on {self.device}, heads and channels contiguous "
+                "and the rows of all sequences one fixed distance apart")
 
     def _write(self, f, what, k, v, length, n):
         pk, M, ld = self._rows(k, "k", self.n_kv)
@@ -143,17 +148,17 @@ class Kv8Cache:
             need = self._need[key] = int(self.L.dfl_kv8_attn_scratch_bytes(self._c, n_q, M, window, score))
             if need < 0:
                 _refuse(f"{n_q} query heads and {M} rows: n_q must be a multiple of n_kv = {self.n_kv}, up to 16 a head, with 1..16 rows and a window >= 0")
-            if self._scratch is None or self._scratch.numel() < need:
-                if self._scratch is not None:
-                    self._kept.append(self._scratch)   # a captured graph may hold its address
+            if self._scratch_bytes < need:
+                self._kept.append(self._scratch)       # a captured graph may hold its address
                 self._scratch = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
+                self._scratch_ptr, self._scratch_bytes = self._scratch.data_ptr(), need
         if out is None:
             out = (self.torch.empty if n is None else self.torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
         po, Mo, ldo = self._rows(out, "out", n_q)
         if Mo != M:
             _refuse("out must have q's rows")
-        self._call(self.L.dfl_kv8_attn, "dfl_kv8_attn", pq, ldq, n_q, M, pl, pn, window, causal, self.head_dim ** -0.5 if scale is None else scale,
-                   score, po, ldo, self._scratch.data_ptr(), self._scratch.numel())
+        self._call(self.L.dfl_kv8_attn, "dfl_kv8_attn", pq, ldq, n_q, M, pl, pn, window, causal, self._scale if scale is None else scale,
+                   score, po, ldo, self._scratch_ptr, self._scratch_bytes)
         return out
 
     def evict(self, length, keep: int, sink: int = 0, recent: int = 0, out=None):
@@ -179,7 +184,7 @@ class Kv8Cache:
     def _check_out(self, new):
         for name, like in (("table", self.table), ("score", self.score), ("sealed", self.sealed)):
             t = new[name]
-            if t.dtype != like.dtype or t.shape != like.shape or not t.is_contiguous() or t.device != self.device:
+            if t.dtype is not like.dtype or t.shape != like.shape or not t.is_contiguous() or t.get_device() != self._idx:
                 _refuse(f"{name} must be contiguous {like.dtype} {list(like.shape)} on {self.device}")
 
     def take(self, new):
@@ -194,7 +199,7 @@ class Kv8Cache:
         if out is None:
             out = [self.torch.zeros(shape, dtype=self.torch.float32, device=self.device) for _ in range(2)]
         for t in out:
-            if t.dtype != self.torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
+            if t.dtype is not self._f32 or t.shape != shape or not t.is_contiguous() or t.get_device() != self._idx:
                 _refuse(f"out must be two contiguous fp32 tensors {list(shape)} on {self.device}")
         self._call(self.L.dfl_kv8_read, "dfl_kv8_read", self._ints(length, "length"), self._ints(first, "first", True), rows,
                    out[0].data_ptr(), out[1].data_ptr())
