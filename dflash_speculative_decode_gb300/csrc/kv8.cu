@@ -56,20 +56,21 @@ __device__ __forceinline__ int rows_of(const int32_t *cnt, int s, int rows) {
     return cnt ? min(max(cnt[s], 0), rows) : rows;
 }
 
-// The code of x at `scale` > 0, 128 + the integer nearest to x / scale, exactly. The fp32 quotient is off by less than
-// 2^-15 (it is at most 128), so it decides except within 2^-10 of a border h between two codes; there the sign of x - h scale
-// does, which a fused multiply-add gives exactly: h scale is a multiple of scale 2^-24, and so is a difference that is not
-// zero, which for scales from 1e-30 is a normal number. Smaller scales take the quotient in fp64.
+// The code of x at `scale` >= kTiny, 128 + the integer nearest to x / scale, exactly: in the low byte of the result. The
+// fp32 quotient is off by less than 2^-15 (it is at most 127 and a rounding), and adding 1.5 * 2^23 + 128 rounds it to an
+// integer c that is off by at most one. The remainder r = x - c scale is exact in fp32 (it is a multiple of the smaller unit
+// in the last place of x and scale, and no larger than about scale / 2), so |r| against scale / 2 tells.
+constexpr float kTiny = 1e-30f;
+constexpr float kRound = 12582912.f + 128.f;
 __device__ __forceinline__ uint32_t code_of(float x, float scale, float inv) {
-    const float y = x * inv;
-    float c = rintf(y);
-    if (scale < 1e-30f) {
-        c = float(rint((double)x / (double)scale));
-    } else if (fabsf(fabsf(y - c) - 0.5f) < 0.0009765625f) {
-        const float h = floorf(y) + 0.5f, d = fmaf(-h, scale, x);
-        c = d > 0.f ? h + 0.5f : d < 0.f ? h - 0.5f : rintf(h);
-    }
-    return uint32_t(int(fminf(fmaxf(c, -127.f), 127.f)) + 128);
+    const float t = fmaf(x, inv, kRound), c = t - kRound, r = fmaf(-c, scale, x);
+    uint32_t code = __float_as_uint(t);
+    if (2.f * fabsf(r) >= scale && (2.f * fabsf(r) > scale || (code & 1))) code += r > 0.f ? 1 : -1;   // a tie goes to the even one
+    return code;
+}
+// for scales whose reciprocal or remainders would leave fp32's normal range: the quotient in fp64
+__device__ __noinline__ uint32_t code_of_tiny(float x, float scale) {
+    return uint32_t(int(fmin(fmax(rint((double)x / (double)scale), -127.0), 127.0)) + 128);
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -134,18 +135,22 @@ __device__ __forceinline__ Rows<V> rows_from(const WriteArgs &a, int s, int h, c
 constexpr int kWriteThreads = 256;
 constexpr int kVPitch = 40;
 
+// the low bytes of four words as one
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
 // Seals block b of the plan: 256 threads, a thread holds 4 tokens x 4 channels at a time. The codes go through shared
 // memory, so that they leave in 16-byte stores whatever their layout. Nothing is written if `bad` anywhere in the CTA.
 template <bool V>
-__device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView &w, int phys, int bad, float *red, uint8_t *code) {
+__device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView &w, int phys, int bad, uint32_t *red, uint8_t *code) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hd = x.hd, dq = hd / 4;
     // piece e: tokens t.. and channels d.. of it, so that a warp's words of shared memory lie in different banks: values with
     // the tokens innermost, a channel's 32 tokens 40 bytes apart
     auto piece_t = [&](int e) { return V ? 4 * (e & 7) : 4 * (e / dq); };
     auto piece_d = [&](int e) { return V ? 4 * (e >> 3) : 4 * (e % dq); };
     float4 y[2][4];
-    float amax = 0.f;
-    bool fin = true;
+    uint32_t top = 0;                                                // magnitudes as bits: infinities and NaN come last
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int e = i * kWriteThreads + tid;                       // of 8 * hd / 4 pieces
@@ -153,20 +158,20 @@ __device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 y[i][k] = x.get(kBlk * b + piece_t(e) + k, piece_d(e));
-                const float4 v = y[i][k];
-                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-                fin = fin && isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w);
+                const float v[4] = {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) top = max(top, __float_as_uint(v[c]) & 0x7fffffffu);
             }
         }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (lane == 0) red[warp] = amax;
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) red[warp] = top;
     if (__syncthreads_or(bad)) return;
-    const bool ok = __syncthreads_and(fin);
 #pragma unroll
-    for (int i = 0; i < kWriteThreads / 32; ++i) amax = fmaxf(amax, red[i]);
-    const float scale = ok ? __fdiv_rn(amax, 127.f) : NAN, inv = scale > 0.f ? 1.f / scale : 0.f;
+    for (int i = 0; i < kWriteThreads / 32; ++i) top = max(top, red[i]);
+    const float scale = top < 0x7f800000u ? __fdiv_rn(__uint_as_float(top), 127.f) : NAN;
+    const bool tiny = scale < kTiny, none = !(scale > 0.f);
+    const float inv = none || tiny ? 0.f : 1.f / scale;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int e = i * kWriteThreads + tid, t = piece_t(e), d = piece_d(e);
@@ -176,11 +181,11 @@ __device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView
             for (int k = 0; k < 4; ++k) {
                 const float v[4] = {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) q[k][c] = scale > 0.f ? code_of(v[c], scale, inv) : 128u;
+                for (int c = 0; c < 4; ++c) q[k][c] = none ? 128u : tiny ? code_of_tiny(v[c], scale) : code_of(v[c], scale, inv);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t word = V ? q[0][k] | q[1][k] << 8 | q[2][k] << 16 | q[3][k] << 24 : q[k][0] | q[k][1] << 8 | q[k][2] << 16 | q[k][3] << 24;
+                const uint32_t word = V ? low_bytes(q[0][k], q[1][k], q[2][k], q[3][k]) : low_bytes(q[k][0], q[k][1], q[k][2], q[k][3]);
                 *reinterpret_cast<uint32_t *>(code + (V ? (d + k) * kVPitch + t : k_at(t + k, d))) = word;
             }
         }
@@ -204,7 +209,7 @@ __device__ __forceinline__ bool bad_table(const KvView &w, const Plan &p) {
 
 // Seals an append's blocks, one CTA for the keys or the values of each: grid (2 x blocks, heads, sequences).
 __global__ void __launch_bounds__(kWriteThreads) k_kv8_seal(WriteArgs a) {
-    __shared__ float red[kWriteThreads / 32];
+    __shared__ uint32_t red[kWriteThreads / 32];
     __shared__ __align__(16) uint8_t code[kVPitch * 256];
     const int b = blockIdx.x >> 1, h = blockIdx.y, s = blockIdx.z;
     const KvView w = view(a.c, s, h);
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(kWriteThreads) k_kv8_seal(WriteArgs a) {
 // tail's front, starts the scores of new blocks and counts. A row that comes from the tail lies 32 * full >= 32 rows
 // further back than its place, behind all rows written here, or is where it belongs.
 __global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a, int sealed_before) {
-    __shared__ float red[kWriteThreads / 32];
+    __shared__ uint32_t red[kWriteThreads / 32];
     __shared__ __align__(16) uint8_t code[kVPitch * 256];
     const int h = blockIdx.x, s = blockIdx.y, hd = a.c.head_dim, tid = threadIdx.x;
     const KvView w = view(a.c, s, h);
@@ -264,22 +269,26 @@ __global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a, int se
             if (e < (left - first) * dq) *reinterpret_cast<float4 *>(w.kt + (size_t)(first + e / dq) * hd + 4 * (e % dq)) = y[i];
         }
     }
-    for (int c = 0; c < hd; c += kTurn) {
-        float4 y[kSome];                                             // at most 47 rows of 16 pieces
+    float4 y[256 / kTurn][kSome];                                    // at most 47 rows of 16 pieces a turn
+#pragma unroll
+    for (int c = 0; c < 256 / kTurn; ++c)
 #pragma unroll
         for (int i = 0; i < kSome; ++i) {
             const int e = tid + i * kWriteThreads;
-            if (e < (left - first) * (kTurn / 4)) y[i] = xv.get(kBlk * p.full + first + e / (kTurn / 4), c + 4 * (e % (kTurn / 4)));
+            if (c * kTurn < hd && e < (left - first) * (kTurn / 4)) y[c][i] = xv.get(kBlk * p.full + first + e / (kTurn / 4), c * kTurn + 4 * (e % (kTurn / 4)));
         }
+#pragma unroll
+    for (int c = 0; c < 256 / kTurn; ++c) {
+        if (c * kTurn >= hd) break;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kSome; ++i) {
             const int e = tid + i * kWriteThreads, t = e / (kTurn / 4), d = 4 * (e % (kTurn / 4));
-            if (e < (left - first) * (kTurn / 4)) turn[d][t] = y[i].x, turn[d + 1][t] = y[i].y, turn[d + 2][t] = y[i].z, turn[d + 3][t] = y[i].w;
+            if (e < (left - first) * (kTurn / 4)) turn[d][t] = y[c][i].x, turn[d + 1][t] = y[c][i].y, turn[d + 2][t] = y[c][i].z, turn[d + 3][t] = y[c][i].w;
         }
         __syncthreads();
         for (int d = tid >> 5; d < kTurn; d += kWriteThreads / 32)
-            for (int t = tid & 31; t < left - first; t += 32) w.vt[(size_t)(c + d) * kTail + first + t] = turn[d][t];
+            for (int t = tid & 31; t < left - first; t += 32) w.vt[(size_t)(c * kTurn + d) * kTail + first + t] = turn[d][t];
     }
     if (w.score) {
         const int L = a.len[s];
