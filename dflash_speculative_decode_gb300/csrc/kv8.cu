@@ -143,7 +143,7 @@ __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c
 // Seals block b of the plan: 256 threads, a thread holds 4 tokens x 4 channels at a time. The codes go through shared
 // memory, so that they leave in 16-byte stores whatever their layout. Nothing is written if `bad` anywhere in the CTA.
 template <bool V>
-__device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView &w, int phys, int bad, uint32_t *red, uint8_t *code) {
+__device__ __forceinline__ bool seal_block(const Rows<V> &x, int b, const KvView &w, int phys, int bad, uint32_t *red, uint8_t *code) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hd = x.hd, dq = hd / 4;
     // piece e: tokens t.. and channels d.. of it, so that a warp's words of shared memory lie in different banks: values with
     // the tokens innermost, a channel's 32 tokens 40 bytes apart
@@ -166,7 +166,7 @@ __device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) red[warp] = top;
-    if (__syncthreads_or(bad)) return;
+    if (__syncthreads_or(bad)) return false;
 #pragma unroll
     for (int i = 0; i < kWriteThreads / 32; ++i) top = max(top, red[i]);
     const float scale = top < 0x7f800000u ? __fdiv_rn(__uint_as_float(top), 127.f) : NAN;
@@ -198,6 +198,7 @@ __device__ __forceinline__ void seal_block(const Rows<V> &x, int b, const KvView
         dst[e] = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
     if (tid == 0) (V ? w.vs : w.ks)[phys] = scale;
+    return true;
 }
 
 // A head whose plan follows a table entry out of range is left alone.
@@ -207,95 +208,118 @@ __device__ __forceinline__ bool bad_table(const KvView &w, const Plan &p) {
     return __syncthreads_or(bad);
 }
 
-// Seals an append's blocks, one CTA for the keys or the values of each: grid (2 x blocks, heads, sequences).
-__global__ void __launch_bounds__(kWriteThreads) k_kv8_seal(WriteArgs a) {
-    __shared__ uint32_t red[kWriteThreads / 32];
-    __shared__ __align__(16) uint8_t code[kVPitch * 256];
-    const int b = blockIdx.x >> 1, h = blockIdx.y, s = blockIdx.z;
-    const KvView w = view(a.c, s, h);
-    const Plan p = plan_of(a, s, w);
-    pdl_trigger();
-    if (p.bad || b >= p.full) return;                               // the launch behind reports what is bad
-    if (p.cut && b == 0 && bad_table(w, p)) return;                  // the entry is read through below
-    int bad = 0;
-    for (int i = threadIdx.x; i < p.full; i += kWriteThreads) bad |= unsigned(w.table[p.z + i]) >= unsigned(w.nb);
-    const int phys = w.table[p.z + b];
-    if (blockIdx.x & 1)
-        seal_block<true>(rows_from<true>(a, s, h, w, p, p.cut && b == 0), b, w, phys, bad, red, code);
-    else
-        seal_block<false>(rows_from<false>(a, s, h, w, p, p.cut && b == 0), b, w, phys, bad, red, code);
-}
-
-// What is left of a call, one CTA per head: seals its blocks unless k_kv8_seal has (sealed_before), moves the rest to the
-// tail's front, starts the scores of new blocks and counts. A row that comes from the tail lies 32 * full >= 32 rows
-// further back than its place, behind all rows written here, or is where it belongs.
-__global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a, int sealed_before) {
-    __shared__ uint32_t red[kWriteThreads / 32];
-    __shared__ __align__(16) uint8_t code[kVPitch * 256];
-    const int h = blockIdx.x, s = blockIdx.y, hd = a.c.head_dim, tid = threadIdx.x;
-    const KvView w = view(a.c, s, h);
-    Plan p = plan_of(a, s, w);
-    if (!p.bad && bad_table(w, p)) p.bad = kErrTable;
-    if (sealed_before) pdl_wait();   // k_kv8_seal has read the tail
-    if (p.bad) {
-        if (tid == 0) atomicOr(a.c.err, p.bad);
-        return;
-    }
-    const Rows<false> xk = rows_from<false>(a, s, h, w, p, p.cut);
-    const Rows<true> xv = rows_from<true>(a, s, h, w, p, p.cut);
-    if (!sealed_before)
-        for (int b = 0; b < p.full; ++b) {
-            const int phys = w.table[p.z + b];
-            seal_block<false>(xk, b, w, phys, 0, red, code);
-            __syncthreads();
-            seal_block<true>(xv, b, w, phys, 0, red, code);
-            __syncthreads();
-        }
-    const int left = p.have + p.n - kBlk * p.full, first = !p.cut && p.full == 0 ? p.have : 0;
-    const int dq = hd / 4;
-    // values turn through shared memory, 64 channels at a time, so that a channel's tokens are stored together
-    constexpr int kSome = 3, kTurn = 64;                             // kSome: pieces of a thread at once, whose loads overlap
-    __shared__ float turn[kTurn][kTail + 1];
-    for (int e0 = tid; e0 < (left - first) * dq; e0 += 2 * kSome * kWriteThreads) {
-        float4 y[2 * kSome];
-#pragma unroll
-        for (int i = 0; i < 2 * kSome; ++i) {
-            const int e = e0 + i * kWriteThreads;
-            if (e < (left - first) * dq) y[i] = xk.get(kBlk * p.full + first + e / dq, 4 * (e % dq));
-        }
-#pragma unroll
-        for (int i = 0; i < 2 * kSome; ++i) {
-            const int e = e0 + i * kWriteThreads;
-            if (e < (left - first) * dq) *reinterpret_cast<float4 *>(w.kt + (size_t)(first + e / dq) * hd + 4 * (e % dq)) = y[i];
-        }
-    }
-    float4 y[256 / kTurn][kSome];                                    // at most 47 rows of 16 pieces a turn
+// What is left of a call behind its full blocks moves to the tail's front, one CTA for a head's keys or values. A row that
+// comes from the tail lies 32 * full >= 32 rows further back than its place, behind all rows written here, or is where it
+// belongs. Every load is under way before the first store.
+constexpr int kTurn = 64;
+using Turn = float[kTurn][kTail + 1];   // values turn through shared memory, so that a channel's tokens are stored together
+template <bool V>
+__device__ __forceinline__ void keep_rest(const Rows<V> &x, const KvView &w, const Plan &p, Turn &turn) {
+    const int tid = threadIdx.x, hd = x.hd, left = p.have + p.n - kBlk * p.full, first = !p.cut && p.full == 0 ? p.have : 0;
+    constexpr int kSome = 3;                                         // at most 47 rows of 16 pieces a turn
+    float4 y[256 / kTurn][kSome];
 #pragma unroll
     for (int c = 0; c < 256 / kTurn; ++c)
 #pragma unroll
         for (int i = 0; i < kSome; ++i) {
             const int e = tid + i * kWriteThreads;
-            if (c * kTurn < hd && e < (left - first) * (kTurn / 4)) y[c][i] = xv.get(kBlk * p.full + first + e / (kTurn / 4), c * kTurn + 4 * (e % (kTurn / 4)));
+            if (c * kTurn < hd && e < (left - first) * (kTurn / 4)) y[c][i] = x.get(kBlk * p.full + first + e / (kTurn / 4), c * kTurn + 4 * (e % (kTurn / 4)));
         }
+    __syncthreads();
 #pragma unroll
     for (int c = 0; c < 256 / kTurn; ++c) {
         if (c * kTurn >= hd) break;
-        __syncthreads();
+        if (V) __syncthreads();
 #pragma unroll
         for (int i = 0; i < kSome; ++i) {
             const int e = tid + i * kWriteThreads, t = e / (kTurn / 4), d = 4 * (e % (kTurn / 4));
-            if (e < (left - first) * (kTurn / 4)) turn[d][t] = y[c][i].x, turn[d + 1][t] = y[c][i].y, turn[d + 2][t] = y[c][i].z, turn[d + 3][t] = y[c][i].w;
+            if (e >= (left - first) * (kTurn / 4)) continue;
+            if (V)
+                turn[d][t] = y[c][i].x, turn[d + 1][t] = y[c][i].y, turn[d + 2][t] = y[c][i].z, turn[d + 3][t] = y[c][i].w;
+            else
+                *reinterpret_cast<float4 *>(w.kt + (size_t)(first + t) * hd + c * kTurn + d) = y[c][i];
         }
+        if (!V) continue;
         __syncthreads();
         for (int d = tid >> 5; d < kTurn; d += kWriteThreads / 32)
             for (int t = tid & 31; t < left - first; t += 32) w.vt[(size_t)(c * kTurn + d) * kTail + first + t] = turn[d][t];
     }
+}
+
+// Scores of the blocks that begin among the new rows, and the count of sealed ones. All threads of the CTA call it.
+__device__ __forceinline__ void settle(const WriteArgs &a, int s, const KvView &w, const Plan &p) {
     if (w.score) {
         const int L = a.len[s];
-        for (int b = (L + kBlk - 1) / kBlk + tid; b * kBlk < L + p.n; b += kWriteThreads) w.score[b] = 0.f;
+        for (int b = (L + kBlk - 1) / kBlk + threadIdx.x; b * kBlk < L + p.n; b += blockDim.x) w.score[b] = 0.f;
     }
     __syncthreads();   // every thread has read the count
-    if (tid == 0) *w.sealed = p.z + p.full;
+    if (threadIdx.x == 0) *w.sealed = p.z + p.full;
+}
+
+// One launch for a call of few rows, one CTA per head.
+__global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a) {
+    __shared__ uint32_t red[kWriteThreads / 32];
+    __shared__ __align__(16) uint8_t code[kVPitch * 256];
+    __shared__ Turn turn;
+    const int h = blockIdx.x, s = blockIdx.y;
+    const KvView w = view(a.c, s, h);
+    Plan p = plan_of(a, s, w);
+    if (!p.bad && bad_table(w, p)) p.bad = kErrTable;
+    if (p.bad) {
+        if (threadIdx.x == 0) atomicOr(a.c.err, p.bad);
+        return;
+    }
+    const Rows<false> xk = rows_from<false>(a, s, h, w, p, p.cut);
+    const Rows<true> xv = rows_from<true>(a, s, h, w, p, p.cut);
+    for (int b = 0; b < p.full; ++b) {
+        const int phys = w.table[p.z + b];
+        seal_block<false>(xk, b, w, phys, 0, red, code);
+        __syncthreads();
+        seal_block<true>(xv, b, w, phys, 0, red, code);
+        __syncthreads();
+    }
+    keep_rest<false>(xk, w, p, turn);
+    keep_rest<true>(xv, w, p, turn);
+    settle(a, s, w, p);
+}
+
+// Many rows: a CTA for the keys or the values of each block, grid (2 x blocks, heads, sequences). The first one, which alone
+// reads rows held before, also keeps the rest. k_kv8_count behind it settles the call and reports what is bad.
+template <bool V>
+__device__ __forceinline__ void append_block(const WriteArgs &a, int s, int h, const KvView &w, const Plan &p, int b, uint32_t *red, uint8_t *code, Turn &turn) {
+    const Rows<V> x = rows_from<V>(a, s, h, w, p, p.cut && b == 0);
+    if (b < p.full) {
+        int bad = 0;
+        for (int i = threadIdx.x; i < p.full; i += kWriteThreads) bad |= unsigned(w.table[p.z + i]) >= unsigned(w.nb);
+        if (!seal_block<V>(x, b, w, w.table[p.z + b], bad, red, code)) return;
+        __syncthreads();
+    }
+    if (b == 0) keep_rest<V>(x, w, p, turn);
+}
+__global__ void __launch_bounds__(kWriteThreads, 4) k_kv8_append(WriteArgs a) {
+    __shared__ uint32_t red[kWriteThreads / 32];
+    __shared__ __align__(16) uint8_t code[kVPitch * 256];
+    __shared__ Turn turn;
+    const int b = blockIdx.x >> 1, h = blockIdx.y, s = blockIdx.z;
+    const KvView w = view(a.c, s, h);
+    const Plan p = plan_of(a, s, w);
+    pdl_trigger();
+    if (p.bad || (b > 0 && b >= p.full) || (p.cut && b == 0 && bad_table(w, p))) return;   // a cut reads through the entry
+    if (blockIdx.x & 1)
+        append_block<true>(a, s, h, w, p, b, red, code, turn);
+    else
+        append_block<false>(a, s, h, w, p, b, red, code, turn);
+}
+__global__ void __launch_bounds__(64) k_kv8_count(WriteArgs a) {
+    const int s = blockIdx.y;
+    const KvView w = view(a.c, s, blockIdx.x);
+    Plan p = plan_of(a, s, w);
+    if (!p.bad && bad_table(w, p)) p.bad = kErrTable;
+    pdl_wait();
+    if (!p.bad)
+        settle(a, s, w, p);
+    else if (threadIdx.x == 0)
+        atomicOr(a.c.err, p.bad);
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -1672,17 +1696,16 @@ int write_rows(const dfl_kv8 *c, const int32_t *len, const int32_t *cnt, int row
     if (!commit && rows > DFL_MAX_ROWS) return DFL_E_UNSUPPORTED;
     if (rows > kBlk * c->n_blocks) return DFL_E_CAPACITY;
     WriteArgs a{*c, len, cnt, k, v, ld, rows, commit};
-    // Up to 64 rows complete three blocks at most: one launch. More rows are sealed by a launch of their own, a CTA for each
-    // block, and the second one settles the tail. At 1024 rows of 8 heads of 128
-    // the two take 9 us, one CTA a head alone 260 us.
+    // Up to 64 rows complete three blocks at most: one launch. More rows take a launch with a CTA for each block and a short
+    // one behind it: at 1024 rows of 8 heads of 128 they take 8 us, one CTA a head alone 260 us.
     if (!commit || rows <= 64) {
-        k_kv8_write<<<dim3(c->n_kv, c->n_seq), kWriteThreads, 0, s>>>(a, 0);
+        k_kv8_write<<<dim3(c->n_kv, c->n_seq), kWriteThreads, 0, s>>>(a);
         return launched();
     }
-    k_kv8_seal<<<dim3(2 * ((kTail + rows) / kBlk), c->n_kv, c->n_seq), kWriteThreads, 0, s>>>(a);
+    k_kv8_append<<<dim3(2 * ((kTail + rows) / kBlk), c->n_kv, c->n_seq), kWriteThreads, 0, s>>>(a);
     const int l = launched();
     if (l) return l;
-    return launch_pdl(k_kv8_write, dim3(c->n_kv, c->n_seq), dim3(kWriteThreads), 0, s, a, 1) == cudaSuccess ? DFL_OK : DFL_E_CUDA;
+    return launch_pdl(k_kv8_count, dim3(c->n_kv, c->n_seq), dim3(64), 0, s, a) == cudaSuccess ? DFL_OK : DFL_E_CUDA;
 }
 
 }  // namespace
