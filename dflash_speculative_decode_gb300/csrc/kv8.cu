@@ -413,15 +413,14 @@ struct AttnKvArgs {
     float *part_o;        // [part][rows of a group][head_dim]
     float *part_ml;       // [part][rows of a group][2]: running maximum (base 2) and sum
     int *part_bad;        // [part]: a table entry was out of range
-    float *blk_lse;       // [sequence][head][n_blocks][16]: log2 of the block's share of row 0's sums
+    float *blk_lse;       // [sequence][head][n_blocks][2][16]: log2 of the shares of a block's halves in row 0's sums
 };
 
-// A unit is one row group of a head: unit (s * n_kv + h) * groups + rg. The sums of its tail and of each CTA that has some
-// of its coded blocks are parts, merged by k_kv8_merge. Part ids: with splits, the tail's of every unit, then the
-// splits'; with shares, CTA + unit, which no two (CTA, unit) have in common, as both only grow along the work.
-__device__ __forceinline__ size_t units_of(const AttnKvArgs &a) { return (size_t)a.c.n_seq * a.c.n_kv * a.groups; }
-__device__ __forceinline__ size_t part_of(const AttnKvArgs &a, size_t unit, int i) {   // i: split or CTA
-    return units_of(a) + (a.share ? unit + i : unit * a.splits + i);
+// A unit is one row group of a head: unit (s * n_kv + h) * groups + rg. The sums of each CTA that has some of it are a part,
+// merged by k_kv8_merge. Part ids: with splits, unit by unit (the tail's own CTA first); with shares, CTA + unit, which no
+// two (CTA, unit) have in common, as both only grow along the work.
+__device__ __forceinline__ size_t part_of(const AttnKvArgs &a, size_t unit, int i) {   // i: CTA of the unit, or CTA
+    return a.share ? unit + i : unit * (a.splits + a.apart) + i;
 }
 
 struct Span {
@@ -474,19 +473,30 @@ constexpr float kTop = 7.f;    // log2 of the weight at a row's maximum
 
 template <int HD, int NT>
 struct AttnShape {
-    static constexpr int kUnit = kBlk * HD;                          // bytes of a block's keys (or values)
-    // Warps of a CTA and CTAs of an SM, by the registers that the sums take (HD * NT / 4 a thread): 255 a thread at
-    // head_dim 256, 168 at 128 with 16 rows, 128 otherwise. Ring slots per warp: as many as fit, so that an SM has about
-    // 128 KB requested.
-    static constexpr int kWarps = HD == 128 && NT == 2 ? 6 : 8;
-    static constexpr int kCtas = HD == 256 ? 1 : 2;
-    static constexpr int kRing = HD == 64 ? 6 : HD == 128 && NT == 2 ? 4 : 3;
-    static constexpr int kTailCh = HD == 64 || (HD == 128 && NT == 1) ? 16 : 32;   // channels of the tail that a warp takes
-    static constexpr int kHold = HD == 64 ? 2 : 1;                   // slots that lend the tail [48][8 NT] floats a warp
-    static_assert(kTail * 8 * NT * 4 <= kHold * kUnit && HD / kTailCh <= kWarps, "the tail's logits and channels fit");
+    static constexpr int kUnit = 16 * HD;                            // bytes of a warp's keys, or values, of a pair of blocks
+    // Groups of four warps: 16 warps an SM of 128 registers a thread, in two CTAs where two rings fit beside the queries. Ring
+    // slots per warp: as many as fit, so that an SM has about 128 KB and more requested.
+    static constexpr int kCtas = HD == 256 && NT == 2 ? 1 : HD == 64 ? 3 : 2;
+    static constexpr int kGroups = HD == 256 && NT == 2 ? 4 : 2;
+    static constexpr int kWarps = 4 * kGroups;
+    static constexpr int kRing = HD == 256 ? 3 : HD == 128 ? 5 : 6;
     static constexpr int kQBytes = NT * 8 * HD * 4;                  // query halves
-    static constexpr int kSmem = kQBytes + kWarps * kRing * kUnit;
+    static constexpr int kPBytes = kGroups * 4 * NT * 512;           // a pair's weights, for each group
+    static constexpr int kSmem = kQBytes + kPBytes + kWarps * kRing * kUnit;
+    static_assert(kGroups * 8 * NT * (HD + 4) * 4 <= kSmem && 3 * NT * 1024 <= 4 * kRing * kUnit, "the merge's and the tail's use of the shared memory");
 };
+
+// the four warps of a group: a barrier, and one that also tells whether x holds anywhere in the group
+__device__ __forceinline__ void group_sync(int grp) { asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(grp + 1) : "memory"); }
+__device__ __forceinline__ bool group_or(int grp, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.aligned.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(uint32_t(x)), "r"(grp + 1)
+        : "memory");
+    return r;
+}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -554,7 +564,7 @@ __device__ __forceinline__ float group_sum(float x) {
 template <int N>
 __device__ __forceinline__ void cp_async_wait_groups() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// the splits that coded blocks are worth: at least one block a warp
+// the splits that coded blocks are worth: at least two pairs a group
 template <int W>
 __device__ __forceinline__ int splits_of(int splits, int coded) { return min(splits, (coded + W - 1) / W); }
 
@@ -580,13 +590,12 @@ __device__ __forceinline__ void block_sums(long &x, long &y, long (*sm)[2]) {
 struct Piece {
     int s, h, rg, x0, x1;
     bool tail, whole;   // whole: all of the unit, which then needs no merge
-    int index;          // of its coded part: the split, or the CTA
+    int index;          // of its part: the split (the tail's own CTA counts as one behind them), or the CTA
 };
 template <int HD, int NT>
-struct AttnShared {     // maxima and sums of the warps, and behind them the tail's
-    float q_scale[8 * NT], m[AttnShape<HD, NT>::kWarps + 1][8 * NT], l[AttnShape<HD, NT>::kWarps + 1][8 * NT];
+struct AttnShared {
+    float q_scale[8 * NT], top[AttnShape<HD, NT>::kGroups][4][8 * NT], m[AttnShape<HD, NT>::kGroups][8 * NT], l[AttnShape<HD, NT>::kWarps][8 * NT];
     int bad;
-    uint32_t poison[2];
 };
 template <int HD, int NT>
 struct QueryRows {      // a warp takes every kWarps-th row of the group
@@ -605,50 +614,108 @@ struct QueryRows {      // a warp takes every kWarps-th row of the group
     }
 };
 
-// One CTA's piece of a unit: 8 NT query rows (row r = m * group + i of the head's rows). Each warp takes every kW-th of the
-// blocks with a running softmax of its own; no barrier until they are merged at the end. A warp's codes pass through a
-// ring of its own in shared memory (16-byte asynchronous copies). The caller has the query rows under way: what is small
-// is asked for first, so that it does not wait behind the codes.
+// One CTA's piece of a unit: 8 NT query rows (row r = m * group + i of the head's rows), its coded blocks and perhaps the
+// tail. Groups of four warps take every kGroups-th pair of blocks, each group with a running softmax of its own, merged at
+// the end. Of a pair each warp takes 16 keys for the first product and, for the second, a quarter of the value channels over
+// all 64 keys; the weights pass through shared memory between them. So a warp's sums are small, its code is short (a short
+// call spends much of its time on fetching code), and each code is read from shared memory and expanded once in the CTA.
+// Keys and values come through a ring of the warp's own (16-byte asynchronous copies): what a warp copies only it reads.
 template <int HD, int NT>
-__device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, const Piece &u, QueryRows<HD, NT> &qr, uint8_t *kv_smem, AttnShared<HD, NT> &sh) {
+__device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, const Piece &u, QueryRows<HD, NT> &qr, uint8_t *smem, AttnShared<HD, NT> &sh) {
     using S = AttnShape<HD, NT>;
-    constexpr int RG = 8 * NT, kW = S::kWarps, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4, kQRows = QueryRows<HD, NT>::kRows;
-    static_assert(kW * RG * kPitch * 4 <= S::kSmem, "the merge reuses the shared memory");
-    auto &q_scale = sh.q_scale;
-    auto &sm_m = sh.m;
-    auto &sm_l = sh.l;
-    auto &qx = qr.x;
-    int &sm_bad = sh.bad;
-    uint32_t(&sm_poison)[2] = sh.poison;
+    constexpr int RG = 8 * NT, kW = S::kWarps, kG = S::kGroups, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4, kMt = HD / 64;
     const int s = u.s, h = u.h, rg = u.rg;
-    const bool tail = u.tail, codes = u.x1 > u.x0, alone = p.coded == 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    // registers are what limits the CTAs of an SM: what the loop needs seldom is found anew
+    const int grp = warp >> 2, wq = warp & 3, key_half = wq & 1;     // first product: block wq / 2 of the pair, keys with bit 2 = key_half
     const size_t head = (size_t)s * a.c.n_kv + h, head_blocks = head * a.c.n_blocks;
     const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG;    // rows of this group that exist
-    const int unit = int(head) * a.groups + rg;
-    const int bfirst = p.b0 + u.x0 + warp;                           // this warp's blocks: bfirst, + kW, ..
-    const int ncoded = max(0, (u.x1 - u.x0 - warp + kW - 1) / kW);
+    const int n = u.x1 - u.x0, first = p.b0 + u.x0 + 2 * grp;        // coded blocks; pair i of this group begins with first + 2 kG i
+    const int pairs = (n - 2 * grp + 2 * kG - 1) / (2 * kG);         // <= 0: none
+    uint8_t *ring = smem + S::kQBytes + S::kPBytes + warp * kRing * kUnit;
+    uint4 *pbuf = reinterpret_cast<uint4 *>(smem + S::kQBytes + grp * (S::kPBytes / kG)) + lane;
+    const uint4 *qf = reinterpret_cast<const uint4 *>(smem) + lane;
+    const bool keep_lse = a.score && rg == 0;
 
     int bad = 0;
-    auto load_phys = [&](int i0) {                                   // lane l: where block i0 + l is stored
-        const int i = i0 + lane;
+    auto load_phys = [&](int i0) {                                   // lane l: where block l % 2 of pair i0 + l / 2 is stored
+        const int b = first + 2 * kG * (i0 + (lane >> 1)) + (lane & 1);
         int at = 0;
-        if (i < ncoded) {
-            at = a.c.table[head_blocks + bfirst + kW * i];
+        if (b < p.b0 + u.x1) {
+            at = a.c.table[head_blocks + b];
             if (unsigned(at) >= unsigned(a.c.n_blocks)) at = 0, bad = 1;
         }
         return at;
     };
-    // this thread's rows: 8 nt + 2 t + e
-    float mx[NT][2], l[NT][2];
+    int phys = load_phys(0), phys_next = load_phys(16);              // of the 16 pairs that are being asked for, and the next
+    float ks = a.c.k_scale[head_blocks + phys], vs = a.c.v_scale[head_blocks + phys], ks_next = 0.f, vs_next = 0.f;
+
+    // unit 2 i is pair i's keys (of this warp), unit 2 i + 1 its values (of this warp's channels)
+    uint8_t *put = ring;                                             // the slot that the next unit goes to
+    const uint8_t *take = ring;                                      // the slot that is read next
+    auto issue = [&](int v) {
+        const int i = v >> 1;
+        if (i < pairs) {
+            if ((v & 31) == 0 && v > 0) {
+                phys = phys_next;
+                phys_next = load_phys(i + 16);
+            }
+            const int two = 2 * (i & 15), left = n - 2 * grp - 2 * kG * i;   // blocks of the pair: one, or two
+            if (v & 1) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+                for (int j = 0; j < 2; ++j) {
+                    const size_t off = (head_blocks + __shfl_sync(0xffffffffu, phys, two + j)) * (kBlk * HD) + wq * (8 * HD) + 16 * lane;
+                    if (j < left)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            mx[nt][e] = -INFINITY;
-            l[nt][e] = 0.f;
+                        for (int k = 0; k < HD / 64; ++k) cp_async16(put + j * (8 * HD) + 512 * k + 16 * lane, a.c.v + off + 512 * k);
+                }
+            } else {
+                const size_t off = (head_blocks + __shfl_sync(0xffffffffu, phys, two + (wq >> 1))) * (kBlk * HD) + key_half * 256 + (lane >> 4) * 512 + (lane & 15) * 16;
+                if ((wq >> 1) < left)
+#pragma unroll
+                    for (int c = 0; c < HD / 64; ++c) {
+                        cp_async16(put + c * 1024 + 16 * lane, a.c.k + off + c * 2048);
+                        cp_async16(put + c * 1024 + 512 + 16 * lane, a.c.k + off + c * 2048 + 1024);
+                    }
+            }
+            put = put == ring + (kRing - 1) * kUnit ? ring : put + kUnit;
         }
+        cp_async_commit();
+    };
+    auto taken = [&]() { take = take == ring + (kRing - 1) * kUnit ? ring : take + kUnit; };
+#pragma unroll
+    for (int v = 0; v < kRing; ++v) issue(v);
+
+    // ---- query rows into their fragments ----
+    if (tid == 0) sh.bad = 0;
+#pragma unroll
+    for (int j = 0; j < QueryRows<HD, NT>::kRows; ++j) {
+        const int r = warp + j * kW;
+        if (r >= RG) break;
+        float amax = 0.f;
+        bool fin = true;
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i) {
+            if (r >= live) qr.x[j][i] = make_float2(0.f, 0.f);
+            fin = fin && isfinite(qr.x[j][i].x) && isfinite(qr.x[j][i].y);
+            amax = fmaxf(amax, fmaxf(fabsf(qr.x[j][i].x), fabsf(qr.x[j][i].y)));
+        }
+        fin = __all_sync(0xffffffffu, fin);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float f = fin ? lift(amax) : 0.f;
+        if (lane == 0) sh.q_scale[r] = fin ? a.scale * kLog2e / f : NAN;
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i) {
+            uint32_t hi = 0, lo = 0;
+            if (fin) halves2(qr.x[j][i].x * f, qr.x[j][i].y * f, hi, lo);
+            const int d = 2 * lane;                                  // of chunk i
+            uint32_t *dst = reinterpret_cast<uint32_t *>(smem) + (((i * NT + r / 8) * 4 + ((d & 15) >> 3)) * 32 + (r & 7) * 4 + (d >> 4)) * 4 + ((d & 7) >> 1);
+            dst[0] = hi;
+            dst[2 * 32 * 4] = lo;
+        }
+    }
+    __syncthreads();
+    auto scale_of = [&](int nt) { return *reinterpret_cast<const float2 *>(&sh.q_scale[8 * nt + 2 * t]); };
     // the tokens lo..hi-1 that row 8 nt + 2 t + e sees; all, if it does not exist: nothing reads its sums
     auto row_sees = [&](int nt, int e, int &lo, int &hi) {
         const int r = 8 * nt + 2 * t + e;
@@ -659,314 +726,58 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
     int all_lo, all_hi, dummy;
     seen(a, p, min(p.n - 1, (rg * RG + RG - 1) / per), all_lo, dummy);
     seen(a, p, rg * RG / per, dummy, all_hi);
-    const uint4 *qf = reinterpret_cast<const uint4 *>(kv_smem) + lane;
-    const bool keep_lse = a.score && rg == 0;
-    const int key0 = 8 * (g >> 1) + (g & 1);                         // key of row g of matrix 0; matrix j: + 2 j
-    auto scale_of = [&](int nt) { return *reinterpret_cast<const float2 *>(&q_scale[8 * nt + 2 * t]); };
-    // query rows into their fragments
-    auto stage_q = [&]() {
-        if (tid < 2) sm_poison[tid] = 0;
-        if (tid == 0) sm_bad = 0;
-        if (tid < RG) sm_m[kW][tid] = -INFINITY, sm_l[kW][tid] = 0.f;
+
+    // A row's weights are 2^(logit - mx + kTop), for all four warps of the group. mx is a maximum that is only renewed when a
+    // weight would pass 2^15, so most pairs need no maximum across the lanes and rescale nothing: the row's largest weight
+    // lies in 2^7..2^15. Values are summed in units of v_ref, the largest value scale so far: the logarithm of a
+    // block's scale over v_ref is added to the exponent, so that the products add straight to the sums, and the sum of the
+    // weights (a warp's own keys') takes it back.
+    float o[kMt][NT][4], mx[NT][2], l[NT][2];
 #pragma unroll
-        for (int j = 0; j < kQRows; ++j) {
-            const int r = warp + j * kW;
-            if (r >= RG) break;
-            float amax = 0.f;
-            bool fin = true;
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int i = 0; i < HD / 64; ++i) {
-                if (r >= live) qx[j][i] = make_float2(0.f, 0.f);
-                fin = fin && isfinite(qx[j][i].x) && isfinite(qx[j][i].y);
-                amax = fmaxf(amax, fmaxf(fabsf(qx[j][i].x), fabsf(qx[j][i].y)));
-            }
-            fin = __all_sync(0xffffffffu, fin);
+        for (int e = 0; e < 2; ++e) mx[nt][e] = -INFINITY, l[nt][e] = 0.f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const float f = fin ? lift(amax) : 0.f;
-            if (lane == 0) q_scale[r] = fin ? a.scale * kLog2e / f : NAN;
+        for (int mt = 0; mt < kMt; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
+    }
+    // Renews mx by the logits y of the group (y == -inf: not seen), and rescales the sums. The four warps call it together.
+    auto renew = [&](const float (&y)[NT][4]) {
 #pragma unroll
-            for (int i = 0; i < HD / 64; ++i) {
-                uint32_t hi = 0, lo = 0;
-                if (fin) halves2(qx[j][i].x * f, qx[j][i].y * f, hi, lo);
-                const int d = 2 * lane;                                  // of chunk i
-                uint32_t *dst = reinterpret_cast<uint32_t *>(kv_smem) + (((i * NT + r / 8) * 4 + ((d & 15) >> 3)) * 32 + (r & 7) * 4 + (d >> 4)) * 4 + ((d & 7) >> 1);
-                dst[0] = hi;
-                dst[2 * 32 * 4] = lo;
-            }
+        for (int nt = 0; nt < NT; ++nt) {
+            const float t0 = group_max(fmaxf(y[nt][0], y[nt][2])), t1 = group_max(fmaxf(y[nt][1], y[nt][3]));
+            if (g == 0) sh.top[grp][wq][8 * nt + 2 * t] = t0, sh.top[grp][wq][8 * nt + 2 * t + 1] = t1;
         }
-        __syncthreads();
+        group_sync(grp);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float now = mx[nt][e];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) now = fmaxf(now, sh.top[grp][i][8 * nt + 2 * t + e]);
+                const float f = mx[nt][e] == now ? 1.f : ex2(mx[nt][e] - now);
+                mx[nt][e] = now;
+                l[nt][e] *= f;
+#pragma unroll
+                for (int mt = 0; mt < kMt; ++mt) o[mt][nt][e] *= f, o[mt][nt][2 + e] *= f;
+            }
+    };
+    auto put_lse = [&](int b, int half, int r, float total, float top) {   // row r's sum over half a block, of weights at `top`
+        a.blk_lse[((head_blocks + b) * 2 + half) * 16 + r] = total == 0.f ? -INFINITY : top - kTop + log2f(total);
     };
 
-    // the tail's rows: a warp takes kTailCh channels, steps 4 tc + tj0 .. of the first product, and of it the key of
-    // row g of matrix m (of 6), which makes thread t's inputs of step s the keys 16 s + 4 t .. + 3
-    constexpr int kSteps = S::kTailCh / 16;
-    const int tc = warp * kSteps / 4, tj0 = warp * kSteps % 4, trows = p.L + p.n - kBlk * p.z;
-    const bool tactive = tail && warp * S::kTailCh < HD;
-    auto tail_key = [&](int m) { return 16 * (m >> 1) + 4 * (g >> 1) + 2 * (m & 1) + (g & 1); };
-    float4 kr[6][kSteps], vr[kSteps][2][3];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-#pragma unroll
-        for (int m = 0; m < 6; ++m) {
-            kr[m][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (tactive && tail_key(m) < trows)
-                kr[m][i] = *reinterpret_cast<const float4 *>(a.c.k_tail + (head * kTail + tail_key(m)) * HD + 64 * tc + 16 * t + 4 * (tj0 + i));
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int st = 0; st < 3; ++st) {
-                vr[i][k][st] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (tactive && 16 * st + 4 * t < trows)
-                    vr[i][k][st] = *reinterpret_cast<const float4 *>(a.c.v_tail + (head * HD + 16 * (warp * kSteps + i) + g + 8 * k) * kTail + 16 * st + 4 * t);
-            }
-    }
-    int phys = load_phys(0);                                         // of the window of 32 blocks that is being asked for
-    int phys_next = load_phys(32);                                   // and of the one behind it
-    float ks = 0.f, vs = 0.f;                                        // lane l: scales of block l of the window that is read
-    if (lane < ncoded) ks = a.c.k_scale[head_blocks + phys], vs = a.c.v_scale[head_blocks + phys];
-    float ks_next = 0.f, vs_next = 0.f;
-
-    // ---- codes on their way: unit 2 i is block i's keys, unit 2 i + 1 its values ----
-    uint8_t *ring = kv_smem + S::kQBytes + warp * kRing * kUnit;
-    uint8_t *put = ring + 16 * lane;                                 // the slot that the next unit goes to
-    const uint8_t *take = ring;                                      // the slot that is read next
-    auto issue = [&](int u) {
-        const int i = u >> 1;
-        if (i < ncoded) {
-            if ((u & 63) == 0 && u > 0) {
-                phys = phys_next;
-                phys_next = load_phys(i + 32);
-            }
-            const size_t off = (head_blocks + __shfl_sync(0xffffffffu, phys, i & 31)) * kUnit;
-            const uint8_t *src = ((u & 1) ? a.c.v : a.c.k) + off + 16 * lane;
-#pragma unroll
-            for (int k = 0; k < kUnit / 512; ++k) cp_async16(put + 512 * k, src + 512 * k);
-            put = put == ring + (kRing - 1) * kUnit + 16 * lane ? ring + 16 * lane : put + kUnit;
-        }
-        cp_async_commit();
-    };
-    auto taken = [&]() { take = take == ring + (kRing - 1) * kUnit ? ring : take + kUnit; };
-#pragma unroll
-    for (int u = 0; u < kRing; ++u)
-        if (u < kRing - S::kHold || !tail) issue(u);
-
-    // ---- the tail (at most 48 fp32 rows), while the first codes are on their way: a warp takes kTailCh channels
-    // of every row. Keys enter as two fp16 halves, each scaled by a power of two of its own; values and weights as
-    // three bf16 parts (fp32's range, so that no token's size touches another's precision). A token that holds an
-    // infinity or a NaN makes the rows that see it NaN; its own numbers enter as 0. ----
-    if (tail) {
-        constexpr int kPart = kRing * kUnit / 4;                     // from one warp's partial logits [48][RG] to the next's
-        float *first = reinterpret_cast<float *>(kv_smem + S::kQBytes + (kRing - S::kHold) * kUnit), *mine = first + warp * kPart;
-        stage_q();
-        if (tactive) {
-            uint32_t poison[2] = {0, 0};
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int st = 0; st < 3; ++st) {
-                        float *v = &vr[i][k][st].x;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = 16 * st + 4 * t + e;
-                            if (key >= trows || !isfinite(v[e])) {
-                                if (key < trows) poison[key >> 5] |= 1u << (key & 31);
-                                v[e] = 0.f;
-                            }
-                        }
-                    }
-            if (poison[0]) atomicOr(&sm_poison[0], poison[0]);
-            if (poison[1]) atomicOr(&sm_poison[1], poison[1]);
-            float up[6], back[6];
-#pragma unroll
-            for (int m = 0; m < 6; ++m) {
-                float amax = 0.f;
-                int fin = 1;
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    const float4 y = kr[m][i];
-                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
-                    fin &= isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w);
-                }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                fin &= __shfl_xor_sync(0xffffffffu, fin, 1);
-                fin &= __shfl_xor_sync(0xffffffffu, fin, 2);
-                up[m] = fin ? lift(amax) : 0.f;
-                back[m] = fin ? 1.f / up[m] : NAN;
-            }
-            float x[3][NT][4];
-#pragma unroll
-            for (int mt = 0; mt < 3; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) x[mt][nt][0] = x[mt][nt][1] = x[mt][nt][2] = x[mt][nt][3] = 0.f;
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int j = tj0 + i;
-                uint2 qh[NT], ql[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint2 *f = reinterpret_cast<const uint2 *>(qf + ((tc * NT + nt) * 4 + (j >> 1)) * 32) + (j & 1);
-                    qh[nt] = f[0];
-                    ql[nt] = f[2 * 32 * 2];
-                }
-#pragma unroll
-                for (int mt = 0; mt < 3; ++mt) {
-                    uint32_t ah[4], al[4];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int m = 2 * mt + k;
-                        const float4 y = up[m] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : kr[m][i];
-                        halves2(y.x * up[m], y.y * up[m], ah[k], al[k]);
-                        halves2(y.z * up[m], y.w * up[m], ah[2 + k], al[2 + k]);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(x[mt][nt], al, qh[nt].x, qh[nt].y);
-                        mma_f16(x[mt][nt], ah, ql[nt].x, ql[nt].y);
-                        mma_f16(x[mt][nt], ah, qh[nt].x, qh[nt].y);
-                    }
-                }
-            }
-#pragma unroll
-            for (int mt = 0; mt < 3; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        *reinterpret_cast<float2 *>(mine + tail_key(2 * mt + k) * RG + 8 * nt + 2 * t) =
-                            make_float2(x[mt][nt][2 * k] * back[2 * mt + k], x[mt][nt][2 * k + 1] * back[2 * mt + k]);
-        }
-        __syncthreads();
-        constexpr int kParts = HD / S::kTailCh;
-        for (int e = tid; e < kTail * RG; e += kW * 32) {
-            float x = 0.f;
-#pragma unroll
-            for (int i = 0; i < kParts; ++i) x += first[i * kPart + e];
-            first[e] = x;
-        }
-        __syncthreads();
-        if (tactive) {
-            uint32_t pf[NT][3][2][3];
-            float total[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float x[6][2];
-                int lo[2], hi[2];
-                row_sees(nt, 0, lo[0], hi[0]);
-                row_sees(nt, 1, lo[1], hi[1]);
-                const float2 qs = scale_of(nt);
-#pragma unroll
-                for (int m = 0; m < 6; ++m) {
-                    const int key = tail_key(m), pos = kBlk * p.z + key;
-                    const float2 y = *reinterpret_cast<const float2 *>(first + key * RG + 8 * nt + 2 * t);
-                    const bool bad_key = sm_poison[key >> 5] >> (key & 31) & 1;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        x[m][e] = pos < lo[e] || pos >= hi[e] ? -INFINITY : bad_key ? NAN : (e ? y.y * qs.y : y.x * qs.x);
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float top = x[0][e];
-#pragma unroll
-                    for (int m = 1; m < 6; ++m) top = fmaxf(top, x[m][e]);
-                    top = group_max(top);
-                    top = isnan(top) ? -INFINITY : top;
-                    const float ref = top == -INFINITY ? 0.f : top - kTop;
-                    float sum[2] = {0.f, 0.f};
-#pragma unroll
-                    for (int m = 0; m < 6; ++m) sum[m >> 2] += x[m][e] = ex2(x[m][e] - ref);
-                    sum[0] = group_sum(sum[0]);
-                    sum[1] = group_sum(sum[1]);
-                    const int r = 8 * nt + 2 * t + e;
-                    total[nt][e] = sum[0] + sum[1];
-                    if (warp == 0 && g == 0) {
-                        *reinterpret_cast<float2 *>(a.part_ml + ((size_t)unit * RG + r) * 2) = make_float2(top, sum[0] + sum[1]);
-                        sm_m[kW][r] = top;
-                        sm_l[kW][r] = sum[0] + sum[1];
-                        if (keep_lse && r < per)
-                            for (int i = 0; i < 2; ++i)
-                                if (p.z + i < p.b0 + p.nb) a.blk_lse[(head_blocks + p.z + i) * 16 + r] = sum[i] == 0.f ? -INFINITY : ref + log2f(sum[i]);
-                    }
-                }
-#pragma unroll
-                for (int m = 0; m < 6; ++m) {
-                    uint32_t y[3];
-                    thirds2(x[m][0], x[m][1], y);
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) pf[nt][m >> 1][m & 1][k] = transpose8x8(y[k]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                float d[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
-#pragma unroll
-                for (int st = 0; st < 3; ++st) {
-                    uint32_t af[3][4];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {                    // channels g and g + 8 of the tile
-                        const float4 y = vr[i][k][st];
-                        uint32_t y0[3], y1[3];
-                        thirds2(y.x, y.y, y0);
-                        thirds2(y.z, y.w, y1);
-#pragma unroll
-                        for (int q = 0; q < 3; ++q) af[q][k] = y0[q], af[q][2 + k] = y1[q];
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int q = 2; q >= 0; --q)                 // the small products first
-#pragma unroll
-                            for (int k = 2 - q; k >= 0; --k)
-                                mma_bf16(d[nt], af[q][0], af[q][1], af[q][2], af[q][3], pf[nt][st][0][k], pf[nt][st][1][k]);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = 8 * nt + 2 * t + (k & 1), d0 = 16 * (warp * kSteps + i) + g + 8 * (k >> 1), rid = rg * RG + r;
-                        if (!alone)
-                            a.part_o[((size_t)unit * RG + r) * HD + d0] = d[nt][k];
-                        else if (r < live)
-                            a.out[((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + d0] = d[nt][k] / total[nt][k & 1];
-                    }
-            }
-        }
-        if (!codes) return;
-        __syncthreads();                                             // the slots held back are free
-#pragma unroll
-        for (int u = kRing - S::kHold; u < kRing; ++u) issue(u);
-    }
-
-    if (!tail) {
-        stage_q();
-    }
-
-    float o[HD / 16][NT][4];
-#pragma unroll
-    for (int i = 0; i < HD / 16; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
-    // A row's weights are 2^(logit - mx + kTop). mx is a maximum that is only renewed when a weight would pass 2^15, so most
-    // blocks need no maximum across the lanes and rescale nothing: the row's largest weight lies in 2^7..2^15. Values are
-    // summed in units of v_ref, the largest value scale so far: the logarithm of a block's scale over v_ref is added to
-    // the exponent, so that the products add straight to the sums, and the sum of the weights takes it back.
     float v_ref = 0.f, v_lb = 0.f, v_inv = 1.f;
-    for (int i = 0; i < ncoded; ++i) {
-        if ((i & 31) == 0) {                                         // the next 32 blocks' scales
+    for (int i = 0; i < pairs; ++i) {
+        if ((i & 15) == 0) {                                         // the next 16 pairs' scales
             if (i > 0) ks = ks_next, vs = vs_next;
-            float top = isnan(vs) ? 0.f : vs;
+            const bool is = first + 2 * kG * (i + (lane >> 1)) + (lane & 1) < p.b0 + u.x1;
+            float top = !is || isnan(vs) ? 0.f : vs;
 #pragma unroll
             for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
             if (top > v_ref) {
                 const float f = v_ref / top;
 #pragma unroll
-                for (int mt = 0; mt < HD / 16; ++mt)
+                for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -978,29 +789,27 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             v_lb = log2f(r);
             v_inv = isnan(vs) ? vs : 1.f / r;
         }
-        if ((i & 31) == 16) {                                        // the next window's, half a window ahead
-            ks_next = vs_next = 0.f;
-            if (i + 16 + lane < ncoded) ks_next = a.c.k_scale[head_blocks + phys_next], vs_next = a.c.v_scale[head_blocks + phys_next];
+        if ((i & 15) == 8) {                                         // the next window's, half a window ahead
+            ks_next = a.c.k_scale[head_blocks + phys_next];
+            vs_next = a.c.v_scale[head_blocks + phys_next];
         }
-        const int b = bfirst + kW * i;
-        const float bks = __shfl_sync(0xffffffffu, ks, i & 31);
-        const float blb = __shfl_sync(0xffffffffu, v_lb, i & 31);
-        float binv = __shfl_sync(0xffffffffu, v_inv, i & 31);
+        const int from = 2 * (i & 15) + (wq >> 1), b = first + 2 * kG * i + (wq >> 1);   // this warp's block of the pair
+        const float bks = __shfl_sync(0xffffffffu, ks, from), blb = __shfl_sync(0xffffffffu, v_lb, from);
+        float binv = __shfl_sync(0xffffffffu, v_inv, from);
+        const bool there = b < p.b0 + u.x1;
         cp_async_wait_groups<kRing - 1>();
         __syncwarp();
-        float x[2][NT][4], xl[2][NT][4];                             // by the query's hi and lo halves
+        float x[NT][4], xl[NT][4];                                   // by the query's hi and lo halves
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[mt][nt][k] = xl[mt][nt][k] = 0.f;
-        const uint8_t *K = take + key0 * 64 + 16 * t;
+            for (int k = 0; k < 4; ++k) x[nt][k] = xl[nt][k] = 0.f;
+        const uint8_t *K = take + (4 * (g >> 1) + (g & 1)) * 64 + 16 * t;
 #pragma unroll
         for (int c = 0; c < HD / 64; ++c) {
-            uint32_t kw[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(kw[j]) = *reinterpret_cast<const uint4 *>(K + (c * kBlk + 2 * j) * 64);
+            uint32_t k0[4], k1[4];
+            *reinterpret_cast<uint4 *>(k0) = *reinterpret_cast<const uint4 *>(K + c * 1024);
+            *reinterpret_cast<uint4 *>(k1) = *reinterpret_cast<const uint4 *>(K + c * 1024 + 128);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t qh[NT][4], ql[NT][4];
@@ -1010,48 +819,34 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                     *reinterpret_cast<uint4 *>(ql[nt]) = qf[((c * NT + nt) * 4 + 2 + half) * 32];
                 }
 #pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {                     // four products of different sums, then their low halves
+                for (int jj = 0; jj < 2; ++jj) {
                     const int j = 2 * half + jj;
-                    uint32_t af[2][4];
+                    const uint32_t af[4] = {codes_lo(k0[j]), codes_lo(k1[j]), codes_hi(k0[j]), codes_hi(k1[j])};
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        af[mt][0] = codes_lo(kw[2 * mt][j]);
-                        af[mt][1] = codes_lo(kw[2 * mt + 1][j]);
-                        af[mt][2] = codes_hi(kw[2 * mt][j]);
-                        af[mt][3] = codes_hi(kw[2 * mt + 1][j]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(x[nt], af, qh[nt][2 * jj], qh[nt][2 * jj + 1]);
+                        mma_f16(xl[nt], af, ql[nt][2 * jj], ql[nt][2 * jj + 1]);
                     }
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                float(&d)[4] = part && NT == 1 ? xl[mt][nt] : x[mt][nt];
-                                const uint32_t b0 = part ? ql[nt][2 * jj] : qh[nt][2 * jj], b1 = part ? ql[nt][2 * jj + 1] : qh[nt][2 * jj + 1];
-                                mma_f16(d, af[mt], b0, b1);
-                            }
                 }
             }
         }
         __syncwarp();
         taken();
         issue(2 * i + kRing);
-        float y[2][NT][4], peak = -INFINITY;                         // exponents of the weights
+        float y[NT][4], peak = -INFINITY;                            // exponents of the weights
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float z = bks * (e ? scale_of(nt).y : scale_of(nt).x), less = blb + kTop - mx[nt][e];   // +inf before a row's first key
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int k = e; k < 4; k += 2) {
-                        if (NT == 1) x[j][nt][k] += xl[j][nt][k];
-                        y[j][nt][k] = fmaf(x[j][nt][k], z, less);
-                    }
+                for (int k = e; k < 4; k += 2) {
+                    x[nt][k] += xl[nt][k];
+                    y[nt][k] = fmaf(x[nt][k], z, less);
+                }
             }
         const int pos0 = kBlk * b;
-        if (pos0 < all_lo || pos0 + kBlk > all_hi) {
+        if (!there || pos0 < all_lo || pos0 + kBlk > all_hi) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1059,45 +854,26 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                     int lo, hi;
                     row_sees(nt, e, lo, hi);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int k = e; k < 4; k += 2) {
-                            const int pos = pos0 + key0 + 4 * j + 2 * (k >> 1);
-                            if (pos < lo || pos >= hi) y[j][nt][k] = -INFINITY;
-                        }
+                    for (int k = e; k < 4; k += 2) {
+                        const int pos = pos0 + 8 * (g >> 1) + 4 * key_half + 2 * (k >> 1) + (g & 1);
+                        if (!there || pos < lo || pos >= hi) y[nt][k] = -INFINITY;
+                    }
                 }
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) peak = fmaxf(peak, y[nt][k]);
+        if (group_or(grp, peak > 15.f)) {                            // seldom, once the maxima have been met
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) peak = fmaxf(peak, y[j][nt][k]);
-        if (__any_sync(0xffffffffu, peak > 15.f)) {                  // seldom, once the maxima have been met
+                for (int k = 0; k < 4; ++k) y[nt][k] = y[nt][k] == -INFINITY ? -INFINITY : x[nt][k] * (bks * (k & 1 ? scale_of(nt).y : scale_of(nt).x));
+            renew(y);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float z = bks * (e ? scale_of(nt).y : scale_of(nt).x);
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int k = e; k < 4; k += 2) {
-                            y[j][nt][k] = y[j][nt][k] == -INFINITY ? -INFINITY : x[j][nt][k] * z;
-                            top = fmaxf(top, y[j][nt][k]);
-                        }
-                    const float now = fmaxf(mx[nt][e], group_max(top)), f = mx[nt][e] == now ? 1.f : ex2(mx[nt][e] - now);
-                    const float less = now == -INFINITY ? 0.f : blb + kTop - now;
-                    mx[nt][e] = now;
-                    l[nt][e] *= f;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int k = e; k < 4; k += 2) y[j][nt][k] += less;
-#pragma unroll
-                    for (int mt = 0; mt < HD / 16; ++mt) o[mt][nt][e] *= f, o[mt][nt][2 + e] *= f;
-                }
+                for (int k = 0; k < 4; ++k) y[nt][k] += mx[nt][k & 1] == -INFINITY ? 0.f : blb + kTop - mx[nt][k & 1];
         }
         if (isnan(binv)) {                                           // rows that see the block are NaN, the others take nothing of it
             binv = 0.f;
@@ -1107,113 +883,280 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                 for (int e = 0; e < 2; ++e) {
                     int lo, hi;
                     row_sees(nt, e, lo, hi);
-                    if (lo < pos0 + kBlk && hi > pos0) l[nt][e] = NAN;
+                    if (there && lo < pos0 + kBlk && hi > pos0) l[nt][e] = NAN;
                 }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[nt][k] = ex2(y[nt][k]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int k = e; k < 4; k += 2) sum += y[j][nt][k] = ex2(y[j][nt][k]);
+                const float sum = y[nt][e] + y[nt][2 + e];
                 l[nt][e] = fmaf(sum, binv, l[nt][e]);
                 if (keep_lse) {
                     const float total = group_sum(sum) * binv;
                     const int r = 8 * nt + 2 * t + e;
-                    if (g == 0 && r < per) a.blk_lse[(head_blocks + b) * 16 + r] = total == 0.f ? -INFINITY : mx[nt][e] - kTop + log2f(total);
+                    if (g == 0 && r < per && there) put_lse(b, key_half, r, total, mx[nt][e]);
                 }
             }
-        uint32_t ph[NT][2][2], pl[NT][2][2];                         // [step][input pair]
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t hw, lw;
-                halves2(y[j >> 1][nt][2 * (j & 1)], y[j >> 1][nt][2 * (j & 1) + 1], hw, lw);
-                ph[nt][j >> 1][j & 1] = transpose8x8(hw);
-                pl[nt][j >> 1][j & 1] = transpose8x8(lw);
-            }
+            uint4 w;                                                 // hi and lo halves of the step's two input pairs
+            halves2(y[nt][0], y[nt][1], w.x, w.z);
+            halves2(y[nt][2], y[nt][3], w.y, w.w);
+            pbuf[(wq * NT + nt) * 32] = make_uint4(transpose8x8(w.x), transpose8x8(w.y), transpose8x8(w.z), transpose8x8(w.w));
+        }
         cp_async_wait_groups<kRing - 1>();
-        __syncwarp();
+        group_sync(grp);
         const uint8_t *V = take + g * kBlk + 8 * t;
-        constexpr int kG = NT == 1 ? 4 : 2;                          // channel tiles at once: four different sums
 #pragma unroll
-        for (int m0 = 0; m0 < HD / 16; m0 += kG) {
-            uint32_t af[kG][2][4];
+        for (int j = 0; j < 2; ++j) {                                // block of the pair
+            uint32_t af[kMt][2][4];
 #pragma unroll
-            for (int i = 0; i < kG; ++i) {
-                const uint2 v0 = *reinterpret_cast<const uint2 *>(V + (16 * (m0 + i)) * kBlk), v1 = *reinterpret_cast<const uint2 *>(V + (16 * (m0 + i) + 8) * kBlk);
-                af[i][0][0] = codes_lo(v0.x), af[i][0][1] = codes_lo(v1.x), af[i][0][2] = codes_hi(v0.x), af[i][0][3] = codes_hi(v1.x);
-                af[i][1][0] = codes_lo(v0.y), af[i][1][1] = codes_lo(v1.y), af[i][1][2] = codes_hi(v0.y), af[i][1][3] = codes_hi(v1.y);
+            for (int mt = 0; mt < kMt; ++mt) {
+                const uint2 v0 = *reinterpret_cast<const uint2 *>(V + j * (8 * HD) + (16 * mt) * kBlk), v1 = *reinterpret_cast<const uint2 *>(V + j * (8 * HD) + (16 * mt + 8) * kBlk);
+                af[mt][0][0] = codes_lo(v0.x), af[mt][0][1] = codes_lo(v1.x), af[mt][0][2] = codes_hi(v0.x), af[mt][0][3] = codes_hi(v1.x);
+                af[mt][1][0] = codes_lo(v0.y), af[mt][1][1] = codes_lo(v1.y), af[mt][1][2] = codes_hi(v0.y), af[mt][1][3] = codes_hi(v1.y);
             }
 #pragma unroll
-            for (int st = 0; st < 2; ++st)
+            for (int st = 0; st < 2; ++st) {
+                uint4 w[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) w[nt] = pbuf[((2 * j + st) * NT + nt) * 32];
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int i = 0; i < kG; ++i)
+                    for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16(o[m0 + i][nt], af[i][st], part ? pl[nt][st][0] : ph[nt][st][0], part ? pl[nt][st][1] : ph[nt][st][1]);
+                        for (int nt = 0; nt < NT; ++nt) mma_f16(o[mt][nt], af[mt][st], part ? w[nt].z : w[nt].x, part ? w[nt].w : w[nt].y);
+            }
         }
         __syncwarp();
         taken();
         issue(2 * i + 1 + kRing);
     }
-
-    // ---- the warps' sums, merged in their order ----
     cp_async_wait_groups<0>();
-    if (bad) sm_bad = 1;
-    __syncthreads();
-    float *om = reinterpret_cast<float *>(kv_smem) + warp * RG * kPitch;
+    if (v_ref > 0.f || pairs > 0)
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[mt][nt][k] *= v_ref;
+
+    // ---- the tail (at most 48 fp32 rows), by the first group: warps 0..2 take 16 keys each, then every warp its channels of
+    // the values. Keys enter as two fp16 halves, each key's 64 channels scaled by a power of two of their own; values and
+    // weights as three bf16 parts (fp32's range, so that no token's size touches another's precision). A token that
+    // holds an infinity or a NaN makes the rows that see it NaN; its own numbers enter as 0. ----
+    if (u.tail && grp == 0) {
+        const int rows = p.L + p.n - kBlk * p.z, base = kBlk * p.z;
+        uint4 *tbuf = reinterpret_cast<uint4 *>(smem + S::kQBytes + S::kPBytes) + lane;   // the group's rings: [3 steps][NT][2] words of weights
+        float x[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[nt][k] = 0.f;
+        const int key0 = 16 * wq + 4 * (g >> 1) + (g & 1);           // and key0 + 2
+        if (wq < 3) {
+            const float *K = a.c.k_tail + (head * kTail + key0) * HD + 16 * t;
+#pragma unroll 1
+            for (int c = 0; c < HD / 64; ++c) {
+                float4 kr[2][4];
+                float up[2], back[2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) kr[m][j] = key0 + 2 * m < rows ? *reinterpret_cast<const float4 *>(K + 2 * m * HD + 64 * c + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t top = 0;                                // magnitudes as bits: infinities and NaN come last
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 y = kr[m][j];
+                        top = max(max(top, __float_as_uint(y.x) & 0x7fffffffu), __float_as_uint(y.y) & 0x7fffffffu);
+                        top = max(max(top, __float_as_uint(y.z) & 0x7fffffffu), __float_as_uint(y.w) & 0x7fffffffu);
+                    }
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const bool fin = top < 0x7f800000u;
+                    up[m] = fin ? lift(__uint_as_float(top)) : 0.f;
+                    back[m] = fin ? 1.f / up[m] : NAN;
+                }
+                float xc[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) xc[nt][0] = xc[nt][1] = xc[nt][2] = xc[nt][3] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t ah[4], al[4];
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const float4 y = up[m] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : kr[m][j];
+                        halves2(y.x * up[m], y.y * up[m], ah[m], al[m]);
+                        halves2(y.z * up[m], y.w * up[m], ah[2 + m], al[2 + m]);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint2 *f = reinterpret_cast<const uint2 *>(qf + ((c * NT + nt) * 4 + (j >> 1)) * 32) + (j & 1);
+                        const uint2 qh = f[0], ql = f[2 * 32 * 2];
+                        mma_f16(xc[nt], al, qh.x, qh.y);
+                        mma_f16(xc[nt], ah, ql.x, ql.y);
+                        mma_f16(xc[nt], ah, qh.x, qh.y);
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[nt][k] = fmaf(xc[nt][k], back[k >> 1], x[nt][k]);
+            }
+        }
+        float y[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                int lo, hi;
+                row_sees(nt, e, lo, hi);
+#pragma unroll
+                for (int k = e; k < 4; k += 2) {
+                    const int pos = base + key0 + 2 * (k >> 1);
+                    y[nt][k] = wq == 3 || pos < lo || pos >= hi ? -INFINITY : x[nt][k] * (e ? scale_of(nt).y : scale_of(nt).x);
+                }
+            }
+        group_sync(0);                                               // every warp is done with its ring, and with sh.top
+        renew(y);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float ref = mx[nt][e] == -INFINITY ? 0.f : mx[nt][e] - kTop;
+                y[nt][e] = ex2(y[nt][e] - ref);
+                y[nt][2 + e] = ex2(y[nt][2 + e] - ref);
+                const float sum = y[nt][e] + y[nt][2 + e];
+                l[nt][e] += sum;
+                if (keep_lse) {
+                    const float total = group_sum(sum);
+                    const int r = 8 * nt + 2 * t + e, b = p.z + (wq >> 1);
+                    if (g == 0 && r < per && b < p.b0 + p.nb) put_lse(b, wq & 1, r, total, mx[nt][e]);
+                }
+            }
+            if (wq < 3) {
+                uint32_t w0[3], w1[3];
+                thirds2(y[nt][0], y[nt][1], w0);
+                thirds2(y[nt][2], y[nt][3], w1);
+                tbuf[((wq * NT + nt) * 2) * 32] = make_uint4(transpose8x8(w0[0]), transpose8x8(w1[0]), transpose8x8(w0[1]), transpose8x8(w1[1]));
+                tbuf[((wq * NT + nt) * 2 + 1) * 32] = make_uint4(transpose8x8(w0[2]), transpose8x8(w1[2]), 0, 0);
+            }
+        }
+        group_sync(0);
+        uint32_t poison[2] = {0, 0};                                 // tokens whose values are not finite
+        const float *V = a.c.v_tail + (head * HD + wq * (HD / 4) + g) * kTail + 4 * t;
+#pragma unroll 1
+        for (int st = 0; st < 3; ++st) {
+            if (16 * st >= rows) break;
+            float4 vr[kMt][2];
+#pragma unroll
+            for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    vr[mt][k] = 16 * st + 4 * t < rows ? *reinterpret_cast<const float4 *>(V + (16 * mt + 8 * k) * kTail + 16 * st) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int mt = 0; mt < kMt; ++mt) {
+                uint32_t af[3][4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float v[4] = {vr[mt][k].x, vr[mt][k].y, vr[mt][k].z, vr[mt][k].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = 16 * st + 4 * t + e;
+                        if (key >= rows || !isfinite(v[e])) {
+                            if (key < rows) poison[key >> 5] |= 1u << (key & 31);
+                            v[e] = 0.f;
+                        }
+                    }
+                    uint32_t y0[3], y1[3];
+                    thirds2(v[0], v[1], y0);
+                    thirds2(v[2], v[3], y1);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) af[i][k] = y0[i], af[i][2 + k] = y1[i];
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint4 w01 = tbuf[((st * NT + nt) * 2) * 32], w2 = tbuf[((st * NT + nt) * 2 + 1) * 32];
+                    const uint32_t wf[3][2] = {{w01.x, w01.y}, {w01.z, w01.w}, {w2.x, w2.y}};
+#pragma unroll
+                    for (int i = 2; i >= 0; --i)                     // the small products first
+#pragma unroll
+                        for (int k = 2 - i; k >= 0; --k) mma_bf16(o[mt][nt], af[i][0], af[i][1], af[i][2], af[i][3], wf[k][0], wf[k][1]);
+                }
+            }
+        }
+        poison[0] = __reduce_or_sync(0xffffffffu, poison[0]);
+        poison[1] = __reduce_or_sync(0xffffffffu, poison[1]);
+        if (poison[0] | poison[1]) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    int lo, hi;
+                    row_sees(nt, e, lo, hi);
+                    for (int k = 0; k < kTail; ++k)
+                        if ((poison[k >> 5] >> (k & 31) & 1) && base + k >= lo && base + k < hi) l[nt][e] = NAN;
+                }
+        }
+    }
+
+    // ---- the groups' sums, merged in their order ----
+    if (bad) sh.bad = 1;
+    __syncthreads();                                                 // also: the shared memory may be reused
+    float *om = reinterpret_cast<float *>(smem) + grp * RG * kPitch;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 8 * nt + 2 * t + e;
             const float sum = group_sum(l[nt][e]);
-            if (g == 0) sm_m[warp][r] = mx[nt][e], sm_l[warp][r] = sum;
+            if (g == 0) {
+                sh.l[warp][r] = sum;
+                if (wq == 0) sh.m[grp][r] = mx[nt][e];
+            }
 #pragma unroll
-            for (int mt = 0; mt < HD / 16; ++mt) {
-                om[r * kPitch + 16 * mt + g] = o[mt][nt][e] * v_ref;
-                om[r * kPitch + 16 * mt + g + 8] = o[mt][nt][2 + e] * v_ref;
+            for (int mt = 0; mt < kMt; ++mt) {
+                om[r * kPitch + wq * (HD / 4) + 16 * mt + g] = o[mt][nt][e];
+                om[r * kPitch + wq * (HD / 4) + 16 * mt + g + 8] = o[mt][nt][2 + e];
             }
         }
     __syncthreads();
-    const size_t part = part_of(a, unit, u.index);
+    const size_t part = part_of(a, size_t(head) * a.groups + rg, u.index);
     if (tid == 0) {
-        if (sm_bad) atomicOr(a.c.err, kErrTable);
-        a.part_bad[part] = sm_bad;
+        if (sh.bad) atomicOr(a.c.err, kErrTable);
+        a.part_bad[part] = sh.bad;
     }
-    if (sm_bad) return;
-    if (tid < RG) {   // each state's factor, in place of its maximum
+    if (sh.bad) return;
+    if (tid < RG) {   // each group's factor, in place of its maximum
         float top = -INFINITY, total = 0.f;
-        const int n = u.whole ? kW + 1 : kW;
-        for (int i = 0; i < n; ++i) top = fmaxf(top, sm_m[i][tid]);
-        for (int i = 0; i < n; ++i) {
-            const float f = sm_m[i][tid] == top ? 1.f : ex2(sm_m[i][tid] - top);
-            sm_m[i][tid] = f;
-            total = fmaf(sm_l[i][tid], f, total);
+#pragma unroll
+        for (int i = 0; i < kG; ++i) top = fmaxf(top, sh.m[i][tid]);
+#pragma unroll
+        for (int i = 0; i < kG; ++i) {
+            const float f = sh.m[i][tid] == top ? 1.f : ex2(sh.m[i][tid] - top);
+            sh.m[i][tid] = f;
+            total = fmaf((sh.l[4 * i][tid] + sh.l[4 * i + 1][tid]) + (sh.l[4 * i + 2][tid] + sh.l[4 * i + 3][tid]), f, total);
         }
-        sm_l[0][tid] = total;
+        sh.l[0][tid] = total;
         *reinterpret_cast<float2 *>(a.part_ml + (part * RG + tid) * 2) = make_float2(top, total);
     }
     __syncthreads();
     for (int e = tid; e < min(live, RG) * (HD / 4); e += kW * 32) {
         const int r = e / (HD / 4), d = 4 * (e % (HD / 4));
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](const float4 &y, float f) {
-            sum.x = fmaf(y.x, f, sum.x), sum.y = fmaf(y.y, f, sum.y), sum.z = fmaf(y.z, f, sum.z), sum.w = fmaf(y.w, f, sum.w);
-        };
-        if (u.whole) add(*reinterpret_cast<const float4 *>(a.part_o + ((size_t)unit * RG + r) * HD + d), sm_m[kW][r]);
 #pragma unroll
-        for (int i = 0; i < kW; ++i) add(*reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(kv_smem) + (i * RG + r) * kPitch + d), sm_m[i][r]);
+        for (int i = 0; i < kG; ++i) {
+            const float4 y = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem) + (i * RG + r) * kPitch + d);
+            const float f = sh.m[i][r];
+            sum.x = fmaf(y.x, f, sum.x), sum.y = fmaf(y.y, f, sum.y), sum.z = fmaf(y.z, f, sum.z), sum.w = fmaf(y.w, f, sum.w);
+        }
         if (u.whole) {
             const int rid = rg * RG + r;
-            const float total = sm_l[0][r];
+            const float total = sh.l[0][r];
             *reinterpret_cast<float4 *>(a.out + ((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + d) =
                 make_float4(sum.x / total, sum.y / total, sum.z / total, sum.w / total);
         } else {
@@ -1244,8 +1187,8 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     const bool codes = split >= 0 && split < nsplit;
     u.x0 = codes ? int((long)p.coded * split / nsplit) : 0;
     u.x1 = codes ? int((long)p.coded * (split + 1) / nsplit) : 0;
-    u.whole = nsplit == 1 && !a.apart;
-    u.index = split;
+    u.whole = nsplit == 0 || (nsplit == 1 && !a.apart);
+    u.index = split + a.apart;
     attn_piece<HD, NT>(a, p, u, q, kv_smem, sh);
 }
 
@@ -1307,7 +1250,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         pos += to - from;
         Piece u{s, ui / p.groups, ui % p.groups, min(from, p.coded), min(to, p.coded)};
         u.tail = from <= p.coded && to > p.coded;
-        u.whole = from == 0 && u.tail && u.x1 > 0;
+        u.whole = from == 0 && u.tail;
         u.index = cta;
         if (a.c.sealed[(size_t)s * a.c.n_kv + u.h] != p.z) {         // heads of a sequence that differ: left alone
             if (tid == 0) atomicOr(a.c.err, kErrState);
@@ -1325,7 +1268,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
 // scores (grid x behind them, row group 0). HD / 4 threads take four channels each of a row; with `apart_rows` all threads of
 // a CTA take one row and share out its parts (few units of many parts), else each such group takes a row of its own.
 constexpr int kMergeThreads = 256;
-constexpr int kMaxCtas = 304;   // two for each SM
+constexpr int kMaxCtas = 456;   // three for each SM
 template <int HD, int NT>
 __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int row_ctas, int apart_rows) {
     constexpr int RG = 8 * NT, kLanes = kMergeThreads / (HD / 4), kSome = 4;
@@ -1339,7 +1282,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
     const Span p = span_of(a, s, sealed, RG);
     const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, row0 = blockIdx.x * (apart_rows ? 1 : kLanes);
     const int b0 = p.b0 + (int(blockIdx.x) - row_ctas) * kMergeThreads;
-    bool off_duty = p.bad || live <= 0 || (row_part ? row0 >= live || p.coded == 0 : rg || b0 >= p.b0 + p.nb);
+    bool off_duty = p.bad || live <= 0 || (row_part ? row0 >= live : rg || b0 >= p.b0 + p.nb);
     long W = 0, before = 0;                                          // the work in all, and that of the sequences before s
     if (a.share && !off_duty) {
         off_duty = a.c.sealed[(size_t)s * a.c.n_kv] != sealed;
@@ -1350,23 +1293,22 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
         }
         block_sums(W, before, sums);
     }
-    // the parts: the tail's, then those of the splits or of the CTAs that took some of the unit's blocks
+    // the parts: those of the unit's CTAs
     const size_t unit = ((size_t)s * a.c.n_kv + h) * a.groups + rg;
-    int first = 0, parts = 1 + splits_of<AttnShape<HD, NT>::kWarps>(a.splits, p.coded);
-    bool whole = parts == 2 && !a.apart;
+    const int nsplit = splits_of<AttnShape<HD, NT>::kWarps>(a.splits, p.coded);
+    int first = 0, parts = a.apart + (a.apart ? nsplit : max(nsplit, 1));
     if (a.share && !off_duty) {
         const int G = shares_of<AttnShape<HD, NT>::kWarps>(a, W);
         const long start = before + (long)(h * p.groups + rg) * (p.coded + kTailWeight);
         first = int(cta_of(start, W, G));
-        parts = p.coded ? 2 + int(cta_of(start + p.coded - 1, W, G)) - first : 1;
-        whole = p.coded && cta_of(start + p.coded, W, G) == first;
+        parts = 1 + int(cta_of(start + p.coded, W, G)) - first;
     }
     pdl_wait();   // by every CTA, so that this grid does not end before the one it follows
-    if (off_duty || (whole && row_part)) return;                     // a whole unit's CTA has written it
+    if (off_duty || (parts == 1 && row_part)) return;                // one CTA had the whole unit and has written it
     const size_t part1 = part_of(a, unit, first);
-    auto id = [&](int i) { return i == 0 ? unit : part1 + i - 1; };
+    auto id = [&](int i) { return part1 + i; };
     int bad = 0;
-    for (int i = 1 + tid; i < parts; i += kMergeThreads) bad |= a.part_bad[id(i)];
+    for (int i = tid; i < parts; i += kMergeThreads) bad |= a.part_bad[id(i)];
     auto put = [&](int r, int d4, const float4 &sum, float total) {
         const int rid = rg * RG + r;
         *reinterpret_cast<float4 *>(a.out + ((size_t)s * a.rows + rid / per) * a.ldo + (size_t)(h * per + rid % per) * HD + 4 * d4) =
@@ -1408,16 +1350,14 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
         return;
     }
     if (__syncthreads_or(bad)) return;
-    // a warp's view of row r: the largest maximum and the sum, and each part's factor to f; a whole unit's coded part holds
-    // the sums of its tail too
+    // a warp's view of row r: the largest maximum and the sum, and each part's factor to f
     auto state = [&](int r, float &top, float &total, float *f) {
-        const int i1 = whole ? 1 : 0;
         top = -INFINITY;
-        for (int i = i1 + lane; i < parts; i += 32) top = fmaxf(top, a.part_ml[(id(i) * RG + r) * 2]);
+        for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_ml[(id(i) * RG + r) * 2]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         total = 0.f;
-        for (int i = i1 + lane; i < parts; i += 32) {
+        for (int i = lane; i < parts; i += 32) {
             const float2 y = *reinterpret_cast<const float2 *>(a.part_ml + (id(i) * RG + r) * 2);
             const float x = y.x == top ? 1.f : ex2(y.x - top);
             total = fmaf(y.y, x, total);
@@ -1460,9 +1400,9 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
     __syncthreads();
     const int b = b0 + tid;
     if (b < p.b0 + p.nb) {
-        const float *x = a.blk_lse + (((size_t)s * a.c.n_kv + h) * w.nb + b) * 16;
+        const float *x = a.blk_lse + (((size_t)s * a.c.n_kv + h) * w.nb + b) * 32;
         float sum = 0.f;
-        for (int r = 0; r < per; ++r) sum += ex2(x[r] - top_s[r]) / total_s[r];
+        for (int r = 0; r < per; ++r) sum += (ex2(x[r] - top_s[r]) + ex2(x[16 + r] - top_s[r])) / total_s[r];
         w.score[b] += sum;
     }
 }
@@ -1484,8 +1424,9 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
     t.nt = r > 8 ? 2 : 1;
     t.groups = (r + 8 * t.nt - 1) / (8 * t.nt);
     t.units = (size_t)c->n_seq * c->n_kv * t.groups;
-    const int warps = c->head_dim == 128 && t.nt == 2 ? AttnShape<128, 2>::kWarps : AttnShape<128, 1>::kWarps;
-    const int slots = c->head_dim == 256 ? kMaxCtas / 2 : kMaxCtas, blocks = window ? std::min(c->n_blocks, window / kBlk + 2) : c->n_blocks;
+    const bool wide = c->head_dim == 256 && t.nt == 2;
+    const int warps = wide ? AttnShape<256, 2>::kWarps : AttnShape<128, 1>::kWarps;
+    const int slots = 152 * (wide ? 1 : c->head_dim == 64 ? 3 : 2), blocks = window ? std::min(c->n_blocks, window / kBlk + 2) : c->n_blocks;
     t.splits = 1;
     if (t.units > (size_t)slots / 2) {
         t.share = 1;
@@ -1499,11 +1440,11 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
                 if (!best || cost < best) best = cost, t.splits = n, t.apart = apart;
             }
     }
-    const size_t parts = t.share ? 2 * t.units + t.ctas : t.units * (t.splits + 1);
+    const size_t parts = t.share ? t.units + t.ctas : t.units * (t.splits + t.apart);
     t.o_bytes = up256(parts * 8 * t.nt * c->head_dim * 4);
     t.ml_bytes = up256(parts * 8 * t.nt * 8);
     t.bad_bytes = up256(parts * 4);
-    t.lse_bytes = score ? up256((size_t)c->n_seq * c->n_kv * c->n_blocks * 64) : 0;
+    t.lse_bytes = score ? up256((size_t)c->n_seq * c->n_kv * c->n_blocks * 128) : 0;
     t.total = t.o_bytes + t.ml_bytes + t.bad_bytes + t.lse_bytes;
     return t;
 }
