@@ -473,17 +473,21 @@ constexpr float kTop = 7.f;    // log2 of the weight at a row's maximum
 
 template <int HD, int NT>
 struct AttnShape {
-    static constexpr int kUnit = 16 * HD;                            // bytes of a warp's keys, or values, of a pair of blocks
-    // Groups of four warps: 16 warps an SM of 128 registers a thread, in two CTAs where two rings fit beside the queries. Ring
-    // slots per warp: as many as fit, so that an SM has about 128 KB and more requested.
-    static constexpr int kCtas = HD == 256 && NT == 2 ? 1 : HD == 64 ? 3 : 2;
+    // Groups of four warps, 16 warps an SM of 128 registers a thread. A warp takes kM tiles of 16 keys at a time: two, which
+    // halves what a turn costs besides its products and the reads of the query halves, or one where the rings would not fit.
+    static constexpr int kM = HD == 256 ? 1 : 2;
+    static constexpr int kTurn = 2 * kM;                             // blocks that a group takes at a time
+    static constexpr int kUnit = 16 * kM * HD;                       // bytes of a warp's keys, or values, of a turn
+    static constexpr int kCtas = HD == 256 && NT == 2 ? 1 : 2;
     static constexpr int kGroups = HD == 256 && NT == 2 ? 4 : 2;
     static constexpr int kWarps = 4 * kGroups;
-    static constexpr int kRing = HD == 256 ? 3 : HD == 128 ? 5 : 6;
+    static constexpr int kRing = (HD == 64 ? 5 : 3) - (HD < 256 && NT == 2 ? 1 : 0);   // units under way, as many as two CTAs have room for
     static constexpr int kQBytes = NT * 8 * HD * 4;                  // query halves
-    static constexpr int kPBytes = kGroups * 4 * NT * 512;           // a pair's weights, for each group
+    static constexpr int kPBytes = kGroups * 2 * kTurn * NT * 512;   // a turn's weights, for each group
     static constexpr int kSmem = kQBytes + kPBytes + kWarps * kRing * kUnit;
-    static_assert(kGroups * 8 * NT * (HD + 4) * 4 <= kSmem && 3 * NT * 1024 <= 4 * kRing * kUnit, "the merge's and the tail's use of the shared memory");
+    static_assert(kGroups * 8 * NT * (HD + 4) * 4 <= kSmem, "the merge's use of the shared memory");
+    static constexpr int kTailPitch = kTail + 4;                     // of the tail's weights [rows][48 tokens], fp32
+    static_assert(kTail * HD * 4 <= 4 * kRing * kUnit && 8 * NT * kTailPitch * 4 <= kPBytes / kGroups, "the tail's: keys or values in a group's rings");
 };
 
 // the four warps of a group: a barrier, and one that also tells whether x holds anywhere in the group
@@ -564,7 +568,7 @@ __device__ __forceinline__ float group_sum(float x) {
 template <int N>
 __device__ __forceinline__ void cp_async_wait_groups() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// the splits that coded blocks are worth: at least two pairs a group
+// the splits that coded blocks are worth: a turn or two a group
 template <int W>
 __device__ __forceinline__ int splits_of(int splits, int coded) { return min(splits, (coded + W - 1) / W); }
 
@@ -615,30 +619,31 @@ struct QueryRows {      // a warp takes every kWarps-th row of the group
 };
 
 // One CTA's piece of a unit: 8 NT query rows (row r = m * group + i of the head's rows), its coded blocks and perhaps the
-// tail. Groups of four warps take every kGroups-th pair of blocks, each group with a running softmax of its own, merged at
-// the end. Of a pair each warp takes 16 keys for the first product and, for the second, a quarter of the value channels over
-// all 64 keys; the weights pass through shared memory between them. So a warp's sums are small, its code is short (a short
+// tail. Groups of four warps take every kGroups-th turn of blocks, each group with a running softmax of its own, merged at
+// the end. In a turn of two or four blocks each warp takes a quarter of the keys for the first product and, for the second,
+// a quarter of the value channels over all keys; the weights pass through shared memory between them. So a warp's sums are small, its code is short (a short
 // call spends much of its time on fetching code), and each code is read from shared memory and expanded once in the CTA.
 // Keys and values come through a ring of the warp's own (16-byte asynchronous copies): what a warp copies only it reads.
 template <int HD, int NT>
 __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, const Piece &u, QueryRows<HD, NT> &qr, uint8_t *smem, AttnShared<HD, NT> &sh) {
     using S = AttnShape<HD, NT>;
-    constexpr int RG = 8 * NT, kW = S::kWarps, kG = S::kGroups, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4, kMt = HD / 64;
+    constexpr int RG = 8 * NT, kW = S::kWarps, kG = S::kGroups, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4, kMt = HD / 64, kM = S::kM, kTurn = S::kTurn, kWin = 32 / kTurn;
     const int s = u.s, h = u.h, rg = u.rg;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int grp = warp >> 2, wq = warp & 3, key_half = wq & 1;     // first product: block wq / 2 of the pair, keys with bit 2 = key_half
+    // first product: block `mine` of the turn, all its keys (kM = 2) or those with bit 2 = key_half
+    const int grp = warp >> 2, wq = warp & 3, mine = kM == 2 ? wq : wq >> 1, key_half = kM == 2 ? 0 : wq & 1;
     const size_t head = (size_t)s * a.c.n_kv + h, head_blocks = head * a.c.n_blocks;
     const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG;    // rows of this group that exist
-    const int n = u.x1 - u.x0, first = p.b0 + u.x0 + 2 * grp;        // coded blocks; pair i of this group begins with first + 2 kG i
-    const int pairs = (n - 2 * grp + 2 * kG - 1) / (2 * kG);         // <= 0: none
+    const int n = u.x1 - u.x0, first = p.b0 + u.x0 + kTurn * grp;    // coded blocks; turn i of this group begins with first + kTurn kG i
+    const int turns = (n - kTurn * grp + kTurn * kG - 1) / (kTurn * kG);   // <= 0: none
     uint8_t *ring = smem + S::kQBytes + S::kPBytes + warp * kRing * kUnit;
     uint4 *pbuf = reinterpret_cast<uint4 *>(smem + S::kQBytes + grp * (S::kPBytes / kG)) + lane;
     const uint4 *qf = reinterpret_cast<const uint4 *>(smem) + lane;
     const bool keep_lse = a.score && rg == 0;
 
     int bad = 0;
-    auto load_phys = [&](int i0) {                                   // lane l: where block l % 2 of pair i0 + l / 2 is stored
-        const int b = first + 2 * kG * (i0 + (lane >> 1)) + (lane & 1);
+    auto load_phys = [&](int i0) {                                   // lane l: where block l % kTurn of turn i0 + l / kTurn is stored
+        const int b = first + kTurn * kG * (i0 + lane / kTurn) + lane % kTurn;
         int at = 0;
         if (b < p.b0 + u.x1) {
             at = a.c.table[head_blocks + b];
@@ -646,36 +651,43 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         }
         return at;
     };
-    int phys = load_phys(0), phys_next = load_phys(16);              // of the 16 pairs that are being asked for, and the next
+    int phys = load_phys(0), phys_next = load_phys(kWin);            // of the kWin turns that are being asked for, and the next
     float ks = a.c.k_scale[head_blocks + phys], vs = a.c.v_scale[head_blocks + phys], ks_next = 0.f, vs_next = 0.f;
 
-    // unit 2 i is pair i's keys (of this warp), unit 2 i + 1 its values (of this warp's channels)
+    // unit 2 i is turn i's keys (of this warp), unit 2 i + 1 its values (of this warp's channels)
     uint8_t *put = ring;                                             // the slot that the next unit goes to
     const uint8_t *take = ring;                                      // the slot that is read next
     auto issue = [&](int v) {
         const int i = v >> 1;
-        if (i < pairs) {
-            if ((v & 31) == 0 && v > 0) {
+        if (i < turns) {
+            if (v % (2 * kWin) == 0 && v > 0) {
                 phys = phys_next;
-                phys_next = load_phys(i + 16);
+                phys_next = load_phys(i + kWin);
             }
-            const int two = 2 * (i & 15), left = n - 2 * grp - 2 * kG * i;   // blocks of the pair: one, or two
+            const int lane0 = kTurn * (i % kWin), left = n - kTurn * (grp + kG * i);   // blocks of the turn: up to kTurn
             if (v & 1) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const size_t off = (head_blocks + __shfl_sync(0xffffffffu, phys, two + j)) * (kBlk * HD) + wq * (8 * HD) + 16 * lane;
+                for (int j = 0; j < kTurn; ++j) {
+                    const size_t off = (head_blocks + __shfl_sync(0xffffffffu, phys, lane0 + j)) * (kBlk * HD) + wq * (8 * HD) + 16 * lane;
                     if (j < left)
 #pragma unroll
                         for (int k = 0; k < HD / 64; ++k) cp_async16(put + j * (8 * HD) + 512 * k + 16 * lane, a.c.v + off + 512 * k);
                 }
             } else {
-                const size_t off = (head_blocks + __shfl_sync(0xffffffffu, phys, two + (wq >> 1))) * (kBlk * HD) + key_half * 256 + (lane >> 4) * 512 + (lane & 15) * 16;
-                if ((wq >> 1) < left)
+                const size_t off = (head_blocks + __shfl_sync(0xffffffffu, phys, lane0 + mine)) * (kBlk * HD);
+                if (mine < left) {
+                    if (kM == 2) {
 #pragma unroll
-                    for (int c = 0; c < HD / 64; ++c) {
-                        cp_async16(put + c * 1024 + 16 * lane, a.c.k + off + c * 2048);
-                        cp_async16(put + c * 1024 + 512 + 16 * lane, a.c.k + off + c * 2048 + 1024);
+                        for (int k = 0; k < HD / 16; ++k) cp_async16(put + 512 * k + 16 * lane, a.c.k + off + 512 * k + 16 * lane);
+                    } else {
+                        const uint8_t *src = a.c.k + off + key_half * 256 + (lane >> 4) * 512 + (lane & 15) * 16;
+#pragma unroll
+                        for (int c = 0; c < HD / 64; ++c) {
+                            cp_async16(put + c * 1024 + 16 * lane, src + c * 2048);
+                            cp_async16(put + c * 1024 + 512 + 16 * lane, src + c * 2048 + 1024);
+                        }
                     }
+                }
             }
             put = put == ring + (kRing - 1) * kUnit ? ring : put + kUnit;
         }
@@ -684,6 +696,24 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
     auto taken = [&]() { take = take == ring + (kRing - 1) * kUnit ? ring : take + kUnit; };
 #pragma unroll
     for (int v = 0; v < kRing; ++v) issue(v);
+
+    // The tail's rows, keys or values, into the first group's rings (by its 128 threads), 16 bytes at a time. The pieces of a key
+    // change places so that a warp's reads of it lie in different banks.
+    const int trows = p.L + p.n - kBlk * p.z;
+    float *tail_rows = reinterpret_cast<float *>(smem + S::kQBytes + S::kPBytes);
+    auto key_piece = [&](int key, int q) { return key * (HD / 4) + (q ^ ((q >> 3) & 1) ^ ((key & 1) << 1)); };
+    auto copy_tail = [&](bool values) {
+        const float *src = values ? a.c.v_tail + head * HD * kTail : a.c.k_tail + head * kTail * HD;
+        if (values) {
+            for (int e = tid; e < HD * (kTail / 4); e += 128)
+                if (4 * (e % (kTail / 4)) < trows) cp_async16(tail_rows + 4 * e, src + 4 * e);
+        } else {
+            for (int e = tid; e < trows * (HD / 4); e += 128) cp_async16(tail_rows + 4 * key_piece(e / (HD / 4), e % (HD / 4)), src + 4 * e);
+        }
+        cp_async_commit();
+    };
+    const bool tail_only = u.tail && n == 0;
+    if (tail_only && grp == 0) copy_tail(false);
 
     // ---- query rows into their fragments ----
     if (tid == 0) sh.bad = 0;
@@ -741,10 +771,14 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         for (int mt = 0; mt < kMt; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
     }
     // Renews mx by the logits y of the group (y == -inf: not seen), and rescales the sums. The four warps call it together.
-    auto renew = [&](const float (&y)[NT][4]) {
+    auto renew = [&](const float (&y)[kM][NT][4]) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float t0 = group_max(fmaxf(y[nt][0], y[nt][2])), t1 = group_max(fmaxf(y[nt][1], y[nt][3]));
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int m = 0; m < kM; ++m) t0 = fmaxf(t0, fmaxf(y[m][nt][0], y[m][nt][2])), t1 = fmaxf(t1, fmaxf(y[m][nt][1], y[m][nt][3]));
+            t0 = group_max(t0);
+            t1 = group_max(t1);
             if (g == 0) sh.top[grp][wq][8 * nt + 2 * t] = t0, sh.top[grp][wq][8 * nt + 2 * t + 1] = t1;
         }
         group_sync(grp);
@@ -767,11 +801,12 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
     };
 
     float v_ref = 0.f, v_lb = 0.f, v_inv = 1.f;
-    for (int i = 0; i < pairs; ++i) {
-        if ((i & 15) == 0) {                                         // the next 16 pairs' scales
+    for (int i = 0; i < turns; ++i) {
+        if (i % kWin == 0) {                                         // the next kWin turns' scales
             if (i > 0) ks = ks_next, vs = vs_next;
-            const bool is = first + 2 * kG * (i + (lane >> 1)) + (lane & 1) < p.b0 + u.x1;
-            float top = !is || isnan(vs) ? 0.f : vs;
+            const bool is = first + kTurn * kG * (i + lane / kTurn) + lane % kTurn < p.b0 + u.x1;
+            if (!is) ks = vs = 0.f;                                  // what is read in place of a block that is not there
+            float top = isnan(vs) ? 0.f : vs;
 #pragma unroll
             for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
             if (top > v_ref) {
@@ -789,27 +824,28 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             v_lb = log2f(r);
             v_inv = isnan(vs) ? vs : 1.f / r;
         }
-        if ((i & 15) == 8) {                                         // the next window's, half a window ahead
+        if (i % kWin == kWin / 2) {                                  // the next window's, half a window ahead
             ks_next = a.c.k_scale[head_blocks + phys_next];
             vs_next = a.c.v_scale[head_blocks + phys_next];
         }
-        const int from = 2 * (i & 15) + (wq >> 1), b = first + 2 * kG * i + (wq >> 1);   // this warp's block of the pair
+        const int from = kTurn * (i % kWin) + mine, b = first + kTurn * kG * i + mine;   // this warp's block of the turn
         const float bks = __shfl_sync(0xffffffffu, ks, from), blb = __shfl_sync(0xffffffffu, v_lb, from);
         float binv = __shfl_sync(0xffffffffu, v_inv, from);
         const bool there = b < p.b0 + u.x1;
         cp_async_wait_groups<kRing - 1>();
         __syncwarp();
-        float x[NT][4], xl[NT][4];                                   // by the query's hi and lo halves
+        // consecutive products go to at least four sums: the query's halves have sums of their own where tiles and rows give fewer
+        constexpr int kParts = kM * NT < 4 ? 2 : 1;
+        float xs[kParts][kM][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[nt][k] = xl[nt][k] = 0.f;
-        const uint8_t *K = take + (4 * (g >> 1) + (g & 1)) * 64 + 16 * t;
+        for (int k = 0; k < kParts * kM * NT * 4; ++k) (&xs[0][0][0][0])[k] = 0.f;
+        float(&x)[kM][NT][4] = xs[0];
+        const uint8_t *K = take + (kM == 2 ? 8 * (g >> 1) + (g & 1) : 4 * (g >> 1) + (g & 1)) * 64 + 16 * t;
 #pragma unroll
         for (int c = 0; c < HD / 64; ++c) {
-            uint32_t k0[4], k1[4];
-            *reinterpret_cast<uint4 *>(k0) = *reinterpret_cast<const uint4 *>(K + c * 1024);
-            *reinterpret_cast<uint4 *>(k1) = *reinterpret_cast<const uint4 *>(K + c * 1024 + 128);
+            uint32_t kw[2 * kM][4];                                  // of matrix j: this thread's key of it, 128 bytes behind matrix j - 1's
+#pragma unroll
+            for (int j = 0; j < 2 * kM; ++j) *reinterpret_cast<uint4 *>(kw[j]) = *reinterpret_cast<const uint4 *>(K + c * (1024 * kM) + 128 * j);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t qh[NT][4], ql[NT][4];
@@ -821,29 +857,38 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
                     const int j = 2 * half + jj;
-                    const uint32_t af[4] = {codes_lo(k0[j]), codes_lo(k1[j]), codes_hi(k0[j]), codes_hi(k1[j])};
+                    uint32_t af[kM][4];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(x[nt], af, qh[nt][2 * jj], qh[nt][2 * jj + 1]);
-                        mma_f16(xl[nt], af, ql[nt][2 * jj], ql[nt][2 * jj + 1]);
+                    for (int m = 0; m < kM; ++m) {
+                        af[m][0] = codes_lo(kw[2 * m][j]), af[m][1] = codes_lo(kw[2 * m + 1][j]);
+                        af[m][2] = codes_hi(kw[2 * m][j]), af[m][3] = codes_hi(kw[2 * m + 1][j]);
                     }
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int m = 0; m < kM; ++m)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(xs[part % kParts][m][nt], af[m], part ? ql[nt][2 * jj] : qh[nt][2 * jj], part ? ql[nt][2 * jj + 1] : qh[nt][2 * jj + 1]);
                 }
             }
         }
         __syncwarp();
         taken();
         issue(2 * i + kRing);
-        float y[NT][4], peak = -INFINITY;                            // exponents of the weights
+        float y[kM][NT][4], peak = -INFINITY;                        // exponents of the weights
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float z = bks * (e ? scale_of(nt).y : scale_of(nt).x), less = blb + kTop - mx[nt][e];   // +inf before a row's first key
 #pragma unroll
-                for (int k = e; k < 4; k += 2) {
-                    x[nt][k] += xl[nt][k];
-                    y[nt][k] = fmaf(x[nt][k], z, less);
-                }
+                for (int m = 0; m < kM; ++m)
+#pragma unroll
+                    for (int k = e; k < 4; k += 2) {
+                        if (kParts == 2) x[m][nt][k] += xs[kParts - 1][m][nt][k];
+                        y[m][nt][k] = fmaf(x[m][nt][k], z, less);
+                    }
             }
         const int pos0 = kBlk * b;
         if (!there || pos0 < all_lo || pos0 + kBlk > all_hi) {
@@ -854,26 +899,34 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                     int lo, hi;
                     row_sees(nt, e, lo, hi);
 #pragma unroll
-                    for (int k = e; k < 4; k += 2) {
-                        const int pos = pos0 + 8 * (g >> 1) + 4 * key_half + 2 * (k >> 1) + (g & 1);
-                        if (!there || pos < lo || pos >= hi) y[nt][k] = -INFINITY;
-                    }
+                    for (int m = 0; m < kM; ++m)
+#pragma unroll
+                        for (int k = e; k < 4; k += 2) {
+                            const int pos = pos0 + 8 * (g >> 1) + 4 * (m + key_half) + 2 * (k >> 1) + (g & 1);
+                            if (!there || pos < lo || pos >= hi) y[m][nt][k] = -INFINITY;
+                        }
                 }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int m = 0; m < kM; ++m)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) peak = fmaxf(peak, y[nt][k]);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) peak = fmaxf(peak, y[m][nt][k]);
         if (group_or(grp, peak > 15.f)) {                            // seldom, once the maxima have been met
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int m = 0; m < kM; ++m)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[nt][k] = y[nt][k] == -INFINITY ? -INFINITY : x[nt][k] * (bks * (k & 1 ? scale_of(nt).y : scale_of(nt).x));
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[m][nt][k] = y[m][nt][k] == -INFINITY ? -INFINITY : x[m][nt][k] * (bks * (k & 1 ? scale_of(nt).y : scale_of(nt).x));
             renew(y);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int m = 0; m < kM; ++m)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[nt][k] += mx[nt][k & 1] == -INFINITY ? 0.f : blb + kTop - mx[nt][k & 1];
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[m][nt][k] += mx[nt][k & 1] == -INFINITY ? 0.f : blb + kTop - mx[nt][k & 1];
         }
         if (isnan(binv)) {                                           // rows that see the block are NaN, the others take nothing of it
             binv = 0.f;
@@ -889,27 +942,36 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[nt][k] = ex2(y[nt][k]);
+            for (int m = 0; m < kM; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[m][nt][k] = ex2(y[m][nt][k]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float sum = y[nt][e] + y[nt][2 + e];
+                float sum = y[0][nt][e] + y[0][nt][2 + e];
+                if (kM == 2) sum += y[kM - 1][nt][e] + y[kM - 1][nt][2 + e];
                 l[nt][e] = fmaf(sum, binv, l[nt][e]);
                 if (keep_lse) {
                     const float total = group_sum(sum) * binv;
                     const int r = 8 * nt + 2 * t + e;
-                    if (g == 0 && r < per && there) put_lse(b, key_half, r, total, mx[nt][e]);
+                    if (g == 0 && r < per && there) {
+                        put_lse(b, key_half, r, total, mx[nt][e]);
+                        if (kM == 2) put_lse(b, 1, r, 0.f, 0.f);     // the block's sum is one
+                    }
                 }
             }
-            uint4 w;                                                 // hi and lo halves of the step's two input pairs
-            halves2(y[nt][0], y[nt][1], w.x, w.z);
-            halves2(y[nt][2], y[nt][3], w.y, w.w);
-            pbuf[(wq * NT + nt) * 32] = make_uint4(transpose8x8(w.x), transpose8x8(w.y), transpose8x8(w.z), transpose8x8(w.w));
+#pragma unroll
+            for (int m = 0; m < kM; ++m) {
+                uint4 w;                                             // hi and lo halves of the step's two input pairs
+                halves2(y[m][nt][0], y[m][nt][1], w.x, w.z);
+                halves2(y[m][nt][2], y[m][nt][3], w.y, w.w);
+                pbuf[((kM * wq + m) * NT + nt) * 32] = make_uint4(transpose8x8(w.x), transpose8x8(w.y), transpose8x8(w.z), transpose8x8(w.w));
+            }
         }
         cp_async_wait_groups<kRing - 1>();
         group_sync(grp);
         const uint8_t *V = take + g * kBlk + 8 * t;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {                                // block of the pair
+        for (int j = 0; j < kTurn; ++j) {                            // block of the turn
             uint32_t af[kMt][2][4];
 #pragma unroll
             for (int mt = 0; mt < kMt; ++mt) {
@@ -935,7 +997,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         issue(2 * i + 1 + kRing);
     }
     cp_async_wait_groups<0>();
-    if (v_ref > 0.f || pairs > 0)
+    if (turns > 0)
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
@@ -948,8 +1010,13 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
     // weights as three bf16 parts (fp32's range, so that no token's size touches another's precision). A token that
     // holds an infinity or a NaN makes the rows that see it NaN; its own numbers enter as 0. ----
     if (u.tail && grp == 0) {
-        const int rows = p.L + p.n - kBlk * p.z, base = kBlk * p.z;
-        uint4 *tbuf = reinterpret_cast<uint4 *>(smem + S::kQBytes + S::kPBytes) + lane;   // the group's rings: [3 steps][NT][2] words of weights
+        const int base = kBlk * p.z;
+        if (!tail_only) {
+            group_sync(0);                                           // every warp is done with its ring
+            copy_tail(false);
+        }
+        cp_async_wait_groups<0>();
+        group_sync(0);
         float x[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -957,7 +1024,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             for (int k = 0; k < 4; ++k) x[nt][k] = 0.f;
         const int key0 = 16 * wq + 4 * (g >> 1) + (g & 1);           // and key0 + 2
         if (wq < 3) {
-            const float *K = a.c.k_tail + (head * kTail + key0) * HD + 16 * t;
+            const float4 *K = reinterpret_cast<const float4 *>(tail_rows);
 #pragma unroll 1
             for (int c = 0; c < HD / 64; ++c) {
                 float4 kr[2][4];
@@ -965,7 +1032,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) kr[m][j] = key0 + 2 * m < rows ? *reinterpret_cast<const float4 *>(K + 2 * m * HD + 64 * c + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int j = 0; j < 4; ++j) kr[m][j] = key0 + 2 * m < trows ? K[key_piece(key0 + 2 * m, 16 * c + 4 * t + j)] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     uint32_t top = 0;                                // magnitudes as bits: infinities and NaN come last
@@ -1008,7 +1075,12 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                     for (int k = 0; k < 4; ++k) x[nt][k] = fmaf(xc[nt][k], back[k >> 1], x[nt][k]);
             }
         }
-        float y[NT][4];
+        group_sync(0);                                               // the keys are read, and sh.top is free
+        copy_tail(true);
+        float y[kM][NT][4];
+        if (kM == 2)
+#pragma unroll
+            for (int k = 0; k < NT * 4; ++k) (&y[kM - 1][0][0])[k] = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1018,57 +1090,54 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
                 for (int k = e; k < 4; k += 2) {
                     const int pos = base + key0 + 2 * (k >> 1);
-                    y[nt][k] = wq == 3 || pos < lo || pos >= hi ? -INFINITY : x[nt][k] * (e ? scale_of(nt).y : scale_of(nt).x);
+                    y[0][nt][k] = wq == 3 || pos < lo || pos >= hi ? -INFINITY : x[nt][k] * (e ? scale_of(nt).y : scale_of(nt).x);
                 }
             }
-        group_sync(0);                                               // every warp is done with its ring, and with sh.top
         renew(y);
+        float *weight = reinterpret_cast<float *>(smem + S::kQBytes);   // [row][token], in the group's buffer
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float ref = mx[nt][e] == -INFINITY ? 0.f : mx[nt][e] - kTop;
-                y[nt][e] = ex2(y[nt][e] - ref);
-                y[nt][2 + e] = ex2(y[nt][2 + e] - ref);
-                const float sum = y[nt][e] + y[nt][2 + e];
+                const int r = 8 * nt + 2 * t + e;
+                y[0][nt][e] = ex2(y[0][nt][e] - ref);
+                y[0][nt][2 + e] = ex2(y[0][nt][2 + e] - ref);
+                const float sum = y[0][nt][e] + y[0][nt][2 + e];
                 l[nt][e] += sum;
                 if (keep_lse) {
                     const float total = group_sum(sum);
-                    const int r = 8 * nt + 2 * t + e, b = p.z + (wq >> 1);
+                    const int b = p.z + (wq >> 1);
                     if (g == 0 && r < per && b < p.b0 + p.nb) put_lse(b, wq & 1, r, total, mx[nt][e]);
                 }
+                if (wq < 3) weight[r * S::kTailPitch + key0] = y[0][nt][e], weight[r * S::kTailPitch + key0 + 2] = y[0][nt][2 + e];
             }
-            if (wq < 3) {
-                uint32_t w0[3], w1[3];
-                thirds2(y[nt][0], y[nt][1], w0);
-                thirds2(y[nt][2], y[nt][3], w1);
-                tbuf[((wq * NT + nt) * 2) * 32] = make_uint4(transpose8x8(w0[0]), transpose8x8(w1[0]), transpose8x8(w0[1]), transpose8x8(w1[1]));
-                tbuf[((wq * NT + nt) * 2 + 1) * 32] = make_uint4(transpose8x8(w0[2]), transpose8x8(w1[2]), 0, 0);
-            }
-        }
+        cp_async_wait_groups<0>();
         group_sync(0);
         uint32_t poison[2] = {0, 0};                                 // tokens whose values are not finite
-        const float *V = a.c.v_tail + (head * HD + wq * (HD / 4) + g) * kTail + 4 * t;
 #pragma unroll 1
         for (int st = 0; st < 3; ++st) {
-            if (16 * st >= rows) break;
-            float4 vr[kMt][2];
+            if (16 * st >= trows) break;
+            uint32_t wf[NT][2][3];
 #pragma unroll
-            for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    vr[mt][k] = 16 * st + 4 * t < rows ? *reinterpret_cast<const float4 *>(V + (16 * mt + 8 * k) * kTail + 16 * st) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int nt = 0; nt < NT; ++nt) {
+                const float4 y = *reinterpret_cast<const float4 *>(weight + (8 * nt + g) * S::kTailPitch + 16 * st + 4 * t);
+                thirds2(y.x, y.y, wf[nt][0]);
+                thirds2(y.z, y.w, wf[nt][1]);
+            }
 #pragma unroll
             for (int mt = 0; mt < kMt; ++mt) {
                 uint32_t af[3][4];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float v[4] = {vr[mt][k].x, vr[mt][k].y, vr[mt][k].z, vr[mt][k].w};
+                    const int key = 16 * st + 4 * t;
+                    float4 vr = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (key < trows) vr = *reinterpret_cast<const float4 *>(tail_rows + (wq * (HD / 4) + 16 * mt + g + 8 * k) * kTail + key);
+                    float v[4] = {vr.x, vr.y, vr.z, vr.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int key = 16 * st + 4 * t + e;
-                        if (key >= rows || !isfinite(v[e])) {
-                            if (key < rows) poison[key >> 5] |= 1u << (key & 31);
+                        if (key + e >= trows || !isfinite(v[e])) {
+                            if (key + e < trows) poison[(key + e) >> 5] |= 1u << ((key + e) & 31);
                             v[e] = 0.f;
                         }
                     }
@@ -1079,14 +1148,11 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                     for (int i = 0; i < 3; ++i) af[i][k] = y0[i], af[i][2 + k] = y1[i];
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 w01 = tbuf[((st * NT + nt) * 2) * 32], w2 = tbuf[((st * NT + nt) * 2 + 1) * 32];
-                    const uint32_t wf[3][2] = {{w01.x, w01.y}, {w01.z, w01.w}, {w2.x, w2.y}};
+                for (int i = 2; i >= 0; --i)                         // the small products first
 #pragma unroll
-                    for (int i = 2; i >= 0; --i)                     // the small products first
+                    for (int k = 2 - i; k >= 0; --k)
 #pragma unroll
-                        for (int k = 2 - i; k >= 0; --k) mma_bf16(o[mt][nt], af[i][0], af[i][1], af[i][2], af[i][3], wf[k][0], wf[k][1]);
-                }
+                        for (int nt = 0; nt < NT; ++nt) mma_bf16(o[mt][nt], af[i][0], af[i][1], af[i][2], af[i][3], wf[nt][0][k], wf[nt][1][k]);
             }
         }
         poison[0] = __reduce_or_sync(0xffffffffu, poison[0]);
@@ -1268,7 +1334,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
 // scores (grid x behind them, row group 0). HD / 4 threads take four channels each of a row; with `apart_rows` all threads of
 // a CTA take one row and share out its parts (few units of many parts), else each such group takes a row of its own.
 constexpr int kMergeThreads = 256;
-constexpr int kMaxCtas = 456;   // three for each SM
+constexpr int kMaxCtas = 304;   // two for each SM
 template <int HD, int NT>
 __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int row_ctas, int apart_rows) {
     constexpr int RG = 8 * NT, kLanes = kMergeThreads / (HD / 4), kSome = 4;
@@ -1426,7 +1492,7 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
     t.units = (size_t)c->n_seq * c->n_kv * t.groups;
     const bool wide = c->head_dim == 256 && t.nt == 2;
     const int warps = wide ? AttnShape<256, 2>::kWarps : AttnShape<128, 1>::kWarps;
-    const int slots = 152 * (wide ? 1 : c->head_dim == 64 ? 3 : 2), blocks = window ? std::min(c->n_blocks, window / kBlk + 2) : c->n_blocks;
+    const int slots = wide ? kMaxCtas / 2 : kMaxCtas, blocks = window ? std::min(c->n_blocks, window / kBlk + 2) : c->n_blocks;
     t.splits = 1;
     if (t.units > (size_t)slots / 2) {
         t.share = 1;
