@@ -481,6 +481,7 @@ struct AttnShape {
     static constexpr int kCtas = HD == 256 && NT == 2 ? 1 : 2;
     static constexpr int kGroups = HD == 256 && NT == 2 ? 4 : 2;
     static constexpr int kWarps = 4 * kGroups;
+    static constexpr int kStep = kGroups * kTurn;                    // blocks that a CTA takes at a time
     static constexpr int kRing = (HD == 64 ? 5 : 3) - (HD < 256 && NT == 2 ? 1 : 0);   // units under way, as many as two CTAs have room for
     static constexpr int kQBytes = NT * 8 * HD * 4;                  // query halves
     static constexpr int kPBytes = kGroups * 2 * kTurn * NT * 512;   // a turn's weights, for each group
@@ -568,7 +569,7 @@ __device__ __forceinline__ float group_sum(float x) {
 template <int N>
 __device__ __forceinline__ void cp_async_wait_groups() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// the splits that coded blocks are worth: a turn or two a group
+// the splits that coded blocks are worth: at least a turn each
 template <int W>
 __device__ __forceinline__ int splits_of(int splits, int coded) { return min(splits, (coded + W - 1) / W); }
 
@@ -1234,12 +1235,13 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 // Splits: grid (splits, heads x row groups, sequences).
 template <int HD, int NT>
 __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, NT>::kCtas) k_kv8_attn(AttnKvArgs a) {
-    constexpr int RG = 8 * NT, kW = AttnShape<HD, NT>::kWarps;
+    constexpr int RG = 8 * NT;
     extern __shared__ __align__(16) uint8_t kv_smem[];
     __shared__ AttnShared<HD, NT> sh;
     const int split = int(blockIdx.x) - a.apart;
     Piece u{int(blockIdx.z), int(blockIdx.y) / a.groups, int(blockIdx.y) % a.groups};
     QueryRows<HD, NT> q;
+    pdl_wait();
     q.load(a, u.s, u.h, u.rg);
     const Span p = span_of(a, u.s, a.c.sealed[(size_t)u.s * a.c.n_kv + u.h], RG);
     pdl_trigger();
@@ -1247,7 +1249,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(a.c.err, p.bad);
         return;
     }
-    const int nsplit = splits_of<kW>(a.splits, p.coded);
+    const int nsplit = splits_of<AttnShape<HD, NT>::kStep>(a.splits, p.coded);
     u.tail = a.apart ? split < 0 : split == max(nsplit - 1, 0);
     if (u.rg >= p.groups || (split >= nsplit && !u.tail)) return;
     const bool codes = split >= 0 && split < nsplit;
@@ -1267,6 +1269,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     __shared__ long sm_sums[kW][2], sm_off;
     __shared__ int sm_seq;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+    pdl_wait();
     pdl_trigger();
     // the work in all, this CTA's share of it, and the sequence that the share begins in
     long work = 0, none = 0;
@@ -1276,7 +1279,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         work += weight_of(a, p);
     }
     block_sums(work, none, sm_sums);
-    const int G = shares_of<kW>(a, work);
+    const int G = shares_of<AttnShape<HD, NT>::kStep>(a, work);
     if (cta >= G) return;
     long pos = work * cta / G, off = 0;
     const long pos_end = work * (cta + 1) / G;
@@ -1343,6 +1346,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
     __shared__ long sums[kMergeThreads / 32][2];
     const int h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
     const bool row_part = int(blockIdx.x) < row_ctas;
+    pdl_trigger();
     const KvView w = view(a.c, s, h);
     const int sealed = *w.sealed;
     const Span p = span_of(a, s, sealed, RG);
@@ -1361,10 +1365,10 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
     }
     // the parts: those of the unit's CTAs
     const size_t unit = ((size_t)s * a.c.n_kv + h) * a.groups + rg;
-    const int nsplit = splits_of<AttnShape<HD, NT>::kWarps>(a.splits, p.coded);
+    const int nsplit = splits_of<AttnShape<HD, NT>::kStep>(a.splits, p.coded);
     int first = 0, parts = a.apart + (a.apart ? nsplit : max(nsplit, 1));
     if (a.share && !off_duty) {
-        const int G = shares_of<AttnShape<HD, NT>::kWarps>(a, W);
+        const int G = shares_of<AttnShape<HD, NT>::kStep>(a, W);
         const long start = before + (long)(h * p.groups + rg) * (p.coded + kTailWeight);
         first = int(cta_of(start, W, G));
         parts = 1 + int(cta_of(start + p.coded, W, G)) - first;
@@ -1415,38 +1419,53 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
         put(r, d4, sum, total);
         return;
     }
-    if (__syncthreads_or(bad)) return;
-    // a warp's view of row r: the largest maximum and the sum, and each part's factor to f
-    auto state = [&](int r, float &top, float &total, float *f) {
-        top = -INFINITY;
-        for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_ml[(id(i) * RG + r) * 2]);
+    // A warp's view of row r: the largest maximum and the sum, and each part's factor to f. `some` holds the first 128 parts'
+    // states, four a lane, asked for before.
+    struct Some {
+        float2 v[4];
+    };
+    auto ask = [&](int r) {
+        Some x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x.v[k] = lane + 32 * k < parts ? *reinterpret_cast<const float2 *>(a.part_ml + (id(lane + 32 * k) * RG + r) * 2) : make_float2(-INFINITY, 0.f);
+        return x;
+    };
+    auto state = [&](int r, const Some &some, float &top, float &total, float *f) {
+        top = fmaxf(fmaxf(some.v[0].x, some.v[1].x), fmaxf(some.v[2].x, some.v[3].x));
+        for (int i = 128 + lane; i < parts; i += 32) top = fmaxf(top, a.part_ml[(id(i) * RG + r) * 2]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         total = 0.f;
-        for (int i = lane; i < parts; i += 32) {
-            const float2 y = *reinterpret_cast<const float2 *>(a.part_ml + (id(i) * RG + r) * 2);
+        auto take = [&](int i, const float2 &y) {
             const float x = y.x == top ? 1.f : ex2(y.x - top);
             total = fmaf(y.y, x, total);
             if (f) f[i] = x;
-        }
+        };
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (lane + 32 * k < parts) take(lane + 32 * k, some.v[k]);
+        for (int i = 128 + lane; i < parts; i += 32) take(i, *reinterpret_cast<const float2 *>(a.part_ml + (id(i) * RG + r) * 2));
         total = warp_sum(total);
     };
     float top, total;
     if (row_part) {
-        float4 y[kSome], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kMany = 8;
+        float4 y[kMany], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        const Some some = ask(row0);
 #pragma unroll
-        for (int k = 0; k < kSome; ++k)                              // on their way while the factors are found
+        for (int k = 0; k < kMany; ++k)                              // on their way while the factors are found
             if (i0 + k * kLanes < parts) y[k] = *reinterpret_cast<const float4 *>(a.part_o + (id(i0 + k * kLanes) * RG + row0) * HD + 4 * d4);
+        if (__syncthreads_or(bad)) return;
         if (tid < 32) {
-            state(row0, top, total, fac);
+            state(row0, some, top, total, fac);
             if (lane == 0) total_s[0] = total;
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kSome; ++k)
+        for (int k = 0; k < kMany; ++k)
             if (i0 + k * kLanes < parts) add(sum, y[k], fac[i0 + k * kLanes]);
 #pragma unroll 4
-        for (int i = i0 + kSome * kLanes; i < parts; i += kLanes) add(sum, *reinterpret_cast<const float4 *>(a.part_o + (id(i) * RG + row0) * HD + 4 * d4), fac[i]);
+        for (int i = i0 + kMany * kLanes; i < parts; i += kLanes) add(sum, *reinterpret_cast<const float4 *>(a.part_o + (id(i) * RG + row0) * HD + 4 * d4), fac[i]);
         acc[i0][d4] = sum;
         __syncthreads();
         if (i0 == 0) {
@@ -1459,25 +1478,37 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
         }
         return;
     }
+    const int b = b0 + tid;
+    float4 lse[2][4];                                                // of the halves, for up to 16 rows
+    const bool on = b < p.b0 + p.nb;
+    const float4 *x = reinterpret_cast<const float4 *>(a.blk_lse + (((size_t)s * a.c.n_kv + h) * w.nb + (on ? b : b0)) * 32);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * i < per) lse[k][i] = x[4 * k + i];
+    const float old = on ? w.score[b] : 0.f;
     for (int r = tid >> 5; r < per; r += kMergeThreads / 32) {
-        state(r, top, total, nullptr);
+        state(r, ask(r), top, total, nullptr);
         if (lane == 0) top_s[r] = top - kTop, total_s[r] = total;
     }
-    __syncthreads();
-    const int b = b0 + tid;
-    if (b < p.b0 + p.nb) {
-        const float *x = a.blk_lse + (((size_t)s * a.c.n_kv + h) * w.nb + b) * 32;
-        float sum = 0.f;
-        for (int r = 0; r < per; ++r) sum += (ex2(x[r] - top_s[r]) + ex2(x[16 + r] - top_s[r])) / total_s[r];
-        w.score[b] += sum;
+    if (__syncthreads_or(bad) || !on) return;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float v[2][4] = {{lse[0][i].x, lse[0][i].y, lse[0][i].z, lse[0][i].w}, {lse[1][i].x, lse[1][i].y, lse[1][i].z, lse[1][i].w}};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (4 * i + k < per) sum += (ex2(v[0][k] - top_s[4 * i + k]) + ex2(v[1][k] - top_s[4 * i + k])) / total_s[4 * i + k];
     }
+    w.score[b] = old + sum;
 }
 
 // ---- host side ----
 // How a call's work is cut: row groups of 8 rows, or of 16 (whose codes are expanded once for two products) where a head
 // has more than 8. Up to as many units as half the CTAs that fit the part's 152 SMs at once: splits of a unit's blocks, and
 // a CTA of its own for the tail or not; all in one wave (CTAs of a second one were measured to wait for tens of microseconds
-// although slots were free). Costs are in blocks a warp; a tail inside a CTA is worth about 3. More units: shares.
+// although slots were free). Costs are in turns; a tail inside a CTA is worth about 2. More units: shares.
 struct AttnCut {
     int nt, groups, splits, apart, share, ctas;
     size_t units, o_bytes, ml_bytes, bad_bytes, lse_bytes, total;
@@ -1491,18 +1522,18 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
     t.groups = (r + 8 * t.nt - 1) / (8 * t.nt);
     t.units = (size_t)c->n_seq * c->n_kv * t.groups;
     const bool wide = c->head_dim == 256 && t.nt == 2;
-    const int warps = wide ? AttnShape<256, 2>::kWarps : AttnShape<128, 1>::kWarps;
+    const int step = wide ? AttnShape<256, 2>::kStep : c->head_dim == 256 ? AttnShape<256, 1>::kStep : AttnShape<128, 1>::kStep;
     const int slots = wide ? kMaxCtas / 2 : kMaxCtas, blocks = window ? std::min(c->n_blocks, window / kBlk + 2) : c->n_blocks;
     t.splits = 1;
     if (t.units > (size_t)slots / 2) {
         t.share = 1;
         t.ctas = slots;
     } else {
-        const int most = std::min(kMaxSplits, (blocks + warps - 1) / warps);
+        const int most = std::min(kMaxSplits, (blocks + step - 1) / step);
         int best = 0;
         for (int apart = 0; apart < 2; ++apart)
             for (int n = 1; n <= most && t.units * (n + apart) <= (size_t)slots; ++n) {
-                const int cost = (blocks + warps * n - 1) / (warps * n) + (apart ? 0 : 3);
+                const int cost = (blocks + step * n - 1) / (step * n) + (apart ? 0 : 2);
                 if (!best || cost < best) best = cost, t.splits = n, t.apart = apart;
             }
     }
@@ -1529,10 +1560,10 @@ cudaError_t launch_kv8_attn(const AttnKvArgs &a, cudaStream_t s) {
     }
     const unsigned heads = unsigned(a.c.n_kv * a.groups);
     if (a.share)
-        k_kv8_attn_share<HD, NT><<<a.ctas, threads, smem, s>>>(a);
+        e = launch_pdl(k_kv8_attn_share<HD, NT>, dim3(a.ctas), dim3(threads), smem, s, a);
     else
-        k_kv8_attn<HD, NT><<<dim3(a.splits + a.apart, heads, a.c.n_seq), threads, smem, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_pdl(k_kv8_attn<HD, NT>, dim3(a.splits + a.apart, heads, a.c.n_seq), dim3(threads), smem, s, a);
+    if (e != cudaSuccess) return e;
     if (!a.share && a.splits == 1 && !a.apart && !a.score) return cudaSuccess;   // every unit is one CTA's
     const int apart_rows = !a.share && a.splits > 8, lanes = kMergeThreads / (HD / 4);
     const int row_ctas = apart_rows ? 8 * NT : (8 * NT + lanes - 1) / lanes;
