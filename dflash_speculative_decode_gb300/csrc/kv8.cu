@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a) {
     __shared__ Turn turn;
     const int h = blockIdx.x, s = blockIdx.y;
     const KvView w = view(a.c, s, h);
+    pdl_wait();
     Plan p = plan_of(a, s, w);
     if (!p.bad && bad_table(w, p)) p.bad = kErrTable;
     if (p.bad) {
@@ -302,6 +303,7 @@ __global__ void __launch_bounds__(kWriteThreads, 4) k_kv8_append(WriteArgs a) {
     __shared__ Turn turn;
     const int b = blockIdx.x >> 1, h = blockIdx.y, s = blockIdx.z;
     const KvView w = view(a.c, s, h);
+    pdl_wait();
     const Plan p = plan_of(a, s, w);
     pdl_trigger();
     if (p.bad || (b > 0 && b >= p.full) || (p.cut && b == 0 && bad_table(w, p))) return;   // a cut reads through the entry
@@ -337,6 +339,7 @@ __global__ void __launch_bounds__(256) k_kv8_read(ReadArgs a) {
     __shared__ uint32_t vcode[256 * 9];
     const int h = blockIdx.y, s = blockIdx.z, hd = a.c.head_dim;
     const KvView w = view(a.c, s, h);
+    pdl_wait();
     const int L = a.len[s], first = a.first ? a.first[s] : 0, z = *w.sealed;
     int bad = 0;
     if (z < 0 || z > w.nb)
@@ -971,27 +974,39 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         cp_async_wait_groups<kRing - 1>();
         group_sync(grp);
         const uint8_t *V = take + g * kBlk + 8 * t;
+        // the turn's products have sums of their own, added to the running ones in fp32: the tensor cores cut off what they add
+        // below the last place, which over a long context would add up (8e-6 against 3e-6 at 4096 tokens a group)
+        constexpr int kMs = kMt < 2 ? kMt : 2;                       // channel tiles at once
 #pragma unroll
-        for (int j = 0; j < kTurn; ++j) {                            // block of the turn
-            uint32_t af[kMt][2][4];
+        for (int m0 = 0; m0 < kMt; m0 += kMs) {
+            float d[kMs][NT][4];
 #pragma unroll
-            for (int mt = 0; mt < kMt; ++mt) {
-                const uint2 v0 = *reinterpret_cast<const uint2 *>(V + j * (8 * HD) + (16 * mt) * kBlk), v1 = *reinterpret_cast<const uint2 *>(V + j * (8 * HD) + (16 * mt + 8) * kBlk);
-                af[mt][0][0] = codes_lo(v0.x), af[mt][0][1] = codes_lo(v1.x), af[mt][0][2] = codes_hi(v0.x), af[mt][0][3] = codes_hi(v1.x);
-                af[mt][1][0] = codes_lo(v0.y), af[mt][1][1] = codes_lo(v1.y), af[mt][1][2] = codes_hi(v0.y), af[mt][1][3] = codes_hi(v1.y);
+            for (int k = 0; k < kMs * NT * 4; ++k) (&d[0][0][0])[k] = 0.f;
+#pragma unroll
+            for (int j = 0; j < kTurn; ++j) {                        // block of the turn
+                uint32_t af[kMs][2][4];
+#pragma unroll
+                for (int m = 0; m < kMs; ++m) {
+                    const uint8_t *from = V + j * (8 * HD) + 16 * (m0 + m) * kBlk;
+                    const uint2 v0 = *reinterpret_cast<const uint2 *>(from), v1 = *reinterpret_cast<const uint2 *>(from + 8 * kBlk);
+                    af[m][0][0] = codes_lo(v0.x), af[m][0][1] = codes_lo(v1.x), af[m][0][2] = codes_hi(v0.x), af[m][0][3] = codes_hi(v1.x);
+                    af[m][1][0] = codes_lo(v0.y), af[m][1][1] = codes_lo(v1.y), af[m][1][2] = codes_hi(v0.y), af[m][1][3] = codes_hi(v1.y);
+                }
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                    uint4 w[NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) w[nt] = pbuf[((2 * j + st) * NT + nt) * 32];
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int m = 0; m < kMs; ++m)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma_f16(d[m][nt], af[m][st], part ? w[nt].z : w[nt].x, part ? w[nt].w : w[nt].y);
+                }
             }
 #pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                uint4 w[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) w[nt] = pbuf[((2 * j + st) * NT + nt) * 32];
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_f16(o[mt][nt], af[mt][st], part ? w[nt].z : w[nt].x, part ? w[nt].w : w[nt].y);
-            }
+            for (int k = 0; k < kMs * NT * 4; ++k) (&o[m0][0][0])[k] += (&d[0][0][0])[k];
         }
         __syncwarp();
         taken();
@@ -1346,7 +1361,6 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
     __shared__ long sums[kMergeThreads / 32][2];
     const int h = blockIdx.y / a.groups, rg = blockIdx.y % a.groups, s = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
     const bool row_part = int(blockIdx.x) < row_ctas;
-    pdl_trigger();
     const KvView w = view(a.c, s, h);
     const int sealed = *w.sealed;
     const Span p = span_of(a, s, sealed, RG);
@@ -1619,6 +1633,7 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_evict(EvictArgs a) {
     const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
     const KvView w = view(a.c, s, h);
     const size_t base = ((size_t)s * a.c.n_kv + h) * w.nb;
+    pdl_wait();
     const int n = *w.sealed;
     if (n < 0 || n > w.nb) {
         if (tid == 0) atomicOr(a.c.err, kErrTable);
@@ -1723,7 +1738,7 @@ int check_rows(const dfl_kv8 *c, const void *p, int64_t ld, int heads) {
     return p && aligned16(p) && ld % 4 == 0 && ld >= (int64_t)heads * c->head_dim ? DFL_OK : DFL_E_INVALID_ARG;
 }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? DFL_OK : DFL_E_CUDA; }
+int launched(cudaError_t e) { return e == cudaSuccess ? DFL_OK : DFL_E_CUDA; }
 
 int write_rows(const dfl_kv8 *c, const int32_t *len, const int32_t *cnt, int rows, const float *k, const float *v, int64_t ld,
                int commit, cudaStream_t s) {
@@ -1737,13 +1752,10 @@ int write_rows(const dfl_kv8 *c, const int32_t *len, const int32_t *cnt, int row
     // Up to 64 rows complete three blocks at most: one launch. More rows take a launch with a CTA for each block and a short
     // one behind it: at 1024 rows of 8 heads of 128 they take 8 us, one CTA a head alone 260 us.
     if (!commit || rows <= 64) {
-        k_kv8_write<<<dim3(c->n_kv, c->n_seq), kWriteThreads, 0, s>>>(a);
-        return launched();
+        return launched(launch_pdl(k_kv8_write, dim3(c->n_kv, c->n_seq), dim3(kWriteThreads), 0, s, a));
     }
-    k_kv8_append<<<dim3(2 * ((kTail + rows) / kBlk), c->n_kv, c->n_seq), kWriteThreads, 0, s>>>(a);
-    const int l = launched();
-    if (l) return l;
-    return launch_pdl(k_kv8_count, dim3(c->n_kv, c->n_seq), dim3(64), 0, s, a) == cudaSuccess ? DFL_OK : DFL_E_CUDA;
+    const int l = launched(launch_pdl(k_kv8_append, dim3(2 * ((kTail + rows) / kBlk), c->n_kv, c->n_seq), dim3(kWriteThreads), 0, s, a));
+    return l ? l : launched(launch_pdl(k_kv8_count, dim3(c->n_kv, c->n_seq), dim3(64), 0, s, a));
 }
 
 }  // namespace
@@ -1758,7 +1770,7 @@ int dfl_kv8_init(const dfl_kv8 *c, void *stream) {
     if (rc) return rc;
     const size_t n = (size_t)c->n_seq * c->n_kv * c->n_blocks;
     k_kv8_init<<<unsigned(std::min<size_t>((n + 255) / 256, 1024)), 256, 0, static_cast<cudaStream_t>(stream)>>>(*c);
-    return launched();
+    return launched(cudaGetLastError());
 }
 
 int dfl_kv8_status(const dfl_kv8 *c, void *stream) {
@@ -1827,8 +1839,7 @@ int dfl_kv8_evict(const dfl_kv8 *c, const int32_t *len, int keep, int sink, int 
         return DFL_E_INVALID_ARG;
     if (table_out == c->table || score_out == c->score || sealed_out == c->sealed || len_out == len) return DFL_E_INVALID_ARG;
     EvictArgs a{*c, len, keep, sink, recent, table_out, score_out, sealed_out, len_out};
-    k_kv8_evict<<<dim3(c->n_kv, c->n_seq), kEvictThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launched();
+    return launched(launch_pdl(k_kv8_evict, dim3(c->n_kv, c->n_seq), dim3(kEvictThreads), 0, static_cast<cudaStream_t>(stream), a));
 }
 
 int dfl_kv8_read(const dfl_kv8 *c, const int32_t *len, const int32_t *first, int rows, float *k_out, float *v_out, void *stream) {
@@ -1837,8 +1848,7 @@ int dfl_kv8_read(const dfl_kv8 *c, const int32_t *len, const int32_t *first, int
     if (!len || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) || rows < 1) return DFL_E_INVALID_ARG;
     const int blocks = std::min(rows / kBlk + 2, c->n_blocks + 2);   // that the range can touch
     ReadArgs a{*c, len, first, k_out, v_out, rows};
-    k_kv8_read<<<dim3(blocks, c->n_kv, c->n_seq), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launched();
+    return launched(launch_pdl(k_kv8_read, dim3(blocks, c->n_kv, c->n_seq), dim3(256), 0, static_cast<cudaStream_t>(stream), a));
 }
 
 }  // extern "C"
