@@ -37,7 +37,7 @@ class dfl_config(ctypes.Structure):
         ("block", ctypes.c_int32), ("n_taps", ctypes.c_int32), ("mask_token", ctypes.c_int32),
         ("taps", ctypes.c_int32 * MAX_TAPS),
         ("d_rope_base", ctypes.c_float), ("d_eps", ctypes.c_float), ("d_emb_scale", ctypes.c_float),
-        ("max_ctx", ctypes.c_int32), ("prefill_rows", ctypes.c_int32),
+        ("max_ctx", ctypes.c_int32), ("prefill_rows", ctypes.c_int32), ("kv8", ctypes.c_int32),
     ]
 
 
@@ -143,9 +143,10 @@ class DflError(RuntimeError):
         self.code = code
 
 
-def config_from_pair(pc, prefill_rows: int = 0) -> dfl_config:
+def config_from_pair(pc, prefill_rows: int = 0, kv8: int = 0) -> dfl_config:
     """dfl_config from a pair description (attributes as in the seeded generator's PairConfig);
-    prefill_rows > 0 lets dfl_prefill take that many prompt rows per pass on the tcgen05 products."""
+    prefill_rows > 0 lets dfl_prefill take that many prompt rows per pass on the tcgen05 products;
+    kv8 = 1 holds the full layers' planes in 8 bits."""
     t, d = pc.target, pc.draft
     c = dfl_config()
     c.n_layers, c.hidden, c.vocab = t.n_layers, t.hidden, t.vocab
@@ -160,6 +161,7 @@ def config_from_pair(pc, prefill_rows: int = 0) -> dfl_config:
     c.d_rope_base, c.d_eps, c.d_emb_scale = d.rope_base, d.eps, d.emb_scale
     c.max_ctx = pc.max_ctx
     c.prefill_rows = prefill_rows
+    c.kv8 = kv8
     return c
 
 

@@ -439,6 +439,7 @@ cudaError_t launch_rows(const RowArgs &a, cudaStream_t s);
 cudaError_t launch_qk(const QkArgs &a, cudaStream_t s);
 cudaError_t launch_attn(const AttnArgs &a, cudaStream_t s);
 cudaError_t attn_prepare(int hd);   // once per head dimension, outside stream capture
+cudaError_t kv8_attn_prepare();     // the same for the attention over 8-bit planes (kv8.cu)
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t s);
 cudaError_t launch_rope_table(float2 *tab, int max_pos, int hd, double base, cudaStream_t s);
 cudaError_t launch_cast_rows(const float *src, int ld_src, int M, int H, const uint16_t *w_norm, float eps,

@@ -71,6 +71,9 @@ struct TLayer {
     Vec attn_norm, q_norm, k_norm, post_attn_norm, pre_ffn_norm, post_ffn_norm, ple_norm, lam;
     float lambda = 1.f;
     float *K = nullptr, *V = nullptr;
+    dfl_kv8 kv8{};              // instead of K and V: a full layer's plane in 8 bits (dfl_config.kv8)
+    uint8_t *kv8_base = nullptr;   // its arrays, one after another: kv8_bytes in all
+    size_t kv8_bytes = 0;
 };
 struct DLayer {
     QMat qkv, o, gu, d;
@@ -141,6 +144,10 @@ struct dfl_ctx {
     float *pf_x = nullptr, *pf_a = nullptr, *pf_b = nullptr;
     uint16_t *pf_ple = nullptr;
     uint8_t *pf_scratch = nullptr;
+    // planes in 8 bits: a pass's key and value rows, the attention's rows and scratch
+    float *kv8_k = nullptr, *kv8_v = nullptr, *kv8_o = nullptr;
+    uint8_t *kv8_scratch = nullptr;
+    size_t kv8_scratch_bytes = 0;
     // host mirror of the state
     int n = 0, draft_n = 0, pending = 0, last_accepted = -1, draft_at = -1;
     int draft_n_ok = 0;       // draft_n as of the last call that read the device state without an error
@@ -239,7 +246,34 @@ std::string validate(const dfl_config *g) {
     if (!(g->eps > 0.f) || !(g->d_eps > 0.f)) return bad("eps must be > 0");
     if (g->prefill_rows != 0 && (g->prefill_rows < 128 || g->prefill_rows > 8192 || g->prefill_rows % 16))
         return bad("prefill_rows must be 0 or 128..8192, a multiple of 16");
+    if (g->kv8 != 0 && g->kv8 != 1) return bad("kv8 must be 0 or 1");
+    if (g->kv8 && g->prefill_rows) return bad("kv8 planes take passes of at most 16 rows (prefill_rows = 0)");
+    for (int l = 0; g->kv8 && l < g->n_layers; ++l)
+        if (g->layer_type[l] == DFL_FULL && g->n_heads / g->kv_heads[l] > 16) return bad("kv8 planes take at most 16 query heads a key/value head");
     return {};
+}
+
+// A full layer's plane in 8 bits, laid out in one piece of the state
+void kv8_plan(TLayer &L, int head_dim, int positions, Arena &S) {
+    dfl_kv8 &c = L.kv8;
+    c = dfl_kv8{1, L.nkv, head_dim, (positions + DFL_KV8_BLOCK - 1) / DFL_KV8_BLOCK};
+    auto lay = [&](uint8_t *base) {
+        Arena A{base, 0};
+        const size_t blocks = (size_t)c.n_kv * c.n_blocks, codes = blocks * DFL_KV8_BLOCK * head_dim, tail = (size_t)c.n_kv * DFL_KV8_TAIL * head_dim;
+        c.k = A.take<uint8_t>(codes);
+        c.v = A.take<uint8_t>(codes);
+        c.k_scale = A.take<float>(blocks);
+        c.v_scale = A.take<float>(blocks);
+        c.k_tail = A.take<float>(tail);
+        c.v_tail = A.take<float>(tail);
+        c.table = A.take<int32_t>(blocks);
+        c.sealed = A.take<int32_t>(c.n_kv);
+        c.err = A.take<int32_t>(1);
+        return A.off;
+    };
+    L.kv8_bytes = lay(nullptr);
+    L.kv8_base = S.take<uint8_t>(L.kv8_bytes);
+    if (L.kv8_base) lay(L.kv8_base);
 }
 
 QMat qmat(int K, int N, bool q41) {
@@ -338,6 +372,10 @@ void plan(dfl_ctx *c, Arena &W, Arena &S, Arena &X) {
         TLayer &L = c->tl[l];
         if (L.owner != l) continue;
         L.cap = L.type == DFL_SLIDING ? c->cap_sliding : g.max_ctx + R;
+        if (g.kv8 && L.type == DFL_FULL) {
+            kv8_plan(L, hd, L.cap, S);
+            continue;
+        }
         L.K = S.take<float>((size_t)L.cap * L.nkv * hd);
         L.V = S.take<float>((size_t)L.cap * L.nkv * hd);
     }
@@ -371,6 +409,21 @@ void plan(dfl_ctx *c, Arena &W, Arena &S, Arena &X) {
     act(c->tapbuf, c->TH);
     c->kB = X.take<float>((size_t)R * dkv * dhd);
     c->vB = X.take<float>((size_t)R * dkv * dhd);
+    if (g.kv8) {
+        size_t sb = 256;
+        int kv_max = 1;
+        for (int l = 0; l < NL; ++l) {
+            const TLayer &L = c->tl[l], &O = c->tl[L.owner];
+            if (L.type != DFL_FULL) continue;
+            kv_max = std::max(kv_max, L.nkv);
+            for (int k = 1; k <= R; ++k) sb = std::max<size_t>(sb, (size_t)std::max<int64_t>(0, dfl_kv8_attn_scratch_bytes(&O.kv8, nq, k, 0, 0)));
+        }
+        c->kv8_k = X.take<float>((size_t)R * kv_max * hd);
+        c->kv8_v = X.take<float>((size_t)R * kv_max * hd);
+        c->kv8_o = X.take<float>((size_t)R * nq * hd);
+        c->kv8_scratch_bytes = sb;
+        c->kv8_scratch = X.take<uint8_t>(sb);
+    }
     c->part = X.take<float>(std::max<size_t>(part_floats, 1));
     c->am_val = X.take<float>((size_t)152 * 4 * kMaxRows);
     c->am_idx = X.take<int>((size_t)152 * 4 * kMaxRows);
@@ -638,6 +691,26 @@ int set_state(dfl_ctx *c, int k, const int32_t *rows_in, bool draft_rows, int ct
     return DFL_OK;
 }
 
+// Attention of a full layer whose plane is held in 8 bits: an owner's rows are staged behind the positions held (which
+// seals the block that the commits before completed), then every row sees its prefix; the output goes into the operand
+// format. Rolling rows back stays index arithmetic: the positions held are the device's own counter.
+int kv8_attention(dfl_ctx *c, const TLayer &O, int k, bool own) {
+    const int nq = c->cfg.n_heads, hd = c->cfg.head_dim;
+    const int32_t *held = &c->st->n;
+    int rc = DFL_OK;
+    if (own) {
+        c->launches += 1;
+        rc = dfl_kv8_stage(&O.kv8, held, nullptr, k, c->kv8_k, c->kv8_v, (int64_t)O.nkv * hd, c->stream);
+        if (rc) return fail(c, rc, "dfl_kv8_stage");
+    }
+    c->launches += 2;
+    rc = dfl_kv8_attn(&O.kv8, c->q, (int64_t)nq * hd, nq, k, held, nullptr, 0, 1, 1.0f / sqrtf((float)hd), 0, c->kv8_o, (int64_t)nq * hd,
+                      c->kv8_scratch, c->kv8_scratch_bytes, c->stream);
+    if (rc) return fail(c, rc, "dfl_kv8_attn");
+    DFL_LAUNCH(launch_act_pack(c->kv8_o, k, nq * hd, c->o.f, c->o.s, c->stream));
+    return DFL_OK;
+}
+
 // ---- target pass: k rows at positions n..n+k-1 ---------------------------------------------------------
 // head_last: the head (and sampling) for the last row only (a prefill chunk needs only its last token)
 int target_body(dfl_ctx *c, int k, bool do_head, bool sampled, bool head_last = false) {
@@ -683,7 +756,13 @@ int target_body(dfl_ctx *c, int k, bool do_head, bool sampled, bool head_last = 
         qa.k_store = own ? L.K : nullptr;
         qa.v_store = own ? L.V : nullptr;
         qa.cap = L.cap;
+        const bool kv8 = g.kv8 && L.type == DFL_FULL;
+        if (kv8 && own) qa.k_store = c->kv8_k, qa.v_store = c->kv8_v, qa.cap = 0;   // row m in slot m
         DFL_CK(gemm_qk(c, L.qkv, c->h, k, qa));   // its last CTAs norm, rotate and store q, k, v
+        if (kv8) {
+            const int rc = kv8_attention(c, O, k, own);
+            if (rc) return rc;
+        }
         AttnArgs aa{};
         aa.M = k;
         aa.nq = nq;
@@ -701,7 +780,7 @@ int target_body(dfl_ctx *c, int k, bool do_head, bool sampled, bool head_last = 
         aa.max_cluster = c->attn_cluster;
         aa.outf = c->o.f;
         aa.outs = c->o.s;
-        DFL_LAUNCH_S(3, aa, launch_attn);
+        if (!kv8) DFL_LAUNCH_S(3, aa, launch_attn);
         // each of the row steps below runs in the last CTAs of the product before it
         RowArgs r1 = rows(c, k, c->x);
         r1.y_out = c->y;
@@ -1151,6 +1230,10 @@ size_t snapshot_size(const dfl_ctx *c, int n, int draft_n) {
     for (int l = 0; l < g.n_layers; ++l) {
         const TLayer &L = c->tl[l];
         if (L.owner != l) continue;
+        if (L.kv8_bytes) {
+            b += L.kv8_bytes;
+            continue;
+        }
         const size_t row = (size_t)L.nkv * g.head_dim * 4;
         const size_t rows = L.type == DFL_SLIDING ? (size_t)L.cap : (size_t)n;
         b += 2 * rows * row;
@@ -1212,6 +1295,9 @@ int dfl_init(const dfl_config *cfg, const dfl_buffers *buf, void *stream, dfl_ct
         return bail(e, "rope table");
     if ((e = attn_prepare(g.head_dim)) != cudaSuccess || (e = attn_prepare(g.d_head_dim)) != cudaSuccess)
         return bail(e, "attention setup");
+    if (g.kv8 && (e = kv8_attn_prepare()) != cudaSuccess) return bail(e, "attention setup");
+    for (const TLayer &L : c->tl)
+        if (L.kv8_bytes && dfl_kv8_init(&L.kv8, c->stream) != DFL_OK) return bail(cudaErrorUnknown, "8-bit planes");
     if ((e = cudaStreamSynchronize(c->stream)) != cudaSuccess) return bail(e, "sync");
     c->launches = 3;   // the rope tables
     *out = c;
@@ -1460,6 +1546,11 @@ int dfl_snapshot(dfl_ctx *c, void *dst, size_t bytes) {
     for (int l = 0; l < g.n_layers; ++l) {
         const TLayer &L = c->tl[l];
         if (L.owner != l) continue;
+        if (L.kv8_bytes) {
+            DFL_CK(cudaMemcpyAsync(d + off, L.kv8_base, L.kv8_bytes, cudaMemcpyDeviceToDevice, c->stream));
+            off += L.kv8_bytes;
+            continue;
+        }
         const size_t row = (size_t)L.nkv * g.head_dim * 4;
         const size_t rows = L.type == DFL_SLIDING ? (size_t)L.cap : (size_t)c->n;
         DFL_CK(cudaMemcpyAsync(d + off, L.K, rows * row, cudaMemcpyDeviceToDevice, c->stream));
@@ -1500,6 +1591,11 @@ int dfl_restore(dfl_ctx *c, const void *src, size_t bytes) {
     for (int l = 0; l < g.n_layers; ++l) {
         const TLayer &L = c->tl[l];
         if (L.owner != l) continue;
+        if (L.kv8_bytes) {
+            DFL_CK(cudaMemcpyAsync(L.kv8_base, s + off, L.kv8_bytes, cudaMemcpyDeviceToDevice, c->stream));
+            off += L.kv8_bytes;
+            continue;
+        }
         const size_t row = (size_t)L.nkv * g.head_dim * 4;
         const size_t rows = L.type == DFL_SLIDING ? (size_t)L.cap : (size_t)hdr.n;
         DFL_CK(cudaMemcpyAsync(L.K, s + off, rows * row, cudaMemcpyDeviceToDevice, c->stream));
@@ -1635,6 +1731,7 @@ int dfl_debug_read(dfl_ctx *c, const char *name, void *dst, size_t bytes) {
         if (used != s.size() - 1 || l < 0 || l >= c->cfg.n_layers) return fail(c, DFL_E_INVALID_ARG, "bad layer in " + s);
         const TLayer &L = c->tl[l];
         if (L.owner != l) return fail(c, DFL_E_INVALID_ARG, s + ": a KV-shared layer holds no plane");
+        if (L.kv8_bytes) return fail(c, DFL_E_UNSUPPORTED, s + ": a plane in 8 bits is not read this way");
         src = s[0] == 'k' ? L.K : L.V;
         have = (size_t)L.cap * L.nkv * c->cfg.head_dim * 4;
     }

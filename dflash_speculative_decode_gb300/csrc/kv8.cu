@@ -1560,18 +1560,24 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
     return t;
 }
 
+// the kernels' shared memory, once per device
+template <int HD, int NT>
+cudaError_t prepare_kv8_attn() {
+    static bool done[kMaxDevices] = {};
+    const int dev = current_device(), smem = AttnShape<HD, NT>::kSmem;
+    if (dev < 0) return cudaErrorInvalidDevice;
+    if (done[dev]) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(k_kv8_attn<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv8_attn_share<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    done[dev] = e == cudaSuccess;
+    return e;
+}
+
 template <int HD, int NT>
 cudaError_t launch_kv8_attn(const AttnKvArgs &a, cudaStream_t s) {
-    static bool attr[kMaxDevices] = {};
-    const int dev = current_device();
-    if (dev < 0) return cudaErrorInvalidDevice;
     const int smem = AttnShape<HD, NT>::kSmem, threads = AttnShape<HD, NT>::kWarps * 32;
-    cudaError_t e;
-    if (!attr[dev]) {
-        if ((e = cudaFuncSetAttribute(k_kv8_attn<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-        if ((e = cudaFuncSetAttribute(k_kv8_attn_share<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-        attr[dev] = true;
-    }
+    cudaError_t e = prepare_kv8_attn<HD, NT>();
+    if (e != cudaSuccess) return e;
     const unsigned heads = unsigned(a.c.n_kv * a.groups);
     if (a.share)
         e = launch_pdl(k_kv8_attn_share<HD, NT>, dim3(a.ctas), dim3(threads), smem, s, a);
@@ -1759,6 +1765,15 @@ int write_rows(const dfl_kv8 *c, const int32_t *len, const int32_t *cnt, int row
 }
 
 }  // namespace
+
+cudaError_t kv8_attn_prepare() {
+    cudaError_t e;
+    if ((e = prepare_kv8_attn<64, 1>()) || (e = prepare_kv8_attn<64, 2>()) || (e = prepare_kv8_attn<128, 1>()) || (e = prepare_kv8_attn<128, 2>()) ||
+        (e = prepare_kv8_attn<256, 1>()))
+        return e;
+    return prepare_kv8_attn<256, 2>();
+}
+
 }  // namespace dfl
 
 using namespace dfl;

@@ -81,6 +81,14 @@ typedef struct dfl_config {
                                               this many prompt rows in one pass whose products run on the
                                               tcgen05 tensor cores (the buffers of such a pass, and sliding
                                               rings of window + prefill_rows - 1 slots, are sized in) */
+    int32_t kv8;                           /* 0, or 1: the planes of full layers, which grow with the context,
+                                              are held in 8 bits (the dfl_kv8 cache below: blocks of 32 committed
+                                              positions as codes, newer positions fp32), a quarter of the
+                                              memory and of the bytes that attention reads. A row sees the blocks
+                                              committed before its pass as their codes' values, so results differ
+                                              from those of fp32 planes by the codes' rounding, and a
+                                              position's by how its passes were cut. Needs prefill_rows = 0 and
+                                              at most 16 query heads a key/value head */
 } dfl_config;
 
 typedef struct dfl_sizes {

@@ -128,3 +128,30 @@ def test_plain_head_seals_and_cuts():
     k, _ = h.rows(41)
     assert k.shape == (41, 64) and np.abs(k[:40] - rows[:40]).max() <= np.abs(rows).max() / 254 * 1.001
     assert (BLOCK, h.evict(0, 0, 0)) == (32, ([], 1))
+
+
+# ---- planes in 8 bits (dfl_config.kv8) --------------------------------------------------------------------
+def test_planes_in_8_bits_take_a_quarter_of_the_state():
+    import gen
+    L, sz = _abi.lib(), _abi.dfl_sizes()
+    got = []
+    for kv8 in (0, 1):
+        cfg = _abi.config_from_pair(gen.e4b_pair(max_ctx=1 << 17), kv8=kv8)
+        assert L.dfl_required_bytes(ctypes.byref(cfg), ctypes.byref(sz)) == 0
+        got.append(sz.state_bytes)
+    full = sum(1 for l in range(24) if gen.e4b_target().layer_type[l] == gen.FULL)
+    plane = full * 2 * 2 * 256 * (1 << 17)                 # values of the full owners' planes
+    assert 0.99 * 3 * plane < got[0] - got[1] < 3 * plane
+
+
+def test_planes_in_8_bits_that_are_refused():
+    import gen
+    L, sz = _abi.lib(), _abi.dfl_sizes()
+    cfg = _abi.config_from_pair(gen.tiny_pair(), prefill_rows=128, kv8=1)
+    assert L.dfl_required_bytes(ctypes.byref(cfg), ctypes.byref(sz)) == _abi.DFL_E_INVALID_ARG
+    for kv8 in (2, -1):
+        cfg = _abi.config_from_pair(gen.tiny_pair(), kv8=kv8)
+        assert L.dfl_required_bytes(ctypes.byref(cfg), ctypes.byref(sz)) == _abi.DFL_E_INVALID_ARG
+    cfg = _abi.config_from_pair(gen.tiny_pair(), kv8=1)
+    cfg.n_heads = 64                                       # 32 query heads a key/value head of the full layer
+    assert L.dfl_required_bytes(ctypes.byref(cfg), ctypes.byref(sz)) == _abi.DFL_E_INVALID_ARG
