@@ -1640,9 +1640,17 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_evict(EvictArgs a) {
     const KvView w = view(a.c, s, h);
     const size_t base = ((size_t)s * a.c.n_kv + h) * w.nb;
     pdl_wait();
-    const int n = *w.sealed;
-    if (n < 0 || n > w.nb) {
-        if (tid == 0) atomicOr(a.c.err, kErrTable);
+    const int n = *w.sealed, L = a.len[s];
+    // the heads of a sequence thin alike, or its len would not fit them all
+    const bool differ = tid < a.c.n_kv && a.c.sealed[(size_t)s * a.c.n_kv + tid] != n;
+    const int bad = __syncthreads_or(n < 0 || n > w.nb) ? kErrTable : __syncthreads_or(differ) || L < kBlk * n || L > kBlk * n + kTail ? kErrState : 0;
+    if (bad) {                                                   // the outputs are the inputs
+        for (int b = tid; b < w.nb; b += kEvictThreads) a.table[base + b] = w.table[b], a.score[base + b] = w.score[b];
+        if (tid == 0) {
+            atomicOr(a.c.err, bad);
+            a.sealed[(size_t)s * a.c.n_kv + h] = n;
+            if (h == 0) a.len_out[s] = L;
+        }
         return;
     }
     const int keep = min(n, a.keep);
@@ -1710,7 +1718,7 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_evict(EvictArgs a) {
     }
     if (tid == 0) {
         a.sealed[(size_t)s * a.c.n_kv + h] = keep;
-        if (h == 0) a.len_out[s] = a.len[s] - kBlk * (n - keep);
+        if (h == 0) a.len_out[s] = L - kBlk * (n - keep);
     }
 }
 
@@ -1742,6 +1750,15 @@ int check_cache(const dfl_kv8 *c) {
 
 int check_rows(const dfl_kv8 *c, const void *p, int64_t ld, int heads) {
     return p && aligned16(p) && ld % 4 == 0 && ld >= (int64_t)heads * c->head_dim ? DFL_OK : DFL_E_INVALID_ARG;
+}
+
+struct Range {
+    const void *p;
+    size_t bytes;
+};
+bool overlap(const Range &a, const Range &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y + b.bytes && y < x + a.bytes;
 }
 
 int launched(cudaError_t e) { return e == cudaSuccess ? DFL_OK : DFL_E_CUDA; }
@@ -1825,9 +1842,8 @@ int dfl_kv8_attn(const dfl_kv8 *c, const float *q, int64_t ldq, int n_q, int row
     if (n_q / c->n_kv > kMaxGroup || rows > DFL_MAX_ROWS) return DFL_E_UNSUPPORTED;
     if ((rc = check_rows(c, q, ldq, n_q)) || (rc = check_rows(c, out, ldo, n_q))) return rc;
     if (score && !c->score) return DFL_E_INVALID_ARG;
-    if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255) || (int64_t)scratch_bytes < dfl_kv8_attn_scratch_bytes(c, n_q, rows, window, score))
-        return DFL_E_INVALID_ARG;
     const AttnCut t = attn_cut(c, n_q, rows, window, score);
+    if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255) || scratch_bytes < t.total) return DFL_E_INVALID_ARG;
     AttnKvArgs a{*c, q, out, ldq, ldo, n_q, rows, window, causal != 0, score != 0, len, cnt, scale, t.groups, t.splits, t.apart, t.share, t.ctas};
     uint8_t *at = static_cast<uint8_t *>(scratch);
     a.part_o = reinterpret_cast<float *>(at);
@@ -1852,7 +1868,12 @@ int dfl_kv8_evict(const dfl_kv8 *c, const int32_t *len, int keep, int sink, int 
     if (!c->score || !len || !table_out || !score_out || !sealed_out || !len_out || keep < 0 || sink < 0 || recent < 0 ||
         (int64_t)sink + recent > keep)
         return DFL_E_INVALID_ARG;
-    if (table_out == c->table || score_out == c->score || sealed_out == c->sealed || len_out == len) return DFL_E_INVALID_ARG;
+    const size_t heads = (size_t)c->n_seq * c->n_kv * 4, all = heads * c->n_blocks, seqs = (size_t)c->n_seq * 4;
+    const Range r[] = {{table_out, all}, {score_out, all}, {sealed_out, heads}, {len_out, seqs},      // written
+                       {c->table, all},  {c->score, all},  {c->sealed, heads},  {len, seqs},     {c->err, 4}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 9; ++j)
+            if (overlap(r[i], r[j])) return DFL_E_INVALID_ARG;
     EvictArgs a{*c, len, keep, sink, recent, table_out, score_out, sealed_out, len_out};
     return launched(launch_pdl(k_kv8_evict, dim3(c->n_kv, c->n_seq), dim3(kEvictThreads), 0, static_cast<cudaStream_t>(stream), a));
 }

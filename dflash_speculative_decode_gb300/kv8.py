@@ -60,9 +60,11 @@ class Kv8Cache:
         self.L = _abi.lib()
         self._idx, self._f32, self._i32 = self.device.index, f32, i32
         self._current_device, self._stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self._streams = set()         # that calls have used since the tensors were last recorded with them
+        self._evicted = self._scratch = None
         self._take(table, sealed, score)
         self._scale = self.head_dim ** -0.5
-        self._scratch, self._kept, self._scratch_ptr, self._scratch_bytes = None, [], 0, 0
+        self._kept, self._scratch_ptr, self._scratch_bytes = [], 0, 0
         self._need = {}
 
     def _take(self, table, sealed, score):
@@ -71,6 +73,16 @@ class Kv8Cache:
         self.c = dfl_kv8(self.n_seq, self.n_kv, self.head_dim, self.n_blocks, p(self.k), p(self.v), p(self.k_scale), p(self.v_scale),
                          p(self.k_tail), p(self.v_tail), p(table), p(sealed), p(score), p(self.err))
         self._c = ctypes.byref(self.c)
+        self._streams.clear()
+
+    def _use(self, stream):
+        """The cache's memory is in use on another stream than before: none of it is given to anyone else before that stream is done."""
+        self._streams.add(stream)
+        now = self.torch.cuda.current_stream(self._idx)
+        for t in (self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail, self.table, self.sealed, self.score, self.err, self._scratch, *self._kept,
+                  *(self._evicted or {}).values()):
+            if t is not None:
+                t.record_stream(now)
 
     @classmethod
     def empty(cls, n_seq: int, n_kv: int, head_dim: int, n_blocks: int, device="cuda:0", score: bool = True) -> "Kv8Cache":
@@ -90,11 +102,14 @@ class Kv8Cache:
     # ---- marshalling (a short call's time is mostly the host's: attributes that are cheap to read come first) ----
     def _call(self, f, what, *args):
         idx = self._idx
+        stream = self._stream(idx)
+        if stream not in self._streams:
+            self._use(stream)
         if self._current_device() != idx:
             with self.torch.cuda.device(idx):
-                rc = f(self._c, *args, self._stream(idx))
+                rc = f(self._c, *args, stream)
         else:
-            rc = f(self._c, *args, self._stream(idx))
+            rc = f(self._c, *args, stream)
         if rc != DFL_OK:
             raise DflError(rc, what)
 
@@ -152,6 +167,7 @@ class Kv8Cache:
                 self._kept.append(self._scratch)       # a captured graph may hold its address
                 self._scratch = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
                 self._scratch_ptr, self._scratch_bytes = self._scratch.data_ptr(), need
+                self._streams.clear()
         if out is None:
             out = (self.torch.empty if n is None else self.torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
         po, Mo, ldo = self._rows(out, "out", n_q)
@@ -162,22 +178,25 @@ class Kv8Cache:
         return out
 
     def evict(self, length, keep: int, sink: int = 0, recent: int = 0, out=None):
-        """dfl_kv8_evict: keep at most `keep` sealed blocks a head. Without `out` the cache goes on with the result and the new length is
-        returned; with `out` (a dict of tensors "table", "score", "sealed" and "len") the result is written there, the cache keeps its
-        own, and `take(out)` changes over."""
+        """dfl_kv8_evict: keep at most `keep` sealed blocks a head. Without `out` the result replaces the cache's table, scores and sealed
+        counts where they lie (a captured graph that uses them stays valid) and the new length is returned; with `out` (a dict of tensors
+        "table", "score", "sealed" and "len") it is written there, the cache keeps its own, and `take(out)` changes over."""
         pl = self._ints(length, "length")
         if self.score is None:
             _refuse("the cache keeps no scores")
         new = out
         if new is None:
-            new = {"table": self.torch.empty_like(self.table), "score": self.torch.empty_like(self.score),
-                   "sealed": self.torch.empty_like(self.sealed), "len": self.torch.empty_like(length)}
+            if self._evicted is None:
+                self._evicted = {name: self.torch.empty_like(getattr(self, name)) for name in ("table", "score", "sealed")}
+                self._streams.clear()
+            new = dict(self._evicted, len=self.torch.empty_like(length))
         else:
             self._check_out(new)
         self._call(self.L.dfl_kv8_evict, "dfl_kv8_evict", pl, keep, sink, recent, new["table"].data_ptr(), new["score"].data_ptr(),
                    new["sealed"].data_ptr(), self._ints(new["len"], "len"))
         if out is None:
-            self._take(new["table"], new["sealed"], new["score"])
+            for name in ("table", "score", "sealed"):
+                getattr(self, name).copy_(new[name])
             return new["len"]
         return out
 
@@ -188,7 +207,8 @@ class Kv8Cache:
                 _refuse(f"{name} must be contiguous {like.dtype} {list(like.shape)} on {self.device}")
 
     def take(self, new):
-        """Go on with an eviction's result (`evict(..., out=new)`); returns its length."""
+        """Go on with an eviction's result (`evict(..., out=new)`) in the tensors given; returns its length. Graphs captured before go on
+        with the tensors that the cache had then."""
         self._check_out(new)
         self._take(new["table"], new["sealed"], new["score"])
         return new["len"]

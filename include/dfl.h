@@ -416,8 +416,11 @@ int dfl_kv8_init(const dfl_kv8 *c, void *cuda_stream);
 /* Status of the calls enqueued on a cache so far: synchronises the stream, then DFL_OK, or (clearing the
  * word) DFL_E_CAPACITY: a sequence's len + rows passed the capacity or was negative; DFL_E_STATE: a len
  * lay further behind the sealed blocks than the tail reaches (tokens that no call has written);
- * DFL_E_INVALID_ARG: a table entry or a sealed count outside 0..n_blocks. A sequence (or head) with such
- * a fault was left as it was by the call that met it, its output rows among them. */
+ * or does not hold what is sealed where a call does not cut back (attn, evict), or the sealed counts of a
+ * sequence's heads differ where a call needs them equal (all calls leave them equal; checked by evict and
+ * by attn of many sequences); DFL_E_INVALID_ARG: a table entry or a sealed count outside 0..n_blocks. A
+ * sequence (or head) with such a fault was left as it was by the call that met it, its output rows among
+ * them; a read leaves out only the blocks whose entries are bad. */
 int dfl_kv8_status(const dfl_kv8 *c, void *cuda_stream);
 /* Append committed rows (a prompt's, or a draft's context): rows k, v (DEVICE fp32, row m of sequence s
  * at k + (s * rows + m) * ld, [n_kv][head_dim] each; ld in floats, a multiple of 4, >= n_kv * head_dim)
@@ -445,8 +448,14 @@ int64_t dfl_kv8_attn_scratch_bytes(const dfl_kv8 *c, int n_q, int rows, int wind
  * logical block's share of row 0's weights, summed over the head's group of query heads in a fixed order,
  * to c->score (row 0 is the one row of a verify that is always committed). Sums and softmax statistics
  * are fp32; queries and weights enter the tensor cores as two fp16 halves each, which hold 22 bits.
- * Results do not depend on what else the batch holds. Calls on one scratch (DEVICE, 256-byte aligned)
- * must not overlap on the GPU; nothing is kept in it from one call to the next. */
+ * What a weight adds is held to about 2^-32 of the row's largest weight times the largest |value| that it
+ * meets, which is what bounds an output that is small beside them. One call gives the same bits each time.
+ * Where heads and sequences are so many that a call shares its work out evenly (n_seq * n_kv * groups of
+ * rows above 152, or 76 for the widest), the last bits of a sequence may depend on the other sequences'
+ * lengths, as they decide where its sums are cut; below that they depend on nothing else in the batch. len
+ * must not lie below what is sealed (dfl_kv8_stage cuts back). out overlaps none of the inputs. Calls on
+ * one scratch (DEVICE, 256-byte aligned) must not overlap on the GPU; nothing is kept in it from one call
+ * to the next. */
 int dfl_kv8_attn(const dfl_kv8 *c, const float *q, int64_t ldq, int n_q, int rows, const int32_t *len,
                  const int32_t *cnt, int window, int causal, float scale, int score, float *out, int64_t ldo,
                  void *scratch, size_t scratch_bytes, void *cuda_stream);
@@ -456,8 +465,9 @@ int dfl_kv8_attn(const dfl_kv8 *c, const float *q, int64_t ldq, int n_q, int row
  * sink + recent <= keep. Writes, for every head, the table (kept blocks, then those evicted, which are
  * free again, then the rest as it was), the scores (kept ones, the two blocks that the tail holds, zeros)
  * and the sealed count to table_out, score_out and sealed_out, and len - 32 * (blocks evicted) to len_out
- * (all DEVICE, shaped like c's and len, none of them an input of the call). The caller goes on with
- * these. Tokens then have new positions in the cache, which len, windows and causality count by; a
+ * (all DEVICE, shaped like c's and len; they overlap neither each other nor an input). The caller goes on
+ * with these. A sequence whose len lies below what is sealed, or more than the tail behind it, keeps all
+ * it has (the outputs are its inputs; DFL_E_STATE). Tokens then have new positions in the cache, which len, windows and causality count by; a
  * model's rotary positions are the caller's own. */
 int dfl_kv8_evict(const dfl_kv8 *c, const int32_t *len, int keep, int sink, int recent, int32_t *table_out,
                   float *score_out, int32_t *sealed_out, int32_t *len_out, void *cuda_stream);

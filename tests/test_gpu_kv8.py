@@ -502,3 +502,161 @@ def test_quantisation_error_is_half_a_step(torch):
                 scale = np.float64(quantise(rows[0, 32 * b:32 * b + 32, h])[1])
                 err = np.abs(x[0, 32 * b:32 * b + 32, h].cpu().numpy() - want)
                 assert (err <= scale / 2 + 127 * scale * 2.0 ** -24).all()
+
+
+# ---- more units than CTAs: the work is shared out evenly -----------------------------------------------------
+@pytest.mark.parametrize("S,n_kv,n_q,hd,rows,held", [(40, 4, 8, 64, 1, 900), (21, 8, 32, 128, 3, 400), (40, 2, 24, 256, 2, 300), (52, 3, 9, 64, 16, 260),
+                                                     (170, 1, 4, 64, 2, 90), (77, 2, 2, 256, 1, 150)])
+def test_attn_of_many_sequences(torch, S, n_kv, n_q, hd, rows, held):
+    """Sequences of very different lengths, some without rows or tokens: full and windowed, causal and not, with scores and without."""
+    p = Pair(torch, S, n_kv, hd, held // BLOCK + 2, seed=S)
+    cnt = p.rng.integers(0, held + 1, S)
+    cnt[::5], cnt[1], cnt[-1] = 0, held, held
+    p.write(held, cnt=cnt)
+    n = p.rng.integers(0, rows + 1, S)
+    n[-3:] = rows
+    p.write(rows, cnt=n, commit=False)
+    p.attn(n_q, rows, cnt=n, score=True)
+    p.attn(n_q, rows, cnt=n, window=70, score=True)
+    p.attn(n_q, rows, cnt=n, window=33, causal=False)
+
+
+def test_attn_of_more_sequences_than_threads(torch):
+    """700 sequences, a few of which have rows: the first, the last, and some on either side of 256 and 512."""
+    p = Pair(torch, 700, 1, 64, 6, seed=31)
+    n = np.zeros(700, np.int32)
+    n[[0, 1, 255, 256, 400, 511, 512, 513, 699]] = [3, 2, 1, 3, 2, 1, 3, 2, 1]
+    p.write(150, cnt=np.where(n > 0, 150 - 17 * n, 0))
+    p.write(3, cnt=n, commit=False)
+    p.attn(4, 3, cnt=n, score=True)
+    p.attn(4, 3, cnt=np.zeros(700, np.int32), score=True)      # nothing to do at all
+
+
+def test_many_sequences_give_the_same_bits_each_time(torch):
+    """Eagerly, and replayed from a graph with other counts of rows than it was captured with."""
+    p = Pair(torch, 90, 2, 64, 30, seed=32)
+    p.write(800, cnt=p.rng.integers(0, 801, 90))
+    p.write(4, commit=False)
+    q, length = p.dev(p.new_rows(4, 8)), p.dev(p.len)
+    p.c.score.zero_()
+    want, side = p.c.attn(q, length, score=True), torch.cuda.Stream()
+    sums, out, g = p.c.score.clone(), torch.empty_like(want), torch.cuda.CUDAGraph()
+    n = torch.zeros(90, dtype=torch.int32, device="cuda")
+    with torch.cuda.graph(g, stream=side):
+        p.c.attn(q, length, n, score=True, out=out)
+    n.fill_(4)
+    for _ in range(3):
+        p.c.score.zero_()
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want) and torch.equal(p.c.score, sums)
+    p.c.status()
+
+
+def test_faults_among_many_sequences(torch):
+    """A bad length, table entry or count concerns its own sequence (or head) only."""
+    from dflash_speculative_decode_gb300 import DflError, _abi
+    S = 80
+    p = Pair(torch, S, 2, 64, 8, seed=33)
+    p.write(200, cnt=p.rng.integers(64, 201, S))
+    p.write(2, commit=False)
+    q = p.dev(p.new_rows(2, 4))
+    good = p.c.attn(q, p.dev(p.len))
+    p.c.status()
+
+    def check(bad, code, length=None):
+        out = torch.full_like(q, 9.0)
+        p.c.attn(q, p.dev(p.len) if length is None else length, out=out)
+        with pytest.raises(DflError) as e:
+            p.c.status()
+        assert e.value.code == code
+        for s in range(S):
+            for h in range(2):
+                x, want = out[s, :, 2 * h:2 * h + 2], good[s, :, 2 * h:2 * h + 2]
+                if (s, h) in bad:
+                    assert (x == 9.0).all()
+                else:           # other cuts than before: the same numbers to a few roundings of fp32 sums of values below 16
+                    assert (x - want).abs().max() < 2e-5
+    length = p.dev(p.len)
+    length[3], length[40] = -1, 31
+    check({(3, 0), (3, 1), (40, 0), (40, 1)}, _abi.DFL_E_STATE, length)
+    keep = p.c.table.clone()
+    p.c.table[7, 1, 0] = 8
+    p.c.table[79, 0, 1] = -1
+    check({(7, 1), (79, 0)}, _abi.DFL_E_INVALID_ARG)
+    p.c.table.copy_(keep)
+    p.c.sealed[11, 1] = 1 if int(p.c.sealed[11, 1]) != 1 else 0
+    check({(11, 1)}, _abi.DFL_E_STATE)
+
+
+# ---- eviction's faults, and its place in graphs ---------------------------------------------------------------
+def test_eviction_of_a_sequence_out_of_order_keeps_it(torch):
+    from dflash_speculative_decode_gb300 import DflError, _abi
+    p = Pair(torch, 4, 2, 64, 12, seed=34)
+    p.write(300)
+    p.c.score.copy_(p.dev(p.rng.random((4, 2, 12)).astype(np.float32)))
+    for change, code in ((dict(len=287), _abi.DFL_E_STATE), (dict(len=9 * 32 + TAIL + 1), _abi.DFL_E_STATE), (dict(sealed=8), _abi.DFL_E_STATE),
+                         (dict(sealed=13), _abi.DFL_E_INVALID_ARG), (dict(sealed=-1), _abi.DFL_E_INVALID_ARG)):
+        length, sealed = p.dev(p.len), p.c.sealed.clone()
+        if "len" in change:
+            length[2] = change["len"]
+        else:
+            p.c.sealed[2, 1] = change["sealed"]
+        to = {"table": torch.full_like(p.c.table, -5), "score": torch.full_like(p.c.score, -5), "sealed": torch.full_like(sealed, -5), "len": torch.full_like(length, -5)}
+        p.c.evict(length, 4, sink=1, recent=1, out=to)
+        with pytest.raises(DflError) as e:
+            p.c.status()
+        assert e.value.code == code
+        assert all(torch.equal(to[name][2], getattr(p.c, name)[2]) for name in ("table", "score", "sealed")) and int(to["len"][2]) == int(length[2])
+        assert to["len"][[0, 1, 3]].tolist() == [300 - 5 * 32] * 3 and (to["sealed"][[0, 1, 3]] == 4).all()
+        p.c.sealed.copy_(sealed)
+
+
+def test_eviction_in_place_keeps_graphs_valid(torch):
+    """A graph captured before evictions attends over what they leave, and an eviction can itself be captured."""
+    p = Pair(torch, 2, 2, 64, 20, seed=35)
+    p.write(500)
+    p.write(3, commit=False)
+    q, length = p.dev(p.new_rows(3, 4)), p.dev(p.len)
+    out, side, g, ge = torch.empty_like(q), torch.cuda.Stream(), torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    p.c.attn(q, length, out=out, score=True)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        p.c.attn(q, length, out=out, score=True)
+    with torch.cuda.graph(ge, stream=side):
+        length.copy_(p.c.evict(length, 6, sink=1, recent=2))
+    for keep, evict in ((10, lambda: length.copy_(p.c.evict(length, 10, sink=1, recent=2))), (6, ge.replay)):
+        for s in range(2):
+            for h in range(2):
+                p.heads[s][h].score = p.c.score[s, h].cpu().numpy().astype(np.float64)
+                p.heads[s][h].evict(keep, 1, 2)
+        evict()
+        p.c.status()
+        p.len = length.cpu().numpy()
+        p.check_state()
+        g.replay()
+        for s in range(2):
+            for h in range(2):
+                want, bound, _, _ = p.heads[s][h].attn(q[s, :, 2 * h:2 * h + 2].cpu().numpy(), int(p.len[s]), 3, 0, True, 0.125)
+                assert (np.abs(out[s, :, 2 * h:2 * h + 2].cpu().numpy() - want) <= bound).all()
+    p.c.status()
+
+
+def test_memory_of_a_cache_used_on_another_stream_is_not_given_away(torch):
+    """A cache is dropped while another stream still works on it: what is allocated next must not be written by that work."""
+    p = Pair(torch, 1, 2, 128, 600, seed=36)
+    p.write(19000)
+    p.write(8, commit=False)
+    q, length, side = p.dev(p.new_rows(8, 8)), p.dev(p.len), torch.cuda.Stream()
+    want = p.c.attn(q, length)
+    c, p.c = p.c, None
+    side.wait_stream(torch.cuda.current_stream())
+    out = torch.empty_like(q)
+    with torch.cuda.stream(side):
+        for _ in range(200):
+            c.attn(q, length, out=out)
+    sizes = [t.numel() * t.element_size() for t in (c.k, c.v, c.table, c._scratch)]
+    del c
+    taken = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    side.synchronize()
+    assert torch.equal(out, want) and all((t == 0).all() for t in taken)

@@ -155,3 +155,13 @@ def test_planes_in_8_bits_that_are_refused():
     cfg = _abi.config_from_pair(gen.tiny_pair(), kv8=1)
     cfg.n_heads = 64                                       # 32 query heads a key/value head of the full layer
     assert L.dfl_required_bytes(ctypes.byref(cfg), ctypes.byref(sz)) == _abi.DFL_E_INVALID_ARG
+
+
+def test_evictions_outputs_overlap_nothing():
+    """c is 2 x 2 heads of 8 blocks: 128 bytes of table and of scores, 16 of sealed counts; len and len_out 8."""
+    L = _abi.lib()
+    evict = calls(cache(table=10 * A, score=11 * A, sealed=12 * A, err=13 * A), L)["evict"]
+    for args in (dict(table=10 * A + 64), dict(table=10 * A - 64), dict(score=11 * A + 124), dict(sealed=12 * A + 12), dict(len_out=A + 4), dict(len_out=A - 4),
+                 dict(table=11 * A), dict(score=10 * A + 4), dict(sealed=A), dict(len_out=13 * A), dict(score=2 * A + 124), dict(sealed=2 * A + 64),
+                 dict(len_out=4 * A + 8)):
+        assert evict(**args) == -1, args
