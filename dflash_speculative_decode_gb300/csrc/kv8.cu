@@ -56,17 +56,29 @@ __device__ __forceinline__ int rows_of(const int32_t *cnt, int s, int rows) {
     return cnt ? min(max(cnt[s], 0), rows) : rows;
 }
 
-// The code of x at `scale` >= kTiny, 128 + the integer nearest to x / scale, exactly: in the low byte of the result. The
-// fp32 quotient is off by less than 2^-15 (it is at most 127 and a rounding), and adding 1.5 * 2^23 + 128 rounds it to an
-// integer c that is off by at most one. The remainder r = x - c scale is exact in fp32 (it is a multiple of the smaller unit
-// in the last place of x and scale, and no larger than about scale / 2), so |r| against scale / 2 tells.
+// The codes of x at `scale` >= kTiny, 128 + the integer nearest to x / scale, exactly: in the low byte of each result. With
+// inv = 1 / scale rounded, x inv is off by at most 127 2^-24 < 2^-17. Adding 1.5 * 2^23 + 128 rounds it to an integer c; the
+// rest f = x inv - c, rounded once, tells where c might not be the nearest: |f| > 1/2 - 2^-15, for one value in some 16,000.
+// There c is off by one at most, and the remainder r = x - c scale, which is exact in fp32 (it is a multiple of the smaller
+// unit in the last place of x and scale, and no larger than about scale / 2), is held against scale / 2.
 constexpr float kTiny = 1e-30f;
 constexpr float kRound = 12582912.f + 128.f;
-__device__ __forceinline__ uint32_t code_of(float x, float scale, float inv) {
-    const float t = fmaf(x, inv, kRound), c = t - kRound, r = fmaf(-c, scale, x);
-    uint32_t code = __float_as_uint(t);
-    if (2.f * fabsf(r) >= scale && (2.f * fabsf(r) > scale || (code & 1))) code += r > 0.f ? 1 : -1;   // a tie goes to the even one
-    return code;
+template <int N>
+__device__ __forceinline__ void codes_of(const float (&x)[N], float scale, float inv, uint32_t (&code)[N]) {
+    float far = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float t = fmaf(x[k], inv, kRound);
+        far = fmaxf(far, fabsf(fmaf(x[k], inv, kRound - t)));
+        code[k] = __float_as_uint(t);
+    }
+    if (far <= 0.5f - 3.0517578125e-05f) return;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float c = __uint_as_float(code[k]) - kRound, r = fmaf(-c, scale, x[k]);
+        const bool off = 2.f * fabsf(r) > scale || (2.f * fabsf(r) == scale && (code[k] & 1));   // a tie goes to the even one
+        code[k] += !off ? 0 : r > 0.f ? 1 : -1;
+    }
 }
 // for scales whose reciprocal or remainders would leave fp32's normal range: the quotient in fp64
 __device__ __noinline__ uint32_t code_of_tiny(float x, float scale) {
@@ -82,6 +94,7 @@ struct WriteArgs {
     const float *k, *v;
     int64_t ld;
     int rows, commit;
+    int run;                 // blocks that a CTA of many rows' seals
 };
 
 // What a call does to one head: tokens from 32 z on are `have` rows of the tail (or, after a cut, of block
@@ -109,27 +122,27 @@ __device__ __forceinline__ Plan plan_of(const WriteArgs &a, int s, const KvView 
 }
 
 // Channels d..d+3 of token 32 z + r of a head, keys (V = false) or values.
-template <bool V>
+template <bool V, int HD>
 struct Rows {
     const float *src;        // the call's rows of this head
     int64_t ld;
     const float *tail;
     const uint8_t *old;      // after a cut: block z's codes and scale
     float old_scale;
-    int have, cut, hd;
+    int have, cut;
     __device__ __forceinline__ float4 get(int r, int d) const {
         if (r >= have) return *reinterpret_cast<const float4 *>(src + (size_t)(r - have) * ld + d);
         float y[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = cut ? expand(old[V ? v_at(r, d + k) : k_at(r, d + k)], old_scale) : V ? tail[(size_t)(d + k) * kTail + r] : tail[(size_t)r * hd + d + k];
+        for (int k = 0; k < 4; ++k) y[k] = cut ? expand(old[V ? v_at(r, d + k) : k_at(r, d + k)], old_scale) : V ? tail[(d + k) * kTail + r] : tail[r * HD + d + k];
         return make_float4(y[0], y[1], y[2], y[3]);
     }
 };
-template <bool V>
-__device__ __forceinline__ Rows<V> rows_from(const WriteArgs &a, int s, int h, const KvView &w, const Plan &p, bool old) {
-    const int hd = a.c.head_dim, phys = old ? w.table[p.z] : 0;      // old: rows before the call's own are wanted after a cut
-    return {(V ? a.v : a.k) + (size_t)s * a.rows * a.ld + (size_t)h * hd, a.ld, V ? w.vt : w.kt, (V ? w.v : w.k) + (size_t)phys * kBlk * hd,
-            old ? (V ? w.vs : w.ks)[phys] : 0.f, p.have, p.cut, hd};
+template <bool V, int HD>
+__device__ __forceinline__ Rows<V, HD> rows_from(const WriteArgs &a, int s, int h, const KvView &w, const Plan &p, bool old) {
+    const int phys = old ? w.table[p.z] : 0;      // old: rows before the call's own are wanted after a cut
+    return {(V ? a.v : a.k) + (size_t)s * a.rows * a.ld + (size_t)h * HD, a.ld, V ? w.vt : w.kt, (V ? w.v : w.k) + (size_t)phys * kBlk * HD,
+            old ? (V ? w.vs : w.ks)[phys] : 0.f, p.have, p.cut};
 }
 
 constexpr int kWriteThreads = 256;
@@ -140,66 +153,77 @@ __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// Seals block b of the plan: 256 threads, a thread holds 4 tokens x 4 channels at a time. The codes go through shared
-// memory, so that they leave in 16-byte stores whatever their layout. Nothing is written if `bad` anywhere in the CTA.
-template <bool V>
-__device__ __forceinline__ bool seal_block(const Rows<V> &x, int b, const KvView &w, int phys, int bad, uint32_t *red, uint8_t *code) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hd = x.hd, dq = hd / 4;
+// Seals block b of the plan: a thread holds 4 tokens x 4 channels at a time, kPieces times. The codes go through shared
+// memory, so that they leave in 16-byte stores whatever their layout.
+template <bool V, int HD, int kThreads>
+struct Seal {
+    static constexpr int kPieces = (2 * HD + kThreads - 1) / kThreads, dq = HD / 4;
+    float y[kPieces][16];                                            // [token][channel]
     // piece e: tokens t.. and channels d.. of it, so that a warp's words of shared memory lie in different banks: values with
     // the tokens innermost, a channel's 32 tokens 40 bytes apart
-    auto piece_t = [&](int e) { return V ? 4 * (e & 7) : 4 * (e / dq); };
-    auto piece_d = [&](int e) { return V ? 4 * (e >> 3) : 4 * (e % dq); };
-    float4 y[2][4];
-    uint32_t top = 0;                                                // magnitudes as bits: infinities and NaN come last
+    static __device__ __forceinline__ int piece_t(int e) { return V ? 4 * (e & 7) : 4 * (e / dq); }
+    static __device__ __forceinline__ int piece_d(int e) { return V ? 4 * (e >> 3) : 4 * (e % dq); }
+    __device__ __forceinline__ void load(const Rows<V, HD> &x, int b) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int e = i * kWriteThreads + tid;                       // of 8 * hd / 4 pieces
-        if (e < 8 * dq) {
+        for (int i = 0; i < kPieces; ++i) {
+            const int e = i * kThreads + int(threadIdx.x), r = kBlk * b + piece_t(e), d = piece_d(e);   // of 8 * hd / 4 pieces
+            if (e >= 8 * dq) break;
+            if (kBlk * b >= x.have) {                                // all of the block is the call's
+                const float *at = x.src + (size_t)(r - x.have) * x.ld + d;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                y[i][k] = x.get(kBlk * b + piece_t(e) + k, piece_d(e));
-                const float v[4] = {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
+                for (int k = 0; k < 4; ++k) put(i, k, *reinterpret_cast<const float4 *>(at + k * x.ld));
+            } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) top = max(top, __float_as_uint(v[c]) & 0x7fffffffu);
+                for (int k = 0; k < 4; ++k) put(i, k, x.get(r + k, d));
             }
         }
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) red[warp] = top;
-    if (__syncthreads_or(bad)) return false;
+    __device__ __forceinline__ void put(int i, int k, const float4 &v) { y[i][4 * k] = v.x, y[i][4 * k + 1] = v.y, y[i][4 * k + 2] = v.z, y[i][4 * k + 3] = v.w; }
+    // Nothing is written if `bad` anywhere in the CTA. Two barriers: what a call reads of red and code is read before the next one's.
+    __device__ __forceinline__ bool store(const KvView &w, int phys, int bad, uint32_t *red, uint8_t *code) const {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        float most = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWriteThreads / 32; ++i) top = max(top, red[i]);
-    const float scale = top < 0x7f800000u ? __fdiv_rn(__uint_as_float(top), 127.f) : NAN;
-    const bool tiny = scale < kTiny, none = !(scale > 0.f);
-    const float inv = none || tiny ? 0.f : 1.f / scale;
+        for (int i = 0; i < kPieces; ++i)
+            if (i * kThreads + tid < 8 * dq)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int e = i * kWriteThreads + tid, t = piece_t(e), d = piece_d(e);
-        if (e < 8 * dq) {
-            uint32_t q[4][4];                                        // [token][channel]
+                for (int k = 0; k < 16; ++k) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(fabsf(y[i][k])));
+        uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most) & 0x7fffffffu);   // as bits: infinities and NaN come last
+        if (lane == 0) red[warp] = top;
+        if (__syncthreads_or(bad)) return false;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float v[4] = {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
+        for (int i = 0; i < kThreads / 32; ++i) top = max(top, red[i]);
+        const float scale = top < 0x7f800000u ? __fdiv_rn(__uint_as_float(top), 127.f) : NAN;
+        const bool tiny = scale < kTiny, none = !(scale > 0.f);
+        const float inv = none || tiny ? 0.f : 1.f / scale;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) q[k][c] = none ? 128u : tiny ? code_of_tiny(v[c], scale) : code_of(v[c], scale, inv);
+        for (int i = 0; i < kPieces; ++i) {
+            const int e = i * kThreads + tid, t = piece_t(e), d = piece_d(e);
+            if (e >= 8 * dq) break;
+            uint32_t q[16];
+            if (!none && !tiny) {
+                codes_of(y[i], scale, inv, q);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) q[k] = none ? 128u : code_of_tiny(y[i][k], scale);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t word = V ? low_bytes(q[0][k], q[1][k], q[2][k], q[3][k]) : low_bytes(q[k][0], q[k][1], q[k][2], q[k][3]);
+                const uint32_t word = V ? low_bytes(q[k], q[4 + k], q[8 + k], q[12 + k]) : low_bytes(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
                 *reinterpret_cast<uint32_t *>(code + (V ? (d + k) * kVPitch + t : k_at(t + k, d))) = word;
             }
         }
+        __syncthreads();
+        uint4 *dst = reinterpret_cast<uint4 *>((V ? w.v : w.k) + (size_t)phys * kBlk * HD);
+        for (int e = tid; e < 2 * HD; e += kThreads) {
+            const uint2 *from = reinterpret_cast<const uint2 *>(code + (V ? (e >> 1) * kVPitch + 16 * (e & 1) : 16 * e));
+            const uint2 lo = from[0], hi = from[1];
+            dst[e] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+        if (tid == 0) (V ? w.vs : w.ks)[phys] = scale;
+        return true;
     }
-    __syncthreads();
-    uint4 *dst = reinterpret_cast<uint4 *>((V ? w.v : w.k) + (size_t)phys * kBlk * hd);
-    for (int e = tid; e < 2 * hd; e += kWriteThreads) {
-        const uint2 *from = reinterpret_cast<const uint2 *>(code + (V ? (e >> 1) * kVPitch + 16 * (e & 1) : 16 * e));
-        const uint2 lo = from[0], hi = from[1];
-        dst[e] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-    }
-    if (tid == 0) (V ? w.vs : w.ks)[phys] = scale;
-    return true;
-}
+};
 
 // A head whose plan follows a table entry out of range is left alone.
 __device__ __forceinline__ bool bad_table(const KvView &w, const Plan &p) {
@@ -213,35 +237,34 @@ __device__ __forceinline__ bool bad_table(const KvView &w, const Plan &p) {
 // belongs. Every load is under way before the first store.
 constexpr int kTurn = 64;
 using Turn = float[kTurn][kTail + 1];   // values turn through shared memory, so that a channel's tokens are stored together
-template <bool V>
-__device__ __forceinline__ void keep_rest(const Rows<V> &x, const KvView &w, const Plan &p, Turn &turn) {
-    const int tid = threadIdx.x, hd = x.hd, left = p.have + p.n - kBlk * p.full, first = !p.cut && p.full == 0 ? p.have : 0;
-    constexpr int kSome = 3;                                         // at most 47 rows of 16 pieces a turn
-    float4 y[256 / kTurn][kSome];
+template <bool V, int HD, int kThreads>
+__device__ __forceinline__ void keep_rest(const Rows<V, HD> &x, const KvView &w, const Plan &p, Turn &turn) {
+    const int tid = threadIdx.x, left = p.have + p.n - kBlk * p.full, first = !p.cut && p.full == 0 ? p.have : 0;
+    constexpr int kSome = (kTail * (kTurn / 4) + kThreads - 1) / kThreads;   // at most 47 rows of 16 pieces a turn
+    float4 y[HD / kTurn][kSome];
 #pragma unroll
-    for (int c = 0; c < 256 / kTurn; ++c)
+    for (int c = 0; c < HD / kTurn; ++c)
 #pragma unroll
         for (int i = 0; i < kSome; ++i) {
-            const int e = tid + i * kWriteThreads;
-            if (c * kTurn < hd && e < (left - first) * (kTurn / 4)) y[c][i] = x.get(kBlk * p.full + first + e / (kTurn / 4), c * kTurn + 4 * (e % (kTurn / 4)));
+            const int e = tid + i * kThreads;
+            if (e < (left - first) * (kTurn / 4)) y[c][i] = x.get(kBlk * p.full + first + e / (kTurn / 4), c * kTurn + 4 * (e % (kTurn / 4)));
         }
     __syncthreads();
 #pragma unroll
-    for (int c = 0; c < 256 / kTurn; ++c) {
-        if (c * kTurn >= hd) break;
+    for (int c = 0; c < HD / kTurn; ++c) {
         if (V) __syncthreads();
 #pragma unroll
         for (int i = 0; i < kSome; ++i) {
-            const int e = tid + i * kWriteThreads, t = e / (kTurn / 4), d = 4 * (e % (kTurn / 4));
+            const int e = tid + i * kThreads, t = e / (kTurn / 4), d = 4 * (e % (kTurn / 4));
             if (e >= (left - first) * (kTurn / 4)) continue;
             if (V)
                 turn[d][t] = y[c][i].x, turn[d + 1][t] = y[c][i].y, turn[d + 2][t] = y[c][i].z, turn[d + 3][t] = y[c][i].w;
             else
-                *reinterpret_cast<float4 *>(w.kt + (size_t)(first + t) * hd + c * kTurn + d) = y[c][i];
+                *reinterpret_cast<float4 *>(w.kt + (size_t)(first + t) * HD + c * kTurn + d) = y[c][i];
         }
         if (!V) continue;
         __syncthreads();
-        for (int d = tid >> 5; d < kTurn; d += kWriteThreads / 32)
+        for (int d = tid >> 5; d < kTurn; d += kThreads / 32)
             for (int t = tid & 31; t < left - first; t += 32) w.vt[(size_t)(c * kTurn + d) * kTail + first + t] = turn[d][t];
     }
 }
@@ -257,9 +280,10 @@ __device__ __forceinline__ void settle(const WriteArgs &a, int s, const KvView &
 }
 
 // One launch for a call of few rows, one CTA per head.
+template <int HD>
 __global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a) {
     __shared__ uint32_t red[kWriteThreads / 32];
-    __shared__ __align__(16) uint8_t code[kVPitch * 256];
+    __shared__ __align__(16) uint8_t code[kVPitch * HD];
     __shared__ Turn turn;
     const int h = blockIdx.x, s = blockIdx.y;
     const KvView w = view(a.c, s, h);
@@ -270,47 +294,61 @@ __global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a) {
         if (threadIdx.x == 0) atomicOr(a.c.err, p.bad);
         return;
     }
-    const Rows<false> xk = rows_from<false>(a, s, h, w, p, p.cut);
-    const Rows<true> xv = rows_from<true>(a, s, h, w, p, p.cut);
+    const Rows<false, HD> xk = rows_from<false, HD>(a, s, h, w, p, p.cut);
+    const Rows<true, HD> xv = rows_from<true, HD>(a, s, h, w, p, p.cut);
     for (int b = 0; b < p.full; ++b) {
         const int phys = w.table[p.z + b];
-        seal_block<false>(xk, b, w, phys, 0, red, code);
-        __syncthreads();
-        seal_block<true>(xv, b, w, phys, 0, red, code);
-        __syncthreads();
+        Seal<false, HD, kWriteThreads> k;
+        k.load(xk, b);
+        k.store(w, phys, 0, red, code);
+        Seal<true, HD, kWriteThreads> v;
+        v.load(xv, b);
+        v.store(w, phys, 0, red, code);
     }
-    keep_rest<false>(xk, w, p, turn);
-    keep_rest<true>(xv, w, p, turn);
+    keep_rest<false, HD, kWriteThreads>(xk, w, p, turn);
+    keep_rest<true, HD, kWriteThreads>(xv, w, p, turn);
     settle(a, s, w, p);
 }
 
-// Many rows: a CTA for the keys or the values of each block, grid (2 x blocks, heads, sequences). The first one, which alone
-// reads rows held before, also keeps the rest. k_kv8_count behind it settles the call and reports what is bad.
-template <bool V>
-__device__ __forceinline__ void append_block(const WriteArgs &a, int s, int h, const KvView &w, const Plan &p, int b, uint32_t *red, uint8_t *code, Turn &turn) {
-    const Rows<V> x = rows_from<V>(a, s, h, w, p, p.cut && b == 0);
-    if (b < p.full) {
+// Many rows: a CTA for the keys or the values of a.run consecutive blocks, the next block's rows asked for as soon as the codes
+// of the one before are out of the registers; grid (2 x runs, heads, sequences). The first one, which alone reads rows held
+// before the call's first whole block, also keeps the rest. k_kv8_count behind it settles the call and reports what is bad.
+// 4 bytes in and one out a value, some 15 instructions: 8 x 8192 rows of 8 heads of 128 take 142 us, 4.7 TB/s, 70 % of a
+// plain copy's; what is missing is loads in flight while the codes are made (asking for a block ahead into registers of
+// its own, or more CTAs of fewer registers, took longer: 151 and 179 us). A short call is latency: 1024 rows 7 us, 2 of them the second launch.
+template <bool V, int HD, int kThreads>
+__device__ __forceinline__ void append_blocks(const WriteArgs &a, int s, int h, const KvView &w, const Plan &p, int b0, uint32_t *red, uint8_t *code, Turn &turn) {
+    const Rows<V, HD> x = rows_from<V, HD>(a, s, h, w, p, p.cut && b0 == 0);
+    const int b1 = min(b0 + a.run, p.full);
+    if (b0 < b1) {
         int bad = 0;
-        for (int i = threadIdx.x; i < p.full; i += kWriteThreads) bad |= unsigned(w.table[p.z + i]) >= unsigned(w.nb);
-        if (!seal_block<V>(x, b, w, w.table[p.z + b], bad, red, code)) return;
+        for (int i = threadIdx.x; i < p.full; i += kThreads) bad |= unsigned(w.table[p.z + i]) >= unsigned(w.nb);
+        Seal<V, HD, kThreads> seal;
+        seal.load(x, b0);
+        for (int b = b0; b < b1; ++b) {
+            if (!seal.store(w, w.table[p.z + b], bad, red, code)) return;
+            if (b + 1 < b1) seal.load(x, b + 1);
+        }
         __syncthreads();
     }
-    if (b == 0) keep_rest<V>(x, w, p, turn);
+    if (b0 == 0) keep_rest<V, HD, kThreads>(x, w, p, turn);
 }
-__global__ void __launch_bounds__(kWriteThreads, 4) k_kv8_append(WriteArgs a) {
-    __shared__ uint32_t red[kWriteThreads / 32];
-    __shared__ __align__(16) uint8_t code[kVPitch * 256];
+template <int HD>
+__global__ void __launch_bounds__(2 * HD, 512 / HD) k_kv8_append(WriteArgs a) {
+    constexpr int kThreads = 2 * HD;                                 // one piece of a block each
+    __shared__ uint32_t red[kThreads / 32];
+    __shared__ __align__(16) uint8_t code[kVPitch * HD];
     __shared__ Turn turn;
-    const int b = blockIdx.x >> 1, h = blockIdx.y, s = blockIdx.z;
+    const int b = (blockIdx.x >> 1) * a.run, h = blockIdx.y, s = blockIdx.z;
     const KvView w = view(a.c, s, h);
     pdl_wait();
     const Plan p = plan_of(a, s, w);
     pdl_trigger();
     if (p.bad || (b > 0 && b >= p.full) || (p.cut && b == 0 && bad_table(w, p))) return;   // a cut reads through the entry
     if (blockIdx.x & 1)
-        append_block<true>(a, s, h, w, p, b, red, code, turn);
+        append_blocks<true, HD, kThreads>(a, s, h, w, p, b, red, code, turn);
     else
-        append_block<false>(a, s, h, w, p, b, red, code, turn);
+        append_blocks<false, HD, kThreads>(a, s, h, w, p, b, red, code, turn);
 }
 __global__ void __launch_bounds__(64) k_kv8_count(WriteArgs a) {
     const int s = blockIdx.y;
@@ -1771,13 +1809,23 @@ int write_rows(const dfl_kv8 *c, const int32_t *len, const int32_t *cnt, int row
     if ((rc = check_rows(c, k, ld, c->n_kv)) || (rc = check_rows(c, v, ld, c->n_kv))) return rc;
     if (!commit && rows > DFL_MAX_ROWS) return DFL_E_UNSUPPORTED;
     if (rows > kBlk * c->n_blocks) return DFL_E_CAPACITY;
-    WriteArgs a{*c, len, cnt, k, v, ld, rows, commit};
-    // Up to 64 rows complete three blocks at most: one launch. More rows take a launch with a CTA for each block and a short
-    // one behind it: at 1024 rows of 8 heads of 128 they take 8 us, one CTA a head alone 260 us.
+    WriteArgs a{*c, len, cnt, k, v, ld, rows, commit, 1};
+    // Up to 64 rows complete three blocks at most: one launch. More rows take a launch with a CTA for each run of blocks and a
+    // short one behind it: at 1024 rows of 8 heads of 128 they take 7 us, one CTA a head alone 260 us.
     if (!commit || rows <= 64) {
-        return launched(launch_pdl(k_kv8_write, dim3(c->n_kv, c->n_seq), dim3(kWriteThreads), 0, s, a));
+        const dim3 grid(c->n_kv, c->n_seq);
+        return launched(c->head_dim == 64    ? launch_pdl(k_kv8_write<64>, grid, dim3(kWriteThreads), 0, s, a)
+                        : c->head_dim == 128 ? launch_pdl(k_kv8_write<128>, grid, dim3(kWriteThreads), 0, s, a)
+                                             : launch_pdl(k_kv8_write<256>, grid, dim3(kWriteThreads), 0, s, a));
     }
-    const int l = launched(launch_pdl(k_kv8_append, dim3(2 * ((kTail + rows) / kBlk), c->n_kv, c->n_seq), dim3(kWriteThreads), 0, s, a));
+    const int blocks = (kTail + rows) / kBlk;
+    // runs of up to 4 blocks, as long as the part's 152 SMs still get four CTAs each (8 x 8192 rows of 8 heads of 128: 142 us,
+    // with a block a CTA 173)
+    a.run = int(std::min<size_t>(4, std::max<size_t>(1, (size_t)2 * blocks * c->n_kv * c->n_seq / (4 * 152))));
+    const dim3 grid(2 * ((blocks + a.run - 1) / a.run), c->n_kv, c->n_seq);
+    const int l = launched(c->head_dim == 64    ? launch_pdl(k_kv8_append<64>, grid, dim3(128), 0, s, a)
+                           : c->head_dim == 128 ? launch_pdl(k_kv8_append<128>, grid, dim3(256), 0, s, a)
+                                                : launch_pdl(k_kv8_append<256>, grid, dim3(512), 0, s, a));
     return l ? l : launched(launch_pdl(k_kv8_count, dim3(c->n_kv, c->n_seq), dim3(64), 0, s, a));
 }
 
