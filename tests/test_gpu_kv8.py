@@ -121,6 +121,18 @@ def test_append_ragged_counts(torch):
     p.check_state()
 
 
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_append_of_many_blocks(torch, hd):
+    """Enough blocks that a CTA seals several, behind contexts that end inside a block, and cut back over what was sealed."""
+    p = Pair(torch, 8, 8, hd, 24, seed=hd + 1)
+    p.write(47, cnt=[0, 1, 31, 32, 33, 40, 47, 47])
+    p.write(700, cnt=[700, 699, 64, 65, 0, 1, 700, 333])
+    p.check_state()
+    p.len = np.minimum(p.len, [600, 31, 64, 70, 20, 41, 97, 380]).astype(np.int32)
+    p.write(620, cnt=[100, 620, 620, 33, 500, 0, 620, 31])
+    p.check_state()
+
+
 @pytest.mark.parametrize("hd", [64, 256])
 def test_staged_rows_roll_back_and_seal_when_committed(torch, hd):
     """A walk of stages and commits of every size: blocks are sealed by the stage after the commit that completes them."""
