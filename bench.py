@@ -132,9 +132,9 @@ def e4b_workload(args):
                 "l2": "weights streamed per step (6.4 GB) exceed the 129 MB L2"}
 
 
-def load_engine(pc, keep=False, workers=None, prefill_rows=0):
+def load_engine(pc, keep=False, workers=None, prefill_rows=0, kv8=0):
     from dflash_speculative_decode_gb300 import Engine, config_from_pair
-    eng = Engine(config_from_pair(pc, prefill_rows=prefill_rows))
+    eng = Engine(config_from_pair(pc, prefill_rows=prefill_rows, kv8=kv8))
     kept = {} if keep else None
     workers = workers or min(16, os.cpu_count() or 1)
     t0 = time.time()
@@ -684,11 +684,15 @@ def bench_long(args):
     tokens must equal them exactly, since sampling is keyed by seed and absolute position and a row's
     logits do not depend on the rows verified beside it. A's two runs must give the same tokens
     (FastFlowLM PR #899 "gemma4e-dflash-flash", "Changes": the pinned prefix is restored, never
-    overwritten). Prints one JSON line (not the bench line)."""
+    overwritten). With --kv8 the full layers' planes are held in 8 bits and prompts are ingested in passes
+    of 16 rows; a position's logits then depend on how its passes were cut, so the plain and the speculative
+    tokens may part. Prints one JSON line (not the bench line)."""
     import torch
     from dflash_speculative_decode_gb300 import build
     build.build()
     T = args.temperature
+    if args.kv8:
+        args.prefill_rows = 0
     requests = [("A", 1, 11), ("B", 2, 12), ("A", 1, 11)]   # (name, prompt request id, sampling seed)
     clk = Clocks(0)
     clk.start()
@@ -698,7 +702,7 @@ def bench_long(args):
         if ctx <= args.prefix + 16:
             raise SystemExit(f"--long-ctx {ctx} must exceed --prefix {args.prefix} + 16")
         pc = gen.e4b_pair(max_ctx=ctx + args.gen + 64)
-        eng, _, t_load = load_engine(pc, prefill_rows=args.prefill_rows)
+        eng, _, t_load = load_engine(pc, prefill_rows=args.prefill_rows, kv8=int(args.kv8))
         V, L = pc.target.vocab, pc.max_ctx + 32
         prefix = gen.prompt(V, args.prefix, request=100)
         empty = eng.dfl_snapshot()
@@ -774,7 +778,7 @@ def bench_long(args):
     print(json.dumps({"workload": "long-context sampled serving, e4b pair, pinned prefix, requests A, B, A",
                       "metric": "decode tokens/s (device-timed speculative passes, prefill excluded)",
                       "temperature": T, "prefix": args.prefix, "generated_per_request": args.gen,
-                      "corruption_p": args.p, "block": 8, "prefill_rows": args.prefill_rows,
+                      "corruption_p": args.p, "block": 8, "prefill_rows": args.prefill_rows, "kv8": bool(args.kv8),
                       "dtype": "fp32 activations, Q4_1/bf16 weights",
                       "data": "synthetic (seeded random-init weights of the E4B-shaped pair, uniform prompts)",
                       "results": results, "clocks": clocks}), flush=True)
@@ -875,6 +879,7 @@ def main():
     ap.add_argument("--long-ctx", default="4096,16384", help="contexts of --workload long")
     ap.add_argument("--prefix", type=int, default=512, help="pinned prefix tokens of --workload long")
     ap.add_argument("--temperature", type=float, default=0.8, help="sampling temperature of --workload long")
+    ap.add_argument("--kv8", action="store_true", help="--workload long with the full layers' planes in 8 bits")
     ap.add_argument("--draft-ctx", default="30,1024,4096", help="contexts of --workload draft")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-sweep", action="store_true", help="leave the product sweep out of the bench line")

@@ -1224,6 +1224,9 @@ int ready(dfl_ctx *c) {
     return DFL_OK;
 }
 
+// of a snapshot's configuration; without 8-bit planes the same as before there were any, so that older snapshots restore
+uint64_t config_hash(const dfl_config &g) { return fnv1a(&g, g.kv8 ? sizeof g : offsetof(dfl_config, kv8)); }
+
 size_t snapshot_size(const dfl_ctx *c, int n, int draft_n) {
     const dfl_config &g = c->cfg;
     size_t b = sizeof(SnapHeader);
@@ -1536,7 +1539,7 @@ int dfl_snapshot(dfl_ctx *c, void *dst, size_t bytes) {
     SnapHeader hdr{};
     hdr.magic = kSnapMagic;
     hdr.version = 1;
-    hdr.cfg_hash = fnv1a(&c->cfg, sizeof(dfl_config));
+    hdr.cfg_hash = config_hash(c->cfg);
     hdr.n = c->n;
     hdr.draft_n = c->draft_n;
     hdr.bytes = need;
@@ -1581,7 +1584,7 @@ int dfl_restore(dfl_ctx *c, const void *src, size_t bytes) {
     DFL_CK(cudaStreamSynchronize(c->stream));
     const dfl_config &g = c->cfg;
     if (hdr.magic != kSnapMagic || hdr.version != 1) return fail(c, DFL_E_INVALID_ARG, "not a snapshot");
-    if (hdr.cfg_hash != fnv1a(&c->cfg, sizeof(dfl_config))) return fail(c, DFL_E_INVALID_ARG, "snapshot of another configuration");
+    if (hdr.cfg_hash != config_hash(c->cfg)) return fail(c, DFL_E_INVALID_ARG, "snapshot of another configuration");
     if (hdr.n < 0 || hdr.n > g.max_ctx || hdr.draft_n < 0 || hdr.draft_n > hdr.n)
         return fail(c, DFL_E_INVALID_ARG, "corrupt snapshot header");
     const size_t need = snapshot_size(c, hdr.n, hdr.draft_n);
