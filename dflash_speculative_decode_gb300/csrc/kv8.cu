@@ -279,7 +279,8 @@ __device__ __forceinline__ void settle(const WriteArgs &a, int s, const KvView &
     if (threadIdx.x == 0) *w.sealed = p.z + p.full;
 }
 
-// One launch for a call of few rows, one CTA per head.
+// One launch for a call of few rows, one CTA per head: latency, of the counts, then the rows, then the stores. 8 staged rows
+// for 4 sequences of 8 heads of 128 take 4.0 us.
 template <int HD>
 __global__ void __launch_bounds__(kWriteThreads) k_kv8_write(WriteArgs a) {
     __shared__ uint32_t red[kWriteThreads / 32];
@@ -372,7 +373,9 @@ struct ReadArgs {
     int rows;
 };
 
-// One CTA per 32-token block of the range and head: grid (blocks, heads, sequences).
+// One CTA per 32-token block of the range and head: grid (blocks, heads, sequences). A code is expanded by one subtraction and
+// one product, rounded once; values turn through shared memory, so that all stores are of 16 bytes. Bound by its stores, 4 of
+// the 5 bytes that a value costs: 8 x 8192 rows of 8 heads of 128 in 118 us, 5.7 TB/s, 84 % of a plain copy's.
 __global__ void __launch_bounds__(256) k_kv8_read(ReadArgs a) {
     __shared__ uint32_t vcode[256 * 9];
     const int h = blockIdx.y, s = blockIdx.z, hd = a.c.head_dim;
@@ -504,11 +507,18 @@ __device__ __forceinline__ void seen(const AttnKvArgs &a, const Span &p, int m, 
 // (2^7 and more for the row's largest, times the block's value scale over the largest one) enter as two fp16
 // halves, hi + lo, which hold 22 bits, and nothing below 2^-25.
 //
+// These are the older tensor instructions on purpose. The fifth generation's take their operands from shared or tensor
+// memory, so every code would be written there a second time at twice its size; a unit has 1 to 16 rows (32 columns with both
+// halves), for which the time is loads, expansion and the softmax between the products. Their rate comes near to a bound
+// only where 16 rows share each code: 8 clocks an instruction of 256 codes, 8 rows and one half are 74 % of the time that HBM
+// takes for the codes (8 sequences of 16384 tokens and 16 heads of 128: 59 of 80 us).
+//
 // Fragment order. A thread (g = lane / 4, t = lane % 4) loads 16 consecutive channels of a key at once, so
 // channel 64 c + 16 t + 4 j + e is input 2t + e (e < 2) or 2t + 6 + e of the product's step 4 c + j, and
-// the query halves are laid out to match. Row r of 8-key matrix j holds key 8 (r / 2) + 2 j + r % 2: the
+// the query halves are laid out to match. Row r of 8-key matrix j holds key 8 (r / 2) + 2 j + r % 2 of a block: the
 // transposed weights of matrices 2 s and 2 s + 1 are then the inputs of step s of the second product, whose
-// thread t takes the keys 8 t + 4 s .. + 3, 8 consecutive codes of a value channel for both steps.
+// thread t takes the keys 8 t + 4 s .. + 3, 8 consecutive codes of a value channel for both steps. A warp with half a
+// block's keys has the matrices 0 and 1, or 2 and 3.
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kTop = 7.f;    // log2 of the weight at a row's maximum
 
@@ -663,9 +673,15 @@ struct QueryRows {      // a warp takes every kWarps-th row of the group
 // One CTA's piece of a unit: 8 NT query rows (row r = m * group + i of the head's rows), its coded blocks and perhaps the
 // tail. Groups of four warps take every kGroups-th turn of blocks, each group with a running softmax of its own, merged at
 // the end. In a turn of two or four blocks each warp takes a quarter of the keys for the first product and, for the second,
-// a quarter of the value channels over all keys; the weights pass through shared memory between them. So a warp's sums are small, its code is short (a short
-// call spends much of its time on fetching code), and each code is read from shared memory and expanded once in the CTA.
-// Keys and values come through a ring of the warp's own (16-byte asynchronous copies): what a warp copies only it reads.
+// a quarter of the value channels over all keys; the weights pass through shared memory between them. So a warp's sums are
+// small, its code is short (a short call spends much of its time on fetching code), and each code is read from shared
+// memory and expanded once in the CTA. Keys and values come through a ring of the warp's own (16-byte asynchronous copies):
+// what a warp copies only it reads.
+// What bounds it: with many sequences the issue of instructions and the latency between the steps of a turn at 16 warps an SM
+// (32 query heads over 8 of 128, one token of 64 sequences of some 5000: 131 us, 5.1 TB/s, 75 % of a plain copy's; verifies of
+// 8 rows of 8 sequences of 16384 and 16 heads of 128, two halves of 16 columns: 157 us, 3.4 TB/s, 51 %). With one
+// sequence a CTA has one to three turns, and the time is the launch, the first loads (table, then scales and codes), some
+// 3 us a turn and the merge: 16384 tokens of 2 heads of 256 take 12.6 us for a token, 27 us for 8 rows of 6 heads each.
 template <int HD, int NT>
 __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, const Piece &u, QueryRows<HD, NT> &qr, uint8_t *smem, AttnShared<HD, NT> &sh) {
     using S = AttnShape<HD, NT>;
@@ -1013,7 +1029,8 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         group_sync(grp);
         const uint8_t *V = take + g * kBlk + 8 * t;
         // the turn's products have sums of their own, added to the running ones in fp32: the tensor cores cut off what they add
-        // below the last place, which over a long context would add up (8e-6 against 3e-6 at 4096 tokens a group)
+        // below the last place, which over a long context would add up (16384 tokens: 5e-6 to 8e-6 of the outputs, 6e-7 to 1.2e-6
+        // with sums of a turn's own)
         constexpr int kMs = kMt < 2 ? kMt : 2;                       // channel tiles at once
 #pragma unroll
         for (int m0 = 0; m0 < kMt; m0 += kMs) {
@@ -1386,6 +1403,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     }
 }
 
+// Latency: some 5 us behind the attention, the parts' states, then their sums, with all loads of a kind at once.
 // Merges the parts of a unit's rows in a fixed order (grid x < row_ctas), and adds row 0's share of 256 blocks to the
 // scores (grid x behind them, row group 0). HD / 4 threads take four channels each of a row; with `apart_rows` all threads of
 // a CTA take one row and share out its parts (few units of many parts), else each such group takes a row of its own.
@@ -1560,7 +1578,10 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
 // How a call's work is cut: row groups of 8 rows, or of 16 (whose codes are expanded once for two products) where a head
 // has more than 8. Up to as many units as half the CTAs that fit the part's 152 SMs at once: splits of a unit's blocks, and
 // a CTA of its own for the tail or not; all in one wave (CTAs of a second one were measured to wait for tens of microseconds
-// although slots were free). Costs are in turns; a tail inside a CTA is worth about 2. More units: shares.
+// although slots were free). Costs are in turns; a tail inside a CTA is worth about 2. More units: shares, which leave no slot
+// idle but cost some 32 blocks' time more (finding the share, pieces of two or three units, their parts' merge). So shares also
+// take long contexts where whole splits leave slots idle: 128 units of 512 blocks on 304 slots take 100 us in shares and 115 in
+// splits (16 rows of 128: 138 and 159), but 72 units 71 and 64, and 128 units of 128 blocks 41 and 40.
 struct AttnCut {
     int nt, groups, splits, apart, share, ctas;
     size_t units, o_bytes, ml_bytes, bad_bytes, lse_bytes, total;
@@ -1577,10 +1598,8 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
     const int step = wide ? AttnShape<256, 2>::kStep : c->head_dim == 256 ? AttnShape<256, 1>::kStep : AttnShape<128, 1>::kStep;
     const int slots = wide ? kMaxCtas / 2 : kMaxCtas, blocks = window ? std::min(c->n_blocks, window / kBlk + 2) : c->n_blocks;
     t.splits = 1;
-    if (t.units > (size_t)slots / 2) {
-        t.share = 1;
-        t.ctas = slots;
-    } else {
+    t.share = t.units > (size_t)slots / 2;
+    if (!t.share) {
         const int most = std::min(kMaxSplits, (blocks + step - 1) / step);
         int best = 0;
         for (int apart = 0; apart < 2; ++apart)
@@ -1588,7 +1607,11 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
                 const int cost = (blocks + step * n - 1) / (step * n) + (apart ? 0 : 2);
                 if (!best || cost < best) best = cost, t.splits = n, t.apart = apart;
             }
+        // a CTA's blocks in splits, and in shares: long ones only, and what is saved
+        const size_t whole = (size_t)best * step, even = t.units * (blocks + kTailWeight) / slots;
+        t.share = even >= 160 && whole >= even + 32;
     }
+    if (t.share) t.splits = 1, t.apart = 0, t.ctas = slots;
     const size_t parts = t.share ? t.units + t.ctas : t.units * (t.splits + t.apart);
     t.o_bytes = up256(parts * 8 * t.nt * c->head_dim * 4);
     t.ml_bytes = up256(parts * 8 * t.nt * 8);
@@ -1666,7 +1689,8 @@ __device__ __forceinline__ int block_scan(int v, int *sums) {
     return before + x - v;
 }
 
-// One CTA per head; a call reads and writes a few bytes a block, so its time is the latency of the steps. The score of
+// One CTA per head; a call reads and writes a few bytes a block, so its time is the latency of the steps: 5.3 us at 512 blocks,
+// 10.3 us at 4096 (64 heads). The score of
 // the last block kept by choice is found digit by digit (8 bits at a time, by a histogram of the candidates that agree
 // so far); blocks above it are kept, and as many of those equal to it as there is room for, the lowest indexes first.
 // Then the table is partitioned in order: a thread takes a run of consecutive blocks, so two prefix sums over the

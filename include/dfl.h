@@ -450,12 +450,12 @@ int64_t dfl_kv8_attn_scratch_bytes(const dfl_kv8 *c, int n_q, int rows, int wind
  * are fp32; queries and weights enter the tensor cores as two fp16 halves each, which hold 22 bits.
  * What a weight adds is held to about 2^-32 of the row's largest weight times the largest |value| that it
  * meets, which is what bounds an output that is small beside them. One call gives the same bits each time.
- * Where heads and sequences are so many that a call shares its work out evenly (n_seq * n_kv * groups of
- * rows above 152, or 76 for the widest), the last bits of a sequence may depend on the other sequences'
- * lengths, as they decide where its sums are cut; below that they depend on nothing else in the batch. len
- * must not lie below what is sealed (dfl_kv8_stage cuts back). out overlaps none of the inputs. Calls on
- * one scratch (DEVICE, 256-byte aligned) must not overlap on the GPU; nothing is kept in it from one call
- * to the next. */
+ * Where heads, rows and sequences are so many that a call shares its work out evenly (n_seq * n_kv * groups
+ * of 8 or 16 rows above 152, above 76 for 9 rows and more of 256 channels, and less where the capacity is
+ * long), the last bits of a sequence may depend on the other sequences' lengths, as they decide where its
+ * sums are cut; below that they depend on nothing else in the batch. len must not lie below what is sealed
+ * (dfl_kv8_stage cuts back). out overlaps none of the inputs. Calls on one scratch (DEVICE, 256-byte
+ * aligned) must not overlap on the GPU; nothing is kept in it from one call to the next. */
 int dfl_kv8_attn(const dfl_kv8 *c, const float *q, int64_t ldq, int n_q, int rows, const int32_t *len,
                  const int32_t *cnt, int window, int causal, float scale, int score, float *out, int64_t ldo,
                  void *scratch, size_t scratch_bytes, void *cuda_stream);

@@ -533,6 +533,20 @@ def test_attn_of_many_sequences(torch, S, n_kv, n_q, hd, rows, held):
     p.attn(n_q, rows, cnt=n, window=33, causal=False)
 
 
+@pytest.mark.parametrize("S,n_kv,n_q,hd,rows,blocks", [(16, 8, 32, 64, 3, 514), (32, 2, 12, 256, 2, 514)])
+def test_attn_shared_out_by_capacity(torch, S, n_kv, n_q, hd, rows, blocks):
+    """Fewer units, but a capacity so long that whole splits would leave CTAs idle; the sequences themselves are short, and one is long."""
+    p = Pair(torch, S, n_kv, hd, blocks, seed=S)
+    cnt = p.rng.integers(0, 200, S)
+    cnt[[0, 3, S - 1]] = 1300, 0, 31
+    p.write(1300, cnt=cnt)
+    n = p.rng.integers(0, rows + 1, S)
+    n[[0, 3, S - 1]] = rows
+    p.write(rows, cnt=n, commit=False)
+    p.attn(n_q, rows, cnt=n, score=True)
+    p.attn(n_q, rows, cnt=n, causal=False)
+
+
 def test_attn_of_more_sequences_than_threads(torch):
     """700 sequences, a few of which have rows: the first, the last, and some on either side of 256 and 512."""
     p = Pair(torch, 700, 1, 64, 6, seed=31)
