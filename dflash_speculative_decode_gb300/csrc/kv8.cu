@@ -9,6 +9,7 @@
 // dimension, values with the tokens innermost).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "dfl.h"
@@ -522,7 +523,7 @@ __device__ __forceinline__ void seen(const AttnKvArgs &a, const Span &p, int m, 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kTop = 7.f;    // log2 of the weight at a row's maximum
 
-template <int HD, int NT>
+template <int HD, int NT, bool PK = false>
 struct AttnShape {
     // Groups of four warps, 16 warps an SM of 128 registers a thread. A warp takes kM tiles of 16 keys at a time: two, which
     // halves what a turn costs besides its products and the reads of the query halves, or one where the rings would not fit.
@@ -533,13 +534,15 @@ struct AttnShape {
     static constexpr int kGroups = HD == 256 && NT == 2 ? 4 : 2;
     static constexpr int kWarps = 4 * kGroups;
     static constexpr int kStep = kGroups * kTurn;                    // blocks that a CTA takes at a time
-    static constexpr int kRing = (HD == 64 ? 5 : 3) - (HD < 256 && NT == 2 ? 1 : 0);   // units under way, as many as two CTAs have room for
-    static constexpr int kQBytes = NT * 8 * HD * 4;                  // query halves
-    static constexpr int kPBytes = kGroups * 2 * kTurn * NT * 512;   // a turn's weights, for each group
+    // Units under way, as many as the CTAs of an SM have room for: two CTAs, or in shares of up to 4 rows three (80 registers).
+    static constexpr int kShareCtas = PK && HD < 256 ? 3 : kCtas;
+    static constexpr int kRing = (HD == 64 ? 5 : 3) - (HD < 256 && (NT == 2 || PK) ? 1 : 0);
+    static constexpr int kQBytes = NT * 8 * HD * (PK ? 2 : 4);                  // query halves
+    static constexpr int kPBytes = kGroups * 2 * kTurn * NT * (PK ? 256 : 512);   // a turn's weights, for each group
     static constexpr int kSmem = kQBytes + kPBytes + kWarps * kRing * kUnit;
     static_assert(kGroups * 8 * NT * (HD + 4) * 4 <= kSmem, "the merge's use of the shared memory");
     static constexpr int kTailPitch = kTail + 4;                     // of the tail's weights [rows][48 tokens], fp32
-    static_assert(kTail * HD * 4 <= 4 * kRing * kUnit && 8 * NT * kTailPitch * 4 <= kPBytes / kGroups, "the tail's: keys or values in a group's rings");
+    static_assert(kTail * HD * 4 <= 4 * kRing * kUnit && (PK ? 4 : 8 * NT) * kTailPitch * 4 <= kPBytes / kGroups, "the tail's: keys or values in a group's rings");
 };
 
 // the four warps of a group: a barrier, and one that also tells whether x holds anywhere in the group
@@ -625,8 +628,10 @@ template <int W>
 __device__ __forceinline__ int splits_of(int splits, int coded) { return min(splits, (coded + W - 1) / W); }
 
 // Shares: the work in the order of its units, each weighing its coded blocks and, behind them, its tail as
-// kTailWeight. CTA b of G takes the weights [W b / G, W (b + 1) / G).
-constexpr int kTailWeight = 8;
+// kTailWeight: what a unit costs besides its blocks, the tail, its first loads and the groups' merge, in blocks. (64 sequences
+// of some 5000 tokens, 8 heads of 128, one token, and 8 of 16384 and 16 heads, 8 rows: 126 and 136 us at 8, 119 and 129 at 40,
+// 122 and 135 at 64.) CTA b of G takes the weights [W b / G, W (b + 1) / G).
+constexpr int kTailWeight = 40;
 __device__ __forceinline__ long weight_of(const AttnKvArgs &a, const Span &p) { return (long)a.c.n_kv * p.groups * (p.coded + kTailWeight); }
 template <int W>
 __device__ __forceinline__ int shares_of(const AttnKvArgs &a, long work) { return int(min((long)a.ctas, (work + W - 1) / W)); }
@@ -677,17 +682,25 @@ struct QueryRows {      // a warp takes every kWarps-th row of the group
 // small, its code is short (a short call spends much of its time on fetching code), and each code is read from shared
 // memory and expanded once in the CTA. Keys and values come through a ring of the warp's own (16-byte asynchronous copies):
 // what a warp copies only it reads.
-// What bounds it: with many sequences the issue of instructions and the latency between the steps of a turn at 16 warps an SM
-// (32 query heads over 8 of 128, one token of 64 sequences of some 5000: 131 us, 5.1 TB/s, 75 % of a plain copy's; verifies of
-// 8 rows of 8 sequences of 16384 and 16 heads of 128, two halves of 16 columns: 157 us, 3.4 TB/s, 51 %). With one
+// What bounds it: with many sequences the issue of instructions and the latency between the steps of a turn at 16 or 24 warps an SM
+// (32 query heads over 8 of 128, one token of 64 sequences of some 5000: 120 us, 5.5 TB/s, 82 % of a plain copy's; verifies of
+// 8 rows of 8 sequences of 16384 and 16 heads of 128, two halves of 16 columns: 129 us, 4.2 TB/s, 62 %). With one
 // sequence a CTA has one to three turns, and the time is the launch, the first loads (table, then scales and codes), some
 // 3 us a turn and the merge: 16384 tokens of 2 heads of 256 take 12.6 us for a token, 27 us for 8 rows of 6 heads each.
-template <int HD, int NT>
+//
+// PK, for up to 4 rows: the query's lo halves take the columns 4..7 that no row needs, so one product does for both halves, in
+// both products. The thread pairs t and t + 2 then hold the same two rows: after the first product each adds up the halves of
+// one of the tile's two keys a thread, so that the softmax's work is halved too. The 64 sequences above: 132 us without, 129
+// with, 126 with the third CTA an SM that its fewer registers allow (120 since units count their tails rightly).
+template <int HD, int NT, bool PK>
 __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, const Piece &u, QueryRows<HD, NT> &qr, uint8_t *smem, AttnShared<HD, NT> &sh) {
-    using S = AttnShape<HD, NT>;
+    using S = AttnShape<HD, NT, PK>;
     constexpr int RG = 8 * NT, kW = S::kWarps, kG = S::kGroups, kRing = S::kRing, kUnit = S::kUnit, kPitch = HD + 4, kMt = HD / 64, kM = S::kM, kTurn = S::kTurn, kWin = 32 / kTurn;
     const int s = u.s, h = u.h, rg = u.rg;
+    static_assert(!PK || NT == 1, "one tile of columns holds both halves");
+    constexpr int kE = PK ? 2 : 4;                                   // logits a thread has of a tile
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int t2 = PK ? 2 * (t & 1) : 2 * t, low = PK ? t >> 1 : 0;  // this thread's rows t2 and t2 + 1 of a tile, and (PK) its key of two
     // first product: block `mine` of the turn, all its keys (kM = 2) or those with bit 2 = key_half
     const int grp = warp >> 2, wq = warp & 3, mine = kM == 2 ? wq : wq >> 1, key_half = kM == 2 ? 0 : wq & 1;
     const size_t head = (size_t)s * a.c.n_kv + h, head_blocks = head * a.c.n_blocks;
@@ -695,7 +708,9 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
     const int n = u.x1 - u.x0, first = p.b0 + u.x0 + kTurn * grp;    // coded blocks; turn i of this group begins with first + kTurn kG i
     const int turns = (n - kTurn * grp + kTurn * kG - 1) / (kTurn * kG);   // <= 0: none
     uint8_t *ring = smem + S::kQBytes + S::kPBytes + warp * kRing * kUnit;
-    uint4 *pbuf = reinterpret_cast<uint4 *>(smem + S::kQBytes + grp * (S::kPBytes / kG)) + lane;
+    using Weights = typename std::conditional<PK, uint2, uint4>::type;   // a thread's of a step
+    constexpr int kQ = PK ? 2 : 4;                                   // pieces of 16 query inputs: hi, and (not PK) lo
+    Weights *pbuf = reinterpret_cast<Weights *>(smem + S::kQBytes + grp * (S::kPBytes / kG)) + lane;
     const uint4 *qf = reinterpret_cast<const uint4 *>(smem) + lane;
     const bool keep_lse = a.score && rg == 0;
 
@@ -797,18 +812,29 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             uint32_t hi = 0, lo = 0;
             if (fin) halves2(qr.x[j][i].x * f, qr.x[j][i].y * f, hi, lo);
             const int d = 2 * lane;                                  // of chunk i
-            uint32_t *dst = reinterpret_cast<uint32_t *>(smem) + (((i * NT + r / 8) * 4 + ((d & 15) >> 3)) * 32 + (r & 7) * 4 + (d >> 4)) * 4 + ((d & 7) >> 1);
+            uint32_t *dst = reinterpret_cast<uint32_t *>(smem) + (((i * NT + r / 8) * kQ + ((d & 15) >> 3)) * 32 + (r & 7) * 4 + (d >> 4)) * 4 + ((d & 7) >> 1);
+            if (PK && r >= 4) continue;
             dst[0] = hi;
-            dst[2 * 32 * 4] = lo;
+            dst[PK ? 4 * 4 * 4 : 2 * 32 * 4] = lo;
         }
     }
     __syncthreads();
-    auto scale_of = [&](int nt) { return *reinterpret_cast<const float2 *>(&sh.q_scale[8 * nt + 2 * t]); };
+    auto scale_of = [&](int nt) { return *reinterpret_cast<const float2 *>(&sh.q_scale[8 * nt + t2]); };
     // the tokens lo..hi-1 that row 8 nt + 2 t + e sees; all, if it does not exist: nothing reads its sums
     auto row_sees = [&](int nt, int e, int &lo, int &hi) {
-        const int r = 8 * nt + 2 * t + e;
+        const int r = 8 * nt + t2 + e;
         lo = 0, hi = 1 << 30;
         if (r < live) seen(a, p, (rg * RG + r) / per, lo, hi);
+    };
+    // PK: both halves of two of a tile's logits, x[0..1] of key 2 low (the other two go to the thread that has their other half)
+    auto join = [&](float (&x)[4]) {
+        const float y0 = __shfl_xor_sync(0xffffffffu, low ? x[0] : x[2], 2), y1 = __shfl_xor_sync(0xffffffffu, low ? x[1] : x[3], 2);
+        x[0] = (low ? x[2] : x[0]) + y0;
+        x[1] = (low ? x[3] : x[1]) + y1;
+    };
+    auto rows_sum = [&](float x) {                                   // over all threads that have the row
+        if (PK) x += __shfl_xor_sync(0xffffffffu, x, 2);
+        return group_sum(x);
     };
     // tokens all_lo..all_hi-1 are seen by every row of the group that exists
     int all_lo, all_hi, dummy;
@@ -829,15 +855,18 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         for (int mt = 0; mt < kMt; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
     }
     // Renews mx by the logits y of the group (y == -inf: not seen), and rescales the sums. The four warps call it together.
-    auto renew = [&](const float (&y)[kM][NT][4]) {
+    auto renew = [&](const float (&y)[kM][NT][kE]) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-            for (int m = 0; m < kM; ++m) t0 = fmaxf(t0, fmaxf(y[m][nt][0], y[m][nt][2])), t1 = fmaxf(t1, fmaxf(y[m][nt][1], y[m][nt][3]));
+            for (int m = 0; m < kM; ++m)
+#pragma unroll
+                for (int k = 0; k < kE; k += 2) t0 = fmaxf(t0, y[m][nt][k]), t1 = fmaxf(t1, y[m][nt][k + 1]);
+            if (PK) t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2)), t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
             t0 = group_max(t0);
             t1 = group_max(t1);
-            if (g == 0) sh.top[grp][wq][8 * nt + 2 * t] = t0, sh.top[grp][wq][8 * nt + 2 * t + 1] = t1;
+            if (g == 0 && low == 0) sh.top[grp][wq][8 * nt + t2] = t0, sh.top[grp][wq][8 * nt + t2 + 1] = t1;
         }
         group_sync(grp);
 #pragma unroll
@@ -846,7 +875,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             for (int e = 0; e < 2; ++e) {
                 float now = mx[nt][e];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) now = fmaxf(now, sh.top[grp][i][8 * nt + 2 * t + e]);
+                for (int i = 0; i < 4; ++i) now = fmaxf(now, sh.top[grp][i][8 * nt + t2 + e]);
                 const float f = mx[nt][e] == now ? 1.f : ex2(mx[nt][e] - now);
                 mx[nt][e] = now;
                 l[nt][e] *= f;
@@ -909,8 +938,8 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                 uint32_t qh[NT][4], ql[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    *reinterpret_cast<uint4 *>(qh[nt]) = qf[((c * NT + nt) * 4 + half) * 32];
-                    *reinterpret_cast<uint4 *>(ql[nt]) = qf[((c * NT + nt) * 4 + 2 + half) * 32];
+                    *reinterpret_cast<uint4 *>(qh[nt]) = qf[((c * NT + nt) * kQ + half) * 32];
+                    if (!PK) *reinterpret_cast<uint4 *>(ql[nt]) = qf[((c * NT + nt) * kQ + 2 + half) * 32];
                 }
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
@@ -922,19 +951,25 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                         af[m][2] = codes_hi(kw[2 * m][j]), af[m][3] = codes_hi(kw[2 * m + 1][j]);
                     }
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < (PK ? 1 : 2); ++part)
 #pragma unroll
                         for (int m = 0; m < kM; ++m)
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma_f16(xs[part % kParts][m][nt], af[m], part ? ql[nt][2 * jj] : qh[nt][2 * jj], part ? ql[nt][2 * jj + 1] : qh[nt][2 * jj + 1]);
+                                mma_f16(xs[(PK ? j : part) % kParts][m][nt], af[m], part ? ql[nt][2 * jj] : qh[nt][2 * jj], part ? ql[nt][2 * jj + 1] : qh[nt][2 * jj + 1]);
                 }
             }
         }
         __syncwarp();
         taken();
         issue(2 * i + kRing);
-        float y[kM][NT][4], peak = -INFINITY;                        // exponents of the weights
+        if (kParts == 2)
+#pragma unroll
+            for (int k = 0; k < kM * NT * 4; ++k) (&x[0][0][0])[k] += (&xs[kParts - 1][0][0][0])[k];
+        if (PK)
+#pragma unroll
+            for (int m = 0; m < kM; ++m) join(x[m][0]);
+        float y[kM][NT][kE], peak = -INFINITY;                       // exponents of the weights
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -943,10 +978,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
                 for (int m = 0; m < kM; ++m)
 #pragma unroll
-                    for (int k = e; k < 4; k += 2) {
-                        if (kParts == 2) x[m][nt][k] += xs[kParts - 1][m][nt][k];
-                        y[m][nt][k] = fmaf(x[m][nt][k], z, less);
-                    }
+                    for (int k = e; k < kE; k += 2) y[m][nt][k] = fmaf(x[m][nt][k], z, less);
             }
         const int pos0 = kBlk * b;
         if (!there || pos0 < all_lo || pos0 + kBlk > all_hi) {
@@ -959,8 +991,8 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
                     for (int m = 0; m < kM; ++m)
 #pragma unroll
-                        for (int k = e; k < 4; k += 2) {
-                            const int pos = pos0 + 8 * (g >> 1) + 4 * (m + key_half) + 2 * (k >> 1) + (g & 1);
+                        for (int k = e; k < kE; k += 2) {
+                            const int pos = pos0 + 8 * (g >> 1) + 4 * (m + key_half) + 2 * (k >> 1 | low) + (g & 1);
                             if (!there || pos < lo || pos >= hi) y[m][nt][k] = -INFINITY;
                         }
                 }
@@ -970,21 +1002,21 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) peak = fmaxf(peak, y[m][nt][k]);
+                for (int k = 0; k < kE; ++k) peak = fmaxf(peak, y[m][nt][k]);
         if (group_or(grp, peak > 15.f)) {                            // seldom, once the maxima have been met
 #pragma unroll
             for (int m = 0; m < kM; ++m)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) y[m][nt][k] = y[m][nt][k] == -INFINITY ? -INFINITY : x[m][nt][k] * (bks * (k & 1 ? scale_of(nt).y : scale_of(nt).x));
+                    for (int k = 0; k < kE; ++k) y[m][nt][k] = y[m][nt][k] == -INFINITY ? -INFINITY : x[m][nt][k] * (bks * (k & 1 ? scale_of(nt).y : scale_of(nt).x));
             renew(y);
 #pragma unroll
             for (int m = 0; m < kM; ++m)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) y[m][nt][k] += mx[nt][k & 1] == -INFINITY ? 0.f : blb + kTop - mx[nt][k & 1];
+                    for (int k = 0; k < kE; ++k) y[m][nt][k] += mx[nt][k & 1] == -INFINITY ? 0.f : blb + kTop - mx[nt][k & 1];
         }
         if (isnan(binv)) {                                           // rows that see the block are NaN, the others take nothing of it
             binv = 0.f;
@@ -1002,16 +1034,16 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
             for (int m = 0; m < kM; ++m)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[m][nt][k] = ex2(y[m][nt][k]);
+                for (int k = 0; k < kE; ++k) y[m][nt][k] = ex2(y[m][nt][k]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float sum = y[0][nt][e] + y[0][nt][2 + e];
-                if (kM == 2) sum += y[kM - 1][nt][e] + y[kM - 1][nt][2 + e];
+                float sum = PK ? y[0][nt][e] : y[0][nt][e] + y[0][nt][kE - 2 + e];
+                if (kM == 2) sum += PK ? y[kM - 1][nt][e] : y[kM - 1][nt][e] + y[kM - 1][nt][kE - 2 + e];
                 l[nt][e] = fmaf(sum, binv, l[nt][e]);
                 if (keep_lse) {
-                    const float total = group_sum(sum) * binv;
-                    const int r = 8 * nt + 2 * t + e;
-                    if (g == 0 && r < per && there) {
+                    const float total = rows_sum(sum) * binv;
+                    const int r = 8 * nt + t2 + e;
+                    if (g == 0 && low == 0 && r < per && there) {
                         put_lse(b, key_half, r, total, mx[nt][e]);
                         if (kM == 2) put_lse(b, 1, r, 0.f, 0.f);     // the block's sum is one
                     }
@@ -1021,8 +1053,14 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             for (int m = 0; m < kM; ++m) {
                 uint4 w;                                             // hi and lo halves of the step's two input pairs
                 halves2(y[m][nt][0], y[m][nt][1], w.x, w.z);
-                halves2(y[m][nt][2], y[m][nt][3], w.y, w.w);
-                pbuf[((kM * wq + m) * NT + nt) * 32] = make_uint4(transpose8x8(w.x), transpose8x8(w.y), transpose8x8(w.z), transpose8x8(w.w));
+                Weights &to = pbuf[((kM * wq + m) * NT + nt) * 32];
+                if constexpr (PK) {                                  // hi in columns 0..3 and lo in 4..7, of both keys
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, low ? w.x : w.z, 2);
+                    to = make_uint2(transpose8x8(low ? other : w.x), transpose8x8(low ? w.z : other));
+                } else {
+                    halves2(y[m][nt][2], y[m][nt][3], w.y, w.w);
+                    to = make_uint4(transpose8x8(w.x), transpose8x8(w.y), transpose8x8(w.z), transpose8x8(w.w));
+                }
             }
         }
         cp_async_wait_groups<kRing - 1>();
@@ -1051,9 +1089,15 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                 for (int st = 0; st < 2; ++st) {
                     uint4 w[NT];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) w[nt] = pbuf[((2 * j + st) * NT + nt) * 32];
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const Weights &from = pbuf[((2 * j + st) * NT + nt) * 32];
+                        if constexpr (PK)
+                            w[nt].x = from.x, w[nt].y = from.y;
+                        else
+                            w[nt] = from;
+                    }
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < (PK ? 1 : 2); ++part)
 #pragma unroll
                         for (int m = 0; m < kMs; ++m)
 #pragma unroll
@@ -1133,10 +1177,13 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const uint2 *f = reinterpret_cast<const uint2 *>(qf + ((c * NT + nt) * 4 + (j >> 1)) * 32) + (j & 1);
-                        const uint2 qh = f[0], ql = f[2 * 32 * 2];
+                        const uint2 *f = reinterpret_cast<const uint2 *>(qf + ((c * NT + nt) * kQ + (j >> 1)) * 32) + (j & 1);
+                        const uint2 qh = f[0];
                         mma_f16(xc[nt], al, qh.x, qh.y);
-                        mma_f16(xc[nt], ah, ql.x, ql.y);
+                        if (!PK) {
+                            const uint2 ql = f[2 * 32 * 2];
+                            mma_f16(xc[nt], ah, ql.x, ql.y);
+                        }
                         mma_f16(xc[nt], ah, qh.x, qh.y);
                     }
                 }
@@ -1146,12 +1193,13 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                     for (int k = 0; k < 4; ++k) x[nt][k] = fmaf(xc[nt][k], back[k >> 1], x[nt][k]);
             }
         }
+        if (PK) join(x[0]);
         group_sync(0);                                               // the keys are read, and sh.top is free
         copy_tail(true);
-        float y[kM][NT][4];
+        float y[kM][NT][kE];
         if (kM == 2)
 #pragma unroll
-            for (int k = 0; k < NT * 4; ++k) (&y[kM - 1][0][0])[k] = -INFINITY;
+            for (int k = 0; k < NT * kE; ++k) (&y[kM - 1][0][0])[k] = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1159,8 +1207,8 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
                 int lo, hi;
                 row_sees(nt, e, lo, hi);
 #pragma unroll
-                for (int k = e; k < 4; k += 2) {
-                    const int pos = base + key0 + 2 * (k >> 1);
+                for (int k = e; k < kE; k += 2) {
+                    const int pos = base + key0 + 2 * (k >> 1 | low);
                     y[0][nt][k] = wq == 3 || pos < lo || pos >= hi ? -INFINITY : x[nt][k] * (e ? scale_of(nt).y : scale_of(nt).x);
                 }
             }
@@ -1171,17 +1219,19 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float ref = mx[nt][e] == -INFINITY ? 0.f : mx[nt][e] - kTop;
-                const int r = 8 * nt + 2 * t + e;
-                y[0][nt][e] = ex2(y[0][nt][e] - ref);
-                y[0][nt][2 + e] = ex2(y[0][nt][2 + e] - ref);
-                const float sum = y[0][nt][e] + y[0][nt][2 + e];
+                const int r = 8 * nt + t2 + e;
+                float sum = 0.f;
+#pragma unroll
+                for (int k = e; k < kE; k += 2) {
+                    sum += y[0][nt][k] = ex2(y[0][nt][k] - ref);
+                    if (wq < 3) weight[r * S::kTailPitch + key0 + 2 * (k >> 1 | low)] = y[0][nt][k];
+                }
                 l[nt][e] += sum;
                 if (keep_lse) {
-                    const float total = group_sum(sum);
+                    const float total = rows_sum(sum);
                     const int b = p.z + (wq >> 1);
-                    if (g == 0 && r < per && b < p.b0 + p.nb) put_lse(b, wq & 1, r, total, mx[nt][e]);
+                    if (g == 0 && low == 0 && r < per && b < p.b0 + p.nb) put_lse(b, wq & 1, r, total, mx[nt][e]);
                 }
-                if (wq < 3) weight[r * S::kTailPitch + key0] = y[0][nt][e], weight[r * S::kTailPitch + key0 + 2] = y[0][nt][2 + e];
             }
         cp_async_wait_groups<0>();
         group_sync(0);
@@ -1192,7 +1242,8 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             uint32_t wf[NT][2][3];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float4 y = *reinterpret_cast<const float4 *>(weight + (8 * nt + g) * S::kTailPitch + 16 * st + 4 * t);
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);          // PK: columns 4..7 hold no rows
+                if (!PK || g < 4) y = *reinterpret_cast<const float4 *>(weight + (8 * nt + g) * S::kTailPitch + 16 * st + 4 * t);
                 thirds2(y.x, y.y, wf[nt][0]);
                 thirds2(y.z, y.w, wf[nt][1]);
             }
@@ -1249,16 +1300,21 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int r = 8 * nt + 2 * t + e;
-            const float sum = group_sum(l[nt][e]);
+            const int r = 8 * nt + t2 + e;
+            const float sum = rows_sum(l[nt][e]);
             if (g == 0) {
                 sh.l[warp][r] = sum;
                 if (wq == 0) sh.m[grp][r] = mx[nt][e];
             }
 #pragma unroll
             for (int mt = 0; mt < kMt; ++mt) {
-                om[r * kPitch + wq * (HD / 4) + 16 * mt + g] = o[mt][nt][e];
-                om[r * kPitch + wq * (HD / 4) + 16 * mt + g + 8] = o[mt][nt][2 + e];
+                float o0 = o[mt][nt][e], o1 = o[mt][nt][2 + e];
+                if (PK) {                                            // the halves' sums
+                    o0 += __shfl_xor_sync(0xffffffffu, o0, 2);
+                    o1 += __shfl_xor_sync(0xffffffffu, o1, 2);
+                }
+                om[r * kPitch + wq * (HD / 4) + 16 * mt + g] = o0;
+                om[r * kPitch + wq * (HD / 4) + 16 * mt + g + 8] = o1;
             }
         }
     __syncthreads();
@@ -1268,7 +1324,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         a.part_bad[part] = sh.bad;
     }
     if (sh.bad) return;
-    if (tid < RG) {   // each group's factor, in place of its maximum
+    if (tid < (PK ? 4 : RG)) {   // each group's factor, in place of its maximum
         float top = -INFINITY, total = 0.f;
 #pragma unroll
         for (int i = 0; i < kG; ++i) top = fmaxf(top, sh.m[i][tid]);
@@ -1303,8 +1359,8 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 }
 
 // Splits: grid (splits, heads x row groups, sequences).
-template <int HD, int NT>
-__global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, NT>::kCtas) k_kv8_attn(AttnKvArgs a) {
+template <int HD, int NT, bool PK>
+__global__ void __launch_bounds__(AttnShape<HD, NT, PK>::kWarps * 32, AttnShape<HD, NT, PK>::kCtas) k_kv8_attn(AttnKvArgs a) {
     constexpr int RG = 8 * NT;
     extern __shared__ __align__(16) uint8_t kv_smem[];
     __shared__ AttnShared<HD, NT> sh;
@@ -1319,7 +1375,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(a.c.err, p.bad);
         return;
     }
-    const int nsplit = splits_of<AttnShape<HD, NT>::kStep>(a.splits, p.coded);
+    const int nsplit = splits_of<AttnShape<HD, NT, PK>::kStep>(a.splits, p.coded);
     u.tail = a.apart ? split < 0 : split == max(nsplit - 1, 0);
     if (u.rg >= p.groups || (split >= nsplit && !u.tail)) return;
     const bool codes = split >= 0 && split < nsplit;
@@ -1327,13 +1383,13 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
     u.x1 = codes ? int((long)p.coded * (split + 1) / nsplit) : 0;
     u.whole = nsplit == 0 || (nsplit == 1 && !a.apart);
     u.index = split + a.apart;
-    attn_piece<HD, NT>(a, p, u, q, kv_smem, sh);
+    attn_piece<HD, NT, PK>(a, p, u, q, kv_smem, sh);
 }
 
 // Shares: a.ctas CTAs.
-template <int HD, int NT>
-__global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, NT>::kCtas) k_kv8_attn_share(AttnKvArgs a) {
-    constexpr int RG = 8 * NT, kW = AttnShape<HD, NT>::kWarps;
+template <int HD, int NT, bool PK>
+__global__ void __launch_bounds__(AttnShape<HD, NT, PK>::kWarps * 32, AttnShape<HD, NT, PK>::kShareCtas) k_kv8_attn_share(AttnKvArgs a) {
+    constexpr int RG = 8 * NT, kW = AttnShape<HD, NT, PK>::kWarps;
     extern __shared__ __align__(16) uint8_t kv_smem[];
     __shared__ AttnShared<HD, NT> sh;
     __shared__ long sm_sums[kW][2], sm_off;
@@ -1349,7 +1405,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         work += weight_of(a, p);
     }
     block_sums(work, none, sm_sums);
-    const int G = shares_of<AttnShape<HD, NT>::kStep>(a, work);
+    const int G = shares_of<AttnShape<HD, NT, PK>::kStep>(a, work);
     if (cta >= G) return;
     long pos = work * cta / G, off = 0;
     const long pos_end = work * (cta + 1) / G;
@@ -1399,7 +1455,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
         QueryRows<HD, NT> q;
         q.load(a, s, u.h, u.rg);
         __syncthreads();                                             // the piece before is done with the shared memory
-        attn_piece<HD, NT>(a, p, u, q, kv_smem, sh);
+        attn_piece<HD, NT, PK>(a, p, u, q, kv_smem, sh);
     }
 }
 
@@ -1408,7 +1464,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT>::kWarps * 32, AttnShape<HD, 
 // scores (grid x behind them, row group 0). HD / 4 threads take four channels each of a row; with `apart_rows` all threads of
 // a CTA take one row and share out its parts (few units of many parts), else each such group takes a row of its own.
 constexpr int kMergeThreads = 256;
-constexpr int kMaxCtas = 304;   // two for each SM
+constexpr int kMaxCtas = 456;   // of a launch that share or split units: three for each SM at most
 template <int HD, int NT>
 __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int row_ctas, int apart_rows) {
     constexpr int RG = 8 * NT, kLanes = kMergeThreads / (HD / 4), kSome = 4;
@@ -1579,9 +1635,10 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
 // has more than 8. Up to as many units as half the CTAs that fit the part's 152 SMs at once: splits of a unit's blocks, and
 // a CTA of its own for the tail or not; all in one wave (CTAs of a second one were measured to wait for tens of microseconds
 // although slots were free). Costs are in turns; a tail inside a CTA is worth about 2. More units: shares, which leave no slot
-// idle but cost some 32 blocks' time more (finding the share, pieces of two or three units, their parts' merge). So shares also
-// take long contexts where whole splits leave slots idle: 128 units of 512 blocks on 304 slots take 100 us in shares and 115 in
-// splits (16 rows of 128: 138 and 159), but 72 units 71 and 64, and 128 units of 128 blocks 41 and 40.
+// idle but cost a little more (finding the share, pieces of two or three units, their parts' merge). So shares also take long
+// contexts where whole splits leave slots idle: 128 units of 512 blocks on 304 slots take 97 us in shares and 115 in splits
+// (16 rows of 128: 130 and 159), 96 units 101 and 114; but 72 units took 71 and 64, 128 units of 128 blocks 41 and 40.
+constexpr int kFewRows = 4;              // rows for which both halves fit one tile of columns
 struct AttnCut {
     int nt, groups, splits, apart, share, ctas;
     size_t units, o_bytes, ml_bytes, bad_bytes, lse_bytes, total;
@@ -1596,7 +1653,7 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
     t.units = (size_t)c->n_seq * c->n_kv * t.groups;
     const bool wide = c->head_dim == 256 && t.nt == 2;
     const int step = wide ? AttnShape<256, 2>::kStep : c->head_dim == 256 ? AttnShape<256, 1>::kStep : AttnShape<128, 1>::kStep;
-    const int slots = wide ? kMaxCtas / 2 : kMaxCtas, blocks = window ? std::min(c->n_blocks, window / kBlk + 2) : c->n_blocks;
+    const int slots = wide ? 152 : 2 * 152, blocks = window ? std::min(c->n_blocks, window / kBlk + 2) : c->n_blocks;
     t.splits = 1;
     t.share = t.units > (size_t)slots / 2;
     if (!t.share) {
@@ -1609,9 +1666,9 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
             }
         // a CTA's blocks in splits, and in shares: long ones only, and what is saved
         const size_t whole = (size_t)best * step, even = t.units * (blocks + kTailWeight) / slots;
-        t.share = even >= 160 && whole >= even + 32;
+        t.share = even >= 160 && whole >= even + 16;
     }
-    if (t.share) t.splits = 1, t.apart = 0, t.ctas = slots;
+    if (t.share) t.splits = 1, t.apart = 0, t.ctas = r <= kFewRows && c->head_dim < 256 ? 3 * 152 : slots;
     const size_t parts = t.share ? t.units + t.ctas : t.units * (t.splits + t.apart);
     t.o_bytes = up256(parts * 8 * t.nt * c->head_dim * 4);
     t.ml_bytes = up256(parts * 8 * t.nt * 8);
@@ -1622,28 +1679,37 @@ AttnCut attn_cut(const dfl_kv8 *c, int n_q, int rows, int window, int score) {
 }
 
 // the kernels' shared memory, once per device
+template <int HD, int NT, bool PK>
+cudaError_t allow_smem() {
+    const int smem = AttnShape<HD, NT, PK>::kSmem;
+    const cudaError_t e = cudaFuncSetAttribute(k_kv8_attn<HD, NT, PK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(k_kv8_attn_share<HD, NT, PK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
 template <int HD, int NT>
 cudaError_t prepare_kv8_attn() {
     static bool done[kMaxDevices] = {};
-    const int dev = current_device(), smem = AttnShape<HD, NT>::kSmem;
+    const int dev = current_device();
     if (dev < 0) return cudaErrorInvalidDevice;
     if (done[dev]) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(k_kv8_attn<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv8_attn_share<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem<HD, NT, false>();
+    if (e == cudaSuccess && NT == 1) e = allow_smem<HD, NT, NT == 1>();
     done[dev] = e == cudaSuccess;
     return e;
 }
 
+template <int HD, int NT, bool PK>
+cudaError_t launch_kv8_pieces(const AttnKvArgs &a, cudaStream_t s) {
+    const int smem = AttnShape<HD, NT, PK>::kSmem, threads = AttnShape<HD, NT, PK>::kWarps * 32;
+    return a.share ? launch_pdl(k_kv8_attn_share<HD, NT, PK>, dim3(a.ctas), dim3(threads), smem, s, a)
+                   : launch_pdl(k_kv8_attn<HD, NT, PK>, dim3(a.splits + a.apart, a.c.n_kv * a.groups, a.c.n_seq), dim3(threads), smem, s, a);
+}
 template <int HD, int NT>
 cudaError_t launch_kv8_attn(const AttnKvArgs &a, cudaStream_t s) {
-    const int smem = AttnShape<HD, NT>::kSmem, threads = AttnShape<HD, NT>::kWarps * 32;
     cudaError_t e = prepare_kv8_attn<HD, NT>();
     if (e != cudaSuccess) return e;
     const unsigned heads = unsigned(a.c.n_kv * a.groups);
-    if (a.share)
-        e = launch_pdl(k_kv8_attn_share<HD, NT>, dim3(a.ctas), dim3(threads), smem, s, a);
-    else
-        e = launch_pdl(k_kv8_attn<HD, NT>, dim3(a.splits + a.apart, heads, a.c.n_seq), dim3(threads), smem, s, a);
+    const bool few = NT == 1 && a.rows * (a.n_q / a.c.n_kv) <= kFewRows;
+    e = few ? launch_kv8_pieces<HD, NT, NT == 1>(a, s) : launch_kv8_pieces<HD, NT, false>(a, s);
     if (e != cudaSuccess) return e;
     if (!a.share && a.splits == 1 && !a.apart && !a.score) return cudaSuccess;   // every unit is one CTA's
     const int apart_rows = !a.share && a.splits > 8, lanes = kMergeThreads / (HD / 4);

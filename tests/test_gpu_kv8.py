@@ -296,6 +296,44 @@ def test_attn_masked_infinities_do_not_leak(torch):
     p.c.status()
 
 
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("n_q,rows", [(2, 1), (4, 2), (8, 1), (2, 4)])
+def test_attn_of_few_rows(torch, hd, n_q, rows):
+    """At most 4 rows a key/value head, the two halves of a query in one tile of columns: hard values, queries, masks and scales."""
+    p = Pair(torch, 2, 2, hd, 24, seed=hd + n_q)
+    k, v = p.new_rows(700), p.new_rows(700)
+    size = np.repeat(10.0 ** np.array([0, -6, 4, -30, 0, 0, 2, -3, 0, -10, 0]), 64)[:700].astype(np.float32)[None, :, None, None]
+    p.write(700, cnt=[700, 333], k=k, v=v * size)
+    p.write(rows, commit=False)
+    p.attn(n_q, rows, score=True)
+    p.attn(n_q, rows, window=100)
+    p.attn(n_q, rows, causal=False, window=33, scale=2.0, score=True)
+    p.attn(n_q, rows, scale=1e-9)
+    p.attn(n_q, rows, cnt=[0, rows], score=True)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("seqs", [1, 90])
+def test_few_rows_see_no_masked_infinities(torch, hd, seqs):
+    """Blocks and tail rows that hold infinities or NaN: rows that see them are NaN, and the others as without them."""
+    p = Pair(torch, seqs, 2, hd, 10, seed=hd)
+    k, v = p.new_rows(200), p.new_rows(200)
+    k[0, 40, 0, 3], v[0, 41, 1, 9] = np.inf, np.nan
+    p.write(200, k=k, v=v)
+    ks, vs = p.new_rows(4), p.new_rows(4)
+    ks[0, 3, 0], vs[0, 3, 1] = np.nan, -np.inf
+    p.write(4, commit=False, k=ks, v=vs)
+    q, length = p.dev(p.new_rows(4, 2)), p.dev(p.len)
+    q[0, 1, 1] = float("inf")
+    out = p.c.attn(q, length, window=136).cpu().numpy()      # row m sees tokens 65 + m .. 200 + m
+    p.c.status()
+    assert np.isfinite(out[0, [0, 2]]).all() and np.isfinite(out[0, 1, 0]).all() and np.isnan(out[0, 1, 1]).all() and np.isnan(out[0, 3]).all()
+    assert np.isfinite(out[1:]).all()
+    out = p.c.attn(q, length, window=138).cpu().numpy()      # row 0 sees a token of the poisoned block (32..63)
+    p.c.status()
+    assert np.isnan(out[0, [0, 3]]).all() and np.isfinite(out[0, 2]).all() and np.isfinite(out[1:]).all()
+
+
 def test_attn_long_and_far(torch):
     """A long context whose stored blocks lie past 2^31 bytes of the code arrays."""
     from dflash_speculative_decode_gb300 import Kv8Cache
