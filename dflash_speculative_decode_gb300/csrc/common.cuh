@@ -28,6 +28,7 @@ struct DevState {
     int props[kMaxRows];   // draft proposals for positions n+1..n+block-1
     int last_tok;          // row 0 of the last draft block
     int err;               // sticky device-side error bits
+    alignas(16) int kv8_err;   // what the planes in 8 bits met (dfl_kv8.err of all of them)
 };
 
 // DevState::err bits

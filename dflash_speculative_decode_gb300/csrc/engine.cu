@@ -156,9 +156,10 @@ struct dfl_ctx {
     bool fuse_steps = false;  // the row and q/k steps run on the products' last CTAs (DFL_OPT_FUSE_STEPS)
     bool ple_split = false;   // the PLE gate and projection as two products (DFL_OPT_PLE_SPLIT)
     bool draft_only = false, keep_logits = false, have_logits = false, have_dlogits = false;
-    // a failed prefill may have overwritten ring slots (sliding planes, the draft context) that the
-    // positions held still need: passes and snapshots are refused until a restore
-    bool needs_restore = false;
+    // Why passes and snapshots are refused until a restore (null: they are not): a failed prefill may have
+    // overwritten ring slots (sliding planes, the draft context) that the positions held still need, or a
+    // plane in 8 bits was out of order
+    const char *needs_restore = nullptr;
     int last_k = 0;
     int stop_layer = -1;   // debug: a target pass runs layers 0..stop_layer only (no head)
     int attn_cluster = 16; // largest attention cluster size allowed: 16, 8 or 4
@@ -253,8 +254,9 @@ std::string validate(const dfl_config *g) {
     return {};
 }
 
-// A full layer's plane in 8 bits, laid out in one piece of the state
-void kv8_plan(TLayer &L, int head_dim, int positions, Arena &S) {
+// A full layer's plane in 8 bits, laid out in one piece of the state; its error word is the state's, which every read of the
+// pass's results fetches
+void kv8_plan(TLayer &L, int head_dim, int positions, DevState *st, Arena &S) {
     dfl_kv8 &c = L.kv8;
     c = dfl_kv8{1, L.nkv, head_dim, (positions + DFL_KV8_BLOCK - 1) / DFL_KV8_BLOCK};
     auto lay = [&](uint8_t *base) {
@@ -268,12 +270,11 @@ void kv8_plan(TLayer &L, int head_dim, int positions, Arena &S) {
         c.v_tail = A.take<float>(tail);
         c.table = A.take<int32_t>(blocks);
         c.sealed = A.take<int32_t>(c.n_kv);
-        c.err = A.take<int32_t>(1);
         return A.off;
     };
     L.kv8_bytes = lay(nullptr);
     L.kv8_base = S.take<uint8_t>(L.kv8_bytes);
-    if (L.kv8_base) lay(L.kv8_base);
+    if (L.kv8_base) lay(L.kv8_base), c.err = &st->kv8_err;
 }
 
 QMat qmat(int K, int N, bool q41) {
@@ -373,7 +374,7 @@ void plan(dfl_ctx *c, Arena &W, Arena &S, Arena &X) {
         if (L.owner != l) continue;
         L.cap = L.type == DFL_SLIDING ? c->cap_sliding : g.max_ctx + R;
         if (g.kv8 && L.type == DFL_FULL) {
-            kv8_plan(L, hd, L.cap, S);
+            kv8_plan(L, hd, L.cap, c->st, S);
             continue;
         }
         L.K = S.take<float>((size_t)L.cap * L.nkv * hd);
@@ -1175,9 +1176,17 @@ int run_draft(dfl_ctx *c, int last_tok) {
 // to the rows confirmed by the last good read (the rows made context since then are made again by the
 // next draft block), and the caller restores its own counters. Committed planes, taps and positions
 // are untouched by a failed pass (it writes only rows past the committed positions).
+// A plane in 8 bits whose counts or table are out of order (a restored snapshot may bring them) has left
+// its attention's rows unwritten: DFL_E_STATE, and nothing runs until a sound snapshot is restored.
 int read_state(dfl_ctx *c, DevState *out) {
     DFL_CK(cudaMemcpyAsync(out, c->st, sizeof(DevState), cudaMemcpyDeviceToHost, c->stream));
     DFL_CK(cudaStreamSynchronize(c->stream));
+    if (out->kv8_err) {
+        DFL_CK(cudaMemsetAsync(&c->st->kv8_err, 0, sizeof(int), c->stream));
+        c->draft_at = -1;
+        c->needs_restore = "a plane in 8 bits was out of order";
+        if (!(out->err & kErrWaitTimeout)) return fail(c, DFL_E_STATE, std::string(c->needs_restore) + ": restore a snapshot");
+    }
     if (out->err & kErrWaitTimeout) {
         DFL_CK(cudaMemsetAsync(&c->st->err, 0, sizeof(int), c->stream));
         // a pass that gave up may leave arrival counters short of their reset: start them from zero
@@ -1199,8 +1208,7 @@ int check_tokens(dfl_ctx *c, const int32_t *t, int n) {
 }
 
 int ready(dfl_ctx *c) {
-    if (c->needs_restore)
-        return fail(c, DFL_E_STATE, "a failed prefill may have overwritten ring slots of the held positions: restore a snapshot");
+    if (c->needs_restore) return fail(c, DFL_E_STATE, std::string(c->needs_restore) + ": restore a snapshot");
     auto chk = [&](bool ok, const char *what) { return ok ? DFL_OK : fail(c, DFL_E_STATE, std::string("tensor not loaded: ") + what); };
     int rc;
     if ((rc = chk(c->emb.loaded && c->head.loaded && c->final_norm.loaded, "emb/head/final_norm"))) return rc;
@@ -1409,7 +1417,8 @@ int dfl_prefill(dfl_ctx *c, const int32_t *tokens, int n, const dfl_sampling *s,
         c->draft_n = std::min(c->draft_n, n_start);
         c->draft_n_ok = std::min(c->draft_n_ok, c->draft_n);
         c->draft_at = -1;
-        c->needs_restore = n_start > 0;   // an empty context has no slot to lose
+        if (n_start > 0 && !c->needs_restore)   // an empty context has no slot to lose
+            c->needs_restore = "a failed prefill may have overwritten ring slots of the held positions";
         return rc_;
     };
     int done = 0;
@@ -1531,7 +1540,7 @@ int dfl_snapshot(dfl_ctx *c, void *dst, size_t bytes) {
     NvtxRange nvtx("dfl_snapshot");
     if (!c) return DFL_E_INVALID_ARG;
     if (c->pending) return fail(c, DFL_E_STATE, "snapshot needs the committed state");
-    if (c->needs_restore) return fail(c, DFL_E_STATE, "a failed prefill left the state unusable: restore first");
+    if (c->needs_restore) return fail(c, DFL_E_STATE, std::string(c->needs_restore) + ": restore a snapshot");
     if (!dst) return fail(c, DFL_E_INVALID_ARG, "null destination");
     const size_t need = snapshot_size(c, c->n, c->draft_n);
     if (bytes < need) return fail(c, DFL_E_INVALID_ARG, "snapshot buffer too small");
@@ -1615,12 +1624,13 @@ int dfl_restore(dfl_ctx *c, const void *src, size_t bytes) {
     }
     const size_t tb = (size_t)(hdr.n - hdr.draft_n) * c->TH * 4;
     if (tb) DFL_CK(cudaMemcpyAsync(c->taps + (size_t)hdr.draft_n * c->TH, s + off, tb, cudaMemcpyDeviceToDevice, c->stream));
+    DFL_CK(cudaMemsetAsync(&c->st->kv8_err, 0, sizeof(int), c->stream));
     c->n = hdr.n;
     c->draft_n = hdr.draft_n;
     c->draft_n_ok = hdr.draft_n;
     c->draft_at = -1;
     c->draft_only = false;
-    c->needs_restore = false;
+    c->needs_restore = nullptr;
     return DFL_OK;
 }
 

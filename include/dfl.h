@@ -194,7 +194,9 @@ int dfl_commit_accepted(dfl_ctx *ctx, int max_keep, int32_t stop_token, int32_t 
  * bytes; restore replaces the state with a snapshot taken from a context with the same configuration.
  * Both need the committed state (no pending verify). KV-shared layers have no plane and contribute
  * nothing. A snapshot taken once after a pinned prefix may be restored any number of times (FastFlowLM
- * PR #899 "gemma4e-dflash-flash", "Changes": the pinned prefix must not be overwritten by a request). */
+ * PR #899 "gemma4e-dflash-flash", "Changes": the pinned prefix must not be overwritten by a request).
+ * Planes in 8 bits hold counts of their own. Where a snapshot's are out of order, the next prefill or verify
+ * meets it on the device: it fails with DFL_E_STATE, and so do passes and snapshots until a sound one is restored. */
 int64_t dfl_snapshot_bytes(const dfl_ctx *ctx);
 int dfl_snapshot(dfl_ctx *ctx, void *dev_dst, size_t bytes);
 int dfl_restore(dfl_ctx *ctx, const void *dev_src, size_t bytes);

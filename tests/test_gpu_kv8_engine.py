@@ -1,0 +1,68 @@
+"""An engine with its full layers' planes in 8 bits: what it reports, counts and stores."""
+import numpy as np
+import pytest
+
+import gen
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def weights():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from dflash_speculative_decode_gb300 import build
+    build.build()
+    return {name: (pc, gen.generate(pc)) for name, pc in (("tiny", gen.tiny_pair()), ("tiny-shared", gen.tiny_shared_pair()))}
+
+
+def engine(pc, W, kv8=1):
+    from dflash_speculative_decode_gb300 import Engine, config_from_pair
+    eng = Engine(config_from_pair(pc, kv8=kv8))
+    eng.load(W)
+    return eng
+
+
+def owner_heads(pc):
+    """Key/value heads of the planes held in 8 bits."""
+    t = pc.target
+    return sum(t.kv_heads[l] for l in range(t.n_layers) if t.layer_type[l] == gen.FULL and t.kv_owner[l] == l)
+
+
+@pytest.mark.parametrize("name", ["tiny", "tiny-shared"])
+@pytest.mark.parametrize("bad", [1 << 20, -1])
+def test_a_plane_out_of_order_is_reported(weights, name, bad):
+    """A snapshot whose sealed counts are out of range: the next pass raises instead of returning tokens, and so do all calls until a
+    sound snapshot is restored. The counts are found as the words that go from 1 to 2 when the next stage seals the second block."""
+    from dflash_speculative_decode_gb300 import DflError
+    from dflash_speculative_decode_gb300._abi import DFL_E_STATE
+    pc, W = weights[name]
+    eng = engine(pc, W)
+    rows = [int(t) for t in gen.prompt(pc.target.vocab, 8, request=2)]
+    eng.dfl_prefill(gen.prompt(pc.target.vocab, 64))
+    before = eng.dfl_snapshot()
+    eng.dfl_verify_block(rows)
+    eng.dfl_commit_verify_rows(0)
+    snap = eng.dfl_snapshot()
+    words = [x[:x.numel() // 4 * 4].cpu().numpy().view(np.int32) for x in (before, snap)]
+    at = np.nonzero((words[0] == 1) & (words[1] == 2))[0]
+    assert len(at) == owner_heads(pc)
+    want = eng.dfl_verify_block(rows)
+    eng.dfl_commit_verify_rows(0)
+    spoilt = words[1].copy()
+    spoilt[at] = bad
+    broken = snap.clone()
+    broken[:4 * len(spoilt)] = eng.torch.from_numpy(spoilt.view(np.uint8)).to(broken.device)
+    for call in (lambda: eng.dfl_verify_block(rows), lambda: eng.dfl_prefill(rows)):
+        eng.dfl_restore(broken)
+        with pytest.raises(DflError) as e:
+            call()
+        assert e.value.code == DFL_E_STATE
+        for again in (lambda: eng.dfl_verify_block(rows), lambda: eng.dfl_prefill(rows), lambda: eng.dfl_snapshot()):
+            with pytest.raises(DflError) as e:
+                again()
+            assert e.value.code == DFL_E_STATE
+        eng.dfl_restore(snap)
+        got = eng.dfl_verify_block(rows)
+        eng.dfl_commit_verify_rows(0)
+        assert list(got[0]) == list(want[0]) and got[1] == want[1]
