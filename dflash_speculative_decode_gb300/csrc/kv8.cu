@@ -659,15 +659,15 @@ struct AttnShared {
     int bad;
 };
 template <int HD, int NT>
-struct QueryRows {      // a warp takes every kWarps-th row of the group
+struct QueryRows {      // a warp takes every kWarps-th row of the group; `n` of the call's rows count, the others are not read
     static constexpr int kW = AttnShape<HD, NT>::kWarps, kRows = (8 * NT + kW - 1) / kW;
     float2 x[kRows][HD / 64];
-    __device__ __forceinline__ void load(const AttnKvArgs &a, int s, int h, int rg) {
+    __device__ __forceinline__ void load(const AttnKvArgs &a, int s, int h, int rg, int n) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = a.n_q / a.c.n_kv;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int r = warp + i * kW, rid = rg * 8 * NT + r;
-            const bool on = r < 8 * NT && rid < a.rows * per;
+            const bool on = r < 8 * NT && rid < n * per;
             const float *q = a.q + ((size_t)s * a.rows + rid / per) * a.ldq + (size_t)(h * per + rid % per) * HD + 2 * lane;
 #pragma unroll
             for (int k = 0; k < HD / 64; ++k) x[i][k] = on ? *reinterpret_cast<const float2 *>(q + 64 * k) : make_float2(0.f, 0.f);
@@ -1366,9 +1366,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT, PK>::kWarps * 32, AttnShape<
     __shared__ AttnShared<HD, NT> sh;
     const int split = int(blockIdx.x) - a.apart;
     Piece u{int(blockIdx.z), int(blockIdx.y) / a.groups, int(blockIdx.y) % a.groups};
-    QueryRows<HD, NT> q;
     pdl_wait();
-    q.load(a, u.s, u.h, u.rg);
     const Span p = span_of(a, u.s, a.c.sealed[(size_t)u.s * a.c.n_kv + u.h], RG);
     pdl_trigger();
     if (p.bad) {
@@ -1383,6 +1381,8 @@ __global__ void __launch_bounds__(AttnShape<HD, NT, PK>::kWarps * 32, AttnShape<
     u.x1 = codes ? int((long)p.coded * (split + 1) / nsplit) : 0;
     u.whole = nsplit == 0 || (nsplit == 1 && !a.apart);
     u.index = split + a.apart;
+    QueryRows<HD, NT> q;
+    q.load(a, u.s, u.h, u.rg, p.n);
     attn_piece<HD, NT, PK>(a, p, u, q, kv_smem, sh);
 }
 
@@ -1453,7 +1453,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT, PK>::kWarps * 32, AttnShape<
         }
         if (!u.tail && u.x0 == u.x1) continue;
         QueryRows<HD, NT> q;
-        q.load(a, s, u.h, u.rg);
+        q.load(a, s, u.h, u.rg, p.n);
         __syncthreads();                                             // the piece before is done with the shared memory
         attn_piece<HD, NT, PK>(a, p, u, q, kv_smem, sh);
     }
