@@ -505,8 +505,9 @@ __device__ __forceinline__ void seen(const AttnKvArgs &a, const Span &p, int m, 
 // 16-row operand, query rows as the 8 columns: S^T = K Q^T and O^T = V^T P^T, so rows that a call does not
 // have cost at most 7 columns. Codes are whole numbers of at most 7 bits and exact in fp16; the block's
 // key scale multiplies the fp32 logits. A query row (scaled by a power of two to 2^14..2^15) and the weights
-// (2^7 and more for the row's largest, times the block's value scale over the largest one) enter as two fp16
-// halves, hi + lo, which hold 22 bits, and nothing below 2^-25.
+// (2^7 and more for the row's largest) enter as two fp16 halves, hi + lo, which hold 22 bits, and nothing below
+// 2^-25. A block's value scale multiplies the fp32 sums of its own products, so that the size of one block's
+// values, seen by a row or not, takes nothing from another's.
 //
 // These are the older tensor instructions on purpose. The fifth generation's take their operands from shared or tensor
 // memory, so every code would be written there a second time at twice its size; a unit has 1 to 16 rows (32 columns with both
@@ -557,8 +558,14 @@ __device__ __forceinline__ bool group_or(int grp, bool x) {
     return r;
 }
 
+template <bool FIRST = false>   // FIRST: d = a b
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    if constexpr (FIRST)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -843,9 +850,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 
     // A row's weights are 2^(logit - mx + kTop), for all four warps of the group. mx is a maximum that is only renewed when a
     // weight would pass 2^15, so most pairs need no maximum across the lanes and rescale nothing: the row's largest weight
-    // lies in 2^7..2^15. Values are summed in units of v_ref, the largest value scale so far: the logarithm of a
-    // block's scale over v_ref is added to the exponent, so that the products add straight to the sums, and the sum of the
-    // weights (a warp's own keys') takes it back.
+    // lies in 2^7..2^15.
     float o[kMt][NT][4], mx[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -887,37 +892,19 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         a.blk_lse[((head_blocks + b) * 2 + half) * 16 + r] = total == 0.f ? -INFINITY : top - kTop + log2f(total);
     };
 
-    float v_ref = 0.f, v_lb = 0.f, v_inv = 1.f;
     for (int i = 0; i < turns; ++i) {
         if (i % kWin == 0) {                                         // the next kWin turns' scales
             if (i > 0) ks = ks_next, vs = vs_next;
             const bool is = first + kTurn * kG * (i + lane / kTurn) + lane % kTurn < p.b0 + u.x1;
             if (!is) ks = vs = 0.f;                                  // what is read in place of a block that is not there
-            float top = isnan(vs) ? 0.f : vs;
-#pragma unroll
-            for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-            if (top > v_ref) {
-                const float f = v_ref / top;
-#pragma unroll
-                for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) o[mt][nt][k] *= f;
-                v_ref = top;
-            }
-            // a block of zeros counts as any scale; one of 2^-60 and less adds nothing that fp32 could hold
-            const float r = vs > 0.f ? fmaxf(vs / v_ref, 8.673617e-19f) : 1.f;
-            v_lb = log2f(r);
-            v_inv = isnan(vs) ? vs : 1.f / r;
         }
         if (i % kWin == kWin / 2) {                                  // the next window's, half a window ahead
             ks_next = a.c.k_scale[head_blocks + phys_next];
             vs_next = a.c.v_scale[head_blocks + phys_next];
         }
         const int from = kTurn * (i % kWin) + mine, b = first + kTurn * kG * i + mine;   // this warp's block of the turn
-        const float bks = __shfl_sync(0xffffffffu, ks, from), blb = __shfl_sync(0xffffffffu, v_lb, from);
-        float binv = __shfl_sync(0xffffffffu, v_inv, from);
+        const float bks = __shfl_sync(0xffffffffu, ks, from);
+        const bool unsound = isnan(__shfl_sync(0xffffffffu, vs, from));
         const bool there = b < p.b0 + u.x1;
         cp_async_wait_groups<kRing - 1>();
         __syncwarp();
@@ -974,7 +961,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float z = bks * (e ? scale_of(nt).y : scale_of(nt).x), less = blb + kTop - mx[nt][e];   // +inf before a row's first key
+                const float z = bks * (e ? scale_of(nt).y : scale_of(nt).x), less = kTop - mx[nt][e];   // +inf before a row's first key
 #pragma unroll
                 for (int m = 0; m < kM; ++m)
 #pragma unroll
@@ -1016,10 +1003,9 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int k = 0; k < kE; ++k) y[m][nt][k] += mx[nt][k & 1] == -INFINITY ? 0.f : blb + kTop - mx[nt][k & 1];
+                    for (int k = 0; k < kE; ++k) y[m][nt][k] += mx[nt][k & 1] == -INFINITY ? 0.f : kTop - mx[nt][k & 1];
         }
-        if (isnan(binv)) {                                           // rows that see the block are NaN, the others take nothing of it
-            binv = 0.f;
+        if (unsound) {                                               // rows that see the block are NaN
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1039,9 +1025,9 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             for (int e = 0; e < 2; ++e) {
                 float sum = PK ? y[0][nt][e] : y[0][nt][e] + y[0][nt][kE - 2 + e];
                 if (kM == 2) sum += PK ? y[kM - 1][nt][e] : y[kM - 1][nt][e] + y[kM - 1][nt][kE - 2 + e];
-                l[nt][e] = fmaf(sum, binv, l[nt][e]);
+                l[nt][e] += sum;
                 if (keep_lse) {
-                    const float total = rows_sum(sum) * binv;
+                    const float total = rows_sum(sum);
                     const int r = 8 * nt + t2 + e;
                     if (g == 0 && low == 0 && r < per && there) {
                         put_lse(b, key_half, r, total, mx[nt][e]);
@@ -1066,17 +1052,16 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         cp_async_wait_groups<kRing - 1>();
         group_sync(grp);
         const uint8_t *V = take + g * kBlk + 8 * t;
-        // the turn's products have sums of their own, added to the running ones in fp32: the tensor cores cut off what they add
-        // below the last place, which over a long context would add up (16384 tokens: 5e-6 to 8e-6 of the outputs, 6e-7 to 1.2e-6
-        // with sums of a turn's own)
+        // A block's products have sums of their own, which its value scale takes to the running ones in fp32. (The tensor cores cut
+        // off what they add below the last place; over a long context that would add up: 16384 tokens 5e-6 to 8e-6 of the outputs.)
         constexpr int kMs = kMt < 2 ? kMt : 2;                       // channel tiles at once
 #pragma unroll
         for (int m0 = 0; m0 < kMt; m0 += kMs) {
-            float d[kMs][NT][4];
-#pragma unroll
-            for (int k = 0; k < kMs * NT * 4; ++k) (&d[0][0][0])[k] = 0.f;
 #pragma unroll
             for (int j = 0; j < kTurn; ++j) {                        // block of the turn
+                float bvs = __shfl_sync(0xffffffffu, vs, kTurn * (i % kWin) + j);
+                bvs = isnan(bvs) ? 0.f : bvs;
+                float d[kMs][NT][4];
                 uint32_t af[kMs][2][4];
 #pragma unroll
                 for (int m = 0; m < kMs; ++m) {
@@ -1101,24 +1086,22 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
                         for (int m = 0; m < kMs; ++m)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma_f16(d[m][nt], af[m][st], part ? w[nt].z : w[nt].x, part ? w[nt].w : w[nt].y);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                if (st + part == 0)
+                                    mma_f16<true>(d[m][nt], af[m][st], w[nt].x, w[nt].y);
+                                else
+                                    mma_f16(d[m][nt], af[m][st], part ? w[nt].z : w[nt].x, part ? w[nt].w : w[nt].y);
+                            }
                 }
-            }
 #pragma unroll
-            for (int k = 0; k < kMs * NT * 4; ++k) (&o[m0][0][0])[k] += (&d[0][0][0])[k];
+                for (int k = 0; k < kMs * NT * 4; ++k) (&o[m0][0][0])[k] = fmaf((&d[0][0][0])[k], bvs, (&o[m0][0][0])[k]);
+            }
         }
         __syncwarp();
         taken();
         issue(2 * i + 1 + kRing);
     }
     cp_async_wait_groups<0>();
-    if (turns > 0)
-#pragma unroll
-        for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[mt][nt][k] *= v_ref;
 
     // ---- the tail (at most 48 fp32 rows), by the first group: warps 0..2 take 16 keys each, then every warp its channels of
     // the values. Keys enter as two fp16 halves, each key's 64 channels scaled by a power of two of their own; values and

@@ -28,3 +28,25 @@ def test_query_rows_behind_the_last_one_need_no_memory(torch, hd, seqs):  # noqa
     assert rc == 0
     p.c.status()
     assert torch.equal(out, want)
+
+
+# ---- values that a row does not see -----------------------------------------------------------------------
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("n_q,rows", [(2, 1), (4, 1), (2, 4), (4, 4), (16, 2)])     # 2, 4, 8, 16 and 32 rows a head
+@pytest.mark.parametrize("seqs,sizes", [(1, (20, 40, 100)), (160, (40,))])
+def test_masked_values_of_any_size_cost_nothing(torch, hd, n_q, rows, seqs, sizes):  # noqa: F811
+    """A value far larger than the others just before the window's edge, inside the first block that rows see, and one that only row 0
+    sees: the others' outputs are held to the bound of what they see."""
+    for size in sizes:
+        p = Pair(torch, seqs, 1, hd, 12, seed=hd + rows)
+        k, v = p.new_rows(300), p.new_rows(300)
+        v[:, 140] *= np.float32(2.0 ** size)     # row m of a window of 150 sees tokens 151 + m .. 300 + m
+        p.write(300, k=k, v=v)
+        p.write(rows, commit=False)
+        p.attn(n_q, rows, window=150)
+        p.attn(n_q, rows, window=150, causal=False)
+        p = Pair(torch, seqs, 1, hd, 12, seed=hd + rows + 1)
+        v[:, 140], v[:, 151] = p.new_rows(1)[:, 0], v[:, 151] * np.float32(2.0 ** size)
+        p.write(300, k=k, v=v)
+        p.write(rows, commit=False)
+        p.attn(n_q, rows, window=150)
