@@ -664,6 +664,7 @@ template <int HD, int NT>
 struct AttnShared {
     float q_scale[8 * NT], top[AttnShape<HD, NT>::kGroups][4][8 * NT], m[AttnShape<HD, NT>::kGroups][8 * NT], l[AttnShape<HD, NT>::kWarps][8 * NT];
     int bad;
+    uint32_t poisoned;   // bit r: row r of the group sees a value that is not finite: its outputs are NaN, its weights what they are
 };
 template <int HD, int NT>
 struct QueryRows {      // a warp takes every kWarps-th row of the group; `n` of the call's rows count, the others are not read
@@ -796,7 +797,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
     if (tail_only && grp == 0) copy_tail(false);
 
     // ---- query rows into their fragments ----
-    if (tid == 0) sh.bad = 0;
+    if (tid == 0) sh.bad = 0, sh.poisoned = 0;
 #pragma unroll
     for (int j = 0; j < QueryRows<HD, NT>::kRows; ++j) {
         const int r = warp + j * kW;
@@ -895,8 +896,15 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
     for (int i = 0; i < turns; ++i) {
         if (i % kWin == 0) {                                         // the next kWin turns' scales
             if (i > 0) ks = ks_next, vs = vs_next;
-            const bool is = first + kTurn * kG * (i + lane / kTurn) + lane % kTurn < p.b0 + u.x1;
-            if (!is) ks = vs = 0.f;                                  // what is read in place of a block that is not there
+            const int at = first + kTurn * kG * (i + lane / kTurn) + lane % kTurn;
+            if (at >= p.b0 + u.x1) ks = vs = 0.f;                    // what is read in place of a block that is not there
+            for (uint32_t nan = __ballot_sync(0xffffffffu, isnan(vs)); nan; nan &= nan - 1) {   // lane r asks for row r
+                const int from = kBlk * __shfl_sync(0xffffffffu, at, __ffs(nan) - 1);
+                int lo = 0, hi = 0;
+                if (lane < min(live, RG)) seen(a, p, (rg * RG + lane) / per, lo, hi);
+                if (lo < from + kBlk && hi > from) atomicOr(&sh.poisoned, 1u << lane);
+            }
+            if (isnan(vs)) vs = 0.f;
         }
         if (i % kWin == kWin / 2) {                                  // the next window's, half a window ahead
             ks_next = a.c.k_scale[head_blocks + phys_next];
@@ -904,7 +912,6 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         }
         const int from = kTurn * (i % kWin) + mine, b = first + kTurn * kG * i + mine;   // this warp's block of the turn
         const float bks = __shfl_sync(0xffffffffu, ks, from);
-        const bool unsound = isnan(__shfl_sync(0xffffffffu, vs, from));
         const bool there = b < p.b0 + u.x1;
         cp_async_wait_groups<kRing - 1>();
         __syncwarp();
@@ -1005,16 +1012,6 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
                     for (int k = 0; k < kE; ++k) y[m][nt][k] += mx[nt][k & 1] == -INFINITY ? 0.f : kTop - mx[nt][k & 1];
         }
-        if (unsound) {                                               // rows that see the block are NaN
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    int lo, hi;
-                    row_sees(nt, e, lo, hi);
-                    if (there && lo < pos0 + kBlk && hi > pos0) l[nt][e] = NAN;
-                }
-        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -1059,8 +1056,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
         for (int m0 = 0; m0 < kMt; m0 += kMs) {
 #pragma unroll
             for (int j = 0; j < kTurn; ++j) {                        // block of the turn
-                float bvs = __shfl_sync(0xffffffffu, vs, kTurn * (i % kWin) + j);
-                bvs = isnan(bvs) ? 0.f : bvs;
+                const float bvs = __shfl_sync(0xffffffffu, vs, kTurn * (i % kWin) + j);
                 float d[kMs][NT][4];
                 uint32_t af[kMs][2][4];
 #pragma unroll
@@ -1218,11 +1214,10 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             }
         cp_async_wait_groups<0>();
         group_sync(0);
-        uint32_t poison[2] = {0, 0};                                 // tokens whose values are not finite
 #pragma unroll 1
         for (int st = 0; st < 3; ++st) {
             if (16 * st >= trows) break;
-            uint32_t wf[NT][2][3];
+            uint32_t wf[NT][2][3], poison = 0;                       // of this step's four tokens of the thread, not finite
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float4 y = make_float4(0.f, 0.f, 0.f, 0.f);          // PK: columns 4..7 hold no rows
@@ -1242,7 +1237,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         if (key + e >= trows || !isfinite(v[e])) {
-                            if (key + e < trows) poison[(key + e) >> 5] |= 1u << ((key + e) & 31);
+                            if (key + e < trows) poison |= 1u << e;
                             v[e] = 0.f;
                         }
                     }
@@ -1259,19 +1254,15 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma_bf16(o[mt][nt], af[i][0], af[i][1], af[i][2], af[i][3], wf[nt][0][k], wf[nt][1][k]);
             }
-        }
-        poison[0] = __reduce_or_sync(0xffffffffu, poison[0]);
-        poison[1] = __reduce_or_sync(0xffffffffu, poison[1]);
-        if (poison[0] | poison[1]) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
+            for (; poison; poison &= poison - 1) {
+                const int pos = base + 16 * st + 4 * t + __ffs(poison) - 1;
+#pragma unroll 1
+                for (int r = 0; r < min(live, RG); ++r) {
                     int lo, hi;
-                    row_sees(nt, e, lo, hi);
-                    for (int k = 0; k < kTail; ++k)
-                        if ((poison[k >> 5] >> (k & 31) & 1) && base + k >= lo && base + k < hi) l[nt][e] = NAN;
+                    seen(a, p, (rg * RG + r) / per, lo, hi);
+                    if (lo <= pos && hi > pos) atomicOr(&sh.poisoned, 1u << r);
                 }
+            }
         }
     }
 
@@ -1330,6 +1321,7 @@ __device__ __forceinline__ void attn_piece(const AttnKvArgs &a, const Span &p, c
             const float f = sh.m[i][r];
             sum.x = fmaf(y.x, f, sum.x), sum.y = fmaf(y.y, f, sum.y), sum.z = fmaf(y.z, f, sum.z), sum.w = fmaf(y.w, f, sum.w);
         }
+        if (sh.poisoned >> r & 1) sum = make_float4(NAN, NAN, NAN, NAN);
         if (u.whole) {
             const int rid = rg * RG + r;
             const float total = sh.l[0][r];

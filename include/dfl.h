@@ -448,10 +448,12 @@ int64_t dfl_kv8_attn_scratch_bytes(const dfl_kv8 *c, int n_q, int rows, int wind
  * <= j < len (all of them with window = 0) and all cnt staged ones. n_q / n_kv is at most 16. q and out
  * are DEVICE fp32, row m of sequence s at (s * rows + m) * ld, [n_q][head_dim] each. score != 0 adds each
  * logical block's share of row 0's weights, summed over the head's group of query heads in a fixed order,
- * to c->score (row 0 is the one row of a verify that is always committed). Sums and softmax statistics
+ * to c->score (row 0 is the one row of a verify that is always committed; weights come from queries and
+ * keys, so values that are not finite make outputs NaN but no score). Sums and softmax statistics
  * are fp32; queries and weights enter the tensor cores as two fp16 halves each, which hold 22 bits.
  * What a token adds is held to about 2^-32 of the row's largest weight times its own value, whatever the
- * values of other tokens, seen or not; the sums stay finite for values up to 2^88. One call gives the same bits each time.
+ * values of other tokens, seen or not; the sums stay finite for values up to 2^88. One call gives the same
+ * bits each time.
  * Where heads, rows and sequences are so many that a call shares its work out evenly (n_seq * n_kv * groups
  * of 8 or 16 rows above 152, above 76 for 9 rows and more of 256 channels, and less where the capacity is
  * long), the last bits of a sequence may depend on the other sequences' lengths, as they decide where its

@@ -50,3 +50,31 @@ def test_masked_values_of_any_size_cost_nothing(torch, hd, n_q, rows, seqs, size
         p.write(300, k=k, v=v)
         p.write(rows, commit=False)
         p.attn(n_q, rows, window=150)
+
+
+# ---- scores where values are not finite ----------------------------------------------------------------------
+@pytest.mark.parametrize("hd", [64, 256])
+@pytest.mark.parametrize("n_q,rows", [(2, 1), (4, 4), (16, 2)])
+def test_scores_are_weights_whatever_the_values(torch, hd, n_q, rows):  # noqa: F811
+    """Weights come from queries and keys: a value that is not finite, in a block or in the tail, makes the rows that see it NaN and leaves
+    what the blocks' scores get as it is."""
+    for at in (41, 198, None):
+        p = Pair(torch, 2, 1, hd, 10, seed=hd + rows)
+        k, v = p.new_rows(200), p.new_rows(200)
+        if at is not None:
+            v[0, at, 0, 9] = np.nan if at == 41 else np.inf
+        p.write(200, k=k, v=v)
+        vs = p.new_rows(rows)
+        if at is None:
+            vs[0, 0, 0, hd - 1] = np.nan
+        p.write(rows, commit=False, v=vs)
+        p.c.score.zero_()
+        q = p.new_rows(rows, n_q)
+        out = p.c.attn(p.dev(q), p.dev(p.len), score=True).cpu().numpy()
+        p.c.status()
+        assert np.isnan(out[0]).all() and np.isfinite(out[1]).all()
+        got = p.c.score.cpu().numpy()
+        for s in range(2):
+            with np.errstate(invalid="ignore"):
+                _, _, add, bound = p.heads[s][0].attn(q[s], 200, rows, 0, True, hd ** -0.5)
+            assert (np.abs(got[s, 0] - add) <= bound + 2.0 ** -23 * add).all()
