@@ -490,7 +490,8 @@ __device__ __forceinline__ Span span_of(const AttnKvArgs &a, int s, int sealed, 
     p.groups = (p.n * (a.n_q / a.c.n_kv) + rows_per_group - 1) / rows_per_group;
     return p;
 }
-// the span of a sequence by its first head: every call leaves the heads of a sequence with equal sealed counts
+// The span of a sequence by its first head. The heads of a sequence have equal sealed counts, but where a bad table entry has kept
+// one from going on with the others, or a caller has set them: heads that differ from the first are left alone (kErrState).
 __device__ __forceinline__ Span span_of_seq(const AttnKvArgs &a, int s, int rows_per_group) {
     return span_of(a, s, a.c.sealed[(size_t)s * a.c.n_kv], rows_per_group);
 }
@@ -1342,8 +1343,10 @@ __global__ void __launch_bounds__(AttnShape<HD, NT, PK>::kWarps * 32, AttnShape<
     const int split = int(blockIdx.x) - a.apart;
     Piece u{int(blockIdx.z), int(blockIdx.y) / a.groups, int(blockIdx.y) % a.groups};
     pdl_wait();
-    const Span p = span_of(a, u.s, a.c.sealed[(size_t)u.s * a.c.n_kv + u.h], RG);
+    const int sealed = a.c.sealed[(size_t)u.s * a.c.n_kv + u.h];
+    Span p = span_of_seq(a, u.s, RG);
     pdl_trigger();
+    if (p.z != sealed) p.bad = kErrState;
     if (p.bad) {
         if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(a.c.err, p.bad);
         return;
@@ -1422,7 +1425,7 @@ __global__ void __launch_bounds__(AttnShape<HD, NT, PK>::kWarps * 32, AttnShape<
         u.tail = from <= p.coded && to > p.coded;
         u.whole = from == 0 && u.tail;
         u.index = cta;
-        if (a.c.sealed[(size_t)s * a.c.n_kv + u.h] != p.z) {         // heads of a sequence that differ: left alone
+        if (a.c.sealed[(size_t)s * a.c.n_kv + u.h] != p.z) {         // a head that differs from the first
             if (tid == 0) atomicOr(a.c.err, kErrState);
             continue;
         }
@@ -1453,10 +1456,9 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(AttnKvArgs a, int r
     const Span p = span_of(a, s, sealed, RG);
     const int per = a.n_q / a.c.n_kv, live = p.n * per - rg * RG, row0 = blockIdx.x * (apart_rows ? 1 : kLanes);
     const int b0 = p.b0 + (int(blockIdx.x) - row_ctas) * kMergeThreads;
-    bool off_duty = p.bad || live <= 0 || (row_part ? row0 >= live : rg || b0 >= p.b0 + p.nb);
+    bool off_duty = p.bad || a.c.sealed[(size_t)s * a.c.n_kv] != sealed || live <= 0 || (row_part ? row0 >= live : rg || b0 >= p.b0 + p.nb);
     long W = 0, before = 0;                                          // the work in all, and that of the sequences before s
     if (a.share && !off_duty) {
-        off_duty = a.c.sealed[(size_t)s * a.c.n_kv] != sealed;
         for (int i = tid; i < a.c.n_seq; i += kMergeThreads) {
             const long x = weight_of(a, span_of_seq(a, i, RG));
             W += x;

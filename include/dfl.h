@@ -416,13 +416,14 @@ typedef struct dfl_kv8 {
 /* An empty cache: table = identity, sealed, score and err = 0. Codes, scales and tails need no values. */
 int dfl_kv8_init(const dfl_kv8 *c, void *cuda_stream);
 /* Status of the calls enqueued on a cache so far: synchronises the stream, then DFL_OK, or (clearing the
- * word) DFL_E_CAPACITY: a sequence's len + rows passed the capacity or was negative; DFL_E_STATE: a len
- * lay further behind the sealed blocks than the tail reaches (tokens that no call has written);
- * or does not hold what is sealed where a call does not cut back (attn, evict), or the sealed counts of a
- * sequence's heads differ where a call needs them equal (all calls leave them equal; checked by evict and
- * by attn of many sequences); DFL_E_INVALID_ARG: a table entry or a sealed count outside 0..n_blocks. A
- * sequence (or head) with such a fault was left as it was by the call that met it, its output rows among
- * them; a read leaves out only the blocks whose entries are bad. */
+ * word) one of these. DFL_E_CAPACITY: a sequence's len + rows passed the capacity or was negative.
+ * DFL_E_STATE: a len lay further behind the sealed blocks than the tail reaches (tokens that no call has
+ * written), or does not hold what is sealed where a call does not cut back (attn, evict), or the sealed counts
+ * of a sequence's heads differ where a call needs them equal (evict; attn leaves the heads that differ from the
+ * first). DFL_E_INVALID_ARG: a table entry or a sealed count outside 0..n_blocks. A sequence (or head) with
+ * such a fault was left as it was by the call that met it, its output rows among them; a read leaves out only
+ * the blocks whose entries are bad. Calls leave the heads of a sequence with equal counts, except where a bad
+ * entry kept one head from going on with the others. */
 int dfl_kv8_status(const dfl_kv8 *c, void *cuda_stream);
 /* Append committed rows (a prompt's, or a draft's context): rows k, v (DEVICE fp32, row m of sequence s
  * at k + (s * rows + m) * ld, [n_kv][head_dim] each; ld in floats, a multiple of 4, >= n_kv * head_dim)

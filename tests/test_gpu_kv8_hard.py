@@ -78,3 +78,40 @@ def test_scores_are_weights_whatever_the_values(torch, hd, n_q, rows):  # noqa: 
             with np.errstate(invalid="ignore"):
                 _, _, add, bound = p.heads[s][0].attn(q[s], 200, rows, 0, True, hd ** -0.5)
             assert (np.abs(got[s, 0] - add) <= bound + 2.0 ** -23 * add).all()
+
+
+# ---- table entries out of range ---------------------------------------------------------------------------
+@pytest.mark.parametrize("odd", [0, 1])
+@pytest.mark.parametrize("rows,commit", [(5, False), (40, True), (150, True)])
+def test_a_head_left_behind_is_met_alike_in_every_batch(torch, odd, rows, commit):  # noqa: F811
+    """A bad entry keeps one head of a sequence from going on with the other. Attention then leaves what differs from the first head,
+    however many sequences there are, and attends the others."""
+    from dflash_speculative_decode_gb300 import DflError, _abi
+    left = []
+    for seqs in (2, 90):
+        p = Pair(torch, seqs, 2, 64, 12, seed=rows)
+        p.write(32)
+        for _ in range(2):
+            p.write(16, commit=False)
+            p.len = p.len + 16                  # 32 rows of the tail are committed: the next call seals block 1
+        table = p.c.table.clone()
+        p.c.table[1, odd, 1] = 12
+        with pytest.raises(DflError) as e:
+            p.write(rows, commit=commit)
+        assert e.value.code == _abi.DFL_E_INVALID_ARG
+        z = (64 + rows) // 32 if commit else 2
+        assert p.c.sealed[1, odd] == 1 and p.c.sealed[1, 1 - odd] == z and (p.c.sealed[0] == z).all()
+        p.c.table.copy_(table)
+        length = p.dev(p.len + (rows if commit else 0))
+        q, n = p.dev(p.new_rows(5, 4)), p.dev(np.full(seqs, 5 if not commit else 0, np.int32))
+        if commit:
+            n[:] = 1
+        out = torch.full_like(q, 9.0)
+        p.c.attn(q, length, n, out=out)         # (after an append the row staged is whatever the tail holds)
+        with pytest.raises(DflError) as e:
+            p.c.status()
+        assert e.value.code == _abi.DFL_E_STATE
+        left.append([[bool((out[s, 0, 2 * h:2 * h + 2] == 9.0).all()) for h in range(2)] for s in range(2)])
+    assert left[0] == left[1]
+    assert left[0][0] == [False, False] and left[0][1][1]      # the sequence beside it, and the head that is not the first one's like
+    assert left[0][1][0] == (odd == 0 and commit)   # the first head: left only where its tail does not reach so far
