@@ -390,14 +390,13 @@ __global__ void __launch_bounds__(256) k_kv8_read(ReadArgs a) {
         bad = kErrCapacity;
     else if (L > kBlk * z + kTail)
         bad = kErrState;
-    if (!bad && first >= L) return;
-    const int b = bad ? 0 : first / kBlk + blockIdx.x;
+    const int hi = int(min((long long)L, (long long)first + a.rows)), b = bad ? 0 : first / kBlk + blockIdx.x;
+    if (!bad && (first >= hi || kBlk * b >= hi)) return;             // no token of the range: the entry is nobody's business
     if (!bad && b < z && unsigned(w.table[b]) >= unsigned(w.nb)) bad = kErrTable;
     if (bad) {
         if (threadIdx.x == 0) atomicOr(a.c.err, bad);
         return;
     }
-    const int hi = int(min((long long)L, (long long)first + a.rows));
     const int dq = hd / 4, pos0 = kBlk * b;
     const size_t blk = (size_t)kBlk * hd, row = (size_t)a.c.n_kv * hd, out0 = ((size_t)s * a.rows * a.c.n_kv + h) * hd;
     auto put = [&](float *out, int t, int d, const float4 &y) {      // token t of the block, channels d..

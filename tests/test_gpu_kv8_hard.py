@@ -115,3 +115,24 @@ def test_a_head_left_behind_is_met_alike_in_every_batch(torch, odd, rows, commit
     assert left[0] == left[1]
     assert left[0][0] == [False, False] and left[0][1][1]      # the sequence beside it, and the head that is not the first one's like
     assert left[0][1][0] == (odd == 0 and commit)   # the first head: left only where its tail does not reach so far
+
+
+def test_read_looks_at_the_blocks_of_its_range_only(torch):  # noqa: F811
+    from dflash_speculative_decode_gb300 import DflError, _abi
+    p = Pair(torch, 1, 2, 64, 8, seed=5)
+    p.write(160)
+    table = p.c.table.clone()
+    length = p.dev(p.len)
+    for first, rows, bad, hit in ((0, 64, 2, False), (0, 64, 3, False), (0, 65, 2, True), (33, 31, 2, False), (33, 31, 0, False), (33, 32, 2, True),
+                                  (70, 20, 4, False), (40, 8, 2, False)):
+        p.c.table.copy_(table)
+        p.c.table[0, 1, bad] = 99
+        got = p.c.read(length, rows, first=p.dev(np.array([first], np.int32)))
+        if hit:
+            with pytest.raises(DflError) as e:
+                p.c.status()
+            assert e.value.code == _abi.DFL_E_INVALID_ARG
+        else:
+            p.c.status()
+            for x, want in zip(got, p.heads[0][1].rows(160)):
+                np.testing.assert_array_equal(x[0, :, 1].cpu().numpy(), want[first:first + rows].astype(np.float32))
