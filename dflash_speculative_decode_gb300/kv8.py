@@ -160,9 +160,10 @@ class Kv8Cache:
         key = (n_q, M, window, score)
         need = self._need.get(key)
         if need is None:
-            need = self._need[key] = int(self.L.dfl_kv8_attn_scratch_bytes(self._c, n_q, M, window, score))
+            need = int(self.L.dfl_kv8_attn_scratch_bytes(self._c, n_q, M, window, score))
             if need < 0:
                 _refuse(f"{n_q} query heads and {M} rows: n_q must be a multiple of n_kv = {self.n_kv}, up to 16 a head, with 1..16 rows and a window >= 0")
+            self._need[key] = need
             if self._scratch_bytes < need:
                 self._kept.append(self._scratch)       # a captured graph may hold its address
                 self._scratch = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)

@@ -136,3 +136,17 @@ def test_read_looks_at_the_blocks_of_its_range_only(torch):  # noqa: F811
             p.c.status()
             for x, want in zip(got, p.heads[0][1].rows(160)):
                 np.testing.assert_array_equal(x[0, :, 1].cpu().numpy(), want[first:first + rows].astype(np.float32))
+
+
+# ---- refusals that repeat -----------------------------------------------------------------------------------
+def test_a_refused_shape_is_refused_the_same_way_again(torch):  # noqa: F811
+    from dflash_speculative_decode_gb300 import DflError
+    p = Pair(torch, 1, 2, 64, 4, seed=6)
+    p.write(40)
+    said = []
+    for q, window in ((p.new_rows(17, 2), 0), (p.new_rows(1, 3), 0), (p.new_rows(1, 2), -1)):
+        for _ in range(2):
+            with pytest.raises(DflError) as e:
+                p.c.attn(p.dev(q), p.dev(p.len), window=window)
+            said.append((e.value.code, str(e.value)))
+        assert said[-1] == said[-2]
