@@ -163,12 +163,12 @@ class Kv8Cache:
             need = int(self.L.dfl_kv8_attn_scratch_bytes(self._c, n_q, M, window, score))
             if need < 0:
                 _refuse(f"{n_q} query heads and {M} rows: n_q must be a multiple of n_kv = {self.n_kv}, up to 16 a head, with 1..16 rows and a window >= 0")
-            self._need[key] = need
             if self._scratch_bytes < need:
+                scratch = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
                 self._kept.append(self._scratch)       # a captured graph may hold its address
-                self._scratch = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
-                self._scratch_ptr, self._scratch_bytes = self._scratch.data_ptr(), need
+                self._scratch, self._scratch_ptr, self._scratch_bytes = scratch, scratch.data_ptr(), need
                 self._streams.clear()
+            self._need[key] = need
         if out is None:
             out = (self.torch.empty if n is None else self.torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
         po, Mo, ldo = self._rows(out, "out", n_q)

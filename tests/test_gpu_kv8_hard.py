@@ -150,3 +150,21 @@ def test_a_refused_shape_is_refused_the_same_way_again(torch):  # noqa: F811
                 p.c.attn(p.dev(q), p.dev(p.len), window=window)
             said.append((e.value.code, str(e.value)))
         assert said[-1] == said[-2]
+
+
+def test_a_call_that_found_no_memory_for_its_scratch_can_be_made_again(torch):  # noqa: F811
+    class Full:
+        def __getattr__(self, name):
+            return getattr(torch, name)
+
+        def empty(self, *args, **kw):
+            raise torch.cuda.OutOfMemoryError("none left")
+    p = Pair(torch, 2, 2, 64, 8, seed=7)
+    p.write(100)
+    p.write(3, commit=False)
+    p.attn(4, 1)
+    p.c.torch = Full()
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        p.attn(32, 3)
+    p.c.torch = torch
+    p.attn(32, 3)
