@@ -1232,8 +1232,27 @@ int ready(dfl_ctx *c) {
     return DFL_OK;
 }
 
+uint32_t snapshot_version(const dfl_config &g) { return g.kv8 ? 2 : 1; }   // 2: of planes in 8 bits, what is held of them
 // of a snapshot's configuration; without 8-bit planes the same as before there were any, so that older snapshots restore
 uint64_t config_hash(const dfl_config &g) { return fnv1a(&g, g.kv8 ? sizeof g : offsetof(dfl_config, kv8)); }
+
+// What a snapshot at position n holds of a plane in 8 bits, in pieces of `rows` rows of `width` bytes, `pitch` apart in the
+// plane: the codes and scales of the blocks that positions below n lie in, the tail and the sealed counts. The table stays the
+// identity in an engine.
+struct PlanePiece {
+    void *at;
+    size_t pitch, width, rows;
+};
+std::vector<PlanePiece> kv8_pieces(const dfl_kv8 &p, int n) {
+    const size_t kv = p.n_kv, blk = (size_t)DFL_KV8_BLOCK * p.head_dim, all = p.n_blocks, held = (n + DFL_KV8_BLOCK - 1) / DFL_KV8_BLOCK;
+    const size_t tail = kv * DFL_KV8_TAIL * p.head_dim * 4;
+    std::vector<PlanePiece> x;
+    if (held) x = {{p.k, all * blk, held * blk, kv}, {p.v, all * blk, held * blk, kv}, {p.k_scale, all * 4, held * 4, kv}, {p.v_scale, all * 4, held * 4, kv}};
+    x.push_back({p.k_tail, tail, tail, 1});
+    x.push_back({p.v_tail, tail, tail, 1});
+    x.push_back({p.sealed, kv * 4, kv * 4, 1});
+    return x;
+}
 
 size_t snapshot_size(const dfl_ctx *c, int n, int draft_n) {
     const dfl_config &g = c->cfg;
@@ -1242,7 +1261,7 @@ size_t snapshot_size(const dfl_ctx *c, int n, int draft_n) {
         const TLayer &L = c->tl[l];
         if (L.owner != l) continue;
         if (L.kv8_bytes) {
-            b += L.kv8_bytes;
+            for (const PlanePiece &x : kv8_pieces(L.kv8, n)) b += x.width * x.rows;
             continue;
         }
         const size_t row = (size_t)L.nkv * g.head_dim * 4;
@@ -1547,7 +1566,7 @@ int dfl_snapshot(dfl_ctx *c, void *dst, size_t bytes) {
     const dfl_config &g = c->cfg;
     SnapHeader hdr{};
     hdr.magic = kSnapMagic;
-    hdr.version = 1;
+    hdr.version = snapshot_version(c->cfg);
     hdr.cfg_hash = config_hash(c->cfg);
     hdr.n = c->n;
     hdr.draft_n = c->draft_n;
@@ -1559,8 +1578,10 @@ int dfl_snapshot(dfl_ctx *c, void *dst, size_t bytes) {
         const TLayer &L = c->tl[l];
         if (L.owner != l) continue;
         if (L.kv8_bytes) {
-            DFL_CK(cudaMemcpyAsync(d + off, L.kv8_base, L.kv8_bytes, cudaMemcpyDeviceToDevice, c->stream));
-            off += L.kv8_bytes;
+            for (const PlanePiece &x : kv8_pieces(L.kv8, c->n)) {
+                DFL_CK(cudaMemcpy2DAsync(d + off, x.width, x.at, x.pitch, x.width, x.rows, cudaMemcpyDeviceToDevice, c->stream));
+                off += x.width * x.rows;
+            }
             continue;
         }
         const size_t row = (size_t)L.nkv * g.head_dim * 4;
@@ -1592,7 +1613,7 @@ int dfl_restore(dfl_ctx *c, const void *src, size_t bytes) {
     DFL_CK(cudaMemcpyAsync(&hdr, src, sizeof hdr, cudaMemcpyDeviceToHost, c->stream));
     DFL_CK(cudaStreamSynchronize(c->stream));
     const dfl_config &g = c->cfg;
-    if (hdr.magic != kSnapMagic || hdr.version != 1) return fail(c, DFL_E_INVALID_ARG, "not a snapshot");
+    if (hdr.magic != kSnapMagic || hdr.version != snapshot_version(g)) return fail(c, DFL_E_INVALID_ARG, "not a snapshot");
     if (hdr.cfg_hash != config_hash(c->cfg)) return fail(c, DFL_E_INVALID_ARG, "snapshot of another configuration");
     if (hdr.n < 0 || hdr.n > g.max_ctx || hdr.draft_n < 0 || hdr.draft_n > hdr.n)
         return fail(c, DFL_E_INVALID_ARG, "corrupt snapshot header");
@@ -1604,8 +1625,10 @@ int dfl_restore(dfl_ctx *c, const void *src, size_t bytes) {
         const TLayer &L = c->tl[l];
         if (L.owner != l) continue;
         if (L.kv8_bytes) {
-            DFL_CK(cudaMemcpyAsync(L.kv8_base, s + off, L.kv8_bytes, cudaMemcpyDeviceToDevice, c->stream));
-            off += L.kv8_bytes;
+            for (const PlanePiece &x : kv8_pieces(L.kv8, hdr.n)) {
+                DFL_CK(cudaMemcpy2DAsync(x.at, x.pitch, s + off, x.width, x.width, x.rows, cudaMemcpyDeviceToDevice, c->stream));
+                off += x.width * x.rows;
+            }
             continue;
         }
         const size_t row = (size_t)L.nkv * g.head_dim * 4;

@@ -66,3 +66,35 @@ def test_a_plane_out_of_order_is_reported(weights, name, bad):
         got = eng.dfl_verify_block(rows)
         eng.dfl_commit_verify_rows(0)
         assert list(got[0]) == list(want[0]) and got[1] == want[1]
+
+
+def test_snapshots_hold_what_is_held(weights):
+    """What a snapshot takes for planes in 8 bits goes by the positions held, not by those that the engine could hold, and is below what
+    fp32 planes take; one taken at any position restores into a used context."""
+    from dataclasses import replace
+    pc, W = weights["tiny"]
+    t, prompt = pc.target, gen.prompt(pc.target.vocab, 150)
+    rows = [int(x) for x in gen.prompt(t.vocab, 8, request=2)]
+    engines = [(engine(p, W), engine(p, W, kv8=0)) for p in (pc, replace(pc, max_ctx=4096))]
+    full = [l for l in range(t.n_layers) if t.layer_type[l] == gen.FULL]
+    heads = sum(t.kv_heads[l] for l in full)
+    for n in (0, 1, 32, 33, 100, 150):
+        planes = []
+        for pair in engines:
+            if n:
+                for eng in pair:
+                    eng.dfl_prefill(prompt[eng.dfl_positions_held():n])
+            planes.append(pair[0].dfl_snapshot_bytes() - pair[1].dfl_snapshot_bytes() + 2 * heads * t.head_dim * 4 * n)
+        # keys and values: codes of the blocks that positions lie in, a scale each, 48 rows in fp32, the sealed counts
+        blocks = -(-n // 32)
+        assert planes == [2 * heads * (blocks * (32 * t.head_dim + 4) + 48 * t.head_dim * 4) + 4 * heads] * 2, n
+        eng = engines[1][0]
+        snap = eng.dfl_snapshot()
+        want = eng.dfl_verify_block(rows)
+        eng.dfl_commit_verify_rows(8)
+        eng.dfl_prefill(gen.prompt(t.vocab, 70, request=9))
+        eng.dfl_restore(snap)
+        assert eng.dfl_positions_held() == n
+        got = eng.dfl_verify_block(rows)
+        eng.dfl_commit_verify_rows(0)
+        assert list(got[0]) == list(want[0]) and got[1] == want[1]
