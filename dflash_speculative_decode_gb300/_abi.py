@@ -67,6 +67,7 @@ vp = ctypes.c_void_p
 
 # name -> (restype, argtypes); every entry point declared in include/dfl.h
 SIGNATURES = {
+    "dfl_config_bytes": (ctypes.c_int64, []),
     "dfl_required_bytes": (ctypes.c_int, [P(dfl_config), P(dfl_sizes)]),
     "dfl_init": (ctypes.c_int, [P(dfl_config), P(dfl_buffers), vp, P(vp)]),
     "dfl_load_tensor": (ctypes.c_int, [vp, ctypes.c_char_p, vp, ctypes.c_size_t]),
@@ -123,7 +124,7 @@ _lib = None
 
 
 def lib() -> ctypes.CDLL:
-    """The loaded library. Raises when libdfl.so is missing (build it with build.py / build())."""
+    """The loaded library. Raises when libdfl.so is missing (build it with build.py / build()) or holds another dfl_config."""
     global _lib
     if _lib is None:
         if not os.path.exists(LIB_PATH):
@@ -133,6 +134,8 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
+        if L.dfl_config_bytes() != ctypes.sizeof(dfl_config):
+            raise RuntimeError(f"{LIB_PATH} is of another build (dfl_config of {L.dfl_config_bytes()} bytes, not {ctypes.sizeof(dfl_config)}); build it again")
         _lib = L
     return _lib
 

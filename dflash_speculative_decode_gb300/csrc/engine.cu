@@ -1280,6 +1280,8 @@ size_t snapshot_size(const dfl_ctx *c, int n, int draft_n) {
 // =====================================================================================================
 extern "C" {
 
+int64_t dfl_config_bytes(void) { return sizeof(dfl_config); }
+
 int dfl_required_bytes(const dfl_config *cfg, dfl_sizes *out) {
     if (!cfg || !out) return DFL_E_INVALID_ARG;
     if (!validate(cfg).empty()) return DFL_E_INVALID_ARG;

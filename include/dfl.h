@@ -114,6 +114,11 @@ typedef struct dfl_sampling {
 
 typedef struct dfl_ctx dfl_ctx;
 
+/* sizeof(dfl_config) of the library. Headers of later builds may add fields at the end of dfl_config, and the
+ * library reads all that its own has: a client that loads a library it was not built beside first compares
+ * this with its own sizeof(dfl_config), and passes no dfl_config where they differ. */
+int64_t dfl_config_bytes(void);
+
 /* Sizes of the three device buffers for a configuration. Fails with DFL_E_INVALID_ARG or
  * DFL_E_UNSUPPORTED on a configuration the library does not take (it states which field). */
 int dfl_required_bytes(const dfl_config *cfg, dfl_sizes *out);
