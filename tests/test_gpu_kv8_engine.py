@@ -98,3 +98,48 @@ def test_snapshots_hold_what_is_held(weights):
         got = eng.dfl_verify_block(rows)
         eng.dfl_commit_verify_rows(0)
         assert list(got[0]) == list(want[0]) and got[1] == want[1]
+
+
+@pytest.fixture(scope="module")
+def wide():
+    """A small target with the E4B pair's head layout: 12 query heads of 256 over 2 key/value heads in full layers, 1 in sliding ones."""
+    from dataclasses import replace
+    pc = gen.tiny_pair()
+    pc = replace(pc, target=replace(pc.target, name="wide", n_heads=12, head_dim=256), max_ctx=512)
+    return pc, gen.generate(pc)
+
+
+@pytest.mark.parametrize("prompt,temperature", [(290, None), (95, 0.8)])
+def test_lockstep_in_the_e4b_pairs_head_layout(wide, prompt, temperature):
+    """Three groups of 16 rows a key/value head, up to eleven sealed blocks, against the oracle with planes rounded to the same codes."""
+    from gpu_harness import lockstep
+    from test_gpu_kv8_planes import oracle_pair
+    pc, W = wide
+    res, _ = lockstep(pc, W, gen.prompt(pc.target.vocab, prompt), 60, p=0.3, temperature=temperature, eng=engine(pc, W), op=oracle_pair(pc, W))
+    assert res.passes > 10
+
+
+def test_recovery_of_planes_in_8_bits(weights):
+    """A prefill whose passes give up over held positions (a test option; no fault): the restored context is as one that never failed."""
+    from dflash_speculative_decode_gb300 import DFL_OPT_KEEP_LOGITS, DflError
+    from dflash_speculative_decode_gb300._abi import DFL_E_STATE, DFL_E_TIMEOUT, DFL_OPT_TEST_STALL
+    pc, W = weights["tiny"]
+    prompt, more = gen.prompt(pc.target.vocab, 90, request=31), gen.prompt(pc.target.vocab, 40, request=32)
+    rows = [int(t) for t in gen.prompt(pc.target.vocab, 8, request=33)]
+    a, b = engine(pc, W), engine(pc, W)
+    for eng in (a, b):
+        eng.dfl_set_option(DFL_OPT_KEEP_LOGITS, 1)
+        eng.dfl_prefill(prompt)
+    snap = a.dfl_snapshot()
+    a.dfl_set_option(DFL_OPT_TEST_STALL, 1)
+    with pytest.raises(DflError) as e:
+        a.dfl_prefill(more)
+    assert e.value.code == DFL_E_TIMEOUT and a.dfl_positions_held() == 90
+    a.dfl_set_option(DFL_OPT_TEST_STALL, 0)
+    with pytest.raises(DflError) as e:
+        a.dfl_verify_block(rows)
+    assert e.value.code == DFL_E_STATE
+    a.dfl_restore(snap)
+    got, want = a.dfl_verify_block(rows), b.dfl_verify_block(rows)
+    np.testing.assert_array_equal(a.dfl_read_logits(0, 8), b.dfl_read_logits(0, 8))
+    assert list(got[0]) == list(want[0]) and got[1] == want[1]
