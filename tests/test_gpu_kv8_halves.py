@@ -18,7 +18,7 @@ def test_no_half_is_missing(torch, hd, kind, heads, rows, seqs):  # noqa: F811
     from dflash_speculative_decode_gb300 import Kv8Cache
     k, v, q = inputs(kind, hd, heads, rows, seed=hd + heads)
     c = Kv8Cache.empty(seqs, 1, hd, 8)
-    dev = lambda x: torch.from_numpy(np.array(np.broadcast_to(x, (seqs, *x.shape)))).cuda()  # noqa: E731
+    dev = lambda x: torch.from_numpy(np.broadcast_to(x, (seqs, *x.shape)).copy()).cuda()  # noqa: E731
     length = torch.zeros(seqs, dtype=torch.int32, device="cuda")
     c.append(dev(k[:CTX, None]), dev(v[:CTX, None]), length)
     length += CTX
