@@ -704,7 +704,7 @@ int kv8_attention(dfl_ctx *c, const TLayer &O, int k, bool own) {
         rc = dfl_kv8_stage(&O.kv8, held, nullptr, k, c->kv8_k, c->kv8_v, (int64_t)O.nkv * hd, c->stream);
         if (rc) return fail(c, rc, "dfl_kv8_stage");
     }
-    c->launches += 2;
+    c->launches += 2;   // and the parts' merge: a call that is not shared out has at least a unit's blocks and its tail apart
     rc = dfl_kv8_attn(&O.kv8, c->q, (int64_t)nq * hd, nq, k, held, nullptr, 0, 1, 1.0f / sqrtf((float)hd), 0, c->kv8_o, (int64_t)nq * hd,
                       c->kv8_scratch, c->kv8_scratch_bytes, c->stream);
     if (rc) return fail(c, rc, "dfl_kv8_attn");

@@ -1687,7 +1687,6 @@ cudaError_t launch_kv8_attn(const AttnKvArgs &a, cudaStream_t s) {
     const bool few = NT == 1 && a.rows * (a.n_q / a.c.n_kv) <= kFewRows;
     e = few ? launch_kv8_pieces<HD, NT, NT == 1>(a, s) : launch_kv8_pieces<HD, NT, false>(a, s);
     if (e != cudaSuccess) return e;
-    if (!a.share && a.splits == 1 && !a.apart && !a.score) return cudaSuccess;   // every unit is one CTA's
     const int apart_rows = !a.share && a.splits > 8, lanes = kMergeThreads / (HD / 4);
     const int row_ctas = apart_rows ? 8 * NT : (8 * NT + lanes - 1) / lanes;
     const unsigned x = row_ctas + (a.score ? (a.c.n_blocks + kMergeThreads - 1) / kMergeThreads : 0);
