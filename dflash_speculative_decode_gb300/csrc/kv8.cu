@@ -691,10 +691,10 @@ struct QueryRows {      // a warp takes every kWarps-th row of the group; `n` of
 // memory and expanded once in the CTA. Keys and values come through a ring of the warp's own (16-byte asynchronous copies):
 // what a warp copies only it reads.
 // What bounds it: with many sequences the issue of instructions and the latency between the steps of a turn at 16 or 24 warps an SM
-// (32 query heads over 8 of 128, one token of 64 sequences of some 5000: 120 us, 5.5 TB/s, 82 % of a plain copy's; verifies of
-// 8 rows of 8 sequences of 16384 and 16 heads of 128, two halves of 16 columns: 129 us, 4.2 TB/s, 62 %). With one
+// (32 query heads over 8 of 128, one token of 64 sequences of some 5000: 119 us, 5.6 TB/s, 83 % of a plain copy's; verifies of
+// 8 rows of 8 sequences of 16384 and 16 heads of 128, two halves of 16 columns: 128 us, 4.2 TB/s, 62 %). With one
 // sequence a CTA has one to three turns, and the time is the launch, the first loads (table, then scales and codes), some
-// 3 us a turn and the merge: 16384 tokens of 2 heads of 256 take 12.6 us for a token, 27 us for 8 rows of 6 heads each.
+// 3 us a turn and the merge: 16384 tokens of 2 heads of 256 take 12.2 us for a token, 27 us for 8 rows of 6 heads each.
 //
 // PK, for up to 4 rows: the query's lo halves take the columns 4..7 that no row needs, so one product does for both halves, in
 // both products. The thread pairs t and t + 2 then hold the same two rows: after the first product each adds up the halves of

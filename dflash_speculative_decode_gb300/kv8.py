@@ -153,7 +153,7 @@ class Kv8Cache:
 
     def attn(self, q, length, n=None, window: int = 0, causal: bool = True, scale=None, score: bool = False, out=None):
         """dfl_kv8_attn: attention of the staged rows, q fp32 [n_seq][rows][n_q][head_dim]; scale defaults to head_dim ** -0.5. Returns
-        `out` (allocated when None, rows behind n then zero)."""
+        `out` (allocated when None, rows behind n then zero), which overlaps none of the inputs."""
         pq, M, ldq = self._rows(q, "q", 0)
         n_q = q.shape[2]
         pl, pn = self._ints(length, "length"), self._ints(n, "n", True)
