@@ -458,7 +458,7 @@ int64_t dfl_kv8_attn_scratch_bytes(const dfl_kv8 *c, int n_q, int rows, int wind
  * keys, so values that are not finite make outputs NaN but no score). Sums and softmax statistics
  * are fp32; queries and weights enter the tensor cores as two fp16 halves each, which hold 22 bits.
  * What a token adds is held to about 2^-32 of the row's largest weight times its own value, whatever the
- * values of other tokens, seen or not; the sums stay finite for values up to 2^88. One call gives the same
+ * values of other tokens, seen or not; the sums stay finite for values up to 2^87. One call gives the same
  * bits each time.
  * Where heads, rows and sequences are so many that a call shares its work out evenly (n_seq * n_kv * groups
  * of 8 or 16 rows above 152, above 76 for 9 rows and more of 256 channels, and less where the capacity is
