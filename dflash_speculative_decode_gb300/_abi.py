@@ -19,6 +19,7 @@ DFL_OK, DFL_E_INVALID_ARG, DFL_E_STATE, DFL_E_CAPACITY, DFL_E_UNSUPPORTED, DFL_E
 DFL_KEEP_ACCEPTED = -1
 DFL_OPT_KEEP_LOGITS, DFL_OPT_GRAPHS, DFL_OPT_STOP_LAYER, DFL_OPT_PROFILE, DFL_OPT_ATTN_CLUSTER = 1, 2, 3, 4, 5
 DFL_OPT_TEST_STALL, DFL_OPT_FUSE_STEPS, DFL_OPT_PLE_SPLIT = 6, 7, 8
+DFL_BF16, DFL_F16 = 0, 1
 ERRORS = {DFL_E_INVALID_ARG: "DFL_E_INVALID_ARG", DFL_E_STATE: "DFL_E_STATE", DFL_E_CAPACITY: "DFL_E_CAPACITY",
           DFL_E_UNSUPPORTED: "DFL_E_UNSUPPORTED", DFL_E_CUDA: "DFL_E_CUDA", DFL_E_TIMEOUT: "DFL_E_TIMEOUT"}
 
@@ -55,6 +56,12 @@ class dfl_kv8(ctypes.Structure):
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
                 ("k_tail", ctypes.c_void_p), ("v_tail", ctypes.c_void_p), ("table", ctypes.c_void_p),
                 ("sealed", ctypes.c_void_p), ("score", ctypes.c_void_p), ("err", ctypes.c_void_p)]
+
+
+class dfl_paged(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("type", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("held", ctypes.c_void_p), ("ring", ctypes.c_void_p), ("queue", ctypes.c_void_p), ("err", ctypes.c_void_p)]
 
 
 class dfl_sampling(ctypes.Structure):
@@ -114,6 +121,15 @@ SIGNATURES = {
                                     ctypes.c_float, ctypes.c_int, vp, ctypes.c_int64, vp, ctypes.c_size_t, vp]),
     "dfl_kv8_evict": (ctypes.c_int, [P(dfl_kv8), vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp]),
     "dfl_kv8_read": (ctypes.c_int, [P(dfl_kv8), vp, vp, ctypes.c_int, vp, vp, vp]),
+    "dfl_paged_init": (ctypes.c_int, [P(dfl_paged), vp]),
+    "dfl_paged_status": (ctypes.c_int, [P(dfl_paged), vp]),
+    "dfl_paged_plan": (ctypes.c_int, [P(dfl_paged), vp, vp, vp, vp, ctypes.c_int, vp]),
+    "dfl_paged_append": (ctypes.c_int, [P(dfl_paged), vp, ctypes.c_int, vp, ctypes.c_int64, vp, ctypes.c_int64, vp]),
+    "dfl_paged_prompt": (ctypes.c_int, [P(dfl_paged), vp, ctypes.c_int64, ctypes.c_int, vp, ctypes.c_int64, vp, ctypes.c_int64, vp, ctypes.c_int,
+                                        ctypes.c_int, ctypes.c_float, vp, ctypes.c_int64, vp]),
+    "dfl_paged_attn_scratch_bytes": (ctypes.c_int64, [P(dfl_paged), ctypes.c_int, ctypes.c_int]),
+    "dfl_paged_attn": (ctypes.c_int, [P(dfl_paged), vp, ctypes.c_int64, ctypes.c_int, ctypes.c_int, vp, vp, ctypes.c_int, ctypes.c_int,
+                                      ctypes.c_int, ctypes.c_float, vp, ctypes.c_int64, vp, ctypes.c_size_t, vp]),
     "dfl_q41_gemm_noalloc": (ctypes.c_int, [vp, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int, vp, vp]),
     "dfl_q41_gemm_noalloc_max_scratch": (ctypes.c_int64, []),
     "dfl_q41_gemm_noalloc_status": (ctypes.c_int, [vp]),

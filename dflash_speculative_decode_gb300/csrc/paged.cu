@@ -1,0 +1,438 @@
+// paged.cu -- a paged key/value cache in 16 bits (include/dfl.h, dfl_paged): plans, rows into pages, attention.
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace dfl {
+namespace {
+
+// ---------------------------------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------------------------------
+// Sums over the sequences give each one's rows, the pages it gives back and those it takes. A CTA reads all
+// lengths and scans them itself, so that one launch of many CTAs can share the writing: slots, table entries
+// and ring places of a plan follow from the state before it alone. Pages taken that the ring did not hold yet
+// are those given back in this call, found by the sums. The CTA that comes last writes what all read.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanEach = DFL_PAGED_MAX_SEQ / kPlanThreads;
+
+struct PlanArgs {
+    dfl_paged c;
+    const int32_t *len, *cnt;
+    int32_t *cu, *slots;
+    int rows;
+};
+
+// Inclusive sum over the CTA's threads; *total gets the whole.
+__device__ long long plan_scan(long long v, long long *red, long long *total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    constexpr int kW = kPlanThreads / 32;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) red[w] = v;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+        if (i < w) before += red[i];
+        all += red[i];
+    }
+    *total = all;
+    return before + v;
+}
+
+// the first sequence whose sum lies above x (sums ascend; one does)
+__device__ __forceinline__ int plan_find(const int *sum, int n, int x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (sum[mid] > x) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
+    extern __shared__ int plan_smem[];
+    __shared__ long long red[kPlanThreads / 32];
+    __shared__ int s_bits, s_used, s_last;
+    const dfl_paged &c = a.c;
+    const int S = c.n_seq, N = c.n_pages, P = c.page, t = threadIdx.x;
+    int *row_end = plan_smem, *give_end = row_end + S, *take_end = give_end + S, *want = take_end + S, *had = want + S, *got = had + S;
+    pdl_wait();
+    if (t == 0) s_bits = s_used = 0;
+    const int first = c.queue[0], count = c.queue[1];
+    // the sequences of a thread follow each other, so that its own sums add up in place
+    const int each = (S + kPlanThreads - 1) / kPlanThreads, s0 = min(t * each, S), s1 = min(s0 + each, S);
+    int bits = 0, n[kPlanEach], len[kPlanEach], held[kPlanEach];
+    long long sum = 0, total, gives, takes;
+    for (int i = 0; i < kPlanEach; ++i)
+        if (s0 + i < s1) {
+            len[i] = a.len[s0 + i], n[i] = a.cnt[s0 + i], held[i] = c.held[s0 + i];
+            if (len[i] < 0 || n[i] < 0) len[i] = -1, n[i] = 0, bits |= kPgArg;
+            sum += n[i];
+        }
+    long long at = plan_scan(sum, red, &total) - sum, give = 0, take = 0;
+    for (int i = 0; i < kPlanEach; ++i)
+        if (s0 + i < s1) {
+            const int s = s0 + i;
+            at += n[i];
+            row_end[s] = int(min(at, (long long)INT32_MAX));
+            bool fine = len[i] >= 0;
+            if (fine && ((long long)len[i] + n[i] > (long long)c.max_pages * P || at > a.rows)) fine = false, bits |= kPgCapacity;
+            if (held[i] < 0 || held[i] > c.max_pages) fine = false, held[i] = 0, bits |= kPgState;
+            want[s] = fine ? int(((long long)len[i] + n[i] + P - 1) / P) : held[i];
+            had[s] = held[i];
+            got[s] = fine;
+            give += max(held[i] - want[s], 0);
+            take += max(want[s] - held[i], 0);
+        }
+    give = plan_scan(give, red, &gives) - give;
+    take = plan_scan(take, red, &takes) - take;
+    const bool sound = first >= 0 && first < N && count >= 0 && count <= N && count + gives <= N;
+    const int have = sound ? int(count + gives) : 0;
+    for (int s = s0; s < s1; ++s) {
+        give += max(had[s] - want[s], 0);
+        const int need = max(want[s] - had[s], 0);
+        take += need;
+        if (!sound) got[s] = 0, bits |= kPgState;
+        if (got[s] && need && take > have) got[s] = 0, bits |= kPgCapacity;
+        give_end[s] = int(min(give, (long long)INT32_MAX));
+        take_end[s] = int(min(take, (long long)INT32_MAX));
+        if (got[s] && need) atomicMax(&s_used, int(take));
+    }
+    if (bits) atomicOr(&s_bits, bits);
+    __syncthreads();
+    const int used = s_used, G = gridDim.x * kPlanThreads, me = blockIdx.x * kPlanThreads + t;
+    const int given = sound ? int(gives) : 0;
+    // page i of those that the plan takes, in their order
+    const auto taken = [&](int i) {
+        if (i < count) return c.ring[i < N - first ? first + i : first + i - N];
+        const int s = plan_find(give_end, S, i - count), j = i - count - (give_end[s] - (had[s] - want[s]));
+        return c.table[(size_t)s * c.max_pages + want[s] + j];
+    };
+    int worse = 0;
+    for (int r = me; r < a.rows; r += G) {
+        int slot = -1;
+        if (r < total) {
+            const int s = plan_find(row_end, S, r);
+            if (got[s]) {
+                const int pos = a.len[s] + r - (s ? row_end[s - 1] : 0), p = pos / P;
+                const int id = p < had[s] ? c.table[(size_t)s * c.max_pages + p] : taken(take_end[s] - (want[s] - had[s]) + p - had[s]);
+                if (id >= 0 && id < N) slot = id * P + pos % P;
+                else worse = kPgArg;
+            }
+        }
+        a.slots[r] = slot;
+    }
+    for (int i = me; i < used; i += G) {
+        const int s = plan_find(take_end, S, i);
+        c.table[(size_t)s * c.max_pages + had[s] + i - (take_end[s] - (want[s] - had[s]))] = taken(i);
+    }
+    for (int j = me; j < given; j += G) {
+        const int s = plan_find(give_end, S, j);
+        const long long to = (long long)first + count + j;
+        c.ring[to % N] = c.table[(size_t)s * c.max_pages + want[s] + j - (give_end[s] - (had[s] - want[s]))];
+    }
+    if (blockIdx.x == 0)
+        for (int s = t; s <= S; s += kPlanThreads) a.cu[s] = s ? min(row_end[s - 1], a.rows) : 0;
+    if (worse) atomicOr(&s_bits, worse);
+    __syncthreads();
+    if (t == 0) {
+        if (s_bits) atomicOr(c.err, s_bits);
+        __threadfence();
+        s_last = atomicInc(reinterpret_cast<unsigned *>(c.queue + 2), gridDim.x - 1) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last || !sound) return;
+    for (int s = t; s < S; s += kPlanThreads)
+        if (got[s]) c.held[s] = want[s];
+    if (t == 0) {
+        c.queue[0] = int(((long long)first + used) % N);
+        c.queue[1] = have - used;
+    }
+}
+
+__global__ void k_paged_init(dfl_paged c) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < c.n_pages) c.ring[i] = i;
+    if (i < c.n_seq) c.held[i] = 0;
+    if (i < 4) c.queue[i] = i == 1 ? c.n_pages : 0;
+    if (i == 0) *c.err = 0;
+}
+
+// ---------------------------------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------------------------------
+struct AppendArgs {
+    dfl_paged c;
+    const int32_t *slots;
+    int rows;
+    const uint8_t *k, *v;
+    int64_t ldk, ldv;          // bytes
+};
+
+// One thread moves 16 bytes of a key and of the value beside it.
+__global__ void __launch_bounds__(256) k_paged_append(AppendArgs a) {
+    const dfl_paged &c = a.c;
+    const int hc = c.head_dim / 8, chunks = c.n_kv * hc;       // 16-byte pieces of a head, of a row
+    pdl_wait();
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int r = int(i / chunks), at = int(i % chunks), h = at / hc, x = at % hc;
+    if (r >= a.rows) return;
+    const int slot = a.slots[r];
+    if (slot < 0) return;
+    const int page = slot / c.page;
+    if (page >= c.n_pages) {
+        pg_report(c.err, kPgArg);
+        return;
+    }
+    const size_t to = (((size_t)page * c.n_kv + h) * c.page + slot % c.page) * hc + x;
+    const uint4 k = ldg_stream(a.k + r * a.ldk + at * 16), v = ldg_stream(a.v + r * a.ldv + at * 16);
+    static_cast<uint4 *>(c.k)[to] = k;
+    static_cast<uint4 *>(c.v)[to] = v;
+}
+
+// ---------------------------------------------------------------------------------------------------
+// attention
+// ---------------------------------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ float to_f32(T x) { return float(x); }
+
+// A CTA takes 16 query rows (a token's heads of one group follow each other) of one key/value head, keys 32 at a time.
+template <typename T, int HD, bool PAGED>
+__global__ void __launch_bounds__(128) k_paged_rows(PagedAttnArgs a) {
+    extern __shared__ float rows_smem[];
+    constexpr int kPitch = HD + 1;
+    float *qs = rows_smem, *ks = qs + 16 * kPitch, *vs = ks + 32 * kPitch, *ps = vs + 32 * kPitch;
+    __shared__ int s_seq, s_tile;
+    const dfl_paged &c = a.c;
+    const int t = threadIdx.x, h = blockIdx.y, g = a.group;
+    pdl_wait();
+    if (t == 0) {
+        s_seq = -1;
+        if (PAGED) {
+            s_seq = blockIdx.z;
+            s_tile = blockIdx.x;
+        } else {
+            int left = blockIdx.x;
+            for (int s = 0; s < c.n_seq; ++s) {
+                const int a0 = a.cu[s], a1 = a.cu[s + 1];
+                if (a0 < 0 || a1 < a0 || a1 > a.total) {
+                    pg_report(c.err, kPgArg);
+                    continue;
+                }
+                const int tiles = int(((long long)(a1 - a0) * g + 15) / 16);
+                if (left < tiles) {
+                    s_seq = s;
+                    s_tile = left;
+                    break;
+                }
+                left -= tiles;
+            }
+        }
+    }
+    __syncthreads();
+    const int s = s_seq;
+    if (s < 0) return;
+    const int row0 = a.cu[s], n = a.cu[s + 1] - row0, len = PAGED ? a.len[s] : 0;
+    if (PAGED) {
+        int bits = 0;
+        if (row0 < 0 || n < 0 || n > a.total - row0 || n > a.rows || len < 0) bits = kPgArg;
+        else if (n > 0 && ((long long)len + n > (long long)c.held[s] * c.page || c.held[s] > c.max_pages)) bits = kPgState;
+        if (bits) {
+            if (t == 0) pg_report(c.err, bits);
+            return;
+        }
+    }
+    const int first = s_tile * 16, live = min(16, n * g - first);
+    if (live <= 0) return;
+    for (int i = t; i < 16 * HD; i += 128) {
+        const int r = i / HD, d = i % HD, p = first + min(r, live - 1);
+        qs[r * kPitch + d] = to_f32(static_cast<const T *>(a.q)[(row0 + p / g) * a.ldq + (h * g + p % g) * HD + d]);
+    }
+    const int r = t / 8, m = (first + min(r, live - 1)) / g, pos = len + m;
+    const int hi = a.causal ? pos + 1 : len + n, lo = !a.window ? 0 : max(0, a.causal ? pos - a.window + 1 : len - a.window);
+    const int m0 = first / g, m1 = (first + live - 1) / g;
+    const int all_lo = !a.window ? 0 : max(0, a.causal ? len + m0 - a.window + 1 : len - a.window), all_hi = a.causal ? len + m1 + 1 : len + n;
+    float top = -INFINITY, sum = 0.f, o[HD / 8];
+    for (int i = 0; i < HD / 8; ++i) o[i] = 0.f;
+    for (int k0 = all_lo; k0 < all_hi; k0 += 32) {
+        __syncthreads();
+        for (int i = t; i < 32 * HD; i += 128) {
+            const int kr = i / HD, d = i % HD, key = min(k0 + kr, all_hi - 1);
+            if (PAGED) {
+                const int id = c.table[(size_t)s * c.max_pages + key / c.page];
+                const bool ok = id >= 0 && id < c.n_pages;
+                if (!ok) pg_report(c.err, kPgArg);
+                const size_t at = (((size_t)(ok ? id : 0) * c.n_kv + h) * c.page + key % c.page) * HD + d;
+                ks[kr * kPitch + d] = ok ? to_f32(static_cast<const T *>(c.k)[at]) : NAN;
+                vs[kr * kPitch + d] = to_f32(static_cast<const T *>(c.v)[at]);
+            } else {
+                ks[kr * kPitch + d] = to_f32(static_cast<const T *>(a.k)[(row0 + key) * a.ldk + h * HD + d]);
+                vs[kr * kPitch + d] = to_f32(static_cast<const T *>(a.v)[(row0 + key) * a.ldv + h * HD + d]);
+            }
+        }
+        __syncthreads();
+        float w[4], best = -INFINITY;
+        bool odd = false;
+        for (int j = 0; j < 4; ++j) {
+            const int kr = t % 8 + 8 * j, key = k0 + kr;
+            float x = 0.f;
+            for (int d = 0; d < HD; ++d) x = fmaf(qs[r * kPitch + d], ks[kr * kPitch + d], x);
+            w[j] = key >= lo && key < hi ? x : -INFINITY;
+            odd |= isnan(w[j]);
+            best = fmaxf(best, w[j]);
+        }
+        for (int b = 1; b < 8; b <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, b));
+        const float next = fmaxf(top, best), base = next == -INFINITY ? 0.f : next * a.scale_log2;
+        const float keep = exp2f(fmaf(top, a.scale_log2, -base));
+        float add = odd ? NAN : 0.f;
+        for (int j = 0; j < 4; ++j) {
+            w[j] = exp2f(fmaf(w[j], a.scale_log2, -base));
+            add += w[j];
+            ps[r * 33 + t % 8 + 8 * j] = w[j];
+        }
+        for (int b = 1; b < 8; b <<= 1) add += __shfl_xor_sync(0xffffffffu, add, b);
+        sum = sum * keep + add;
+        top = next;
+        __syncwarp();
+        for (int i = 0; i < HD / 8; ++i) o[i] *= keep;
+        for (int kr = max(0, lo - k0); kr < min(32, hi - k0); ++kr) {
+            const float p = ps[r * 33 + kr];
+            for (int i = 0; i < HD / 8; ++i) o[i] = fmaf(p, vs[kr * kPitch + t % 8 + 8 * i], o[i]);
+        }
+    }
+    if (r >= live) return;
+    T *out = static_cast<T *>(a.out) + (row0 + m) * a.ldo + (h * g + (first + r) % g) * HD;
+    for (int i = 0; i < HD / 8; ++i) out[t % 8 + 8 * i] = T(o[i] / sum);
+}
+
+template <typename T, int HD, bool PAGED>
+cudaError_t launch_rows16(const PagedAttnArgs &a, dim3 grid, cudaStream_t s) {
+    const int dev = current_device();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    constexpr int kSmem = (80 * (HD + 1) + 16 * 33) * 4;
+    static bool done[kMaxDevices] = {};
+    if (!done[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(k_paged_rows<T, HD, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        done[dev] = true;
+    }
+    return launch_pdl(k_paged_rows<T, HD, PAGED>, grid, dim3(128), kSmem, s, a);
+}
+
+template <bool PAGED>
+cudaError_t launch_any(const PagedAttnArgs &a, dim3 grid, cudaStream_t s) {
+    const int hd = a.c.head_dim;
+    if (a.c.type == DFL_BF16)
+        return hd == 64 ? launch_rows16<__nv_bfloat16, 64, PAGED>(a, grid, s) : hd == 128 ? launch_rows16<__nv_bfloat16, 128, PAGED>(a, grid, s)
+                                                                                          : launch_rows16<__nv_bfloat16, 256, PAGED>(a, grid, s);
+    return hd == 64 ? launch_rows16<__half, 64, PAGED>(a, grid, s) : hd == 128 ? launch_rows16<__half, 128, PAGED>(a, grid, s)
+                                                                               : launch_rows16<__half, 256, PAGED>(a, grid, s);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+}  // namespace
+}  // namespace dfl
+
+using namespace dfl;
+
+extern "C" {
+
+int dfl_paged_init(const dfl_paged *c, void *stream) {
+    const int rc = pg_check(c);
+    if (rc) return rc;
+    const int n = std::max(std::max(c->n_pages, c->n_seq), 4);
+    k_paged_init<<<unsigned((n + 255) / 256), 256, 0, static_cast<cudaStream_t>(stream)>>>(*c);
+    return pg_launched(cudaGetLastError());
+}
+
+int dfl_paged_status(const dfl_paged *c, void *stream) {
+    const int rc = pg_check(c);
+    if (rc) return rc;
+    int bits = 0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cudaMemcpyAsync(&bits, c->err, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+        return DFL_E_CUDA;
+    if (!bits) return DFL_OK;
+    if (cudaMemsetAsync(c->err, 0, 4, s) != cudaSuccess) return DFL_E_CUDA;
+    return bits & kPgTimeout ? DFL_E_TIMEOUT : bits & kPgArg ? DFL_E_INVALID_ARG : bits & kPgState ? DFL_E_STATE : DFL_E_CAPACITY;
+}
+
+int dfl_paged_plan(const dfl_paged *c, const int32_t *len, const int32_t *cnt, int32_t *cu, int32_t *slots, int rows, void *stream) {
+    const int rc = pg_check(c);
+    if (rc) return rc;
+    if (!len || !cnt || !cu || rows < 0 || (rows && !slots)) return DFL_E_INVALID_ARG;
+    const void *p[] = {len, cnt, cu, slots};
+    for (const void *q : p)
+        if (!pg_aligned(q, 4)) return DFL_E_INVALID_ARG;
+    const int dev = current_device();
+    if (dev < 0) return DFL_E_CUDA;
+    static bool done[kMaxDevices] = {};
+    if (!done[dev]) {
+        if (cudaFuncSetAttribute(k_paged_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, 6 * 4 * DFL_PAGED_MAX_SEQ) != cudaSuccess)
+            return DFL_E_CUDA;
+        done[dev] = true;
+    }
+    const int ctas = std::min(std::max({1, (rows + 2047) / 2048, std::min(16, c->n_pages / 4096)}), 152);
+    const PlanArgs a{*c, len, cnt, cu, slots, rows};
+    return pg_launched(launch_pdl(k_paged_plan, dim3(ctas), dim3(kPlanThreads), (size_t)6 * 4 * c->n_seq, static_cast<cudaStream_t>(stream), a));
+}
+
+int dfl_paged_append(const dfl_paged *c, const int32_t *slots, int rows, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                     void *stream) {
+    int rc = pg_check(c);
+    if (rc) return rc;
+    if (rows == 0) return DFL_OK;
+    if (rows < 0 || !slots || !pg_aligned(slots, 4)) return DFL_E_INVALID_ARG;
+    if ((rc = pg_check_rows(c, k, ldk, c->n_kv)) || (rc = pg_check_rows(c, v, ldv, c->n_kv))) return rc;
+    const AppendArgs a{*c, slots, rows, static_cast<const uint8_t *>(k), static_cast<const uint8_t *>(v), ldk * 2, ldv * 2};
+    const int64_t blocks = ((int64_t)rows * c->n_kv * (c->head_dim / 8) + 255) / 256;
+    if (blocks > INT32_MAX) return DFL_E_UNSUPPORTED;
+    return pg_launched(launch_pdl(k_paged_append, dim3(unsigned(blocks)), dim3(256), 0, static_cast<cudaStream_t>(stream), a));
+}
+
+int dfl_paged_prompt(const dfl_paged *c, const void *q, int64_t ldq, int n_q, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                     const int32_t *cu, int rows, int window, float scale, void *out, int64_t ldo, void *stream) {
+    int rc = pg_check(c);
+    if (rc || (rc = pg_check_heads(c, n_q, window, scale))) return rc;
+    if (rows == 0) return DFL_OK;
+    if (rows < 0 || !cu || !pg_aligned(cu, 4)) return DFL_E_INVALID_ARG;
+    if ((rc = pg_check_rows(c, q, ldq, n_q)) || (rc = pg_check_rows(c, k, ldk, c->n_kv)) || (rc = pg_check_rows(c, v, ldv, c->n_kv)) ||
+        (rc = pg_check_rows(c, out, ldo, n_q)))
+        return rc;
+    const int g = n_q / c->n_kv;
+    const PagedAttnArgs a{*c, q, k, v, out, ldq, ldk, ldv, ldo, n_q, g, rows, cu, nullptr, 0, window, 1, scale * kLog2e};
+    const int64_t tiles = ((int64_t)rows * g + 15) / 16 + std::min(c->n_seq, rows);
+    if (tiles > INT32_MAX) return DFL_E_UNSUPPORTED;
+    return pg_launched(launch_any<false>(a, dim3(unsigned(tiles), c->n_kv), static_cast<cudaStream_t>(stream)));
+}
+
+int64_t dfl_paged_attn_scratch_bytes(const dfl_paged *c, int n_q, int rows) {
+    if (!c || c->n_seq < 1 || c->n_seq > DFL_PAGED_MAX_SEQ || c->n_kv < 1 || n_q < 1 || n_q % c->n_kv || n_q / c->n_kv > kPgMaxGroup ||
+        rows < 1 || rows > DFL_MAX_ROWS || (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256))
+        return -1;
+    return 256;
+}
+
+int dfl_paged_attn(const dfl_paged *c, const void *q, int64_t ldq, int n_q, int total, const int32_t *cu, const int32_t *len, int rows,
+                   int window, int causal, float scale, void *out, int64_t ldo, void *scratch, size_t scratch_bytes, void *stream) {
+    int rc = pg_check(c);
+    if (rc || (rc = pg_check_heads(c, n_q, window, scale))) return rc;
+    if (rows < 1 || total < 0 || !cu || !len || !pg_aligned(cu, 4) || !pg_aligned(len, 4)) return DFL_E_INVALID_ARG;
+    if (rows > DFL_MAX_ROWS) return DFL_E_UNSUPPORTED;
+    if (!scratch || !pg_aligned(scratch, 256) || (int64_t)scratch_bytes < dfl_paged_attn_scratch_bytes(c, n_q, rows)) return DFL_E_INVALID_ARG;
+    if (total == 0) return DFL_OK;
+    if ((rc = pg_check_rows(c, q, ldq, n_q)) || (rc = pg_check_rows(c, out, ldo, n_q))) return rc;
+    const int g = n_q / c->n_kv;
+    const PagedAttnArgs a{*c, q, nullptr, nullptr, out, ldq, 0, 0, ldo, n_q, g, total, cu, len, rows, window, causal != 0, scale * kLog2e};
+    return pg_launched(launch_any<true>(a, dim3((rows * g + 15) / 16, c->n_kv, c->n_seq), static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

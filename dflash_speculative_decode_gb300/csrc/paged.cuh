@@ -1,0 +1,58 @@
+// paged.cuh -- what the paged cache's sources share: error bits, argument checks, types.
+#pragma once
+
+#include <cmath>
+
+#include "common.cuh"
+#include "dfl.h"
+
+namespace dfl {
+
+// error bits (dfl_paged.err)
+constexpr int kPgCapacity = 1, kPgState = 2, kPgArg = 4, kPgTimeout = 8;
+constexpr int kPgMaxGroup = 16;          // query heads per key/value head
+
+inline bool pg_aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+inline int pg_check(const dfl_paged *c) {
+    if (!c || c->n_seq < 1 || c->n_seq > DFL_PAGED_MAX_SEQ || c->n_kv < 1 || c->n_kv > 1024 || c->n_pages < 1 || c->max_pages < 1)
+        return DFL_E_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return DFL_E_UNSUPPORTED;
+    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return DFL_E_UNSUPPORTED;
+    if (c->type != DFL_BF16 && c->type != DFL_F16) return DFL_E_UNSUPPORTED;
+    if ((int64_t)c->n_pages * c->page > INT32_MAX || (int64_t)c->max_pages * c->page > INT32_MAX) return DFL_E_INVALID_ARG;
+    if (!c->k || !c->v || !pg_aligned(c->k, 16) || !pg_aligned(c->v, 16)) return DFL_E_INVALID_ARG;
+    const void *p[] = {c->table, c->held, c->ring, c->queue, c->err};
+    for (const void *q : p)
+        if (!q || !pg_aligned(q, 4)) return DFL_E_INVALID_ARG;
+    return DFL_OK;
+}
+
+inline int pg_check_rows(const dfl_paged *c, const void *p, int64_t ld, int heads) {
+    return p && pg_aligned(p, 16) && ld % 8 == 0 && ld >= (int64_t)heads * c->head_dim ? DFL_OK : DFL_E_INVALID_ARG;
+}
+
+inline int pg_check_heads(const dfl_paged *c, int n_q, int window, float scale) {
+    if (n_q < 1 || n_q % c->n_kv || window < 0 || !(scale > 0) || !std::isfinite(scale * 1.5f)) return DFL_E_INVALID_ARG;
+    return n_q / c->n_kv > kPgMaxGroup ? DFL_E_UNSUPPORTED : DFL_OK;
+}
+
+inline int pg_launched(cudaError_t e) { return e == cudaSuccess ? DFL_OK : DFL_E_CUDA; }
+
+__device__ __forceinline__ void pg_report(int *err, int bits) {
+    if (bits) atomicOr(err, bits);
+}
+
+// Arguments of both attentions
+struct PagedAttnArgs {
+    dfl_paged c;
+    const void *q, *k, *v;     // k, v: packed rows of prompts; the pages are c.k, c.v
+    void *out;
+    int64_t ldq, ldk, ldv, ldo;
+    int n_q, group, total;     // rows of the packed buffers
+    const int32_t *cu, *len;
+    int rows, window, causal;
+    float scale_log2;          // scale * log2(e): weights are powers of two
+};
+
+}  // namespace dfl

@@ -487,6 +487,95 @@ int dfl_kv8_evict(const dfl_kv8 *c, const int32_t *len, int keep, int sink, int 
 int dfl_kv8_read(const dfl_kv8 *c, const int32_t *len, const int32_t *first, int rows, float *k_out,
                  float *v_out, void *cuda_stream);
 
+/* ---- a paged key/value cache in 16 bits: pages planned from lengths, rows in, attention ------------ */
+
+/* dfl_kv8 gives every sequence its whole capacity. This cache is one pool of pages that sequences of any
+ * lengths share, in bf16 or fp16. A page holds `page` tokens of every key/value head; a sequence's tokens lie
+ * in the pages that its row of the table names, in order. A step over it:
+ *   dfl_paged_plan(len, cnt)       which pages each sequence needs for its len tokens and cnt new rows
+ *   dfl_paged_append(slots)        a layer's new keys and values into their pages
+ *   dfl_paged_prompt               attention of whole prompts among their own rows, or
+ *   dfl_paged_attn                 attention of a token, or of a verify's rows, over the pages
+ * The caller then adds the rows that it keeps to len; the others' places are written again by the next step
+ * (a rollback is index arithmetic). A sequence that has ended gets len = cnt = 0, and its pages go back.
+ * The layers of a model that share lengths share the plan: one table, held, ring and queue, a k and v each.
+ *
+ * Rows of a call are packed: sequence s has rows cu[s] .. cu[s+1]-1 (cu: DEVICE int32 [n_seq+1]) of buffers
+ * [rows][heads][head_dim], row r at r * ld elements, heads and channels contiguous. Rows from cu[n_seq] on
+ * are neither read for anything that shows nor written.
+ *
+ * Everything is DEVICE memory of the caller's; the calls read the struct on the host and enqueue on the
+ * stream given. k and v are 16-byte aligned, the int32 arrays 4-byte aligned. */
+#define DFL_PAGED_MAX_SEQ 4096
+enum { DFL_BF16 = 0, DFL_F16 = 1 };
+typedef struct dfl_paged {
+    int32_t n_seq, n_kv, head_dim;   /* n_seq <= DFL_PAGED_MAX_SEQ, n_kv <= 1024, head_dim 64, 128 or 256 */
+    int32_t page;                    /* tokens of a page: 16, 32, 64 or 128 */
+    int32_t n_pages, max_pages;      /* of the pool, and of one sequence; both times page below 2^31 */
+    int32_t type;                    /* DFL_BF16 or DFL_F16: of k, v and the rows of all calls */
+    void *k, *v;                     /* [n_pages][n_kv][page][head_dim] */
+    int32_t *table;                  /* [n_seq][max_pages]: the page of each `page` tokens; entries from held on
+                                        mean nothing */
+    int32_t *held;                   /* [n_seq]: pages that a sequence has */
+    int32_t *ring;                   /* [n_pages]: the pages that no sequence has, a ring: queue[1] of them
+                                        from place queue[0] on */
+    int32_t *queue;                  /* [4]: where the ring begins, the pages in it, and two words of the
+                                        library's, which are 0 between calls */
+    int32_t *err;                    /* [1] sticky error bits, read and cleared by dfl_paged_status */
+} dfl_paged;
+
+/* An empty cache: no sequence holds a page, the ring has all of them in order, err = 0. */
+int dfl_paged_init(const dfl_paged *c, void *cuda_stream);
+/* Status of the calls enqueued on a cache so far: synchronises the stream, then DFL_OK, or (clearing the word)
+ * the first of these that a call met. DFL_E_TIMEOUT: a bounded device wait of dfl_paged_prompt gave up, and its
+ * output is undefined. DFL_E_INVALID_ARG: a row count out of order (cu descending or past the buffers, a negative
+ * len or cnt, more rows of a sequence than the call's `rows`), a slot past the pool, or a table or ring entry
+ * outside 0..n_pages-1. DFL_E_STATE: held or the queue out of order, or attention over tokens that the sequence has
+ * no pages for. DFL_E_CAPACITY: a sequence longer than max_pages, more rows than slots, or no pages left. */
+int dfl_paged_status(const dfl_paged *c, void *cuda_stream);
+/* Plan a step: sequence s is to hold ceil((len + cnt) / page) pages. What it has beyond them goes to the ring's
+ * end, then what it lacks comes from the ring's front, both in the order of the sequences and of their pages, so
+ * that a plan is the same each time. Writes
+ *   cu     [n_seq+1]  sums of cnt: where each sequence's rows begin (limited to `rows`)
+ *   slots  [rows]     each row's place, page * (tokens of a page) + the token's place in it, and -1 for rows
+ *                     behind the last sequence's (a captured graph's spare ones)
+ * A sequence that a plan cannot serve keeps the pages that it has, and its rows have slots -1: one longer than
+ * max_pages, one whose rows reach past `rows` and one whose pages are not there (after it no sequence of the call
+ * gets new pages) with DFL_E_CAPACITY; a negative len or cnt (DFL_E_INVALID_ARG) counts as no rows.
+ * len and cnt: int32 [n_seq], neither overlaps what is written. Calls of a cache must not overlap on the GPU. */
+int dfl_paged_plan(const dfl_paged *c, const int32_t *len, const int32_t *cnt, int32_t *cu, int32_t *slots, int rows,
+                   void *cuda_stream);
+/* Rows k, v (row r at r * ldk, r * ldv elements, [n_kv][head_dim] each; 16-byte aligned, ld a multiple of 8) into
+ * the places of slots[0..rows-1]; a negative slot's row is left out. Two rows of one call must not have one slot
+ * (a plan's have not). */
+int dfl_paged_append(const dfl_paged *c, const int32_t *slots, int rows, const void *k, int64_t ldk, const void *v,
+                     int64_t ldv, void *cuda_stream);
+/* Causal grouped-query attention of packed prompts among their own rows (of a sequence's first tokens; the cache's
+ * pages are not read):  out[i][h] = sum_j softmax_j(scale * q[i][h] . k[j][h / g]) v[j][h / g],  g = n_q / n_kv at
+ * most 16, over the rows j <= i of the same sequence, with window > 0 only j > i - window. scale > 0. The buffers
+ * have `rows` rows, 16-byte aligned, ld multiples of 8. Scores, softmax statistics and sums are fp32; a row's
+ * weights are rounded once to the cache's type, as what the tensor cores take, and the output once. A value that
+ * is not finite makes NaN of the outputs of rows that see it, and touches no other. out overlaps no input.
+ * Each row's bits depend on its own sequence alone. */
+int dfl_paged_prompt(const dfl_paged *c, const void *q, int64_t ldq, int n_q, const void *k, int64_t ldk, const void *v,
+                     int64_t ldv, const int32_t *cu, int rows, int window, float scale, void *out, int64_t ldo,
+                     void *cuda_stream);
+/* Scratch bytes that dfl_paged_attn needs for n_q query heads and at most `rows` rows a sequence, or -1 for a shape
+ * it does not take. */
+int64_t dfl_paged_attn_scratch_bytes(const dfl_paged *c, int n_q, int rows);
+/* Grouped-query attention over the pages, of at most `rows` (1..DFL_MAX_ROWS) rows a sequence: row m of sequence s
+ * (row cu[s] + m of q and out, which have `total` rows) sits at position p = len[s] + m. causal != 0: it sees the
+ * tokens j <= p, with window > 0 only j > p - window. causal == 0 (a draft's block): every row sees the tokens
+ * len - window <= j < len (all of them with window = 0) and all the sequence's new ones. The new rows' keys and
+ * values are in the pages (dfl_paged_append). Numbers, groups and scale as for dfl_paged_prompt. A sequence with
+ * more rows than `rows`, or without the pages that it needs, is left as it is and reported; rows that see a page
+ * whose table entry is bad get NaN (reported). out overlaps no input. Calls on one scratch (DEVICE, 256-byte
+ * aligned) must not overlap on the GPU; nothing is kept in it from one call to the next. One call gives the same
+ * bits each time. */
+int dfl_paged_attn(const dfl_paged *c, const void *q, int64_t ldq, int n_q, int total, const int32_t *cu,
+                   const int32_t *len, int rows, int window, int causal, float scale, void *out, int64_t ldo,
+                   void *scratch, size_t scratch_bytes, void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif
