@@ -409,9 +409,7 @@ int dfl_paged_prompt(const dfl_paged *c, const void *q, int64_t ldq, int n_q, co
         return rc;
     const int g = n_q / c->n_kv;
     const PagedAttnArgs a{*c, q, k, v, out, ldq, ldk, ldv, ldo, n_q, g, rows, cu, nullptr, 0, window, 1, scale * kLog2e};
-    const int64_t tiles = ((int64_t)rows * g + 15) / 16 + std::min(c->n_seq, rows);
-    if (tiles > INT32_MAX) return DFL_E_UNSUPPORTED;
-    return pg_launched(launch_any<false>(a, dim3(unsigned(tiles), c->n_kv), static_cast<cudaStream_t>(stream)));
+    return launch_paged_prompt(a, static_cast<cudaStream_t>(stream));
 }
 
 int64_t dfl_paged_attn_scratch_bytes(const dfl_paged *c, int n_q, int rows) {

@@ -55,4 +55,6 @@ struct PagedAttnArgs {
     float scale_log2;          // scale * log2(e): weights are powers of two
 };
 
+int launch_paged_prompt(const PagedAttnArgs &a, cudaStream_t s);   // prompt.cu; a DFL_* code
+
 }  // namespace dfl

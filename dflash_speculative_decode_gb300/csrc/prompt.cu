@@ -1,0 +1,573 @@
+// prompt.cu -- causal grouped-query attention of packed prompts (include/dfl.h, dfl_paged_prompt) on the tcgen05
+// tensor cores.
+//
+// A tile's 128 rows are tokens x query heads: 128 / g tokens, the g heads of one key/value head beside each other
+// (row r = token r / g, head r % g), so a group's heads read their keys and values once and a short prompt fills
+// one tile. A CTA takes kTiles tiles that follow each other and walks over the keys they see, kKeys at a time:
+//     S = Q K^T (tensor memory), P = 2^(c S - m) rounded to the type (tensor memory, over S), O += P V
+// with c = scale * log2(e). A thread owns one row: it holds the row's maximum and sum and needs no other thread's
+// values. The maximum in use is renewed only where a tile's passes it by more than 8 powers of two; until then P
+// is larger than 1 and no sum changes scale, so O in tensor memory is seldom touched.
+//
+// P is rounded to the type of the values, as the tensor cores take their operands: a relative 2^-9 (bf16) or 2^-12
+// (fp16) of each weight at most, the size of the output's own rounding; the sum that divides is of the unrounded
+// weights, in fp32. fp16 weights are held times 2^6, so that what is lost below its smallest number lies 2^-31
+// below the largest weight.
+//
+// Masked places. A masked score is replaced, so what a key holds there shows nowhere. A masked weight is 0, and 0
+// times a value that is not finite would make NaN of rows that do not see it; that shows in the sums at the end
+// (a NaN sum where the weights' sum is none). Then the CTA does its tiles once more, taking what is not finite out
+// of each tile of values before the product, and notes for each row which channels it saw such a value in. So a
+// prompt without such values pays nothing for them, and one with them pays a few times its price.
+#include <algorithm>
+
+#include "paged.cuh"
+#include "tc.cuh"
+
+namespace dfl {
+namespace {
+
+template <int HD>
+struct PromptShape {
+    // 256 channels: one tile's sums take half of the tensor memory, so S is held twice instead of two tiles, and Q is
+    // in tensor memory too, where the product reads it beside the keys from shared memory
+    static constexpr int kTiles = HD == 256 ? 1 : 2;
+    static constexpr int kKeys = HD == 256 ? 64 : 128;
+    static constexpr int kStage = kKeys * HD * 2;
+    static constexpr int kStages = HD == 64 ? 8 : HD == 128 ? 5 : 7;
+    static constexpr int kQBytes = HD == 256 ? 0 : kTiles * 128 * HD * 2;
+    static constexpr int kSmem = kQBytes + kStages * kStage + 1024;   // + slack to align to 1024 bytes
+    static constexpr int kThreads = kTiles * 128 + 64;
+    // tensor memory columns
+    static constexpr int kS = 0, kSPitch = kKeys;                      // two of them: a tile's each, or two in turn
+    static constexpr int kO = 256;
+    static constexpr int kQ = 128;                                     // (256 channels alone)
+};
+
+struct PromptArgs {
+    dfl_paged c;
+    const uint8_t *q;
+    uint8_t *out;
+    int64_t ldq, ldo;          // bytes
+    int group, total, window;
+    const int32_t *cu;
+    float scale_log2;
+};
+
+// Instruction descriptor of kind::f16 with an fp32 accumulator of 128 rows and N columns: operands of the type, A
+// along its inputs, B along them or (transposed) along its columns.
+template <typename T>
+__device__ constexpr uint32_t prompt_idesc(int N, bool transposed) {
+    const uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | (transposed ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) | (128u >> 4 << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// A from tensor memory: 128 lanes, two inputs a column
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of a tile [keys][64-channel blocks of 128 bytes] read along its channels (the product's columns): 8 keys
+// are 1024 bytes, the next 64 channels `block` bytes further.
+__device__ __forceinline__ uint64_t values_desc(const void *tile, int block) {
+    const uint64_t a = saddr(tile);
+    return ((a >> 4) & 0x3FFFull) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *b) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(saddr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(saddr(b))
+        : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// two numbers rounded to the type, the first in the low half
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+// Whether a 16-bit number is an infinity or a NaN
+template <typename T>
+__device__ __forceinline__ bool odd16(uint32_t x) {
+    const uint32_t e = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+    return (x & e) == e;
+}
+
+__device__ __forceinline__ void mbar_inval(uint64_t *b) { asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(saddr(b)) : "memory"); }
+
+// The keys that tile w of the item sees, as tiles of kKeys
+struct KeyRange {
+    int begin, end;
+};
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
+    k_prompt(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PromptArgs a) {
+    using Sh = PromptShape<HD>;
+    constexpr int kTiles = Sh::kTiles, kKeys = Sh::kKeys, kSoft = kTiles * 128, kMaxStages = Sh::kStages;
+    extern __shared__ uint8_t prompt_smem_raw[];
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], b_q, b_s[2], b_p[2], b_o[2], b_meet[3], b_done;
+    __shared__ uint32_t s_tmem, s_odd[3][kKeys / 32];
+    __shared__ int s_seq, s_item, s_row0, s_rows, s_issued, s_again, s_sum[Sh::kThreads / 32];
+    __shared__ volatile int s_bad;
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(prompt_smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *qs = base, *ring = base + Sh::kQBytes;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, h = blockIdx.y, g = a.group;
+    const int tokens = 128 / g;                                  // of a tile
+    pdl_wait();
+
+    // ---- the CTA's item: tiles item * kTiles .. of a sequence; the longest items of a sequence come first ----
+    {
+        const int S = a.c.n_seq, each = (S + Sh::kThreads - 1) / Sh::kThreads, s0 = min(t * each, S), s1 = min(s0 + each, S);
+        const auto items = [&](int s) {
+            const int b = a.cu[s], e = a.cu[s + 1];
+            if (b < 0 || e < b || e > a.total) {
+                if (blockIdx.x == 0 && h == 0) pg_report(a.c.err, kPgArg);
+                return 0;
+            }
+            return (e - b + kTiles * tokens - 1) / (kTiles * tokens);
+        };
+        int mine = 0, sum;
+        for (int s = s0; s < s1; ++s) mine += items(s);
+        sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
+        }
+        if (t == 0) s_seq = -1;
+        if (lane == 31) s_sum[warp] = sum;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) sum += s_sum[w];
+        int left = int(blockIdx.x) - (sum - mine);
+        if (left >= 0 && left < mine)
+            for (int s = s0; s < s1; ++s) {
+                const int n = items(s);
+                if (left < n) {
+                    s_seq = s;
+                    s_item = n - 1 - left;
+                    s_row0 = a.cu[s];
+                    s_rows = a.cu[s + 1] - a.cu[s];
+                    break;
+                }
+                left -= n;
+            }
+        __syncthreads();
+        if (s_seq < 0) return;
+    }
+    const int row0 = s_row0, n = s_rows, tok0 = s_item * kTiles * tokens;
+    const auto range = [&](int w) {
+        const int lo = tok0 + w * tokens, hi = min(lo + tokens, n);
+        KeyRange r{0, 0};
+        if (lo < n) {
+            r.begin = a.window ? max(0, lo - a.window + 1) / kKeys : 0;
+            r.end = (hi + kKeys - 1) / kKeys;
+        }
+        return r;
+    };
+    const KeyRange r0 = range(0), r1 = kTiles == 2 ? range(1) : KeyRange{0, 0};
+    const int jb = r0.begin, je = max(r0.end, r1.end);           // tiles of keys that any row sees
+    if (warp == kTiles * 4 + 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&s_tmem)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (t == 0) s_bad = 0;
+
+    for (int again = 0; again < 2; ++again) {
+        // the second time the last stage of the ring holds the notes on values that are not finite
+        const int stages = kMaxStages - again;
+        if (t == 0) {
+            if (again) {
+                for (int i = 0; i < kMaxStages; ++i) mbar_inval(&full[i]), mbar_inval(&empty[i]);
+                for (int i = 0; i < 2; ++i) mbar_inval(&b_s[i]), mbar_inval(&b_p[i]), mbar_inval(&b_o[i]);
+                for (int i = 0; i < 3; ++i) mbar_inval(&b_meet[i]);
+                mbar_inval(&b_q), mbar_inval(&b_done);
+            }
+            for (int i = 0; i < kMaxStages; ++i) {
+                mbar_init(&full[i], 1);        // the producer's arrival (with the stage's bytes)
+                mbar_init(&empty[i], 1);       // the MMA thread's commit
+            }
+            mbar_init(&b_q, kSoft);            // Q lies where the products read it
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&b_s[i], 1);         // S is complete: the MMA thread's commit
+                mbar_init(&b_p[i], 128);       // P lies in tensor memory, and O may be added to
+                mbar_init(&b_o[i], 1);         // P V is added
+            }
+            for (int i = 0; i < 3; ++i) mbar_init(&b_meet[i], i ? 128 : kSoft);   // the threads of both tiles, of one
+            mbar_init(&b_done, 1);             // the MMA thread's last commit
+            s_issued = s_again = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        const uint32_t tmem = s_tmem;
+
+        if (warp == kTiles * 4) {
+            // ---- copies: K and V of each tile in turn through the ring ----
+            if (lane == 0) {
+                int k = 0;
+                bool stop = false;
+                for (int j = jb; j < je && !stop; ++j)
+                    for (int kv = 0; kv < 2; ++kv, ++k) {
+                        const int s = k % stages;
+                        if ((k >= stages && !mbar_wait(&empty[s], unsigned(k / stages - 1) & 1u, &s_bad)) || s_bad) {
+                            stop = true;
+                            break;
+                        }
+                        mbar_expect(&full[s], unsigned(Sh::kStage));
+                        for (int x = 0; x < HD / 64; ++x)
+                            tma_load_3d(ring + s * Sh::kStage + x * kKeys * 128, kv ? &tv : &tk, 64 * x, h, row0 + j * kKeys, &full[s]);
+                    }
+                s_issued = k;
+            }
+        } else if (warp == kTiles * 4 + 1) {
+            // ---- products ----
+            if (lane == 0) {
+                const uint32_t id_s = prompt_idesc<T>(kKeys, false), id_o = prompt_idesc<T>(HD, true);
+                bool ok = mbar_wait(&b_q, 0u, &s_bad);
+                const auto arrived = [&](int k) { return mbar_wait(&full[k % stages], unsigned(k / stages) & 1u, &s_bad); };
+                const auto scores = [&](int w, int at, int k) {        // tile w, S number `at`, keys in stage k
+                    const uint8_t *kt = ring + (k % stages) * Sh::kStage;
+                    const uint32_t d = tmem + Sh::kS + at * Sh::kSPitch;
+#pragma unroll
+                    for (int i = 0; i < HD / 16; ++i) {
+                        const uint64_t b = sw128_desc(kt + (i / 4) * kKeys * 128) + 2 * (i % 4);
+                        if constexpr (HD == 256) mma_ts(d, tmem + Sh::kQ + 8 * i, b, id_s, i > 0);
+                        else mma_ss(d, sw128_desc(qs + (w * (HD / 64) + i / 4) * 16384) + 2 * (i % 4), b, id_s, i > 0);
+                    }
+                };
+                const auto values = [&](int w, int at, int k, bool add) {
+                    const uint8_t *vt = ring + (k % stages) * Sh::kStage;
+#pragma unroll
+                    for (int i = 0; i < kKeys / 16; ++i)
+                        mma_ts(tmem + Sh::kO + w * HD, tmem + Sh::kS + at * Sh::kSPitch + 8 * i, values_desc(vt + i * 2048, kKeys * 128), id_o, add || i > 0);
+                };
+                tc_fence_after();
+                // a thread's products run in the order of issue: S may be written over P as soon as P V has been issued
+                for (int j = jb; ok && j <= je; ++j) {
+                    const int kk = 2 * (j - jb), kv = kk - 1;          // the stages of K j and V j - 1
+                    if constexpr (kTiles == 1) {
+                        if (j < je) {
+                            if (!(ok = arrived(kk))) break;
+                            tc_fence_after();
+                            scores(0, j & 1, kk);
+                            tc_commit(&b_s[j & 1]);
+                            tc_commit(&empty[kk % stages]);
+                        }
+                        if (j > jb) {
+                            if (!(ok = mbar_wait(&b_p[(j - 1) & 1], unsigned((j - 1 - jb) >> 1) & 1u, &s_bad) && arrived(kv))) break;
+                            tc_fence_after();
+                            values(0, (j - 1) & 1, kv, j - 1 > jb);
+                            tc_commit(&b_o[0]);
+                            tc_commit(&empty[kv % stages]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const KeyRange r = w ? r1 : r0;
+                            if (j - 1 >= r.begin && j - 1 < r.end) {
+                                if (!(ok = mbar_wait(&b_p[w], unsigned(j - 1 - r.begin) & 1u, &s_bad) && arrived(kv))) break;
+                                tc_fence_after();
+                                values(w, w, kv, j - 1 > r.begin);
+                                tc_commit(&b_o[w]);
+                            }
+                            if (w == 1 && j > jb) tc_commit(&empty[kv % stages]);
+                            if (j >= r.begin && j < r.end) {
+                                if (!(ok = arrived(kk))) break;
+                                tc_fence_after();
+                                scores(w, w, kk);
+                                tc_commit(&b_s[w]);
+                            }
+                        }
+                        if (!ok) break;
+                        if (j < je) tc_commit(&empty[kk % stages]);
+                    }
+                }
+                tc_commit(&b_done);
+            }
+            __syncwarp();
+        } else {
+            // ---- softmax: tile w, a row a thread ----
+            const int w = warp >> 2, r = t & 127;
+            const KeyRange rg = w ? r1 : r0;
+            const int t0 = tok0 + w * tokens;                          // the tile's first token
+            const bool live = r < tokens * g && t0 + r / g < n;
+            const int tok = min(t0 + min(r / g, tokens - 1), n - 1), hi = tok + 1, lo = a.window ? max(0, tok - a.window + 1) : 0;
+            const int full_lo = a.window ? max(0, min(t0 + tokens, n) - a.window) : 0;   // keys from here to t0 are seen by all rows
+            const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+            const uint32_t t_o = tmem + Sh::kO + w * HD + lanes;
+            // Q: rows of tokens behind the sequence's last one are zeros
+            if constexpr (HD == 256) {
+                const uint8_t *src = a.q + (int64_t)(row0 + tok) * a.ldq + (h * g + r % g) * HD * 2;
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 u = live ? *reinterpret_cast<const uint4 *>(src + 128 * x + 16 * i) : make_uint4(0, 0, 0, 0);
+                        v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+                    }
+                    tc_st32(tmem + Sh::kQ + 32 * x + lanes, v);
+                }
+                tc_wait_st();
+                tc_fence_before();
+            } else {
+                for (int i = r; i < 128 * (HD / 8); i += 128) {
+                    const int row = i / (HD / 8), ch = i % (HD / 8), at = t0 + row / g;
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (row < tokens * g && at < n)
+                        u = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(row0 + at) * a.ldq + ((h * g + row % g) * HD + 8 * ch) * 2);
+                    *reinterpret_cast<uint4 *>(qs + (w * (HD / 64) + ch / 8) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = u;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            mbar_arrive(&b_q);
+
+            constexpr float kShift = std::is_same<T, __nv_bfloat16>::value ? 0.f : 6.f;
+            const float c = a.scale_log2;
+            float top = -INFINITY, sum = 0.f;      // the maximum in use and the weights' sum
+            uint32_t seen[HD / 32];                // channels in which the row saw a value that is not finite
+#pragma unroll
+            for (int i = 0; i < HD / 32; ++i) seen[i] = 0;
+            int met[2] = {0, 0};                   // meetings of both tiles' threads, of this one's
+            bool ok = true;
+            for (int j = rg.begin; j < rg.end; ++j) {
+                const int it = j - rg.begin, at = kTiles == 1 ? (j & 1) : w;
+                const int phase = kTiles == 1 ? (j - jb) >> 1 : it;
+                // (a wait names a phase by its parity, so none may be left out: P V of the tile before, or with S held twice
+                // of the one before that, has been added already and only has to be ticked off)
+                constexpr int kAhead = kTiles == 1 ? 2 : 1;
+                ok = mbar_wait(&b_s[at], unsigned(phase) & 1u, &s_bad) && (it < kAhead || mbar_wait(&b_o[w], unsigned(it - kAhead) & 1u, &s_bad));
+                if (!__all_sync(0xffffffffu, ok)) break;               // tcgen05.ld takes the whole warp
+                tc_fence_after();
+                uint32_t s[kKeys / 32][32];
+                const uint32_t t_s = tmem + Sh::kS + at * Sh::kSPitch + lanes;
+#pragma unroll
+                for (int x = 0; x < kKeys / 32; ++x) tc_ld32_async(t_s + 32 * x, s[x]);
+                tc_wait_ld();
+#pragma unroll
+                for (int x = 0; x < kKeys / 32; ++x) tc_tie32(s[x]);
+                const int k0 = j * kKeys;
+                if (k0 + kKeys > t0 + 1 || k0 < full_lo) {
+#pragma unroll
+                    for (int x = 0; x < kKeys / 32; ++x)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int key = k0 + 32 * x + i;
+                            if (key < lo || key >= hi) s[x][i] = __float_as_uint(-INFINITY);
+                        }
+                }
+                float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int x = 0; x < kKeys / 32; ++x)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) m[y] = fmaxf(m[y], __uint_as_float(s[x][i + y]));
+                const float best = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                const bool renew = (best - top) * c > 8.f;
+                float keep = 1.f;
+                if (renew) {
+                    keep = exp2_fast((top - best) * c);
+                    top = best;
+                }
+                if (__any_sync(0xffffffffu, renew) && it > 0) {
+                    if constexpr (kAhead == 2) {
+                        ok = mbar_wait(&b_o[w], unsigned(it - 1) & 1u, &s_bad);
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                        tc_fence_after();
+                    }
+#pragma unroll 1
+                    for (int x = 0; x < HD; x += 32) {
+                        uint32_t o[32];
+                        tc_ld32(t_o + x, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                        tc_st32(t_o + x, o);
+                    }
+                }
+                const float off = top == -INFINITY ? 0.f : kShift - top * c;
+                float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int x = 0; x < kKeys / 64; ++x) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float p0 = exp2_fast(fmaf(__uint_as_float(s[2 * x + i / 16][2 * (i % 16)]), c, off));
+                        const float p1 = exp2_fast(fmaf(__uint_as_float(s[2 * x + i / 16][2 * (i % 16) + 1]), c, off));
+                        add[2 * (i & 1)] += p0;
+                        add[2 * (i & 1) + 1] += p1;
+                        p[i] = pack2<T>(p0, p1);
+                    }
+                    tc_st32(t_s + 32 * x, p);
+                }
+                sum = sum * keep + ((add[0] + add[1]) + (add[2] + add[3]));
+                if (again) {
+                    // what is not finite leaves the tile of values, and each row notes what it saw of it
+                    const bool both = kTiles == 2 && j >= r0.begin && j < r0.end && j >= r1.begin && j < r1.end;
+                    const int who = both ? t : r, count = both ? 256 : 128, id = both ? 0 : 1 + w;
+                    const int k = 2 * (j - jb) + 1, parts = count / kKeys, key = who / parts, part = who % parts;
+                    uint32_t *notes = reinterpret_cast<uint32_t *>(ring + (kMaxStages - 1) * Sh::kStage) + id * kKeys * (HD / 32), *odd = s_odd[id];
+                    const auto meet = [&] {
+                        mbar_arrive(&b_meet[id]);
+                        return __all_sync(0xffffffffu, mbar_wait(&b_meet[id], unsigned(met[id != 0]++) & 1u, &s_bad)) != 0;
+                    };
+                    ok = mbar_wait(&full[k % stages], unsigned(k / stages) & 1u, &s_bad);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    if (!(ok = meet())) break;     // the notes of the tile before have been read
+                    if (who < kKeys / 32) odd[who] = 0;
+                    if (!(ok = meet())) break;
+                    uint8_t *vt = ring + (k % stages) * Sh::kStage;
+                    bool any = false;
+                    for (int word = part * (HD / 32) / parts; word < (part + 1) * (HD / 32) / parts; ++word) {
+                        uint32_t bits = 0;
+                        for (int i = 0; i < 4; ++i) {
+                            const int ch = word * 4 + i;               // 16-byte pieces of the key's channels
+                            uint4 *p = reinterpret_cast<uint4 *>(vt + (ch / 8) * kKeys * 128 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+                            uint32_t v[4] = {p->x, p->y, p->z, p->w}, hit = 0;
+                            for (int y = 0; y < 4; ++y) {
+                                if (odd16<T>(v[y] & 0xFFFFu)) hit |= 1u << (2 * y), v[y] &= 0xFFFF0000u;
+                                if (odd16<T>(v[y] >> 16)) hit |= 2u << (2 * y), v[y] &= 0xFFFFu;
+                            }
+                            if (hit) *p = make_uint4(v[0], v[1], v[2], v[3]);
+                            bits |= hit << (8 * i);
+                        }
+                        notes[key * (HD / 32) + word] = bits;
+                        any |= bits != 0;
+                    }
+                    if (any) atomicOr(&odd[key / 32], 1u << (key % 32));
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    if (!(ok = meet())) break;
+                    for (int x = 0; x < kKeys / 32; ++x)
+                        for (uint32_t left = odd[x]; left; left &= left - 1) {
+                            const int kr = 32 * x + __ffs(left) - 1;
+                            if (k0 + kr >= lo && k0 + kr < hi)
+#pragma unroll
+                                for (int i = 0; i < HD / 32; ++i) seen[i] |= notes[kr * (HD / 32) + i];
+                        }
+                }
+                tc_wait_st();
+                tc_fence_before();
+                mbar_arrive(&b_p[at]);
+            }
+            // ---- the sums, divided and rounded ----
+            const int last = rg.end - rg.begin - 1;
+            if (last >= 0) {
+                if (kTiles == 1 && ok && last > 0) ok = mbar_wait(&b_o[w], unsigned(last - 1) & 1u, &s_bad);
+                if (ok) ok = mbar_wait(&b_o[w], unsigned(last) & 1u, &s_bad);
+                if (__all_sync(0xffffffffu, ok)) {
+                    tc_fence_after();
+                    const float part = 1.f / sum;
+                    uint8_t *dst = a.out + (int64_t)(row0 + tok) * a.ldo + (h * g + r % g) * HD * 2;
+                    bool odd = false;
+#pragma unroll
+                    for (int x = 0; x < HD / 32; ++x) {
+                        uint32_t o[32];
+                        tc_ld32(t_o + 32 * x, o);
+                        const uint32_t gone = seen[x];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            odd |= isnan(__uint_as_float(o[i]));
+                            o[i] = gone >> i & 1u ? 0x7FFFFFFFu : __float_as_uint(__uint_as_float(o[i]) * part);
+                        }
+                        if (live)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<uint4 *>(dst + 64 * x + 16 * i) =
+                                    make_uint4(pack2<T>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
+                                               pack2<T>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
+                                               pack2<T>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
+                                               pack2<T>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
+                    }
+                    if (live && odd && !isnan(sum)) s_again = 1;
+                }
+            }
+        }
+        tc_fence_before();
+        __syncthreads();
+        if (t == 0) {
+            // every commit has landed before anything is used again; after a wait gave up, every copy issued too
+            if (s_bad)
+                for (int k = max(0, s_issued - stages); k < s_issued; ++k) mbar_drain(&full[k % stages], unsigned(k / stages) & 1u);
+            if (!mbar_drain(&b_done, 0u)) s_bad = 1;
+            if (s_bad) pg_report(a.c.err, kPgTimeout);
+        }
+        __syncthreads();
+        tc_fence_after();
+        const bool done = s_bad || !s_again;
+        __syncthreads();
+        if (done) break;
+    }
+    if (warp == kTiles * 4 + 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "r"(512) : "memory");
+}
+
+// Rows [rows][n_kv][HD] of the type, ld elements apart, as boxes of 64 channels x 1 head x `keys` rows in the 128-byte
+// swizzle; rows past the end read as zero.
+bool rows_map(CUtensorMap *map, const dfl_paged &c, const void *p, int64_t ld, int rows, int keys) {
+    const EncodeTiled enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(c.head_dim), cuuint64_t(c.n_kv), cuuint64_t(rows)};
+    const cuuint64_t strides[2] = {cuuint64_t(c.head_dim) * 2, cuuint64_t(ld) * 2};
+    const cuuint32_t box[3] = {64u, 1u, cuuint32_t(keys)}, estr[3] = {1u, 1u, 1u};
+    return enc(map, c.type == DFL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(p), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int HD>
+int launch_prompt(const PagedAttnArgs &a, cudaStream_t s) {
+    using Sh = PromptShape<HD>;
+    const int dev = current_device();
+    if (dev < 0) return DFL_E_CUDA;
+    static bool done[kMaxDevices] = {};
+    if (!done[dev]) {
+        if (cudaFuncSetAttribute(k_prompt<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess) return DFL_E_CUDA;
+        done[dev] = true;
+    }
+    CUtensorMap tk, tv;
+    if (!rows_map(&tk, a.c, a.k, a.ldk, a.total, Sh::kKeys) || !rows_map(&tv, a.c, a.v, a.ldv, a.total, Sh::kKeys)) return DFL_E_CUDA;
+    const PromptArgs p{a.c, static_cast<const uint8_t *>(a.q), static_cast<uint8_t *>(a.out), a.ldq * 2, a.ldo * 2, a.group, a.total, a.window, a.cu,
+                       a.scale_log2};
+    const int per = Sh::kTiles * (128 / a.group);                // tokens of an item
+    const int64_t items = (int64_t)a.total / per + std::min(a.c.n_seq, a.total);
+    if (items > INT32_MAX) return DFL_E_UNSUPPORTED;
+    return pg_launched(launch_pdl(k_prompt<T, HD>, dim3(unsigned(items), a.c.n_kv), dim3(Sh::kThreads), Sh::kSmem, s, tk, tv, p));
+}
+
+}  // namespace
+
+int launch_paged_prompt(const PagedAttnArgs &a, cudaStream_t s) {
+    const int hd = a.c.head_dim;
+    if (a.c.type == DFL_BF16)
+        return hd == 64 ? launch_prompt<__nv_bfloat16, 64>(a, s) : hd == 128 ? launch_prompt<__nv_bfloat16, 128>(a, s) : launch_prompt<__nv_bfloat16, 256>(a, s);
+    return hd == 64 ? launch_prompt<__half, 64>(a, s) : hd == 128 ? launch_prompt<__half, 128>(a, s) : launch_prompt<__half, 256>(a, s);
+}
+
+}  // namespace dfl
