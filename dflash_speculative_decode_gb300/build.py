@@ -12,7 +12,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdfl.so")
-SOURCES = ["gemm.cu", "rows.cu", "engine.cu", "tcgemm.cu", "kv8.cu", "paged.cu", "prompt.cu"]
+SOURCES = ["gemm.cu", "rows.cu", "engine.cu", "tcgemm.cu", "kv8.cu", "paged.cu", "prompt.cu", "pagedattn.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
          "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

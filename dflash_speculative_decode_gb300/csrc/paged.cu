@@ -197,145 +197,6 @@ __global__ void __launch_bounds__(256) k_paged_append(AppendArgs a) {
     static_cast<uint4 *>(c.v)[to] = v;
 }
 
-// ---------------------------------------------------------------------------------------------------
-// attention
-// ---------------------------------------------------------------------------------------------------
-template <typename T>
-__device__ __forceinline__ float to_f32(T x) { return float(x); }
-
-// A CTA takes 16 query rows (a token's heads of one group follow each other) of one key/value head, keys 32 at a time.
-template <typename T, int HD, bool PAGED>
-__global__ void __launch_bounds__(128) k_paged_rows(PagedAttnArgs a) {
-    extern __shared__ float rows_smem[];
-    constexpr int kPitch = HD + 1;
-    float *qs = rows_smem, *ks = qs + 16 * kPitch, *vs = ks + 32 * kPitch, *ps = vs + 32 * kPitch;
-    __shared__ int s_seq, s_tile;
-    const dfl_paged &c = a.c;
-    const int t = threadIdx.x, h = blockIdx.y, g = a.group;
-    pdl_wait();
-    if (t == 0) {
-        s_seq = -1;
-        if (PAGED) {
-            s_seq = blockIdx.z;
-            s_tile = blockIdx.x;
-        } else {
-            int left = blockIdx.x;
-            for (int s = 0; s < c.n_seq; ++s) {
-                const int a0 = a.cu[s], a1 = a.cu[s + 1];
-                if (a0 < 0 || a1 < a0 || a1 > a.total) {
-                    pg_report(c.err, kPgArg);
-                    continue;
-                }
-                const int tiles = int(((long long)(a1 - a0) * g + 15) / 16);
-                if (left < tiles) {
-                    s_seq = s;
-                    s_tile = left;
-                    break;
-                }
-                left -= tiles;
-            }
-        }
-    }
-    __syncthreads();
-    const int s = s_seq;
-    if (s < 0) return;
-    const int row0 = a.cu[s], n = a.cu[s + 1] - row0, len = PAGED ? a.len[s] : 0;
-    if (PAGED) {
-        int bits = 0;
-        if (row0 < 0 || n < 0 || n > a.total - row0 || n > a.rows || len < 0) bits = kPgArg;
-        else if (n > 0 && ((long long)len + n > (long long)c.held[s] * c.page || c.held[s] > c.max_pages)) bits = kPgState;
-        if (bits) {
-            if (t == 0) pg_report(c.err, bits);
-            return;
-        }
-    }
-    const int first = s_tile * 16, live = min(16, n * g - first);
-    if (live <= 0) return;
-    for (int i = t; i < 16 * HD; i += 128) {
-        const int r = i / HD, d = i % HD, p = first + min(r, live - 1);
-        qs[r * kPitch + d] = to_f32(static_cast<const T *>(a.q)[(row0 + p / g) * a.ldq + (h * g + p % g) * HD + d]);
-    }
-    const int r = t / 8, m = (first + min(r, live - 1)) / g, pos = len + m;
-    const int hi = a.causal ? pos + 1 : len + n, lo = !a.window ? 0 : max(0, a.causal ? pos - a.window + 1 : len - a.window);
-    const int m0 = first / g, m1 = (first + live - 1) / g;
-    const int all_lo = !a.window ? 0 : max(0, a.causal ? len + m0 - a.window + 1 : len - a.window), all_hi = a.causal ? len + m1 + 1 : len + n;
-    float top = -INFINITY, sum = 0.f, o[HD / 8];
-    for (int i = 0; i < HD / 8; ++i) o[i] = 0.f;
-    for (int k0 = all_lo; k0 < all_hi; k0 += 32) {
-        __syncthreads();
-        for (int i = t; i < 32 * HD; i += 128) {
-            const int kr = i / HD, d = i % HD, key = min(k0 + kr, all_hi - 1);
-            if (PAGED) {
-                const int id = c.table[(size_t)s * c.max_pages + key / c.page];
-                const bool ok = id >= 0 && id < c.n_pages;
-                if (!ok) pg_report(c.err, kPgArg);
-                const size_t at = (((size_t)(ok ? id : 0) * c.n_kv + h) * c.page + key % c.page) * HD + d;
-                ks[kr * kPitch + d] = ok ? to_f32(static_cast<const T *>(c.k)[at]) : NAN;
-                vs[kr * kPitch + d] = to_f32(static_cast<const T *>(c.v)[at]);
-            } else {
-                ks[kr * kPitch + d] = to_f32(static_cast<const T *>(a.k)[(row0 + key) * a.ldk + h * HD + d]);
-                vs[kr * kPitch + d] = to_f32(static_cast<const T *>(a.v)[(row0 + key) * a.ldv + h * HD + d]);
-            }
-        }
-        __syncthreads();
-        float w[4], best = -INFINITY;
-        bool odd = false;
-        for (int j = 0; j < 4; ++j) {
-            const int kr = t % 8 + 8 * j, key = k0 + kr;
-            float x = 0.f;
-            for (int d = 0; d < HD; ++d) x = fmaf(qs[r * kPitch + d], ks[kr * kPitch + d], x);
-            w[j] = key >= lo && key < hi ? x : -INFINITY;
-            odd |= isnan(w[j]);
-            best = fmaxf(best, w[j]);
-        }
-        for (int b = 1; b < 8; b <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, b));
-        const float next = fmaxf(top, best), base = next == -INFINITY ? 0.f : next * a.scale_log2;
-        const float keep = exp2f(fmaf(top, a.scale_log2, -base));
-        float add = odd ? NAN : 0.f;
-        for (int j = 0; j < 4; ++j) {
-            w[j] = exp2f(fmaf(w[j], a.scale_log2, -base));
-            add += w[j];
-            ps[r * 33 + t % 8 + 8 * j] = w[j];
-        }
-        for (int b = 1; b < 8; b <<= 1) add += __shfl_xor_sync(0xffffffffu, add, b);
-        sum = sum * keep + add;
-        top = next;
-        __syncwarp();
-        for (int i = 0; i < HD / 8; ++i) o[i] *= keep;
-        for (int kr = max(0, lo - k0); kr < min(32, hi - k0); ++kr) {
-            const float p = ps[r * 33 + kr];
-            for (int i = 0; i < HD / 8; ++i) o[i] = fmaf(p, vs[kr * kPitch + t % 8 + 8 * i], o[i]);
-        }
-    }
-    if (r >= live) return;
-    T *out = static_cast<T *>(a.out) + (row0 + m) * a.ldo + (h * g + (first + r) % g) * HD;
-    for (int i = 0; i < HD / 8; ++i) out[t % 8 + 8 * i] = T(o[i] / sum);
-}
-
-template <typename T, int HD, bool PAGED>
-cudaError_t launch_rows16(const PagedAttnArgs &a, dim3 grid, cudaStream_t s) {
-    const int dev = current_device();
-    if (dev < 0) return cudaErrorInvalidDevice;
-    constexpr int kSmem = (80 * (HD + 1) + 16 * 33) * 4;
-    static bool done[kMaxDevices] = {};
-    if (!done[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(k_paged_rows<T, HD, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e != cudaSuccess) return e;
-        done[dev] = true;
-    }
-    return launch_pdl(k_paged_rows<T, HD, PAGED>, grid, dim3(128), kSmem, s, a);
-}
-
-template <bool PAGED>
-cudaError_t launch_any(const PagedAttnArgs &a, dim3 grid, cudaStream_t s) {
-    const int hd = a.c.head_dim;
-    if (a.c.type == DFL_BF16)
-        return hd == 64 ? launch_rows16<__nv_bfloat16, 64, PAGED>(a, grid, s) : hd == 128 ? launch_rows16<__nv_bfloat16, 128, PAGED>(a, grid, s)
-                                                                                          : launch_rows16<__nv_bfloat16, 256, PAGED>(a, grid, s);
-    return hd == 64 ? launch_rows16<__half, 64, PAGED>(a, grid, s) : hd == 128 ? launch_rows16<__half, 128, PAGED>(a, grid, s)
-                                                                               : launch_rows16<__half, 256, PAGED>(a, grid, s);
-}
-
 constexpr float kLog2e = 1.4426950408889634f;
 
 }  // namespace
@@ -416,7 +277,7 @@ int64_t dfl_paged_attn_scratch_bytes(const dfl_paged *c, int n_q, int rows) {
     if (!c || c->n_seq < 1 || c->n_seq > DFL_PAGED_MAX_SEQ || c->n_kv < 1 || n_q < 1 || n_q % c->n_kv || n_q / c->n_kv > kPgMaxGroup ||
         rows < 1 || rows > DFL_MAX_ROWS || (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256))
         return -1;
-    return 256;
+    return (int64_t)paged_attn_scratch(c, n_q, rows);
 }
 
 int dfl_paged_attn(const dfl_paged *c, const void *q, int64_t ldq, int n_q, int total, const int32_t *cu, const int32_t *len, int rows,
@@ -430,7 +291,7 @@ int dfl_paged_attn(const dfl_paged *c, const void *q, int64_t ldq, int n_q, int 
     if ((rc = pg_check_rows(c, q, ldq, n_q)) || (rc = pg_check_rows(c, out, ldo, n_q))) return rc;
     const int g = n_q / c->n_kv;
     const PagedAttnArgs a{*c, q, nullptr, nullptr, out, ldq, 0, 0, ldo, n_q, g, total, cu, len, rows, window, causal != 0, scale * kLog2e};
-    return pg_launched(launch_any<true>(a, dim3((rows * g + 15) / 16, c->n_kv, c->n_seq), static_cast<cudaStream_t>(stream)));
+    return launch_paged_attn(a, scratch, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -55,6 +55,9 @@ struct PagedAttnArgs {
     float scale_log2;          // scale * log2(e): weights are powers of two
 };
 
-int launch_paged_prompt(const PagedAttnArgs &a, cudaStream_t s);   // prompt.cu; a DFL_* code
+// a DFL_* code each
+int launch_paged_prompt(const PagedAttnArgs &a, cudaStream_t s);                 // prompt.cu
+int launch_paged_attn(const PagedAttnArgs &a, void *scratch, cudaStream_t s);    // pagedattn.cu
+size_t paged_attn_scratch(const dfl_paged *c, int n_q, int rows);
 
 }  // namespace dfl

@@ -486,6 +486,22 @@ def test_values_over_pages_that_are_not_finite(torch, heads, value, long):
         p.c.status()
 
 
+@pytest.mark.parametrize("window", [1, 5, 16, 17, 40, 100])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_token_does_not_touch_what_its_window_has_left(torch, window, causal):
+    """One row: every token before its window is a NaN, and so is what lies behind the row in its page."""
+    p = Pages(torch, (4, 2, 64), [200, 77], [1, 1], 32, "bf16")
+    for s, length in enumerate((200, 77)):
+        lo = max(0, length - window + 1 if causal else length - window)
+        for token in range(lo):
+            for x in ("k", "v"):
+                p.put(x, s, token, float("nan"), 3)
+    want, tol = p.want(window, causal, 0.125)
+    got = p.run(1, window, causal)
+    assert np.isfinite(got).all()
+    near(got, want, tol)
+
+
 def test_keys_over_pages_that_are_not_finite(torch):
     p = Pages(torch, (4, 2, 64), [100], [6], 16, "bf16")
     p.put("k", 0, 103, float("nan"), 5)
