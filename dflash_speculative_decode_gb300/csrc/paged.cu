@@ -13,36 +13,36 @@ namespace {
 // lengths and scans them itself, so that one launch of many CTAs can share the writing: slots, table entries
 // and ring places of a plan follow from the state before it alone. Pages taken that the ring did not hold yet
 // are those given back in this call, found by the sums. The CTA that comes last writes what all read.
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 256;
 constexpr int kPlanEach = DFL_PAGED_MAX_SEQ / kPlanThreads;
 
 struct PlanArgs {
     dfl_paged c;
     const int32_t *len, *cnt;
     int32_t *cu, *slots;
-    int rows;
+    int rows, shift;           // page = 1 << shift
 };
 
-// Inclusive sum over the CTA's threads; *total gets the whole.
-__device__ long long plan_scan(long long v, long long *red, long long *total) {
+// Sums over the CTA's threads of two numbers, up to each thread's own; *all gets the whole ones'.
+__device__ longlong2 plan_scan(longlong2 v, longlong2 *red, longlong2 *all) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     constexpr int kW = kPlanThreads / 32;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
+        const long long x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
+        if (lane >= o) v.x += x, v.y += y;
     }
-    __syncthreads();
     if (lane == 31) red[w] = v;
     __syncthreads();
-    long long before = 0, all = 0;
+    longlong2 total{0, 0};
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
-        if (i < w) before += red[i];
-        all += red[i];
+        const longlong2 r = red[i];
+        if (i == w) v.x += total.x, v.y += total.y;
+        total.x += r.x, total.y += r.y;
     }
-    *total = all;
-    return before + v;
+    *all = total;
+    return v;
 }
 
 // the first sequence whose sum lies above x (sums ascend; one does)
@@ -56,45 +56,53 @@ __device__ __forceinline__ int plan_find(const int *sum, int n, int x) {
     return lo;
 }
 
+template <int EACH>            // sequences of a thread at most
 __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
     extern __shared__ int plan_smem[];
-    __shared__ long long red[kPlanThreads / 32];
+    __shared__ longlong2 red[2][kPlanThreads / 32];
     __shared__ int s_bits, s_used, s_last;
     const dfl_paged &c = a.c;
     const int S = c.n_seq, N = c.n_pages, P = c.page, t = threadIdx.x;
-    int *row_end = plan_smem, *give_end = row_end + S, *take_end = give_end + S, *want = take_end + S, *had = want + S, *got = had + S;
+    int *row_end = plan_smem, *give_end = row_end + S, *take_end = give_end + S, *want = take_end + S, *had = want + S, *got = had + S, *lens = got + S;
     pdl_wait();
+    pdl_trigger();
     if (t == 0) s_bits = s_used = 0;
     const int first = c.queue[0], count = c.queue[1];
     // the sequences of a thread follow each other, so that its own sums add up in place
     const int each = (S + kPlanThreads - 1) / kPlanThreads, s0 = min(t * each, S), s1 = min(s0 + each, S);
-    int bits = 0, n[kPlanEach], len[kPlanEach], held[kPlanEach];
-    long long sum = 0, total, gives, takes;
-    for (int i = 0; i < kPlanEach; ++i)
+    int bits = 0, n[EACH], len[EACH], held[EACH];
+    longlong2 sum{0, 0}, total, moved;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        if (s0 + i < s1) len[i] = a.len[s0 + i], n[i] = a.cnt[s0 + i], held[i] = c.held[s0 + i];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
         if (s0 + i < s1) {
-            len[i] = a.len[s0 + i], n[i] = a.cnt[s0 + i], held[i] = c.held[s0 + i];
             if (len[i] < 0 || n[i] < 0) len[i] = -1, n[i] = 0, bits |= kPgArg;
-            sum += n[i];
+            sum.x += n[i];
         }
-    long long at = plan_scan(sum, red, &total) - sum, give = 0, take = 0;
-    for (int i = 0; i < kPlanEach; ++i)
+    long long at = plan_scan(sum, red[0], &total).x - sum.x;
+    longlong2 move{0, 0};      // pages given back, pages taken
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
         if (s0 + i < s1) {
             const int s = s0 + i;
             at += n[i];
             row_end[s] = int(min(at, (long long)INT32_MAX));
+            lens[s] = len[i];
             bool fine = len[i] >= 0;
             if (fine && ((long long)len[i] + n[i] > (long long)c.max_pages * P || at > a.rows)) fine = false, bits |= kPgCapacity;
             if (held[i] < 0 || held[i] > c.max_pages) fine = false, held[i] = 0, bits |= kPgState;
-            want[s] = fine ? int(((long long)len[i] + n[i] + P - 1) / P) : held[i];
+            want[s] = fine ? int(((long long)len[i] + n[i] + P - 1) >> a.shift) : held[i];
             had[s] = held[i];
             got[s] = fine;
-            give += max(held[i] - want[s], 0);
-            take += max(want[s] - held[i], 0);
+            move.x += max(held[i] - want[s], 0);
+            move.y += max(want[s] - held[i], 0);
         }
-    give = plan_scan(give, red, &gives) - give;
-    take = plan_scan(take, red, &takes) - take;
-    const bool sound = first >= 0 && first < N && count >= 0 && count <= N && count + gives <= N;
-    const int have = sound ? int(count + gives) : 0;
+    const longlong2 upto = plan_scan(move, red[1], &moved);
+    long long give = upto.x - move.x, take = upto.y - move.y;
+    const bool sound = first >= 0 && first < N && count >= 0 && count <= N && count + moved.x <= N;
+    const int have = sound ? int(count + moved.x) : 0;
     for (int s = s0; s < s1; ++s) {
         give += max(had[s] - want[s], 0);
         const int need = max(want[s] - had[s], 0);
@@ -108,7 +116,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
     if (bits) atomicOr(&s_bits, bits);
     __syncthreads();
     const int used = s_used, G = gridDim.x * kPlanThreads, me = blockIdx.x * kPlanThreads + t;
-    const int given = sound ? int(gives) : 0;
+    const int given = sound ? int(moved.x) : 0;
     // page i of those that the plan takes, in their order
     const auto taken = [&](int i) {
         if (i < count) return c.ring[i < N - first ? first + i : first + i - N];
@@ -116,18 +124,30 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
         return c.table[(size_t)s * c.max_pages + want[s] + j];
     };
     int worse = 0;
-    for (int r = me; r < a.rows; r += G) {
-        int slot = -1;
-        if (r < total) {
-            const int s = plan_find(row_end, S, r);
-            if (got[s]) {
-                const int pos = a.len[s] + r - (s ? row_end[s - 1] : 0), p = pos / P;
-                const int id = p < had[s] ? c.table[(size_t)s * c.max_pages + p] : taken(take_end[s] - (want[s] - had[s]) + p - had[s]);
-                if (id >= 0 && id < N) slot = id * P + pos % P;
-                else worse = kPgArg;
+    // four rows a thread: they mostly lie in one page, which is looked up once
+    for (int r0 = 4 * me; r0 < a.rows; r0 += 4 * G) {
+        int slot[4] = {-1, -1, -1, -1}, s = -1, page = -1, id = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + i;
+            if (r >= total.x) break;
+            if (s < 0) s = plan_find(row_end, S, r);
+            while (row_end[s] <= r) ++s, page = -1;
+            if (!got[s]) continue;
+            const int pos = lens[s] + r - (s ? row_end[s - 1] : 0), p = pos >> a.shift;
+            if (p != page) {
+                page = p;
+                id = p < had[s] ? c.table[(size_t)s * c.max_pages + p] : taken(take_end[s] - (want[s] - had[s]) + p - had[s]);
             }
+            if (id >= 0 && id < N) slot[i] = (id << a.shift) + (pos & (P - 1));
+            else worse = kPgArg;
         }
-        a.slots[r] = slot;
+        if (r0 + 4 <= a.rows && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0)
+            *reinterpret_cast<int4 *>(a.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        else
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r0 + i < a.rows) a.slots[r0 + i] = slot[i];
     }
     for (int i = me; i < used; i += G) {
         const int s = plan_find(take_end, S, i);
@@ -144,8 +164,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
     __syncthreads();
     if (t == 0) {
         if (s_bits) atomicOr(c.err, s_bits);
-        __threadfence();
-        s_last = atomicInc(reinterpret_cast<unsigned *>(c.queue + 2), gridDim.x - 1) == gridDim.x - 1;
+        s_last = 1;
+        if (gridDim.x > 1) {
+            __threadfence();
+            s_last = atomicInc(reinterpret_cast<unsigned *>(c.queue + 2), gridDim.x - 1) == gridDim.x - 1;
+        }
     }
     __syncthreads();
     if (!s_last || !sound) return;
@@ -155,6 +178,21 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
         c.queue[0] = int(((long long)first + used) % N);
         c.queue[1] = have - used;
     }
+}
+
+template <int EACH>
+int launch_plan(const PlanArgs &a, cudaStream_t s) {
+    const int dev = current_device();
+    if (dev < 0) return DFL_E_CUDA;
+    const size_t smem = (size_t)7 * 4 * a.c.n_seq;
+    static bool done[kMaxDevices] = {};
+    if (!done[dev]) {
+        if (cudaFuncSetAttribute(k_paged_plan<EACH>, cudaFuncAttributeMaxDynamicSharedMemorySize, 7 * 4 * DFL_PAGED_MAX_SEQ) != cudaSuccess)
+            return DFL_E_CUDA;
+        done[dev] = true;
+    }
+    const int ctas = std::min(std::max((a.rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads), std::max(1, std::min(16, a.c.n_pages / 16384))), 304);
+    return pg_launched(launch_pdl(k_paged_plan<EACH>, dim3(ctas), dim3(kPlanThreads), smem, s, a));
 }
 
 __global__ void k_paged_init(dfl_paged c) {
@@ -181,6 +219,7 @@ __global__ void __launch_bounds__(256) k_paged_append(AppendArgs a) {
     const dfl_paged &c = a.c;
     const int hc = c.head_dim / 8, chunks = c.n_kv * hc;       // 16-byte pieces of a head, of a row
     pdl_wait();
+    pdl_trigger();
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     const int r = int(i / chunks), at = int(i % chunks), h = at / hc, x = at % hc;
     if (r >= a.rows) return;
@@ -233,17 +272,11 @@ int dfl_paged_plan(const dfl_paged *c, const int32_t *len, const int32_t *cnt, i
     const void *p[] = {len, cnt, cu, slots};
     for (const void *q : p)
         if (!pg_aligned(q, 4)) return DFL_E_INVALID_ARG;
-    const int dev = current_device();
-    if (dev < 0) return DFL_E_CUDA;
-    static bool done[kMaxDevices] = {};
-    if (!done[dev]) {
-        if (cudaFuncSetAttribute(k_paged_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, 6 * 4 * DFL_PAGED_MAX_SEQ) != cudaSuccess)
-            return DFL_E_CUDA;
-        done[dev] = true;
-    }
-    const int ctas = std::min(std::max({1, (rows + 2047) / 2048, std::min(16, c->n_pages / 4096)}), 152);
-    const PlanArgs a{*c, len, cnt, cu, slots, rows};
-    return pg_launched(launch_pdl(k_paged_plan, dim3(ctas), dim3(kPlanThreads), (size_t)6 * 4 * c->n_seq, static_cast<cudaStream_t>(stream), a));
+    int shift = 4;
+    while (1 << shift < c->page) ++shift;
+    const PlanArgs a{*c, len, cnt, cu, slots, rows, shift};
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return c->n_seq <= kPlanThreads ? launch_plan<1>(a, s) : launch_plan<kPlanEach>(a, s);
 }
 
 int dfl_paged_append(const dfl_paged *c, const int32_t *slots, int rows, const void *k, int64_t ldk, const void *v, int64_t ldv,

@@ -6,12 +6,14 @@
 // where the cuts fall. A unit that a cut goes through leaves a part (sums, maximum, weight) for each CTA, and a
 // second launch adds the parts in their order.
 //
-// A CTA is four warps. A step is 16 keys, which lie in one page: the warps of a key group bring its keys and values
-// into a ring of their own (16-byte asynchronous copies, no other warp waits), the scores S = Q K^T and sums P V go
-// through mma.m16n8k16 with 16 query rows (a token's heads of one group beside each other) as the rows, and the
-// group keeps a softmax of its own over its steps; groups are joined when the CTA is done with the unit. mma.sync
-// and not tcgen05: with 16 rows a tile the products are a fifth of what even these units can do while the keys
-// arrive, and each warp goes at its own pace.
+// A CTA is four warps with a ring of tiles of 64 keys (32 of 256 channels), brought in by 16-byte asynchronous
+// copies. Each warp brings its quarter of a tile's keys, takes their scores S = Q K^T (mma.m16n8k16, a token's heads
+// of one group beside each other as the rows) as soon as they are there, and puts its weights P into shared memory;
+// after the tile's one barrier each warp adds P V for a quarter of the channels. So no score or sum is computed
+// twice, and at the end of a unit nothing but the weights' sums has to be joined. Weights are relative to a maximum
+// that all warps hold, renewed only when one of them meets a score that passes it by more than 8 powers of two (the
+// barrier says so, and the tile's weights are taken again). mma.sync and not tcgen05: with 16 rows a tile the
+// products are a small part of what even these units do while the keys arrive.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -21,10 +23,11 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kGranule = 64;                    // keys of a granule
-constexpr int kStep = 16;                       // keys of a step
-constexpr int kLeast = 4;                       // granules of a CTA at least
+constexpr int kStep = 16;                       // a unit's keys begin at a multiple of it: a page at least
+constexpr int kLeast = 1;                       // granules of a CTA at least
+constexpr int kSolo = 96 * 1024;                // units of so many bytes at most need no cut
 constexpr int kMaxCtas = 304;                   // two an SM
-constexpr int kBudget = 108 * 1024;             // shared memory of a CTA's queries and rings
+constexpr int kBudget = 112 * 1024;             // shared memory of a CTA, two an SM
 constexpr int kMergeThreads = 256;
 
 struct AttnWork {
@@ -32,20 +35,20 @@ struct AttnWork {
     int chunks;                                 // of query rows
     int *pre;                                   // [n_seq + 1] granules before each sequence's, of one unit each; then the CTAs in use
     float *ml, *o;                              // parts: [CTA][2][rows][2], [CTA][2][rows][HD]
-    int ways;                                   // merge: warps that share a row
+    int solo;                                   // a CTA has one unit and no cut is made
 };
 
-// MT tiles of 16 rows a warp, MW warps beside each other along the rows, CW along the channels of the values
-template <int HD, int MT_, int MW_>
+// MT tiles of 16 query rows
+template <int HD, int MT_>
 struct Shape {
-    static constexpr int MT = MT_, MW = MW_, CW = HD == 256 ? 2 : 1;
-    static constexpr int GW = MW * CW, KW = kWarps / GW;      // warps of a key group, key groups
-    static constexpr int kRows = 16 * MT * MW;
-    static constexpr int kQ = kRows * HD * 2;
-    static constexpr int kStage = kStep * HD * 2 * 2;
-    static constexpr int kStages = (kBudget - kQ) / (KW * kStage);
-    static constexpr int kRing = KW * kStages * kStage;
-    static_assert(KW >= 1 && kStages >= 2 && KW * kRows * HD * 4 <= kRing, "");
+    static constexpr int MT = MT_, kKeys = HD == 256 ? 32 : 64;   // keys of a tile
+    static constexpr int kMine = kKeys / kWarps;                  // of a warp
+    static constexpr int kRows = 16 * MT;
+    static constexpr int kQ = kRows * HD * 2, kP = kRows * kKeys * 2;
+    static constexpr int kTile = kKeys * HD * 2 * 2;
+    static constexpr int kStages = (kBudget - kQ - 2 * kP) / kTile;
+    static constexpr int kBytes = kQ + 2 * kP + kStages * kTile;
+    static_assert(kStages >= 2 && kGranule % kKeys == 0 && kStep % kMine == 0, "");
 };
 
 template <typename T>
@@ -80,10 +83,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // What a sequence brings to a call
 struct SeqWork {
-    int n, len, seen, lo, hi, granules;         // rows, tokens before them, keys that some row sees: seen .. hi - 1; lo: seen rounded down to a step
+    int n, row0, len, seen, lo, hi, granules;   // rows, the first of them, tokens before them, keys that some row sees: seen .. hi - 1; lo: seen rounded down to a step
 };
 __device__ SeqWork seq_work(const PagedAttnArgs &a, int s, int *bits) {
-    SeqWork w{0, 0, 0, 0, 0, 0};
+    SeqWork w{0, 0, 0, 0, 0, 0, 0};
     const int r0 = a.cu[s], r1 = a.cu[s + 1], len = a.len[s], held = a.c.held[s];
     if (r0 < 0 || r1 < r0 || r1 > a.total || len < 0 || r1 - r0 > a.rows) {
         *bits |= kPgArg;
@@ -96,6 +99,7 @@ __device__ SeqWork seq_work(const PagedAttnArgs &a, int s, int *bits) {
         return w;
     }
     w.n = n;
+    w.row0 = r0;
     w.len = len;
     w.hi = len + n;
     w.seen = !a.window ? 0 : max(0, a.causal ? len - a.window + 1 : len - a.window);
@@ -125,33 +129,36 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t x) {
     return ((x & e) == e ? 0xFFFFu : 0u) | ((x >> 16 & e) == e ? 0xFFFF0000u : 0u);
 }
 
-template <typename T, int HD, int MT, int MW>
+template <typename T, int HD, int MT>
 __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
-    using Sh = Shape<HD, MT, MW>;
-    constexpr int KW = Sh::KW, GW = Sh::GW, CW = Sh::CW, kStages = Sh::kStages, kRows = Sh::kRows;
+    using Sh = Shape<HD, MT>;
+    constexpr int kStages = Sh::kStages, kRows = Sh::kRows, kKeys = Sh::kKeys, kMine = Sh::kMine;
     constexpr int kCh = HD / 8;                                  // 16-byte pieces of a row
-    constexpr int kN = HD / CW / 8;                              // tiles of 8 channels of a warp's sums
-    constexpr float kShift = std::is_same<T, __nv_bfloat16>::value ? 0.f : 10.f;   // fp16 weights are held times 2^10: lost below 2^-35
+    constexpr int kNt = kMine / 8;                               // tiles of 8 keys of a warp's scores
+    constexpr int kN = HD / kWarps / 8;                          // tiles of 8 channels of a warp's sums
+    constexpr float kShift = std::is_same<T, __nv_bfloat16>::value ? 0.f : 6.f;   // fp16 weights are held times 2^6: lost below 2^-31
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_sum[kWarps];
-    __shared__ float s_ml[KW][kRows][2];
+    __shared__ float s_row[kWarps][kRows];                       // maxima, and at the end the weights' sums
     const PagedAttnArgs &a = w.a;
     const dfl_paged &c = a.c;
-    uint8_t *qs = smem, *ring0 = smem + Sh::kQ;
-    int *pre = reinterpret_cast<int *>(smem + Sh::kQ + Sh::kRing);
+    uint8_t *qs = smem, *ps = qs + Sh::kQ, *ring = ps + 2 * Sh::kP;
+    int *pre = reinterpret_cast<int *>(smem + Sh::kBytes);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = a.group, S = c.n_seq;
-    const int kg = warp / GW, mw = warp % GW / CW, cw = warp % CW;
+    const unsigned q_at = saddr(qs), p_at = saddr(ps), ring_at = saddr(ring);
     pdl_wait();
+    pdl_trigger();
 
     // ---- granules before each sequence's, of one unit a sequence ----
-    int bits = 0;
-    {
-        int *mine = pre;
+    const int units = c.n_kv * w.chunks;
+    long long all = 0, x = 0, end = 1;
+    if (!w.solo) {
+        int bits = 0;
         const int each = (S + kThreads - 1) / kThreads, s0 = min(t * each, S), s1 = min(s0 + each, S);
         int sum = 0;
         for (int s = s0; s < s1; ++s) {
             const int n = seq_work(a, s, &bits).granules;
-            mine[s + 1] = n;
+            pre[s + 1] = n;
             sum += n;
         }
         int upto = sum;
@@ -164,76 +171,77 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
         __syncthreads();
         int at = upto - sum;
         for (int i = 0; i < warp; ++i) at += s_sum[i];
-        for (int s = s0; s < s1; ++s) mine[s + 1] = at += mine[s + 1];
-        if (t == 0) mine[0] = 0;
+        for (int s = s0; s < s1; ++s) pre[s + 1] = at += pre[s + 1];
+        if (t == 0) pre[0] = 0;
         __syncthreads();
+        all = (long long)pre[S] * units;
+        const int ctas = int(min((long long)gridDim.x, max(1ll, (all + kLeast - 1) / kLeast)));
+        if (blockIdx.x == 0) {
+            pg_report(c.err, bits);
+            for (int s = t; s <= S; s += kThreads) w.pre[s] = pre[s];
+            if (t == 0) w.pre[S + 1] = ctas;
+        }
+        if (int(blockIdx.x) >= ctas) return;
+        x = cut(all, blockIdx.x, ctas);
+        end = cut(all, blockIdx.x + 1, ctas);
     }
-    const int units = c.n_kv * w.chunks;
-    const long long all = (long long)pre[S] * units;
-    const int ctas = int(min((long long)gridDim.x, max(1ll, (all + kLeast - 1) / kLeast)));
-    if (blockIdx.x == 0) {
-        pg_report(c.err, bits);
-        for (int s = t; s <= S; s += kThreads) w.pre[s] = pre[s];
-        if (t == 0) w.pre[S + 1] = ctas;
-    }
-    if (int(blockIdx.x) >= ctas) return;
-    long long x = cut(all, blockIdx.x, ctas);
-    const long long end = cut(all, blockIdx.x + 1, ctas);
 
     for (int slot = 0; x < end;) {
         // ---- the piece: granules g0 .. g1 - 1 of a unit ----
-        int s = 0;
-        for (int hi = S - 1; s < hi;) {                          // the last sequence that begins at or before x, of those with granules
-            const int mid = (s + hi) >> 1;
-            if ((long long)pre[mid + 1] * units > x) hi = mid;
-            else s = mid + 1;
+        int s = 0, u, g0 = 0, g1, bits = 0;
+        SeqWork sw;
+        if (w.solo) {
+            s = blockIdx.x / units, u = blockIdx.x % units;
+            sw = seq_work(a, s, &bits);
+            g1 = sw.granules;
+            if (u == 0 && t == 0) pg_report(c.err, bits);
+            x = end;
+        } else {
+            for (int hi = S - 1; s < hi;) {                      // the last sequence that begins at or before x, of those with granules
+                const int mid = (s + hi) >> 1;
+                if ((long long)pre[mid + 1] * units > x) hi = mid;
+                else s = mid + 1;
+            }
+            sw = seq_work(a, s, &bits);
+            const long long at = x - (long long)pre[s] * units;
+            u = int(at / sw.granules), g0 = int(at % sw.granules), g1 = int(min((long long)sw.granules, g0 + (end - x)));
+            x += g1 - g0;
         }
-        int none = 0;
-        const SeqWork sw = seq_work(a, s, &none);
-        const long long at = x - (long long)pre[s] * units;
-        const int u = int(at / sw.granules), g0 = int(at % sw.granules), g1 = int(min((long long)sw.granules, g0 + (end - x)));
         const int h = u / w.chunks, first = u % w.chunks * kRows, live = min(kRows, sw.n * g - first);
-        x += g1 - g0;
         const bool whole = g0 == 0 && g1 == sw.granules;
         const int part = slot;
         slot = 1;                                                // a CTA's first piece, or the one that its cut ends in
         if (live <= 0) continue;
-        const int row0 = a.cu[s];
+        const int row0 = sw.row0;
         const int base = sw.lo + g0 * kGranule, stop = min(sw.hi, sw.lo + g1 * kGranule);
-        const int steps = (stop - base + kStep - 1) / kStep, mine = (steps - kg + KW - 1) / KW;
+        const int tiles = (stop - base + kKeys - 1) / kKeys;
         const int32_t *table = c.table + (size_t)s * c.max_pages;
-        uint8_t *ring = ring0 + kg * kStages * Sh::kStage;
-        const unsigned ring_at = saddr(ring);
 
-        // the pages of the group's next 32 steps, a step a lane; asked for 32 steps ahead
+        // the pages of the warp's keys in the next 32 tiles, a tile a lane; asked for 32 tiles ahead
         const auto pages = [&](int i) {
-            const int key = base + kStep * (kg + KW * (i + lane));
+            const int key = base + kKeys * (i + lane) + kMine * warp;
             return key < stop ? table[key / c.page] : 0;
         };
         int page_now = pages(0), page_next = pages(32);
-        const auto fetch = [&](int i) {                          // step i of the group into its stage
-            if (i < mine) {
+        const auto fetch = [&](int i) {                          // the warp's keys of tile i into its stage
+            if (i < tiles) {
                 if (i && i % 32 == 0) page_now = page_next, page_next = pages(i + 32);
-                const int id = __shfl_sync(0xffffffffu, page_now, i % 32), key0 = base + kStep * (kg + KW * i);
+                const int id = __shfl_sync(0xffffffffu, page_now, i % 32), key0 = base + kKeys * i + kMine * warp;
                 const bool ok = id >= 0 && id < c.n_pages;
                 const size_t from = (((size_t)(ok ? id : 0) * c.n_kv + h) * c.page + key0 % c.page) * HD;
-                const unsigned to = ring_at + i % kStages * Sh::kStage;
+                const unsigned to = ring_at + i % kStages * Sh::kTile + kMine * warp * HD * 2;
 #pragma unroll
-                for (int y = 0; y < 2 * kStep * kCh / 32 / GW; ++y) {
-                    const int p = (y * GW + warp % GW) * 32 + lane, kv = p / (kStep * kCh), key = p / kCh % kStep, ch = p % kCh;
-                    const unsigned dst = to + kv * (kStep * HD * 2) + key * HD * 2 + ((ch ^ (key & 7)) << 4);
+                for (int y = 0; y < 2 * kMine * kCh / 32; ++y) {
+                    const int p = y * 32 + lane, kv = p / (kMine * kCh), key = p / kCh % kMine, ch = p % kCh;
+                    const unsigned dst = to + kv * (kKeys * HD * 2) + key * HD * 2 + ((ch ^ (key & 7)) << 4);
                     const T *src = static_cast<const T *>(kv ? c.v : c.k) + from + key * HD + ch * 8;
                     if (ok || kv) cp16(dst, src, ok && key0 + key < stop && key0 + key >= sw.seen);
                     else                                         // a page that is none: keys that make NaN of what sees them
                         asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0x7FFF7FFFu) : "memory");
                 }
-                if (!ok && lane == 0) pg_report(c.err, kPgArg);
+                if (!ok && key0 < stop && lane == 0) pg_report(c.err, kPgArg);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        const auto group_sync = [&] {
-            if constexpr (GW == 1) __syncwarp();
-            else asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * GW) : "memory");
         };
         __syncthreads();                                         // the memory of the piece before is free
 #pragma unroll
@@ -246,21 +254,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
             *reinterpret_cast<uint4 *>(qs + r * HD * 2 + ((ch ^ (r & 7)) << 4)) = v;
         }
         __syncthreads();
-        const auto q_at = [&](int mt, int ks) {                  // a lane's row address of a 16 x 16 tile of queries
-            const int r = (mw * MT + mt) * 16 + lane % 16, ch = 2 * ks + lane / 16;
-            return saddr(qs) + r * HD * 2 + ((ch ^ (r & 7)) << 4);
+        const auto q_tile = [&](int mt, int ks) {                // a lane's row address of a 16 x 16 tile of queries
+            const int r = mt * 16 + lane % 16, ch = 2 * ks + lane / 16;
+            return q_at + r * HD * 2 + ((ch ^ (r & 7)) << 4);
         };
         uint32_t qf[MT == 1 ? HD / 16 : 1][4];
         if constexpr (MT == 1)
 #pragma unroll
-            for (int ks = 0; ks < HD / 16; ++ks) ldsm4(qf[ks], q_at(0, ks));
+            for (int ks = 0; ks < HD / 16; ++ks) ldsm4(qf[ks], q_tile(0, ks));
         // what each of the lane's rows sees: keys lo .. hi - 1, counted from base
         int lo[MT][2], hi[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int p = first + min((mw * MT + mt) * 16 + lane / 4 + 8 * b, live - 1), pos = sw.len + p / g;
+                const int p = first + min(mt * 16 + lane / 4 + 8 * b, live - 1), pos = sw.len + p / g;
                 hi[mt][b] = (a.causal ? pos + 1 : sw.hi) - base;
                 lo[mt][b] = (!a.window ? 0 : max(0, a.causal ? pos - a.window + 1 : sw.len - a.window)) - base;
             }
@@ -277,109 +285,164 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
 #pragma unroll
             for (int i = 0; i < kN; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.f;
         }
-        for (int i = 0; i < mine; ++i) {
+        for (int i = 0; i < tiles; ++i) {
             cp_wait<kStages - 2>();
-            group_sync();
-            fetch(i + kStages - 1);
-            const unsigned kt = ring_at + i % kStages * Sh::kStage, vt = kt + kStep * HD * 2;
-            const int k0 = kStep * (kg + KW * i);
-            // S: rows x 16 keys
-            float sc[MT][2][4];
+            __syncwarp();
+            const unsigned kt = ring_at + i % kStages * Sh::kTile, vt = kt + kKeys * HD * 2;
+            const int k0 = kKeys * i, mine = k0 + kMine * warp;  // the tile's first key, the warp's
+            // S: rows x the warp's keys. One tile of rows: even and odd steps in sums of their own, so that fewer wait for each other
+            constexpr int kChains = MT == 1 ? 2 : 1;
+            float sc[MT][kNt][4];
+            {
+                float part[kChains][MT][kNt][4] = {};
+                if constexpr (kNt == 2) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+                    for (int ks = 0; ks < HD / 16; ++ks) {
+                        uint32_t kf[4];                          // keys 0-7: channels 0-7, 8-15; keys 8-15: the same
+                        const int key = kMine * warp + (lane / 16) * 8 + lane % 8, ch = 2 * ks + lane / 8 % 2;
+                        ldsm4(kf, kt + key * HD * 2 + ((ch ^ (key & 7)) << 4));
 #pragma unroll
-                for (int b = 0; b < 2; ++b) sc[mt][b][0] = sc[mt][b][1] = sc[mt][b][2] = sc[mt][b][3] = 0.f;
+                        for (int mt = 0; mt < MT; ++mt) {
+                            uint32_t q[4];
+                            if constexpr (MT > 1) ldsm4(q, q_tile(mt, ks));
+                            mma16<T>(part[ks % kChains][mt][0], MT == 1 ? qf[ks % (HD / 16)] : q, kf[0], kf[1]);
+                            mma16<T>(part[ks % kChains][mt][1], MT == 1 ? qf[ks % (HD / 16)] : q, kf[2], kf[3]);
+                        }
+                    }
+                } else {
 #pragma unroll
-            for (int ks = 0; ks < HD / 16; ++ks) {
-                uint32_t kf[4];                                  // keys 0-7: channels 0-7, 8-15; keys 8-15: the same
-                const int key = (lane / 16) * 8 + lane % 8, ch = 2 * ks + lane / 8 % 2;
-                ldsm4(kf, kt + key * HD * 2 + ((ch ^ (key & 7)) << 4));
+                    for (int ks = 0; ks < HD / 16; ks += 2) {
+                        uint32_t kf[4];                          // 8 keys: channels 0-7, 8-15, 16-23, 24-31
+                        const int key = kMine * warp + lane % 8, ch = 2 * ks + lane / 8;
+                        ldsm4(kf, kt + key * HD * 2 + ((ch ^ (key & 7)) << 4));
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    if constexpr (MT == 1) {
-                        mma16<T>(sc[0][0], qf[ks], kf[0], kf[1]);
-                        mma16<T>(sc[0][1], qf[ks], kf[2], kf[3]);
-                    } else {
-                        uint32_t q[4];
-                        ldsm4(q, q_at(mt, ks));
-                        mma16<T>(sc[mt][0], q, kf[0], kf[1]);
-                        mma16<T>(sc[mt][1], q, kf[2], kf[3]);
+                        for (int z = 0; z < 2; ++z)
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                uint32_t q[4];
+                                if constexpr (MT > 1) ldsm4(q, q_tile(mt, ks + z));
+                                mma16<T>(part[z % kChains][mt][0], MT == 1 ? qf[(ks + z) % (HD / 16)] : q, kf[2 * z], kf[2 * z + 1]);
+                            }
                     }
                 }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int b = 0; b < kNt; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[mt][b][e] = kChains == 2 ? part[0][mt][b][e] + part[kChains - 1][mt][b][e] : part[0][mt][b][e];
             }
-            const bool masked = k0 < all_lo || k0 + kStep > all_hi;
+            const bool masked = k0 < all_lo || k0 + kKeys > all_hi;
             if (masked)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
+                    for (int b = 0; b < kNt; ++b)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int key = k0 + 8 * b + 2 * (lane % 4) + (e & 1);
+                            const int key = mine + 8 * b + 2 * (lane % 4) + (e & 1);
                             if (key < lo[mt][e >> 1] || key >= hi[mt][e >> 1]) sc[mt][b][e] = -INFINITY;
                         }
-            uint32_t pf[MT][4];
+            float most[MT][2], add[MT][2];
+            bool renew = false;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                float next[2];
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    float m = fmaxf(fmaxf(sc[mt][0][2 * b], sc[mt][0][2 * b + 1]), fmaxf(sc[mt][1][2 * b], sc[mt][1][2 * b + 1]));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                    next[b] = fmaxf(m, top[mt][b]);
+                    float m = fmaxf(sc[mt][0][2 * b], sc[mt][0][2 * b + 1]);
+                    if constexpr (kNt == 2) m = fmaxf(m, fmaxf(sc[mt][1][2 * b], sc[mt][1][2 * b + 1]));
+                    most[mt][b] = m;
+                    renew |= (m - top[mt][b]) * a.scale_log2 > 8.f;
                 }
-                if (__any_sync(0xffffffffu, next[0] > top[mt][0] || next[1] > top[mt][1])) {
+            const auto weigh = [&] {                             // the tile's weights into shared memory
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const float keep = next[b] > top[mt][b] ? exp2_fast((top[mt][b] - next[b]) * a.scale_log2) : 1.f;
-                        top[mt][b] = next[b];
-                        sum[mt][b] *= keep;
+                        const float off = top[mt][b] == -INFINITY ? 0.f : kShift - top[mt][b] * a.scale_log2;
+                        add[mt][b] = 0.f;
+                        const int r = mt * 16 + lane / 4 + 8 * b;
 #pragma unroll
-                        for (int y = 0; y < kN; ++y) o[mt][y][2 * b] *= keep, o[mt][y][2 * b + 1] *= keep;
+                        for (int y = 0; y < kNt; ++y) {
+                            const float e0 = exp2_fast(fmaf(sc[mt][y][2 * b], a.scale_log2, off)), e1 = exp2_fast(fmaf(sc[mt][y][2 * b + 1], a.scale_log2, off));
+                            add[mt][b] += e0 + e1;
+                            const int ch = warp * kNt + y;
+                            *reinterpret_cast<uint32_t *>(ps + (i & 1) * Sh::kP + r * kKeys * 2 + ((ch ^ (kKeys == 64 ? r & 7 : r >> 1 & 3)) << 4) + 4 * (lane % 4)) =
+                                pack2<T>(e0, e1);
+                        }
                     }
-                }
+            };
+            weigh();
+            if (__syncthreads_or(renew)) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float off = top[mt][b] == -INFINITY ? 0.f : kShift - top[mt][b] * a.scale_log2;
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float e0 = exp2_fast(fmaf(sc[mt][y][2 * b], a.scale_log2, off)), e1 = exp2_fast(fmaf(sc[mt][y][2 * b + 1], a.scale_log2, off));
-                        sum[mt][b] += e0 + e1;
-                        pf[mt][2 * y + b] = pack2<T>(e0, e1);
+                    for (int b = 0; b < 2; ++b) {
+                        float m = most[mt][b];
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                        if (lane % 4 == 0) s_row[warp][mt * 16 + lane / 4 + 8 * b] = m;
                     }
-                }
+                __syncthreads();
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int r = mt * 16 + lane / 4 + 8 * b;
+                        const float m = fmaxf(fmaxf(s_row[0][r], s_row[1][r]), fmaxf(s_row[2][r], s_row[3][r]));
+                        if (m > top[mt][b]) {
+                            const float keep = exp2_fast((top[mt][b] - m) * a.scale_log2);
+                            top[mt][b] = m;
+                            sum[mt][b] *= keep;
+#pragma unroll
+                            for (int y = 0; y < kN; ++y) o[mt][y][2 * b] *= keep, o[mt][y][2 * b + 1] *= keep;
+                        }
+                    }
+                weigh();
+                __syncthreads();
             }
-            // O += P V. Where a row does not see all keys of the step, a value that is not finite counts for none in the product,
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) sum[mt][0] += add[mt][0], sum[mt][1] += add[mt][1];
+            fetch(i + kStages - 1);                              // where tile i - 1 was: all warps are past its products
+            // O += P V. Where a row does not see all keys of the tile, a value that is not finite counts for none in the product,
             // and makes NaN of the sums of the rows that see it
             const bool mixed = masked && differ;
             uint32_t odd = 0;
 #pragma unroll
-            for (int y = 0; y < kN / 2; ++y) {
-                uint32_t vf[4];                                  // channels 0-7: keys 0-7, 8-15; channels 8-15: the same
-                const int key = lane % 16, ch = cw * kN + 2 * y + lane / 16;
-                ldsm4t(vf, vt + key * HD * 2 + ((ch ^ (key & 7)) << 4));
-                if (mixed)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const uint32_t m = odd_halves<T>(vf[z]);
-                        odd |= m;
-                        vf[z] &= ~m;
-                    }
+            for (int ks = 0; ks < kKeys / 16; ++ks) {
+                uint32_t pf[MT][4];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    mma16<T>(o[mt][2 * y], pf[mt], vf[0], vf[1]);
-                    mma16<T>(o[mt][2 * y + 1], pf[mt], vf[2], vf[3]);
+                    const int r = mt * 16 + lane % 16, ch = 2 * ks + lane / 16;
+                    ldsm4(pf[mt], p_at + (i & 1) * Sh::kP + r * kKeys * 2 + ((ch ^ (kKeys == 64 ? r & 7 : r >> 1 & 3)) << 4));
+                }
+#pragma unroll
+                for (int y = 0; y < kN / 2; ++y) {
+                    uint32_t vf[4];                              // channels 0-7: keys 0-7, 8-15; channels 8-15: the same
+                    const int key = 16 * ks + lane % 16, ch = warp * kN + 2 * y + lane / 16;
+                    ldsm4t(vf, vt + key * HD * 2 + ((ch ^ (key & 7)) << 4));
+                    if (mixed)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const uint32_t m = odd_halves<T>(vf[z]);
+                            odd |= m;
+                            vf[z] &= ~m;
+                        }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma16<T>(o[mt][2 * y], pf[mt], vf[0], vf[1]);
+                        mma16<T>(o[mt][2 * y + 1], pf[mt], vf[2], vf[3]);
+                    }
                 }
             }
             if (mixed && __any_sync(0xffffffffu, odd)) {
-                const uint16_t *v = reinterpret_cast<const uint16_t *>(ring + i % kStages * Sh::kStage + kStep * HD * 2);
-                for (int key = 0; key < kStep; ++key)
+                const uint16_t *v = reinterpret_cast<const uint16_t *>(ring + i % kStages * Sh::kTile + kKeys * HD * 2);
+                for (int key = 0; key < kKeys; ++key)
 #pragma unroll
                     for (int y = 0; y < kN; ++y)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int ch = cw * kN + y, x16 = 2 * (lane % 4) + e;
+                            const int ch = warp * kN + y, x16 = 2 * (lane % 4) + e;
                             if (odd_halves<T>(v[key * HD + ((ch ^ (key & 7)) << 3) + x16]) & 0xFFFFu)
 #pragma unroll
                                 for (int mt = 0; mt < MT; ++mt)
@@ -390,132 +453,111 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
             }
         }
         cp_wait<0>();
+        // ---- the weights' sums joined; out, or into the parts ----
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 sum[mt][b] += __shfl_xor_sync(0xffffffffu, sum[mt][b], 1);
                 sum[mt][b] += __shfl_xor_sync(0xffffffffu, sum[mt][b], 2);
+                if (lane % 4 == 0) s_row[warp][mt * 16 + lane / 4 + 8 * b] = sum[mt][b];
             }
-        // ---- the groups' sums through shared memory, then out or into the parts ----
         __syncthreads();
-        float *all_o = reinterpret_cast<float *>(ring0);         // [group][row][HD], 8 channels of a row turned by its number
+        const size_t slot_at = (size_t)blockIdx.x * 2 + part;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int r = (mw * MT + mt) * 16 + lane / 4 + 8 * b;
+                const int r = mt * 16 + lane / 4 + 8 * b;
                 if (r >= live) continue;
-                float *to = all_o + ((size_t)kg * kRows + r) * HD;
+                const float l = (s_row[0][r] + s_row[1][r]) + (s_row[2][r] + s_row[3][r]);
+                if (whole) {
+                    const float d = 1.f / l;
+                    const int p = first + r;
+                    T *to = static_cast<T *>(a.out) + (int64_t)(row0 + p / g) * a.ldo + (h * g + p % g) * HD + warp * kN * 8 + 2 * (lane % 4);
 #pragma unroll
-                for (int y = 0; y < kN; ++y)
-                    *reinterpret_cast<float2 *>(to + (((cw * kN + y) ^ (r & 3)) << 3) + 2 * (lane % 4)) = make_float2(o[mt][y][2 * b], o[mt][y][2 * b + 1]);
-                if (cw == 0 && lane % 4 == 0) s_ml[kg][r][0] = top[mt][b], s_ml[kg][r][1] = sum[mt][b];
-            }
-        __syncthreads();
-        float *part_o = w.o + ((size_t)blockIdx.x * 2 + part) * kRows * HD, *part_ml = w.ml + ((size_t)blockIdx.x * 2 + part) * kRows * 2;
-        for (int i = t; i < live * kCh; i += kThreads) {
-            const int r = i / kCh, ch = i % kCh;
-            float m = -INFINITY, l = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    for (int y = 0; y < kN; ++y) *reinterpret_cast<uint32_t *>(to + 8 * y) = pack2<T>(o[mt][y][2 * b] * d, o[mt][y][2 * b + 1] * d);
+                } else {
+                    float *to = w.o + (slot_at * kRows + r) * HD + warp * kN * 8 + 2 * (lane % 4);
 #pragma unroll
-            for (int k = 0; k < KW; ++k) m = fmaxf(m, s_ml[k][r][0]);
-#pragma unroll
-            for (int k = 0; k < KW; ++k) {
-                const float mk = s_ml[k][r][0], f = mk == m ? 1.f : exp2_fast((mk - m) * a.scale_log2);
-                l = fmaf(s_ml[k][r][1], f, l);
-                const float4 *from = reinterpret_cast<const float4 *>(all_o + ((size_t)k * kRows + r) * HD + ((ch ^ (r & 3)) << 3));
-                const float4 p = from[0], q = from[1];
-                v[0] = fmaf(p.x, f, v[0]), v[1] = fmaf(p.y, f, v[1]), v[2] = fmaf(p.z, f, v[2]), v[3] = fmaf(p.w, f, v[3]);
-                v[4] = fmaf(q.x, f, v[4]), v[5] = fmaf(q.y, f, v[5]), v[6] = fmaf(q.z, f, v[6]), v[7] = fmaf(q.w, f, v[7]);
-            }
-            if (whole) {
-                const float d = 1.f / l;
-                const int p = first + r;
-                T *to = static_cast<T *>(a.out) + (int64_t)(row0 + p / g) * a.ldo + (h * g + p % g) * HD + ch * 8;
-                *reinterpret_cast<uint4 *>(to) = make_uint4(pack2<T>(v[0] * d, v[1] * d), pack2<T>(v[2] * d, v[3] * d), pack2<T>(v[4] * d, v[5] * d),
-                                                            pack2<T>(v[6] * d, v[7] * d));
-            } else {
-                float4 *to = reinterpret_cast<float4 *>(part_o + (size_t)r * HD + ch * 8);
-                to[0] = make_float4(v[0], v[1], v[2], v[3]);
-                to[1] = make_float4(v[4], v[5], v[6], v[7]);
-                if (ch == 0) part_ml[2 * r] = m, part_ml[2 * r + 1] = l;
-            }
-        }
-    }
-}
-
-// The parts of units that cuts went through, added in the order of their CTAs. `ways` warps share a row.
-template <typename T, int HD>
-__global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const AttnWork w, int kRows) {
-    constexpr int kW = kMergeThreads / 32, kV = HD / 32;         // a lane's channels
-    __shared__ float s_o[kW][HD];
-    const PagedAttnArgs &a = w.a;
-    const dfl_paged &c = a.c;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = a.group, units = c.n_kv * w.chunks;
-    const int u = blockIdx.y, s = blockIdx.z, h = u / w.chunks, first = u % w.chunks * kRows;
-    pdl_wait();
-    const int begin = w.pre[s], granules = w.pre[s + 1] - begin;
-    if (!granules) return;
-    const int ctas = w.pre[c.n_seq + 1], row0 = a.cu[s], live = min(kRows, (a.cu[s + 1] - row0) * g - first);
-    const long long all = (long long)w.pre[c.n_seq] * units, from = (long long)begin * units + (long long)u * granules;
-    const int c0 = cta_at(from, all, ctas), c1 = cta_at(from + granules - 1, all, ctas), parts = c1 - c0 + 1;
-    if (parts == 1) return;
-    const int head = cut(all, c0, ctas) < from;                  // the first part is its CTA's second piece
-    const int share = w.ways, way = warp % share;
-    for (int r = blockIdx.x * (kW / share) + warp / share; r - warp / share < live; r += gridDim.x * (kW / share)) {
-        const bool mine = r < live;
-        const auto slot = [&](int p) { return (size_t)(c0 + p) * 2 + (p == 0 ? head : 0); };
-        float m = -INFINITY, l = 0.f, v[kV];
-#pragma unroll
-        for (int i = 0; i < kV; ++i) v[i] = 0.f;
-        if (mine) {
-            for (int p = lane; p < parts; p += 32) m = fmaxf(m, w.ml[(slot(p) * kRows + r) * 2]);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            for (int p = lane; p < parts; p += 32) {
-                const float2 ml = *reinterpret_cast<const float2 *>(w.ml + (slot(p) * kRows + r) * 2);
-                l = fmaf(ml.y, ml.x == m ? 1.f : exp2_fast((ml.x - m) * a.scale_log2), l);
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-#pragma unroll 4
-            for (int p = way; p < parts; p += share) {
-                const float mp = w.ml[(slot(p) * kRows + r) * 2], f = mp == m ? 1.f : exp2_fast((mp - m) * a.scale_log2);
-                const float *src = w.o + (slot(p) * kRows + r) * HD + lane * kV;
-#pragma unroll
-                for (int i = 0; i < kV; i += 2) {
-                    const float2 x = *reinterpret_cast<const float2 *>(src + i);
-                    v[i] = fmaf(x.x, f, v[i]), v[i + 1] = fmaf(x.y, f, v[i + 1]);
+                    for (int y = 0; y < kN; ++y) *reinterpret_cast<float2 *>(to + 8 * y) = make_float2(o[mt][y][2 * b], o[mt][y][2 * b + 1]);
+                    if (warp == 0 && lane % 4 == 0) *reinterpret_cast<float2 *>(w.ml + (slot_at * kRows + r) * 2) = make_float2(top[mt][b], l);
                 }
             }
-        }
-        if (share > 1) {
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kV; ++i) s_o[warp][lane * kV + i] = v[i];
-            __syncthreads();
-            if (way) continue;
-            for (int k = 1; k < share; ++k)
-#pragma unroll
-                for (int i = 0; i < kV; ++i) v[i] += s_o[warp + k][lane * kV + i];
-        }
-        if (!mine) continue;
-        const float d = 1.f / l;
-        const int p = first + r;
-        uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + (int64_t)(row0 + p / g) * a.ldo + (h * g + p % g) * HD + lane * kV);
-#pragma unroll
-        for (int i = 0; i < kV; i += 2) to[i / 2] = pack2<T>(v[i] * d, v[i + 1] * d);
     }
 }
 
-// Rows of a chunk: the fewest of 16, 32, 64 (and 128 below 256 channels, whose sums fit the registers) that hold all, or the most
-int chunk_rows(int hd, int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || hd == 256 ? 64 : 128; }
+// The parts of units that cuts went through, added in the order of their CTAs. A half warp takes 64 channels of a row, 16 bytes a
+// lane; SHARE half warps share them where rows are few and parts many, each every SHARE-th part.
+template <typename T, int HD, int SHARE>
+__global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const AttnWork w, int kRows) {
+    constexpr int kHalves = kMergeThreads / 16, kSlices = HD / 64;
+    __shared__ float s_o[SHARE > 1 ? SHARE : 1][64], s_ml[SHARE > 1 ? SHARE : 1][2];
+    const PagedAttnArgs &a = w.a;
+    const dfl_paged &c = a.c;
+    const int half = threadIdx.x >> 4, lane = threadIdx.x & 15, g = a.group, units = c.n_kv * w.chunks;
+    const int u = blockIdx.y, s = blockIdx.z, h = u / w.chunks, first = u % w.chunks * kRows;
+    const int id = blockIdx.x * (kHalves / SHARE) + half / SHARE, r = id / kSlices, ch = id % kSlices * 64 + 4 * lane;
+    pdl_wait();
+    const int begin = w.pre[s], granules = w.pre[s + 1] - begin, total = w.pre[c.n_seq], ctas = w.pre[c.n_seq + 1];
+    const int row0 = a.cu[s], live = min(kRows, (a.cu[s + 1] - row0) * g - first);
+    if (!granules || (SHARE > 1 && r >= live)) return;
+    const long long all = (long long)total * units, from = (long long)begin * units + (long long)u * granules;
+    const int c0 = cta_at(from, all, ctas), parts = cta_at(from + granules - 1, all, ctas) - c0 + 1;
+    if (parts == 1 || r >= live) return;
+    const int head = cut(all, c0, ctas) < from;                  // the first part is its CTA's second piece
+    float m = -INFINITY, l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int kBatch = 4;
+    for (int p0 = half % SHARE; p0 < parts; p0 += SHARE * kBatch) {
+        float2 ml[kBatch];
+        float4 o[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int p = min(p0 + i * SHARE, parts - 1);
+            const size_t at = ((size_t)(c0 + p) * 2 + (p == 0 ? head : 0)) * kRows + r;
+            ml[i] = *reinterpret_cast<const float2 *>(w.ml + at * 2);
+            o[i] = *reinterpret_cast<const float4 *>(w.o + at * HD + ch);
+            if (p0 + i * SHARE >= parts) ml[i] = make_float2(-INFINITY, 0.f), o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const float next = fmaxf(m, ml[i].x), keep = m == next ? 1.f : exp2_fast((m - next) * a.scale_log2);
+            const float f = ml[i].x == next ? 1.f : exp2_fast((ml[i].x - next) * a.scale_log2);
+            m = next;
+            l = l * keep + ml[i].y * f;
+            v[0] = v[0] * keep + o[i].x * f, v[1] = v[1] * keep + o[i].y * f, v[2] = v[2] * keep + o[i].z * f, v[3] = v[3] * keep + o[i].w * f;
+        }
+    }
+    if constexpr (SHARE > 1) {
+        *reinterpret_cast<float4 *>(&s_o[half][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+        if (lane == 0) s_ml[half][0] = m, s_ml[half][1] = l;
+        __syncthreads();
+        if (half) return;
+        m = -INFINITY, l = 0.f, v[0] = v[1] = v[2] = v[3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < SHARE; ++i) m = fmaxf(m, s_ml[i][0]);
+#pragma unroll
+        for (int i = 0; i < SHARE; ++i) {
+            const float f = s_ml[i][0] == m ? 1.f : exp2_fast((s_ml[i][0] - m) * a.scale_log2);
+            const float4 o = *reinterpret_cast<const float4 *>(&s_o[i][4 * lane]);
+            l = fmaf(s_ml[i][1], f, l);
+            v[0] = fmaf(o.x, f, v[0]), v[1] = fmaf(o.y, f, v[1]), v[2] = fmaf(o.z, f, v[2]), v[3] = fmaf(o.w, f, v[3]);
+        }
+    }
+    const float d = 1.f / l;
+    const int p = first + r;
+    *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + (int64_t)(row0 + p / g) * a.ldo + (h * g + p % g) * HD + ch) =
+        make_uint2(pack2<T>(v[0] * d, v[1] * d), pack2<T>(v[2] * d, v[3] * d));
+}
+
+// Rows of a chunk: the fewest of 16, 32 and 64 that hold all, or the most
+int chunk_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 struct Scratch {
     size_t pre, ml, o, total;
 };
 Scratch scratch_of(const dfl_paged *c, int n_q, int rows) {
-    const size_t r = (size_t)kMaxCtas * 2 * chunk_rows(c->head_dim, rows * (n_q / c->n_kv));
+    const size_t r = (size_t)kMaxCtas * 2 * chunk_rows(rows * (n_q / c->n_kv));
     Scratch s;
     s.pre = ((size_t)(c->n_seq + 2) * 4 + 255) / 256 * 256;
     s.ml = r * 2 * 4;
@@ -524,41 +566,37 @@ Scratch scratch_of(const dfl_paged *c, int n_q, int rows) {
     return s;
 }
 
-template <typename T, int HD, int MT, int MW>
+template <typename T, int HD, int MT>
 int launch_shape(const AttnWork &w, cudaStream_t st) {
-    using Sh = Shape<HD, MT, MW>;
+    using Sh = Shape<HD, MT>;
     const int dev = current_device();
     if (dev < 0) return DFL_E_CUDA;
     static int sms[kMaxDevices] = {};
     if (!sms[dev]) {
         int n = 0;
-        if (cudaFuncSetAttribute(k_paged_attn<T, HD, MT, MW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Sh::kQ + Sh::kRing + (DFL_PAGED_MAX_SEQ + 1) * 4) != cudaSuccess ||
+        if (cudaFuncSetAttribute(k_paged_attn<T, HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Sh::kBytes + (DFL_PAGED_MAX_SEQ + 1) * 4) != cudaSuccess ||
             cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return DFL_E_CUDA;
         sms[dev] = n;
     }
     const dfl_paged &c = w.a.c;
-    const int64_t most = (int64_t)c.n_seq * c.n_kv * w.chunks * (((int64_t)c.max_pages * c.page + kGranule - 1) / kGranule + 1);
-    const int ctas = int(std::min<int64_t>(std::min(2 * sms[dev], kMaxCtas), (most + kLeast - 1) / kLeast));
-    const cudaError_t e = launch_pdl(k_paged_attn<T, HD, MT, MW>, dim3(ctas), dim3(kThreads), Sh::kQ + Sh::kRing + (c.n_seq + 1) * 4, st, w);
-    if (e != cudaSuccess) return DFL_E_CUDA;
-    const int units = c.n_kv * w.chunks, rows = std::min(Sh::kRows, w.a.rows * w.a.group);
+    const int64_t granules = ((int64_t)c.max_pages * c.page + kGranule - 1) / kGranule + 1;   // of a unit at most
+    const int units = c.n_kv * w.chunks, rows = std::min(Sh::kRows, w.a.rows * w.a.group) * (HD / 64);
     AttnWork m = w;
-    m.ways = (int64_t)c.n_seq * units * rows >= 8 * sms[dev] ? 1 : kMergeThreads / 32;
-    const dim3 grid(m.ways > 1 ? rows : (rows + 7) / 8, units, c.n_seq);
-    return pg_launched(launch_pdl(k_paged_merge<T, HD>, grid, dim3(kMergeThreads), 0, st, m, int(Sh::kRows)));
+    m.solo = granules * kGranule * HD * 4 <= kSolo;
+    const int64_t ctas = m.solo ? (int64_t)c.n_seq * units : std::min<int64_t>(std::min(2 * sms[dev], kMaxCtas), (c.n_seq * units * granules + kLeast - 1) / kLeast);
+    const cudaError_t e = launch_pdl(k_paged_attn<T, HD, MT>, dim3(unsigned(ctas)), dim3(kThreads), Sh::kBytes + (m.solo ? 0 : (c.n_seq + 1) * 4), st, m);
+    if (e != cudaSuccess || m.solo) return pg_launched(e);
+    constexpr int kHalves = kMergeThreads / 16;
+    if ((int64_t)c.n_seq * units * rows < 8 * sms[dev])
+        return pg_launched(launch_pdl(k_paged_merge<T, HD, kHalves>, dim3(rows, units, c.n_seq), dim3(kMergeThreads), 0, st, m, int(Sh::kRows)));
+    return pg_launched(launch_pdl(k_paged_merge<T, HD, 1>, dim3((rows + kHalves - 1) / kHalves, units, c.n_seq), dim3(kMergeThreads), 0, st, m, int(Sh::kRows)));
 }
 
 template <typename T, int HD>
 int launch_rows(const AttnWork &w, int rows, cudaStream_t st) {
-    if constexpr (HD == 256)
-        return rows == 16 ? launch_shape<T, HD, 1, 1>(w, st) : rows == 32 ? launch_shape<T, HD, 1, 2>(w, st) : launch_shape<T, HD, 2, 2>(w, st);
-    else
-        return rows == 16   ? launch_shape<T, HD, 1, 1>(w, st)
-               : rows == 32 ? launch_shape<T, HD, 2, 1>(w, st)
-               : rows == 64 ? launch_shape<T, HD, 2, 2>(w, st)
-                            : launch_shape<T, HD, 2, 4>(w, st);
+    return rows == 16 ? launch_shape<T, HD, 1>(w, st) : rows == 32 ? launch_shape<T, HD, 2>(w, st) : launch_shape<T, HD, 4>(w, st);
 }
 
 template <typename T>
@@ -573,10 +611,10 @@ size_t paged_attn_scratch(const dfl_paged *c, int n_q, int rows) { return scratc
 
 int launch_paged_attn(const PagedAttnArgs &a, void *scratch, cudaStream_t st) {
     const Scratch s = scratch_of(&a.c, a.n_q, a.rows);
-    const int rows = chunk_rows(a.c.head_dim, a.rows * a.group);
+    const int rows = chunk_rows(a.rows * a.group);
     uint8_t *at = static_cast<uint8_t *>(scratch);
     const AttnWork w{a, (a.rows * a.group + rows - 1) / rows, reinterpret_cast<int *>(at), reinterpret_cast<float *>(at + s.pre),
-                     reinterpret_cast<float *>(at + s.pre + s.ml), 1};
+                     reinterpret_cast<float *>(at + s.pre + s.ml), 0};
     return a.c.type == DFL_BF16 ? launch_type<__nv_bfloat16>(w, rows, st) : launch_type<__half>(w, rows, st);
 }
 
