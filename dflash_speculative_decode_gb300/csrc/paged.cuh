@@ -37,6 +37,12 @@ inline int pg_check_heads(const dfl_paged *c, int n_q, int window, float scale) 
     return n_q / c->n_kv > kPgMaxGroup ? DFL_E_UNSUPPORTED : DFL_OK;
 }
 
+inline int pg_shift(const dfl_paged *c) {
+    int shift = 4;
+    while (1 << shift < c->page) ++shift;
+    return shift;
+}
+
 inline int pg_launched(cudaError_t e) { return e == cudaSuccess ? DFL_OK : DFL_E_CUDA; }
 
 __device__ __forceinline__ void pg_report(int *err, int bits) {
@@ -52,6 +58,7 @@ struct PagedAttnArgs {
     int n_q, group, total;     // rows of the packed buffers
     const int32_t *cu, *len;
     int rows, window, causal;
+    int shift;                 // page = 1 << shift
     float scale_log2;          // scale * log2(e): weights are powers of two
 };
 

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
         // the pages of the warp's keys in the next 32 tiles, a tile a lane; asked for 32 tiles ahead
         const auto pages = [&](int i) {
             const int key = base + kKeys * (i + lane) + kMine * warp;
-            return key < stop ? table[key / c.page] : 0;
+            return key < stop ? table[key >> a.shift] : 0;
         };
         int page_now = pages(0), page_next = pages(32);
         const auto fetch = [&](int i) {                          // the warp's keys of tile i into its stage
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
                 if (i && i % 32 == 0) page_now = page_next, page_next = pages(i + 32);
                 const int id = __shfl_sync(0xffffffffu, page_now, i % 32), key0 = base + kKeys * i + kMine * warp;
                 const bool ok = id >= 0 && id < c.n_pages;
-                const size_t from = (((size_t)(ok ? id : 0) * c.n_kv + h) * c.page + key0 % c.page) * HD;
+                const size_t from = ((((size_t)(ok ? id : 0) * c.n_kv + h) << a.shift) + (key0 & (c.page - 1))) * HD;
                 const unsigned to = ring_at + i % kStages * Sh::kTile + kMine * warp * HD * 2;
 #pragma unroll
                 for (int y = 0; y < 2 * kMine * kCh / 32; ++y) {
