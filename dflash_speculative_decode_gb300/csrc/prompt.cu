@@ -37,7 +37,8 @@ struct PromptShape {
     static constexpr int kStages = HD == 64 ? 8 : HD == 128 ? 5 : 7;
     static constexpr int kQBytes = HD == 256 ? 0 : kTiles * 128 * HD * 2;
     static constexpr int kSmem = kQBytes + kStages * kStage + 1024;   // + slack to align to 1024 bytes
-    static constexpr int kThreads = kTiles * 128 + 64;
+    static constexpr int kThreads = kTiles * 128 + 128;   // softmax; copies, products and two idle warps
+    // (two tiles: a launch of 384 threads x 168 registers; 2 x 128 x 208 + 128 x 80 are fewer)
     // tensor memory columns
     static constexpr int kS = 0, kSPitch = kKeys;                      // two of them: a tile's each, or two in turn
     static constexpr int kO = 256;
@@ -78,6 +79,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
+// One lane of a warp whose lanes are all here. The products are issued under it and not under a lane's number: the compiler then
+// knows that one thread is active, and keeps descriptors and addresses in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+template <typename X>
+__device__ __forceinline__ X uniform(X x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Descriptor of a tile [keys][64-channel blocks of 128 bytes] read along its channels (the product's columns): 8 keys
 // are 1024 bytes, the next 64 channels `block` bytes further.
 __device__ __forceinline__ uint64_t values_desc(const void *tile, int block) {
@@ -90,6 +101,44 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(saddr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(saddr(b))
         : "memory");
+}
+
+// mbar_wait with what mostly happens first: the phase is over
+__device__ __forceinline__ bool wait_for(uint64_t *b, unsigned parity, volatile int *bad) {
+    return mbar_test(b, parity) || mbar_wait(b, parity, bad);
+}
+
+// A place in the ring and the parity of the phase there, moved on without divisions
+struct Place {
+    int s;
+    unsigned phase;
+    __device__ void go(int by, int stages) {
+        s += by;
+        if (s >= stages) s -= stages, phase ^= 1u;
+    }
+};
+
+// two numbers in a register pair
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ void halves(uint64_t p, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -197,9 +246,9 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
     }
     if (t == 0) s_bad = 0;
 
-    for (int again = 0; again < 2; ++again) {
-        // the second time the last stage of the ring holds the notes on values that are not finite
-        const int stages = kMaxStages - again;
+    // What each pass begins and ends with; the warps of a kind go through both of their passes by themselves, so that each kind has its
+    // registers.
+    const auto begin_pass = [&](int again) {
         if (t == 0) {
             if (again) {
                 for (int i = 0; i < kMaxStages; ++i) mbar_inval(&full[i]), mbar_inval(&empty[i]);
@@ -226,93 +275,147 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        const uint32_t tmem = s_tmem;
+    };
+    const auto end_pass = [&](int stages) {
+        tc_fence_before();
+        __syncthreads();
+        if (t == 0) {
+            // every commit has landed before anything is used again; after a wait gave up, every copy issued too
+            if (s_bad)
+                for (int k = max(0, s_issued - stages); k < s_issued; ++k) mbar_drain(&full[k % stages], unsigned(k / stages) & 1u);
+            if (!mbar_drain(&b_done, 0u)) s_bad = 1;
+            if (s_bad) pg_report(a.c.err, kPgTimeout);
+        }
+        __syncthreads();
+        tc_fence_after();
+        const bool done = s_bad || !s_again;
+        __syncthreads();
+        return done;
+    };
 
-        if (warp == kTiles * 4) {
-            // ---- copies: K and V of each tile in turn through the ring ----
-            if (lane == 0) {
-                int k = 0;
-                bool stop = false;
-                for (int j = jb; j < je && !stop; ++j)
-                    for (int kv = 0; kv < 2; ++kv, ++k) {
-                        const int s = k % stages;
-                        if ((k >= stages && !mbar_wait(&empty[s], unsigned(k / stages - 1) & 1u, &s_bad)) || s_bad) {
-                            stop = true;
-                            break;
+    if (warp >= kTiles * 4) {
+        if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        for (int again = 0; again < 2; ++again) {
+            const int stages = kMaxStages - again;     // the second time the last stage holds the notes on values that are not finite
+            begin_pass(again);
+            if (warp == kTiles * 4) {
+                // ---- copies: K and V of each tile in turn through the ring ----
+                if (lane == 0) {
+                    int k = 0;
+                    bool stop = false;
+                    Place at{0, 1u};                   // (the first round's stages are free: the phase before counts as over)
+                    for (int j = jb; j < je && !stop; ++j)
+                        for (int kv = 0; kv < 2; ++kv, ++k) {
+                            if (!wait_for(&empty[at.s], at.phase, &s_bad) || s_bad) {
+                                stop = true;
+                                break;
+                            }
+                            mbar_expect(&full[at.s], unsigned(Sh::kStage));
+                            for (int x = 0; x < HD / 64; ++x)
+                                tma_load_3d(ring + at.s * Sh::kStage + x * kKeys * 128, kv ? &tv : &tk, 64 * x, h, row0 + j * kKeys, &full[at.s]);
+                            at.go(1, stages);
                         }
-                        mbar_expect(&full[s], unsigned(Sh::kStage));
-                        for (int x = 0; x < HD / 64; ++x)
-                            tma_load_3d(ring + s * Sh::kStage + x * kKeys * 128, kv ? &tv : &tk, 64 * x, h, row0 + j * kKeys, &full[s]);
-                    }
-                s_issued = k;
-            }
-        } else if (warp == kTiles * 4 + 1) {
-            // ---- products ----
-            if (lane == 0) {
-                const uint32_t id_s = prompt_idesc<T>(kKeys, false), id_o = prompt_idesc<T>(HD, true);
-                bool ok = mbar_wait(&b_q, 0u, &s_bad);
-                const auto arrived = [&](int k) { return mbar_wait(&full[k % stages], unsigned(k / stages) & 1u, &s_bad); };
-                const auto scores = [&](int w, int at, int k) {        // tile w, S number `at`, keys in stage k
-                    const uint8_t *kt = ring + (k % stages) * Sh::kStage;
-                    const uint32_t d = tmem + Sh::kS + at * Sh::kSPitch;
+                    s_issued = k;
+                }
+            } else if (warp == kTiles * 4 + 1) {
+                const uint32_t tmem = s_tmem;
+                // ---- products: the whole warp waits, one lane issues ----
+                constexpr uint32_t id_s = prompt_idesc<T>(kKeys, false), id_o = prompt_idesc<T>(HD, true);
+                const uint64_t q_desc = uniform(sw128_desc(qs)), k_desc = uniform(sw128_desc(ring)), v_desc = uniform(values_desc(ring, kKeys * 128));
+                const uint32_t tm = uniform(tmem);
+                const int begin = uniform(jb), end = uniform(je);
+                const KeyRange rs[2] = {{uniform(r0.begin), uniform(r0.end)}, {uniform(r1.begin), uniform(r1.end)}};
+                const auto scores = [&](int w, int at, int stage) {        // tile w, S number `at`, keys in the stage
+                    const uint64_t b = k_desc + uint64_t(stage * (Sh::kStage >> 4)), q = q_desc + uint64_t(w * (HD / 64) * (16384 >> 4));
+                    const uint32_t d = tm + Sh::kS + at * Sh::kSPitch;
 #pragma unroll
                     for (int i = 0; i < HD / 16; ++i) {
-                        const uint64_t b = sw128_desc(kt + (i / 4) * kKeys * 128) + 2 * (i % 4);
-                        if constexpr (HD == 256) mma_ts(d, tmem + Sh::kQ + 8 * i, b, id_s, i > 0);
-                        else mma_ss(d, sw128_desc(qs + (w * (HD / 64) + i / 4) * 16384) + 2 * (i % 4), b, id_s, i > 0);
+                        const uint64_t bi = b + uint64_t((i / 4) * (kKeys * 128 >> 4) + 2 * (i % 4));
+                        if constexpr (HD == 256) mma_ts(d, tm + Sh::kQ + 8 * i, bi, id_s, i > 0);
+                        else mma_ss(d, q + uint64_t((i / 4) * (16384 >> 4) + 2 * (i % 4)), bi, id_s, i > 0);
                     }
                 };
-                const auto values = [&](int w, int at, int k, bool add) {
-                    const uint8_t *vt = ring + (k % stages) * Sh::kStage;
+                const auto values = [&](int w, int at, int stage, bool add) {
+                    const uint64_t b = v_desc + uint64_t(stage * (Sh::kStage >> 4));
+                    const uint32_t d = tm + Sh::kO + w * HD, p = tm + Sh::kS + at * Sh::kSPitch;
 #pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i)
-                        mma_ts(tmem + Sh::kO + w * HD, tmem + Sh::kS + at * Sh::kSPitch + 8 * i, values_desc(vt + i * 2048, kKeys * 128), id_o, add || i > 0);
+                    for (int i = 0; i < kKeys / 16; ++i) mma_ts(d, p + 8 * i, b + uint64_t(i * (2048 >> 4)), id_o, add || i > 0);
                 };
+                const auto over = [&](uint64_t *b, unsigned parity) { return __all_sync(0xffffffffu, wait_for(b, parity, &s_bad)) != 0; };
+                bool ok = over(&b_q, 0u);
                 tc_fence_after();
+                Place k{0, 0u}, v{1, 0u};              // the stages of K j and of V j - 1
+                unsigned p_phase[2] = {0u, 0u};
                 // a thread's products run in the order of issue: S may be written over P as soon as P V has been issued
-                for (int j = jb; ok && j <= je; ++j) {
-                    const int kk = 2 * (j - jb), kv = kk - 1;          // the stages of K j and V j - 1
+                for (int j = begin; ok && j <= end; ++j) {
                     if constexpr (kTiles == 1) {
-                        if (j < je) {
-                            if (!(ok = arrived(kk))) break;
+                        if (j < end) {
+                            if (!(ok = over(&full[k.s], k.phase))) break;
                             tc_fence_after();
-                            scores(0, j & 1, kk);
-                            tc_commit(&b_s[j & 1]);
-                            tc_commit(&empty[kk % stages]);
+                            if (elect_one()) {
+                                scores(0, j & 1, k.s);
+                                tc_commit(&b_s[j & 1]);
+                                tc_commit(&empty[k.s]);
+                            }
+                            k.go(2, stages);
                         }
-                        if (j > jb) {
-                            if (!(ok = mbar_wait(&b_p[(j - 1) & 1], unsigned((j - 1 - jb) >> 1) & 1u, &s_bad) && arrived(kv))) break;
+                        if (j > begin) {
+                            const int at = (j - 1) & 1;
+                            if (!(ok = over(&full[v.s], v.phase) && over(&b_p[at], p_phase[at]))) break;
+                            p_phase[at] ^= 1u;
                             tc_fence_after();
-                            values(0, (j - 1) & 1, kv, j - 1 > jb);
-                            tc_commit(&b_o[0]);
-                            tc_commit(&empty[kv % stages]);
+                            if (elect_one()) {
+                                values(0, at, v.s, j - 1 > begin);
+                                tc_commit(&b_o[0]);
+                                tc_commit(&empty[v.s]);
+                            }
+                            v.go(2, stages);
                         }
                     } else {
+                        bool has_k = false, has_v = false;
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
-                            const KeyRange r = w ? r1 : r0;
-                            if (j - 1 >= r.begin && j - 1 < r.end) {
-                                if (!(ok = mbar_wait(&b_p[w], unsigned(j - 1 - r.begin) & 1u, &s_bad) && arrived(kv))) break;
-                                tc_fence_after();
-                                values(w, w, kv, j - 1 > r.begin);
-                                tc_commit(&b_o[w]);
+                            const KeyRange r = rs[w];
+                            const bool adds = j - 1 >= r.begin && j - 1 < r.end, takes = j >= r.begin && j < r.end;
+                            if (adds) {
+                                if (!(ok = (has_v || over(&full[v.s], v.phase)) && over(&b_p[w], p_phase[w]))) break;
+                                has_v = true;
+                                p_phase[w] ^= 1u;
                             }
-                            if (w == 1 && j > jb) tc_commit(&empty[kv % stages]);
-                            if (j >= r.begin && j < r.end) {
-                                if (!(ok = arrived(kk))) break;
-                                tc_fence_after();
-                                scores(w, w, kk);
-                                tc_commit(&b_s[w]);
+                            if (takes) {
+                                if (!(ok = has_k || over(&full[k.s], k.phase))) break;
+                                has_k = true;
+                            }
+                            tc_fence_after();
+                            if (elect_one()) {
+                                if (adds) {
+                                    values(w, w, v.s, j - 1 > r.begin);
+                                    tc_commit(&b_o[w]);
+                                }
+                                if (w == 1 && j > begin) tc_commit(&empty[v.s]);
+                                if (takes) {
+                                    scores(w, w, k.s);
+                                    tc_commit(&b_s[w]);
+                                }
+                                if (w == 1 && j < end) tc_commit(&empty[k.s]);
                             }
                         }
                         if (!ok) break;
-                        if (j < je) tc_commit(&empty[kk % stages]);
+                        if (j > begin) v.go(2, stages);
+                        k.go(2, stages);
                     }
                 }
-                tc_commit(&b_done);
+                if (elect_one()) tc_commit(&b_done);
+                __syncwarp();
             }
-            __syncwarp();
-        } else {
+            if (end_pass(stages)) break;
+        }
+    } else {
+        if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        for (int again = 0; again < 2; ++again) {
+            const int stages = kMaxStages - again;     // the second time the last stage holds the notes on values that are not finite
+            begin_pass(again);
+            const uint32_t tmem = s_tmem;
             // ---- softmax: tile w, a row a thread ----
             const int w = warp >> 2, r = t & 127;
             const KeyRange rg = w ? r1 : r0;
@@ -325,7 +428,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
             // Q: rows of tokens behind the sequence's last one are zeros
             if constexpr (HD == 256) {
                 const uint8_t *src = a.q + (int64_t)(row0 + tok) * a.ldq + (h * g + r % g) * HD * 2;
-#pragma unroll 1
+#pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     uint32_t v[32];
 #pragma unroll
@@ -338,12 +441,21 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                 tc_wait_st();
                 tc_fence_before();
             } else {
-                for (int i = r; i < 128 * (HD / 8); i += 128) {
-                    const int row = i / (HD / 8), ch = i % (HD / 8), at = t0 + row / g;
-                    uint4 u = make_uint4(0, 0, 0, 0);
+                // a row's pieces by HD / 8 threads beside each other, all asked for before the first is stored
+                constexpr int kCh = HD / 8, kStep = 128 / kCh;
+                const int ch = r % kCh;
+                uint4 u[kCh];
+#pragma unroll
+                for (int i = 0; i < kCh; ++i) {
+                    const int row = r / kCh + i * kStep, at = t0 + row / g;
+                    u[i] = make_uint4(0, 0, 0, 0);
                     if (row < tokens * g && at < n)
-                        u = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(row0 + at) * a.ldq + ((h * g + row % g) * HD + 8 * ch) * 2);
-                    *reinterpret_cast<uint4 *>(qs + (w * (HD / 64) + ch / 8) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = u;
+                        u[i] = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(row0 + at) * a.ldq + ((h * g + row % g) * HD + 8 * ch) * 2);
+                }
+#pragma unroll
+                for (int i = 0; i < kCh; ++i) {
+                    const int row = r / kCh + i * kStep;
+                    *reinterpret_cast<uint4 *>(qs + (w * (HD / 64) + ch / 8) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = u[i];
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
@@ -363,7 +475,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                 // (a wait names a phase by its parity, so none may be left out: P V of the tile before, or with S held twice
                 // of the one before that, has been added already and only has to be ticked off)
                 constexpr int kAhead = kTiles == 1 ? 2 : 1;
-                ok = mbar_wait(&b_s[at], unsigned(phase) & 1u, &s_bad) && (it < kAhead || mbar_wait(&b_o[w], unsigned(it - kAhead) & 1u, &s_bad));
+                ok = wait_for(&b_s[at], unsigned(phase) & 1u, &s_bad) && (it < kAhead || wait_for(&b_o[w], unsigned(it - kAhead) & 1u, &s_bad));
                 if (!__all_sync(0xffffffffu, ok)) break;               // tcgen05.ld takes the whole warp
                 tc_fence_after();
                 uint32_t s[kKeys / 32][32];
@@ -374,22 +486,22 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
 #pragma unroll
                 for (int x = 0; x < kKeys / 32; ++x) tc_tie32(s[x]);
                 const int k0 = j * kKeys;
-                if (k0 + kKeys > t0 + 1 || k0 < full_lo) {
+                if (k0 + kKeys > t0 + 1) {
 #pragma unroll
-                    for (int x = 0; x < kKeys / 32; ++x)
+                    for (int x = 0; x < kKeys; ++x)
+                        if (x >= hi - k0) s[x / 32][x % 32] = __float_as_uint(-INFINITY);
+                }
+                if (k0 < full_lo) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int key = k0 + 32 * x + i;
-                            if (key < lo || key >= hi) s[x][i] = __float_as_uint(-INFINITY);
-                        }
+                    for (int x = 0; x < kKeys; ++x)
+                        if (x < lo - k0) s[x / 32][x % 32] = __float_as_uint(-INFINITY);
                 }
                 float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int x = 0; x < kKeys / 32; ++x)
+                for (int x = 0; x < kKeys; x += 8)
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) m[y] = fmaxf(m[y], __uint_as_float(s[x][i + y]));
+                    for (int y = 0; y < 4; ++y)
+                        m[y] = fmaxf(fmaxf(m[y], __uint_as_float(s[x / 32][x % 32 + y])), __uint_as_float(s[x / 32][x % 32 + y + 4]));
                 const float best = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
                 const bool renew = (best - top) * c > 8.f;
                 float keep = 1.f;
@@ -399,7 +511,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                 }
                 if (__any_sync(0xffffffffu, renew) && it > 0) {
                     if constexpr (kAhead == 2) {
-                        ok = mbar_wait(&b_o[w], unsigned(it - 1) & 1u, &s_bad);
+                        ok = wait_for(&b_o[w], unsigned(it - 1) & 1u, &s_bad);
                         if (!__all_sync(0xffffffffu, ok)) break;
                         tc_fence_after();
                     }
@@ -413,21 +525,25 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                     }
                 }
                 const float off = top == -INFINITY ? 0.f : kShift - top * c;
-                float add[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t c2 = pair(__float_as_uint(c), __float_as_uint(c)), off2 = pair(__float_as_uint(off), __float_as_uint(off));
+                uint64_t add[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int x = 0; x < kKeys / 64; ++x) {
                     uint32_t p[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float p0 = exp2_fast(fmaf(__uint_as_float(s[2 * x + i / 16][2 * (i % 16)]), c, off));
-                        const float p1 = exp2_fast(fmaf(__uint_as_float(s[2 * x + i / 16][2 * (i % 16) + 1]), c, off));
-                        add[2 * (i & 1)] += p0;
-                        add[2 * (i & 1) + 1] += p1;
+                        const int k = 64 * x + 2 * i;
+                        float p0, p1;
+                        halves(fma2(pair(s[k / 32][k % 32], s[k / 32][k % 32 + 1]), c2, off2), p0, p1);
+                        p0 = exp2_fast(p0), p1 = exp2_fast(p1);
+                        add[i & 3] = add2(add[i & 3], pair(__float_as_uint(p0), __float_as_uint(p1)));
                         p[i] = pack2<T>(p0, p1);
                     }
                     tc_st32(t_s + 32 * x, p);
                 }
-                sum = sum * keep + ((add[0] + add[1]) + (add[2] + add[3]));
+                float a0, a1;
+                halves(add2(add2(add[0], add[1]), add2(add[2], add[3])), a0, a1);
+                sum = sum * keep + (a0 + a1);
                 if (again) {
                     // what is not finite leaves the tile of values, and each row notes what it saw of it
                     const bool both = kTiles == 2 && j >= r0.begin && j < r0.end && j >= r1.begin && j < r1.end;
@@ -436,9 +552,9 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                     uint32_t *notes = reinterpret_cast<uint32_t *>(ring + (kMaxStages - 1) * Sh::kStage) + id * kKeys * (HD / 32), *odd = s_odd[id];
                     const auto meet = [&] {
                         mbar_arrive(&b_meet[id]);
-                        return __all_sync(0xffffffffu, mbar_wait(&b_meet[id], unsigned(met[id != 0]++) & 1u, &s_bad)) != 0;
+                        return __all_sync(0xffffffffu, wait_for(&b_meet[id], unsigned(met[id != 0]++) & 1u, &s_bad)) != 0;
                     };
-                    ok = mbar_wait(&full[k % stages], unsigned(k / stages) & 1u, &s_bad);
+                    ok = wait_for(&full[k % stages], unsigned(k / stages) & 1u, &s_bad);
                     if (!__all_sync(0xffffffffu, ok)) break;
                     if (!(ok = meet())) break;     // the notes of the tile before have been read
                     if (who < kKeys / 32) odd[who] = 0;
@@ -479,8 +595,8 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
             // ---- the sums, divided and rounded ----
             const int last = rg.end - rg.begin - 1;
             if (last >= 0) {
-                if (kTiles == 1 && ok && last > 0) ok = mbar_wait(&b_o[w], unsigned(last - 1) & 1u, &s_bad);
-                if (ok) ok = mbar_wait(&b_o[w], unsigned(last) & 1u, &s_bad);
+                if (kTiles == 1 && ok && last > 0) ok = wait_for(&b_o[w], unsigned(last - 1) & 1u, &s_bad);
+                if (ok) ok = wait_for(&b_o[w], unsigned(last) & 1u, &s_bad);
                 if (__all_sync(0xffffffffu, ok)) {
                     tc_fence_after();
                     const float part = 1.f / sum;
@@ -508,21 +624,8 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                     if (live && odd && !isnan(sum)) s_again = 1;
                 }
             }
+            if (end_pass(stages)) break;
         }
-        tc_fence_before();
-        __syncthreads();
-        if (t == 0) {
-            // every commit has landed before anything is used again; after a wait gave up, every copy issued too
-            if (s_bad)
-                for (int k = max(0, s_issued - stages); k < s_issued; ++k) mbar_drain(&full[k % stages], unsigned(k / stages) & 1u);
-            if (!mbar_drain(&b_done, 0u)) s_bad = 1;
-            if (s_bad) pg_report(a.c.err, kPgTimeout);
-        }
-        __syncthreads();
-        tc_fence_after();
-        const bool done = s_bad || !s_again;
-        __syncthreads();
-        if (done) break;
     }
     if (warp == kTiles * 4 + 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "r"(512) : "memory");
