@@ -34,15 +34,16 @@ struct PromptShape {
     static constexpr int kTiles = HD == 256 ? 1 : 2;
     static constexpr int kKeys = HD == 256 ? 64 : 128;
     static constexpr int kStage = kKeys * HD * 2;
-    static constexpr int kStages = HD == 64 ? 8 : HD == 128 ? 5 : 7;
-    static constexpr int kQBytes = HD == 256 ? 0 : kTiles * 128 * HD * 2;
+    static constexpr int kStages = HD == 64 ? 8 : HD == 128 ? 5 : 6;
+    // Q of each tile; afterwards, and with 256 channels from the start, a place where each warp turns its rows round
+    static constexpr int kQBytes = kTiles * 128 * (HD == 256 ? 128 : HD) * 2;
     static constexpr int kSmem = kQBytes + kStages * kStage + 1024;   // + slack to align to 1024 bytes
     static constexpr int kThreads = kTiles * 128 + 128;   // softmax; copies, products and two idle warps
     // (two tiles: a launch of 384 threads x 168 registers; 2 x 128 x 208 + 128 x 80 are fewer)
     // tensor memory columns
     static constexpr int kS = 0, kSPitch = kKeys;                      // two of them: a tile's each, or two in turn
     static constexpr int kO = 256;
-    static constexpr int kQ = 128;                                     // (256 channels alone)
+    [[maybe_unused]] static constexpr int kQ = 128;                                     // (256 channels alone)
 };
 
 struct PromptArgs {
@@ -50,7 +51,7 @@ struct PromptArgs {
     const uint8_t *q;
     uint8_t *out;
     int64_t ldq, ldo;          // bytes
-    int group, total, window;
+    int group, inverse, total, window;            // r / group is (r * inverse) >> 12 for rows of a tile
     const int32_t *cu;
     float scale_log2;
 };
@@ -135,11 +136,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -173,6 +169,99 @@ struct KeyRange {
     int begin, end;
 };
 
+// Items: kTiles tiles of a sequence. Of all sequences together the last ones, which see most keys, come first, so that what the
+// grid's end is made of is short: item number x has the largest index i for which more than x items have an index of i or above.
+struct Item {
+    int row0, rows, at;                          // the sequence's first row and rows; the item's index in it
+};
+constexpr int kItemLanes = 8;                    // sequences of a lane at most
+
+__device__ __forceinline__ int items_of(const PromptArgs &a, int per, int s, int h, int number, int *row0, int *rows) {
+    const int b = a.cu[s], e = a.cu[s + 1];
+    if (b < 0 || e < b || e > a.total) {
+        if (number == 0 && h == 0) pg_report(a.c.err, kPgArg);
+        return 0;
+    }
+    *row0 = b, *rows = e - b;
+    return (e - b + per - 1) / per;
+}
+
+// Every warp for itself, up to 32 * kItemLanes sequences
+__device__ __forceinline__ bool find_item(const PromptArgs &a, int per, int number, int h, Item &item) {
+    const int lane = threadIdx.x & 31, S = a.c.n_seq;
+    if (S == 1) {
+        const int n = items_of(a, per, 0, h, number, &item.row0, &item.rows);
+        item.at = n - 1 - number;
+        return number < n;
+    }
+    int n[kItemLanes], row0[kItemLanes], rows[kItemLanes], most = 0;
+#pragma unroll
+    for (int v = 0; v < kItemLanes; ++v) {
+        const int s = 32 * v + lane;
+        n[v] = s < S ? items_of(a, per, s, h, number, &row0[v], &rows[v]) : 0;
+        most = max(most, n[v]);
+    }
+    const auto from = [&](int i) {               // items with an index of i or above
+        int sum = 0;
+#pragma unroll
+        for (int v = 0; v < kItemLanes; ++v) sum += max(0, n[v] - i);
+        return __reduce_add_sync(0xffffffffu, sum);
+    };
+    int lo = 0, hi = __reduce_max_sync(0xffffffffu, most);       // from(lo) > number >= from(hi)
+    if (number >= from(0)) return false;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (from(mid) > number) lo = mid;
+        else hi = mid;
+    }
+    int left = number - from(hi);                // of the sequences that have an item of index lo, the left-th
+#pragma unroll
+    for (int v = 0; v < kItemLanes; ++v) {
+        const uint32_t has = __ballot_sync(0xffffffffu, n[v] > lo);
+        const int count = __popc(has);
+        if (left >= 0 && left < count) {
+            const uint32_t who = __ballot_sync(0xffffffffu, (has >> lane & 1u) && __popc(has & ((1u << lane) - 1u)) == left);
+            const int from_lane = __ffs(who) - 1;
+            item.row0 = __shfl_sync(0xffffffffu, row0[v], from_lane);
+            item.rows = __shfl_sync(0xffffffffu, rows[v], from_lane);
+        }
+        left -= count;
+    }
+    item.at = lo;
+    return true;
+}
+
+// The CTA together, any number of sequences: one after another, the last items of each first
+template <int THREADS>
+__device__ bool find_item_wide(const PromptArgs &a, int per, int number, int h, int *sums, Item *item) {
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, S = a.c.n_seq;
+    const int each = (S + THREADS - 1) / THREADS, s0 = min(t * each, S), s1 = min(s0 + each, S);
+    int mine = 0, row0 = 0, rows = 0;
+    for (int s = s0; s < s1; ++s) mine += items_of(a, per, s, h, number, &row0, &rows);
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+    }
+    if (t == 0) item->rows = 0;
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) sum += sums[w];
+    int left = number - (sum - mine);
+    if (left >= 0 && left < mine)
+        for (int s = s0; s < s1; ++s) {
+            const int n = items_of(a, per, s, h, 1, &row0, &rows);
+            if (left < n) {
+                *item = Item{row0, rows, n - 1 - left};
+                break;
+            }
+            left -= n;
+        }
+    __syncthreads();
+    return item->rows > 0;
+}
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
     k_prompt(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PromptArgs a) {
@@ -181,54 +270,29 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
     extern __shared__ uint8_t prompt_smem_raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], b_q, b_s[2], b_p[2], b_o[2], b_meet[3], b_done;
     __shared__ uint32_t s_tmem, s_odd[3][kKeys / 32];
-    __shared__ int s_seq, s_item, s_row0, s_rows, s_issued, s_again, s_sum[Sh::kThreads / 32];
+    __shared__ int s_issued, s_again, s_sum[Sh::kThreads / 32];
+    __shared__ Item s_item;
     __shared__ volatile int s_bad;
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(prompt_smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *qs = base, *ring = base + Sh::kQBytes;
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, h = blockIdx.y, g = a.group;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = a.group;
     const int tokens = 128 / g;                                  // of a tile
+    const int h = blockIdx.x % a.c.n_kv, number = blockIdx.x / a.c.n_kv;
+    if (warp == kTiles * 4 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tk) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tv) : "memory");
+    }
     pdl_wait();
 
-    // ---- the CTA's item: tiles item * kTiles .. of a sequence; the longest items of a sequence come first ----
-    {
-        const int S = a.c.n_seq, each = (S + Sh::kThreads - 1) / Sh::kThreads, s0 = min(t * each, S), s1 = min(s0 + each, S);
-        const auto items = [&](int s) {
-            const int b = a.cu[s], e = a.cu[s + 1];
-            if (b < 0 || e < b || e > a.total) {
-                if (blockIdx.x == 0 && h == 0) pg_report(a.c.err, kPgArg);
-                return 0;
-            }
-            return (e - b + kTiles * tokens - 1) / (kTiles * tokens);
-        };
-        int mine = 0, sum;
-        for (int s = s0; s < s1; ++s) mine += items(s);
-        sum = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += u;
-        }
-        if (t == 0) s_seq = -1;
-        if (lane == 31) s_sum[warp] = sum;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) sum += s_sum[w];
-        int left = int(blockIdx.x) - (sum - mine);
-        if (left >= 0 && left < mine)
-            for (int s = s0; s < s1; ++s) {
-                const int n = items(s);
-                if (left < n) {
-                    s_seq = s;
-                    s_item = n - 1 - left;
-                    s_row0 = a.cu[s];
-                    s_rows = a.cu[s + 1] - a.cu[s];
-                    break;
-                }
-                left -= n;
-            }
-        __syncthreads();
-        if (s_seq < 0) return;
+    // ---- the CTA's item: tiles item * kTiles .. of a sequence ----
+    Item item;
+    if (a.c.n_seq <= 32 * kItemLanes) {
+        if (!find_item(a, kTiles * tokens, number, h, item)) return;             // each warp by itself
+    } else {
+        if (!find_item_wide<Sh::kThreads>(a, kTiles * tokens, number, h, s_sum, &s_item)) return;
+        item = s_item;
     }
-    const int row0 = s_row0, n = s_rows, tok0 = s_item * kTiles * tokens;
+    const int row0 = item.row0, n = item.rows, tok0 = item.at * kTiles * tokens;
     const auto range = [&](int w) {
         const int lo = tok0 + w * tokens, hi = min(lo + tokens, n);
         KeyRange r{0, 0};
@@ -244,34 +308,34 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&s_tmem)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (t == 0) s_bad = 0;
 
     // What each pass begins and ends with; the warps of a kind go through both of their passes by themselves, so that each kind has its
     // registers.
-    const auto begin_pass = [&](int again) {
-        if (t == 0) {
-            if (again) {
-                for (int i = 0; i < kMaxStages; ++i) mbar_inval(&full[i]), mbar_inval(&empty[i]);
-                for (int i = 0; i < 2; ++i) mbar_inval(&b_s[i]), mbar_inval(&b_p[i]), mbar_inval(&b_o[i]);
-                for (int i = 0; i < 3; ++i) mbar_inval(&b_meet[i]);
-                mbar_inval(&b_q), mbar_inval(&b_done);
-            }
-            for (int i = 0; i < kMaxStages; ++i) {
-                mbar_init(&full[i], 1);        // the producer's arrival (with the stage's bytes)
-                mbar_init(&empty[i], 1);       // the MMA thread's commit
-            }
-            mbar_init(&b_q, kSoft);            // Q lies where the products read it
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&b_s[i], 1);         // S is complete: the MMA thread's commit
-                mbar_init(&b_p[i], 128);       // P lies in tensor memory, and O may be added to
-                mbar_init(&b_o[i], 1);         // P V is added
-            }
-            for (int i = 0; i < 3; ++i) mbar_init(&b_meet[i], i ? 128 : kSoft);   // the threads of both tiles, of one
-            mbar_init(&b_done, 1);             // the MMA thread's last commit
-            s_issued = s_again = 0;
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    const auto init_pass = [&](int again) {      // by the thread that copies: its first copies need not wait for the others
+        if (again) {
+            for (int i = 0; i < kMaxStages; ++i) mbar_inval(&full[i]), mbar_inval(&empty[i]);
+            for (int i = 0; i < 2; ++i) mbar_inval(&b_s[i]), mbar_inval(&b_p[i]), mbar_inval(&b_o[i]);
+            for (int i = 0; i < 3; ++i) mbar_inval(&b_meet[i]);
+            mbar_inval(&b_q), mbar_inval(&b_done);
         }
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(&full[i], 1);              // the producer's arrival (with the stage's bytes)
+            mbar_init(&empty[i], 1);             // the MMA thread's commit
+        }
+        mbar_init(&b_q, kSoft);                  // Q lies where the products read it
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b_s[i], 1);               // S is complete: the MMA thread's commit
+            mbar_init(&b_p[i], 128);             // P lies in tensor memory, and O may be added to
+            mbar_init(&b_o[i], 1);               // P V is added
+        }
+        for (int i = 0; i < 3; ++i) mbar_init(&b_meet[i], i ? 128 : kSoft);   // the threads of both tiles, of one
+        mbar_init(&b_done, 1);                   // the MMA thread's last commit
+        s_issued = s_again = 0;
+        s_bad = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    };
+    const auto begin_pass = [&] {
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
@@ -297,27 +361,31 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
         if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         for (int again = 0; again < 2; ++again) {
             const int stages = kMaxStages - again;     // the second time the last stage holds the notes on values that are not finite
-            begin_pass(again);
             if (warp == kTiles * 4) {
                 // ---- copies: K and V of each tile in turn through the ring ----
+                const int all = 2 * (je - jb);
+                int k = 0;
+                Place at{0, 1u};                       // (the first round's stages are free: the phase before counts as over)
+                const auto copy = [&] {
+                    mbar_expect(&full[at.s], unsigned(Sh::kStage));
+                    for (int x = 0; x < HD / 64; ++x)
+                        tma_load_3d(ring + at.s * Sh::kStage + x * kKeys * 128, k & 1 ? &tv : &tk, 64 * x, h, row0 + (jb + (k >> 1)) * kKeys, &full[at.s]);
+                    at.go(1, stages);
+                    ++k;
+                };
                 if (lane == 0) {
-                    int k = 0;
-                    bool stop = false;
-                    Place at{0, 1u};                   // (the first round's stages are free: the phase before counts as over)
-                    for (int j = jb; j < je && !stop; ++j)
-                        for (int kv = 0; kv < 2; ++kv, ++k) {
-                            if (!wait_for(&empty[at.s], at.phase, &s_bad) || s_bad) {
-                                stop = true;
-                                break;
-                            }
-                            mbar_expect(&full[at.s], unsigned(Sh::kStage));
-                            for (int x = 0; x < HD / 64; ++x)
-                                tma_load_3d(ring + at.s * Sh::kStage + x * kKeys * 128, kv ? &tv : &tk, 64 * x, h, row0 + j * kKeys, &full[at.s]);
-                            at.go(1, stages);
-                        }
+                    init_pass(again);
+                    while (k < min(all, stages)) copy();
+                }
+                __syncwarp();
+                begin_pass();
+                if (lane == 0) {
+                    while (k < all && wait_for(&empty[at.s], at.phase, &s_bad) && !s_bad) copy();
                     s_issued = k;
                 }
+                __syncwarp();
             } else if (warp == kTiles * 4 + 1) {
+                begin_pass();
                 const uint32_t tmem = s_tmem;
                 // ---- products: the whole warp waits, one lane issues ----
                 constexpr uint32_t id_s = prompt_idesc<T>(kKeys, false), id_o = prompt_idesc<T>(HD, true);
@@ -407,6 +475,8 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                 }
                 if (elect_one()) tc_commit(&b_done);
                 __syncwarp();
+            } else {
+                begin_pass();
             }
             if (end_pass(stages)) break;
         }
@@ -414,50 +484,67 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
         if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         for (int again = 0; again < 2; ++again) {
             const int stages = kMaxStages - again;     // the second time the last stage holds the notes on values that are not finite
-            begin_pass(again);
-            const uint32_t tmem = s_tmem;
             // ---- softmax: tile w, a row a thread ----
             const int w = warp >> 2, r = t & 127;
             const KeyRange rg = w ? r1 : r0;
             const int t0 = tok0 + w * tokens;                          // the tile's first token
-            const bool live = r < tokens * g && t0 + r / g < n;
-            const int tok = min(t0 + min(r / g, tokens - 1), n - 1), hi = tok + 1, lo = a.window ? max(0, tok - a.window + 1) : 0;
+            const auto token_of = [&](int row) { return row * a.inverse >> 12; };
+            const bool live = r < tokens * g && t0 + token_of(r) < n;
+            const int tok = min(t0 + min(token_of(r), tokens - 1), n - 1), hi = tok + 1, lo = a.window ? max(0, tok - a.window + 1) : 0;
             const int full_lo = a.window ? max(0, min(t0 + tokens, n) - a.window) : 0;   // keys from here to t0 are seen by all rows
             const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
-            const uint32_t t_o = tmem + Sh::kO + w * HD + lanes;
-            // Q: rows of tokens behind the sequence's last one are zeros
-            if constexpr (HD == 256) {
-                const uint8_t *src = a.q + (int64_t)(row0 + tok) * a.ldq + (h * g + r % g) * HD * 2;
+            // A row of the tile in a buffer of packed rows, and whether it is one
+            const auto row_at = [&](int row, int64_t ld, bool &there) {
+                const int token = token_of(row), at = t0 + token;
+                there = row < tokens * g && at < n;
+                return (int64_t)(row0 + min(at, n - 1)) * ld + (h * g + min(row - token * g, g - 1)) * HD * 2;
+            };
+            // Rows cross between memory, where a row's pieces of 16 bytes go by lanes beside each other, and tensor memory, where a lane
+            // has a row, through the warp's part of the shared memory (pieces turned by the row's number)
+            constexpr int kPieces = HD == 64 ? 8 : 16, kRounds = HD / 8 / kPieces, kEach = 32 / (32 / kPieces);   // of a row in a round; rounds; rows a lane
+            uint8_t *turn = qs + (w * 4 + (warp & 3)) * 32 * kPieces * 16;
+            const auto turn_at = [&](int row, int piece) { return reinterpret_cast<uint4 *>(turn + (row * kPieces + (piece ^ (row & 7))) * 16); };
+            // Q, all of it asked for before the CTA's threads meet; rows of tokens behind the sequence's last one are zeros
+            constexpr int kCh = HD / 8;
+            uint4 u[kCh];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 u = live ? *reinterpret_cast<const uint4 *>(src + 128 * x + 16 * i) : make_uint4(0, 0, 0, 0);
-                        v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
-                    }
-                    tc_st32(tmem + Sh::kQ + 32 * x + lanes, v);
-                }
-                tc_wait_st();
-                tc_fence_before();
-            } else {
-                // a row's pieces by HD / 8 threads beside each other, all asked for before the first is stored
-                constexpr int kCh = HD / 8, kStep = 128 / kCh;
-                const int ch = r % kCh;
-                uint4 u[kCh];
-#pragma unroll
-                for (int i = 0; i < kCh; ++i) {
-                    const int row = r / kCh + i * kStep, at = t0 + row / g;
-                    u[i] = make_uint4(0, 0, 0, 0);
-                    if (row < tokens * g && at < n)
-                        u[i] = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(row0 + at) * a.ldq + ((h * g + row % g) * HD + 8 * ch) * 2);
-                }
+            for (int i = 0; i < kCh; ++i) {
+                const int round = i / kEach, row = 32 * (warp & 3) + i % kEach * (32 / kPieces) + lane / kPieces;
+                bool there;
+                const int64_t at = row_at(row, a.ldq, there);
+                u[i] = *reinterpret_cast<const uint4 *>(a.q + at + (round * kPieces + lane % kPieces) * 16);
+                if (!there) u[i] = make_uint4(0, 0, 0, 0);
+            }
+            if constexpr (HD < 256) {
 #pragma unroll
                 for (int i = 0; i < kCh; ++i) {
-                    const int row = r / kCh + i * kStep;
+                    const int row = 32 * (warp & 3) + i * (32 / kPieces) + lane / kPieces, ch = lane % kPieces;
                     *reinterpret_cast<uint4 *>(qs + (w * (HD / 64) + ch / 8) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = u[i];
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            begin_pass();
+            const uint32_t tmem = s_tmem, t_o = tmem + Sh::kO + w * HD + lanes;
+            if constexpr (HD == 256) {
+#pragma unroll
+                for (int round = 0; round < kRounds; ++round) {
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i) *turn_at(i * (32 / kPieces) + lane / kPieces, lane % kPieces) = u[round * kEach + i];
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint4 p = *turn_at(lane, 8 * x + i);
+                            v[4 * i] = p.x, v[4 * i + 1] = p.y, v[4 * i + 2] = p.z, v[4 * i + 3] = p.w;
+                        }
+                        tc_st32(tmem + Sh::kQ + 64 * round + 32 * x + lanes, v);
+                    }
+                    __syncwarp();
+                }
+                tc_wait_st();
+                tc_fence_before();
             }
             mbar_arrive(&b_q);
 
@@ -486,15 +573,15 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
 #pragma unroll
                 for (int x = 0; x < kKeys / 32; ++x) tc_tie32(s[x]);
                 const int k0 = j * kKeys;
-                if (k0 + kKeys > t0 + 1) {
+                if (k0 + kKeys > t0 + 1 || k0 < full_lo) {
 #pragma unroll
-                    for (int x = 0; x < kKeys; ++x)
-                        if (x >= hi - k0) s[x / 32][x % 32] = __float_as_uint(-INFINITY);
-                }
-                if (k0 < full_lo) {
+                    for (int x = 0; x < kKeys / 32; ++x) {
+                        const int up = min(max(hi - k0 - 32 * x, 0), 32), down = min(max(lo - k0 - 32 * x, 0), 32);
+                        const uint32_t seen_by = (up == 32 ? 0xffffffffu : (1u << up) - 1u) & ~(down == 32 ? 0xffffffffu : (1u << down) - 1u);
 #pragma unroll
-                    for (int x = 0; x < kKeys; ++x)
-                        if (x < lo - k0) s[x / 32][x % 32] = __float_as_uint(-INFINITY);
+                        for (int i = 0; i < 32; ++i)
+                            if (!(seen_by >> i & 1u)) s[x][i] = __float_as_uint(-INFINITY);
+                    }
                 }
                 float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -600,26 +687,36 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                 if (__all_sync(0xffffffffu, ok)) {
                     tc_fence_after();
                     const float part = 1.f / sum;
-                    uint8_t *dst = a.out + (int64_t)(row0 + tok) * a.ldo + (h * g + r % g) * HD * 2;
                     bool odd = false;
 #pragma unroll
-                    for (int x = 0; x < HD / 32; ++x) {
-                        uint32_t o[32];
-                        tc_ld32(t_o + 32 * x, o);
-                        const uint32_t gone = seen[x];
+                    for (int round = 0; round < kRounds; ++round) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            odd |= isnan(__uint_as_float(o[i]));
-                            o[i] = gone >> i & 1u ? 0x7FFFFFFFu : __float_as_uint(__uint_as_float(o[i]) * part);
-                        }
-                        if (live)
+                        for (int x = 0; x < kPieces / 4; ++x) {
+                            uint32_t o[32];
+                            const int at = round * (kPieces / 4) + x;
+                            tc_ld32(t_o + 32 * at, o);
+                            const uint32_t gone = seen[at];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                odd |= isnan(__uint_as_float(o[i]));
+                                o[i] = gone >> i & 1u ? 0x7FFFFFFFu : __float_as_uint(__uint_as_float(o[i]) * part);
+                            }
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                *reinterpret_cast<uint4 *>(dst + 64 * x + 16 * i) =
-                                    make_uint4(pack2<T>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
-                                               pack2<T>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
-                                               pack2<T>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
-                                               pack2<T>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
+                                *turn_at(lane, 4 * x + i) = make_uint4(pack2<T>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
+                                                                       pack2<T>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
+                                                                       pack2<T>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
+                                                                       pack2<T>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < kEach; ++i) {
+                            const int row = i * (32 / kPieces) + lane / kPieces;
+                            bool there;
+                            const int64_t to = row_at(32 * (warp & 3) + row, a.ldo, there);
+                            if (there) *reinterpret_cast<uint4 *>(a.out + to + (round * kPieces + lane % kPieces) * 16) = *turn_at(row, lane % kPieces);
+                        }
+                        __syncwarp();
                     }
                     if (live && odd && !isnan(sum)) s_again = 1;
                 }
@@ -656,12 +753,12 @@ int launch_prompt(const PagedAttnArgs &a, cudaStream_t s) {
     }
     CUtensorMap tk, tv;
     if (!rows_map(&tk, a.c, a.k, a.ldk, a.total, Sh::kKeys) || !rows_map(&tv, a.c, a.v, a.ldv, a.total, Sh::kKeys)) return DFL_E_CUDA;
-    const PromptArgs p{a.c, static_cast<const uint8_t *>(a.q), static_cast<uint8_t *>(a.out), a.ldq * 2, a.ldo * 2, a.group, a.total, a.window, a.cu,
+    const PromptArgs p{a.c, static_cast<const uint8_t *>(a.q), static_cast<uint8_t *>(a.out), a.ldq * 2, a.ldo * 2, a.group, (4096 + a.group - 1) / a.group, a.total, a.window, a.cu,
                        a.scale_log2};
     const int per = Sh::kTiles * (128 / a.group);                // tokens of an item
     const int64_t items = (int64_t)a.total / per + std::min(a.c.n_seq, a.total);
-    if (items > INT32_MAX) return DFL_E_UNSUPPORTED;
-    return pg_launched(launch_pdl(k_prompt<T, HD>, dim3(unsigned(items), a.c.n_kv), dim3(Sh::kThreads), Sh::kSmem, s, tk, tv, p));
+    if (items * a.c.n_kv > INT32_MAX) return DFL_E_UNSUPPORTED;
+    return pg_launched(launch_pdl(k_prompt<T, HD>, dim3(unsigned(items * a.c.n_kv)), dim3(Sh::kThreads), Sh::kSmem, s, tk, tv, p));
 }
 
 }  // namespace
