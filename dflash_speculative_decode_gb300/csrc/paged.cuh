@@ -11,6 +11,7 @@ namespace dfl {
 // error bits (dfl_paged.err)
 constexpr int kPgCapacity = 1, kPgState = 2, kPgArg = 4, kPgTimeout = 8;
 constexpr int kPgMaxGroup = 16;          // query heads per key/value head
+constexpr int64_t kPgMaxLd = 1 << 22;    // elements between rows: what a tile of 128 rows spans fits 31 bits of bytes
 
 inline bool pg_aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -29,7 +30,8 @@ inline int pg_check(const dfl_paged *c) {
 }
 
 inline int pg_check_rows(const dfl_paged *c, const void *p, int64_t ld, int heads) {
-    return p && pg_aligned(p, 16) && ld % 8 == 0 && ld >= (int64_t)heads * c->head_dim ? DFL_OK : DFL_E_INVALID_ARG;
+    if (!p || !pg_aligned(p, 16) || ld % 8 || ld < (int64_t)heads * c->head_dim) return DFL_E_INVALID_ARG;
+    return ld <= kPgMaxLd ? DFL_OK : DFL_E_UNSUPPORTED;
 }
 
 inline int pg_check_heads(const dfl_paged *c, int n_q, int window, float scale) {

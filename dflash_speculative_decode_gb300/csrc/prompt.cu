@@ -34,9 +34,9 @@ struct PromptShape {
     static constexpr int kTiles = HD == 256 ? 1 : 2;
     static constexpr int kKeys = HD == 256 ? 64 : 128;
     static constexpr int kStage = kKeys * HD * 2;
-    static constexpr int kStages = HD == 64 ? 8 : HD == 128 ? 5 : 6;
+    static constexpr int kStages = HD == 64 ? 8 : 5;
     // Q of each tile; afterwards, and with 256 channels from the start, a place where each warp turns its rows round
-    static constexpr int kQBytes = kTiles * 128 * (HD == 256 ? 128 : HD) * 2;
+    static constexpr int kQBytes = kTiles * 128 * HD * 2;
     static constexpr int kSmem = kQBytes + kStages * kStage + 1024;   // + slack to align to 1024 bytes
     static constexpr int kThreads = kTiles * 128 + 128;   // softmax; copies, products and two idle warps
     // (two tiles: a launch of 384 threads x 168 registers; 2 x 128 x 208 + 128 x 80 are fewer)
@@ -119,6 +119,18 @@ struct Place {
     }
 };
 
+__device__ __forceinline__ void st_shared(unsigned at, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zeros(unsigned to, const void *from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(unsigned at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
 // two numbers in a register pair
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
     uint64_t r;
@@ -197,14 +209,18 @@ __device__ __forceinline__ bool find_item(const PromptArgs &a, int per, int numb
     int n[kItemLanes], row0[kItemLanes], rows[kItemLanes], most = 0;
 #pragma unroll
     for (int v = 0; v < kItemLanes; ++v) {
-        const int s = 32 * v + lane;
-        n[v] = s < S ? items_of(a, per, s, h, number, &row0[v], &rows[v]) : 0;
-        most = max(most, n[v]);
+        n[v] = 0;
+        if (32 * v < S) {                        // (the warp together)
+            const int s = min(32 * v + lane, S - 1), count = items_of(a, per, s, h, number, &row0[v], &rows[v]);
+            n[v] = 32 * v + lane < S ? count : 0;
+            most = max(most, n[v]);
+        }
     }
     const auto from = [&](int i) {               // items with an index of i or above
         int sum = 0;
 #pragma unroll
-        for (int v = 0; v < kItemLanes; ++v) sum += max(0, n[v] - i);
+        for (int v = 0; v < kItemLanes; ++v)
+            if (32 * v < S) sum += max(0, n[v] - i);
         return __reduce_add_sync(0xffffffffu, sum);
     };
     int lo = 0, hi = __reduce_max_sync(0xffffffffu, most);       // from(lo) > number >= from(hi)
@@ -217,9 +233,10 @@ __device__ __forceinline__ bool find_item(const PromptArgs &a, int per, int numb
     int left = number - from(hi);                // of the sequences that have an item of index lo, the left-th
 #pragma unroll
     for (int v = 0; v < kItemLanes; ++v) {
+        if (32 * v >= S || left < 0) break;
         const uint32_t has = __ballot_sync(0xffffffffu, n[v] > lo);
         const int count = __popc(has);
-        if (left >= 0 && left < count) {
+        if (left < count) {
             const uint32_t who = __ballot_sync(0xffffffffu, (has >> lane & 1u) && __popc(has & ((1u << lane) - 1u)) == left);
             const int from_lane = __ffs(who) - 1;
             item.row0 = __shfl_sync(0xffffffffu, row0[v], from_lane);
@@ -326,7 +343,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b_s[i], 1);               // S is complete: the MMA thread's commit
             mbar_init(&b_p[i], 128);             // P lies in tensor memory, and O may be added to
-            mbar_init(&b_o[i], 1);               // P V is added
+            mbar_init(&b_o[i], 1);               // P V is added: a tile's, or of every other tile of keys
         }
         for (int i = 0; i < 3; ++i) mbar_init(&b_meet[i], i ? 128 : kSoft);   // the threads of both tiles, of one
         mbar_init(&b_done, 1);                   // the MMA thread's last commit
@@ -375,7 +392,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                 };
                 if (lane == 0) {
                     init_pass(again);
-                    while (k < min(all, stages)) copy();
+                    copy();                        // (the others would stand in the queries' way)
                 }
                 __syncwarp();
                 begin_pass();
@@ -434,7 +451,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                             tc_fence_after();
                             if (elect_one()) {
                                 values(0, at, v.s, j - 1 > begin);
-                                tc_commit(&b_o[0]);
+                                tc_commit(&b_o[(j - 1 - begin) & 1]);
                                 tc_commit(&empty[v.s]);
                             }
                             v.go(2, stages);
@@ -493,58 +510,61 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
             const int tok = min(t0 + min(token_of(r), tokens - 1), n - 1), hi = tok + 1, lo = a.window ? max(0, tok - a.window + 1) : 0;
             const int full_lo = a.window ? max(0, min(t0 + tokens, n) - a.window) : 0;   // keys from here to t0 are seen by all rows
             const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
-            // A row of the tile in a buffer of packed rows, and whether it is one
-            const auto row_at = [&](int row, int64_t ld, bool &there) {
-                const int token = token_of(row), at = t0 + token;
-                there = row < tokens * g && at < n;
-                return (int64_t)(row0 + min(at, n - 1)) * ld + (h * g + min(row - token * g, g - 1)) * HD * 2;
-            };
             // Rows cross between memory, where a row's pieces of 16 bytes go by lanes beside each other, and tensor memory, where a lane
             // has a row, through the warp's part of the shared memory (pieces turned by the row's number)
-            constexpr int kPieces = HD == 64 ? 8 : 16, kRounds = HD / 8 / kPieces, kEach = 32 / (32 / kPieces);   // of a row in a round; rounds; rows a lane
-            uint8_t *turn = qs + (w * 4 + (warp & 3)) * 32 * kPieces * 16;
-            const auto turn_at = [&](int row, int piece) { return reinterpret_cast<uint4 *>(turn + (row * kPieces + (piece ^ (row & 7))) * 16); };
-            // Q, all of it asked for before the CTA's threads meet; rows of tokens behind the sequence's last one are zeros
-            constexpr int kCh = HD / 8;
-            uint4 u[kCh];
+            constexpr int kPieces = HD / 8;            // of a row
+            const unsigned q_at = saddr(qs), turn = q_at + (w * 4 + (warp & 3)) * 32 * kPieces * 16;
+            const auto turn_at = [&](int row, int piece) { return turn + (row * kPieces + (piece ^ (row & 7))) * 16; };
+            // The rows that a lane meets there, from the warp's first ones on, in a buffer of packed rows
+            constexpr int kRowStep = 32 / kPieces, kEach = kPieces;
+            const int step_t = kRowStep / g, step_h = kRowStep - step_t * g, tokens_here = min(tokens, n - t0);
+            struct Walk {
+                unsigned at;                           // bytes from the tile's first row on
+                int token, head;
+            };
+            const auto walk = [&](unsigned ld) {
+                int row = 32 * (warp & 3) + lane / kPieces;
+                asm volatile("" : "+r"(row));          // (each walk is to be made where it is used, not all of its places kept in registers)
+                const int token = token_of(row), head = row - token * g;
+                return Walk{token * ld + head * HD * 2 + lane % kPieces * 16, token, head};
+            };
+            const auto walk_on = [&](Walk &x, unsigned ld) {
+                x.at += step_t * ld + step_h * HD * 2, x.token += step_t, x.head += step_h;
+                if (x.head >= g) x.at += ld - g * HD * 2, ++x.token, x.head -= g;
+            };
+            const int64_t first = row0 + min(t0, n - 1), head0 = h * g * HD * 2;   // (a tile without tokens reads a row that is there, and writes none)
+            // Q, asked for before the CTA's threads meet; rows of tokens behind the sequence's last one are zeros
+            {
+                const uint8_t *from = a.q + first * a.ldq + head0;
+                Walk x = walk(unsigned(a.ldq));
 #pragma unroll
-            for (int i = 0; i < kCh; ++i) {
-                const int round = i / kEach, row = 32 * (warp & 3) + i % kEach * (32 / kPieces) + lane / kPieces;
-                bool there;
-                const int64_t at = row_at(row, a.ldq, there);
-                u[i] = *reinterpret_cast<const uint4 *>(a.q + at + (round * kPieces + lane % kPieces) * 16);
-                if (!there) u[i] = make_uint4(0, 0, 0, 0);
-            }
-            if constexpr (HD < 256) {
-#pragma unroll
-                for (int i = 0; i < kCh; ++i) {
-                    const int row = 32 * (warp & 3) + i * (32 / kPieces) + lane / kPieces, ch = lane % kPieces;
-                    *reinterpret_cast<uint4 *>(qs + (w * (HD / 64) + ch / 8) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = u[i];
+                for (int i = 0; i < kEach; ++i) {
+                    const bool there = x.token < tokens_here;
+                    const int row = i * kRowStep + lane / kPieces, ch = lane % kPieces, all = 32 * (warp & 3) + row;
+                    const unsigned to = HD == 256 ? turn_at(row, ch) : q_at + (w * (HD / 64) + ch / 8) * 16384 + all * 128 + (((ch & 7) ^ (all & 7)) << 4);
+                    cp_async16_or_zeros(to, from + (there ? x.at : 0u), there);
+                    walk_on(x, unsigned(a.ldq));
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             begin_pass();
             const uint32_t tmem = s_tmem, t_o = tmem + Sh::kO + w * HD + lanes;
+            cp_async_wait_all();
             if constexpr (HD == 256) {
+                __syncwarp();
 #pragma unroll
-                for (int round = 0; round < kRounds; ++round) {
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t v[32];
 #pragma unroll
-                    for (int i = 0; i < kEach; ++i) *turn_at(i * (32 / kPieces) + lane / kPieces, lane % kPieces) = u[round * kEach + i];
-                    __syncwarp();
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t v[32];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint4 p = *turn_at(lane, 8 * x + i);
-                            v[4 * i] = p.x, v[4 * i + 1] = p.y, v[4 * i + 2] = p.z, v[4 * i + 3] = p.w;
-                        }
-                        tc_st32(tmem + Sh::kQ + 64 * round + 32 * x + lanes, v);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 p = ld_shared(turn_at(lane, 8 * x + i));
+                        v[4 * i] = p.x, v[4 * i + 1] = p.y, v[4 * i + 2] = p.z, v[4 * i + 3] = p.w;
                     }
-                    __syncwarp();
+                    tc_st32(tmem + Sh::kQ + 32 * x + lanes, v);
                 }
                 tc_wait_st();
                 tc_fence_before();
+            } else {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             mbar_arrive(&b_q);
 
@@ -559,10 +579,14 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
             for (int j = rg.begin; j < rg.end; ++j) {
                 const int it = j - rg.begin, at = kTiles == 1 ? (j & 1) : w;
                 const int phase = kTiles == 1 ? (j - jb) >> 1 : it;
-                // (a wait names a phase by its parity, so none may be left out: P V of the tile before, or with S held twice
-                // of the one before that, has been added already and only has to be ticked off)
+                // A wait names a phase by its parity: it must not be possible that the next but one has begun, and none may be left out.
+                // With S held twice the sums of tile it - 1 may or may not be there, so they tick on two barriers in turn, of which one
+                // goes on only after the tile's own P; those of the tile before (or before that) are there already and are ticked off
                 constexpr int kAhead = kTiles == 1 ? 2 : 1;
-                ok = wait_for(&b_s[at], unsigned(phase) & 1u, &s_bad) && (it < kAhead || wait_for(&b_o[w], unsigned(it - kAhead) & 1u, &s_bad));
+                const auto added = [&](int i) {
+                    return kTiles == 1 ? wait_for(&b_o[i & 1], unsigned(i >> 1) & 1u, &s_bad) : wait_for(&b_o[w], unsigned(i) & 1u, &s_bad);
+                };
+                ok = wait_for(&b_s[at], unsigned(phase) & 1u, &s_bad) && (it < kAhead || added(it - kAhead));
                 if (!__all_sync(0xffffffffu, ok)) break;               // tcgen05.ld takes the whole warp
                 tc_fence_after();
                 uint32_t s[kKeys / 32][32];
@@ -590,15 +614,14 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                     for (int y = 0; y < 4; ++y)
                         m[y] = fmaxf(fmaxf(m[y], __uint_as_float(s[x / 32][x % 32 + y])), __uint_as_float(s[x / 32][x % 32 + y + 4]));
                 const float best = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-                const bool renew = (best - top) * c > 8.f;
+                // a row that has seen nothing yet has no sums that a new maximum would change
+                const bool renew = (best - top) * c > 8.f, scale = renew && top != -INFINITY;
                 float keep = 1.f;
-                if (renew) {
-                    keep = exp2_fast((top - best) * c);
-                    top = best;
-                }
-                if (__any_sync(0xffffffffu, renew) && it > 0) {
+                if (scale) keep = exp2_fast((top - best) * c);
+                if (renew) top = best;
+                if (__any_sync(0xffffffffu, scale)) {
                     if constexpr (kAhead == 2) {
-                        ok = wait_for(&b_o[w], unsigned(it - 1) & 1u, &s_bad);
+                        ok = added(it - 1);
                         if (!__all_sync(0xffffffffu, ok)) break;
                         tc_fence_after();
                     }
@@ -682,42 +705,43 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
             // ---- the sums, divided and rounded ----
             const int last = rg.end - rg.begin - 1;
             if (last >= 0) {
-                if (kTiles == 1 && ok && last > 0) ok = wait_for(&b_o[w], unsigned(last - 1) & 1u, &s_bad);
-                if (ok) ok = wait_for(&b_o[w], unsigned(last) & 1u, &s_bad);
+                if (ok) ok = kTiles == 1 ? wait_for(&b_o[last & 1], unsigned(last >> 1) & 1u, &s_bad) : wait_for(&b_o[w], unsigned(last) & 1u, &s_bad);
                 if (__all_sync(0xffffffffu, ok)) {
                     tc_fence_after();
                     const float part = 1.f / sum;
                     bool odd = false;
 #pragma unroll
-                    for (int round = 0; round < kRounds; ++round) {
+                    for (int x = 0; x < HD / 32; ++x) {
+                        uint32_t o[32];
+                        tc_ld32(t_o + 32 * x, o);
+                        const uint32_t gone = seen[x];
 #pragma unroll
-                        for (int x = 0; x < kPieces / 4; ++x) {
-                            uint32_t o[32];
-                            const int at = round * (kPieces / 4) + x;
-                            tc_ld32(t_o + 32 * at, o);
-                            const uint32_t gone = seen[at];
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                odd |= isnan(__uint_as_float(o[i]));
-                                o[i] = gone >> i & 1u ? 0x7FFFFFFFu : __float_as_uint(__uint_as_float(o[i]) * part);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                *turn_at(lane, 4 * x + i) = make_uint4(pack2<T>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
-                                                                       pack2<T>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
-                                                                       pack2<T>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
-                                                                       pack2<T>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
+                        for (int i = 0; i < 32; ++i) {
+                            odd |= isnan(__uint_as_float(o[i]));
+                            o[i] = gone >> i & 1u ? 0x7FFFFFFFu : __float_as_uint(__uint_as_float(o[i]) * part);
                         }
-                        __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < kEach; ++i) {
-                            const int row = i * (32 / kPieces) + lane / kPieces;
-                            bool there;
-                            const int64_t to = row_at(32 * (warp & 3) + row, a.ldo, there);
-                            if (there) *reinterpret_cast<uint4 *>(a.out + to + (round * kPieces + lane % kPieces) * 16) = *turn_at(row, lane % kPieces);
-                        }
-                        __syncwarp();
+                        for (int i = 0; i < 4; ++i)
+                            st_shared(turn_at(lane, 4 * x + i), make_uint4(pack2<T>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
+                                                                           pack2<T>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
+                                                                           pack2<T>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
+                                                                           pack2<T>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7]))));
                     }
+                    __syncwarp();
+                    uint8_t *rows = a.out + first * a.ldo + head0;
+                    Walk to = walk(unsigned(a.ldo));
+#pragma unroll
+                    for (int half = 0; half < kEach; half += 8) {
+                        uint4 v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = ld_shared(turn_at((half + i) * kRowStep + lane / kPieces, lane % kPieces));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (to.token < tokens_here) *reinterpret_cast<uint4 *>(rows + to.at) = v[i];
+                            walk_on(to, unsigned(a.ldo));
+                        }
+                    }
+                    __syncwarp();
                     if (live && odd && !isnan(sum)) s_again = 1;
                 }
             }
