@@ -11,7 +11,7 @@
 // of one group beside each other as the rows) as soon as they are there, and puts its weights P into shared memory;
 // after the tile's one barrier each warp adds P V for a quarter of the channels. So no score or sum is computed
 // twice, and at the end of a unit nothing but the weights' sums has to be joined. Weights are relative to a maximum
-// that all warps hold, renewed only when one of them meets a score that passes it by more than 8 powers of two (the
+// that all warps hold, renewed only when one of them meets a score that passes it by more than 16 powers of two (12, fp16; the
 // barrier says so, and the tile's weights are taken again). mma.sync and not tcgen05: with 16 rows a tile the
 // products are a small part of what even these units do while the keys arrive.
 #include <algorithm>
@@ -136,7 +136,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
     constexpr int kCh = HD / 8;                                  // 16-byte pieces of a row
     constexpr int kNt = kMine / 8;                               // tiles of 8 keys of a warp's scores
     constexpr int kN = HD / kWarps / 8;                          // tiles of 8 channels of a warp's sums
-    constexpr float kShift = std::is_same<T, __nv_bfloat16>::value ? 0.f : 6.f;   // fp16 weights are held times 2^6: lost below 2^-31
+    // fp16 weights are held times 2^kShift (what is lost lies 2^-28 below the largest); the maximum in use may fall behind by kBehind powers of two
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr float kShift = kBf16 ? 0.f : 3.f, kBehind = kBf16 ? 16.f : 12.f;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_sum[kWarps];
     __shared__ float s_row[kWarps][kRows];                       // maxima, and at the end the weights' sums
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
                     float m = fmaxf(sc[mt][0][2 * b], sc[mt][0][2 * b + 1]);
                     if constexpr (kNt == 2) m = fmaxf(m, fmaxf(sc[mt][1][2 * b], sc[mt][1][2 * b + 1]));
                     most[mt][b] = m;
-                    renew |= (m - top[mt][b]) * a.scale_log2 > 8.f;
+                    renew |= (m - top[mt][b]) * a.scale_log2 > kBehind;
                 }
             const auto weigh = [&] {                             // the tile's weights into shared memory
 #pragma unroll

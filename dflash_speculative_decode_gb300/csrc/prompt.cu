@@ -6,17 +6,17 @@
 // one tile. A CTA takes kTiles tiles that follow each other and walks over the keys they see, kKeys at a time:
 //     S = Q K^T (tensor memory), P = 2^(c S - m) rounded to the type (tensor memory, over S), O += P V
 // with c = scale * log2(e). A thread owns one row: it holds the row's maximum and sum and needs no other thread's
-// values. The maximum in use is renewed only where a tile's passes it by more than 8 powers of two; until then P
+// values. The maximum in use is renewed only where a tile's passes it by more than 16 powers of two (12, fp16); until then P
 // is larger than 1 and no sum changes scale, so O in tensor memory is seldom touched.
 //
 // P is rounded to the type of the values, as the tensor cores take their operands: a relative 2^-9 (bf16) or 2^-12
 // (fp16) of each weight at most, the size of the output's own rounding; the sum that divides is of the unrounded
-// weights, in fp32. fp16 weights are held times 2^6, so that what is lost below its smallest number lies 2^-31
+// weights, in fp32. fp16 weights are held times 2^3, so that what is lost below its smallest number lies 2^-28
 // below the largest weight.
 //
 // Masked places. A masked score is replaced, so what a key holds there shows nowhere. A masked weight is 0, and 0
 // times a value that is not finite would make NaN of rows that do not see it; that shows in the sums at the end
-// (a NaN sum where the weights' sum is none). Then the CTA does its tiles once more, taking what is not finite out
+// (one that is not finite where the weights' sum is). Then the CTA does its tiles once more, taking what is not finite out
 // of each tile of values before the product, and notes for each row which channels it saw such a value in. So a
 // prompt without such values pays nothing for them, and one with them pays a few times its price.
 #include <algorithm>
@@ -198,7 +198,8 @@ __device__ __forceinline__ int items_of(const PromptArgs &a, int per, int s, int
     return (e - b + per - 1) / per;
 }
 
-// Every warp for itself, up to 32 * kItemLanes sequences
+// Every warp for itself, up to 32 * LANES sequences
+template <int LANES>
 __device__ __forceinline__ bool find_item(const PromptArgs &a, int per, int number, int h, Item &item) {
     const int lane = threadIdx.x & 31, S = a.c.n_seq;
     if (S == 1) {
@@ -206,9 +207,9 @@ __device__ __forceinline__ bool find_item(const PromptArgs &a, int per, int numb
         item.at = n - 1 - number;
         return number < n;
     }
-    int n[kItemLanes], row0[kItemLanes], rows[kItemLanes], most = 0;
+    int n[LANES], row0[LANES], rows[LANES], most = 0;
 #pragma unroll
-    for (int v = 0; v < kItemLanes; ++v) {
+    for (int v = 0; v < LANES; ++v) {
         n[v] = 0;
         if (32 * v < S) {                        // (the warp together)
             const int s = min(32 * v + lane, S - 1), count = items_of(a, per, s, h, number, &row0[v], &rows[v]);
@@ -219,7 +220,7 @@ __device__ __forceinline__ bool find_item(const PromptArgs &a, int per, int numb
     const auto from = [&](int i) {               // items with an index of i or above
         int sum = 0;
 #pragma unroll
-        for (int v = 0; v < kItemLanes; ++v)
+        for (int v = 0; v < LANES; ++v)
             if (32 * v < S) sum += max(0, n[v] - i);
         return __reduce_add_sync(0xffffffffu, sum);
     };
@@ -232,7 +233,7 @@ __device__ __forceinline__ bool find_item(const PromptArgs &a, int per, int numb
     }
     int left = number - from(hi);                // of the sequences that have an item of index lo, the left-th
 #pragma unroll
-    for (int v = 0; v < kItemLanes; ++v) {
+    for (int v = 0; v < LANES; ++v) {
         if (32 * v >= S || left < 0) break;
         const uint32_t has = __ballot_sync(0xffffffffu, n[v] > lo);
         const int count = __popc(has);
@@ -300,11 +301,14 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tv) : "memory");
     }
     pdl_wait();
+    pdl_trigger();
 
     // ---- the CTA's item: tiles item * kTiles .. of a sequence ----
     Item item;
-    if (a.c.n_seq <= 32 * kItemLanes) {
-        if (!find_item(a, kTiles * tokens, number, h, item)) return;             // each warp by itself
+    if (a.c.n_seq <= 32) {
+        if (!find_item<1>(a, kTiles * tokens, number, h, item)) return;          // each warp by itself
+    } else if (a.c.n_seq <= 32 * kItemLanes) {
+        if (!find_item<kItemLanes>(a, kTiles * tokens, number, h, item)) return;
     } else {
         if (!find_item_wide<Sh::kThreads>(a, kTiles * tokens, number, h, s_sum, &s_item)) return;
         item = s_item;
@@ -568,7 +572,9 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
             }
             mbar_arrive(&b_q);
 
-            constexpr float kShift = std::is_same<T, __nv_bfloat16>::value ? 0.f : 6.f;
+            // fp16 weights are held times 2^kShift; the maximum in use may fall behind by kBehind powers of two
+            constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+            constexpr float kShift = kBf16 ? 0.f : 3.f, kBehind = kBf16 ? 16.f : 12.f;
             const float c = a.scale_log2;
             float top = -INFINITY, sum = 0.f;      // the maximum in use and the weights' sum
             uint32_t seen[HD / 32];                // channels in which the row saw a value that is not finite
@@ -615,7 +621,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                         m[y] = fmaxf(fmaxf(m[y], __uint_as_float(s[x / 32][x % 32 + y])), __uint_as_float(s[x / 32][x % 32 + y + 4]));
                 const float best = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
                 // a row that has seen nothing yet has no sums that a new maximum would change
-                const bool renew = (best - top) * c > 8.f, scale = renew && top != -INFINITY;
+                const bool renew = (best - top) * c > kBehind, scale = renew && top != -INFINITY;
                 float keep = 1.f;
                 if (scale) keep = exp2_fast((top - best) * c);
                 if (renew) top = best;
@@ -709,23 +715,25 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                 if (__all_sync(0xffffffffu, ok)) {
                     tc_fence_after();
                     const float part = 1.f / sum;
-                    bool odd = false;
+                    float odd = 0.f;                   // NaN where a sum is not finite
 #pragma unroll
                     for (int x = 0; x < HD / 32; ++x) {
                         uint32_t o[32];
                         tc_ld32(t_o + 32 * x, o);
-                        const uint32_t gone = seen[x];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            odd |= isnan(__uint_as_float(o[i]));
-                            o[i] = gone >> i & 1u ? 0x7FFFFFFFu : __float_as_uint(__uint_as_float(o[i]) * part);
+                        for (int i = 0; i < 32; ++i) odd = fmaf(__uint_as_float(o[i]), 0.f, odd);
+                        if (again) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (seen[x] >> i & 1u) o[i] = 0x7FFFFFFFu;
                         }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            st_shared(turn_at(lane, 4 * x + i), make_uint4(pack2<T>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
-                                                                           pack2<T>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
-                                                                           pack2<T>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
-                                                                           pack2<T>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7]))));
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t p[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) p[y] = pack2<T>(__uint_as_float(o[8 * i + 2 * y]) * part, __uint_as_float(o[8 * i + 2 * y + 1]) * part);
+                            st_shared(turn_at(lane, 4 * x + i), make_uint4(p[0], p[1], p[2], p[3]));
+                        }
                     }
                     __syncwarp();
                     uint8_t *rows = a.out + first * a.ldo + head0;
@@ -742,7 +750,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                         }
                     }
                     __syncwarp();
-                    if (live && odd && !isnan(sum)) s_again = 1;
+                    if (live && isnan(odd) && !isnan(sum)) s_again = 1;
                 }
             }
             if (end_pass(stages)) break;
