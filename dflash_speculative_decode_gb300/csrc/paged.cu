@@ -300,7 +300,7 @@ int dfl_paged_prompt(const dfl_paged *c, const void *q, int64_t ldq, int n_q, co
         (rc = pg_check_rows(c, out, ldo, n_q)))
         return rc;
     const int g = n_q / c->n_kv;
-    const PagedAttnArgs a{*c, q, k, v, out, ldq, ldk, ldv, ldo, n_q, g, rows, cu, nullptr, 0, window, 1, pg_shift(c), scale * kLog2e};
+    const PagedAttnArgs a{*c, q, k, v, out, ldq, ldk, ldv, ldo, n_q, g, rows, cu, nullptr, 0, window, 1, pg_shift(c), (4096 + g - 1) / g, scale * kLog2e};
     return launch_paged_prompt(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -321,7 +321,7 @@ int dfl_paged_attn(const dfl_paged *c, const void *q, int64_t ldq, int n_q, int 
     if (total == 0) return DFL_OK;
     if ((rc = pg_check_rows(c, q, ldq, n_q)) || (rc = pg_check_rows(c, out, ldo, n_q))) return rc;
     const int g = n_q / c->n_kv;
-    const PagedAttnArgs a{*c, q, nullptr, nullptr, out, ldq, 0, 0, ldo, n_q, g, total, cu, len, rows, window, causal != 0, pg_shift(c), scale * kLog2e};
+    const PagedAttnArgs a{*c, q, nullptr, nullptr, out, ldq, 0, 0, ldo, n_q, g, total, cu, len, rows, window, causal != 0, pg_shift(c), (4096 + g - 1) / g, scale * kLog2e};
     return launch_paged_attn(a, scratch, static_cast<cudaStream_t>(stream));
 }
 

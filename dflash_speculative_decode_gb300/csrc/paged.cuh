@@ -61,6 +61,7 @@ struct PagedAttnArgs {
     const int32_t *cu, *len;
     int rows, window, causal;
     int shift;                 // page = 1 << shift
+    int inverse;               // r / group is (r * inverse) >> 12 for r < 256
     float scale_log2;          // scale * log2(e): weights are powers of two
 };
 

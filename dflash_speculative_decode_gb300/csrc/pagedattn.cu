@@ -108,9 +108,14 @@ __device__ SeqWork seq_work(const PagedAttnArgs &a, int s, int *bits) {
     return w;
 }
 
-// The first granule of CTA i of n over `all`, and the CTA that has granule x
-__device__ __forceinline__ long long cut(long long all, int i, int n) { return all * i / n; }
-__device__ __forceinline__ int cta_at(long long x, long long all, int n) { return int(((x + 1) * n - 1) / all); }
+// The first granule of CTA i of n over `all`, and the CTA that has granule x (in 32 bits where they do: the divisions are on the way
+// to a call's first loads)
+__device__ __forceinline__ long long cut(long long all, int i, int n) {
+    return all <= 0xffffffffu / kMaxCtas ? (long long)(unsigned(all) * unsigned(i) / unsigned(n)) : all * i / n;
+}
+__device__ __forceinline__ int cta_at(long long x, long long all, int n) {
+    return all <= 0xffffffffu / kMaxCtas ? int((unsigned(x + 1) * unsigned(n) - 1u) / unsigned(all)) : int(((x + 1) * n - 1) / all);
+}
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -206,7 +211,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
             }
             sw = seq_work(a, s, &bits);
             const long long at = x - (long long)pre[s] * units;
-            u = int(at / sw.granules), g0 = int(at % sw.granules), g1 = int(min((long long)sw.granules, g0 + (end - x)));
+            u = at <= 0xffffffffu ? int(unsigned(at) / unsigned(sw.granules)) : int(at / sw.granules);
+            g0 = int(at - (long long)u * sw.granules), g1 = int(min((long long)sw.granules, g0 + (end - x)));
             x += g1 - g0;
         }
         const int h = u / w.chunks, first = u % w.chunks * kRows, live = min(kRows, sw.n * g - first);
@@ -246,15 +252,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         __syncthreads();                                         // the memory of the piece before is free
+        // queries, with the first tile's copies; rows behind the last one are zeros
+#pragma unroll
+        for (int i = 0; i < kRows * kCh / kThreads; ++i) {
+            const int at = i * kThreads + t, r = at / kCh, ch = at % kCh, p = first + min(r, live - 1), token = p * a.inverse >> 12;
+            cp16(q_at + r * HD * 2 + ((ch ^ (r & 7)) << 4), static_cast<const T *>(a.q) + (int64_t)(row0 + token) * a.ldq + (h * g + p - token * g) * HD + ch * 8, r < live);
+        }
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) fetch(i);
-        // queries: rows behind the last one are zeros
-        for (int i = t; i < kRows * kCh; i += kThreads) {
-            const int r = i / kCh, ch = i % kCh, p = first + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < live) v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (int64_t)(row0 + p / g) * a.ldq + (h * g + p % g) * HD + ch * 8);
-            *reinterpret_cast<uint4 *>(qs + r * HD * 2 + ((ch ^ (r & 7)) << 4)) = v;
-        }
+        cp_wait<kStages - 2>();
         __syncthreads();
         const auto q_tile = [&](int mt, int ks) {                // a lane's row address of a 16 x 16 tile of queries
             const int r = mt * 16 + lane % 16, ch = 2 * ks + lane / 16;
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int p = first + min(mt * 16 + lane / 4 + 8 * b, live - 1), pos = sw.len + p / g;
+                const int p = first + min(mt * 16 + lane / 4 + 8 * b, live - 1), pos = sw.len + (p * a.inverse >> 12);
                 hi[mt][b] = (a.causal ? pos + 1 : sw.hi) - base;
                 lo[mt][b] = (!a.window ? 0 : max(0, a.causal ? pos - a.window + 1 : sw.len - a.window)) - base;
             }
@@ -475,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
                 const float l = (s_row[0][r] + s_row[1][r]) + (s_row[2][r] + s_row[3][r]);
                 if (whole) {
                     const float d = 1.f / l;
-                    const int p = first + r;
-                    T *to = static_cast<T *>(a.out) + (int64_t)(row0 + p / g) * a.ldo + (h * g + p % g) * HD + warp * kN * 8 + 2 * (lane % 4);
+                    const int p = first + r, token = p * a.inverse >> 12;
+                    T *to = static_cast<T *>(a.out) + (int64_t)(row0 + token) * a.ldo + (h * g + p - token * g) * HD + warp * kN * 8 + 2 * (lane % 4);
 #pragma unroll
                     for (int y = 0; y < kN; ++y) *reinterpret_cast<uint32_t *>(to + 8 * y) = pack2<T>(o[mt][y][2 * b] * d, o[mt][y][2 * b + 1] * d);
                 } else {

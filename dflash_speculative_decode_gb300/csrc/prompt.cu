@@ -785,7 +785,7 @@ int launch_prompt(const PagedAttnArgs &a, cudaStream_t s) {
     }
     CUtensorMap tk, tv;
     if (!rows_map(&tk, a.c, a.k, a.ldk, a.total, Sh::kKeys) || !rows_map(&tv, a.c, a.v, a.ldv, a.total, Sh::kKeys)) return DFL_E_CUDA;
-    const PromptArgs p{a.c, static_cast<const uint8_t *>(a.q), static_cast<uint8_t *>(a.out), a.ldq * 2, a.ldo * 2, a.group, (4096 + a.group - 1) / a.group, a.total, a.window, a.cu,
+    const PromptArgs p{a.c, static_cast<const uint8_t *>(a.q), static_cast<uint8_t *>(a.out), a.ldq * 2, a.ldo * 2, a.group, a.inverse, a.total, a.window, a.cu,
                        a.scale_log2};
     const int per = Sh::kTiles * (128 / a.group);                // tokens of an item
     const int64_t items = (int64_t)a.total / per + std::min(a.c.n_seq, a.total);
