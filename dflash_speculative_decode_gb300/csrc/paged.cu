@@ -272,6 +272,17 @@ int dfl_paged_plan(const dfl_paged *c, const int32_t *len, const int32_t *cnt, i
     const void *p[] = {len, cnt, cu, slots};
     for (const void *q : p)
         if (!pg_aligned(q, 4)) return DFL_E_INVALID_ARG;
+    // what is written shares memory with nothing else
+    const struct {
+        const void *p;
+        int64_t bytes;
+    } all[] = {{cu, (c->n_seq + 1) * 4ll}, {slots, rows * 4ll}, {len, c->n_seq * 4ll}, {cnt, c->n_seq * 4ll}, {c->held, c->n_seq * 4ll},
+               {c->table, (int64_t)c->n_seq * c->max_pages * 4}, {c->ring, c->n_pages * 4ll}, {c->queue, 16}};
+    for (int i = 0; i < 2; ++i)
+        for (int j = i + 1; j < 8; ++j)
+            if (pg_overlap(all[i].p, all[i].bytes, all[j].p, all[j].bytes)) return DFL_E_INVALID_ARG;
+    for (int i = 4; i < 8; ++i)
+        if (pg_overlap(len, all[2].bytes, all[i].p, all[i].bytes) || pg_overlap(cnt, all[3].bytes, all[i].p, all[i].bytes)) return DFL_E_INVALID_ARG;
     const PlanArgs a{*c, len, cnt, cu, slots, rows, pg_shift(c)};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return c->n_seq <= kPlanThreads ? launch_plan<1>(a, s) : launch_plan<kPlanEach>(a, s);
@@ -284,6 +295,9 @@ int dfl_paged_append(const dfl_paged *c, const int32_t *slots, int rows, const v
     if (rows == 0) return DFL_OK;
     if (rows < 0 || !slots || !pg_aligned(slots, 4)) return DFL_E_INVALID_ARG;
     if ((rc = pg_check_rows(c, k, ldk, c->n_kv)) || (rc = pg_check_rows(c, v, ldv, c->n_kv))) return rc;
+    const int64_t w = (int64_t)c->n_kv * c->head_dim, pool = (int64_t)c->n_pages * c->page * w * 2;
+    for (const void *p : {static_cast<const void *>(c->k), static_cast<const void *>(c->v)})
+        if (pg_overlap(p, pool, k, ((rows - 1) * ldk + w) * 2) || pg_overlap(p, pool, v, ((rows - 1) * ldv + w) * 2)) return DFL_E_INVALID_ARG;
     const AppendArgs a{*c, slots, rows, static_cast<const uint8_t *>(k), static_cast<const uint8_t *>(v), ldk * 2, ldv * 2};
     const int64_t blocks = ((int64_t)rows * c->n_kv * (c->head_dim / 8) + 255) / 256;
     if (blocks > INT32_MAX) return DFL_E_UNSUPPORTED;
@@ -299,6 +313,10 @@ int dfl_paged_prompt(const dfl_paged *c, const void *q, int64_t ldq, int n_q, co
     if ((rc = pg_check_rows(c, q, ldq, n_q)) || (rc = pg_check_rows(c, k, ldk, c->n_kv)) || (rc = pg_check_rows(c, v, ldv, c->n_kv)) ||
         (rc = pg_check_rows(c, out, ldo, n_q)))
         return rc;
+    const int64_t wq = (int64_t)n_q * c->head_dim, wk = (int64_t)c->n_kv * c->head_dim;
+    if (pg_rows_overlap(out, ldo, wq, q, ldq, wq, rows) || pg_rows_overlap(out, ldo, wq, k, ldk, wk, rows) ||
+        pg_rows_overlap(out, ldo, wq, v, ldv, wk, rows))
+        return DFL_E_INVALID_ARG;
     const int g = n_q / c->n_kv;
     const PagedAttnArgs a{*c, q, k, v, out, ldq, ldk, ldv, ldo, n_q, g, rows, cu, nullptr, 0, window, 1, pg_shift(c), (4096 + g - 1) / g, scale * kLog2e};
     return launch_paged_prompt(a, static_cast<cudaStream_t>(stream));
@@ -320,6 +338,8 @@ int dfl_paged_attn(const dfl_paged *c, const void *q, int64_t ldq, int n_q, int 
     if (!scratch || !pg_aligned(scratch, 256) || (int64_t)scratch_bytes < dfl_paged_attn_scratch_bytes(c, n_q, rows)) return DFL_E_INVALID_ARG;
     if (total == 0) return DFL_OK;
     if ((rc = pg_check_rows(c, q, ldq, n_q)) || (rc = pg_check_rows(c, out, ldo, n_q))) return rc;
+    const int64_t wq = (int64_t)n_q * c->head_dim, pool = (int64_t)c->n_pages * c->page * c->n_kv * c->head_dim * 2, all = ((total - 1) * ldo + wq) * 2;
+    if (pg_rows_overlap(out, ldo, wq, q, ldq, wq, total) || pg_overlap(out, all, c->k, pool) || pg_overlap(out, all, c->v, pool)) return DFL_E_INVALID_ARG;
     const int g = n_q / c->n_kv;
     const PagedAttnArgs a{*c, q, nullptr, nullptr, out, ldq, 0, 0, ldo, n_q, g, total, cu, len, rows, window, causal != 0, pg_shift(c), (4096 + g - 1) / g, scale * kLog2e};
     return launch_paged_attn(a, scratch, static_cast<cudaStream_t>(stream));

@@ -34,6 +34,20 @@ inline int pg_check_rows(const dfl_paged *c, const void *p, int64_t ld, int head
     return ld <= kPgMaxLd ? DFL_OK : DFL_E_UNSUPPORTED;
 }
 
+// Whether two ranges of bytes, or two sets of rows [n][width] of 16-bit numbers, share memory. Rows the same distance apart may lie in
+// the gaps between each other; others are taken for overlapping where their whole ranges do.
+inline bool pg_overlap(const void *p, int64_t n, const void *q, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return p && q && n && m && x < y + uintptr_t(m) && y < x + uintptr_t(n);
+}
+inline bool pg_rows_overlap(const void *p, int64_t ldp, int64_t wp, const void *q, int64_t ldq, int64_t wq, int64_t n) {
+    if (!pg_overlap(p, ((n - 1) * ldp + wp) * 2, q, ((n - 1) * ldq + wq) * 2)) return false;
+    if (ldp != ldq) return true;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    const int64_t off = int64_t((x < y ? y - x : x - y) / 2) % ldp;              // of the later one's rows in the earlier one's
+    return off < (x < y ? wp : wq) || off + (x < y ? wq : wp) > ldp;
+}
+
 inline int pg_check_heads(const dfl_paged *c, int n_q, int window, float scale) {
     if (n_q < 1 || n_q % c->n_kv || window < 0 || !(scale > 0) || !std::isfinite(scale * 1.5f)) return DFL_E_INVALID_ARG;
     return n_q / c->n_kv > kPgMaxGroup ? DFL_E_UNSUPPORTED : DFL_OK;

@@ -301,6 +301,96 @@ def test_keys_and_queries_that_are_not_finite(torch, heads):
         near(got, want, tol)
 
 
+def some_rows(p, rows, got, first=0):
+    """Rows of the first sequence, alone against the definition."""
+    for m in rows:
+        want, tol = attend(p.q64[m:m + 1], p.k64[:m + 1], p.v64[:m + 1], m, p.window, True, p.scale, BITS[p.t])
+        near(got[m:m + 1], want, tol)
+
+
+@pytest.mark.parametrize("heads,n,window", [((12, 1, 256), 9000, 0), ((12, 2, 256), 6000, 512), ((4, 2, 64), 12000, 0), ((8, 4, 128), 10000, 0), ((16, 8, 128), 8000, 700)])
+def test_prompts_of_many_items(torch, heads, n, window):
+    """Many items a CTA and long rows of keys: some rows of each, several times over."""
+    p = Prompts(torch, heads, [n], "bf16", window, seed=n)
+    got = p.run()
+    some_rows(p, [0, 1, 9, 10, 63, 64, 127, 128, 129, 1000, 2047, n // 2, n - 130, n - 65, n - 2, n - 1], got)
+    for _ in range(6):
+        np.testing.assert_array_equal(got, p.run())
+
+
+@pytest.mark.parametrize("n_seq", [33, 256, 257, 900, 4096])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (2, 1, 128), (12, 1, 256)])
+def test_prompts_of_many_sequences(torch, n_seq, heads):
+    rng = np.random.default_rng(n_seq)
+    lens = [int(x) for x in rng.integers(0, 4 if n_seq > 300 else 12, n_seq)]
+    lens[n_seq // 2], lens[-1] = 150, 0
+    Prompts(torch, heads, lens, "fp16", 0 if n_seq % 2 else 3, seed=n_seq).check()
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (2, 2, 128), (12, 1, 256)])
+@pytest.mark.parametrize("window", [0, 130])
+def test_values_that_are_not_finite_in_long_prompts(torch, heads, window):
+    """Found in the middle of long rows of keys, of which some of a tile's rows see them and others do not."""
+    p = Prompts(torch, heads, [1100, 300], "bf16", window, seed=7)
+    for row, ch in ((500, 0), (501, 33), (777, 63), (1099, 8), (1100, 9), (1399, 10)):
+        p.put("v", row, float("inf") if row % 2 else float("nan"), ch)
+    want, tol = p.want()
+    got, g = p.run(), p.n_q // p.n_kv
+    sees = np.zeros(got.shape, bool)
+    for row, ch in ((500, 0), (501, 33), (777, 63), (1099, 8), (1100, 9), (1399, 10)):
+        sees[row:min(row + (window or 10 ** 6), 1100 if row < 1100 else 1400), :g, ch] = True
+    assert not np.isfinite(got[sees]).any()
+    near(np.where(sees, 0, got), np.where(sees, 0, want), np.where(sees, 0, tol))
+
+
+@pytest.mark.parametrize("value", [2.0 ** 90, -2.0 ** 90])
+def test_large_values(torch, value):
+    """Sums stay finite, also where the maximum in use falls behind."""
+    p = Prompts(torch, (4, 2, 64), [400], "bf16", seed=3)
+    ramp = torch.linspace(-10, 10, p.total, device="cuda")[:, None, None]
+    p.q.fill_(1.0), p.k.copy_((ramp / (64 * p.scale)).expand(-1, 2, 64)), p.v.fill_(value)
+    p.q64, p.k64, p.v64 = back(p.q), back(p.k), back(p.v)
+    p.check()
+    a = Pages(torch, (4, 2, 64), [400], [3], 16, "bf16", seed=3)
+    a.c.v.fill_(value), a.v64[0].fill(float(value))
+    a.check(3)
+
+
+def test_rows_in_the_gaps_of_a_wide_buffer(torch):
+    """Queries, keys, values and outputs as parts of one buffer's rows."""
+    p = Prompts(torch, (4, 2, 64), [70, 20], "fp16", seed=5)
+    wide = torch.zeros(p.total, 12 * 64, dtype=p.q.dtype, device="cuda")
+    q, k, v, out = (wide[:, a * 64:b * 64].view(p.total, b - a, 64) for a, b in ((8, 12), (4, 6), (6, 8), (0, 4)))
+    for x, y in ((q, p.q), (k, p.k), (v, p.v)):
+        x.copy_(y)
+    out.fill_(-77.0)
+    p.c.prompt(q, k, v, i32(torch, p.cu), out=out)
+    want, tol = p.want()
+    near(back(out), want, tol)
+    from dflash_speculative_decode_gb300 import DflError
+    with pytest.raises(DflError):
+        p.c.prompt(q, k, v, i32(torch, p.cu), out=q)
+
+
+def test_rows_far_apart(torch):
+    """Offsets that pass 32 bits: rows of 160 KiB, some 5 GiB of them."""
+    p = Prompts(torch, (4, 2, 64), [32000, 200], "bf16", seed=6)
+    wide = torch.empty(p.total, 80 * 1024, dtype=p.q.dtype, device="cuda")
+    n = p.total
+    q, k, v, out = (wide[:, a * 64:b * 64].view(n, b - a, 64) for a, b in ((0, 4), (6, 8), (1000, 1002), (1100, 1104)))
+    for x, y in ((q, p.q), (k, p.k), (v, p.v)):
+        x.copy_(y)
+    out.fill_(-77.0)
+    p.c.prompt(q, k, v, i32(torch, p.cu), window=300, out=out)
+    p.c.status()
+    got, p.window = back(out), 300
+    some_rows(p, [0, 5000, 27000, 31999], got)
+    a, b = 32000, 32200
+    want, tol = attend(p.q64[a:b], p.k64[a:b], p.v64[a:b], 0, 300, True, p.scale, BITS["bf16"])
+    near(got[a:b], want, tol)
+    assert (got[b:] == -77).all()
+
+
 def test_every_value_nan(torch):
     p = Prompts(torch, (4, 2, 128), [700], "bf16")
     p.v[:700].fill_(float("nan"))
@@ -562,6 +652,31 @@ def test_rows_over_pages_out_of_order_are_reported(torch, cu):
     assert (got[~good] == -77).all() and np.isfinite(got).all()
     with pytest.raises(RuntimeError, match="DFL_E_INVALID_ARG"):
         p.c.status()
+
+
+@pytest.mark.parametrize("n_seq,most", [(3000, 40), (4096, 3), (700, 300)])
+def test_attention_of_very_many_sequences(torch, n_seq, most):
+    rng = np.random.default_rng(n_seq)
+    Pages(torch, (4, 2, 64), rng.integers(0, most, n_seq), rng.integers(0, 2, n_seq), 16, "bf16").check(1)
+
+
+def test_pages_far_into_the_pool(torch):
+    """A pool of more than 4 GiB each of keys and values, whose last pages are in use."""
+    p = Pages(torch, (8, 8, 256), [300, 20], [2, 1], 128, "bf16", seed=9)
+    big = cache(torch, 2, 8, 256, 1, p.c.max_pages, 128)
+    from dflash_speculative_decode_gb300 import PagedCache
+    N, n = 9000, p.c.n_pages
+    k, v = (torch.empty(N, 8, 128, 256, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.where(p.c.table < n, p.c.table + (N - n), p.c.table)
+    c = PagedCache(k, v, table.contiguous(), p.c.held, torch.zeros(N, dtype=torch.int32, device="cuda"), big.queue)
+    rows = torch.arange(n * 128, device="cuda")
+    for x, y in ((k, p.c.k), (v, p.c.v)):
+        x[:N - n].fill_(float("nan"))
+    flat = [y.transpose(1, 2).reshape(n * 128, 8, 256) for y in (p.c.k, p.c.v)]
+    c.append(*flat, ((N - n) * 128 + rows).to(torch.int32))
+    assert torch.equal(k[N - n:].view(torch.int16), p.c.k.view(torch.int16)) and torch.equal(v[N - n:].view(torch.int16), p.c.v.view(torch.int16))
+    p.c = c
+    p.check(2)
 
 
 def test_the_same_bits_each_time(torch):

@@ -7,11 +7,12 @@ import pytest
 from dflash_speculative_decode_gb300 import _abi
 from paged_plain import Plan, attend
 
-A = 1 << 20          # an aligned address that nothing reads
+A = 1 << 20          # aligned addresses that nothing reads, far enough apart
+B = [A * (i + 2) for i in range(12)]
 
 
 def cache(**change):
-    f = dict(n_seq=2, n_kv=2, head_dim=64, page=32, n_pages=8, max_pages=4, type=0, k=A, v=A, table=A, held=A, ring=A, queue=A, err=A)
+    f = dict(n_seq=2, n_kv=2, head_dim=64, page=32, n_pages=8, max_pages=4, type=0, k=B[0], v=B[1], table=B[2], held=B[3], ring=B[4], queue=B[5], err=B[6])
     f.update(change)
     return _abi.dfl_paged(**f)
 
@@ -21,13 +22,13 @@ def calls(c, L):
     r = ctypes.byref(c)
     return {
         "init": lambda **k: L.dfl_paged_init(r, None),
-        "plan": lambda **k: L.dfl_paged_plan(r, k.get("len", A), k.get("cnt", A), k.get("cu", A), k.get("slots", A), k.get("rows", 4), None),
+        "plan": lambda **k: L.dfl_paged_plan(r, k.get("len", A), k.get("cnt", A), k.get("cu", B[7]), k.get("slots", B[8]), k.get("rows", 4), None),
         "append": lambda **k: L.dfl_paged_append(r, k.get("slots", A), k.get("rows", 4), k.get("k", A), k.get("ldk", 128), k.get("v", A), k.get("ldv", 128), None),
         "prompt": lambda **k: L.dfl_paged_prompt(r, k.get("q", A), k.get("ldq", 256), k.get("n_q", 4), k.get("k", A), k.get("ldk", 128), k.get("v", A),
                                                  k.get("ldv", 128), k.get("cu", A), k.get("rows", 4), k.get("window", 0), k.get("scale", 0.125),
-                                                 k.get("out", A), k.get("ldo", 256), None),
+                                                 k.get("out", B[9]), k.get("ldo", 256), None),
         "attn": lambda **k: L.dfl_paged_attn(r, k.get("q", A), k.get("ldq", 256), k.get("n_q", 4), k.get("total", 4), k.get("cu", A), k.get("len", A),
-                                             k.get("rows", 4), k.get("window", 0), 1, k.get("scale", 0.125), k.get("out", A), k.get("ldo", 256),
+                                             k.get("rows", 4), k.get("window", 0), 1, k.get("scale", 0.125), k.get("out", B[9]), k.get("ldo", 256),
                                              k.get("scratch", A), k.get("bytes", 1 << 40), None),
     }
 
@@ -63,6 +64,17 @@ def test_a_bad_cache_is_refused_by_every_call(change, code):
     ("attn", dict(scratch=A + 16), -1), ("attn", dict(bytes=0), -1)])
 def test_bad_arguments_are_refused(name, args, code):
     assert calls(cache(), _abi.lib())[name](**args) == code
+
+
+@pytest.mark.parametrize("name,args", [
+    ("plan", dict(cu=A)), ("plan", dict(slots=A + 4)), ("plan", dict(cu=B[7], slots=B[7] + 8)), ("plan", dict(len=B[3])), ("plan", dict(cnt=B[2] + 28)),
+    ("plan", dict(cu=B[4] + 28)), ("plan", dict(slots=B[5] + 12)), ("plan", dict(slots=B[2] - 12)),
+    ("append", dict(k=B[0] + 64)), ("append", dict(v=B[1] - 16)), ("append", dict(k=B[1])),
+    ("prompt", dict(out=A)), ("prompt", dict(q=B[9])), ("prompt", dict(k=B[9] + 1536)), ("prompt", dict(v=B[9] - 768)), ("prompt", dict(q=B[9] + 16, ldq=512, ldo=512)),
+    ("prompt", dict(q=B[9] + 512 + 16, ldq=512, ldo=512)), ("prompt", dict(k=B[9] + 512, ldk=520, ldo=512)),
+    ("attn", dict(q=B[9])), ("attn", dict(out=A + 1024)), ("attn", dict(out=B[0] + 64)), ("attn", dict(out=B[1] - 1024)), ("attn", dict(q=B[9] - 16, ldq=512, ldo=512))])
+def test_outputs_that_lie_in_something_else_are_refused(name, args):
+    assert calls(cache(), _abi.lib())[name](**args) == -1
 
 
 def test_calls_of_no_rows_do_nothing():
