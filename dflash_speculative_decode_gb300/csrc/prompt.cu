@@ -43,7 +43,7 @@ struct PromptShape {
     // tensor memory columns
     static constexpr int kS = 0, kSPitch = kKeys;                      // two of them: a tile's each, or two in turn
     static constexpr int kO = 256;
-    [[maybe_unused]] static constexpr int kQ = 128;                                     // (256 channels alone)
+    static constexpr int kQ = 128;                                     // (256 channels alone)
 };
 
 struct PromptArgs {
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
     using Sh = PromptShape<HD>;
     constexpr int kTiles = Sh::kTiles, kKeys = Sh::kKeys, kSoft = kTiles * 128, kMaxStages = Sh::kStages;
     extern __shared__ uint8_t prompt_smem_raw[];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], b_q, b_s[2], b_p[2], b_o[2], b_meet[3], b_done;
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], b_q, b_s[2], b_p[2], b_h[2], b_o[2], b_meet[3], b_done;
     __shared__ uint32_t s_tmem, s_odd[3][kKeys / 32];
     __shared__ int s_issued, s_again, s_sum[Sh::kThreads / 32];
     __shared__ Item s_item;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
     const auto init_pass = [&](int again) {      // by the thread that copies: its first copies need not wait for the others
         if (again) {
             for (int i = 0; i < kMaxStages; ++i) mbar_inval(&full[i]), mbar_inval(&empty[i]);
-            for (int i = 0; i < 2; ++i) mbar_inval(&b_s[i]), mbar_inval(&b_p[i]), mbar_inval(&b_o[i]);
+            for (int i = 0; i < 2; ++i) mbar_inval(&b_s[i]), mbar_inval(&b_p[i]), mbar_inval(&b_h[i]), mbar_inval(&b_o[i]);
             for (int i = 0; i < 3; ++i) mbar_inval(&b_meet[i]);
             mbar_inval(&b_q), mbar_inval(&b_done);
         }
@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
         mbar_init(&b_q, kSoft);                  // Q lies where the products read it
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b_s[i], 1);               // S is complete: the MMA thread's commit
-            mbar_init(&b_p[i], 128);             // P lies in tensor memory, and O may be added to
+            mbar_init(&b_h[i], 128);             // two tiles: the first half of P lies in tensor memory, and O may be added to
+            mbar_init(&b_p[i], 128);             // all of it does
             mbar_init(&b_o[i], 1);               // P V is added: a tile's, or of every other tile of keys
         }
         for (int i = 0; i < 3; ++i) mbar_init(&b_meet[i], i ? 128 : kSoft);   // the threads of both tiles, of one
@@ -424,11 +425,15 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                         else mma_ss(d, q + uint64_t((i / 4) * (16384 >> 4) + 2 * (i % 4)), bi, id_s, i > 0);
                     }
                 };
-                const auto values = [&](int w, int at, int stage, bool add) {
+                const auto values = [&](int w, int at, int stage, bool add, int half) {      // of the tile's keys the first or second half
+
                     const uint64_t b = v_desc + uint64_t(stage * (Sh::kStage >> 4));
                     const uint32_t d = tm + Sh::kO + w * HD, p = tm + Sh::kS + at * Sh::kSPitch;
 #pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i) mma_ts(d, p + 8 * i, b + uint64_t(i * (2048 >> 4)), id_o, add || i > 0);
+                    for (int y = 0; y < kKeys / 32; ++y) {
+                        const int i = half * (kKeys / 32) + y;
+                        mma_ts(d, p + 8 * i, b + uint64_t(i * (2048 >> 4)), id_o, add || i > 0);
+                    }
                 };
                 const auto over = [&](uint64_t *b, unsigned parity) { return __all_sync(0xffffffffu, wait_for(b, parity, &s_bad)) != 0; };
                 bool ok = over(&b_q, 0u);
@@ -454,7 +459,8 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                             p_phase[at] ^= 1u;
                             tc_fence_after();
                             if (elect_one()) {
-                                values(0, at, v.s, j - 1 > begin);
+                                values(0, at, v.s, j - 1 > begin, 0);
+                                values(0, at, v.s, true, 1);
                                 tc_commit(&b_o[(j - 1 - begin) & 1]);
                                 tc_commit(&empty[v.s]);
                             }
@@ -467,8 +473,11 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                             const KeyRange r = rs[w];
                             const bool adds = j - 1 >= r.begin && j - 1 < r.end, takes = j >= r.begin && j < r.end;
                             if (adds) {
-                                if (!(ok = (has_v || over(&full[v.s], v.phase)) && over(&b_p[w], p_phase[w]))) break;
+                                if (!(ok = (has_v || over(&full[v.s], v.phase)) && over(&b_h[w], p_phase[w]))) break;
                                 has_v = true;
+                                tc_fence_after();
+                                if (elect_one()) values(w, w, v.s, j - 1 > r.begin, 0);
+                                if (!(ok = over(&b_p[w], p_phase[w]))) break;
                                 p_phase[w] ^= 1u;
                             }
                             if (takes) {
@@ -478,7 +487,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                             tc_fence_after();
                             if (elect_one()) {
                                 if (adds) {
-                                    values(w, w, v.s, j - 1 > r.begin);
+                                    values(w, w, v.s, true, 1);
                                     tc_commit(&b_o[w]);
                                 }
                                 if (w == 1 && j > begin) tc_commit(&empty[v.s]);
@@ -644,18 +653,27 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                 const uint64_t c2 = pair(__float_as_uint(c), __float_as_uint(c)), off2 = pair(__float_as_uint(off), __float_as_uint(off));
                 uint64_t add[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int x = 0; x < kKeys / 64; ++x) {
-                    uint32_t p[32];
+                for (int x = 0; x < 2; ++x) {              // half of the keys: with two tiles their products need not wait for the others
+                    uint32_t p[kKeys / 4];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int k = 64 * x + 2 * i;
+                    for (int i = 0; i < kKeys / 4; ++i) {
+                        const int k = x * (kKeys / 2) + 2 * i;
                         float p0, p1;
                         halves(fma2(pair(s[k / 32][k % 32], s[k / 32][k % 32 + 1]), c2, off2), p0, p1);
                         p0 = exp2_fast(p0), p1 = exp2_fast(p1);
                         add[i & 3] = add2(add[i & 3], pair(__float_as_uint(p0), __float_as_uint(p1)));
                         p[i] = pack2<T>(p0, p1);
                     }
-                    tc_st32(t_s + 32 * x, p);
+                    if constexpr (kTiles == 2) {
+                        tc_st32(t_s + 32 * x, p);
+                        if (x == 0 && !again) {
+                            tc_wait_st();
+                            tc_fence_before();
+                            mbar_arrive(&b_h[at]);
+                        }
+                    } else {
+                        tc_st16(t_s + 16 * x, p);
+                    }
                 }
                 float a0, a1;
                 halves(add2(add2(add[0], add[1]), add2(add[2], add[3])), a0, a1);
@@ -706,6 +724,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                 }
                 tc_wait_st();
                 tc_fence_before();
+                if (kTiles == 2 && again) mbar_arrive(&b_h[at]);
                 mbar_arrive(&b_p[at]);
             }
             // ---- the sums, divided and rounded ----
