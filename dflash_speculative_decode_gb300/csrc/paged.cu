@@ -13,8 +13,9 @@ namespace {
 // lengths and scans them itself, so that one launch of many CTAs can share the writing: slots, table entries
 // and ring places of a plan follow from the state before it alone. Pages taken that the ring did not hold yet
 // are those given back in this call, found by the sums. The CTA that comes last writes what all read.
-constexpr int kPlanThreads = 256;
-constexpr int kPlanEach = DFL_PAGED_MAX_SEQ / kPlanThreads;
+// THREADS: 512 where there are many rows to write (328 thousand of 512 sequences in 9.4 us, 11.2 with 256), 256 where
+// the call is short (64 sequences in 5.0 us, 5.8 with 512).
+constexpr int kPlanMany = 32768;
 
 struct PlanArgs {
     dfl_paged c;
@@ -24,9 +25,10 @@ struct PlanArgs {
 };
 
 // Sums over the CTA's threads of two numbers, up to each thread's own; *all gets the whole ones'.
+template <int THREADS>
 __device__ longlong2 plan_scan(longlong2 v, longlong2 *red, longlong2 *all) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    constexpr int kW = kPlanThreads / 32;
+    constexpr int kW = THREADS / 32;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
@@ -56,10 +58,10 @@ __device__ __forceinline__ int plan_find(const int *sum, int n, int x) {
     return lo;
 }
 
-template <int EACH>            // sequences of a thread at most
-__global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
+template <int THREADS, int EACH>               // EACH: sequences of a thread at most
+__global__ void __launch_bounds__(THREADS) k_paged_plan(PlanArgs a) {
     extern __shared__ int plan_smem[];
-    __shared__ longlong2 red[2][kPlanThreads / 32];
+    __shared__ longlong2 red[2][THREADS / 32];
     __shared__ int s_bits, s_used, s_last;
     const dfl_paged &c = a.c;
     const int S = c.n_seq, N = c.n_pages, P = c.page, t = threadIdx.x;
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
     if (t == 0) s_bits = s_used = 0;
     const int first = c.queue[0], count = c.queue[1];
     // the sequences of a thread follow each other, so that its own sums add up in place
-    const int each = (S + kPlanThreads - 1) / kPlanThreads, s0 = min(t * each, S), s1 = min(s0 + each, S);
+    const int each = (S + THREADS - 1) / THREADS, s0 = min(t * each, S), s1 = min(s0 + each, S);
     int bits = 0, n[EACH], len[EACH], held[EACH];
     longlong2 sum{0, 0}, total, moved;
 #pragma unroll
@@ -81,7 +83,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
             if (len[i] < 0 || n[i] < 0) len[i] = -1, n[i] = 0, bits |= kPgArg;
             sum.x += n[i];
         }
-    long long at = plan_scan(sum, red[0], &total).x - sum.x;
+    long long at = plan_scan<THREADS>(sum, red[0], &total).x - sum.x;
     longlong2 move{0, 0};      // pages given back, pages taken
 #pragma unroll
     for (int i = 0; i < EACH; ++i)
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
             move.x += max(held[i] - want[s], 0);
             move.y += max(want[s] - held[i], 0);
         }
-    const longlong2 upto = plan_scan(move, red[1], &moved);
+    const longlong2 upto = plan_scan<THREADS>(move, red[1], &moved);
     long long give = upto.x - move.x, take = upto.y - move.y;
     const bool sound = first >= 0 && first < N && count >= 0 && count <= N && count + moved.x <= N;
     const int have = sound ? int(count + moved.x) : 0;
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
     }
     if (bits) atomicOr(&s_bits, bits);
     __syncthreads();
-    const int used = s_used, G = gridDim.x * kPlanThreads, me = blockIdx.x * kPlanThreads + t;
+    const int used = s_used, G = gridDim.x * THREADS, me = blockIdx.x * THREADS + t;
     const int given = sound ? int(moved.x) : 0;
     // page i of those that the plan takes, in their order
     const auto taken = [&](int i) {
@@ -123,6 +125,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
         const int s = plan_find(give_end, S, i - count), j = i - count - (give_end[s] - (had[s] - want[s]));
         return c.table[(size_t)s * c.max_pages + want[s] + j];
     };
+    const auto wrap = [&](int i) { return i < N ? i : i < 2 * N ? i - N : i - 2 * N; };   // (N is below 2^27)
+    // a thread's first page taken and first page given back, asked for before the rows are looked at
+    const int taker = me < used ? plan_find(take_end, S, me) : 0, giver = me < given ? plan_find(give_end, S, me) : 0;
+    const int first_taken = me < used ? taken(me) : 0;
+    const auto back = [&](int j, int s) { return c.table[(size_t)s * c.max_pages + want[s] + j - (give_end[s] - (had[s] - want[s]))]; };
+    const int first_given = me < given ? back(me, giver) : 0;
     int worse = 0;
     // four rows a thread: they mostly lie in one page, which is looked up once
     for (int r0 = 4 * me; r0 < a.rows; r0 += 4 * G) {
@@ -150,16 +158,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
                 if (r0 + i < a.rows) a.slots[r0 + i] = slot[i];
     }
     for (int i = me; i < used; i += G) {
-        const int s = plan_find(take_end, S, i);
-        c.table[(size_t)s * c.max_pages + had[s] + i - (take_end[s] - (want[s] - had[s]))] = taken(i);
+        const int s = i == me ? taker : plan_find(take_end, S, i);
+        c.table[(size_t)s * c.max_pages + had[s] + i - (take_end[s] - (want[s] - had[s]))] = i == me ? first_taken : taken(i);
     }
-    for (int j = me; j < given; j += G) {
-        const int s = plan_find(give_end, S, j);
-        const long long to = (long long)first + count + j;
-        c.ring[to % N] = c.table[(size_t)s * c.max_pages + want[s] + j - (give_end[s] - (had[s] - want[s]))];
-    }
+    for (int j = me; j < given; j += G) c.ring[wrap(first + count + j)] = j == me ? first_given : back(j, plan_find(give_end, S, j));
     if (blockIdx.x == 0)
-        for (int s = t; s <= S; s += kPlanThreads) a.cu[s] = s ? min(row_end[s - 1], a.rows) : 0;
+        for (int s = t; s <= S; s += THREADS) a.cu[s] = s ? min(row_end[s - 1], a.rows) : 0;
     if (worse) atomicOr(&s_bits, worse);
     __syncthreads();
     if (t == 0) {
@@ -172,27 +176,30 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PlanArgs a) {
     }
     __syncthreads();
     if (!s_last || !sound) return;
-    for (int s = t; s < S; s += kPlanThreads)
+    for (int s = t; s < S; s += THREADS)
         if (got[s]) c.held[s] = want[s];
     if (t == 0) {
-        c.queue[0] = int(((long long)first + used) % N);
+        c.queue[0] = wrap(first + used);
         c.queue[1] = have - used;
     }
 }
 
-template <int EACH>
+template <int THREADS, int EACH>
 int launch_plan(const PlanArgs &a, cudaStream_t s) {
     const int dev = current_device();
     if (dev < 0) return DFL_E_CUDA;
-    const size_t smem = (size_t)7 * 4 * a.c.n_seq;
     static bool done[kMaxDevices] = {};
     if (!done[dev]) {
-        if (cudaFuncSetAttribute(k_paged_plan<EACH>, cudaFuncAttributeMaxDynamicSharedMemorySize, 7 * 4 * DFL_PAGED_MAX_SEQ) != cudaSuccess)
+        if (cudaFuncSetAttribute(k_paged_plan<THREADS, EACH>, cudaFuncAttributeMaxDynamicSharedMemorySize, 7 * 4 * DFL_PAGED_MAX_SEQ) != cudaSuccess)
             return DFL_E_CUDA;
         done[dev] = true;
     }
-    const int ctas = std::min(std::max((a.rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads), std::max(1, std::min(16, a.c.n_pages / 16384))), 304);
-    return pg_launched(launch_pdl(k_paged_plan<EACH>, dim3(ctas), dim3(kPlanThreads), smem, s, a));
+    const int ctas = std::min(std::max(int(((int64_t)a.rows + 4 * THREADS - 1) / (4 * THREADS)), std::max(1, std::min(16, a.c.n_pages / 16384))), 304);
+    return pg_launched(launch_pdl(k_paged_plan<THREADS, EACH>, dim3(ctas), dim3(THREADS), (size_t)7 * 4 * a.c.n_seq, s, a));
+}
+template <int THREADS>
+int launch_plan(const PlanArgs &a, cudaStream_t s) {
+    return a.c.n_seq <= THREADS ? launch_plan<THREADS, 1>(a, s) : launch_plan<THREADS, DFL_PAGED_MAX_SEQ / THREADS>(a, s);
 }
 
 __global__ void k_paged_init(dfl_paged c) {
@@ -269,6 +276,7 @@ int dfl_paged_plan(const dfl_paged *c, const int32_t *len, const int32_t *cnt, i
     const int rc = pg_check(c);
     if (rc) return rc;
     if (!len || !cnt || !cu || rows < 0 || (rows && !slots)) return DFL_E_INVALID_ARG;
+    if (rows > kPgMaxRows) return DFL_E_UNSUPPORTED;
     const void *p[] = {len, cnt, cu, slots};
     for (const void *q : p)
         if (!pg_aligned(q, 4)) return DFL_E_INVALID_ARG;
@@ -285,7 +293,7 @@ int dfl_paged_plan(const dfl_paged *c, const int32_t *len, const int32_t *cnt, i
         if (pg_overlap(len, all[2].bytes, all[i].p, all[i].bytes) || pg_overlap(cnt, all[3].bytes, all[i].p, all[i].bytes)) return DFL_E_INVALID_ARG;
     const PlanArgs a{*c, len, cnt, cu, slots, rows, pg_shift(c)};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return c->n_seq <= kPlanThreads ? launch_plan<1>(a, s) : launch_plan<kPlanEach>(a, s);
+    return rows > kPlanMany ? launch_plan<512>(a, s) : launch_plan<256>(a, s);
 }
 
 int dfl_paged_append(const dfl_paged *c, const int32_t *slots, int rows, const void *k, int64_t ldk, const void *v, int64_t ldv,
@@ -294,6 +302,7 @@ int dfl_paged_append(const dfl_paged *c, const int32_t *slots, int rows, const v
     if (rc) return rc;
     if (rows == 0) return DFL_OK;
     if (rows < 0 || !slots || !pg_aligned(slots, 4)) return DFL_E_INVALID_ARG;
+    if (rows > kPgMaxRows) return DFL_E_UNSUPPORTED;
     if ((rc = pg_check_rows(c, k, ldk, c->n_kv)) || (rc = pg_check_rows(c, v, ldv, c->n_kv))) return rc;
     const int64_t w = (int64_t)c->n_kv * c->head_dim, pool = (int64_t)c->n_pages * c->page * w * 2;
     for (const void *p : {static_cast<const void *>(c->k), static_cast<const void *>(c->v)})
@@ -310,6 +319,7 @@ int dfl_paged_prompt(const dfl_paged *c, const void *q, int64_t ldq, int n_q, co
     if (rc || (rc = pg_check_heads(c, n_q, window, scale))) return rc;
     if (rows == 0) return DFL_OK;
     if (rows < 0 || !cu || !pg_aligned(cu, 4)) return DFL_E_INVALID_ARG;
+    if (rows > kPgMaxRows) return DFL_E_UNSUPPORTED;
     if ((rc = pg_check_rows(c, q, ldq, n_q)) || (rc = pg_check_rows(c, k, ldk, c->n_kv)) || (rc = pg_check_rows(c, v, ldv, c->n_kv)) ||
         (rc = pg_check_rows(c, out, ldo, n_q)))
         return rc;
@@ -334,7 +344,7 @@ int dfl_paged_attn(const dfl_paged *c, const void *q, int64_t ldq, int n_q, int 
     int rc = pg_check(c);
     if (rc || (rc = pg_check_heads(c, n_q, window, scale))) return rc;
     if (rows < 1 || total < 0 || !cu || !len || !pg_aligned(cu, 4) || !pg_aligned(len, 4)) return DFL_E_INVALID_ARG;
-    if (rows > DFL_MAX_ROWS) return DFL_E_UNSUPPORTED;
+    if (rows > DFL_MAX_ROWS || total > kPgMaxRows) return DFL_E_UNSUPPORTED;
     if (!scratch || !pg_aligned(scratch, 256) || (int64_t)scratch_bytes < dfl_paged_attn_scratch_bytes(c, n_q, rows)) return DFL_E_INVALID_ARG;
     if (total == 0) return DFL_OK;
     if ((rc = pg_check_rows(c, q, ldq, n_q)) || (rc = pg_check_rows(c, out, ldo, n_q))) return rc;

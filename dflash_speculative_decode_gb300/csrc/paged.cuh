@@ -11,6 +11,7 @@ namespace dfl {
 // error bits (dfl_paged.err)
 constexpr int kPgCapacity = 1, kPgState = 2, kPgArg = 4, kPgTimeout = 8;
 constexpr int kPgMaxGroup = 16;          // query heads per key/value head
+constexpr int kPgMaxRows = 1 << 30;      // rows of a call's buffers: places a tile behind the last one are numbers too
 constexpr int64_t kPgMaxLd = 1 << 22;    // elements between rows: what a tile of 128 rows spans fits 31 bits of bytes
 
 inline bool pg_aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -500,8 +500,8 @@ int dfl_kv8_read(const dfl_kv8 *c, const int32_t *len, const int32_t *first, int
  * (a rollback is index arithmetic). A sequence that has ended gets len = cnt = 0, and its pages go back.
  * The layers of a model that share lengths share the plan: one table, held, ring and queue, a k and v each.
  *
- * Rows of a call are packed: sequence s has rows cu[s] .. cu[s+1]-1 (cu: DEVICE int32 [n_seq+1]) of buffers
- * [rows][heads][head_dim], row r at r * ld elements (at most 2^22), heads and channels contiguous. Rows from cu[n_seq] on
+ * Rows of a call (at most 2^30) are packed: sequence s has rows cu[s] .. cu[s+1]-1 (cu: DEVICE int32 [n_seq+1])
+ * of buffers [rows][heads][head_dim], row r at r * ld elements (at most 2^22), heads and channels contiguous. Rows from cu[n_seq] on
  * are neither read for anything that shows nor written.
  *
  * Everything is DEVICE memory of the caller's; the calls read the struct on the host and enqueue on the

@@ -90,6 +90,27 @@ def test_plans_of_many_steps(torch, n_seq, n_pages, most, page, rows):
     c.status()
 
 
+@pytest.mark.parametrize("n_seq,rows,shift", [(3, 40003, 0), (300, 50001, 1), (700, 33000, 2), (4096, 70000, 3)])
+def test_plans_of_many_rows(torch, n_seq, rows, shift):
+    """Slots that begin anywhere (shift: int32 numbers past a 16-byte boundary), two batches of prompts in turn."""
+    rng = np.random.default_rng(n_seq)
+    per = 2 * rows // n_seq
+    n_pages = rows // 16 + n_seq
+    c, p = cache(torch, n_seq, 1, 64, n_pages, -(-per // 16) + 1, 16), Plan(n_seq, n_pages, -(-per // 16) + 1, 16)
+    cu, slots = i32(torch, [-5] * (n_seq + 1)), i32(torch, [-5] * (rows + 8))[shift:shift + rows]
+    for step in range(4):
+        n = np.where(np.arange(n_seq) % 2 == step % 2, rng.integers(0, per - per // 8, n_seq), 0)
+        c.plan(i32(torch, np.zeros(n_seq)), i32(torch, n), out=(cu, slots))
+        want_cu, want_slots, _ = p.step(np.zeros(n_seq, int), n, rows)
+        assert cu.tolist() == want_cu.tolist()
+        np.testing.assert_array_equal(slots.cpu().numpy(), want_slots)
+        same_plan(c, p)
+    try:
+        c.status()
+    except RuntimeError as e:
+        assert "DFL_E_CAPACITY" in str(e)
+
+
 def test_a_plan_that_frees_all_and_one_of_no_rows(torch):
     c, p = cache(torch, 3, 1, 64, 50, 20, 16), Plan(3, 50, 20, 16)
     for length, n, rows in (([0, 0, 0], [300, 200, 250], 750), ([0, 0, 0], [0, 0, 0], 0), ([0, 0, 0], [320, 320, 160], 800), ([5, 0, 319], [0, 0, 1], 1)):

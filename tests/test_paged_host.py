@@ -51,6 +51,7 @@ def test_a_bad_cache_is_refused_by_every_call(change, code):
     ("plan", dict(len=None), -1), ("plan", dict(cnt=None), -1), ("plan", dict(cu=None), -1), ("plan", dict(slots=None), -1), ("plan", dict(rows=-1), -1),
     ("plan", dict(len=A + 2), -1), ("plan", dict(cu=A + 1), -1),
     ("append", dict(slots=None), -1), ("append", dict(slots=A + 2), -1), ("append", dict(rows=-1), -1), ("append", dict(k=None), -1), ("append", dict(v=A + 8), -1),
+    ("plan", dict(rows=(1 << 30) + 1), -4), ("append", dict(rows=(1 << 30) + 1), -4), ("prompt", dict(rows=(1 << 30) + 1), -4), ("attn", dict(total=(1 << 30) + 1), -4),
     ("append", dict(ldk=(1 << 22) + 8), -4), ("prompt", dict(ldo=(1 << 22) + 8), -4), ("attn", dict(ldq=(1 << 22) + 8), -4),
     ("append", dict(ldk=120), -1), ("append", dict(ldv=132), -1), ("append", dict(ldk=-128), -1),
     ("prompt", dict(q=None), -1), ("prompt", dict(q=A + 2), -1), ("prompt", dict(ldq=248), -1), ("prompt", dict(ldq=260), -1), ("prompt", dict(k=None), -1),
