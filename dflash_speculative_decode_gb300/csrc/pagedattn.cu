@@ -24,7 +24,10 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kGranule = 64;                    // keys of a granule
 constexpr int kStep = 16;                       // a unit's keys begin at a multiple of it: a page at least
-constexpr int kSolo = 96 * 1024;                // units of so many bytes at most need no cut
+// Units of so many bytes at most are taken whole, one CTA each: a cut of many short units costs more (parts to write and to
+// add, a second unit to begin in most CTAs) than a last unit that others wait for. One token, 8 heads of 128, sequences
+// of up to 400 tokens: 64 of them 16.5 us (20.9 cut), 256 of them 55 us (69); 8 of 1000: 15.9 us (11.6 cut).
+__host__ __device__ inline long long whole_bytes(long long units) { return min(96ll * 1024 + 2560 * units, 1024ll * 1024); }
 constexpr int kMaxCtas = 304;                   // two an SM
 constexpr int kBudget = 112 * 1024;             // shared memory of a CTA, two an SM
 constexpr int kMergeThreads = 256;
@@ -32,9 +35,9 @@ constexpr int kMergeThreads = 256;
 struct AttnWork {
     PagedAttnArgs a;
     int chunks;                                 // of query rows
-    int *pre;                                   // [n_seq + 1] granules before each sequence's, of one unit each; then the CTAs in use
+    int *pre;                                   // [n_seq + 1] granules before each sequence's, of one unit each; then the CTAs in use, 0 without cuts
     float *ml, *o;                              // parts: [CTA][2][rows][2], [CTA][2][rows][HD]
-    int solo;                                   // a CTA has one unit and no cut is made
+    int solo;                                   // the capacity alone says that units are taken whole: a CTA has one
 };
 
 // MT tiles of 16 query rows
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr float kShift = kBf16 ? 0.f : 3.f, kBehind = kBf16 ? 16.f : 12.f;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int s_sum[kWarps];
+    __shared__ int s_sum[kWarps], s_most[kWarps], s_some[kWarps];
     __shared__ float s_row[kWarps][kRows];                       // maxima, and at the end the weights' sums
     const PagedAttnArgs &a = w.a;
     const dfl_paged &c = a.c;
@@ -157,15 +160,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
 
     // ---- granules before each sequence's, of one unit a sequence ----
     const int units = c.n_kv * w.chunks;
-    long long all = 0, x = 0, end = 1;
+    bool whole_units = w.solo;
+    long long x = blockIdx.x, end = (long long)S * units;
     if (!w.solo) {
         int bits = 0;
         const int each = (S + kThreads - 1) / kThreads, s0 = min(t * each, S), s1 = min(s0 + each, S);
-        int sum = 0;
+        int sum = 0, most = 0, some = 0;
         for (int s = s0; s < s1; ++s) {
             const int n = seq_work(a, s, &bits).granules;
             pre[s + 1] = n;
             sum += n;
+            most = max(most, n), some += n != 0;
         }
         int upto = sum;
 #pragma unroll
@@ -173,14 +178,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
             const int u = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += u;
         }
-        if (lane == 31) s_sum[warp] = upto;
+        most = __reduce_max_sync(0xffffffffu, most), some = __reduce_add_sync(0xffffffffu, some);
+        if (lane == 31) s_sum[warp] = upto, s_most[warp] = most, s_some[warp] = some;
         __syncthreads();
         int at = upto - sum;
         for (int i = 0; i < warp; ++i) at += s_sum[i];
         for (int s = s0; s < s1; ++s) pre[s + 1] = at += pre[s + 1];
         if (t == 0) pre[0] = 0;
+        most = 0, some = 0;
+        for (int i = 0; i < kWarps; ++i) most = max(most, s_most[i]), some += s_some[i];
         __syncthreads();
-        all = (long long)pre[S] * units;
+        const long long all = (long long)pre[S] * units;
+        whole_units = (long long)most * kGranule * HD * 4 <= whole_bytes((long long)some * units);
         // 256 channels: as many granules each as the fullest of all CTAs would have, so that fewer of the larger parts are to be added
         // (16384 tokens of 2 heads in 13.6 us, 14.9 with all CTAs). Below, all CTAs (2 heads of 64 in 9.0 us, 10.0; 8 of 128 15.3, 16.8)
         const long long least = HD == 256 ? max((all + gridDim.x - 1) / gridDim.x, 1ll) : 1;
@@ -188,23 +197,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
         if (blockIdx.x == 0) {
             pg_report(c.err, bits);
             for (int s = t; s <= S; s += kThreads) w.pre[s] = pre[s];
-            if (t == 0) w.pre[S + 1] = ctas;
+            if (t == 0) w.pre[S + 1] = whole_units ? 0 : ctas;
         }
-        if (int(blockIdx.x) >= ctas) return;
-        x = cut(all, blockIdx.x, ctas);
-        end = cut(all, blockIdx.x + 1, ctas);
+        if (!whole_units) {
+            if (int(blockIdx.x) >= ctas) return;
+            x = cut(all, blockIdx.x, ctas);
+            end = cut(all, blockIdx.x + 1, ctas);
+        }
     }
 
     for (int slot = 0; x < end;) {
         // ---- the piece: granules g0 .. g1 - 1 of a unit ----
         int s = 0, u, g0 = 0, g1, bits = 0;
         SeqWork sw;
-        if (w.solo) {
-            s = blockIdx.x / units, u = blockIdx.x % units;
+        if (whole_units) {
+            s = int(unsigned(x) / unsigned(units)), u = int(unsigned(x) % unsigned(units));
             sw = seq_work(a, s, &bits);
             g1 = sw.granules;
-            if (u == 0 && t == 0) pg_report(c.err, bits);
-            x = end;
+            if (w.solo && u == 0 && t == 0) pg_report(c.err, bits);
+            x += gridDim.x;
         } else {
             for (int hi = S - 1; s < hi;) {                      // the last sequence that begins at or before x, of those with granules
                 const int mid = (s + hi) >> 1;
@@ -511,7 +522,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const AttnWork w,
     pdl_wait();
     const int begin = w.pre[s], granules = w.pre[s + 1] - begin, total = w.pre[c.n_seq], ctas = w.pre[c.n_seq + 1];
     const int row0 = a.cu[s], live = min(kRows, (a.cu[s + 1] - row0) * g - first);
-    if (!granules || (SHARE > 1 && r >= live)) return;
+    if (!granules || !ctas || (SHARE > 1 && r >= live)) return;
     const long long all = (long long)total * units, from = (long long)begin * units + (long long)u * granules;
     const int c0 = cta_at(from, all, ctas), parts = cta_at(from + granules - 1, all, ctas) - c0 + 1;
     if (parts == 1 || r >= live) return;
@@ -594,7 +605,7 @@ int launch_shape(const AttnWork &w, cudaStream_t st) {
     const int64_t granules = ((int64_t)c.max_pages * c.page + kGranule - 1) / kGranule + 1;   // of a unit at most
     const int units = c.n_kv * w.chunks, rows = std::min(Sh::kRows, w.a.rows * w.a.group) * (HD / 64);
     AttnWork m = w;
-    m.solo = granules * kGranule * HD * 4 <= kSolo;
+    m.solo = granules * kGranule * HD * 4 <= whole_bytes((long long)c.n_seq * units);
     const int64_t ctas = m.solo ? (int64_t)c.n_seq * units : std::min<int64_t>(std::min(2 * sms[dev], kMaxCtas), c.n_seq * units * granules);
     const cudaError_t e = launch_pdl(k_paged_attn<T, HD, MT>, dim3(unsigned(ctas)), dim3(kThreads), Sh::kBytes + (m.solo ? 0 : (c.n_seq + 1) * 4), st, m);
     if (e != cudaSuccess || m.solo) return pg_launched(e);

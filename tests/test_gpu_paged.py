@@ -465,13 +465,13 @@ def test_rows_out_of_order_are_reported(torch, cu):
 class Pages:
     """Sequences of given lengths in pages in any order, the rows of a step behind them, and their attention in 64 bits."""
 
-    def __init__(self, torch, heads, lens, counts, page, t, seed=0, spare=2, gain=1.5):
+    def __init__(self, torch, heads, lens, counts, page, t, seed=0, spare=2, gain=1.5, wide=0):
         self.torch, self.lens, self.counts, self.t = torch, np.asarray(lens), np.asarray(counts), t
         self.n_q, self.n_kv, self.hd = heads
         rng = np.random.default_rng(seed)
         S = len(lens)
         need = [-(-(a + b) // page) for a, b in zip(lens, counts)]
-        n_pages, most = sum(need) + 2, max(need) + 1
+        n_pages, most = sum(need) + 2, max(need) + 1 + wide
         self.c = c = cache(torch, S, self.n_kv, self.hd, n_pages, most, page, t)
         order = rng.permutation(n_pages)
         table = np.full((S, most), 2 ** 30, np.int32)              # entries that no call may follow
@@ -557,6 +557,16 @@ def test_many_sequences_of_many_lengths(torch):
     lens = rng.integers(0, 400, 150)
     Pages(torch, (4, 2, 64), lens, rng.integers(0, 2, 150), 16, "bf16").check(1)
     Pages(torch, (4, 1, 128), lens[:60], rng.integers(0, 9, 60), 32, "bf16").check(8)
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (32, 8, 128), (12, 1, 256)])
+@pytest.mark.parametrize("lens", [[100], [0, 5, 0], [300] * 20, [900, 20, 0, 3], [5000] + [10] * 30, [60] * 400])
+def test_short_sequences_in_a_wide_table(torch, heads, lens):
+    """The capacity says nothing of the lengths: units are taken whole or cut by what the sequences hold."""
+    n = [1 if i % 7 != 6 else 0 for i in range(len(lens))]
+    Pages(torch, heads, lens, n, 16, "bf16", seed=len(lens), wide=2000).check(1)
+    if len(lens) < 100:
+        Pages(torch, heads, lens, [3 * x for x in n], 64, "fp16", seed=len(lens), wide=500).check(3)
 
 
 @pytest.mark.parametrize("heads,rows", [((12, 2, 256), 1), ((32, 8, 128), 1), ((4, 1, 64), 8), ((16, 1, 128), 16), ((16, 1, 256), 16)])
