@@ -36,7 +36,9 @@ struct AttnWork {
     PagedAttnArgs a;
     int chunks;                                 // of query rows
     int *pre;                                   // [n_seq + 1] granules before each sequence's, of one unit each; then the CTAs in use, 0 without cuts
+    int4 *first;                                // [CTA] the unit that its share begins in (sequence, unit) and whether inside it
     float *ml, *o;                              // parts: [CTA][2][rows][2], [CTA][2][rows][HD]
+    int by_cut;                                 // merge: a CTA a cut, not a unit
     int solo;                                   // the capacity alone says that units are taken whole: a CTA has one
 };
 
@@ -87,9 +89,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 struct SeqWork {
     int n, row0, len, seen, lo, hi, granules;   // rows, the first of them, tokens before them, keys that some row sees: seen .. hi - 1; lo: seen rounded down to a step
 };
-__device__ SeqWork seq_work(const PagedAttnArgs &a, int s, int *bits) {
+__device__ __forceinline__ SeqWork seq_work(const PagedAttnArgs &a, int r0, int r1, int len, int held, int *bits) {
     SeqWork w{0, 0, 0, 0, 0, 0, 0};
-    const int r0 = a.cu[s], r1 = a.cu[s + 1], len = a.len[s], held = a.c.held[s];
     if (r0 < 0 || r1 < r0 || r1 > a.total || len < 0 || r1 - r0 > a.rows) {
         *bits |= kPgArg;
         return w;
@@ -108,6 +109,10 @@ __device__ SeqWork seq_work(const PagedAttnArgs &a, int s, int *bits) {
     w.lo = w.seen / kStep * kStep;
     w.granules = (w.hi - w.lo + kGranule - 1) / kGranule;
     return w;
+}
+
+__device__ __forceinline__ SeqWork seq_work(const PagedAttnArgs &a, int s, int *bits) {
+    return seq_work(a, a.cu[s], a.cu[s + 1], a.len[s], a.c.held[s], bits);
 }
 
 // The first granule of CTA i of n over `all`, and the CTA that has granule x (in 32 bits where they do: the divisions are on the way
@@ -166,12 +171,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
         int bits = 0;
         const int each = (S + kThreads - 1) / kThreads, s0 = min(t * each, S), s1 = min(s0 + each, S);
         int sum = 0, most = 0, some = 0;
-        for (int s = s0; s < s1; ++s) {
-            const int n = seq_work(a, s, &bits).granules;
-            pre[s + 1] = n;
-            sum += n;
-            most = max(most, n), some += n != 0;
+        constexpr int kBatch = 4;                                // sequences whose numbers a thread asks for together
+        for (int s = t; s < S; s += kBatch * kThreads) {
+            int r0[kBatch], r1[kBatch], len[kBatch], held[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int at = min(s + i * kThreads, S - 1);
+                r0[i] = a.cu[at], r1[i] = a.cu[at + 1], len[i] = a.len[at], held[i] = c.held[at];
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (s + i * kThreads < S) {
+                    const int n = seq_work(a, r0[i], r1[i], len[i], held[i], &bits).granules;
+                    pre[s + i * kThreads + 1] = n;
+                    most = max(most, n), some += n != 0;
+                }
         }
+        __syncthreads();
+        for (int s = s0; s < s1; ++s) sum += pre[s + 1];
         int upto = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -189,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
         for (int i = 0; i < kWarps; ++i) most = max(most, s_most[i]), some += s_some[i];
         __syncthreads();
         const long long all = (long long)pre[S] * units;
-        whole_units = (long long)most * kGranule * HD * 4 <= whole_bytes((long long)some * units);
+        // (of few sequences among many, the line has them side by side)
+        whole_units = (long long)most * kGranule * HD * 4 <= whole_bytes((long long)some * units) && 4 * some >= S;
         // 256 channels: as many granules each as the fullest of all CTAs would have, so that fewer of the larger parts are to be added
         // (16384 tokens of 2 heads in 13.6 us, 14.9 with all CTAs). Below, all CTAs (2 heads of 64 in 9.0 us, 10.0; 8 of 128 15.3, 16.8)
         const long long least = HD == 256 ? max((all + gridDim.x - 1) / gridDim.x, 1ll) : 1;
@@ -230,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
         }
         const int h = u / w.chunks, first = u % w.chunks * kRows, live = min(kRows, sw.n * g - first);
         const bool whole = g0 == 0 && g1 == sw.granules;
+        if (!whole_units && slot == 0 && t == 0) w.first[blockIdx.x] = make_int4(s, u, g0 > 0, 0);
         const int part = slot;
         slot = 1;                                                // a CTA's first piece, or the one that its cut ends in
         if (live <= 0) continue;
@@ -513,23 +532,32 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
 template <typename T, int HD, int SHARE>
 __global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const AttnWork w, int kRows) {
     constexpr int kHalves = kMergeThreads / 16, kSlices = HD / 64;
-    __shared__ float s_o[SHARE > 1 ? SHARE : 1][64], s_ml[SHARE > 1 ? SHARE : 1][2];
+    __shared__ float s_o[SHARE > 1 ? kHalves : 1][64], s_ml[SHARE > 1 ? kHalves : 1][2];
     const PagedAttnArgs &a = w.a;
     const dfl_paged &c = a.c;
     const int half = threadIdx.x >> 4, lane = threadIdx.x & 15, g = a.group, units = c.n_kv * w.chunks;
-    const int u = blockIdx.y, s = blockIdx.z, h = u / w.chunks, first = u % w.chunks * kRows;
-    const int id = blockIdx.x * (kHalves / SHARE) + half / SHARE, r = id / kSlices, ch = id % kSlices * 64 + 4 * lane;
     pdl_wait();
-    const int begin = w.pre[s], granules = w.pre[s + 1] - begin, total = w.pre[c.n_seq], ctas = w.pre[c.n_seq + 1];
+    const int total = w.pre[c.n_seq], ctas = w.pre[c.n_seq + 1];
+    int u = blockIdx.y, s = blockIdx.z;
+    if (w.by_cut) {                                              // the unit that the share of CTA blockIdx.y + 1 begins inside of
+        if (int(blockIdx.y) + 1 >= ctas) return;
+        const int4 at = w.first[blockIdx.y + 1];
+        if (!at.z) return;
+        s = at.x, u = at.y;
+    }
+    const int h = u / w.chunks, first = u % w.chunks * kRows;
+    const int id = blockIdx.x * (kHalves / SHARE) + half / SHARE, r = id / kSlices, ch = id % kSlices * 64 + 4 * lane;
+    const int begin = w.pre[s], granules = w.pre[s + 1] - begin;
     const int row0 = a.cu[s], live = min(kRows, (a.cu[s + 1] - row0) * g - first);
-    if (!granules || !ctas || (SHARE > 1 && r >= live)) return;
+    if (!granules || !ctas) return;
     const long long all = (long long)total * units, from = (long long)begin * units + (long long)u * granules;
     const int c0 = cta_at(from, all, ctas), parts = cta_at(from + granules - 1, all, ctas) - c0 + 1;
-    if (parts == 1 || r >= live) return;
+    if (parts == 1 || (w.by_cut && c0 != int(blockIdx.y))) return;                // (of a unit's cuts, the first one's CTA adds)
+    const bool mine = r < live;
     const int head = cut(all, c0, ctas) < from;                  // the first part is its CTA's second piece
     float m = -INFINITY, l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
     constexpr int kBatch = 4;
-    for (int p0 = half % SHARE; p0 < parts; p0 += SHARE * kBatch) {
+    for (int p0 = half % SHARE; mine && p0 < parts; p0 += SHARE * kBatch) {
         float2 ml[kBatch];
         float4 o[kBatch];
 #pragma unroll
@@ -553,18 +581,19 @@ __global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const AttnWork w,
         *reinterpret_cast<float4 *>(&s_o[half][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
         if (lane == 0) s_ml[half][0] = m, s_ml[half][1] = l;
         __syncthreads();
-        if (half) return;
+        if (half % SHARE) return;
         m = -INFINITY, l = 0.f, v[0] = v[1] = v[2] = v[3] = 0.f;
 #pragma unroll
-        for (int i = 0; i < SHARE; ++i) m = fmaxf(m, s_ml[i][0]);
+        for (int i = 0; i < SHARE; ++i) m = fmaxf(m, s_ml[half + i][0]);
 #pragma unroll
         for (int i = 0; i < SHARE; ++i) {
-            const float f = s_ml[i][0] == m ? 1.f : exp2_fast((s_ml[i][0] - m) * a.scale_log2);
-            const float4 o = *reinterpret_cast<const float4 *>(&s_o[i][4 * lane]);
-            l = fmaf(s_ml[i][1], f, l);
+            const float f = s_ml[half + i][0] == m ? 1.f : exp2_fast((s_ml[half + i][0] - m) * a.scale_log2);
+            const float4 o = *reinterpret_cast<const float4 *>(&s_o[half + i][4 * lane]);
+            l = fmaf(s_ml[half + i][1], f, l);
             v[0] = fmaf(o.x, f, v[0]), v[1] = fmaf(o.y, f, v[1]), v[2] = fmaf(o.z, f, v[2]), v[3] = fmaf(o.w, f, v[3]);
         }
     }
+    if (!mine) return;
     const float d = 1.f / l;
     const int p = first + r;
     *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + (int64_t)(row0 + p / g) * a.ldo + (h * g + p % g) * HD + ch) =
@@ -575,15 +604,16 @@ __global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const AttnWork w,
 int chunk_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 struct Scratch {
-    size_t pre, ml, o, total;
+    size_t pre, first, ml, o, total;
 };
 Scratch scratch_of(const dfl_paged *c, int n_q, int rows) {
     const size_t r = (size_t)kMaxCtas * 2 * chunk_rows(rows * (n_q / c->n_kv));
     Scratch s;
     s.pre = ((size_t)(c->n_seq + 2) * 4 + 255) / 256 * 256;
+    s.first = (size_t)kMaxCtas * sizeof(int4);
     s.ml = r * 2 * 4;
     s.o = r * c->head_dim * 4;
-    s.total = s.pre + s.ml + s.o;
+    s.total = s.pre + s.first + s.ml + s.o;
     return s;
 }
 
@@ -605,13 +635,20 @@ int launch_shape(const AttnWork &w, cudaStream_t st) {
     const int64_t granules = ((int64_t)c.max_pages * c.page + kGranule - 1) / kGranule + 1;   // of a unit at most
     const int units = c.n_kv * w.chunks, rows = std::min(Sh::kRows, w.a.rows * w.a.group) * (HD / 64);
     AttnWork m = w;
-    m.solo = granules * kGranule * HD * 4 <= whole_bytes((long long)c.n_seq * units);
+    // (more CTAs than that are not launched for units of which many may be without rows)
+    m.solo = granules * kGranule * HD * 4 <= whole_bytes((long long)c.n_seq * units) && (int64_t)c.n_seq * units <= 8 * kMaxCtas;
     const int64_t ctas = m.solo ? (int64_t)c.n_seq * units : std::min<int64_t>(std::min(2 * sms[dev], kMaxCtas), c.n_seq * units * granules);
     const cudaError_t e = launch_pdl(k_paged_attn<T, HD, MT>, dim3(unsigned(ctas)), dim3(kThreads), Sh::kBytes + (m.solo ? 0 : (c.n_seq + 1) * 4), st, m);
     if (e != cudaSuccess || m.solo) return pg_launched(e);
-    constexpr int kHalves = kMergeThreads / 16;
+    // A CTA a unit, or where these are more than the cuts, a cut; half warps share a row's parts: 16 where rows are few in all, 4 of
+    // cuts, as one sequence among many may have most of them
+    constexpr int kHalves = kMergeThreads / 16, kFew = 4;
     if ((int64_t)c.n_seq * units * rows < 8 * sms[dev])
         return pg_launched(launch_pdl(k_paged_merge<T, HD, kHalves>, dim3(rows, units, c.n_seq), dim3(kMergeThreads), 0, st, m, int(Sh::kRows)));
+    m.by_cut = (int64_t)c.n_seq * units >= ctas;
+    if (m.by_cut)
+        return pg_launched(launch_pdl(k_paged_merge<T, HD, kFew>, dim3((rows * kFew + kHalves - 1) / kHalves, unsigned(std::max<int64_t>(ctas - 1, 1))),
+                                      dim3(kMergeThreads), 0, st, m, int(Sh::kRows)));
     return pg_launched(launch_pdl(k_paged_merge<T, HD, 1>, dim3((rows + kHalves - 1) / kHalves, units, c.n_seq), dim3(kMergeThreads), 0, st, m, int(Sh::kRows)));
 }
 
@@ -634,8 +671,8 @@ int launch_paged_attn(const PagedAttnArgs &a, void *scratch, cudaStream_t st) {
     const Scratch s = scratch_of(&a.c, a.n_q, a.rows);
     const int rows = chunk_rows(a.rows * a.group);
     uint8_t *at = static_cast<uint8_t *>(scratch);
-    const AttnWork w{a, (a.rows * a.group + rows - 1) / rows, reinterpret_cast<int *>(at), reinterpret_cast<float *>(at + s.pre),
-                     reinterpret_cast<float *>(at + s.pre + s.ml), 0};
+    const AttnWork w{a, (a.rows * a.group + rows - 1) / rows, reinterpret_cast<int *>(at), reinterpret_cast<int4 *>(at + s.pre),
+                     reinterpret_cast<float *>(at + s.pre + s.first), reinterpret_cast<float *>(at + s.pre + s.first + s.ml), 0, 0};
     return a.c.type == DFL_BF16 ? launch_type<__nv_bfloat16>(w, rows, st) : launch_type<__half>(w, rows, st);
 }
 

@@ -560,10 +560,11 @@ def test_many_sequences_of_many_lengths(torch):
 
 
 @pytest.mark.parametrize("heads", [(4, 2, 64), (32, 8, 128), (12, 1, 256)])
-@pytest.mark.parametrize("lens", [[100], [0, 5, 0], [300] * 20, [900, 20, 0, 3], [5000] + [10] * 30, [60] * 400])
+@pytest.mark.parametrize("lens", [[100], [0, 5, 0], [300] * 20, [900, 20, 0, 3], [5000] + [10] * 30, [60] * 400, [5000] + [70] * 400, [2000] * 40,
+                                  [0] * 900 + [6000] + [0] * 1000 + [500]])
 def test_short_sequences_in_a_wide_table(torch, heads, lens):
     """The capacity says nothing of the lengths: units are taken whole or cut by what the sequences hold."""
-    n = [1 if i % 7 != 6 else 0 for i in range(len(lens))]
+    n = [1 if (i % 7 != 6 if len(lens) < 1000 else x > 0) else 0 for i, x in enumerate(lens)]
     Pages(torch, heads, lens, n, 16, "bf16", seed=len(lens), wide=2000).check(1)
     if len(lens) < 100:
         Pages(torch, heads, lens, [3 * x for x in n], 64, "fp16", seed=len(lens), wide=500).check(3)
