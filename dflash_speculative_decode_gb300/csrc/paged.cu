@@ -1,4 +1,4 @@
-// paged.cu -- a paged key/value cache in 16 bits (include/dfl.h, dfl_paged): plans, rows into pages, attention.
+// paged.cu -- a paged key/value cache in 16 bits (include/dfl.h, dfl_paged): plans, rows into pages, and the entry points.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -12,7 +12,8 @@ namespace {
 // Sums over the sequences give each one's rows, the pages it gives back and those it takes. A CTA reads all
 // lengths and scans them itself, so that one launch of many CTAs can share the writing: slots, table entries
 // and ring places of a plan follow from the state before it alone. Pages taken that the ring did not hold yet
-// are those given back in this call, found by the sums. The CTA that comes last writes what all read.
+// are those given back in this call, found by the sums. The CTA that comes last writes what all read. Its bytes are a
+// few microseconds' at most (1.4 MB for 512 prompts); what it takes is the chain of loads, two scans and the last CTA.
 // THREADS: 512 where there are many rows to write (328 thousand of 512 sequences in 9.4 us, 11.2 with 256), 256 where
 // the call is short (64 sequences in 5.0 us, 5.8 with 512).
 constexpr int kPlanMany = 32768;
@@ -221,7 +222,8 @@ struct AppendArgs {
     int64_t ldk, ldv;          // bytes
 };
 
-// One thread moves 16 bytes of a key and of the value beside it.
+// One thread moves 16 bytes of a key and of the value beside it: bound by HBM (24 thousand rows of 16 heads of 128 in 38.6 us, 6.2
+// TB/s, 91 % of measured), or for few rows by the launch (64 rows in 1.6 us in a graph, 5.2 with the host).
 __global__ void __launch_bounds__(256) k_paged_append(AppendArgs a) {
     const dfl_paged &c = a.c;
     const int hc = c.head_dim / 8, chunks = c.n_kv * hc;       // 16-byte pieces of a head, of a row

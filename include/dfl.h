@@ -542,12 +542,14 @@ int dfl_paged_status(const dfl_paged *c, void *cuda_stream);
  * A sequence that a plan cannot serve keeps the pages that it has, and its rows have slots -1: one longer than
  * max_pages, one whose rows reach past `rows` and one whose pages are not there (after it no sequence of the call
  * gets new pages) with DFL_E_CAPACITY; a negative len or cnt (DFL_E_INVALID_ARG) counts as no rows.
- * len and cnt: int32 [n_seq], neither overlaps what is written. Calls of a cache must not overlap on the GPU. */
+ * len and cnt: int32 [n_seq]; cu and slots share no memory with anything else. Calls of a cache must not overlap on
+ * the GPU. */
 int dfl_paged_plan(const dfl_paged *c, const int32_t *len, const int32_t *cnt, int32_t *cu, int32_t *slots, int rows,
                    void *cuda_stream);
 /* Rows k, v (row r at r * ldk, r * ldv elements, [n_kv][head_dim] each; 16-byte aligned, ld a multiple of 8) into
  * the places of slots[0..rows-1]; a negative slot's row is left out. Two rows of one call must not have one slot
- * (a plan's have not). */
+ * (a plan's have not).
+ * k and v lie outside the pages. */
 int dfl_paged_append(const dfl_paged *c, const int32_t *slots, int rows, const void *k, int64_t ldk, const void *v,
                      int64_t ldv, void *cuda_stream);
 /* Causal grouped-query attention of packed prompts among their own rows (of a sequence's first tokens; the cache's
@@ -555,8 +557,10 @@ int dfl_paged_append(const dfl_paged *c, const int32_t *slots, int rows, const v
  * most 16, over the rows j <= i of the same sequence, with window > 0 only j > i - window. scale > 0. The buffers
  * have `rows` rows, 16-byte aligned, ld multiples of 8. Scores, softmax statistics and sums are fp32; a row's
  * weights are rounded once to the cache's type, as what the tensor cores take, and the output once. A value that
- * is not finite makes NaN of the outputs of rows that see it, and touches no other. out overlaps no input.
- * Each row's bits depend on its own sequence alone. */
+ * is not finite leaves nothing finite of its channel in the rows that see it, and touches no other output; a key or
+ * query that is not finite makes NaN of the rows that meet it. The sums stay finite for values up to 2^90. out
+ * shares no memory with an input (rows may lie in the gaps of others that are as far apart). Each row's bits
+ * depend on its own sequence alone. */
 int dfl_paged_prompt(const dfl_paged *c, const void *q, int64_t ldq, int n_q, const void *k, int64_t ldk, const void *v,
                      int64_t ldv, const int32_t *cu, int rows, int window, float scale, void *out, int64_t ldo,
                      void *cuda_stream);
@@ -569,9 +573,10 @@ int64_t dfl_paged_attn_scratch_bytes(const dfl_paged *c, int n_q, int rows);
  * len - window <= j < len (all of them with window = 0) and all the sequence's new ones. The new rows' keys and
  * values are in the pages (dfl_paged_append). Numbers, groups and scale as for dfl_paged_prompt. A sequence with
  * more rows than `rows`, or without the pages that it needs, is left as it is and reported; rows that see a page
- * whose table entry is bad get NaN (reported). out overlaps no input. Calls on one scratch (DEVICE, 256-byte
- * aligned) must not overlap on the GPU; nothing is kept in it from one call to the next. One call gives the same
- * bits each time. */
+ * whose table entry is bad get NaN (reported). out shares no memory with q or the pages. Calls on one scratch
+ * (DEVICE, 256-byte aligned) must not overlap on the GPU; nothing is kept in it from one call to the next. One call
+ * gives the same bits each time; the last bits of a sequence may depend on the other sequences' lengths, which
+ * decide where its sums are cut. */
 int dfl_paged_attn(const dfl_paged *c, const void *q, int64_t ldq, int n_q, int total, const int32_t *cu,
                    const int32_t *len, int rows, int window, int causal, float scale, void *out, int64_t ldo,
                    void *scratch, size_t scratch_bytes, void *cuda_stream);
