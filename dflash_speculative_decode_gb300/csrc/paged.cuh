@@ -11,7 +11,7 @@ namespace dfl {
 // error bits (dfl_paged.err)
 constexpr int kPgCapacity = 1, kPgState = 2, kPgArg = 4, kPgTimeout = 8;
 constexpr int kPgMaxGroup = 16;          // query heads per key/value head
-constexpr int kPgMaxRows = 1 << 30;      // rows of a call's buffers: places a tile behind the last one are numbers too
+constexpr int kPgMaxRows = 1 << 30;      // rows of a call's buffers, tokens of a pool or a sequence: places some tiles behind the last one are numbers too
 constexpr int64_t kPgMaxLd = 1 << 22;    // elements between rows: what a tile of 128 rows spans fits 31 bits of bytes
 
 inline bool pg_aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -22,7 +22,7 @@ inline int pg_check(const dfl_paged *c) {
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return DFL_E_UNSUPPORTED;
     if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return DFL_E_UNSUPPORTED;
     if (c->type != DFL_BF16 && c->type != DFL_F16) return DFL_E_UNSUPPORTED;
-    if ((int64_t)c->n_pages * c->page > INT32_MAX || (int64_t)c->max_pages * c->page > INT32_MAX) return DFL_E_INVALID_ARG;
+    if ((int64_t)c->n_pages * c->page > kPgMaxRows || (int64_t)c->max_pages * c->page > kPgMaxRows) return DFL_E_INVALID_ARG;
     if (!c->k || !c->v || !pg_aligned(c->k, 16) || !pg_aligned(c->v, 16)) return DFL_E_INVALID_ARG;
     const void *p[] = {c->table, c->held, c->ring, c->queue, c->err};
     for (const void *q : p)

@@ -511,7 +511,7 @@ enum { DFL_BF16 = 0, DFL_F16 = 1 };
 typedef struct dfl_paged {
     int32_t n_seq, n_kv, head_dim;   /* n_seq <= DFL_PAGED_MAX_SEQ, n_kv <= 1024, head_dim 64, 128 or 256 */
     int32_t page;                    /* tokens of a page: 16, 32, 64 or 128 */
-    int32_t n_pages, max_pages;      /* of the pool, and of one sequence; both times page below 2^31 */
+    int32_t n_pages, max_pages;      /* of the pool, and of one sequence; both times page at most 2^30 */
     int32_t type;                    /* DFL_BF16 or DFL_F16: of k, v and the rows of all calls */
     void *k, *v;                     /* [n_pages][n_kv][page][head_dim] */
     int32_t *table;                  /* [n_seq][max_pages]: the page of each `page` tokens; entries from held on

@@ -35,7 +35,8 @@ def calls(c, L):
 
 @pytest.mark.parametrize("change,code", [
     (dict(n_seq=0), -1), (dict(n_seq=4097), -1), (dict(n_kv=0), -1), (dict(n_kv=1025), -1), (dict(n_pages=0), -1), (dict(max_pages=0), -1),
-    (dict(n_pages=1 << 26, page=32), -1), (dict(max_pages=1 << 25, page=64), -1), (dict(head_dim=96), -4), (dict(head_dim=512), -4), (dict(page=0), -4),
+    (dict(n_pages=1 << 26, page=32), -1), (dict(max_pages=1 << 25, page=64), -1), (dict(n_pages=(1 << 25) + 1, page=32), -1),
+    (dict(max_pages=(1 << 24) + 1, page=64), -1), (dict(head_dim=96), -4), (dict(head_dim=512), -4), (dict(page=0), -4),
     (dict(page=48), -4), (dict(page=256), -4), (dict(type=2), -4), (dict(type=-1), -4), (dict(k=None), -1), (dict(v=A + 8), -1), (dict(table=None), -1),
     (dict(held=A + 2), -1), (dict(ring=None), -1), (dict(queue=None), -1), (dict(err=None), -1)])
 def test_a_bad_cache_is_refused_by_every_call(change, code):
