@@ -12,12 +12,14 @@
 // after the tile's one barrier each warp adds P V for a quarter of the channels. So no score or sum is computed
 // twice, and at the end of a unit nothing but the weights' sums has to be joined. Weights are relative to a maximum
 // that all warps hold, renewed only when one of them meets a score that passes it by more than 16 powers of two (12, fp16; the
-// barrier says so, and the tile's weights are taken again). mma.sync and not tcgen05: with 16 rows a tile the
+// barrier says so, and the tile's weights are taken again). Up to 16 rows a weight goes to its product in two parts of the type
+// (rounded, and what the rounding left), so that the output's own rounding is all that shows: 1 to 6 % slower, and the outputs as
+// near the formulas as those of fp32 weights; units of more rows, whose products count, take it rounded. mma.sync and not tcgen05: with 16 rows a tile the
 // products are a small part of what even these units do while the keys arrive.
 //
-// Measured: one token of 64 sequences of up to 8191 tokens (8 heads of 128) in 198 us, 6.7 TB/s, 99 % of measured; verifies of 8
-// rows over 8 x 16384 tokens (16 heads) in 164 us, 97 %. One sequence is bound by latency: 16384 tokens of 2 heads of 256 in
-// 13.2 us, of which the merge is 2.5 (floor 5.0). Before: a key group a warp, each with a softmax and all channels of its own,
+// Measured: one token of 64 sequences of up to 8191 tokens (8 heads of 128) in 203 us, 6.6 TB/s, 97 % of measured; verifies of 8
+// rows over 8 x 16384 tokens (16 heads) in 168 us, 94 %. One sequence is bound by latency: 16384 tokens of 2 heads of 256 in
+// 14.5 us, of which the merge is 2.5 (floor 5.0). Before: a key group a warp, each with a softmax and all channels of its own,
 // 209, 182 and 21 us; the next tile's scores beside the products in the same warp's stream 2 to 4 % slower than now.
 #include <algorithm>
 
@@ -53,7 +55,8 @@ struct Shape {
     static constexpr int MT = MT_, kKeys = HD == 256 ? 32 : 64;   // keys of a tile
     static constexpr int kMine = kKeys / kWarps;                  // of a warp
     static constexpr int kRows = 16 * MT;
-    static constexpr int kQ = kRows * HD * 2, kP = kRows * kKeys * 2;
+    static constexpr int kParts = MT == 1 ? 2 : 1;                // of a weight: rounded, and what the rounding left
+    static constexpr int kQ = kRows * HD * 2, kHalf = kRows * kKeys * 2, kP = kParts * kHalf;
     static constexpr int kTile = kKeys * HD * 2 * 2;
     static constexpr int kStages = (kBudget - kQ - 2 * kP) / kTile;
     static constexpr int kBytes = kQ + 2 * kP + kStages * kTile;
@@ -137,6 +140,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     } else {
         const __half2 v = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void unpack2(uint32_t x, float &lo, float &hi) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        lo = __uint_as_float(x << 16), hi = __uint_as_float(x & 0xFFFF0000u);
+    } else {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+        lo = v.x, hi = v.y;
     }
 }
 // The halves of x that are an infinity or a NaN, as masks
@@ -412,13 +424,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
                             const float e0 = exp2_fast(fmaf(sc[mt][y][2 * b], a.scale_log2, off)), e1 = exp2_fast(fmaf(sc[mt][y][2 * b + 1], a.scale_log2, off));
                             add[mt][b] += e0 + e1;
                             const int ch = warp * kNt + y;
-                            *reinterpret_cast<uint32_t *>(ps + (i & 1) * Sh::kP + r * kKeys * 2 + ((ch ^ (kKeys == 64 ? r & 7 : r >> 1 & 3)) << 4) + 4 * (lane % 4)) =
-                                pack2<T>(e0, e1);
+                            uint32_t *to = reinterpret_cast<uint32_t *>(ps + (i & 1) * Sh::kP + r * kKeys * 2 + ((ch ^ (kKeys == 64 ? r & 7 : r >> 1 & 3)) << 4) + 4 * (lane % 4));
+                            const uint32_t both = pack2<T>(e0, e1);
+                            to[0] = both;
+                            if constexpr (Sh::kParts == 2) {
+                                float r0, r1;
+                                unpack2<T>(both, r0, r1);
+                                to[Sh::kHalf / 4] = pack2<T>(e0 - r0, e1 - r1);
+                            }
                         }
                     }
             };
-            weigh();
-            if (__syncthreads_or(renew)) {
+            if (i > 0) weigh();                                  // (the first tile has no maximum yet)
+            if (i == 0 || __syncthreads_or(renew)) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -455,11 +473,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
             uint32_t odd = 0;
 #pragma unroll
             for (int ks = 0; ks < kKeys / 16; ++ks) {
-                uint32_t pf[MT][4];
+                uint32_t pf[MT][4], pl[4];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     const int r = mt * 16 + lane % 16, ch = 2 * ks + lane / 16;
-                    ldsm4(pf[mt], p_at + (i & 1) * Sh::kP + r * kKeys * 2 + ((ch ^ (kKeys == 64 ? r & 7 : r >> 1 & 3)) << 4));
+                    const unsigned at = p_at + (i & 1) * Sh::kP + r * kKeys * 2 + ((ch ^ (kKeys == 64 ? r & 7 : r >> 1 & 3)) << 4);
+                    ldsm4(pf[mt], at);
+                    if constexpr (Sh::kParts == 2) ldsm4(pl, at + Sh::kHalf);
                 }
 #pragma unroll
                 for (int y = 0; y < kN / 2; ++y) {
@@ -477,6 +497,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
                     for (int mt = 0; mt < MT; ++mt) {
                         mma16<T>(o[mt][2 * y], pf[mt], vf[0], vf[1]);
                         mma16<T>(o[mt][2 * y + 1], pf[mt], vf[2], vf[3]);
+                    }
+                    if constexpr (Sh::kParts == 2) {
+                        mma16<T>(o[0][2 * y], pl, vf[0], vf[1]);
+                        mma16<T>(o[0][2 * y + 1], pl, vf[2], vf[3]);
                     }
                 }
             }

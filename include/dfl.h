@@ -571,7 +571,8 @@ int64_t dfl_paged_attn_scratch_bytes(const dfl_paged *c, int n_q, int rows);
  * (row cu[s] + m of q and out, which have `total` rows) sits at position p = len[s] + m. causal != 0: it sees the
  * tokens j <= p, with window > 0 only j > p - window. causal == 0 (a draft's block): every row sees the tokens
  * len - window <= j < len (all of them with window = 0) and all the sequence's new ones. The new rows' keys and
- * values are in the pages (dfl_paged_append). Numbers, groups and scale as for dfl_paged_prompt. A sequence with
+ * values are in the pages (dfl_paged_append). Numbers, groups and scale as for dfl_paged_prompt (up to
+ * 16 rows x heads of a group, weights as two numbers of the type each). A sequence with
  * more rows than `rows`, or without the pages that it needs, is left as it is and reported; rows that see a page
  * whose table entry is bad get NaN (reported). out shares no memory with q or the pages. Calls on one scratch
  * (DEVICE, 256-byte aligned) must not overlap on the GPU; nothing is kept in it from one call to the next. One call
