@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
 
             // fp16 weights are held times 2^kShift; the maximum in use may fall behind by kBehind powers of two
             constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-            constexpr float kShift = kBf16 ? 0.f : 3.f, kBehind = kBf16 ? 16.f : 12.f;
+            constexpr float kShift = kBf16 ? 0.f : 3.f, kBehind = kBf16 ? 16.f : 12.f, kFar = 1024.f;
             const float c = a.scale_log2;
             float top = -INFINITY, sum = 0.f;      // the maximum in use and the weights' sum
             uint32_t seen[HD / 32];                // channels in which the row saw a value that is not finite
@@ -660,7 +660,16 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                         tc_st32(t_o + x, o);
                     }
                 }
-                const float off = top == -INFINITY ? 0.f : kShift - top * c;
+                // Where the maximum is so large that the rounding of its product with c is worth 2^-15 of a power of two and more (16 of them at
+                // 2^28, which fp16 weights have no room for), it leaves the scores before they are scaled. (Always: packed prompts 269.6 us, 266.5 so)
+                const float base = top != -INFINITY && fabsf(top) * c > kFar ? top : 0.f;
+                if (__any_sync(0xffffffffu, base != 0.f)) {
+#pragma unroll
+                    for (int x = 0; x < kKeys / 32; ++x)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) s[x][i] = __float_as_uint(__uint_as_float(s[x][i]) - base);
+                }
+                const float off = top == -INFINITY ? 0.f : kShift - (top - base) * c;
                 const uint64_t c2 = pair(__float_as_uint(c), __float_as_uint(c)), off2 = pair(__float_as_uint(off), __float_as_uint(off));
                 uint64_t add[4] = {0, 0, 0, 0};
 #pragma unroll

@@ -555,8 +555,9 @@ int dfl_paged_append(const dfl_paged *c, const int32_t *slots, int rows, const v
 /* Causal grouped-query attention of packed prompts among their own rows (of a sequence's first tokens; the cache's
  * pages are not read):  out[i][h] = sum_j softmax_j(scale * q[i][h] . k[j][h / g]) v[j][h / g],  g = n_q / n_kv at
  * most 16, over the rows j <= i of the same sequence, with window > 0 only j > i - window. scale > 0. The buffers
- * have `rows` rows, 16-byte aligned, ld multiples of 8. Scores, softmax statistics and sums are fp32; a row's
- * weights are rounded once to the cache's type, as what the tensor cores take, and the output once. A value that
+ * have `rows` rows, 16-byte aligned, ld multiples of 8. Scores (of any size that fp32 holds), softmax
+ * statistics and sums are fp32; a row's weights are rounded once to the cache's type, as what the tensor cores take,
+ * and the output once. A value that
  * is not finite leaves nothing finite of its channel in the rows that see it, and touches no other output; a key or
  * query that is not finite makes NaN of the rows that meet it. The sums stay finite for values up to 2^90. out
  * shares no memory with an input (rows may lie in the gaps of others that are as far apart). Each row's bits
