@@ -416,12 +416,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const float off = top[mt][b] == -INFINITY ? 0.f : kShift - top[mt][b] * a.scale_log2;
+                        // (the maximum is taken off before the scale: the product of a large one is rounded by many powers of two, and parts have
+                        // maxima of their own)
+                        const float base = top[mt][b] == -INFINITY ? 0.f : top[mt][b];
                         add[mt][b] = 0.f;
                         const int r = mt * 16 + lane / 4 + 8 * b;
 #pragma unroll
                         for (int y = 0; y < kNt; ++y) {
-                            const float e0 = exp2_fast(fmaf(sc[mt][y][2 * b], a.scale_log2, off)), e1 = exp2_fast(fmaf(sc[mt][y][2 * b + 1], a.scale_log2, off));
+                            const float e0 = exp2_fast(fmaf(sc[mt][y][2 * b] - base, a.scale_log2, kShift)), e1 = exp2_fast(fmaf(sc[mt][y][2 * b + 1] - base, a.scale_log2, kShift));
                             add[mt][b] += e0 + e1;
                             const int ch = warp * kNt + y;
                             uint32_t *to = reinterpret_cast<uint32_t *>(ps + (i & 1) * Sh::kP + r * kKeys * 2 + ((ch ^ (kKeys == 64 ? r & 7 : r >> 1 & 3)) << 4) + 4 * (lane % 4));

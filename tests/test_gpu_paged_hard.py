@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from paged_bounds import attend_exact, far, lifted
-from test_gpu_paged import Prompts, torch  # noqa: F401  (torch: the fixture)
+from test_gpu_paged import Pages, Prompts, near, torch  # noqa: F401  (torch: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -34,6 +34,38 @@ class ExactPrompts(Prompts):
         return out, tol
 
 
+class ExactPages(Pages):
+    """The same over pages. `wide`: pages of a table beyond what a sequence needs, so that the capacity does not say that its units are short."""
+
+    def __init__(self, torch, heads, lens, counts, page, t, make, seed=0, wide=0):
+        super().__init__(torch, heads, lens, counts, page, t, seed, spare=0, wide=wide)
+        rng = np.random.default_rng(seed)
+        n_q, n_kv, hd = heads
+        made = [make(rng, b, n_q, n_kv, a + b, hd) for a, b in zip(lens, counts)]
+        self.q, self.q64 = rounded(torch, np.concatenate([m[0] for m in made]), t)
+        for s, m in enumerate(made):
+            table = self.c.table[s].tolist()
+            for x, keep, rows in ((self.c.k, self.k64, m[1]), (self.c.v, self.v64, m[2])):
+                y, keep[s] = rounded(torch, rows, t)
+                for i in range(-(-len(rows) // page)):
+                    part = y[i * page:(i + 1) * page]
+                    x[table[i], :, :part.shape[0]] = part.transpose(0, 1)
+
+    def want(self, window, causal, scale, rows=1):
+        g = self.n_q // self.n_kv
+        out, tol = np.full(self.q64.shape, -77.0), np.zeros(self.q64.shape)
+        for s in range(len(self.lens)):
+            a, b = self.cu[s], self.cu[s + 1]
+            if b > a:
+                out[a:b], tol[a:b] = attend_exact(self.q64[a:b], self.k64[s], self.v64[s], int(self.lens[s]), window, causal, scale, self.t, 2 if rows * g <= 16 else 1)
+        return out, tol
+
+    def check(self, rows, window=0, causal=True, scale=None):
+        want, tol = self.want(window, causal, self.hd ** -0.5 if scale is None else scale, rows)
+        near(self.run(rows, window, causal, scale), want, tol)
+        self.c.status()
+
+
 LARGE = {"fp16": 2.0 ** 28, "bf16": 2.0 ** 60}       # units of scores whose numbers the type holds
 
 
@@ -51,3 +83,22 @@ def test_prompts_of_very_large_scores(torch, heads, t):
 @pytest.mark.parametrize("lift", [0.0, 2.0 ** 10, 2.0 ** 14, 2.0 ** 18])
 def test_prompts_of_scores_around_a_large_one(torch, heads, t, lift):
     ExactPrompts(torch, heads, [400, 30], t, lambda *a: lifted(*a, lift), seed=3).check()
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (6, 2, 128), (12, 1, 256)])
+@pytest.mark.parametrize("lens,wide", [([300, 70], 0), ([1500], 2000)])
+def test_pages_of_very_large_scores(torch, heads, t, lens, wide):
+    """Units that are taken whole, and cut ones, whose parts have maxima of their own."""
+    for unit, rows in ((LARGE[t], 1), (LARGE[t], 3), (2.0 ** 14, 3)):
+        ExactPages(torch, heads, lens, [rows] * len(lens), 16, t, lambda *a: far(*a, unit), seed=1, wide=wide).check(rows, scale=0.3)
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (6, 2, 128), (12, 1, 256)])
+@pytest.mark.parametrize("lift", [0.0, 2.0 ** 10, 2.0 ** 14, 2.0 ** 18])
+def test_pages_of_scores_around_a_large_one(torch, heads, t, lift):
+    for lens, wide in (([300, 70], 0), ([1500], 2000)):
+        p = ExactPages(torch, heads, lens, [2] * len(lens), 16, t, lambda *a: lifted(*a, lift), seed=3, wide=wide)
+        p.check(2)
+        p.check(2, window=200)
