@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from paged_bounds import attend_exact, far, lifted
+from paged_bounds import attend_exact, far, lifted, spiked
 from test_gpu_paged import Pages, Prompts, near, torch  # noqa: F401  (torch: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -102,3 +102,15 @@ def test_pages_of_scores_around_a_large_one(torch, heads, t, lift):
         p = ExactPages(torch, heads, lens, [2] * len(lens), 16, t, lambda *a: lifted(*a, lift), seed=3, wide=wide)
         p.check(2)
         p.check(2, window=200)
+
+
+# ---- weights as two numbers of the type -------------------------------------------------------------------------
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,rows", [((4, 2, 64), 4), ((2, 1, 64), 8), ((12, 2, 128), 2), ((16, 1, 128), 1), ((12, 1, 256), 1), ((4, 2, 256), 7)])
+@pytest.mark.parametrize("lens,wide", [([100, 33], 0), ([600], 2000)])
+def test_both_parts_of_a_weight(torch, heads, rows, t, lens, wide):
+    """Units of up to 16 rows are as near the definition as their output's rounding and fp32 let them: a bound that outputs without
+    a weight's second part, or with one of the wrong sign, exceed (tests/test_paged_bounds.py). Units taken whole, and cut ones."""
+    p = ExactPages(torch, heads, lens, [rows] * len(lens), 16, t, spiked, seed=5, wide=wide)
+    p.check(rows)
+    p.check(rows, causal=False)
