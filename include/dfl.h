@@ -557,11 +557,11 @@ int dfl_paged_append(const dfl_paged *c, const int32_t *slots, int rows, const v
  * most 16, over the rows j <= i of the same sequence, with window > 0 only j > i - window. scale > 0. The buffers
  * have `rows` rows, 16-byte aligned, ld multiples of 8. Scores (of any size that fp32 holds), softmax
  * statistics and sums are fp32; a row's weights are rounded once to the cache's type, as what the tensor cores take,
- * and the output once. A value that
- * is not finite leaves nothing finite of its channel in the rows that see it, and touches no other output; a key or
- * query that is not finite makes NaN of the rows that meet it. The sums stay finite for values up to 2^90. out
- * shares no memory with an input (rows may lie in the gaps of others that are as far apart). Each row's bits
- * depend on its own sequence alone. */
+ * and the output once. A value that is not finite leaves nothing finite of its channel in the rows that see it, and
+ * touches no other output. A key or query that is not finite counts by the scores that it makes: one of minus infinity
+ * takes no weight, and a row that meets one of plus infinity or NaN, or nothing but minus infinity, is NaN. The sums
+ * stay finite for values up to 2^90. out shares no memory with an input (rows may lie in the gaps of others that are as
+ * far apart). Each row's bits depend on its own sequence alone. */
 int dfl_paged_prompt(const dfl_paged *c, const void *q, int64_t ldq, int n_q, const void *k, int64_t ldk, const void *v,
                      int64_t ldv, const int32_t *cu, int rows, int window, float scale, void *out, int64_t ldo,
                      void *cuda_stream);

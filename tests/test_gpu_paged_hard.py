@@ -114,3 +114,54 @@ def test_both_parts_of_a_weight(torch, heads, rows, t, lens, wide):
     p = ExactPages(torch, heads, lens, [rows] * len(lens), 16, t, spiked, seed=5, wide=wide)
     p.check(rows)
     p.check(rows, causal=False)
+
+
+# ---- keys and queries that are infinite -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (2, 1, 128), (12, 1, 256)])
+@pytest.mark.parametrize("window", [0, 40])
+def test_infinite_keys_and_queries_of_prompts(torch, heads, window, t):
+    """A score of minus infinity takes no weight, and NaN is what has no other score, or one of plus infinity or NaN."""
+    g = heads[0] // heads[1]
+    p = ExactPrompts(torch, heads, [260, 70], t, spiked, window, seed=7)
+    sign = np.sign(p.q64[:, 0])                  # (of head 0's queries: the same in all rows, and no 0)
+    low, high = sign[0] * -np.inf, sign[260] * np.inf
+    p.put("k", 0, low[3], 3)                     # the first row sees nothing else
+    p.put("k", 100, low[5], 5)
+    p.put("k", 300, high[7], 7)                  # (a row of the second prompt)
+    p.q[200, heads[0] - 1, 2], p.q64[200, heads[0] - 1, 2] = float("inf"), np.inf
+    with np.errstate(invalid="ignore"):
+        want, tol = p.want()
+    got = p.run()
+    nan = np.zeros(got.shape[:2], bool)
+    nan[0, :g], nan[200, -1] = True, True
+    nan[300:(330 if not window else 340), :g] = True
+    np.testing.assert_array_equal(np.isnan(want).all(-1), nan)
+    assert np.isfinite(want[~nan]).all()
+    near(got, want, tol)
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (6, 2, 128), (12, 1, 256)])
+@pytest.mark.parametrize("lens,wide", [([200, 0], 0), ([1500, 0], 2000)])
+def test_infinite_keys_and_queries_over_pages(torch, heads, lens, wide, t):
+    g = heads[0] // heads[1]
+    n = lens[0]
+    for where in (7, n // 2, n + 1):             # in a unit's first part, a middle one, and among the rows themselves
+        for high in (False, True):
+            p = ExactPages(torch, heads, lens, [4, 3], 16, t, spiked, seed=n, wide=wide)
+            p.put("k", 0, where, np.sign(p.q64[0, 0, 5]) * (np.inf if high else -np.inf), 5)
+            p.put("k", 1, 0, np.sign(p.q64[4, 0, 3]) * -np.inf, 3)        # the second sequence's first row sees nothing else
+            p.q[3, heads[0] - 1, 2], p.q64[3, heads[0] - 1, 2] = float("-inf"), -np.inf
+            for window in (0, 50):
+                with np.errstate(invalid="ignore"):
+                    want, tol = p.want(window, True, p.hd ** -0.5, 4)
+                nan = np.zeros(want.shape[:2], bool)
+                nan[4, :g], nan[3, -1] = True, True
+                if high and (not window or where > n - 47):
+                    nan[max(0, where - n):4, :g] = True
+                np.testing.assert_array_equal(np.isnan(want).all(-1), nan)
+                assert np.isfinite(want[~nan]).all()
+                near(p.run(4, window), want, tol)
+                p.c.status()
