@@ -127,6 +127,7 @@ SIGNATURES = {
     "dfl_paged_append": (ctypes.c_int, [P(dfl_paged), vp, ctypes.c_int, vp, ctypes.c_int64, vp, ctypes.c_int64, vp]),
     "dfl_paged_prompt": (ctypes.c_int, [P(dfl_paged), vp, ctypes.c_int64, ctypes.c_int, vp, ctypes.c_int64, vp, ctypes.c_int64, vp, ctypes.c_int,
                                         ctypes.c_int, ctypes.c_float, vp, ctypes.c_int64, vp]),
+    "dfl_paged_test_stall": (ctypes.c_int, [ctypes.c_int]),
     "dfl_paged_attn_scratch_bytes": (ctypes.c_int64, [P(dfl_paged), ctypes.c_int, ctypes.c_int]),
     "dfl_paged_attn": (ctypes.c_int, [P(dfl_paged), vp, ctypes.c_int64, ctypes.c_int, ctypes.c_int, vp, vp, ctypes.c_int, ctypes.c_int,
                                       ctypes.c_int, ctypes.c_float, vp, ctypes.c_int64, vp, ctypes.c_size_t, vp]),

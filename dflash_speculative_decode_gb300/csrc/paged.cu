@@ -1,5 +1,6 @@
 // paged.cu -- a paged key/value cache in 16 bits (include/dfl.h, dfl_paged): plans, rows into pages, and the entry points.
 #include <algorithm>
+#include <atomic>
 
 #include "paged.cuh"
 
@@ -247,6 +248,8 @@ __global__ void __launch_bounds__(256) k_paged_append(AppendArgs a) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+std::atomic<int> test_stall{0};
+
 }  // namespace
 }  // namespace dfl
 
@@ -330,8 +333,14 @@ int dfl_paged_prompt(const dfl_paged *c, const void *q, int64_t ldq, int n_q, co
         pg_rows_overlap(out, ldo, wq, v, ldv, wk, rows))
         return DFL_E_INVALID_ARG;
     const int g = n_q / c->n_kv;
-    const PagedAttnArgs a{*c, q, k, v, out, ldq, ldk, ldv, ldo, n_q, g, rows, cu, nullptr, 0, window, 1, pg_shift(c), (4096 + g - 1) / g, scale * kLog2e};
+    const PagedAttnArgs a{*c, q, k, v, out, ldq, ldk, ldv, ldo, n_q, g, rows, cu, nullptr, 0, window, 1, pg_shift(c), (4096 + g - 1) / g, scale * kLog2e,
+                          test_stall.load(std::memory_order_relaxed)};
     return launch_paged_prompt(a, static_cast<cudaStream_t>(stream));
+}
+
+int dfl_paged_test_stall(int copies) {
+    test_stall.store(copies, std::memory_order_relaxed);
+    return DFL_OK;
 }
 
 int64_t dfl_paged_attn_scratch_bytes(const dfl_paged *c, int n_q, int rows) {
@@ -353,7 +362,7 @@ int dfl_paged_attn(const dfl_paged *c, const void *q, int64_t ldq, int n_q, int 
     const int64_t wq = (int64_t)n_q * c->head_dim, pool = (int64_t)c->n_pages * c->page * c->n_kv * c->head_dim * 2, all = ((total - 1) * ldo + wq) * 2;
     if (pg_rows_overlap(out, ldo, wq, q, ldq, wq, total) || pg_overlap(out, all, c->k, pool) || pg_overlap(out, all, c->v, pool)) return DFL_E_INVALID_ARG;
     const int g = n_q / c->n_kv;
-    const PagedAttnArgs a{*c, q, nullptr, nullptr, out, ldq, 0, 0, ldo, n_q, g, total, cu, len, rows, window, causal != 0, pg_shift(c), (4096 + g - 1) / g, scale * kLog2e};
+    const PagedAttnArgs a{*c, q, nullptr, nullptr, out, ldq, 0, 0, ldo, n_q, g, total, cu, len, rows, window, causal != 0, pg_shift(c), (4096 + g - 1) / g, scale * kLog2e, 0};
     return launch_paged_attn(a, scratch, static_cast<cudaStream_t>(stream));
 }
 

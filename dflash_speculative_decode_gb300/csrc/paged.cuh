@@ -78,6 +78,7 @@ struct PagedAttnArgs {
     int shift;                 // page = 1 << shift
     int inverse;               // r / group is (r * inverse) >> 12 for r < 256
     float scale_log2;          // scale * log2(e): weights are powers of two
+    int stall;                 // dfl_paged_test_stall
 };
 
 // a DFL_* code each

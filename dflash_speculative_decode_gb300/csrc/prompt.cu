@@ -65,6 +65,7 @@ struct PromptArgs {
     int group, inverse, total, window;            // r / group is (r * inverse) >> 12 for rows of a tile
     const int32_t *cu;
     float scale_log2;
+    int stall;                 // test of the give-up path: the most copies of an item in its first pass, or, negative, its second
 };
 
 // Instruction descriptor of kind::f16 with an fp32 accumulator of 128 rows and N columns: operands of the type, A
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
             const int stages = kMaxStages - again;     // the second time the last stage holds the notes on values that are not finite
             if (warp == kTiles * 4) {
                 // ---- copies: K and V of each tile in turn through the ring ----
-                const int all = 2 * (je - jb);
+                const int limit = again ? -a.stall : a.stall, all = limit > 0 ? min(limit, 2 * (je - jb)) : 2 * (je - jb);
                 int k = 0;
                 Place at{0, 1u};                       // (the first round's stages are free: the phase before counts as over)
                 const auto copy = [&] {
@@ -825,7 +826,7 @@ int launch_prompt(const PagedAttnArgs &a, cudaStream_t s) {
     CUtensorMap tk, tv;
     if (!rows_map(&tk, a.c, a.k, a.ldk, a.total, Sh::kKeys) || !rows_map(&tv, a.c, a.v, a.ldv, a.total, Sh::kKeys)) return DFL_E_CUDA;
     const PromptArgs p{a.c, static_cast<const uint8_t *>(a.q), static_cast<uint8_t *>(a.out), a.ldq * 2, a.ldo * 2, a.group, a.inverse, a.total, a.window, a.cu,
-                       a.scale_log2};
+                       a.scale_log2, a.stall};
     const int per = Sh::kTiles * (128 / a.group);                // tokens of an item
     const int64_t items = (int64_t)a.total / per + std::min(a.c.n_seq, a.total);
     if (items * a.c.n_kv > INT32_MAX) return DFL_E_UNSUPPORTED;

@@ -565,6 +565,10 @@ int dfl_paged_append(const dfl_paged *c, const int32_t *slots, int rows, const v
 int dfl_paged_prompt(const dfl_paged *c, const void *q, int64_t ldq, int n_q, const void *k, int64_t ldk, const void *v,
                      int64_t ldv, const int32_t *cu, int rows, int window, float scale, void *out, int64_t ldo,
                      void *cuda_stream);
+/* Tests of the error path only, for the whole process: the items of the following dfl_paged_prompt calls issue no more
+ * than `copies` > 0 of their copies (of keys and values in turn), or with copies < 0 no more than -copies in the pass
+ * over values that are not finite, so that their bounded waits give up after about a second. 0: as always. */
+int dfl_paged_test_stall(int copies);
 /* Scratch bytes that dfl_paged_attn needs for n_q query heads and at most `rows` rows a sequence, or -1 for a shape
  * it does not take. */
 int64_t dfl_paged_attn_scratch_bytes(const dfl_paged *c, int n_q, int rows);

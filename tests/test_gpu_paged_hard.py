@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from paged_bounds import attend_exact, far, lifted, spiked
-from test_gpu_paged import Pages, Prompts, near, torch  # noqa: F401  (torch: the fixture)
+from test_gpu_paged import Pages, Prompts, i32, near, torch  # noqa: F401  (torch: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -165,3 +165,34 @@ def test_infinite_keys_and_queries_over_pages(torch, heads, lens, wide, t):
                 assert np.isfinite(want[~nan]).all()
                 near(p.run(4, window), want, tol)
                 p.c.status()
+
+
+# ---- a wait that gives up ------------------------------------------------------------------------------------------
+@pytest.fixture
+def stall():
+    from dflash_speculative_decode_gb300._abi import lib
+    yield lib().dfl_paged_test_stall
+    lib().dfl_paged_test_stall(0)
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (2, 1, 128), (3, 1, 256)])
+@pytest.mark.parametrize("copies", [1, 2, 5, -1, -4])
+def test_a_prompt_whose_copies_do_not_come(torch, stall, heads, copies):
+    """No fault and no endless wait: the copies of every item stop, in its first pass or in the one over values that are not finite; the
+    waits give up after a second, the status says so, and the cache works as before."""
+    from dflash_speculative_decode_gb300 import DflError
+    from dflash_speculative_decode_gb300._abi import DFL_E_TIMEOUT
+    p = Prompts(torch, heads, [700, 40], "bf16", seed=4)
+    if copies < 0:
+        for row in (1, 300, 705):                # (each item has rows that do not see one of its keys' values)
+            p.put("v", row, float("nan"), 2)
+    stall(copies)
+    p.c.prompt(p.q, p.k, p.v, i32(torch, p.cu), out=torch.empty_like(p.q))
+    with pytest.raises(DflError) as e:
+        p.c.status()
+    assert e.value.code == DFL_E_TIMEOUT
+    p.c.status()
+    stall(0)
+    want, tol = p.want()
+    near(p.run(), want, tol)
+    p.c.status()
