@@ -38,6 +38,7 @@ __host__ __device__ inline long long whole_bytes(long long units) { return min(9
 constexpr int kMaxCtas = 304;                   // two an SM
 constexpr int kBudget = 112 * 1024;             // shared memory of a CTA, two an SM
 constexpr int kMergeThreads = 256;
+constexpr int kMostGranules = (1 << 30) - 1;    // of all sequences, 2^36 tokens: what is added up below stays a 32-bit number
 
 struct AttnWork {
     PagedAttnArgs a;
@@ -210,21 +211,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += u;
+            if (lane >= o) upto = min(upto + u, kMostGranules);  // (a thread's own are fewer than 2^30)
         }
         most = __reduce_max_sync(0xffffffffu, most), some = __reduce_add_sync(0xffffffffu, some);
         if (lane == 31) s_sum[warp] = upto, s_most[warp] = most, s_some[warp] = some;
         __syncthreads();
         int at = upto - sum;
-        for (int i = 0; i < warp; ++i) at += s_sum[i];
+        for (int i = 0; i < warp; ++i) at = min(at + s_sum[i], kMostGranules);
         for (int s = s0; s < s1; ++s) pre[s + 1] = at += pre[s + 1];
         if (t == 0) pre[0] = 0;
         most = 0, some = 0;
-        for (int i = 0; i < kWarps; ++i) most = max(most, s_most[i]), some += s_some[i];
+        long long total = 0;
+        for (int i = 0; i < kWarps; ++i) most = max(most, s_most[i]), some += s_some[i], total += s_sum[i];
         __syncthreads();
-        const long long all = (long long)pre[S] * units;
+        // a table whose rows name the same pages over and over can hold more than a pool: nothing of the call is done
+        const bool far = total >= kMostGranules;
+        if (far) bits |= kPgState;
+        const long long all = far ? 0 : (long long)pre[S] * units;
         // (of few sequences among many, the line has them side by side)
-        whole_units = (long long)most * kGranule * HD * 4 <= whole_bytes((long long)some * units) && 4 * some >= S;
+        whole_units = (long long)most * kGranule * HD * 4 <= whole_bytes((long long)some * units) && 4 * some >= S && !far;
         // 256 channels: as many granules each as the fullest of all CTAs would have, so that fewer of the larger parts are to be added
         // (16384 tokens of 2 heads in 13.6 us, 14.9 with all CTAs). Below, all CTAs (2 heads of 64 in 9.0 us, 10.0; 8 of 128 15.3, 16.8)
         const long long least = HD == 256 ? max((all + gridDim.x - 1) / gridDim.x, 1ll) : 1;
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
         if (blockIdx.x == 0) {
             pg_report(c.err, bits);
             for (int s = t; s <= S; s += kThreads) w.pre[s] = pre[s];
-            if (t == 0) w.pre[S + 1] = whole_units ? 0 : ctas;
+            if (t == 0) w.pre[S + 1] = whole_units || far ? 0 : ctas;
         }
         if (!whole_units) {
             if (int(blockIdx.x) >= ctas) return;

@@ -531,7 +531,7 @@ int dfl_paged_init(const dfl_paged *c, void *cuda_stream);
  * output is undefined. DFL_E_INVALID_ARG: a row count out of order (cu descending or past the buffers, a negative
  * len or cnt, more rows of a sequence than the call's `rows`), a slot past the pool, or a table or ring entry
  * outside 0..n_pages-1. DFL_E_STATE: held or the queue out of order, or attention over tokens that the sequence has
- * no pages for. DFL_E_CAPACITY: a sequence longer than max_pages, more rows than slots, or no pages left. */
+ * no pages for, or over 2^36 tokens and more in one call. DFL_E_CAPACITY: a sequence longer than max_pages, more rows than slots, or no pages left. */
 int dfl_paged_status(const dfl_paged *c, void *cuda_stream);
 /* Plan a step: sequence s is to hold ceil((len + cnt) / page) pages. What it has beyond them goes to the ring's
  * end, then what it lacks comes from the ring's front, both in the order of the sequences and of their pages, so

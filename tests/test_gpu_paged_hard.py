@@ -196,3 +196,25 @@ def test_a_prompt_whose_copies_do_not_come(torch, stall, heads, copies):
     want, tol = p.want()
     near(p.run(), want, tol)
     p.c.status()
+
+
+# ---- sizes at the limits -------------------------------------------------------------------------------------------
+def test_more_tokens_than_a_call_counts(torch):
+    """A table whose rows all name one page: 4096 sequences of 2^25 tokens each are as many as 2^31 granules of 64. Nothing is done, and
+    the next call works."""
+    from dflash_speculative_decode_gb300 import PagedCache
+    S, per = 4096, 1 << 18
+    z = lambda *shape: torch.zeros(*shape, dtype=torch.int32, device="cuda")  # noqa: E731
+    k = torch.zeros(1, 1, 128, 64, dtype=torch.bfloat16, device="cuda")
+    c = PagedCache(k, k.clone(), z(S, per), z(S) + per, z(1), z(4))
+    q, cu = torch.zeros(S, 1, 64, dtype=torch.bfloat16, device="cuda"), torch.arange(S + 1, dtype=torch.int32, device="cuda")
+    for n in (S, 2100):                          # (2^30 and some granules)
+        length = z(S)
+        length[:n] = per * 128 - 1
+        out = torch.full_like(q, -77.0)
+        c.attn(q, cu, length, 1, out=out)
+        assert (out == -77).all()
+        with pytest.raises(RuntimeError, match="DFL_E_STATE"):
+            c.status()
+    assert (c.attn(q, cu, z(S) + 5, 1, out=out) == 0).all()
+    c.status()
