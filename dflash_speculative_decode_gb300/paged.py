@@ -22,6 +22,9 @@ def _refuse(msg: str):
     raise DflError(DFL_E_INVALID_ARG, msg)
 
 
+MOST = 2 ** 31 - 1       # of a size: the library's are 32-bit numbers, and what is larger would arrive as another one
+
+
 class PagedCache:
     """A dfl_paged over the caller's tensors (layouts in include/dfl.h), or `empty(...)` to allocate them.
 
@@ -46,6 +49,8 @@ class PagedCache:
         for name, (t, dtype, shape) in want.items():
             if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != k.device:
                 _refuse(f"{name} must be contiguous {dtype} {list(shape)} on {k.device}")
+        if max(N, H, P, hd, S, most) > MOST:
+            _refuse("sizes of the cache must be below 2^31")
         self.n_seq, self.n_kv, self.head_dim, self.page, self.n_pages, self.max_pages = S, H, hd, P, N, most
         self.device, self.dtype = k.device, k.dtype
         if self.device.type != "cuda":
@@ -122,8 +127,8 @@ class PagedCache:
                 _refuse("plan needs the rows of the step's buffers, or out")
             out = self.torch.empty(self.n_seq + 1, dtype=self._i32, device=self.device), self.torch.empty(rows, dtype=self._i32, device=self.device)
         cu, slots = out
-        if rows is not None and slots.numel() != rows:
-            _refuse(f"slots must be int32 [{rows}] on {self.device}")
+        if rows is not None and slots.numel() != rows or slots.numel() > MOST:
+            _refuse(f"slots must be int32 [{'rows' if rows is None else rows}] on {self.device}, rows below 2^31")
         self._call(self.L.dfl_paged_plan, "dfl_paged_plan", self._ints(length, "length", self.n_seq), self._ints(n, "n", self.n_seq),
                    self._ints(cu, "cu", self.n_seq + 1), self._ints(slots, "slots", 0), slots.numel())
         return out
@@ -146,8 +151,8 @@ class PagedCache:
         if out is None:
             out = self.torch.zeros(q.shape, dtype=q.dtype, device=q.device)
         po, no, ldo = self._rows(out, "out", n_q)
-        if nk != n or nv != n or no != n:
-            _refuse("q, k, v and out must have the same rows")
+        if nk != n or nv != n or no != n or window > MOST:
+            _refuse("q, k, v and out must have the same rows, and window be below 2^31")
         self._call(self.L.dfl_paged_prompt, "dfl_paged_prompt", pq, ldq, n_q, pk, ldk, pv, ldv, self._ints(cu, "cu", self.n_seq + 1), n, window,
                    self._scale if scale is None else scale, po, ldo)
         return out
@@ -159,7 +164,7 @@ class PagedCache:
         n_q = q.shape[1]
         need = self._need.get((n_q, rows))
         if need is None:
-            need = int(self.L.dfl_paged_attn_scratch_bytes(self._c, n_q, rows))
+            need = int(self.L.dfl_paged_attn_scratch_bytes(self._c, n_q, rows)) if rows <= MOST else -1
             if need < 0:
                 _refuse(f"{n_q} query heads and {rows} rows: n_q must be a multiple of n_kv = {self.n_kv}, up to 16 a head, with 1..16 rows")
             if self._scratch_bytes < need:
@@ -171,8 +176,8 @@ class PagedCache:
         if out is None:
             out = self.torch.zeros(q.shape, dtype=q.dtype, device=q.device)
         po, no, ldo = self._rows(out, "out", n_q)
-        if no != n:
-            _refuse("out must have q's rows")
+        if no != n or window > MOST:
+            _refuse("out must have q's rows, and window be below 2^31")
         self._call(self.L.dfl_paged_attn, "dfl_paged_attn", pq, ldq, n_q, n, self._ints(cu, "cu", self.n_seq + 1), self._ints(length, "length", self.n_seq),
                    rows, window, causal, self._scale if scale is None else scale, po, ldo, self._scratch_ptr, self._scratch_bytes)
         return out

@@ -218,3 +218,19 @@ def test_more_tokens_than_a_call_counts(torch):
             c.status()
     assert (c.attn(q, cu, z(S) + 5, 1, out=out) == 0).all()
     c.status()
+
+
+def test_sizes_that_32_bits_do_not_hold(torch):
+    """What ctypes would cut down to a size that the library takes is refused: windows, rows, slots, a table of 2^32 + 2 pages."""
+    from dflash_speculative_decode_gb300 import DflError, PagedCache
+    p, a = Prompts(torch, (4, 2, 64), [20], "bf16"), Pages(torch, (4, 2, 64), [300], [2], 16, "bf16")
+    cu, length, c = i32(torch, a.cu), i32(torch, a.lens), a.c
+    wide = torch.empty(2 ** 32 + 2, dtype=torch.int32, device="cuda")
+    for f in (lambda: p.c.prompt(p.q, p.k, p.v, i32(torch, p.cu), window=2 ** 32 + 5), lambda: c.attn(a.q, cu, length, 2, window=2 ** 32 + 5),
+              lambda: c.attn(a.q, cu, length, 2 ** 32 + 2), lambda: c.plan(length, i32(torch, [2]), out=(i32(torch, [0, 0]), wide)),
+              lambda: PagedCache(c.k, c.v, wide[None], c.held, c.free, c.queue)):
+        with pytest.raises(DflError, match="DFL_E_INVALID_ARG"):
+            f()
+    p.window = 2 ** 31 - 1
+    p.check()
+    a.check(2, window=2 ** 31 - 1)
