@@ -539,9 +539,13 @@ int dfl_paged_status(const dfl_paged *c, void *cuda_stream);
  *   cu     [n_seq+1]  sums of cnt: where each sequence's rows begin (limited to `rows`)
  *   slots  [rows]     each row's place, page * (tokens of a page) + the token's place in it, and -1 for rows
  *                     behind the last sequence's (a captured graph's spare ones)
- * A sequence that a plan cannot serve keeps the pages that it has, and its rows have slots -1: one longer than
- * max_pages, one whose rows reach past `rows` and one whose pages are not there (after it no sequence of the call
- * gets new pages) with DFL_E_CAPACITY; a negative len or cnt (DFL_E_INVALID_ARG) counts as no rows.
+ * A sequence that a plan cannot serve keeps the pages that it has, and its rows have slots -1: with DFL_E_CAPACITY one
+ * longer than max_pages, one whose rows reach past `rows` and all behind it (those without rows too: what has ended gives
+ * its pages back in the next plan whose rows fit), and one whose pages are not there (after it no sequence of the call
+ * gets new pages); a negative len or cnt (DFL_E_INVALID_ARG) counts as no rows.
+ * A plan takes steps of any kind, but each attention below one kind: rows of whole prompts, or at most DFL_MAX_ROWS rows
+ * a sequence behind the tokens that it has. Where requests of both kinds are there, they are two steps: the prompts with
+ * cnt = 0 for the others, whose len keeps their pages, then the others with the prompts' rows in len.
  * len and cnt: int32 [n_seq]; cu and slots share no memory with anything else. Calls of a cache must not overlap on
  * the GPU. */
 int dfl_paged_plan(const dfl_paged *c, const int32_t *len, const int32_t *cnt, int32_t *cu, int32_t *slots, int rows,

@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 
 from paged_bounds import attend_exact, far, lifted, spiked
-from test_gpu_paged import Pages, Prompts, i32, near, torch  # noqa: F401  (torch: the fixture)
+from paged_plain import Plan
+from test_gpu_paged import Pages, Prompts, Server, cache, i32, near, same_plan, torch  # noqa: F401  (torch: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -234,3 +235,37 @@ def test_sizes_that_32_bits_do_not_hold(torch):
     p.window = 2 ** 31 - 1
     p.check()
     a.check(2, window=2 ** 31 - 1)
+
+
+# ---- plans ---------------------------------------------------------------------------------------------------------
+def test_what_lies_behind_rows_that_do_not_fit(torch):
+    """The third sequence has ended, but lies behind one whose rows reach past the buffer: it keeps its pages in this plan, and gives them back in
+    the next. One before it gives its pages back at once."""
+    c, p = cache(torch, 4, 1, 64, 12, 4, 16), Plan(4, 12, 4, 16)
+    for length, n, rows in (([0, 0, 0, 0], [40, 16, 30, 5], 100), ([0, 16, 0, 5], [0, 20, 0, 3], 10), ([0, 16, 0, 5], [0, 4, 0, 3], 10)):
+        cu, slots = c.plan(i32(torch, length), i32(torch, n), rows)
+        want_cu, want_slots, short = p.step(length, n, rows)
+        assert cu.tolist() == want_cu.tolist() and slots.tolist() == want_slots.tolist()
+        same_plan(c, p)
+        if short:
+            assert c.held.tolist() == [0, 1, 2, 1]
+            with pytest.raises(RuntimeError, match="DFL_E_CAPACITY"):
+                c.status()
+    assert c.held.tolist() == [0, 2, 0, 1]
+    c.status()
+
+
+@pytest.mark.parametrize("heads,t", [((4, 2, 64), "bf16"), ((12, 1, 256), "fp16")])
+def test_prompts_come_in_while_others_decode(torch, heads, t):
+    """As two steps each time: the prompt's rows with none of the others', then theirs with the prompt in its pages."""
+    z = Server(torch, heads, 3, 40, 16, t, 100, 6)
+    z.step(np.array([50, 0, 33]), True, np.array([50, 0, 33]))
+    for i, n in enumerate((70, 100, 1)):
+        z.step(np.array([0, n, 0]), True, np.array([0, n, 0]))
+        held = z.layers[0].held.tolist()
+        assert held == [-(-int(x) // 16) for x in z.length]
+        z.step(np.array([3, 0, 8]), False, np.array([3, 0, 5]))
+        z.step(np.array([1, 4, 1]), False, np.array([1, 2, 0]))
+        z.end(1)
+    z.step(np.array([2, 0, 1]), False, np.array([2, 0, 1]))
+    assert z.layers[0].held[1] == 0
