@@ -143,6 +143,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
         return *reinterpret_cast<const uint32_t *>(&v);
     }
 }
+// Outputs. Those of finite values lie between the largest and the smallest value, but where weights are rounded and the sum that divides is not, by
+// up to 2^-11 (fp16) further out: at the type's end, where that would be infinite, they are its largest number. (For bf16 the header's limit on
+// values is far below it.)
+template <typename T>
+__device__ __forceinline__ float held(float x) {
+    if constexpr (std::is_same<T, __half>::value) x = fabsf(x) < 65600.f ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
+    return x;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2_out(float lo, float hi) { return pack2<T>(held<T>(lo), held<T>(hi)); }
 template <typename T>
 __device__ __forceinline__ void unpack2(uint32_t x, float &lo, float &hi) {
     if constexpr (std::is_same<T, __nv_bfloat16>::value) {
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
                     const int p = first + r, token = p * a.inverse >> 12;
                     T *to = static_cast<T *>(a.out) + (int64_t)(row0 + token) * a.ldo + (h * g + p - token * g) * HD + warp * kN * 8 + 2 * (lane % 4);
 #pragma unroll
-                    for (int y = 0; y < kN; ++y) *reinterpret_cast<uint32_t *>(to + 8 * y) = pack2<T>(o[mt][y][2 * b] * d, o[mt][y][2 * b + 1] * d);
+                    for (int y = 0; y < kN; ++y) *reinterpret_cast<uint32_t *>(to + 8 * y) = pack2_out<T>(o[mt][y][2 * b] * d, o[mt][y][2 * b + 1] * d);
                 } else {
                     float *to = w.o + (slot_at * kRows + r) * HD + warp * kN * 8 + 2 * (lane % 4);
 #pragma unroll
@@ -633,7 +643,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const AttnWork w,
     const float d = 1.f / l;
     const int p = first + r;
     *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + (int64_t)(row0 + p / g) * a.ldo + (h * g + p % g) * HD + ch) =
-        make_uint2(pack2<T>(v[0] * d, v[1] * d), pack2<T>(v[2] * d, v[3] * d));
+        make_uint2(pack2_out<T>(v[0] * d, v[1] * d), pack2_out<T>(v[2] * d, v[3] * d));
 }
 
 // Rows of a chunk: the fewest of 16, 32 and 64 that hold all, or the most

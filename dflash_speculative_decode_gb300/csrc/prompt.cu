@@ -179,6 +179,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
+// Outputs of finite values. They lie between the largest and the smallest value, but as weights are rounded and the sum that divides is not, by
+// up to 2^-11 (fp16) further out: at the type's end, where that would be infinite, they are its largest number. A NaN stays one.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2_out(float lo, float hi) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) return pack2<T>(lo, hi);   // (the header's limit on values is far below its end)
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Whether a 16-bit number is an infinity or a NaN
 template <typename T>
 __device__ __forceinline__ bool odd16(uint32_t x) {
@@ -771,7 +781,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                         for (int i = 0; i < 4; ++i) {
                             uint32_t p[4];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) p[y] = pack2<T>(__uint_as_float(o[8 * i + 2 * y]) * part, __uint_as_float(o[8 * i + 2 * y + 1]) * part);
+                            for (int y = 0; y < 4; ++y) p[y] = pack2_out<T>(__uint_as_float(o[8 * i + 2 * y]) * part, __uint_as_float(o[8 * i + 2 * y + 1]) * part);
                             st_shared(turn_at(lane, 4 * x + i), make_uint4(p[0], p[1], p[2], p[3]));
                         }
                     }

@@ -269,3 +269,37 @@ def test_prompts_come_in_while_others_decode(torch, heads, t):
         z.end(1)
     z.step(np.array([2, 0, 1]), False, np.array([2, 0, 1]))
     assert z.layers[0].held[1] == 0
+
+
+# ---- values at the type's end --------------------------------------------------------------------------------------
+@pytest.mark.parametrize("heads", [(4, 2, 64), (2, 1, 128), (12, 1, 256)])
+@pytest.mark.parametrize("value", [65504.0, -65504.0])
+def test_the_largest_values_of_fp16(torch, heads, value):
+    """Weights that are all rounded up by nearly half a step, and values that are all the type's largest number: so are the outputs. And where
+    one value is infinite, what sees it is not finite."""
+    n_q, n_kv, hd = heads
+    scale = (1 - np.log2(1 + 2.0 ** -11 * 1.02)) / np.log2(np.e)       # a weight of 4 and a half step of its type, and some more, beside one of 8
+    k = np.full((400, n_kv, hd), 0.0)
+    k[1:, :, 0] = -1
+    q = np.zeros((400, n_q, hd))
+    q[..., 0] = 1
+    make = lambda rng, n, *_: (q[:n], k[:n], np.full((n, n_kv, hd), value))  # noqa: E731
+    p = ExactPrompts(torch, heads, [400], "fp16", make, scale=scale)
+    assert (p.run() == value).all()
+    p.put("v", 300, np.inf, 3)
+    got, g = p.run(), n_q // n_kv
+    assert not np.isfinite(got[300:, :g, 3]).any()
+    got[300:, :g, 3] = value
+    assert (got == value).all()
+    for lens, rows, wide in (([390], 1, 0), ([390], 9, 0), ([1500], 9, 2000), ([1500], 16, 2000)):
+        k = np.full((lens[0] + rows, n_kv, hd), 0.0)
+        k[1:, :, 0] = -1
+        many = lambda rng, n, n_q, n_kv, keys, hd: (q[:n], k, np.full((keys, n_kv, hd), value))  # noqa: E731
+        a = ExactPages(torch, heads, lens, [rows], 16, "fp16", many, wide=wide)
+        assert (a.run(rows, scale=scale) == value).all()
+        a.put("v", 0, 200, np.inf, 3)
+        got = a.run(rows, scale=scale)
+        assert not np.isfinite(got[:, :g, 3]).any()
+        got[:, :g, 3] = value
+        assert (got == value).all()
+        a.c.status()
