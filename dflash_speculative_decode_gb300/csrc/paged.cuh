@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "dfl.h"
@@ -64,6 +65,30 @@ inline int pg_launched(cudaError_t e) { return e == cudaSuccess ? DFL_OK : DFL_E
 
 __device__ __forceinline__ void pg_report(int *err, int bits) {
     if (bits) atomicOr(err, bits);
+}
+
+// ---- what both attentions use -------------------------------------------------------------------------
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// two numbers rounded to the type, the first in the low half
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+// 16 bytes into shared memory, asynchronously, or zeros
+__device__ __forceinline__ void cp_async16_or_zeros(unsigned to, const void *from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
 
 // Arguments of both attentions

@@ -81,18 +81,8 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], unsigned addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-// 16 bytes into shared memory, or zeros
-__device__ __forceinline__ void cp16(unsigned dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // What a sequence brings to a call
 struct SeqWork {
@@ -133,16 +123,6 @@ __device__ __forceinline__ int cta_at(long long x, long long all, int n) {
     return all <= 0xffffffffu / kMaxCtas ? int((unsigned(x + 1) * unsigned(n) - 1u) / unsigned(all)) : int(((x + 1) * n - 1) / all);
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    } else {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
-}
 // Outputs. Those of finite values lie between the largest and the smallest value, but where weights are rounded and the sum that divides is not, by
 // up to 2^-11 (fp16) further out: at the type's end, where that would be infinite, they are its largest number. (For bf16 the header's limit on
 // values is far below it.)
@@ -307,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
                     const int p = y * 32 + lane, kv = p / (kMine * kCh), key = p / kCh % kMine, ch = p % kCh;
                     const unsigned dst = to + kv * (kKeys * HD * 2) + key * HD * 2 + ((ch ^ (key & 7)) << 4);
                     const T *src = static_cast<const T *>(kv ? c.v : c.k) + from + key * HD + ch * 8;
-                    if (ok || kv) cp16(dst, src, ok && key0 + key < stop && key0 + key >= sw.seen);
+                    if (ok || kv) cp_async16_or_zeros(dst, src, ok && key0 + key < stop && key0 + key >= sw.seen);
                     else                                         // a page that is none: keys that make NaN of what sees them
                         asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0x7FFF7FFFu) : "memory");
                 }
@@ -320,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
 #pragma unroll
         for (int i = 0; i < kRows * kCh / kThreads; ++i) {
             const int at = i * kThreads + t, r = at / kCh, ch = at % kCh, p = first + min(r, live - 1), token = p * a.inverse >> 12;
-            cp16(q_at + r * HD * 2 + ((ch ^ (r & 7)) << 4), static_cast<const T *>(a.q) + (int64_t)(row0 + token) * a.ldq + (h * g + p - token * g) * HD + ch * 8, r < live);
+            cp_async16_or_zeros(q_at + r * HD * 2 + ((ch ^ (r & 7)) << 4), static_cast<const T *>(a.q) + (int64_t)(row0 + token) * a.ldq + (h * g + p - token * g) * HD + ch * 8, r < live);
         }
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) fetch(i);

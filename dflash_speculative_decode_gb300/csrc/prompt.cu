@@ -38,6 +38,8 @@
 namespace dfl {
 namespace {
 
+constexpr int kPromptQ = 128;    // tensor memory column of Q (256 channels alone)
+
 template <int HD>
 struct PromptShape {
     // 256 channels: one tile's sums take half of the tensor memory, so S is held twice instead of two tiles, and Q is
@@ -54,7 +56,6 @@ struct PromptShape {
     // tensor memory columns
     static constexpr int kS = 0, kSPitch = kKeys;                      // two of them: a tile's each, or two in turn
     static constexpr int kO = 256;
-    static constexpr int kQ = 128;                                     // (256 channels alone)
 };
 
 struct PromptArgs {
@@ -134,9 +135,6 @@ struct Place {
 __device__ __forceinline__ void st_shared(unsigned at, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-__device__ __forceinline__ void cp_async16_or_zeros(unsigned to, const void *from, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ uint4 ld_shared(unsigned at) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
@@ -159,24 +157,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// two numbers rounded to the type, the first in the low half
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    } else {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
 }
 
 // Outputs of finite values. They lie between the largest and the smallest value, but as weights are rounded and the sum that divides is not, by
@@ -443,7 +423,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < HD / 16; ++i) {
                         const uint64_t bi = b + uint64_t((i / 4) * (kKeys * 128 >> 4) + 2 * (i % 4));
-                        if constexpr (HD == 256) mma_ts(d, tm + Sh::kQ + 8 * i, bi, id_s, i > 0);
+                        if constexpr (HD == 256) mma_ts(d, tm + kPromptQ + 8 * i, bi, id_s, i > 0);
                         else mma_ss(d, q + uint64_t((i / 4) * (16384 >> 4) + 2 * (i % 4)), bi, id_s, i > 0);
                     }
                 };
@@ -594,7 +574,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::kThreads, 1)
                         const uint4 p = ld_shared(turn_at(lane, 8 * x + i));
                         v[4 * i] = p.x, v[4 * i + 1] = p.y, v[4 * i + 2] = p.z, v[4 * i + 3] = p.w;
                     }
-                    tc_st32(tmem + Sh::kQ + 32 * x + lanes, v);
+                    tc_st32(tmem + kPromptQ + 32 * x + lanes, v);
                 }
                 tc_wait_st();
                 tc_fence_before();
