@@ -223,7 +223,7 @@ struct AppendArgs {
     int64_t ldk, ldv;          // bytes
 };
 
-// One thread moves 16 bytes of a key and of the value beside it: bound by HBM (24 thousand rows of 16 heads of 128 in 38.6 us, 6.2
+// One thread moves 16 bytes of a key and of the value beside it: bound by HBM (14.6 thousand rows of 16 heads of 128 in 38.8 us, 6.2
 // TB/s, 91 % of measured), or for few rows by the launch (64 rows in 1.6 us in a graph, 5.2 with the host).
 __global__ void __launch_bounds__(256) k_paged_append(AppendArgs a) {
     const dfl_paged &c = a.c;

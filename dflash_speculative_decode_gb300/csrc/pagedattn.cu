@@ -1,6 +1,7 @@
 // pagedattn.cu -- attention of one token, or of a verify's rows, over the paged cache (include/dfl.h, dfl_paged_attn).
 //
-// The call reads every visible key and value once, so it is bound by HBM as long as few rows share them. The keys
+// The call reads every visible key and value once for each chunk of up to 64 query rows x heads, so it is bound by HBM as long
+// as few rows share them. The keys
 // of all units (a sequence, a key/value head, a chunk of query rows) lie one after another on a line of granules of
 // 64, which is cut evenly among the CTAs: the lengths of a batch, which the host does not know, decide nothing but
 // where the cuts fall. A unit that a cut goes through leaves a part (sums, maximum, weight) for each CTA, and a
@@ -13,13 +14,17 @@
 // twice, and at the end of a unit nothing but the weights' sums has to be joined. Weights are relative to a maximum
 // that all warps hold, renewed only when one of them meets a score that passes it by more than 16 powers of two (12, fp16; the
 // barrier says so, and the tile's weights are taken again). Up to 16 rows a weight goes to its product in two parts of the type
-// (rounded, and what the rounding left), so that the output's own rounding is all that shows: 1 to 6 % slower, and the outputs as
-// near the formulas as those of fp32 weights; units of more rows, whose products count, take it rounded. mma.sync and not tcgen05: with 16 rows a tile the
-// products are a small part of what even these units do while the keys arrive.
+// (rounded, and what the rounding left), so that the output's own rounding is all that shows: the outputs are as near the formulas
+// as those of fp32 weights, and calls 1 to 9 % slower (token batch 203 us, 201 with one part; one sequence of 16384 tokens 13.1 and
+// 12.7; 64 of up to 300 15.6 and 14.5). Units of more rows, whose products count, take it rounded. mma.sync and not tcgen05: with 16
+// rows a tile the products are a small part of what even these units do while the keys arrive. They are not with more rows: 8 rows
+// of 12 heads over 1 of 256 are 96 a unit, two chunks that each read all keys, through a ring of two stages with queries
+// read from shared memory for each tile, and take 24 us over 16384 tokens (floor 2.5), 189 us for 64 sequences of 5000 (49); 8 rows
+// of 4 heads a group of 128 channels (32 a unit) 20 us (9.9) and 225 us (195).
 //
 // Measured: one token of 64 sequences of up to 8191 tokens (8 heads of 128) in 203 us, 6.6 TB/s, 97 % of measured; verifies of 8
-// rows over 8 x 16384 tokens (16 heads) in 168 us, 94 %. One sequence is bound by latency: 16384 tokens of 2 heads of 256 in
-// 14.5 us, of which the merge is 2.5 (floor 5.0). Before: a key group a warp, each with a softmax and all channels of its own,
+// rows over 8 x 16384 tokens (16 heads) in 167 us, 95 %. One sequence is bound by latency: 16384 tokens of 2 heads of 256 in
+// 13 to 14.5 us in a graph, of which the merge is 2.5 (floor 5.0). Before: a key group a warp, each with a softmax and all channels of its own,
 // 209, 182 and 21 us; the next tile's scores beside the products in the same warp's stream 2 to 4 % slower than now.
 #include <algorithm>
 
@@ -33,10 +38,13 @@ constexpr int kGranule = 64;                    // keys of a granule
 constexpr int kStep = 16;                       // a unit's keys begin at a multiple of it: a page at least
 // Units of so many bytes at most are taken whole, one CTA each: a cut of many short units costs more (parts to write and to
 // add, a second unit to begin in most CTAs) than a last unit that others wait for. One token, 8 heads of 128, sequences
-// of up to 400 tokens: 64 of them 16.5 us (20.9 cut), 256 of them 55 us (69); 8 of 1000: 15.9 us (11.6 cut).
+// of up to 400 tokens: 64 of them 18.8 us (24.5 cut), 256 of them 60 us (73); 8 of up to 1000: 18.7 us (12.4 cut).
 __host__ __device__ inline long long whole_bytes(long long units) { return min(96ll * 1024 + 2560 * units, 1024ll * 1024); }
 constexpr int kMaxCtas = 304;                   // two an SM
-constexpr int kBudget = 112 * 1024;             // shared memory of a CTA, two an SM
+// Shared memory of a CTA, two an SM. The granules before each sequence's lie behind it, so above some 1180 sequences (64 channels 1690;
+// units of 17 to 32 rows: 95 of 128 channels, 1120 of 64) one CTA fits, and the line's 304 shares go in two turns: 1150 sequences of
+// 100 tokens, 8 heads of 128, take 124 ns each, 1200 220 ns; 8 rows of 32 heads over 2000 tokens 1.65 us each for 90, 2.4 for 100.
+constexpr int kBudget = 112 * 1024;
 constexpr int kMergeThreads = 256;
 constexpr int kMostGranules = (1 << 30) - 1;    // of all sequences, 2^36 tokens: what is added up below stays a 32-bit number
 
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn(const AttnWork w) {
         // (of few sequences among many, the line has them side by side)
         whole_units = (long long)most * kGranule * HD * 4 <= whole_bytes((long long)some * units) && 4 * some >= S && !far;
         // 256 channels: as many granules each as the fullest of all CTAs would have, so that fewer of the larger parts are to be added
-        // (16384 tokens of 2 heads in 13.6 us, 14.9 with all CTAs). Below, all CTAs (2 heads of 64 in 9.0 us, 10.0; 8 of 128 15.3, 16.8)
+        // (16384 tokens of 2 heads in 13.1 us, 15.8 with all CTAs). Below, all CTAs (2 heads of 64 in 9.8 us, 10.6; 8 of 128 17.1, 18.5)
         const long long least = HD == 256 ? max((all + gridDim.x - 1) / gridDim.x, 1ll) : 1;
         const int ctas = int(min((long long)gridDim.x, max(1ll, (all + least - 1) / least)));
         if (blockIdx.x == 0) {

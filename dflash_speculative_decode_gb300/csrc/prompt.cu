@@ -9,7 +9,7 @@
 // values. The maximum in use is renewed only where a tile's passes it by more than 16 powers of two (12, fp16); until then P
 // is larger than 1 and no sum changes scale, so O in tensor memory is seldom touched.
 //
-// P is rounded to the type of the values, as the tensor cores take their operands: a relative 2^-9 (bf16) or 2^-12
+// P is rounded to the type of the values, as the tensor cores take their operands: a relative 2^-8 (bf16) or 2^-11
 // (fp16) of each weight at most, the size of the output's own rounding; the sum that divides is of the unrounded
 // weights, in fp32. fp16 weights are held times 2^3, so that what is lost below its smallest number lies 2^-28
 // below the largest weight.
@@ -18,18 +18,22 @@
 // times a value that is not finite would make NaN of rows that do not see it; that shows in the sums at the end
 // (one that is not finite where the weights' sum is). Then the CTA does its tiles once more, taking what is not finite out
 // of each tile of values before the product, and notes for each row which channels it saw such a value in. So a
-// prompt without such values pays nothing for them, and one with them pays a few times its price.
+// prompt without such values pays nothing for them. One in 16384 tokens costs 1.1 to 3 times the price (32 heads of 128: 1.39 ms, 1.51 to
+// 1.61; 12 of 256: 1.16, 2.3 to 2.8; 4 of 64: 0.16, 0.51), a prompt of nothing else ten times as much.
 // What bounds it (measured in cycles of one CTA). Long rows of keys, 128 channels: a pair of tiles takes 128 keys in some
 // 2900, of which the products are 2200 at full rate: a tile's softmax (1250: the maximum 400, the weights 750, the rest
 // tensor memory) and its products (1100) follow each other, and two tiles in turn hide one behind the other. 256 channels:
 // 64 keys in 1600, as the scores' products of 64 columns run at half rate (128 would need S or Q somewhere else).
-// 16384 tokens: 1.39 ms for 32 heads of 128 (1580 TFLOP/s, 82 % of measured; 1.45 to 1.5 ms over seconds, where the card's
-// power counts), 1.18 ms for 12 of 256 (1400), 0.16 ms for 4 of 64 (860). Short rows: an item begins and ends in some
+// 64 channels: a tile's softmax costs as much beside half the products, and with 2 key/value heads 256 items of 1 to 128 pairs on 152
+// SMs take as long as the longest one (an even share were 109).
+// 16384 tokens: 1.39 to 1.44 ms for 32 heads of 128 (1530 to 1580 TFLOP/s, 79 to 82 % of measured; 1.45 to 1.5 ms over seconds,
+// where the card's power counts), 1.15 to 1.18 ms for 12 of 256 (1400 to 1430), 0.16 ms for 4 of 64 (860). Short rows: an item begins and ends in some
 // 10 thousand cycles (its place 1000 to 3000, queries and first keys 4000, sums out 3000 to 5000), as much as 3 pairs.
 // What was measured on the way (the 16384 tokens above): one lane issuing its products under `lane == 0` 2.23 ms, under
 // elect 1.58; queries by a thread a row 18 thousand cycles a tile, by asynchronous copies 3 thousand; weights handed over in
 // halves 1.43 -> 1.39 ms (256 channels: 6 % slower, not done); CTAs that stay and take items in turn 1.53 ms (a short
 // prompt 7.6 us, 4.9 with a CTA an item; packed prompts 3 % faster); one tile a CTA, two CTAs an SM 1.56 ms.
+// The kernel of 128 channels spills 120 bytes a thread at its 168 registers (148 loaded back).
 #include <algorithm>
 
 #include "paged.cuh"
