@@ -151,8 +151,8 @@ class PagedCache:
         if out is None:
             out = self.torch.zeros(q.shape, dtype=q.dtype, device=q.device)
         po, no, ldo = self._rows(out, "out", n_q)
-        if nk != n or nv != n or no != n or window > MOST:
-            _refuse("q, k, v and out must have the same rows, and window be below 2^31")
+        if nk != n or nv != n or no != n or not 0 <= window <= MOST:
+            _refuse("q, k, v and out must have the same rows, and window be 0 to 2^31 - 1")
         self._call(self.L.dfl_paged_prompt, "dfl_paged_prompt", pq, ldq, n_q, pk, ldk, pv, ldv, self._ints(cu, "cu", self.n_seq + 1), n, window,
                    self._scale if scale is None else scale, po, ldo)
         return out
@@ -164,7 +164,7 @@ class PagedCache:
         n_q = q.shape[1]
         need = self._need.get((n_q, rows))
         if need is None:
-            need = int(self.L.dfl_paged_attn_scratch_bytes(self._c, n_q, rows)) if rows <= MOST else -1
+            need = int(self.L.dfl_paged_attn_scratch_bytes(self._c, n_q, rows)) if 0 < rows <= MOST else -1
             if need < 0:
                 _refuse(f"{n_q} query heads and {rows} rows: n_q must be a multiple of n_kv = {self.n_kv}, up to 16 a head, with 1..16 rows")
             if self._scratch_bytes < need:
@@ -176,8 +176,8 @@ class PagedCache:
         if out is None:
             out = self.torch.zeros(q.shape, dtype=q.dtype, device=q.device)
         po, no, ldo = self._rows(out, "out", n_q)
-        if no != n or window > MOST:
-            _refuse("out must have q's rows, and window be below 2^31")
+        if no != n or not 0 <= window <= MOST:
+            _refuse("out must have q's rows, and window be 0 to 2^31 - 1")
         self._call(self.L.dfl_paged_attn, "dfl_paged_attn", pq, ldq, n_q, n, self._ints(cu, "cu", self.n_seq + 1), self._ints(length, "length", self.n_seq),
                    rows, window, causal, self._scale if scale is None else scale, po, ldo, self._scratch_ptr, self._scratch_bytes)
         return out

@@ -228,7 +228,8 @@ def test_sizes_that_32_bits_do_not_hold(torch):
     cu, length, c = i32(torch, a.cu), i32(torch, a.lens), a.c
     wide = torch.empty(2 ** 32 + 2, dtype=torch.int32, device="cuda")
     for f in (lambda: p.c.prompt(p.q, p.k, p.v, i32(torch, p.cu), window=2 ** 32 + 5), lambda: c.attn(a.q, cu, length, 2, window=2 ** 32 + 5),
-              lambda: c.attn(a.q, cu, length, 2 ** 32 + 2), lambda: c.plan(length, i32(torch, [2]), out=(i32(torch, [0, 0]), wide)),
+              lambda: p.c.prompt(p.q, p.k, p.v, i32(torch, p.cu), window=5 - 2 ** 32), lambda: c.attn(a.q, cu, length, 2, window=5 - 2 ** 32),
+              lambda: c.attn(a.q, cu, length, 2 ** 32 + 2), lambda: c.attn(a.q, cu, length, 2 - 2 ** 32), lambda: c.plan(length, i32(torch, [2]), out=(i32(torch, [0, 0]), wide)),
               lambda: PagedCache(c.k, c.v, wide[None], c.held, c.free, c.queue)):
         with pytest.raises(DflError, match="DFL_E_INVALID_ARG"):
             f()
