@@ -304,3 +304,54 @@ def test_the_largest_values_of_fp16(torch, heads, value):
         got[:, :g, 3] = value
         assert (got == value).all()
         a.c.status()
+
+
+# ---- calls that nothing else makes -----------------------------------------------------------------------------------
+def test_a_graph_after_the_scratch_has_grown(torch):
+    """Two captured graphs and eager calls of one cache, one after another: a call of more rows brings a larger scratch, and the graph captured
+    before goes on with its own."""
+    lens, few = [700, 90], i32(torch, [0, 1, 2])
+    p = Pages(torch, (12, 1, 256), lens, [16, 16], 16, "bf16", seed=3, wide=2000)
+    want, tol = p.want(0, True, 1 / 16)
+    first = torch.stack([p.q[0], p.q[16]]).contiguous()          # each sequence's first row
+    calls = [(first, few, i32(torch, lens), 1), (p.q, i32(torch, p.cu), i32(torch, lens), 16)]
+    wants = [(want[[0, 16]], tol[[0, 16]]), (want, tol)]
+    outs, graphs = [torch.full_like(c[0], -77.0) for c in calls], []
+    torch.cuda.synchronize()
+    for c, out in zip(calls, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            p.c.attn(*c, out=out)
+        graphs.append(g)
+    for turn in (0, 1, 0, 1):
+        for out in outs:
+            out.fill_(-77.0)
+        graphs[turn].replay()
+        p.c.attn(*calls[1 - turn], out=outs[1 - turn])
+        for out, (w, t) in zip(outs, wants):
+            near(out.double().cpu().numpy(), w, t)
+    p.c.status()
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (12, 1, 256)])
+def test_rows_before_the_first_sequence(torch, heads):
+    """Sequences that begin behind the buffers' first rows, which are left as they were."""
+    p, a = Prompts(torch, heads, [5, 60, 0, 33], "bf16"), Pages(torch, heads, [5, 100, 40], [5, 3, 2], 16, "bf16")
+    for x, rows in ((p, None), (a, 3)):
+        x.cu = np.array([5, *x.cu[2:]])
+        if x is p:
+            x.lens, x.c = x.lens[1:], cache(torch, 3, heads[1], heads[2])
+        else:
+            full = x.c
+            x.lens, x.counts, x.k64, x.v64 = x.lens[1:], x.counts[1:], x.k64[1:], x.v64[1:]
+            from dflash_speculative_decode_gb300 import PagedCache
+            x.c = PagedCache(full.k, full.v, full.table[1:].contiguous(), full.held[1:].contiguous(), full.free, full.queue)
+        x.check() if rows is None else x.check(rows)
+
+
+@pytest.mark.parametrize("heads", [(1024, 1024, 64), (2048, 1024, 64), (4096, 256, 64)])
+def test_very_many_heads(torch, heads):
+    Prompts(torch, heads, [9, 3], "bf16").check()
+    p = Pages(torch, heads, [5, 150], [1, 3], 16, "fp16", wide=300)
+    p.check(3)
+    p.check(16, window=40)
